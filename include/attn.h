@@ -359,14 +359,212 @@ size_t attn_bwd_workspace_bytes(int64_t B, int64_t H, int64_t Nq, int64_t dk);
 attn_status_t attn_bwd(const attn_bwd_params_t *params, void *workspace, size_t workspace_bytes,
                        attn_stream_t stream);
 
+/*
+ * Head norms and position rotation.
+ *
+ * For every query and key head row x of d elements at position pos:
+ *     t_c = w_c x_c / sqrt(mean_c x_c^2 + eps)              (t = x when w is NULL)
+ *     (y_a, y_b) = (t_a cos - t_b sin, t_a sin + t_b cos)   for the pairs of the first rot
+ *     dimensions, y_c = t_c for the others
+ * with cos and sin of pair c at cos_sin[pos*cos_sin_stride + c] and [... + rot/2 + c].
+ *
+ *   dtype         element type of every tensor but cos_sin, positions and the weight gradients
+ *   interleaved   0: pair c is (c, c + rot/2);  1: pair c is (2c, 2c + 1)
+ *   q, k          [B, N, Hq, d] and [B, N, Hkv, d], strides in elements (b, n, h), d contiguous
+ *   q_out, k_out  written, same shapes; each may be its input itself (same strides), and must
+ *                 not overlap it otherwise
+ *   wq, wk        [d], or NULL: that tensor is not normalised
+ *   cos_sin       fp32 [cos_sin_rows, rot], row stride cos_sin_stride floats, or NULL: nothing
+ *                 is rotated (rot is then ignored)
+ *   positions     int32, (b, n) at positions + b*positions_stride[0] + n*positions_stride[1], or
+ *                 NULL: token n of every sequence is at position n.  A position outside
+ *                 [0, cos_sin_rows) sets bit 2 of the device error word and is clamped.
+ * Supported: d a multiple of 16 up to 256; rot a multiple of 16 up to d; Hq, Hkv >= 1; tensors
+ * 16-byte aligned with strides that are multiples of 16 bytes.
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t interleaved;
+    int64_t B, N, Hq, Hkv, d, rot;
+    const void *q;
+    const void *k;
+    void *q_out;
+    void *k_out;
+    int64_t q_stride[3];      /* b, n, h */
+    int64_t k_stride[3];
+    int64_t q_out_stride[3];
+    int64_t k_out_stride[3];
+    const void *wq;
+    const void *wk;
+    const float *cos_sin;
+    int64_t cos_sin_rows;
+    int64_t cos_sin_stride;
+    const int32_t *positions;
+    int64_t positions_stride[2];  /* b, n */
+    float eps;                    /* > 0 */
+} attn_qk_norm_rope_params_t;
+
+/*
+ * attn_qk_norm_rope -- both tensors in one pass, before attn_fwd.  The arithmetic is fp32, each
+ * output rounded once.  Queues one kernel.
+ */
+attn_status_t attn_qk_norm_rope(const attn_qk_norm_rope_params_t *params, attn_stream_t stream);
+
+/*
+ * Arguments of its backward: the forward's arguments (fwd.q_out and fwd.k_out are not used; q and
+ * k are the forward's inputs), the gradients of its outputs, and the gradients to write.
+ *   dq_out, dk_out  [B, N, Hq, d], [B, N, Hkv, d]
+ *   dq, dk          written; each may be dq_out / dk_out itself, and must not overlap an input otherwise
+ *   dwq, dwk        fp32 [d], written; NULL exactly where the weight is NULL
+ */
+typedef struct {
+    attn_qk_norm_rope_params_t fwd;
+    const void *dq_out;
+    const void *dk_out;
+    void *dq;
+    void *dk;
+    int64_t dq_out_stride[3];
+    int64_t dk_out_stride[3];
+    int64_t dq_stride[3];
+    int64_t dk_stride[3];
+    float *dwq;
+    float *dwk;
+} attn_qk_norm_rope_bwd_params_t;
+
+/* Bytes of workspace attn_qk_norm_rope_bwd needs (partial weight gradients; 0 for a negative or
+ * zero size). */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t d);
+
+/*
+ * attn_qk_norm_rope_bwd -- with n_c = x_c r (r = 1 / sqrt(mean x^2 + eps)), dt = R^T dy:
+ *     dw_c = sum over rows dt_c n_c,   dx_c = r (w_c dt_c - n_c mean_j w_j dt_j n_j).
+ * The row sums are added in a fixed order (the same bits from run to run).  The workspace is
+ * caller-owned device memory, 16-byte aligned, of any contents on entry; it may be NULL when both
+ * weights are.  Queues one kernel, and one more for the weight gradients.
+ */
+attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t *params, void *workspace,
+                                    size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * A paged key/value cache and a ragged batch of new tokens over it.
+ *
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d]: strides in elements (page, slot, head), d
+ *                     contiguous (a [num_pages, Hkv, page_size, d] cache is passed by its strides)
+ *   block_table       int32 [B, table_width], row stride table_stride: the key at position j of
+ *                     sequence b is slot j % page_size of page block_table[b][j / page_size].
+ *                     Entries past a sequence's last page are never read.  A page outside
+ *                     [0, num_pages) sets bit 2 of the device error word; nothing is read or
+ *                     written there.
+ *   kv_lens           int32 [B]: keys of each sequence, the new tokens included; clamped to
+ *                     [0, table_width * page_size] (bit 1 of the device error word)
+ *   cu_q              int32 [B + 1], not decreasing: tokens cu_q[b] .. cu_q[b + 1] - 1 of the T
+ *                     packed tokens are sequence b's newest (token i of its nq lies at position
+ *                     kv_lens[b] - nq + i).  NULL: every sequence has T / B of them.  Tokens
+ *                     before cu_q[0] and from cu_q[B] on belong to no sequence: their outputs are
+ *                     left as they were.  Entries outside [0, T] or decreasing set bit 2.
+ */
+typedef struct {
+    int32_t dtype;       /* attn_dtype_t */
+    int32_t page_size;
+    int64_t B, T, Hkv, d;
+    void *k_pages;
+    void *v_pages;
+    int64_t k_stride[3]; /* page, slot, head */
+    int64_t v_stride[3];
+    int64_t num_pages;
+    const int32_t *block_table;
+    int64_t table_width;
+    int64_t table_stride;
+    const int32_t *kv_lens;
+    const int32_t *cu_q;
+} attn_paged_cache_t;
+
+/*
+ * Arguments of attn_paged_append: packed tokens q [T, Hq, d], k and v [T, Hkv, d] (strides token,
+ * head), and the head norms and rotation of attn_qk_norm_rope (weights, cos_sin, rot, eps,
+ * interleaved as there).
+ *   q_out      [T, Hq, d], written; may be q itself
+ *   positions  int32 [T], the rotation's positions, or NULL: each token's place in its sequence
+ *              (0 for a token with no place, see below)
+ */
+typedef struct {
+    attn_paged_cache_t cache;
+    int64_t Hq, rot;
+    const void *q;
+    const void *k;
+    const void *v;
+    void *q_out;
+    int64_t q_stride[2];      /* token, head */
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t q_out_stride[2];
+    const void *wq;
+    const void *wk;
+    const float *cos_sin;
+    int64_t cos_sin_rows;
+    int64_t cos_sin_stride;
+    const int32_t *positions;
+    float eps;
+    int32_t interleaved;
+} attn_paged_append_params_t;
+
+/*
+ * attn_paged_append -- norms and rotates q and k, writes the keys and the values (as they are) to
+ * their slots of the cache, and q to q_out, in one pass.  A token whose place kv_lens[b] - nq + i
+ * is negative (a place of the batch without a sequence) writes no key or value.
+ * Supported: as attn_qk_norm_rope; any page_size >= 1; B >= 1 when T > 0.  Queues one kernel.
+ */
+attn_status_t attn_paged_append(const attn_paged_append_params_t *params, attn_stream_t stream);
+
+/*
+ * Arguments of attn_paged_fwd: packed queries q [T, Hq, d] (strides token, head) of the batch that
+ * cache describes; Hq is a multiple of Hkv, and query head h reads key/value head h / (Hq / Hkv).
+ *   causal   0: a token sees all kv_lens[b] keys; 1: token i of nq sees keys j <= i + kv_lens[b] - nq
+ *   max_q    the largest number of new tokens of any sequence, or 0 when it is not known: it
+ *            chooses the kernel, the results hold for any value
+ *   o        [T, Hq, d], written;  lse fp32 [T, Hq] contiguous, written; may be NULL
+ */
+typedef struct {
+    attn_paged_cache_t cache;
+    int32_t causal;
+    float scale;
+    int64_t Hq, max_q;
+    const void *q;
+    void *o;
+    int64_t q_stride[2];
+    int64_t o_stride[2];
+    float *lse;
+} attn_paged_fwd_params_t;
+
+/* Bytes of workspace attn_paged_fwd needs for these arguments on the current device (pointers are
+ * not looked at); 0 for invalid ones. */
+size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
+
+/*
+ * attn_paged_fwd -- attention of the new tokens, one or many per sequence in one call, over the
+ * paged cache.  ("How Does FlashAttention Preserve Global Softmax Across Tiles?", sections 3, 6
+ * and 8.)  The keys of a sequence are read once for all query heads that share them.  The work is
+ * cut into equal shares of key tiles over the GPU; a row whose keys fall into several shares is
+ * merged from their states (m, l, u), in a fixed order: the same bits from run to run.
+ * Values at positions >= kv_lens[b] are never used, whatever lies there.  A visible value that is
+ * infinite or NaN reaches every query row of its tile, as 0 * inf does in a product.
+ * workspace: caller-owned device memory, 16-byte aligned, of any contents on entry; calls that
+ * overlap on the GPU need one each.
+ * Supported: bfloat16, d in {64, 128}, page_size a power of two >= 16, 1 <= Hq / Hkv <= 64,
+ * scale > 0; tensors 16-byte aligned, strides non-zero multiples of 8 elements.
+ */
+attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *workspace, size_t workspace_bytes,
+                             attn_stream_t stream);
+
 /* Message describing the last non-OK status returned on the calling thread ("" if none). */
 const char *attn_last_error(void);
 
 /*
  * Device error word of the current device (synchronous: waits for the device to finish its
  * queued work first).  Bit 0: a kernel gave up a bounded wait on an mbarrier and returned
- * early (its outputs are then incomplete).  Bit 1: a kv_lens value was outside [0, Nk] and
- * was clamped.  clear != 0 resets the word to 0 after reading.  Returns ATTN_OK or
+ * early (its outputs are then incomplete).  Bit 1: a kv_lens value was outside its range and
+ * was clamped.  Bit 2: a page, a position or a cu_q entry was out of range (nothing out of bounds
+ * was read or written).  clear != 0 resets the word to 0 after reading.  Returns ATTN_OK or
  * ATTN_ERR_CUDA.
  */
 attn_status_t attn_device_error_flags(uint32_t *out, int32_t clear);

@@ -9,6 +9,12 @@ CUDA device every call raises.
     o, lse = attn_decode_splitkv(q, k_cache, v_cache, kv_lens, num_splits=16)
     o, lse = attn_merge_states(partials)
 
+Around the attention (module ``paged``, same rules; include/attn.h):
+
+    q2, k2 = attn_qk_norm_rope(q, k, wq, wk, cos_sin)         # head norms and position rotation
+    q2 = attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, ...)
+    o, lse = attn_paged_fwd(q2, k_pages, v_pages, block_table, kv_lens, cu_q)
+
 Shapes: q [B, Nq, H, dk], k [B, Nk, H, dk], v [B, Nk, H, dv] (any strides with the last
 dimension contiguous), bias [B, H, Nq, Nk] fp32 (any strides with the last dimension
 contiguous, 0 strides broadcast), kv_lens int32 [B].  Outputs o [B, Nq, H, dv] in q's dtype
@@ -26,6 +32,8 @@ import torch
 __all__ = ["attn_fwd", "attn_fwd_partial", "attn_merge_states_rows", "attn_bwd", "attn_decode_splitkv",
            "attn_decode_splitkv_fused", "attn_decode_splitkv_noalloc",
            "attn_merge_states", "decode_workspace_bytes", "bwd_workspace_bytes",
+           "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_append", "attn_paged_fwd",
+           "paged_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes",
            "device_error_flags", "last_error", "library_path", "load", "AttnError", "Status"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -426,7 +434,12 @@ def attn_merge_states(partials, out_dtype=torch.bfloat16, out=None, lse=None, st
 
 
 def device_error_flags(clear=True) -> int:
-    """Device error word (bit 0: a bounded wait gave up; bit 1: kv_lens clamped)."""
+    """Device error word (bit 0: a bounded wait gave up; bit 1: kv_lens clamped; bit 2: a page, a
+    position or a cu_q entry out of range)."""
     v = ctypes.c_uint32(0)
     _check(load().attn_device_error_flags(ctypes.byref(v), 1 if clear else 0))
     return int(v.value)
+
+
+from .paged import (attn_paged_append, attn_paged_fwd, attn_qk_norm_rope, attn_qk_norm_rope_bwd,  # noqa: E402
+                    paged_fwd_workspace_bytes, qk_norm_rope_bwd_workspace_bytes)

@@ -22,6 +22,8 @@ attn_status_t fail(attn_status_t st, const char *fmt, ...) {
     return st;
 }
 
+void clear_error() { g_msg[0] = 0; }
+
 // The device error word: one per device, lives as long as the library is loaded.
 __device__ uint32_t g_device_flags;
 

@@ -10,10 +10,13 @@
 namespace attn {
 
 // Error bits of the device error word (see attn_device_error_flags).
-enum : uint32_t { kFlagWaitTimeout = 1u, kFlagKvLenClamped = 2u };
+enum : uint32_t { kFlagWaitTimeout = 1u, kFlagKvLenClamped = 2u, kFlagBadIndex = 4u };
 
 // Records a message for attn_last_error() and returns `st`.
 attn_status_t fail(attn_status_t st, const char *fmt, ...);
+
+// Clears the calling thread's last error message (at the start of every entry point).
+void clear_error();
 
 // Device address of the device error word of the current device (nullptr on failure).
 uint32_t *device_flags();

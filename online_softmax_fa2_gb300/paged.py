@@ -1,0 +1,325 @@
+"""Head norms with the position rotation, and the paged key/value cache: binding over the C ABI.
+
+    q2, k2 = attn_qk_norm_rope(q, k, wq, wk, cos_sin)                    # before attn_fwd
+    dq, dk, dwq, dwk = attn_qk_norm_rope_bwd(q, k, dq2, dk2, wq, wk, cos_sin)
+    q2 = attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq=..., wk=..., cos_sin=...)
+    o, lse = attn_paged_fwd(q2, k_pages, v_pages, block_table, kv_lens, cu_q, max_q=...)
+
+Shapes: q [B, N, Hq, d] and k [B, N, Hkv, d] for the first two; packed tokens q [T, Hq, d], k and
+v [T, Hkv, d] for the others, with k_pages and v_pages [num_pages, page_size, Hkv, d],
+block_table int32 [B, width], kv_lens int32 [B] (the new tokens included) and cu_q int32 [B + 1]
+(None: T / B new tokens in every sequence).  Any strides with the last dimension contiguous.
+The names' kernels and rules are those of include/attn.h.
+
+A call runs on torch's current stream of the tensors' device, which need not be the current
+device; with ``stream`` it runs there, and what it allocates is kept for that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+import online_softmax_fa2_gb300 as _ofa
+
+__all__ = ["attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_append", "attn_paged_fwd",
+           "paged_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes"]
+
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+_S2, _S3 = _i64 * 2, _i64 * 3
+
+
+class NormRopeParams(ctypes.Structure):
+    """Mirror of attn_qk_norm_rope_params_t (include/attn.h)."""
+    _fields_ = [("dtype", _i32), ("interleaved", _i32),
+                ("B", _i64), ("N", _i64), ("Hq", _i64), ("Hkv", _i64), ("d", _i64), ("rot", _i64),
+                ("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp),
+                ("q_stride", _S3), ("k_stride", _S3), ("q_out_stride", _S3), ("k_out_stride", _S3),
+                ("wq", _vp), ("wk", _vp),
+                ("cos_sin", _vp), ("cos_sin_rows", _i64), ("cos_sin_stride", _i64),
+                ("positions", _vp), ("positions_stride", _S2), ("eps", _f32)]
+
+
+class NormRopeBwdParams(ctypes.Structure):
+    """Mirror of attn_qk_norm_rope_bwd_params_t (include/attn.h)."""
+    _fields_ = [("fwd", NormRopeParams),
+                ("dq_out", _vp), ("dk_out", _vp), ("dq", _vp), ("dk", _vp),
+                ("dq_out_stride", _S3), ("dk_out_stride", _S3), ("dq_stride", _S3), ("dk_stride", _S3),
+                ("dwq", _vp), ("dwk", _vp)]
+
+
+class PagedCache(ctypes.Structure):
+    """Mirror of attn_paged_cache_t (include/attn.h)."""
+    _fields_ = [("dtype", _i32), ("page_size", _i32),
+                ("B", _i64), ("T", _i64), ("Hkv", _i64), ("d", _i64),
+                ("k_pages", _vp), ("v_pages", _vp), ("k_stride", _S3), ("v_stride", _S3), ("num_pages", _i64),
+                ("block_table", _vp), ("table_width", _i64), ("table_stride", _i64),
+                ("kv_lens", _vp), ("cu_q", _vp)]
+
+
+class PagedAppendParams(ctypes.Structure):
+    """Mirror of attn_paged_append_params_t (include/attn.h)."""
+    _fields_ = [("cache", PagedCache), ("Hq", _i64), ("rot", _i64),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("q_out", _vp),
+                ("q_stride", _S2), ("k_stride", _S2), ("v_stride", _S2), ("q_out_stride", _S2),
+                ("wq", _vp), ("wk", _vp),
+                ("cos_sin", _vp), ("cos_sin_rows", _i64), ("cos_sin_stride", _i64),
+                ("positions", _vp), ("eps", _f32), ("interleaved", _i32)]
+
+
+class PagedFwdParams(ctypes.Structure):
+    """Mirror of attn_paged_fwd_params_t (include/attn.h)."""
+    _fields_ = [("cache", PagedCache), ("causal", _i32), ("scale", _f32), ("Hq", _i64), ("max_q", _i64),
+                ("q", _vp), ("o", _vp), ("q_stride", _S2), ("o_stride", _S2), ("lse", _vp)]
+
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = _ofa.load()
+        P, size = ctypes.POINTER, ctypes.c_size_t
+        for name, args, res in (
+                ("attn_qk_norm_rope", [P(NormRopeParams), _vp], _i32),
+                ("attn_qk_norm_rope_bwd_workspace_bytes", [_i64] * 5, size),
+                ("attn_qk_norm_rope_bwd", [P(NormRopeBwdParams), _vp, size, _vp], _i32),
+                ("attn_paged_append", [P(PagedAppendParams), _vp], _i32),
+                ("attn_paged_fwd_workspace_bytes", [P(PagedFwdParams)], size),
+                ("attn_paged_fwd", [P(PagedFwdParams), _vp, size, _vp], _i32)):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, res
+        _lib = lib
+    return _lib
+
+
+_DTYPES = {torch.float32: _ofa.F32, torch.bfloat16: _ofa.BF16}
+
+
+def _need(t, name, shape, dtype, dev):
+    """t as a tensor of that shape and dtype on dev, its last dimension contiguous."""
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _device(q, dim):
+    if not q.is_cuda:
+        raise ValueError("every tensor must be on a CUDA device (there is no CPU path)")
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}: use torch.float32 or torch.bfloat16")
+    if q.dim() != dim:
+        raise ValueError(f"q must be {dim}-D, got {tuple(q.shape)}")
+    return q.device
+
+
+def _call(dev, stream, made, fn, *args):
+    """fn(*args, stream) with dev current; tensors made here are kept for a stream given."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        raw = stream.cuda_stream
+        for t in made:
+            t.record_stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st:
+        raise _ofa.AttnError(st, _ofa.last_error())
+
+
+def _weight(w, name, d, dtype, dev):
+    return None if w is None else _need(w, name, (d,), dtype, dev)
+
+
+def _angles(cos_sin, dev):
+    """(pointer, rows, row stride, rot) of the angle table [P, rot], or Nones."""
+    if cos_sin is None:
+        return None, 0, 0, 0
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [positions, rot]")
+    rows, rot = cos_sin.shape
+    return _need(cos_sin, "cos_sin", (rows, rot), torch.float32, dev), rows, cos_sin.stride(0), rot
+
+
+def _norm_rope_params(q, k, qo, ko, wq, wk, cos_sin, positions, eps, interleaved):
+    dev, dt = _device(q, 4), q.dtype
+    B, N, Hq, d = q.shape
+    Hkv = k.shape[2] if k.dim() == 4 else -1
+    kp = _need(k, "k", (B, N, Hkv, d), dt, dev)
+    qp = _need(q, "q", (B, N, Hq, d), dt, dev)
+    qop = None if qo is None else _need(qo, "q_out", (B, N, Hq, d), dt, dev)
+    kop = None if ko is None else _need(ko, "k_out", (B, N, Hkv, d), dt, dev)
+    cs, rows, row, rot = _angles(cos_sin, dev)
+    pos, ps = None, (0, 0)
+    if positions is not None:
+        if positions.dtype != torch.int32 or positions.device != dev:
+            raise ValueError(f"positions must be int32 on {dev}")
+        positions = positions.expand(B, N)
+        pos, ps = positions.data_ptr(), positions.stride()
+    z = (0, 0, 0)
+    return NormRopeParams(_DTYPES[dt], 1 if interleaved else 0, B, N, Hq, Hkv, d, rot, qp, kp, qop, kop,
+                          q.stride()[:3], k.stride()[:3], z if qo is None else qo.stride()[:3],
+                          z if ko is None else ko.stride()[:3], _weight(wq, "wq", d, dt, dev),
+                          _weight(wk, "wk", d, dt, dev), cs, rows, row, pos, ps, eps)
+
+
+def attn_qk_norm_rope(q, k, wq=None, wk=None, cos_sin=None, positions=None, eps=1e-6, interleaved=False, q_out=None,
+                      k_out=None, stream=None):
+    """RMS norm of every head of q [B, N, Hq, d] and k [B, N, Hkv, d] (weights wq, wk [d]; None: no
+    norm) and the rotation by the angle table cos_sin (float32 [P, rot], cos then sin; None: none)
+    at positions (int32 [B, N] or broadcast; None: 0 .. N - 1).  Pairs are (c, c + rot/2), or
+    (2c, 2c + 1) when interleaved.  Returns (q_out, k_out), which may be given, q and k
+    themselves included.  See include/attn.h, attn_qk_norm_rope."""
+    lib, made = _load(), []
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        made.append(q_out)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        made.append(k_out)
+    p = _norm_rope_params(q, k, q_out, k_out, wq, wk, cos_sin, positions, eps, interleaved)
+    _call(q.device, stream, made, lib.attn_qk_norm_rope, p)
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d) -> int:
+    return int(_load().attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d))
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, positions=None, eps=1e-6,
+                          interleaved=False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradients of attn_qk_norm_rope: q, k are its inputs, dq_out, dk_out the gradients of its
+    outputs.  Returns (dq, dk, dwq, dwk); dq and dk may be given (dq_out and dk_out themselves
+    included), dwq and dwk are float32 [d], None where the weight is."""
+    lib, made = _load(), []
+    dev = _device(q, 4)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        made.append(dq)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        made.append(dk)
+    f = _norm_rope_params(q, k, None, None, wq, wk, cos_sin, positions, eps, interleaved)
+    B, N, Hq, Hkv, d = f.B, f.N, f.Hq, f.Hkv, f.d
+    dwq = dwk = None
+    if wq is not None:
+        dwq = torch.empty(d, dtype=torch.float32, device=dev)
+        made.append(dwq)
+    if wk is not None:
+        dwk = torch.empty(d, dtype=torch.float32, device=dev)
+        made.append(dwk)
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
+                                device=dev)
+        made.append(workspace)
+    sq, sk, dt = (B, N, Hq, d), (B, N, Hkv, d), q.dtype
+    p = NormRopeBwdParams(f, _need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev),
+                          _need(dq, "dq", sq, dt, dev), _need(dk, "dk", sk, dt, dev), dq_out.stride()[:3],
+                          dk_out.stride()[:3], dq.stride()[:3], dk.stride()[:3],
+                          None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr())
+    wsp, wsn = _workspace(workspace, dev)
+    _call(dev, stream, made, lib.attn_qk_norm_rope_bwd, p, wsp, wsn)
+    return dq, dk, dwq, dwk
+
+
+def _workspace(t, dev):
+    if t is None:
+        return None, 0
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q):
+    if k_pages.dim() != 4 or k_pages.shape[3] != d:
+        raise ValueError(f"k_pages must be [num_pages, page_size, Hkv, {d}], got {tuple(k_pages.shape)}")
+    pages, page, Hkv, _ = shape = k_pages.shape
+    kp, vp = _need(k_pages, "k_pages", shape, dt, dev), _need(v_pages, "v_pages", shape, dt, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, width]")
+    B, width = block_table.shape
+    bt = _need(block_table, "block_table", (B, width), torch.int32, dev)
+    lens = _need(kv_lens, "kv_lens", (B,), torch.int32, dev)
+    cu = None if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)
+    return PagedCache(_DTYPES[dt], page, B, T, Hkv, d, kp, vp, k_pages.stride()[:3], v_pages.stride()[:3], pages, bt,
+                      width, block_table.stride(0), lens, cu)
+
+
+def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None, wq=None, wk=None, cos_sin=None,
+                      positions=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """Writes the new tokens' keys (normed and rotated as by attn_qk_norm_rope) and values to their
+    slots of the paged cache, in place, and returns the normed and rotated queries.  kv_lens
+    counts the new tokens; positions (int32 [T]; None: each token's place in its sequence) are
+    the rotation's.  See include/attn.h, attn_paged_append."""
+    lib, made = _load(), []
+    dev, dt = _device(q, 3), q.dtype
+    T, Hq, d = q.shape
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        made.append(q_out)
+    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
+    sk = (T, c.Hkv, d)
+    cs, rows, row, rot = _angles(cos_sin, dev)
+    p = PagedAppendParams(c, Hq, rot, _need(q, "q", q.shape, dt, dev), _need(k, "k", sk, dt, dev),
+                          _need(v, "v", sk, dt, dev), _need(q_out, "q_out", q.shape, dt, dev), q.stride()[:2],
+                          k.stride()[:2], v.stride()[:2], q_out.stride()[:2], _weight(wq, "wq", d, dt, dev),
+                          _weight(wk, "wk", d, dt, dev), cs, rows, row,
+                          None if positions is None else _need(positions, "positions", (T,), torch.int32, dev), eps,
+                          1 if interleaved else 0)
+    _call(dev, stream, made, lib.attn_paged_append, p)
+    return q_out
+
+
+def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse):
+    dev, dt = _device(q, 3), q.dtype
+    T, Hq, d = q.shape
+    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
+    lp = None
+    if lse is not None:
+        lp = _need(lse, "lse", (T, Hq), torch.float32, dev)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    if max_q is None:
+        max_q = 0 if cu_q is not None else T // c.B if c.B else 0
+    o = q if out is None else out
+    return PagedFwdParams(c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q,
+                          _need(q, "q", q.shape, dt, dev), _need(o, "out", q.shape, dt, dev), q.stride()[:2],
+                          o.stride()[:2], lp)
+
+
+def paged_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True) -> int:
+    """Bytes of workspace attn_paged_fwd needs for these arguments (the lengths' values play no part)."""
+    p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, None, None, None)
+    return int(_load().attn_paged_fwd_workspace_bytes(p))
+
+
+def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True, scale=None,
+                   workspace=None, out=None, lse=None, stream=None):
+    """Attention of the packed new tokens q [T, Hq, d] over the paged cache, one or many per
+    sequence in one call; query head h reads key/value head h // (Hq // Hkv).  causal aligns the
+    new tokens to the end of their sequences.  max_q: the largest number of new tokens of any
+    sequence, where the caller knows it (it chooses the kernel; the results hold without it).
+    Returns (o [T, Hq, d], lse [T, Hq]).  See include/attn.h, attn_paged_fwd."""
+    lib, made = _load(), []
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        made.append(out)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        made.append(lse)
+    p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse)
+    if workspace is None:
+        n = lib.attn_paged_fwd_workspace_bytes(p)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            made.append(workspace)
+    wsp, wsn = _workspace(workspace, q.device)
+    _call(q.device, stream, made, lib.attn_paged_fwd, p, wsp, wsn)
+    return out, lse

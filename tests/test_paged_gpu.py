@@ -1,0 +1,270 @@
+"""Attention over a paged cache against a plain form in 64 bits (paged_helpers), and runs of the
+operators together."""
+import math
+
+import pytest
+import torch
+
+import online_softmax_fa2_gb300 as ofa
+from paged_helpers import angles, check_paged, paged_inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def run(s, causal=True, scale=None, **kw):
+    return ofa.attn_paged_fwd(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], causal=causal, scale=scale, **kw)
+
+
+CASES = [  # new, lens, Hq, Hkv, d, page, causal
+    ([1], [1], 1, 1, 64, 16, True),
+    ([1], [300], 8, 2, 64, 16, True),
+    ([1], [5000], 4, 1, 128, 128, True),
+    ([1, 1, 1, 1], [1, 16, 17, 0], 8, 8, 128, 16, True),
+    ([1] * 9, [129, 128, 127, 64, 63, 65, 1000, 2, 0], 32, 8, 128, 64, True),
+    ([4, 4, 4], [4, 700, 33], 4, 4, 64, 16, True),
+    ([4, 2, 0, 8], [3, 1, 50, 0], 6, 2, 128, 32, True),      # rows that see no key
+    ([7, 7], [129, 256], 7, 1, 128, 32, False),
+    ([33], [33], 5, 1, 128, 16, True),
+    ([100, 1, 17], [350, 1025, 17], 28, 4, 128, 32, True),
+    ([129], [400], 4, 4, 64, 64, False),
+    ([300, 2], [300, 900], 8, 8, 128, 128, True),
+    ([255, 0, 257], [255, 0, 700], 3, 1, 64, 16, True),
+    ([64], [64], 64, 1, 128, 16, True),
+    ([150, 20], [149, 10], 2, 1, 128, 16, True),             # more queries than keys
+    ([513], [1100], 12, 4, 64, 256, True),
+]
+
+
+@pytest.mark.parametrize("hint", [True, False])
+@pytest.mark.parametrize("case", CASES)
+def test_paged_fwd(case, hint):
+    new, lens, Hq, Hkv, d, page, causal = case
+    s = paged_inputs(new, lens, Hq, Hkv, d, page, seed=len(new), heads_first=page == 32)
+    ofa.device_error_flags()
+    o, lse = run(s, causal, max_q=max(new) if hint else None)
+    assert ofa.device_error_flags() == 0
+    check_paged(o, lse, s, new, lens, causal, 1 / math.sqrt(d))
+    o2, lse2 = run(s, causal, max_q=max(new) if hint else None)
+    assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_paged_fwd_random(seed):
+    g = torch.Generator().manual_seed(100 + seed)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))  # noqa: E731
+    B, Hkv, G = r(1, 7), r(1, 3), r(1, 9)
+    d, page, causal = (64, 128)[r(0, 1)], (16, 32, 64, 128)[r(0, 3)], r(0, 4) > 0
+    big = r(0, 2)
+    new = [1 if big == 0 else r(0, (0, 12, 200)[big]) for _ in range(B)]
+    lens = [r(0, (2000, 300, 600)[big]) for _ in range(B)]
+    s = paged_inputs(new, lens, Hkv * G, Hkv, d, page, seed=seed, heads_first=bool(r(0, 1)))
+    if sum(new) == 0:
+        return
+    o, lse = run(s, causal, max_q=r(0, 1) * max(new), scale=0.2)
+    assert ofa.device_error_flags() == 0
+    check_paged(o, lse, s, new, lens, causal, 0.2, f"seed {seed}")
+
+
+def test_large_logits_and_growing_maxima():
+    # each page's keys are larger than the last one's: the maximum moves at every tile
+    new, lens = [3, 200], [900, 700]
+    s = paged_inputs(new, lens, 4, 2, 128, 64, seed=5)
+    for b in range(2):
+        for j in range(-(-lens[b] // 64)):
+            s["kp"][s["bt"][b, j].long()] *= 1 + j
+    o, lse = run(s)
+    check_paged(o, lse, s, new, lens, True, 1 / math.sqrt(128))
+
+
+def test_rows_outside_the_sequences_stay():
+    new, lens = [2, 30], [40, 50]
+    s = paged_inputs(new, lens, 4, 2, 64, 16)
+    o0, l0 = run(s)
+    pad = torch.randn(5, 4, 64, device=DEV).bfloat16()
+    q = torch.cat([pad, s["q"], pad])
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 5.0, device=DEV)
+    ofa.attn_paged_fwd(q, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"] + 5, out=out, lse=lse)
+    assert torch.equal(out[5:-5], o0) and torch.equal(lse[5:-5], l0)
+    for t in (out[:5], out[-5:]):
+        assert bool((t == 3.0).all())
+    assert bool((lse[:5] == 5.0).all()) and bool((lse[-5:] == 5.0).all())
+    assert ofa.device_error_flags() == 0
+
+
+def test_strided_queries_and_outputs_no_lse():
+    new, lens = [1, 20], [100, 70]
+    s = paged_inputs(new, lens, 6, 2, 128, 32)
+    want, _ = run(s)
+    wide = torch.zeros(21, 10, 2, 128, dtype=torch.bfloat16, device=DEV)
+    q = wide[:, 2:8, 1]
+    q.copy_(s["q"])
+    out = torch.zeros(6, 21, 256, dtype=torch.bfloat16, device=DEV).permute(1, 0, 2)[..., :128]
+    ofa.attn_paged_fwd(q, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], out=out)
+    assert torch.equal(out, want)
+
+
+def test_uniform_batch_needs_no_cu():
+    s = paged_inputs([3] * 4, [50, 3, 200, 1], 4, 2, 128, 16)
+    a = run(s)
+    b = ofa.attn_paged_fwd(s["q"], s["kp"], s["vp"], s["bt"], s["lens"])
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_bad_pages_and_lengths_are_reported():
+    s = paged_inputs([1, 1], [100, 40], 2, 1, 64, 16)
+    want, _ = run(s)
+    s["bt"][0, 3] = -7
+    s["bt"][0, 4] = 1 << 30
+    ofa.device_error_flags()
+    o, _ = run(s)
+    assert ofa.device_error_flags() == 4
+    assert torch.equal(o[1], want[1])
+    s = paged_inputs([1, 40], [112, 40], 2, 1, 64, 16, width=7)
+    want, _ = run(s)
+    s["lens"][0] = 5000  # the table holds 112
+    o, _ = run(s)
+    assert ofa.device_error_flags() == 2 and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("cu", [[0, 4, 2, 6], [0, 9, 9, 9], [-5, 2, 3, 6], [6, 4, 2, 0], [2, 3, 4, 5]])
+def test_a_malformed_cu_faults_nothing(cu):
+    s = paged_inputs([2, 2, 2], [20, 30, 17], 2, 1, 64, 16)
+    for mq in (0, 2, 64):
+        ofa.attn_paged_fwd(s["q"], s["kp"], s["vp"], s["bt"], s["lens"],
+                           torch.tensor(cu, dtype=torch.int32, device=DEV), max_q=mq)
+    torch.cuda.synchronize()
+    ofa.device_error_flags()
+
+
+def test_a_cache_past_two_gib_of_elements():
+    # pages at offsets beyond 2^31 elements (and 2^32 bytes) in both caches
+    page, Hkv, d = 128, 8, 128
+    pages = (1 << 31) // (page * Hkv * d) + 40
+    kp = torch.zeros(pages, page, Hkv, d, dtype=torch.bfloat16, device=DEV)
+    vp = torch.zeros_like(kp)
+    s = paged_inputs([1, 40], [900, 700], 16, 8, d, page, poison=False)
+    n = s["kp"].shape[0]
+    kp[-n:], vp[-n:] = s["kp"], s["vp"]
+    a = run(s, max_q=40)
+    bt = torch.where(s["bt"] < n, s["bt"] + (pages - n), s["bt"])
+    b = ofa.attn_paged_fwd(s["q"], kp, vp, bt, s["lens"], s["cu"], max_q=40)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    k, v = (torch.randn(41, 8, d, device=DEV).bfloat16() for _ in range(2))
+    ofa.attn_paged_append(s["q"], k, v, kp, vp, bt, s["lens"], s["cu"])
+    assert torch.equal(kp[bt[0, 7].long(), 899 % 128], k[0]) and torch.equal(vp[bt[1, 5].long(), 699 % 128], v[40])
+
+
+def step(s, k, v, w, cs):
+    q = ofa.attn_paged_append(s["q"], k, v, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], wq=w, wk=w, cos_sin=cs)
+    return ofa.attn_paged_fwd(q, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], max_q=1)
+
+
+def test_prompt_in_chunks_then_tokens_equals_the_whole_at_once():
+    """A prompt appended in chunks of many sizes and then token by token gives the rows that the
+    prefill over the same normed and rotated tensors gives, and the cache it leaves holds them."""
+    N, Hq, Hkv, d, page = 333, 8, 2, 128, 16
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(1, N, h, d, generator=g).bfloat16().to(DEV) for h in (Hq, Hkv, Hkv))
+    w = (1 + 0.2 * torch.randn(d, generator=g)).bfloat16().to(DEV)
+    cs = angles(N, d).to(DEV)
+    q2, k2 = ofa.attn_qk_norm_rope(q, k, w, w, cs)
+    rep = lambda t: t.repeat_interleave(Hq // Hkv, 2)  # noqa: E731
+    want, wl = ofa.attn_fwd(q2, rep(k2), rep(v), causal=True)
+    pages = -(-N // page)
+    kp = torch.full((pages + 2, page, Hkv, d), math.nan, dtype=torch.bfloat16, device=DEV)
+    vp = kp.clone()
+    bt = torch.randperm(pages + 2, generator=g)[:pages].int().to(DEV)[None]
+    at = 0
+    for c in [100, 1, 64, 130, 5] + [1] * 33:
+        sl = slice(at, at + c)
+        at += c
+        lens = torch.tensor([at], dtype=torch.int32, device=DEV)
+        cu = torch.tensor([0, c], dtype=torch.int32, device=DEV)
+        qr = ofa.attn_paged_append(q[0, sl], k[0, sl], v[0, sl], kp, vp, bt, lens, cu, wq=w, wk=w, cos_sin=cs)
+        assert torch.equal(qr, q2[0, sl])
+        o, lse = ofa.attn_paged_fwd(qr, kp, vp, bt, lens, cu, max_q=c)
+        # both round weights and outputs to bf16: a step of 2^-8 each of values below 4
+        assert float((o.float() - want[0, sl].float()).abs().max()) <= 4 * 2 * 2.0 ** -8
+        assert float((lse - wl[0, :, sl].T).abs().max()) <= 1e-4
+    assert at == N and ofa.device_error_flags() == 0
+    assert torch.equal(kp[bt[0].long()].flatten(0, 1)[:N], k2[0])
+
+
+def test_training_run_norm_rope_attention_and_back():
+    """attn_qk_norm_rope -> attn_fwd -> attn_bwd -> attn_qk_norm_rope_bwd against the same chain in
+    64 bits differentiated by torch, on the relative norm of each gradient."""
+    B, N, H, d = 2, 130, 2, 64
+    g = torch.Generator().manual_seed(4)
+    q, k, v, do = (torch.randn(B, N, H, d, generator=g).bfloat16().to(DEV) for _ in range(4))
+    wq, wk = ((1 + 0.2 * torch.randn(d, generator=g)).bfloat16().to(DEV) for _ in range(2))
+    cs = angles(N, d).to(DEV)
+    q2, k2 = ofa.attn_qk_norm_rope(q, k, wq, wk, cs)
+    o, lse = ofa.attn_fwd(q2, k2, v, causal=True)
+    dq2, dk2, dv = ofa.attn_bwd(q2, k2, v, o, lse, do, causal=True)
+    dq, dk, dwq, dwk = ofa.attn_qk_norm_rope_bwd(q, k, dq2, dk2, wq, wk, cs)
+
+    leaves = [t.cpu().double().requires_grad_() for t in (q, k, v, wq, wk)]
+    c = cs.cpu().double()[None, :, None]
+
+    def nr(x, w):
+        t = x / (x.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w
+        a, b = t[..., :d // 2], t[..., d // 2:]
+        co, si = c[..., :d // 2], c[..., d // 2:]
+        return torch.cat([a * co - b * si, a * si + b * co], -1)
+
+    Q, K = nr(leaves[0], leaves[3]), nr(leaves[1], leaves[4])
+    X = torch.einsum("bihd,bjhd->bhij", Q, K) / math.sqrt(d)
+    X = X.masked_fill(torch.ones(N, N, dtype=torch.bool).triu(1), -math.inf)
+    O = torch.einsum("bhij,bjhd->bihd", X.softmax(-1), leaves[2])
+    refs = torch.autograd.grad(O, leaves, do.cpu().double())
+    # bf16 roundings on the way: q', k', o, the weights, dS, dq', dk', and the result: eight half
+    # steps of 2^-8 that do not all point one way (their root sum of squares is 0.011)
+    for got, ref, n in zip((dq, dk, dv, dwq, dwk), refs, "dq dk dv dwq dwk".split()):
+        rel = float((got.cpu().double() - ref).norm() / ref.norm())
+        assert rel <= 8 * 2.0 ** -8, (n, rel)
+
+
+def test_captured_step_replays_with_new_values():
+    new, lens = [1] * 5, [300, 20, 1, 64, 1000]
+    s = paged_inputs(new, lens, 8, 2, 128, 16, seed=2, poison=False)
+    w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    cs = angles(1024, 128).to(DEV)
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(5, 2, 128, generator=g).bfloat16().to(DEV) for _ in range(2))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(s, k, v, w, cs)
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step(s, k, v, w, cs)
+    for i in range(3):
+        s["lens"].copy_(torch.tensor([300 - i, 20, 1 + i, 64, 1000], dtype=torch.int32))
+        s["q"].copy_(torch.randn(s["q"].shape, generator=g).bfloat16())
+        k.copy_(torch.randn(k.shape, generator=g).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = o.clone(), lse.clone()
+        eo, el = step(s, k, v, w, cs)
+        assert torch.equal(a, eo) and torch.equal(b, el), i
+    assert ofa.device_error_flags() == 0
+
+
+def test_two_streams_at_once():
+    jobs = []
+    for i in range(4):
+        new, lens = ([1] * 6, [500 + 100 * i] * 6) if i % 2 else ([90, 3], [400, 800])
+        s = paged_inputs(new, lens, 8, 2, 128, 32, seed=i)
+        jobs.append((s, run(s)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(5):
+        for (s, _), st, into in zip(jobs, streams, got):
+            into.append(run(s, stream=st))
+    torch.cuda.synchronize()
+    for (s, want), into in zip(jobs, got):
+        for o, lse in into:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
