@@ -58,6 +58,10 @@ attn_status_t encode(CUtensorMap *m, const void *ptr, int64_t B, int64_t N, int6
 attn_status_t launch_bwd_tc(const attn_bwd_params_t &p, float *dq_acc, const float *crow, const float *lrow,
                             cudaStream_t s);
 
+// A tag for the counters of a call that merges in its own kernel: 48 bits, never 0, another one
+// every call (decode.cu).
+unsigned long long next_call_tag();
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 

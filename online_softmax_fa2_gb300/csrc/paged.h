@@ -1,11 +1,19 @@
-// paged.h -- launcher of the attention over a paged cache (arguments validated by paged_api.cu).
+// paged.h -- host side of the attention over a paged cache (arguments validated by paged_api.cu).
 #pragma once
 
 #include "attn_internal.h"
 
 namespace attn {
+namespace paged {
+struct Args;
+}
 
 size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p);
 attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t s);
+
+// The kernels (paged_rows.cu); maps of the key and value pages with a box of min(page, box_keys) keys.
+constexpr int kRowsBoxKeys = 64;
+attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
+                                cudaStream_t s);
 
 }  // namespace attn

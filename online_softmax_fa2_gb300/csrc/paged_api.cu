@@ -116,6 +116,7 @@ attn_status_t check_paged_fwd(const attn_paged_fwd_params_t *p) {
     if (c.Hkv < 1 || p->Hq < 1 || p->Hq % c.Hkv)
         return fail(ATTN_ERR_INVALID_ARG, "Hq = %lld must be a multiple of Hkv = %lld", (long long)p->Hq, (long long)c.Hkv);
     if (p->Hq / c.Hkv > 64) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv must be <= 64 (got %lld)", (long long)(p->Hq / c.Hkv));
+    if (c.T > (1 << 30) / (p->Hq / c.Hkv)) return fail(ATTN_ERR_UNSUPPORTED, "T * Hq / Hkv must be at most 2^30");
     if (p->max_q < 0) return fail(ATTN_ERR_INVALID_ARG, "max_q is negative");
     return ATTN_OK;
 }

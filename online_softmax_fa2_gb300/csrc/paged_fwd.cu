@@ -1,113 +1,104 @@
-// paged_fwd.cu -- attention of the new tokens of a ragged batch over a paged key/value cache.
-//
-// One warp per (token, query head): the warp walks the visible keys, D / 32 dimensions a lane,
-// with the online update of (m, l, u) ("How Does FlashAttention Preserve Global Softmax Across
-// Tiles?", sections 3 and 5).
-#include <cuda_bf16.h>
+// paged_fwd.cu -- attention of the new tokens of a ragged batch over a paged key/value cache: the
+// choice of a kernel, the cut of its workspace, the tensor maps.
+#include <cudaTypedefs.h>
 
 #include "paged.h"
-#include "sm100_ptx.cuh"
+#include "paged_sched.cuh"
 
 namespace attn {
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encoder();  // fwd_bf16_sm103.cu
+
 namespace {
 
-constexpr int kThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+using namespace paged;
 
-struct PagedArgs {
-    int B, T, Hq, G, causal, page_size, table_width, num_pages;
-    float scale_log2;
-    const __nv_bfloat16 *q, *k, *v;
-    __nv_bfloat16 *o;
-    float *lse;
-    long long qs[2], os[2], ks[3], vs[3], bt_s;
-    const int *bt, *lens, *cu;
-    uint32_t *flags;
+struct Plan {
+    int R, kt, grid, box;
+    size_t off_ml, off_u, bytes;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) paged_simple_kernel(const PagedArgs a) {
-    constexpr int E = D / 32;
-    ptx::grid_dep_wait();
-    ptx::launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= (long long)a.T * a.Hq) return;
-    const int t = (int)(row / a.Hq), h = (int)(row % a.Hq), hk = h / a.G;
-    int b, i, nq;
-    if (a.cu) {
-        b = 0;
-        while (b < a.B && __ldg(a.cu + b + 1) <= t) ++b;
-        if (b >= a.B) return;
-        nq = __ldg(a.cu + b + 1) - __ldg(a.cu + b);
-        i = t - __ldg(a.cu + b);
-        if (i < 0 || i >= nq) return;
-    } else {
-        nq = a.T / a.B;
-        b = t / nq;
-        i = t - b * nq;
-    }
-    const long long room = (long long)a.table_width * a.page_size;
-    const int raw = __ldg(a.lens + b);
-    const int n = (int)(raw < 0 ? 0 : raw > room ? room : raw);
-    if (n != raw && lane == 0) atomicOr(a.flags, kFlagKvLenClamped);
-    const int end = a.causal ? max(0, min(n, i + n - nq + 1)) : n;
-    float q[E], u[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = __bfloat162float(a.q[t * a.qs[0] + h * a.qs[1] + lane * E + e]) * a.scale_log2;
-        u[e] = 0.f;
-    }
-    for (int j = 0; j < end; ++j) {
-        const int page = __ldg(a.bt + b * a.bt_s + j / a.page_size), slot = j % a.page_size;
-        if (page < 0 || page >= a.num_pages) {
-            if (lane == 0) atomicOr(a.flags, kFlagBadIndex);
-            continue;
-        }
-        const __nv_bfloat16 *kr = a.k + page * a.ks[0] + slot * a.ks[1] + hk * a.ks[2] + lane * E;
-        const __nv_bfloat16 *vr = a.v + page * a.vs[0] + slot * a.vs[1] + hk * a.vs[2] + lane * E;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) x = fmaf(q[e], __bfloat162float(kr[e]), x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        const float mn = fmaxf(m, x), al = m == -INFINITY ? 0.f : ptx::ex2(m - mn), p = ptx::ex2(x - mn);
-        l = fmaf(al, l, p);
-#pragma unroll
-        for (int e = 0; e < E; ++e) u[e] = fmaf(al, u[e], p * __bfloat162float(vr[e]));
-        m = mn;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.o[t * a.os[0] + h * a.os[1] + lane * E + e] = __float2bfloat16(l > 0.f ? u[e] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+Plan make_plan(const attn_paged_fwd_params_t &p) {
+    const attn_paged_cache_t &c = p.cache;
+    const int64_t G = p.Hq / c.Hkv;
+    const int64_t most = p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;  // tokens a sequence, or their mean
+    const int64_t rows = most * G;
+    Plan pl;
+    pl.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    pl.kt = 6;
+    pl.box = kRowsBoxKeys;
+    const int sms = sm_count() ? sm_count() : 152;
+    // no more shares than tiles there can be
+    const int64_t keys = c.table_width * c.page_size;
+    const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 1);
+    const int64_t full = (int64_t)sms * (pl.R <= 32 ? 2 : 1);
+    pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
+    const size_t slots = 2 * (size_t)pl.grid;
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    pl.off_ml = up((size_t)pl.grid * sizeof(unsigned long long));
+    pl.off_u = pl.off_ml + up(slots * pl.R * 2 * sizeof(float));
+    pl.bytes = pl.off_u + slots * pl.R * (size_t)c.d * sizeof(float);
+    return pl;
+}
+
+// 4-D map over pages [num_pages, page_size, Hkv, d] with element strides s (page, slot, head); a
+// box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle.
+attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cache_t &c, const int64_t s[3], int box,
+                           const char *name) {
+    auto enc = get_encoder();
+    if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    auto bytes = [](int64_t st, int64_t size) -> cuuint64_t { return size <= 1 ? 16u : (cuuint64_t)(st * 2); };
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
+    cuuint64_t strides[3] = {bytes(s[1], c.page_size), bytes(s[2], c.Hkv), bytes(s[0], c.num_pages)};
+    cuuint32_t b[4] = {64, (cuuint32_t)(c.page_size < box ? c.page_size : box), 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, b, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "TMA descriptor for %s rejected (CUresult %d)", name, (int)r);
+    return ATTN_OK;
+}
+
+int log2_of(int x) {
+    int l = 0;
+    while ((1 << l) < x) ++l;
+    return l;
 }
 
 }  // namespace
 
-size_t paged_fwd_workspace(const attn_paged_fwd_params_t &) { return 0; }
+size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p) { return make_plan(p).bytes; }
 
-attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *, cudaStream_t st) {
+attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t st) {
     const attn_paged_cache_t &c = p.cache;
-    PagedArgs a;
-    a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
-    a.page_size = c.page_size; a.table_width = (int)c.table_width; a.num_pages = (int)c.num_pages;
+    const Plan pl = make_plan(p);
+    Args a;
+    a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hkv = (int)c.Hkv; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
+    a.R = pl.R; a.kt = pl.kt;
+    a.page_log2 = log2_of(c.page_size);
+    a.width = c.num_pages > 0 ? (int)c.table_width : 0;  // without pages there are no keys
+    a.num_pages = (int)c.num_pages;
+    a.min_share = 4;
     a.scale_log2 = p.scale * kLog2e;
     a.q = static_cast<const __nv_bfloat16 *>(p.q);
-    a.k = static_cast<const __nv_bfloat16 *>(c.k_pages);
-    a.v = static_cast<const __nv_bfloat16 *>(c.v_pages);
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.lse = p.lse;
-    for (int i = 0; i < 2; ++i) { a.qs[i] = p.q_stride[i]; a.os[i] = p.o_stride[i]; }
-    for (int i = 0; i < 3; ++i) { a.ks[i] = c.k_stride[i]; a.vs[i] = c.v_stride[i]; }
+    a.qs0 = p.q_stride[0]; a.qs1 = p.q_stride[1]; a.os0 = p.o_stride[0]; a.os1 = p.o_stride[1];
     a.bt = c.block_table; a.bt_s = c.table_stride; a.lens = c.kv_lens; a.cu = c.cu_q;
+    char *ws = static_cast<char *>(workspace);
+    a.counters = reinterpret_cast<unsigned long long *>(ws);
+    a.ml = reinterpret_cast<float *>(ws + pl.off_ml);
+    a.u = reinterpret_cast<float *>(ws + pl.off_u);
+    a.tag = next_call_tag();
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
-    const long long rows = (long long)c.T * p.Hq;
-    const cudaError_t e = launch_pdl(c.d == 64 ? paged_simple_kernel<64> : paged_simple_kernel<128>,
-                                     dim3((unsigned)((rows + 3) / 4)), dim3(kThreads), 0, st, a);
-    return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_fwd launch: %s", cudaGetErrorString(e));
+    CUtensorMap mk{}, mv{};  // not used when there are no pages
+    if (c.num_pages > 0) {
+        attn_status_t r;
+        if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, "k_pages"))) return r;
+        if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, "v_pages"))) return r;
+    }
+    return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }
 
 }  // namespace attn

@@ -1,0 +1,382 @@
+// paged_rows.cu -- attention over a paged cache for few rows per key/value head (a decode step,
+// a few drafted tokens): R = 16 MT rows a block, MT in {1, 2, 4}.
+//
+// The bound is the cache, read once for all rows that share a key head.  Warp 4 copies 64-key
+// tiles of K and V, page by page, into a ring of shared-memory stages with TMA (128-byte
+// swizzle); warps 0-3 compute on them with warp-level tensor-core products (mma.sync m16n8k16):
+// 16 to 64 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
+// copy (64 keys x 16 rows x 128 dimensions take 128 products of the SM's warps against 1.4 us of copy at the
+// SM's share of HBM).
+//   S = Q K^T   warp w takes keys 16 w .. 16 w + 15 of the tile, all rows;
+//   the row maxima of the four warps meet in shared memory, so that the CTA keeps one reference
+//   per row; P = exp2(S - m) goes to shared memory in bf16;
+//   O += P V    warp w takes dimensions [w D/4, (w + 1) D/4), all keys and rows.
+// So no state is merged across warps, and a row's accumulator takes D/16 registers a thread.
+#include <cudaTypedefs.h>
+
+#include "paged.h"
+#include "paged_sched.cuh"
+#include "warp_mma.cuh"
+
+namespace attn {
+
+using namespace paged;
+using namespace wmma16;
+
+namespace {
+
+constexpr int kConsumers = 128, kThreads = kConsumers + 32;
+constexpr int KT = 64;  // keys a tile
+
+template <int D, int MT>
+struct Rows {
+    static constexpr int R = 16 * MT;
+    static constexpr int kPanels = D / 64;
+    static constexpr int kPanelBytes = KT * 128;
+    static constexpr int kTile = kPanels * kPanelBytes;  // K or V
+    static constexpr int kStages = 96 * 1024 / (2 * kTile);
+    static constexpr int kQRow = 2 * D + 16, kPRow = 2 * KT + 16;  // padded: ldmatrix without bank conflicts
+    static constexpr int kQOff = kStages * 2 * kTile;
+    static constexpr int kPOff = kQOff + R * kQRow;
+    static constexpr int kRedOff = kPOff + R * kPRow;  // [4][R] maxima, then sums
+    static constexpr int kCtrlOff = kRedOff + 4 * R * 4;
+};
+
+struct Ctrl {
+    uint64_t full[8], empty[8];
+    Share share;
+    int abort, last;
+};
+
+template <int D, int MT>
+constexpr int smem_bytes() { return Rows<D, MT>::kCtrlOff + (int)sizeof(Ctrl) + 1024; }
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
+    paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    using L = Rows<D, MT>;
+    constexpr int R = L::R, NS = L::kStages, DW = D / 4;  // DW: a warp's dimensions of O
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + L::kCtrlOff);
+    volatile int *abort = &ctrl->abort;
+    float *red = reinterpret_cast<float *>(smem + L::kRedOff);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            ptx::mbar_init(&ctrl->full[s], 1);
+            ptx::mbar_init(&ctrl->empty[s], 4);
+        }
+        ctrl->abort = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::grid_dep_wait();
+    ptx::launch_dependents();
+    if (warp == 4) {
+        const Share sh = find_share(a, blockIdx.x, gridDim.x);
+        if (lane == 0) ctrl->share = sh;
+    }
+    __syncthreads();
+    Walk w;
+    if (!w.begin(a, ctrl->share)) return;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA producer
+        const int pb_log2 = min(a.page_log2, 6), boxes = KT >> pb_log2;
+        int st = 0, ph = 0, issued = 0;
+        bool ok = true;
+        do {
+            if (w.keys == 0) continue;
+            const int *row = a.bt + w.b * a.bt_s;
+            int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
+            for (int j = w.j0; j < w.j1 && ok; ++j) {
+                const int kv0 = j * KT, first = kv0 >> a.page_log2;
+                const int last = (min(kv0 + KT, w.seq.n) - 1) >> a.page_log2;
+                if (held < 0 || last >= held + 32) {
+                    held = first;
+                    const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
+                    pages = at <= end ? __ldg(row + at) : 0;
+                    if (pages < 0 || pages >= a.num_pages) {
+                        atomicOr(a.flags, kFlagBadIndex);
+                        pages = a.num_pages;  // outside the tensor: TMA fills zeros
+                    }
+                }
+                if (issued >= NS) ok = ptx::mbar_wait(&ctrl->empty[st], ph ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                // boxes that hold a key of the sequence; each is kPanels copies of K and of V
+                const int nbox = min(boxes, ((w.seq.n - kv0 - 1) >> pb_log2) + 1);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->full[st], (uint32_t)(nbox * 2 * L::kPanels) << (pb_log2 + 7));
+                __syncwarp();
+                const int box = lane / (2 * L::kPanels), part = lane % (2 * L::kPanels);
+                const int key = kv0 + (box << pb_log2);
+                const int page = __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31));
+                if (box < nbox) {
+                    const int panel = part >> 1;
+                    uint8_t *dst = smem + st * 2 * L::kTile + (part & 1) * L::kTile + panel * L::kPanelBytes + (box << (pb_log2 + 7));
+                    ptx::tma_load_4d(dst, (part & 1) ? &tm_v : &tm_k, &ctrl->full[st], panel * 64,
+                                     key & ((1 << a.page_log2) - 1), w.hk, page);
+                }
+                ++issued;
+                if (++st == NS) { st = 0; ph ^= 1; }
+            }
+        } while (ok && w.next(a));
+        if (*abort) {  // copies in flight land before the CTA leaves
+            const int n = min(issued, NS);
+            for (int i = 0; i < n; ++i) {
+                if (--st < 0) { st = NS - 1; ph ^= 1; }
+                ptx::mbar_wait_quiet(&ctrl->full[st], ph, kWaitLimitNs);
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
+    uint8_t *sQ = smem + L::kQOff, *sP = smem + L::kPOff;
+    int st = 0, ph = 0;
+    do {
+        const int rows = min(R, w.seq.nq * a.G - w.k * R), row0 = w.k * R;
+        // the block's queries (rows past its end are zero)
+        for (int i = threadIdx.x; i < R * (D / 8); i += kConsumers) {
+            const int r = i / (D / 8), c = i % (D / 8), tok = (row0 + r) / a.G, hd = (row0 + r) % a.G;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows)
+                v = *reinterpret_cast<const uint4 *>(a.q + (w.seq.q0 + tok) * a.qs0 + (w.hk * a.G + hd) * a.qs1 + c * 8);
+            *reinterpret_cast<uint4 *>(sQ + r * L::kQRow + c * 16) = v;
+        }
+        int lim[MT][2];  // keys < lim are visible to this lane's rows 16 mt + 8 e + g
+        float m[MT][2], l[MT][2], o[MT][DW / 8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * mt + 8 * e + g;
+                lim[mt][e] = (a.causal && r < rows) ? min(max(w.seq.n - w.seq.nq + (row0 + r) / a.G + 1, 0), w.seq.n) : w.seq.n;
+                m[mt][e] = -INFINITY;
+                l[mt][e] = 0.f;
+            }
+        const int lim0 = a.causal ? min(max(w.seq.n - w.seq.nq + row0 / a.G + 1, 0), w.seq.n) : w.seq.n;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < DW / 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+        consumer_sync();
+
+        for (int j = w.j0; w.keys > 0 && j < w.j1; ++j) {
+            const int kv0 = j * KT;
+            // a wait that gave up is reported; the walk goes on (the four warps keep meeting at the
+            // same barriers) and ends, its waits returning at once
+            ptx::mbar_wait(&ctrl->full[st], ph, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+            __syncwarp();
+            uint8_t *sK = smem + st * 2 * L::kTile, *sV = sK + L::kTile;
+
+            // S of this warp's 16 keys
+            float s[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = 0.f;
+            const int krow = 16 * warp + (mi >> 1) * 8 + mr;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t kf[4];
+                const int ch = (kk & 3) * 2 + (mi & 1);
+                ldsm_x4(smem_addr(sK + (kk >> 2) * L::kPanelBytes + krow * 128 + ((ch ^ (krow & 7)) << 4)), kf);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t qf[4];
+                    ldsm_x4(smem_addr(sQ + (16 * mt + (mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf);
+                    mma_16816(s[mt][0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
+                    mma_16816(s[mt][1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
+                }
+            }
+            // scale, mask, row maxima of this warp's keys
+            const bool edge = kv0 + KT > lim0;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x[4] = {s[mt][0][2 * e], s[mt][0][2 * e + 1], s[mt][1][2 * e], s[mt][1][2 * e + 1]};
+                    const int key = kv0 + 16 * warp + 2 * t;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] *= a.scale_log2;
+                        if (edge && key + (i >> 1) * 8 + (i & 1) >= lim[mt][e]) x[i] = -INFINITY;
+                        s[mt][i >> 1][2 * e + (i & 1)] = x[i];
+                    }
+                    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    if (t == 0) red[warp * R + 16 * mt + 8 * e + g] = mx;
+                }
+            // value rows past the sequence may hold anything: zero, so that 0 * v is 0
+            const bool ragged = kv0 + KT > w.seq.n;
+            if (ragged)
+                for (int i = threadIdx.x; i < KT * L::kPanels * 8; i += kConsumers) {
+                    const int key = (i >> 3) % KT, panel = (i >> 3) / KT;
+                    if (kv0 + key >= w.seq.n)
+                        *reinterpret_cast<uint4 *>(sV + panel * L::kPanelBytes + key * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            consumer_sync();
+            float al[MT][2];
+            bool moved = false;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 16 * mt + 8 * e + g;
+                    const float mn = fmaxf(fmaxf(m[mt][e], fmaxf(red[r], red[R + r])), fmaxf(red[2 * R + r], red[3 * R + r]));
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    al[mt][e] = ptx::ex2(m[mt][e] - ref);
+                    moved |= mn != m[mt][e];
+                    m[mt][e] = mn;
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = ptx::ex2(s[mt][i >> 1][2 * e + (i & 1)] - ref);
+                    l[mt][e] = fmaf(al[mt][e], l[mt][e], (p[0] + p[1]) + (p[2] + p[3]));
+                    uint8_t *pr = sP + r * L::kPRow + (16 * warp + 2 * t) * 2;
+                    *reinterpret_cast<uint32_t *>(pr) = pack_bf16(p[0], p[1]);
+                    *reinterpret_cast<uint32_t *>(pr + 16) = pack_bf16(p[2], p[3]);
+                }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < DW / 8; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt][nt][e] *= al[mt][e >> 1];
+            }
+            consumer_sync();
+            // O of this warp's dimensions
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk) {
+                uint32_t pf[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    ldsm_x4(smem_addr(sP + (16 * mt + (mi & 1) * 8 + mr) * L::kPRow + (2 * kk + (mi >> 1)) * 16), pf[mt]);
+                const int vrow = 16 * kk + (mi & 1) * 8 + mr;
+#pragma unroll
+                for (int nt = 0; nt < DW / 16; ++nt) {
+                    uint32_t vf[4];
+                    const int c = (warp * DW + nt * 16) / 8 + (mi >> 1);
+                    ldsm_x4_trans(smem_addr(sV + (c >> 3) * L::kPanelBytes + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4)), vf);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma_16816(o[mt][2 * nt], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], vf[0], vf[1]);
+                        mma_16816(o[mt][2 * nt + 1], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], vf[2], vf[3]);
+                    }
+                }
+            }
+            if (ragged) ptx::fence_proxy_async_smem();  // the zeros above, before the stage's next copy
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctrl->empty[st]);
+            if (++st == NS) { st = 0; ph ^= 1; }
+        }
+
+        // ------------------------------------------------------------ the piece's rows
+        // row sums: over the quad, then over the four warps
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = l[mt][e];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                l[mt][e] = v;
+            }
+        consumer_sync();  // every warp is done with red's maxima, and with sQ and sP
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (t == 0) red[warp * R + 16 * mt + 8 * e + g] = l[mt][e];
+        consumer_sync();
+        const bool whole = w.whole();
+        const int c0 = whole ? 0 : w.first_share();
+        const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 16 * mt + 8 * e + g;
+                if (r >= rows) continue;
+                const float sum = (red[r] + red[R + r]) + (red[2 * R + r] + red[3 * R + r]);
+                if (whole) {
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const int tok = w.seq.q0 + (row0 + r) / a.G, h = w.hk * a.G + (row0 + r) % a.G;
+                    __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
+#pragma unroll
+                    for (int nt = 0; nt < DW / 8; ++nt)
+                        *reinterpret_cast<uint32_t *>(orow + 8 * nt) = sum > 0.f ? pack_bf16(o[mt][nt][2 * e] * inv, o[mt][nt][2 * e + 1] * inv) : 0u;
+                    if (a.lse && warp == 0 && t == 0)
+                        a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (m[mt][e] + log2f(sum)) * kLn2 : -INFINITY;
+                } else {
+                    float *ur = a.u + (slot * R + r) * D + warp * DW + 2 * t;
+#pragma unroll
+                    for (int nt = 0; nt < DW / 8; ++nt)
+                        *reinterpret_cast<float2 *>(ur + 8 * nt) = make_float2(o[mt][nt][2 * e], o[mt][nt][2 * e + 1]);
+                    if (warp == 0 && t == 0)
+                        *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum > 0.f ? m[mt][e] : -INFINITY, sum);
+                }
+            }
+        consumer_sync();  // red is free again; the state is written
+        if (!whole) {
+            const int n = w.last_share() - c0 + 1;
+            if (threadIdx.x == 0) ctrl->last = count_state(a, a.counters + c0, n);
+            consumer_sync();
+            if (ctrl->last) {
+                // merge: four columns a thread
+                for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers) {
+                    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+                    float M = -INFINITY;
+                    for (int p = 0; p < n; ++p)
+                        M = fmaxf(M, __ldcg(a.ml + ((long long)state_slot(c0 + p, c0) * R + r) * 2));
+                    const float ref = M == -INFINITY ? 0.f : M;
+                    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                    for (int p = 0; p < n; ++p) {
+                        const long long at = (long long)state_slot(c0 + p, c0) * R + r;
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + at * 2));
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.u + at * D + c));
+                        const float f = ptx::ex2(ml.x - ref);
+                        sum = fmaf(f, ml.y, sum);
+                        v[0] = fmaf(f, x.x, v[0]);
+                        v[1] = fmaf(f, x.y, v[1]);
+                        v[2] = fmaf(f, x.z, v[2]);
+                        v[3] = fmaf(f, x.w, v[3]);
+                    }
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    const int tok = w.seq.q0 + (row0 + r) / a.G, h = w.hk * a.G + (row0 + r) % a.G;
+                    *reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + c) =
+                        sum > 0.f ? make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)) : make_uint2(0u, 0u);
+                    if (a.lse && c == 0)
+                        a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+    } while (w.next(a));
+}
+
+template <int D, int MT>
+attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int grid, cudaStream_t st) {
+    auto kern = paged_rows_kernel<D, MT>;
+    const int smem = smem_bytes<D, MT>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);
+    return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_rows launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int d, int grid, cudaStream_t st) {
+    if (d == 64) return a.R == 16 ? launch<64, 1>(mk, mv, a, grid, st) : a.R == 32 ? launch<64, 2>(mk, mv, a, grid, st) : launch<64, 4>(mk, mv, a, grid, st);
+    return a.R == 16 ? launch<128, 1>(mk, mv, a, grid, st) : a.R == 32 ? launch<128, 2>(mk, mv, a, grid, st) : launch<128, 4>(mk, mv, a, grid, st);
+}
+
+}  // namespace attn
