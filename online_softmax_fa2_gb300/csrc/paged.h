@@ -11,9 +11,12 @@ struct Args;
 size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p);
 attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t s);
 
-// The kernels (paged_rows.cu); maps of the key and value pages with a box of min(page, box_keys) keys.
+// The kernels (paged_rows.cu, paged_tc_sm103.cu); maps of the key and value pages with a box of min(page, box_keys) keys.
 constexpr int kRowsBoxKeys = 64;
 attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
                                 cudaStream_t s);
+constexpr int kTcBoxKeys = 128;
+attn_status_t launch_paged_tc(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
+                              cudaStream_t s);
 
 }  // namespace attn

@@ -14,6 +14,7 @@ namespace {
 using namespace paged;
 
 struct Plan {
+    bool tc;
     int R, kt, grid, box;
     size_t off_ml, off_u, bytes;
 };
@@ -24,18 +25,19 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t most = p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;  // tokens a sequence, or their mean
     const int64_t rows = most * G;
     Plan pl;
-    pl.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    pl.kt = 6;
-    pl.box = kRowsBoxKeys;
+    pl.tc = rows > 32;
+    pl.R = pl.tc ? 256 : rows <= 16 ? 16 : 32;
+    pl.kt = pl.tc ? 7 : 6;
+    pl.box = pl.tc ? kTcBoxKeys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 1);
-    const int64_t full = (int64_t)sms * (pl.R <= 32 ? 2 : 1);
+    const int64_t full = (int64_t)sms * (pl.tc ? 1 : 2);
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     const size_t slots = 2 * (size_t)pl.grid;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.off_ml = up((size_t)pl.grid * sizeof(unsigned long long));
+    pl.off_ml = up(slots * sizeof(unsigned long long));
     pl.off_u = pl.off_ml + up(slots * pl.R * 2 * sizeof(float));
     pl.bytes = pl.off_u + slots * pl.R * (size_t)c.d * sizeof(float);
     return pl;
@@ -98,6 +100,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
         if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, "k_pages"))) return r;
         if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, "v_pages"))) return r;
     }
+    if (pl.tc) return launch_paged_tc(mk, mv, a, (int)c.d, pl.grid, st);
     return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }
 

@@ -1,0 +1,469 @@
+// paged_tc_sm103.cu -- attention over a paged cache for many rows per key/value head (prompt
+// chunks) on the 5th-generation tensor cores.
+//
+// A block is 256 rows of one (sequence, key/value head) -- tokens times the query heads that share
+// the head, so a key or value tile in shared memory serves all of them -- as two 128-row tiles A
+// and B whose softmax warpgroups take turns with the tensor cores, as in the two-tile prefill
+// kernel: while one warpgroup turns its S into P, the products of the other run.  One CTA an SM
+// walks its share of the line of key tiles (paged_sched.cuh).
+//
+// Roles (384 threads):
+//   warp 0       TMA producer: 128-key tiles of K and V into two rings, a box a page (or a part of
+//                one), the boxes of a tile issued by as many lanes.
+//   warp 1       tensor-core issuer (one thread); owns the 512 TMEM columns:
+//                  S_A/P_A [0,128)  S_B/P_B [128,256)  O_A [256,384)  O_B [384,512).
+//   warps 4-7    rows of tile A, one thread a row (its TMEM lane);  warps 8-11  rows of tile B.
+//                They also bring their rows of Q into shared memory, the next block's right
+//                after the last P of this one, so that its first S runs under this one's epilogue.
+// A row's state over its part of an item goes to the workspace when the item is cut; tiles A and B
+// count and merge apart.
+#include <cudaTypedefs.h>
+
+#include "fwd_bf16_common.cuh"
+#include "paged.h"
+#include "paged_sched.cuh"
+
+namespace attn {
+
+using paged::Share;
+using paged::Walk;
+
+namespace {
+
+using bf16fwd::BK;
+using bf16fwd::BQ;
+using bf16fwd::kPanelBytes;
+using bf16fwd::kSmemMax;
+using paged::kLn2;
+using paged::kWaitLimitNs;
+
+constexpr int kThreads = 384;
+// Registers: launched at 168 a thread (384 x 168 = 64512), split 128 x 56 + 256 x 224 = 64512.
+constexpr uint32_t kRegsIssue = 56, kRegsSoftmax = 224;
+static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreads * 168, "register split");
+constexpr uint32_t kTmemCols = 512;
+
+struct Ctrl {
+    uint64_t q_full[2], s_full[2], p_full[2], o_final[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t final_mma, group[2];  // group: the 128 threads of a warpgroup meet (bounded waits)
+    Share share;
+    uint32_t tmem_base;
+    int abort, last[2];
+};
+
+template <int D>
+struct Layout {
+    static constexpr int kTile = (D / 64) * kPanelBytes;  // 128 rows of Q, K or V
+    static constexpr int kKStages = D == 128 ? 3 : 4, kVStages = D == 128 ? 2 : 4;
+    static constexpr int kKOff = 2 * kTile, kVOff = kKOff + kKStages * kTile;
+    static constexpr int kDataBytes = kVOff + kVStages * kTile;
+    static constexpr int kBytes = kDataBytes + (int)sizeof(Ctrl) + 1024;
+    static_assert(kBytes <= kSmemMax, "shared memory budget");
+};
+
+// The two tiles of a piece: key tiles of each in the whole item, and in the piece.
+struct Tiles {
+    int t[2], n[2];
+};
+__device__ __forceinline__ Tiles tiles_of(const paged::Args &a, const Walk &w) {
+    Tiles r;
+    const int rows = w.seq.nq * a.G - w.k * a.R;  // >= 1
+    int ka = w.keys;
+    if (rows > BQ && a.causal) {
+        const int last = (w.k * a.R + BQ - 1) / a.G;
+        ka = min(max(w.seq.n - w.seq.nq + last + 1, 0), w.seq.n);
+    }
+    r.t[0] = (ka + BK - 1) / BK;
+    r.t[1] = rows > BQ ? (w.keys + BK - 1) / BK : 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) r.n[x] = max(0, min(w.j1, r.t[x]) - w.j0);
+    return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
+    using L = Layout<D>;
+    constexpr int KS = L::kKStages, VS = L::kVStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + L::kDataBytes);
+    volatile int *abort = &ctrl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            ptx::mbar_init(&ctrl->q_full[x], BQ);
+            ptx::mbar_init(&ctrl->s_full[x], 1);
+            ptx::mbar_init(&ctrl->p_full[x], BQ);
+            ptx::mbar_init(&ctrl->o_final[x], 1);
+            ptx::mbar_init(&ctrl->group[x], BQ);
+        }
+        for (int s = 0; s < KS; ++s) {
+            ptx::mbar_init(&ctrl->k_full[s], 1);
+            ptx::mbar_init(&ctrl->k_empty[s], 1);
+        }
+        for (int s = 0; s < VS; ++s) {
+            ptx::mbar_init(&ctrl->v_full[s], 1);
+            ptx::mbar_init(&ctrl->v_empty[s], 1);
+        }
+        ptx::mbar_init(&ctrl->final_mma, 1);
+        ctrl->abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&ctrl->tmem_base, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_dep_wait();
+    ptx::launch_dependents();
+    if (warp == 2) {
+        const Share sh = paged::find_share(a, blockIdx.x, gridDim.x);
+        if (lane == 0) ctrl->share = sh;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = ctrl->tmem_base;
+    Walk w;
+    const bool any = w.begin(a, ctrl->share);
+
+    if (warp < 4) {
+        ptx::regs_dec<kRegsIssue>();
+        if (warp == 0 && any) {
+            // -------------------------------------------------------- TMA producer
+            const int pb_log2 = min(a.page_log2, 7), boxes = BK >> pb_log2;
+            int ks = 0, vs = 0, kp = 0, vp = 0, nk = 0, nv = 0;
+            bool ok = true;
+            do {
+                if (w.keys == 0) continue;
+                const int *row = a.bt + w.b * a.bt_s;
+                int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
+                for (int j = w.j0; j < w.j1; ++j) {
+                    const int kv0 = j * BK, first = kv0 >> a.page_log2;
+                    const int last = (min(kv0 + BK, w.seq.n) - 1) >> a.page_log2;
+                    if (held < 0 || last >= held + 32) {
+                        held = first;
+                        const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
+                        pages = at <= end ? __ldg(row + at) : 0;
+                        if (pages < 0 || pages >= a.num_pages) {
+                            atomicOr(a.flags, kFlagBadIndex);
+                            pages = a.num_pages;  // outside the tensor: TMA fills zeros
+                        }
+                    }
+                    // boxes that hold a key of the sequence, D / 64 copies each
+                    const int nbox = min(boxes, ((w.seq.n - kv0 - 1) >> pb_log2) + 1);
+                    const uint32_t bytes = (uint32_t)(nbox * (D / 64)) << (pb_log2 + 7);
+                    const int box = lane / (D / 64), panel = lane % (D / 64);
+                    const int key = kv0 + (box << pb_log2), slot = key & ((1 << a.page_log2) - 1);
+                    const int page = __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31));
+                    const int off = panel * kPanelBytes + (box << (pb_log2 + 7));
+                    if (nk >= KS) ok = ptx::mbar_wait(&ctrl->k_empty[ks], kp ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->k_full[ks], bytes);
+                    __syncwarp();
+                    if (box < nbox)
+                        ptx::tma_load_4d(smem + L::kKOff + ks * L::kTile + off, &tm_k, &ctrl->k_full[ks], panel * 64, slot, w.hk, page);
+                    ++nk;
+                    if (++ks == KS) { ks = 0; kp ^= 1; }
+                    if (nv >= VS) ok = ptx::mbar_wait(&ctrl->v_empty[vs], vp ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->v_full[vs], bytes);
+                    __syncwarp();
+                    if (box < nbox)
+                        ptx::tma_load_4d(smem + L::kVOff + vs * L::kTile + off, &tm_v, &ctrl->v_full[vs], panel * 64, slot, w.hk, page);
+                    ++nv;
+                    if (++vs == VS) { vs = 0; vp ^= 1; }
+                }
+            } while (ok && w.next(a));
+            if (!ok || *abort) {  // copies in flight land before the CTA leaves
+                for (int i = min(nk, KS); i > 0; --i) {
+                    if (--ks < 0) { ks = KS - 1; kp ^= 1; }
+                    ptx::mbar_wait_quiet(&ctrl->k_full[ks], kp, kWaitLimitNs);
+                }
+                for (int i = min(nv, VS); i > 0; --i) {
+                    if (--vs < 0) { vs = VS - 1; vp ^= 1; }
+                    ptx::mbar_wait_quiet(&ctrl->v_full[vs], vp, kWaitLimitNs);
+                }
+            }
+        } else if (warp == 1 && lane == 0 && any) {
+            // -------------------------------------------------------- tensor-core issuer
+            constexpr uint32_t kIdS = ptx::idesc_bf16_f32(BQ, BK, false);
+            constexpr uint32_t kIdO = ptx::idesc_bf16_f32(BQ, D, true);
+            const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem), 16);
+            constexpr uint32_t kStep = L::kTile >> 4, kKLo = L::kKOff >> 4;
+            constexpr uint32_t kVLo = (L::kVOff >> 4) + (((uint32_t)kPanelBytes >> 4) << 16) - (1u << 16);
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+            };
+            auto s_products = [&](int x, int ks) {
+                uint32_t ql = q_lo, tm = tmem;
+                ptx::opaque(ql);
+                ptx::opaque(tm);
+                const uint32_t qt = ql + x * kStep, kt = ql + kKLo + ks * kStep;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk / 4) * kPanelBytes + (kk % 4) * 32) >> 4;
+                    ptx::mma_ss_lo(tm + x * BQ, qt + off, kt + off, kIdS, kk > 0 ? 1u : 0u);
+                }
+                ptx::mma_commit(&ctrl->s_full[x]);
+            };
+            auto pv_products = [&](int x, int vs, bool first) {
+                uint32_t ql = q_lo, tm = tmem;
+                ptx::opaque(ql);
+                ptx::opaque(tm);
+                const uint32_t vt = ql + kVLo + vs * kStep;
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                    ptx::mma_ts_lo(tm + 2 * BQ + x * BQ, tm + x * BQ + kk * 8, vt + ((kk * 16 * 128) >> 4), kIdO,
+                                   (!first || kk > 0) ? 1u : 0u);
+            };
+            // ring slots and barrier parities: 0 K full, 1 V full, 2/3 Q_A/Q_B, 4/5 P_A/P_B
+            int ks = 0, vs = 0;
+            uint32_t ph = 0;
+            auto par = [&](int bit) -> uint32_t { return (ph >> bit) & 1u; };
+            auto flip = [&](int bit) { ph ^= 1u << bit; };
+            bool ok = true;
+            do {
+                if (w.keys == 0) continue;
+                const Tiles tl = tiles_of(a, w);
+                const int nmax = w.j1 - w.j0;
+                if (!wait(&ctrl->k_full[ks], par(0))) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (ok && tl.n[x] > 0) {
+                        ok = wait(&ctrl->q_full[x], par(2 + x));
+                        if (!ok) break;
+                        flip(2 + x);
+                        ptx::tc_fence_after();
+                        s_products(x, ks);
+                    }
+                if (!ok) break;
+                ptx::mma_commit(&ctrl->k_empty[ks]);
+                if (++ks == KS) { ks = 0; flip(0); }
+                for (int i = 0; ok && i < nmax; ++i) {
+                    // O_x += P_x V, then S_x of the next tile into the columns P_x occupies: the
+                    // products of one thread execute in issue order
+                    const bool more = i + 1 < nmax;
+                    if (!wait(&ctrl->v_full[vs], par(1)) || (more && !wait(&ctrl->k_full[ks], par(0)))) { ok = false; break; }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (ok && i < tl.n[x]) {
+                            ok = wait(&ctrl->p_full[x], par(4 + x));
+                            if (!ok) break;
+                            flip(4 + x);
+                            ptx::tc_fence_after();
+                            pv_products(x, vs, i == 0);
+                            if (i == tl.n[x] - 1) ptx::mma_commit(&ctrl->o_final[x]);
+                            else s_products(x, ks);
+                        }
+                    if (!ok) break;
+                    ptx::mma_commit(&ctrl->v_empty[vs]);
+                    if (more) {
+                        ptx::mma_commit(&ctrl->k_empty[ks]);
+                        if (++ks == KS) { ks = 0; flip(0); }
+                    }
+                    if (++vs == VS) { vs = 0; flip(1); }
+                }
+            } while (ok && w.next(a));
+            ptx::mma_commit(&ctrl->final_mma);
+            if (!ptx::mbar_wait_quiet(&ctrl->final_mma, 0, kWaitLimitNs)) atomicOr(a.flags, kFlagWaitTimeout);
+        }
+    } else {
+        ptx::regs_inc<kRegsSoftmax>();
+        // ------------------------------------------------------------ softmax warpgroups
+        const int X = warp >= 8 ? 1 : 0;
+        const int r = (int)threadIdx.x - 128 - X * BQ;  // row in the tile == TMEM lane
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_col = X * BQ, o_col = 2 * BQ + X * BQ;
+        const float c = a.scale_log2;
+        auto wait_warp = [&](uint64_t *bar, uint32_t parity) -> bool {
+            const bool ok = ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+            return __all_sync(0xffffffffu, ok);
+        };
+        uint32_t gph = 0;
+        auto group_sync = [&]() -> bool {
+            ptx::mbar_arrive(&ctrl->group[X]);
+            const bool met = wait_warp(&ctrl->group[X], gph);
+            gph ^= 1;
+            return met;
+        };
+        // this thread's row of the piece's queries into tile X's buffer (zeros past the block's rows)
+        auto bring_q = [&](const Walk &p) {
+            const int row = p.k * a.R + X * BQ + r;
+            uint8_t *dst = smem + X * L::kTile + r * 128;
+            if (row < p.seq.nq * a.G) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (long long)(p.seq.q0 + row / a.G) * a.qs0 +
+                                                                   (p.hk * a.G + row % a.G) * a.qs1);
+                uint4 v[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<uint4 *>(dst + (i / 8) * kPanelBytes + (((i % 8) ^ (r & 7)) << 4)) = v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<uint4 *>(dst + (i / 8) * kPanelBytes + ((i % 8) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&ctrl->q_full[X]);
+        };
+        int vs = 0;                     // V ring slot and phase, for the rows that are zeroed
+        uint32_t vph = 0, sph = 0, oph = 0;
+        bool ok = true, more = any;
+        if (any && tiles_of(a, w).n[X] > 0) bring_q(w);
+        while (more && ok) {
+            __syncwarp();
+            const Tiles tl = tiles_of(a, w);
+            const int n = tl.n[X], i0 = w.k * a.R + X * BQ, i = i0 + r, nmax = w.keys == 0 ? 0 : w.j1 - w.j0;
+            const bool mine = i < w.seq.nq * a.G;
+            const int tok = i / a.G, seqn = w.seq.n;
+            const int lim = a.causal && mine ? min(max(seqn - w.seq.nq + tok + 1, 0), seqn) : seqn;
+            const int lim0 = a.causal ? min(max(seqn - w.seq.nq + i0 / a.G + 1, 0), seqn) : seqn;
+            float m_run = -INFINITY, l_run = 0.f;
+            for (int jj = 0; jj < n; ++jj) {
+                const int kv0 = (w.j0 + jj) * BK;
+                if (!wait_warp(&ctrl->s_full[X], sph)) { ok = false; break; }
+                sph ^= 1;
+                ptx::tc_fence_after();
+                float x[BK];
+                bf16fwd::load_s_row(lane_addr + s_col, x);
+                const float mt = bf16fwd::tile_logits<false>(x, c, kv0, kv0 + BK > lim0, lim);
+                bool rescale;
+                const float alpha = bf16fwd::update_max(mt, m_run, rescale);
+                const float lsum = bf16fwd::tile_exp<false>(x, c, m_run);
+                l_run = fmaf(alpha, l_run, lsum);
+                if (__any_sync(0xffffffffu, rescale)) bf16fwd::scale_o<D>(lane_addr + o_col, alpha);
+                // value rows past the sequence may hold anything: the first of the two tiles that
+                // uses this V zeroes them before its product reads them
+                if (kv0 + BK > seqn && (X == 0 || jj >= tl.n[0])) {
+                    if (!wait_warp(&ctrl->v_full[vs], vph)) { ok = false; break; }
+                    if (kv0 + r >= seqn) bf16fwd::zero_v_row<D>(smem + L::kVOff + vs * L::kTile, r);
+                    ptx::fence_proxy_async_smem();
+                }
+                if (++vs == VS) { vs = 0; vph ^= 1; }
+                bf16fwd::store_p(lane_addr + s_col, x);
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&ctrl->p_full[X]);
+            }
+            if (!ok) break;
+            for (int jj = n; jj < nmax; ++jj)  // tiles that only the other rows see
+                if (++vs == VS) { vs = 0; vph ^= 1; }
+            // where this row goes, before the walk moves on
+            const bool whole = w.j0 == 0 && w.j1 >= tl.t[X];
+            const int c0 = w.first_share();
+            const int cn = tl.t[X] > 0 ? (int)((w.t - w.j0 + tl.t[X] - 1) / w.s.per) - c0 + 1 : 1;
+            const bool first = w.j0 == 0;
+            __nv_bfloat16 *orow = nullptr;
+            float *lrow = nullptr;
+            if (mine) {
+                const long long t = w.seq.q0 + tok;
+                const int h = w.hk * a.G + i % a.G;
+                orow = a.o + t * a.os0 + h * a.os1;
+                lrow = a.lse ? a.lse + t * a.Hq + h : nullptr;
+            }
+            // the next block's queries, under the last product of this one (this tile's last S, the
+            // buffer's last reader, is done)
+            more = w.next(a);
+            if (more && tiles_of(a, w).n[X] > 0) bring_q(w);
+            if (n == 0) {
+                // no key tile here: the item's first share writes rows that see no key at all
+                if (tl.t[X] == 0 && first && mine) bf16fwd::write_empty_row<D>(orow, lrow);
+                continue;
+            }
+            if (!wait_warp(&ctrl->o_final[X], oph)) { ok = false; break; }
+            oph ^= 1;
+            ptx::tc_fence_after();
+            if (whole) {
+                bf16fwd::write_row<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
+                ptx::tc_fence_before();
+                continue;
+            }
+            // the state of this part
+            const long long slot = paged::state_slot(blockIdx.x, c0);
+            const long long at = slot * a.R + X * BQ + r;
+            *reinterpret_cast<float2 *>(a.ml + at * 2) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t ov[32];
+                ptx::tmem_ld32(lane_addr + o_col + cc * 32, ov);
+                ptx::tmem_ld_wait();
+                ptx::reg_fence(ov);
+                uint4 *dst = reinterpret_cast<uint4 *>(a.u + at * D + cc * 32);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) dst[t] = make_uint4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
+            }
+            ptx::tc_fence_before();
+            if (!group_sync()) { ok = false; break; }
+            if (r == 0) ctrl->last[X] = paged::count_state(a, a.counters + 2 * c0 + X, cn);
+            if (!group_sync()) { ok = false; break; }
+            if (!ctrl->last[X] || !mine) continue;
+            // merge, a row a thread: the parts' common reference and sum, then the columns
+            float M = -INFINITY;
+            const long long row = X * BQ + r;
+            for (int p = 0; p < cn; ++p)
+                M = fmaxf(M, __ldcg(a.ml + (paged::state_slot(c0 + p, c0) * (long long)a.R + row) * 2));
+            const float ref = M == -INFINITY ? 0.f : M;
+            float sum = 0.f;
+            for (int p = 0; p < cn; ++p) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + (paged::state_slot(c0 + p, c0) * (long long)a.R + row) * 2));
+                sum = fmaf(ptx::ex2(ml.x - ref), ml.y, sum);
+            }
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            if (lrow) *lrow = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+            for (int cc = 0; cc < D; cc += 32) {
+                float v[32];
+#pragma unroll
+                for (int t = 0; t < 32; ++t) v[t] = 0.f;
+                for (int p = 0; p < cn; ++p) {
+                    const long long at2 = paged::state_slot(c0 + p, c0) * (long long)a.R + row;
+                    const float f = ptx::ex2(__ldcg(a.ml + at2 * 2) - ref);
+                    const float4 *src = reinterpret_cast<const float4 *>(a.u + at2 * D + cc);
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        const float4 y = __ldcg(src + t);
+                        v[4 * t] = fmaf(f, y.x, v[4 * t]);
+                        v[4 * t + 1] = fmaf(f, y.y, v[4 * t + 1]);
+                        v[4 * t + 2] = fmaf(f, y.z, v[4 * t + 2]);
+                        v[4 * t + 3] = fmaf(f, y.w, v[4 * t + 3]);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        pk[e] = sum > 0.f ? ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv) : 0u;
+                    *reinterpret_cast<uint4 *>(orow + cc + 8 * t) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid, cudaStream_t st) {
+    auto kern = paged_tc_kernel<D>;
+    int smem = Layout<D>::kBytes;
+    if (smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);
+    return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+attn_status_t launch_paged_tc(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid, cudaStream_t st) {
+    return d == 64 ? launch<64>(mk, mv, a, grid, st) : launch<128>(mk, mv, a, grid, st);
+}
+
+}  // namespace attn
