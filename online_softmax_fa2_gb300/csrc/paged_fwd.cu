@@ -3,7 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include "paged.h"
-#include "paged_sched.cuh"
+#include "paged_merge.cuh"
 
 namespace attn {
 
@@ -33,18 +33,21 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 1);
-    const int64_t full = (int64_t)sms * (pl.tc ? 1 : 2);
+    const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
+    if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = 2 * (size_t)pl.grid;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.off_ml = up(slots * sizeof(unsigned long long));
+    pl.off_ml = up((pl.tc ? 2 : 1) * (size_t)counter_words(pl.grid) * sizeof(unsigned long long));
     pl.off_u = pl.off_ml + up(slots * pl.R * 2 * sizeof(float));
     pl.bytes = pl.off_u + slots * pl.R * (size_t)c.d * sizeof(float);
     return pl;
 }
 
 // 4-D map over pages [num_pages, page_size, Hkv, d] with element strides s (page, slot, head); a
-// box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle.
+// box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle.  L2 fetches whole
+// rows of a head and no more: with 64 dimensions (128 bytes) a 256-byte fetch would bring the next
+// head's row too (351 MB read for 278 MB of cache, measured).
 attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cache_t &c, const int64_t s[3], int box,
                            const char *name) {
     auto enc = get_encoder();
@@ -55,7 +58,8 @@ attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cac
     cuuint32_t b[4] = {64, (cuuint32_t)(c.page_size < box ? c.page_size : box), 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, b, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "TMA descriptor for %s rejected (CUresult %d)", name, (int)r);
     return ATTN_OK;

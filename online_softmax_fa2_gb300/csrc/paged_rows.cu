@@ -1,10 +1,10 @@
 // paged_rows.cu -- attention over a paged cache for few rows per key/value head (a decode step,
-// a few drafted tokens): R = 16 MT rows a block, MT in {1, 2, 4}.
+// a few drafted tokens): R = 16 MT rows a block, MT in {1, 2}.
 //
 // The bound is the cache, read once for all rows that share a key head.  Warp 4 copies 64-key
 // tiles of K and V, page by page, into a ring of shared-memory stages with TMA (128-byte
 // swizzle); warps 0-3 compute on them with warp-level tensor-core products (mma.sync m16n8k16):
-// 16 to 64 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
+// 16 or 32 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
 // copy (64 keys x 16 rows x 128 dimensions take 128 products of the SM's warps against 1.4 us of copy at the
 // SM's share of HBM).
 //   S = Q K^T   warp w takes keys 16 w .. 16 w + 15 of the tile, all rows;
@@ -15,7 +15,7 @@
 #include <cudaTypedefs.h>
 
 #include "paged.h"
-#include "paged_sched.cuh"
+#include "paged_merge.cuh"
 #include "warp_mma.cuh"
 
 namespace attn {
@@ -34,7 +34,8 @@ struct Rows {
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = KT * 128;
     static constexpr int kTile = kPanels * kPanelBytes;  // K or V
-    static constexpr int kStages = 96 * 1024 / (2 * kTile);
+    static constexpr int kBlocks = rows_blocks(D);
+    static constexpr int kStages = (kBlocks == 3 ? 64 : 96) * 1024 / (2 * kTile);
     static constexpr int kQRow = 2 * D + 16, kPRow = 2 * KT + 16;  // padded: ldmatrix without bank conflicts
     static constexpr int kQOff = kStages * 2 * kTile;
     static constexpr int kPOff = kQOff + R * kQRow;
@@ -54,7 +55,7 @@ constexpr int smem_bytes() { return Rows<D, MT>::kCtrlOff + (int)sizeof(Ctrl) + 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
     using L = Rows<D, MT>;
     constexpr int R = L::R, NS = L::kStages, DW = D / 4;  // DW: a warp's dimensions of O
@@ -177,11 +178,11 @@ __global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
             uint8_t *sK = smem + st * 2 * L::kTile, *sV = sK + L::kTile;
 
             // S of this warp's 16 keys
-            float s[MT][2][4];
+            float s[MT][2][4], s2[MT][2][4];  // even and odd k steps: two chains of products
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = s2[mt][0][e] = s2[mt][1][e] = 0.f;
             const int krow = 16 * warp + (mi >> 1) * 8 + mr;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
                 for (int mt = 0; mt < MT; ++mt) {
                     uint32_t qf[4];
                     ldsm_x4(smem_addr(sQ + (16 * mt + (mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf);
-                    mma_16816(s[mt][0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
-                    mma_16816(s[mt][1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
+                    mma_16816((kk & 1 ? s2 : s)[mt][0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
+                    mma_16816((kk & 1 ? s2 : s)[mt][1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
                 }
             }
             // scale, mask, row maxima of this warp's keys
@@ -202,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x[4] = {s[mt][0][2 * e], s[mt][0][2 * e + 1], s[mt][1][2 * e], s[mt][1][2 * e + 1]};
+                    float x[4] = {s[mt][0][2 * e] + s2[mt][0][2 * e], s[mt][0][2 * e + 1] + s2[mt][0][2 * e + 1],
+                                  s[mt][1][2 * e] + s2[mt][1][2 * e], s[mt][1][2 * e + 1] + s2[mt][1][2 * e + 1]};
                     const int key = kv0 + 16 * warp + 2 * t;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -325,41 +327,19 @@ __global__ void __launch_bounds__(kThreads, MT == 4 ? 1 : 2)
                         *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum > 0.f ? m[mt][e] : -INFINITY, sum);
                 }
             }
-        consumer_sync();  // red is free again; the state is written
-        if (!whole) {
-            const int n = w.last_share() - c0 + 1;
-            if (threadIdx.x == 0) ctrl->last = count_state(a, a.counters + c0, n);
-            consumer_sync();
-            if (ctrl->last) {
-                // merge: four columns a thread
-                for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers) {
-                    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
-                    float M = -INFINITY;
-                    for (int p = 0; p < n; ++p)
-                        M = fmaxf(M, __ldcg(a.ml + ((long long)state_slot(c0 + p, c0) * R + r) * 2));
-                    const float ref = M == -INFINITY ? 0.f : M;
-                    float sum = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-                    for (int p = 0; p < n; ++p) {
-                        const long long at = (long long)state_slot(c0 + p, c0) * R + r;
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + at * 2));
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(a.u + at * D + c));
-                        const float f = ptx::ex2(ml.x - ref);
-                        sum = fmaf(f, ml.y, sum);
-                        v[0] = fmaf(f, x.x, v[0]);
-                        v[1] = fmaf(f, x.y, v[1]);
-                        v[2] = fmaf(f, x.z, v[2]);
-                        v[3] = fmaf(f, x.w, v[3]);
-                    }
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        if (!whole)
+            finish_cut<D, MT == 1 ? 2 : 1>(
+                a, a.counters, gridDim.x, 0, rows, blockIdx.x, c0, w.last_share() - c0 + 1, threadIdx.x, &ctrl->last,
+                [] {
+                    consumer_sync();
+                    return true;
+                },
+                [&](int r, __nv_bfloat16 *&orow, float *&lse) {
                     const int tok = w.seq.q0 + (row0 + r) / a.G, h = w.hk * a.G + (row0 + r) % a.G;
-                    *reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + c) =
-                        sum > 0.f ? make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)) : make_uint2(0u, 0u);
-                    if (a.lse && c == 0)
-                        a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
-                }
-            }
-        }
+                    orow = a.o + tok * a.os0 + h * a.os1;
+                    lse = a.lse ? a.lse + (long long)tok * a.Hq + h : nullptr;
+                });
+        consumer_sync();  // red is free again
     } while (w.next(a));
 }
 
@@ -375,8 +355,8 @@ attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a
 }  // namespace
 
 attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int d, int grid, cudaStream_t st) {
-    if (d == 64) return a.R == 16 ? launch<64, 1>(mk, mv, a, grid, st) : a.R == 32 ? launch<64, 2>(mk, mv, a, grid, st) : launch<64, 4>(mk, mv, a, grid, st);
-    return a.R == 16 ? launch<128, 1>(mk, mv, a, grid, st) : a.R == 32 ? launch<128, 2>(mk, mv, a, grid, st) : launch<128, 4>(mk, mv, a, grid, st);
+    if (d == 64) return a.R == 16 ? launch<64, 1>(mk, mv, a, grid, st) : launch<64, 2>(mk, mv, a, grid, st);
+    return a.R == 16 ? launch<128, 1>(mk, mv, a, grid, st) : launch<128, 2>(mk, mv, a, grid, st);
 }
 
 }  // namespace attn

@@ -21,7 +21,7 @@
 
 #include "fwd_bf16_common.cuh"
 #include "paged.h"
-#include "paged_sched.cuh"
+#include "paged_merge.cuh"
 
 namespace attn {
 
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c0 = w.first_share();
             const int cn = tl.t[X] > 0 ? (int)((w.t - w.j0 + tl.t[X] - 1) / w.s.per) - c0 + 1 : 1;
             const bool first = w.j0 == 0;
+            const int rows = w.seq.nq * a.G - w.k * a.R, q0 = w.seq.q0, hk = w.hk;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
             if (mine) {
@@ -396,49 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < 8; ++t) dst[t] = make_uint4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
             }
             ptx::tc_fence_before();
-            if (!group_sync()) { ok = false; break; }
-            if (r == 0) ctrl->last[X] = paged::count_state(a, a.counters + 2 * c0 + X, cn);
-            if (!group_sync()) { ok = false; break; }
-            if (!ctrl->last[X] || !mine) continue;
-            // merge, a row a thread: the parts' common reference and sum, then the columns
-            float M = -INFINITY;
-            const long long row = X * BQ + r;
-            for (int p = 0; p < cn; ++p)
-                M = fmaxf(M, __ldcg(a.ml + (paged::state_slot(c0 + p, c0) * (long long)a.R + row) * 2));
-            const float ref = M == -INFINITY ? 0.f : M;
-            float sum = 0.f;
-            for (int p = 0; p < cn; ++p) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.ml + (paged::state_slot(c0 + p, c0) * (long long)a.R + row) * 2));
-                sum = fmaf(ptx::ex2(ml.x - ref), ml.y, sum);
-            }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            if (lrow) *lrow = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
-            for (int cc = 0; cc < D; cc += 32) {
-                float v[32];
-#pragma unroll
-                for (int t = 0; t < 32; ++t) v[t] = 0.f;
-                for (int p = 0; p < cn; ++p) {
-                    const long long at2 = paged::state_slot(c0 + p, c0) * (long long)a.R + row;
-                    const float f = ptx::ex2(__ldcg(a.ml + at2 * 2) - ref);
-                    const float4 *src = reinterpret_cast<const float4 *>(a.u + at2 * D + cc);
-#pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        const float4 y = __ldcg(src + t);
-                        v[4 * t] = fmaf(f, y.x, v[4 * t]);
-                        v[4 * t + 1] = fmaf(f, y.y, v[4 * t + 1]);
-                        v[4 * t + 2] = fmaf(f, y.z, v[4 * t + 2]);
-                        v[4 * t + 3] = fmaf(f, y.w, v[4 * t + 3]);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        pk[e] = sum > 0.f ? ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv) : 0u;
-                    *reinterpret_cast<uint4 *>(orow + cc + 8 * t) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-            }
+            ok = paged::finish_cut<D, 4>(
+                a, a.counters + X * paged::counter_words(gridDim.x), gridDim.x, X * BQ, min(BQ, rows - X * BQ), blockIdx.x, c0,
+                cn, r, &ctrl->last[X], group_sync, [&](int rr, __nv_bfloat16 *&orow, float *&lse) {
+                    const long long t = q0 + (i0 + rr) / a.G;
+                    const int h = hk * a.G + (i0 + rr) % a.G;
+                    orow = a.o + t * a.os0 + h * a.os1;
+                    lse = a.lse ? a.lse + t * a.Hq + h : nullptr;
+                });
         }
     }
     ptx::tc_fence_before();

@@ -269,3 +269,35 @@ def test_two_streams_at_once():
     for (s, want), into in zip(jobs, got):
         for o, lse in into:
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hkv,d,page", [
+    ([1], [200001], 2, 1, 64, 64),         # hundreds of shares of one row block: merged in two levels
+    ([3, 1], [90000, 5], 4, 1, 128, 128),
+    ([40], [60011], 2, 1, 64, 32),         # the same on the 128-row tiles
+    ([5, 150], [40000, 30000], 7, 1, 128, 64),
+])
+def test_one_long_cache_over_the_whole_gpu(new, lens, Hq, Hkv, d, page):
+    s = paged_inputs(new, lens, Hq, Hkv, d, page, seed=11)
+    o, lse = run(s, max_q=max(new))
+    check_paged(o, lse, s, new, lens, True, 1 / math.sqrt(d))
+    o2, lse2 = run(s, max_q=max(new))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and ofa.device_error_flags() == 0
+
+
+def test_a_workspace_of_any_contents_shared_by_calls_of_many_shapes():
+    """The counters are found in whatever state another call (or other data) left the workspace."""
+    jobs = []
+    for i, (new, lens) in enumerate([([1] * 3, [3000, 10, 500]), ([200], [900]), ([1], [20000]), ([33, 1], [5000, 4000])]):
+        s = paged_inputs(new, lens, 4, 2, 64, 16, seed=i)
+        jobs.append((s, max(new), run(s, max_q=max(new))))
+    n = max(ofa.paged_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], max_q=mq) for s, mq, _ in jobs)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    for fill in range(3):
+        ws.random_(0, 256, generator=g)
+        for s, mq, (o, lse) in jobs + jobs[::-1]:
+            a, b = run(s, max_q=mq, workspace=ws)
+            assert torch.equal(a, o) and torch.equal(b, lse)
+    assert ofa.device_error_flags() == 0
