@@ -16,6 +16,7 @@ using namespace paged;
 struct Plan {
     bool tc;
     int R, kt, grid, box;
+    bool fits;  // the line of tiles is shorter than 2^31
     size_t off_ml, off_u, bytes;
 };
 
@@ -33,12 +34,13 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 1);
-    const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d));
+    pl.fits = tiles < 2147483648.0 - 65536.0;
+    const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d, pl.R));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
-    const size_t slots = 2 * (size_t)pl.grid;
+    const size_t slots = (size_t)all_slots(pl.grid);
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.off_ml = up((pl.tc ? 2 : 1) * (size_t)counter_words(pl.grid) * sizeof(unsigned long long));
+    pl.off_ml = up((pl.tc ? 2 : 1) * slots * sizeof(unsigned long long));
     pl.off_u = pl.off_ml + up(slots * pl.R * 2 * sizeof(float));
     pl.bytes = pl.off_u + slots * pl.R * (size_t)c.d * sizeof(float);
     return pl;
@@ -78,9 +80,11 @@ size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p) { return make_plan(
 attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t st) {
     const attn_paged_cache_t &c = p.cache;
     const Plan pl = make_plan(p);
+    if (!pl.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
     Args a;
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hkv = (int)c.Hkv; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
-    a.R = pl.R; a.kt = pl.kt;
+    a.R = pl.R; a.r_log2 = log2_of(pl.R); a.kt = pl.kt;
+    bf16fwd::fast_div_params((uint32_t)a.G, a.g_m, a.g_s);
     a.page_log2 = log2_of(c.page_size);
     a.width = c.num_pages > 0 ? (int)c.table_width : 0;  // without pages there are no keys
     a.num_pages = (int)c.num_pages;
@@ -92,7 +96,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     a.qs0 = p.q_stride[0]; a.qs1 = p.q_stride[1]; a.os0 = p.o_stride[0]; a.os1 = p.o_stride[1];
     a.bt = c.block_table; a.bt_s = c.table_stride; a.lens = c.kv_lens; a.cu = c.cu_q;
     char *ws = static_cast<char *>(workspace);
-    a.counters = reinterpret_cast<unsigned long long *>(ws);
+    a.marks = reinterpret_cast<unsigned long long *>(ws);
     a.ml = reinterpret_cast<float *>(ws + pl.off_ml);
     a.u = reinterpret_cast<float *>(ws + pl.off_u);
     a.tag = next_call_tag();

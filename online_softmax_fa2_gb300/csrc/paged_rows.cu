@@ -34,13 +34,15 @@ struct Rows {
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = KT * 128;
     static constexpr int kTile = kPanels * kPanelBytes;  // K or V
-    static constexpr int kBlocks = rows_blocks(D);
+    static constexpr int kBlocks = rows_blocks(D, R);
     static constexpr int kStages = (kBlocks == 3 ? 64 : 96) * 1024 / (2 * kTile);
     static constexpr int kQRow = 2 * D + 16, kPRow = 2 * KT + 16;  // padded: ldmatrix without bank conflicts
     static constexpr int kQOff = kStages * 2 * kTile;
-    static constexpr int kPOff = kQOff + R * kQRow;
-    static constexpr int kRedOff = kPOff + R * kPRow;  // [4][R] maxima, then sums
-    static constexpr int kCtrlOff = kRedOff + 4 * R * 4;
+    // this block's queries and, where there is room, the next one's
+    static constexpr int kQBufs = MT == 2 ? 1 : 2;
+    static constexpr int kPOff = kQOff + kQBufs * R * kQRow;
+    static constexpr int kRedOff = kPOff + R * kPRow;    // [4][R] maxima, [4][R] sums
+    static constexpr int kCtrlOff = kRedOff + 2 * 4 * R * 4;
 };
 
 struct Ctrl {
@@ -50,7 +52,11 @@ struct Ctrl {
 };
 
 template <int D, int MT>
-constexpr int smem_bytes() { return Rows<D, MT>::kCtrlOff + (int)sizeof(Ctrl) + 1024; }
+constexpr int smem_bytes() {
+    constexpr int n = Rows<D, MT>::kCtrlOff + (int)sizeof(Ctrl) + 1024;
+    static_assert((n + 1024) * Rows<D, MT>::kBlocks <= 228 * 1024, "shared memory of the CTAs an SM holds");
+    return n;
+}
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -87,44 +93,47 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
     if (warp == 4) {
         // ------------------------------------------------------------ TMA producer
         const int pb_log2 = min(a.page_log2, 6), boxes = KT >> pb_log2;
+        const int box = lane / (2 * L::kPanels), part = lane % (2 * L::kPanels), panel = part >> 1;
+        const CUtensorMap *tm = (part & 1) ? &tm_v : &tm_k;
         int st = 0, ph = 0, issued = 0;
-        bool ok = true;
-        do {
-            if (w.keys == 0) continue;
-            const int *row = a.bt + w.b * a.bt_s;
-            int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
-            for (int j = w.j0; j < w.j1 && ok; ++j) {
-                const int kv0 = j * KT, first = kv0 >> a.page_log2;
-                const int last = (min(kv0 + KT, w.seq.n) - 1) >> a.page_log2;
-                if (held < 0 || last >= held + 32) {
-                    held = first;
-                    const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
-                    pages = at <= end ? __ldg(row + at) : 0;
-                    if (pages < 0 || pages >= a.num_pages) {
-                        atomicOr(a.flags, kFlagBadIndex);
-                        pages = a.num_pages;  // outside the tensor: TMA fills zeros
-                    }
+        bool ok = true, more = true;
+        // this lane's page among the 32 table entries from that of tile j on
+        auto pages_at = [&](const Walk &p, int j) -> int {
+            const int at = ((j * KT) >> a.page_log2) + lane;
+            return p.keys > 0 && at <= (p.seq.n - 1) >> a.page_log2 ? __ldg(a.bt + p.b * a.bt_s + at) : 0;
+        };
+        int ahead = pages_at(w, w.j0);
+        while (more && ok) {
+            const Walk p = w;
+            int pages = ahead, held = (p.j0 * KT) >> a.page_log2;
+            // the next piece's pages load under this one's tiles
+            more = w.next(a);
+            if (more) ahead = pages_at(w, w.j0);
+            for (int j = p.j0; p.keys > 0 && j < p.j1; ++j) {
+                const int kv0 = j * KT;
+                if ((min(kv0 + KT, p.seq.n) - 1) >> a.page_log2 >= held + 32) {
+                    held = kv0 >> a.page_log2;
+                    pages = pages_at(p, j);
                 }
+                if (pages < 0 || pages >= a.num_pages) pages = a.num_pages;  // outside the tensor: TMA fills zeros
                 if (issued >= NS) ok = ptx::mbar_wait(&ctrl->empty[st], ph ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 // boxes that hold a key of the sequence; each is kPanels copies of K and of V
-                const int nbox = min(boxes, ((w.seq.n - kv0 - 1) >> pb_log2) + 1);
+                const int nbox = min(boxes, ((p.seq.n - kv0 - 1) >> pb_log2) + 1);
                 if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->full[st], (uint32_t)(nbox * 2 * L::kPanels) << (pb_log2 + 7));
                 __syncwarp();
-                const int box = lane / (2 * L::kPanels), part = lane % (2 * L::kPanels);
                 const int key = kv0 + (box << pb_log2);
                 const int page = __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31));
                 if (box < nbox) {
-                    const int panel = part >> 1;
                     uint8_t *dst = smem + st * 2 * L::kTile + (part & 1) * L::kTile + panel * L::kPanelBytes + (box << (pb_log2 + 7));
-                    ptx::tma_load_4d(dst, (part & 1) ? &tm_v : &tm_k, &ctrl->full[st], panel * 64,
-                                     key & ((1 << a.page_log2) - 1), w.hk, page);
+                    ptx::tma_load_4d(dst, tm, &ctrl->full[st], panel * 64, key & ((1 << a.page_log2) - 1), p.hk, page);
+                    if (page == a.num_pages && part == 0) atomicOr(a.flags, kFlagBadIndex);
                 }
                 ++issued;
                 if (++st == NS) { st = 0; ph ^= 1; }
             }
-        } while (ok && w.next(a));
+        }
         if (*abort) {  // copies in flight land before the CTA leaves
             const int n = min(issued, NS);
             for (int i = 0; i < n; ++i) {
@@ -137,18 +146,28 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
 
     // ---------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
-    uint8_t *sQ = smem + L::kQOff, *sP = smem + L::kPOff;
-    int st = 0, ph = 0;
-    do {
-        const int rows = min(R, w.seq.nq * a.G - w.k * R), row0 = w.k * R;
-        // the block's queries (rows past its end are zero)
+    uint8_t *sP = smem + L::kPOff;
+    float *sums = red + 4 * R;
+    int st = 0, ph = 0, qb = 0;
+    // a block's queries into one of the two buffers (rows past the block's end are zero)
+    auto bring_q = [&](const Walk &p, int buf) {
+        const int left = p.seq.nq * a.G - p.k * R;
+        uint8_t *dst = smem + L::kQOff + buf * R * L::kQRow;
+#pragma unroll
         for (int i = threadIdx.x; i < R * (D / 8); i += kConsumers) {
-            const int r = i / (D / 8), c = i % (D / 8), tok = (row0 + r) / a.G, hd = (row0 + r) % a.G;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows)
-                v = *reinterpret_cast<const uint4 *>(a.q + (w.seq.q0 + tok) * a.qs0 + (w.hk * a.G + hd) * a.qs1 + c * 8);
-            *reinterpret_cast<uint4 *>(sQ + r * L::kQRow + c * 16) = v;
+            const int r = i / (D / 8), c = i % (D / 8), row = p.k * R + r, tok = div_g(a, row);
+            const bool in = r < left;
+            const __nv_bfloat16 *src = a.q + (in ? (p.seq.q0 + tok) * a.qs0 + (p.hk * a.G + row - tok * a.G) * a.qs1 + c * 8 : 0);
+            cp_async16(smem_addr(dst + r * L::kQRow + c * 16), src, in ? 16u : 0u);
         }
+        cp_async_commit();
+    };
+    bring_q(w, 0);
+    bool more = true;
+    while (more) {
+        const Walk p = w;
+        const int rows = min(R, p.seq.nq * a.G - p.k * R), row0 = p.k * R;
+        const uint8_t *sQ = smem + L::kQOff + qb * R * L::kQRow;
         int lim[MT][2];  // keys < lim are visible to this lane's rows 16 mt + 8 e + g
         float m[MT][2], l[MT][2], o[MT][DW / 8][4];
 #pragma unroll
@@ -156,20 +175,26 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 16 * mt + 8 * e + g;
-                lim[mt][e] = (a.causal && r < rows) ? min(max(w.seq.n - w.seq.nq + (row0 + r) / a.G + 1, 0), w.seq.n) : w.seq.n;
+                lim[mt][e] = (a.causal && r < rows) ? min(max(p.seq.n - p.seq.nq + div_g(a, row0 + r) + 1, 0), p.seq.n) : p.seq.n;
                 m[mt][e] = -INFINITY;
                 l[mt][e] = 0.f;
             }
-        const int lim0 = a.causal ? min(max(w.seq.n - w.seq.nq + row0 / a.G + 1, 0), w.seq.n) : w.seq.n;
+        const int lim0 = a.causal ? min(max(p.seq.n - p.seq.nq + div_g(a, row0) + 1, 0), p.seq.n) : p.seq.n;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int nt = 0; nt < DW / 8; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-        consumer_sync();
+        cp_async_wait<0>();
+        consumer_sync();  // the queries are there; the last piece is done with the other buffer and with sums
+        more = w.next(a);
+        if (L::kQBufs == 2) {
+            qb ^= 1;
+            if (more) bring_q(w, qb);
+        }
 
-        for (int j = w.j0; w.keys > 0 && j < w.j1; ++j) {
+        for (int j = p.j0; p.keys > 0 && j < p.j1; ++j) {
             const int kv0 = j * KT;
             // a wait that gave up is reported; the walk goes on (the four warps keep meeting at the
             // same barriers) and ends, its waits returning at once
@@ -218,11 +243,11 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                     if (t == 0) red[warp * R + 16 * mt + 8 * e + g] = mx;
                 }
             // value rows past the sequence may hold anything: zero, so that 0 * v is 0
-            const bool ragged = kv0 + KT > w.seq.n;
+            const bool ragged = kv0 + KT > p.seq.n;
             if (ragged)
                 for (int i = threadIdx.x; i < KT * L::kPanels * 8; i += kConsumers) {
                     const int key = (i >> 3) % KT, panel = (i >> 3) / KT;
-                    if (kv0 + key >= w.seq.n)
+                    if (kv0 + key >= p.seq.n)
                         *reinterpret_cast<uint4 *>(sV + panel * L::kPanelBytes + key * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
             consumer_sync();
@@ -281,6 +306,8 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
             if (++st == NS) { st = 0; ph ^= 1; }
         }
 
+        if (L::kQBufs == 1 && more) bring_q(w, 0);  // every warp is past its last S
+
         // ------------------------------------------------------------ the piece's rows
         // row sums: over the quad, then over the four warps
 #pragma unroll
@@ -292,15 +319,14 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 l[mt][e] = v;
             }
-        consumer_sync();  // every warp is done with red's maxima, and with sQ and sP
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                if (t == 0) red[warp * R + 16 * mt + 8 * e + g] = l[mt][e];
+                if (t == 0) sums[warp * R + 16 * mt + 8 * e + g] = l[mt][e];
         consumer_sync();
-        const bool whole = w.whole();
-        const int c0 = whole ? 0 : w.first_share();
+        const bool whole = p.whole();
+        const int c0 = whole ? 0 : p.first_share();
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -308,10 +334,10 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
             for (int e = 0; e < 2; ++e) {
                 const int r = 16 * mt + 8 * e + g;
                 if (r >= rows) continue;
-                const float sum = (red[r] + red[R + r]) + (red[2 * R + r] + red[3 * R + r]);
+                const float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
                 if (whole) {
                     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    const int tok = w.seq.q0 + (row0 + r) / a.G, h = w.hk * a.G + (row0 + r) % a.G;
+                    const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                     __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
 #pragma unroll
                     for (int nt = 0; nt < DW / 8; ++nt)
@@ -328,19 +354,18 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                 }
             }
         if (!whole)
-            finish_cut<D, MT == 1 ? 2 : 1>(
-                a, a.counters, gridDim.x, 0, rows, blockIdx.x, c0, w.last_share() - c0 + 1, threadIdx.x, &ctrl->last,
+            finish_cut<D, 2, 8>(
+                a, a.marks, gridDim.x, 0, rows, blockIdx.x, c0, p.share_of(p.tiles - 1) - c0 + 1, threadIdx.x, &ctrl->last,
                 [] {
                     consumer_sync();
                     return true;
                 },
                 [&](int r, __nv_bfloat16 *&orow, float *&lse) {
-                    const int tok = w.seq.q0 + (row0 + r) / a.G, h = w.hk * a.G + (row0 + r) % a.G;
+                    const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                     orow = a.o + tok * a.os0 + h * a.os1;
                     lse = a.lse ? a.lse + (long long)tok * a.Hq + h : nullptr;
                 });
-        consumer_sync();  // red is free again
-    } while (w.next(a));
+    }
 }
 
 template <int D, int MT>

@@ -6,19 +6,17 @@
 // in order (sequence, head, block) form one line of `total` tiles, cut into equal shares, one a
 // CTA, whatever the lengths: a batch of one long and many short sequences, or a single one,
 // loads every SM alike.  An item inside one share is finished there.  An item cut by a boundary
-// leaves one state (m, l, u) per share in the workspace; the share that comes last, told by a
-// counter, merges them in share order (so the bits do not depend on who came last).
+// leaves one state (m, l, u) per share in the workspace; one of the shares that come last merges
+// them (paged_merge.cuh).
 //
 // A share holds at most one cut item that began before it (slot 2 c) and one that goes on past its
-// end (slot 2 c + 1; the counter of c counts that item's states).  A counter word holds
-// (tag of the call, count); under another tag, or zero, it reads as zero, and whoever merges sets
-// it to zero: the workspace may hold anything on entry, and a captured call, whose tag is
-// the same at every replay, finds zero.
+// end (slot 2 c + 1).
 #pragma once
 
 #include <cuda_bf16.h>
 
 #include "attn_internal.h"
+#include "fwd_bf16_common.cuh"
 #include "sm100_ptx.cuh"
 
 namespace attn {
@@ -29,7 +27,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
 struct Args {
-    int B, T, Hq, Hkv, G, causal, R, kt;  // R rows a block, 2^kt keys a tile
+    int B, T, Hq, Hkv, G, causal, R, r_log2, kt;  // R = 2^r_log2 rows a block, 2^kt keys a tile
     int page_log2, width, num_pages, min_share;
     float scale_log2;
     const __nv_bfloat16 *q;
@@ -37,11 +35,15 @@ struct Args {
     float *lse;
     long long qs0, qs1, os0, os1, bt_s;
     const int *bt, *lens, *cu;
-    unsigned long long *counters;
+    uint32_t g_m;  // division by G as a multiply-high and shifts (bf16fwd::fast_div_params)
+    int g_s;
+    unsigned long long *marks;  // what is written, see paged_merge.cuh
     unsigned long long tag;
     float *ml, *u;  // states: (m, l) [slot][R][2], u [slot][R][D]
     uint32_t *flags;
 };
+
+__device__ __forceinline__ int div_g(const Args &a, int x) { return (int)bf16fwd::div_fast((uint32_t)x, a.g_m, a.g_s); }
 
 struct Seq {
     int q0, nq, n;  // first packed token, new tokens, keys
@@ -65,14 +67,14 @@ __device__ __forceinline__ Seq seq_info(const Args &a, int b, bool report) {
     return s;
 }
 
-__device__ __forceinline__ int num_blocks(const Args &a, const Seq &s) { return (s.nq * a.G + a.R - 1) / a.R; }
+__device__ __forceinline__ int num_blocks(const Args &a, const Seq &s) { return (s.nq * a.G + a.R - 1) >> a.r_log2; }
 
 // Keys that the last row of block k sees, and the tiles that hold them; a block that sees none
 // counts as one tile (its rows are written all the same).
 __device__ __forceinline__ int block_keys(const Args &a, const Seq &s, int k) {
     if (!a.causal) return s.n;
     const int last = min((k + 1) * a.R, s.nq * a.G) - 1;
-    return min(max(s.n - s.nq + last / a.G + 1, 0), s.n);
+    return min(max(s.n - s.nq + div_g(a, last) + 1, 0), s.n);
 }
 __device__ __forceinline__ int block_tiles(const Args &a, const Seq &s, int k) {
     return max(1, (block_keys(a, s, k) + (1 << a.kt) - 1) >> a.kt);
@@ -101,84 +103,91 @@ __device__ __forceinline__ int seq_tiles(const Args &a, const Seq &s, int nb) {
 }
 
 struct Share {
-    long long per, t0, t1;  // tiles a share, and this CTA's [t0, t1)
-    int b, hk, k, j;        // where t0 lies
+    int per, t0, t1;     // tiles a share, and this CTA's [t0, t1); the line is shorter than 2^31
+    int b, hk, k, j;     // where t0 lies
+    Seq seq;
 };
 
-// The share of CTA c of C.  One warp; every lane gets the result.
+// The share of CTA c of C.  One warp; every lane gets the result.  It runs once, cold, before
+// anything else can: short code counts for more than fast code.
 __device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        Seq s{0, 0, 0};
-        if (b < a.B) s = seq_info(a, b, c == 0);
-        int w = seq_tiles(a, s, num_blocks(a, s));
-        long long v = w;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        total += v;
+    Share r;
+    r.b = r.hk = r.k = r.j = 0;
+    Seq s, ahead{0, 0, 0};
+    int w = 0, nb = 0, total = 0;
+    if (lane < a.B) ahead = seq_info(a, lane, c == 0);
+#pragma unroll 1
+    for (int b = lane; b < a.B + lane; b += 32) {
+        s = ahead;
+        ahead = Seq{0, 0, 0};
+        if (b + 32 < a.B) ahead = seq_info(a, b + 32, c == 0);
+        nb = num_blocks(a, s);
+        w = seq_tiles(a, s, nb);
+        total += __reduce_add_sync(0xffffffffu, w);
     }
     total *= a.Hkv;
-    Share r;
-    r.per = max((total + C - 1) / C, (long long)a.min_share);
-    r.t0 = min(r.per * c, total);
+    r.per = max((int)((unsigned)(total + C - 1) / (unsigned)C), a.min_share);
+    r.t0 = (int)min((long long)r.per * c, (long long)total);
     r.t1 = min(r.t0 + r.per, total);
-    r.b = r.hk = r.k = r.j = 0;
     if (r.t0 >= r.t1) return r;
-    long long before = 0;
+    int left = r.t0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        Seq s{0, 0, 0};
-        if (b < a.B) s = seq_info(a, b, false);
-        const int nb = num_blocks(a, s), w = seq_tiles(a, s, nb);
-        long long incl = w;
+        if (a.B > 32) {  // (up to 32 sequences: s and w are theirs still)
+            s = Seq{0, 0, 0};
+            if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
+            nb = num_blocks(a, s);
+            w = seq_tiles(a, s, nb);
+        }
+        int incl = w * a.Hkv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, (before + incl) * a.Hkv > r.t0);
+        const unsigned past = __ballot_sync(0xffffffffu, incl > left);
         if (!past) {
-            before += __shfl_sync(0xffffffffu, incl, 31);
+            left -= __shfl_sync(0xffffffffu, incl, 31);
             continue;
         }
         const int src = __ffs(past) - 1;
-        Seq o;
-        o.q0 = 0;
-        o.nq = __shfl_sync(0xffffffffu, s.nq, src);
-        o.n = __shfl_sync(0xffffffffu, s.n, src);
-        const int ow = __shfl_sync(0xffffffffu, w, src), onb = __shfl_sync(0xffffffffu, nb, src);
-        long long rest = r.t0 - (before + __shfl_sync(0xffffffffu, incl, src) - ow) * a.Hkv;
         r.b = b0 + src;
-        r.hk = (int)(rest / ow);
-        int left = (int)(rest - (long long)r.hk * ow);
-        for (int k0 = 0; k0 < onb; k0 += 32) {
-            const int k = k0 + lane, t = k < onb ? block_tiles(a, o, k) : 0;
-            int in = t;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, in, d);
-                if (lane >= d) in += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, in > left);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                r.k = k0 + l;
-                r.j = left - (__shfl_sync(0xffffffffu, in, l) - __shfl_sync(0xffffffffu, t, l));
-                break;
-            }
-            left -= __shfl_sync(0xffffffffu, in, 31);
-        }
+        r.seq.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+        r.seq.nq = __shfl_sync(0xffffffffu, s.nq, src);
+        r.seq.n = __shfl_sync(0xffffffffu, s.n, src);
+        w = __shfl_sync(0xffffffffu, w, src);
+        nb = __shfl_sync(0xffffffffu, nb, src);
+        left -= __shfl_sync(0xffffffffu, incl, src) - w * a.Hkv;
+        r.hk = (int)((unsigned)left / (unsigned)w);
+        left -= r.hk * w;
         break;
+    }
+    r.j = left;
+#pragma unroll 1
+    for (int k0 = 0; nb > 1; k0 += 32) {
+        const int k = k0 + lane, t = k < nb ? block_tiles(a, r.seq, k) : 0;
+        int in = t;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, in, d);
+            if (lane >= d) in += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, in > left);
+        if (hit || k0 + 32 >= nb) {
+            const int l = hit ? __ffs(hit) - 1 : 0;
+            r.k = k0 + l;
+            r.j = left - (__shfl_sync(0xffffffffu, in, l) - __shfl_sync(0xffffffffu, t, l));
+            break;
+        }
+        left -= __shfl_sync(0xffffffffu, in, 31);
     }
     return r;
 }
 
 // A walk over the pieces of a share; every role of the CTA makes the same walk.
 struct Walk {
-    Share s;
-    long long t;  // the line's tile at which the current piece begins
+    int per, t, t1;  // tiles a share; the line's tile at which the piece begins; where the share ends
     Seq seq;
     int b, hk, k, nb;
     int j0, j1, tiles, keys;  // the piece: tiles [j0, j1) of the block's `tiles`, which hold `keys` keys
@@ -187,24 +196,25 @@ struct Walk {
         keys = block_keys(a, seq, k);
         tiles = max(1, (keys + (1 << a.kt) - 1) >> a.kt);
         j0 = j;
-        j1 = (int)min((long long)tiles, j + (s.t1 - t));
+        j1 = min(tiles, j + (t1 - t));
     }
     // false when the share is empty
     __device__ __forceinline__ bool begin(const Args &a, const Share &sh) {
-        s = sh;
-        t = s.t0;
-        if (t >= s.t1) return false;
-        b = s.b;
-        hk = s.hk;
-        k = s.k;
-        seq = seq_info(a, b, false);
+        per = sh.per;
+        t = sh.t0;
+        t1 = sh.t1;
+        if (t >= t1) return false;
+        b = sh.b;
+        hk = sh.hk;
+        k = sh.k;
+        seq = sh.seq;
         nb = num_blocks(a, seq);
-        piece(a, s.j);
+        piece(a, sh.j);
         return true;
     }
     __device__ __forceinline__ bool next(const Args &a) {
         t += j1 - j0;
-        if (t >= s.t1) return false;
+        if (t >= t1) return false;
         if (++k == nb) {
             k = 0;
             if (++hk == a.Hkv) {
@@ -220,35 +230,12 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
-    // the shares that hold the item, and the slot of this one's state
-    __device__ __forceinline__ int first_share() const { return (int)((t - j0) / s.per); }
-    __device__ __forceinline__ int last_share() const { return (int)((t - j0 + tiles - 1) / s.per); }
+    // the shares that hold the item's first tile and its tile `last`
+    __device__ __forceinline__ int first_share() const { return (int)((unsigned)(t - j0) / (unsigned)per); }
+    __device__ __forceinline__ int share_of(int last) const { return (int)((unsigned)(t - j0 + last) / (unsigned)per); }
 };
 
 __device__ __forceinline__ int state_slot(int share, int first) { return 2 * share + (share == first ? 1 : 0); }
-
-// Counts this share's state of an item of n states whose counter is *cnt; true for the one that
-// completes them, which then sees every state written before.  One thread, after a barrier behind
-// the state's writes.  Retries only when another share counted in between (n - 1 times at most).
-__device__ __forceinline__ bool count_state(const Args &a, unsigned long long *cnt, int n) {
-    __threadfence();
-    unsigned long long seen = *reinterpret_cast<volatile unsigned long long *>(cnt), mine = 0;
-    for (int tries = 0;; ++tries) {
-        mine = ((seen >> 16) == a.tag ? (seen & 0xffffull) : 0ull) + 1ull;
-        // the last one leaves zero for the next call (which may be this one, replayed)
-        const unsigned long long put = mine == (unsigned long long)n ? 0ull : (a.tag << 16) | mine;
-        const unsigned long long prev = atomicCAS(cnt, seen, put);
-        if (prev == seen) break;
-        seen = prev;
-        if (tries >= 65536) {
-            atomicOr(a.flags, kFlagWaitTimeout);
-            return false;
-        }
-    }
-    if (mine != (unsigned long long)n) return false;
-    __threadfence();
-    return true;
-}
 
 }  // namespace paged
 }  // namespace attn

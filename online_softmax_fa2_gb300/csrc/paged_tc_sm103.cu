@@ -71,7 +71,7 @@ __device__ __forceinline__ Tiles tiles_of(const paged::Args &a, const Walk &w) {
     const int rows = w.seq.nq * a.G - w.k * a.R;  // >= 1
     int ka = w.keys;
     if (rows > BQ && a.causal) {
-        const int last = (w.k * a.R + BQ - 1) / a.G;
+        const int last = paged::div_g(a, w.k * a.R + BQ - 1);
         ka = min(max(w.seq.n - w.seq.nq + last + 1, 0), w.seq.n);
     }
     r.t[0] = (ka + BK - 1) / BK;
@@ -294,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = p.k * a.R + X * BQ + r;
             uint8_t *dst = smem + X * L::kTile + r * 128;
             if (row < p.seq.nq * a.G) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (long long)(p.seq.q0 + row / a.G) * a.qs0 +
-                                                                   (p.hk * a.G + row % a.G) * a.qs1);
+                const int tok = paged::div_g(a, row);
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (p.seq.q0 + tok) * a.qs0 +
+                                                                   (p.hk * a.G + row - tok * a.G) * a.qs1);
                 uint4 v[D / 8];
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
@@ -319,9 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tiles tl = tiles_of(a, w);
             const int n = tl.n[X], i0 = w.k * a.R + X * BQ, i = i0 + r, nmax = w.keys == 0 ? 0 : w.j1 - w.j0;
             const bool mine = i < w.seq.nq * a.G;
-            const int tok = i / a.G, seqn = w.seq.n;
+            const int tok = paged::div_g(a, i), seqn = w.seq.n;
             const int lim = a.causal && mine ? min(max(seqn - w.seq.nq + tok + 1, 0), seqn) : seqn;
-            const int lim0 = a.causal ? min(max(seqn - w.seq.nq + i0 / a.G + 1, 0), seqn) : seqn;
+            const int lim0 = a.causal ? min(max(seqn - w.seq.nq + paged::div_g(a, i0) + 1, 0), seqn) : seqn;
             float m_run = -INFINITY, l_run = 0.f;
             for (int jj = 0; jj < n; ++jj) {
                 const int kv0 = (w.j0 + jj) * BK;
@@ -354,14 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // where this row goes, before the walk moves on
             const bool whole = w.j0 == 0 && w.j1 >= tl.t[X];
             const int c0 = w.first_share();
-            const int cn = tl.t[X] > 0 ? (int)((w.t - w.j0 + tl.t[X] - 1) / w.s.per) - c0 + 1 : 1;
+            const int cn = tl.t[X] > 0 ? w.share_of(tl.t[X] - 1) - c0 + 1 : 1;
             const bool first = w.j0 == 0;
             const int rows = w.seq.nq * a.G - w.k * a.R, q0 = w.seq.q0, hk = w.hk;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
             if (mine) {
                 const long long t = w.seq.q0 + tok;
-                const int h = w.hk * a.G + i % a.G;
+                const int h = w.hk * a.G + i - tok * a.G;
                 orow = a.o + t * a.os0 + h * a.os1;
                 lrow = a.lse ? a.lse + t * a.Hq + h : nullptr;
             }
@@ -397,11 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < 8; ++t) dst[t] = make_uint4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
             }
             ptx::tc_fence_before();
-            ok = paged::finish_cut<D, 4>(
-                a, a.counters + X * paged::counter_words(gridDim.x), gridDim.x, X * BQ, min(BQ, rows - X * BQ), blockIdx.x, c0,
+            ok = paged::finish_cut<D, 4, 4>(
+                a, a.marks + X * paged::all_slots(gridDim.x), gridDim.x, X * BQ, min(BQ, rows - X * BQ), blockIdx.x, c0,
                 cn, r, &ctrl->last[X], group_sync, [&](int rr, __nv_bfloat16 *&orow, float *&lse) {
-                    const long long t = q0 + (i0 + rr) / a.G;
-                    const int h = hk * a.G + (i0 + rr) % a.G;
+                    const int tk = paged::div_g(a, i0 + rr);
+                    const long long t = q0 + tk;
+                    const int h = hk * a.G + i0 + rr - tk * a.G;
                     orow = a.o + t * a.os0 + h * a.os1;
                     lse = a.lse ? a.lse + t * a.Hq + h : nullptr;
                 });
