@@ -17,7 +17,7 @@ constexpr int rows_blocks(int64_t d, int R) { return d == 64 && R == 16 ? 3 : 2;
 attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
                                 cudaStream_t s);
 constexpr int kTcBoxKeys = 128;
-attn_status_t launch_paged_tc(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
-                              cudaStream_t s);
+attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
+                              int d, int grid, cudaStream_t s);
 
 }  // namespace attn

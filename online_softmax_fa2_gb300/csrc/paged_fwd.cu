@@ -27,7 +27,8 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t rows = most * G;
     Plan pl;
     pl.tc = rows > 32;
-    pl.R = pl.tc ? 256 : rows <= 16 ? 16 : 32;
+    // (the 128-row tiles take whole tokens, so that TMA can bring their queries)
+    pl.R = pl.tc ? (int)(2 * (128 / G) * G) : rows <= 16 ? 16 : 32;
     pl.kt = pl.tc ? 7 : 6;
     pl.box = pl.tc ? kTcBoxKeys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;
@@ -38,11 +39,12 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d, pl.R));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
-    const size_t slots = (size_t)all_slots(pl.grid);
+    const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.off_ml = up((pl.tc ? 2 : 1) * slots * sizeof(unsigned long long));
-    pl.off_u = pl.off_ml + up(slots * pl.R * 2 * sizeof(float));
-    pl.bytes = pl.off_u + slots * pl.R * (size_t)c.d * sizeof(float);
+    pl.off_ml = up((pl.tc ? 0 : slots) * sizeof(unsigned long long));
+    const size_t srows = pl.tc ? 256 : pl.R;  // rows a slot
+    pl.off_u = pl.off_ml + up(slots * srows * 2 * sizeof(float));
+    pl.bytes = pl.off_u + slots * srows * (size_t)c.d * sizeof(float);
     return pl;
 }
 
@@ -67,6 +69,24 @@ attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cac
     return ATTN_OK;
 }
 
+// 3-D map over the packed queries [T, Hq, d]; a box is 64 dimensions of the G heads that share a
+// key head, of `tokens` tokens: 128 rows or nearly.
+attn_status_t encode_q(CUtensorMap *m, const attn_paged_fwd_params_t &p, int tokens) {
+    auto enc = get_encoder();
+    if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const int64_t G = p.Hq / p.cache.Hkv;
+    auto bytes = [](int64_t st, int64_t size) -> cuuint64_t { return size <= 1 ? 16u : (cuuint64_t)(st * 2); };
+    cuuint64_t dims[3] = {(cuuint64_t)p.cache.d, (cuuint64_t)p.Hq, (cuuint64_t)p.cache.T};
+    cuuint64_t strides[2] = {bytes(p.q_stride[1], p.Hq), bytes(p.q_stride[0], p.cache.T)};
+    cuuint32_t b[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
+    cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), dims, strides, b, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "TMA descriptor for q rejected (CUresult %d)", (int)r);
+    return ATTN_OK;
+}
+
 int log2_of(int x) {
     int l = 0;
     while ((1 << l) < x) ++l;
@@ -83,12 +103,18 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     if (!pl.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
     Args a;
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hkv = (int)c.Hkv; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
-    a.R = pl.R; a.r_log2 = log2_of(pl.R); a.kt = pl.kt;
+    a.R = pl.R; a.kt = pl.kt;
     bf16fwd::fast_div_params((uint32_t)a.G, a.g_m, a.g_s);
+    bf16fwd::fast_div_params((uint32_t)a.R, a.r_m, a.r_s);
     a.page_log2 = log2_of(c.page_size);
     a.width = c.num_pages > 0 ? (int)c.table_width : 0;  // without pages there are no keys
     a.num_pages = (int)c.num_pages;
-    a.min_share = 4;
+    // Least tiles a share, and inside an item at either side of a cut.  Few rows: a cut costs 4 to 8
+    // tiles (8 decodes over 2048 keys take 29 us with shares of 4 tiles, 27 with 8; one over 1024
+    // keys 17 either way, 19 with cuts of 8).  128-row tiles: an uncut block needs no share of its
+    // own (512 tokens over 512 keys take 62 us with shares of 4, 29 with 1).
+    a.min_share = pl.tc ? 1 : 8;
+    a.min_cut = 4;
     a.scale_log2 = p.scale * kLog2e;
     a.q = static_cast<const __nv_bfloat16 *>(p.q);
     a.o = static_cast<__nv_bfloat16 *>(p.o);
@@ -108,7 +134,12 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
         if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, "k_pages"))) return r;
         if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, "v_pages"))) return r;
     }
-    if (pl.tc) return launch_paged_tc(mk, mv, a, (int)c.d, pl.grid, st);
+    if (pl.tc) {
+        CUtensorMap mq;
+        const attn_status_t r = encode_q(&mq, p, 128 / a.G);
+        if (r) return r;
+        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.grid, st);
+    }
     return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }
 

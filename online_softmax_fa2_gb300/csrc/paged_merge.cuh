@@ -13,7 +13,7 @@
 // With more than kGroup parts the merge goes in two levels, so that no one walks hundreds of
 // parts: every kGroup shares are merged into a slot of the group's own, then the groups.  The parts come
 // from L2, written by other SMs a moment ago: the time is latency, so a warp keeps
-// U rows x P parts of loads in flight.
+// many of them in flight.
 #pragma once
 
 #include <type_traits>
@@ -62,11 +62,12 @@ __device__ __forceinline__ bool all_marked(const Args &a, unsigned long long *ma
     return ok && *flag;
 }
 
-// Merges the states at slots slot(0) .. slot(n - 1), n <= kGroup, rows [row0, row0 + rows) of a
-// slot, rows <= 128.  Four warps, tid 0 .. 127.  To the slot `to`, or, with to < 0, to the rows that
-// out(r, orow, lse) names.  Of a row's states, lane p holds the weights of p and p + 32.
+// The merge for few rows: the states at slots slot(0) .. slot(n - 1), n <= kGroup, u as [slot][R][D],
+// to the slot `to`, or, with to < 0, to the rows that out(r, orow, lse) names.  Four warps, tid 0 ..
+// 127, a row a warp at a time (U of them in flight); of a row's states, lane p holds the weights
+// of p and p + 32.
 template <int D, int U, int P, class Slot, class Out>
-__device__ __forceinline__ void merge_parts(const Args &a, int row0, int rows, int n, int to, int tid, Slot slot, Out out) {
+__device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int to, int tid, Slot slot, Out out) {
     constexpr int C = D / 32;  // columns a lane: C lane .. C lane + C - 1
     using Vec = typename std::conditional<C == 4, float4, float2>::type;
     const int warp = tid >> 5, lane = tid & 31;
@@ -78,7 +79,7 @@ __device__ __forceinline__ void merge_parts(const Args &a, int row0, int rows, i
         float v[U][C];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const long long r = row0 + min(r0 + u, hi - 1);  // a row past the warp's last is read again
+            const long long r = min(r0 + u, hi - 1);  // a row past the warp's last is read again
             w0[u] = w1[u] = make_float2(-INFINITY, 0.f);
             if (lane < n) w0[u] = __ldcg(reinterpret_cast<const float2 *>(a.ml + (s0 * (long long)a.R + r) * 2));
             if (lane + 32 < n) w1[u] = __ldcg(reinterpret_cast<const float2 *>(a.ml + (s1 * (long long)a.R + r) * 2));
@@ -95,7 +96,7 @@ __device__ __forceinline__ void merge_parts(const Args &a, int row0, int rows, i
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     x[u][p] = __ldcg(reinterpret_cast<const Vec *>(
-                        a.u + (sl * (long long)a.R + row0 + min(r0 + u, hi - 1)) * D + C * lane));
+                        a.u + (sl * (long long)a.R + min(r0 + u, hi - 1)) * D + C * lane));
             }
             if (p0 == 0) {  // the weights, under the first states' loads
 #pragma unroll
@@ -131,7 +132,7 @@ __device__ __forceinline__ void merge_parts(const Args &a, int row0, int rows, i
             const int r = r0 + u;
             if (r >= hi) break;  // the whole warp
             if (to >= 0) {
-                const long long at = (long long)to * a.R + row0 + r;
+                const long long at = (long long)to * a.R + r;
                 Vec y;
 #pragma unroll
                 for (int e = 0; e < C; ++e) reinterpret_cast<float *>(&y)[e] = v[u][e];
@@ -151,11 +152,11 @@ __device__ __forceinline__ void merge_parts(const Args &a, int row0, int rows, i
     }
 }
 
-// This share's state is written (by these 128 threads): mark it, and merge what is complete.
-// marks: the row tile's; sync(): the 128 threads meet (false: gave up).
-template <int D, int U, int P, class Sync, class Out>
-__device__ __forceinline__ bool finish_cut(const Args &a, unsigned long long *marks, int shares, int row0, int rows, int share,
-                                           int c0, int n, int tid, volatile int *flag, Sync sync, Out out) {
+// This share's state is written (by these 128 threads): mark it, and merge what is complete, by
+// merge(n, to, slot).  marks: the row tile's; sync(): the 128 threads meet (false: gave up).
+template <class Sync, class Merge>
+__device__ __forceinline__ bool finish_cut(const Args &a, unsigned long long *marks, int shares, int share, int c0, int n,
+                                           int tid, volatile int *flag, Sync sync, Merge merge) {
     const int g = (share - c0) / kGroup, base = 2 * shares;
     bool groups = n > kGroup;  // first the shares of a group, then the groups
     int mine = state_slot(share, c0);
@@ -172,7 +173,7 @@ __device__ __forceinline__ bool finish_cut(const Args &a, unsigned long long *ma
         const bool all = all_marked(a, marks, mine, parts, tid, flag, sync, slot, ok);
         if (!all) return ok;
         const int to = groups ? base + group_slot(c0 + g * kGroup, g) : -1;
-        merge_parts<D, U, P>(a, row0, rows, parts, to, tid, slot, out);
+        merge(parts, to, slot);
         if (!groups) return true;
         groups = false;
         mine = to;

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                 if (t == 0) sums[warp * R + 16 * mt + 8 * e + g] = l[mt][e];
         consumer_sync();
         const bool whole = p.whole();
-        const int c0 = whole ? 0 : p.first_share();
+        const int c0 = whole ? 0 : p.first_share(a);
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -354,16 +354,18 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                 }
             }
         if (!whole)
-            finish_cut<D, 2, 8>(
-                a, a.marks, gridDim.x, 0, rows, blockIdx.x, c0, p.share_of(p.tiles - 1) - c0 + 1, threadIdx.x, &ctrl->last,
+            finish_cut(
+                a, a.marks, gridDim.x, blockIdx.x, c0, p.parts(a, c0, p.tiles), threadIdx.x, &ctrl->last,
                 [] {
                     consumer_sync();
                     return true;
                 },
-                [&](int r, __nv_bfloat16 *&orow, float *&lse) {
-                    const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
-                    orow = a.o + tok * a.os0 + h * a.os1;
-                    lse = a.lse ? a.lse + (long long)tok * a.Hq + h : nullptr;
+                [&](int n, int to, auto slot) {
+                    merge_parts<D, 2, 8>(a, rows, n, to, threadIdx.x, slot, [&](int r, __nv_bfloat16 *&orow, float *&lse) {
+                        const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
+                        orow = a.o + tok * a.os0 + h * a.os1;
+                        lse = a.lse ? a.lse + (long long)tok * a.Hq + h : nullptr;
+                    });
                 });
     }
 }

@@ -3,11 +3,12 @@
 // The rows of a sequence that share key/value head hk are numbered token * G + g (G = Hq / Hkv
 // query heads a key head) and taken R at a time: block k holds rows [k R, (k + 1) R).  An item
 // (b, hk, k) walks the 2^kt-key tiles up to the last key that its last row sees.  All items' tiles
-// in order (sequence, head, block) form one line of `total` tiles, cut into equal shares, one a
-// CTA, whatever the lengths: a batch of one long and many short sequences, or a single one,
-// loads every SM alike.  An item inside one share is finished there.  An item cut by a boundary
-// leaves one state (m, l, u) per share in the workspace; one of the shares that come last merges
-// them (paged_merge.cuh).
+// in order (sequence, head, block) form one line of `total` tiles, cut at equal distances into
+// shares, one a CTA, whatever the lengths: a batch of one long and many short sequences, or a
+// single one, loads every SM alike.  A boundary that falls less than min_cut tiles inside an item
+// goes to that end of it (a cut costs about as much as so many tiles).  An item inside one share
+// is finished there.  An item cut by a boundary leaves one state (m, l, u) per share in the
+// workspace; one of the shares that come last merges them (paged_merge.cuh).
 //
 // A share holds at most one cut item that began before it (slot 2 c) and one that goes on past its
 // end (slot 2 c + 1).
@@ -27,16 +28,16 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
 struct Args {
-    int B, T, Hq, Hkv, G, causal, R, r_log2, kt;  // R = 2^r_log2 rows a block, 2^kt keys a tile
-    int page_log2, width, num_pages, min_share;
+    int B, T, Hq, Hkv, G, causal, R, kt;  // R rows a block, 2^kt keys a tile
+    int page_log2, width, num_pages, min_share, min_cut;
     float scale_log2;
     const __nv_bfloat16 *q;
     __nv_bfloat16 *o;
     float *lse;
     long long qs0, qs1, os0, os1, bt_s;
     const int *bt, *lens, *cu;
-    uint32_t g_m;  // division by G as a multiply-high and shifts (bf16fwd::fast_div_params)
-    int g_s;
+    uint32_t g_m, r_m;  // division by G and by R as a multiply-high and shifts (bf16fwd::fast_div_params)
+    int g_s, r_s;
     unsigned long long *marks;  // what is written, see paged_merge.cuh
     unsigned long long tag;
     float *ml, *u;  // states: (m, l) [slot][R][2], u [slot][R][D]
@@ -67,7 +68,7 @@ __device__ __forceinline__ Seq seq_info(const Args &a, int b, bool report) {
     return s;
 }
 
-__device__ __forceinline__ int num_blocks(const Args &a, const Seq &s) { return (s.nq * a.G + a.R - 1) >> a.r_log2; }
+__device__ __forceinline__ int num_blocks(const Args &a, const Seq &s) { return (int)bf16fwd::div_fast((uint32_t)(s.nq * a.G + a.R - 1), a.r_m, a.r_s); }
 
 // Keys that the last row of block k sees, and the tiles that hold them; a block that sees none
 // counts as one tile (its rows are written all the same).
@@ -103,84 +104,100 @@ __device__ __forceinline__ int seq_tiles(const Args &a, const Seq &s, int nb) {
 }
 
 struct Share {
-    int per, t0, t1;     // tiles a share, and this CTA's [t0, t1); the line is shorter than 2^31
-    int b, hk, k, j;     // where t0 lies
+    int per, t0, t1;  // tiles between two boundaries, and this CTA's [t0, t1); the line is shorter than 2^31
+    int b, hk, k, j;  // where t0 lies (j = the item's tiles: at its end)
+    int cut;          // the boundary looked for last lies inside an item
     Seq seq;
 };
 
-// The share of CTA c of C.  One warp; every lane gets the result.  It runs once, cold, before
-// anything else can: short code counts for more than fast code.
-__device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
+// The share of CTA c of C; with last = 1, where its end lies (in b, hk, k, j and cut) and no t0.  One
+// warp; every lane gets the result.  It runs once, cold, before anything else can: short code
+// counts for more than fast code.
+__device__ __forceinline__ Share find_share(const Args &a, int c, int C, int last = 0) {
     const int lane = threadIdx.x & 31;
     Share r;
-    r.b = r.hk = r.k = r.j = 0;
+    r.b = r.hk = r.k = r.j = r.cut = 0;
     Seq s, ahead{0, 0, 0};
     int w = 0, nb = 0, total = 0;
-    if (lane < a.B) ahead = seq_info(a, lane, c == 0);
+    const bool report = c == 0 && last == 0;
+    if (lane < a.B) ahead = seq_info(a, lane, report);
 #pragma unroll 1
     for (int b = lane; b < a.B + lane; b += 32) {
         s = ahead;
         ahead = Seq{0, 0, 0};
-        if (b + 32 < a.B) ahead = seq_info(a, b + 32, c == 0);
+        if (b + 32 < a.B) ahead = seq_info(a, b + 32, report);
         nb = num_blocks(a, s);
         w = seq_tiles(a, s, nb);
         total += __reduce_add_sync(0xffffffffu, w);
     }
     total *= a.Hkv;
     r.per = max((int)((unsigned)(total + C - 1) / (unsigned)C), a.min_share);
-    r.t0 = (int)min((long long)r.per * c, (long long)total);
-    r.t1 = min(r.t0 + r.per, total);
-    if (r.t0 >= r.t1) return r;
-    int left = r.t0;
+    r.t0 = r.t1 = 0;
+    // the boundaries c + 1, then c: the item that each falls into, and which side of it it goes to
 #pragma unroll 1
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        if (a.B > 32) {  // (up to 32 sequences: s and w are theirs still)
-            s = Seq{0, 0, 0};
-            if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
-            nb = num_blocks(a, s);
-            w = seq_tiles(a, s, nb);
-        }
-        int incl = w * a.Hkv;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, incl > left);
-        if (!past) {
-            left -= __shfl_sync(0xffffffffu, incl, 31);
+    for (int e = 1; e >= last; --e) {
+        const int at = (int)min((long long)r.per * (c + e), (long long)total);
+        r.cut = 0;
+        if (at >= total) {
+            if (e == 0) r.t0 = total;
+            else r.t1 = total;
             continue;
         }
-        const int src = __ffs(past) - 1;
-        r.b = b0 + src;
-        r.seq.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-        r.seq.nq = __shfl_sync(0xffffffffu, s.nq, src);
-        r.seq.n = __shfl_sync(0xffffffffu, s.n, src);
-        w = __shfl_sync(0xffffffffu, w, src);
-        nb = __shfl_sync(0xffffffffu, nb, src);
-        left -= __shfl_sync(0xffffffffu, incl, src) - w * a.Hkv;
-        r.hk = (int)((unsigned)left / (unsigned)w);
-        left -= r.hk * w;
-        break;
-    }
-    r.j = left;
+        int left = at;
 #pragma unroll 1
-    for (int k0 = 0; nb > 1; k0 += 32) {
-        const int k = k0 + lane, t = k < nb ? block_tiles(a, r.seq, k) : 0;
-        int in = t;
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            if (a.B > 32) {  // (up to 32 sequences: s and w are theirs still)
+                s = Seq{0, 0, 0};
+                if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
+                nb = num_blocks(a, s);
+                w = seq_tiles(a, s, nb);
+            }
+            int incl = w * a.Hkv;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, in, d);
-            if (lane >= d) in += x;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, in > left);
-        if (hit || k0 + 32 >= nb) {
-            const int l = hit ? __ffs(hit) - 1 : 0;
-            r.k = k0 + l;
-            r.j = left - (__shfl_sync(0xffffffffu, in, l) - __shfl_sync(0xffffffffu, t, l));
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, incl > left);
+            if (!past) {
+                left -= __shfl_sync(0xffffffffu, incl, 31);
+                continue;
+            }
+            const int src = __ffs(past) - 1, ws = __shfl_sync(0xffffffffu, w, src);
+            r.b = b0 + src;
+            r.seq.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+            r.seq.nq = __shfl_sync(0xffffffffu, s.nq, src);
+            r.seq.n = __shfl_sync(0xffffffffu, s.n, src);
+            left -= __shfl_sync(0xffffffffu, incl, src) - ws * a.Hkv;
+            r.hk = (int)((unsigned)left / (unsigned)ws);
+            left -= r.hk * ws;
             break;
         }
-        left -= __shfl_sync(0xffffffffu, in, 31);
+        const int nbs = num_blocks(a, r.seq);
+        r.k = 0;
+#pragma unroll 1
+        for (int k0 = 0; nbs > 1; k0 += 32) {
+            const int k = k0 + lane, t = k < nbs ? block_tiles(a, r.seq, k) : 0;
+            int in = t;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, in, d);
+                if (lane >= d) in += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, in > left);
+            if (hit || k0 + 32 >= nbs) {
+                const int l = hit ? __ffs(hit) - 1 : 0;
+                r.k = k0 + l;
+                left -= __shfl_sync(0xffffffffu, in, l) - __shfl_sync(0xffffffffu, t, l);
+                break;
+            }
+            left -= __shfl_sync(0xffffffffu, in, 31);
+        }
+        const int tiles = block_tiles(a, r.seq, r.k);
+        r.j = left < a.min_cut ? 0 : tiles - left < a.min_cut ? tiles : left;
+        r.cut = r.j == left && left > 0;
+        if (e == 0) r.t0 = at + r.j - left;
+        else r.t1 = at + r.j - left;
     }
     return r;
 }
@@ -198,6 +215,18 @@ struct Walk {
         j0 = j;
         j1 = min(tiles, j + (t1 - t));
     }
+    // the item that the end of a share cuts, as one piece of all its tiles
+    __device__ __forceinline__ void at(const Args &a, const Share &sh) {
+        per = sh.per;
+        t = sh.t1 - sh.j;
+        t1 = 0x7fffffff;
+        b = sh.b;
+        hk = sh.hk;
+        k = sh.k;
+        seq = sh.seq;
+        nb = num_blocks(a, seq);
+        piece(a, 0);
+    }
     // false when the share is empty
     __device__ __forceinline__ bool begin(const Args &a, const Share &sh) {
         per = sh.per;
@@ -210,7 +239,7 @@ struct Walk {
         seq = sh.seq;
         nb = num_blocks(a, seq);
         piece(a, sh.j);
-        return true;
+        return j0 < tiles || next(a);
     }
     __device__ __forceinline__ bool next(const Args &a) {
         t += j1 - j0;
@@ -230,9 +259,15 @@ struct Walk {
         return true;
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == tiles; }
-    // the shares that hold the item's first tile and its tile `last`
-    __device__ __forceinline__ int first_share() const { return (int)((unsigned)(t - j0) / (unsigned)per); }
-    __device__ __forceinline__ int share_of(int last) const { return (int)((unsigned)(t - j0 + last) / (unsigned)per); }
+    // the share that holds the first part of the item, and the parts that its first n tiles fall
+    // into: the boundaries c per that lie min_cut tiles or more inside the item
+    __device__ __forceinline__ int first_share(const Args &a) const {
+        return (int)((unsigned)(t - j0 + a.min_cut + per - 1) / (unsigned)per) - 1;
+    }
+    __device__ __forceinline__ int parts(const Args &a, int c0, int n) const {
+        const int last = min(tiles - a.min_cut, n - 1);  // no boundary behind this tile counts
+        return last < 0 ? 1 : max((int)((unsigned)(t - j0 + last) / (unsigned)per) - c0, 0) + 1;
+    }
 };
 
 __device__ __forceinline__ int state_slot(int share, int first) { return 2 * share + (share == first ? 1 : 0); }

@@ -1,9 +1,9 @@
 // paged_tc_sm103.cu -- attention over a paged cache for many rows per key/value head (prompt
 // chunks) on the 5th-generation tensor cores.
 //
-// A block is 256 rows of one (sequence, key/value head) -- tokens times the query heads that share
-// the head, so a key or value tile in shared memory serves all of them -- as two 128-row tiles A
-// and B whose softmax warpgroups take turns with the tensor cores, as in the two-tile prefill
+// A block is up to 256 rows of one (sequence, key/value head) -- tokens times the G query heads that
+// share the head, so a key or value tile in shared memory serves all of them -- as two tiles A and
+// B of floor(128 / G) tokens (128 rows, or 125 and more for G < 8) whose softmax warpgroups take turns with the tensor cores, as in the two-tile prefill
 // kernel: while one warpgroup turns its S into P, the products of the other run.  One CTA an SM
 // walks its share of the line of key tiles (paged_sched.cuh).
 //
@@ -13,15 +13,16 @@
 //   warp 1       tensor-core issuer (one thread); owns the 512 TMEM columns:
 //                  S_A/P_A [0,128)  S_B/P_B [128,256)  O_A [256,384)  O_B [384,512).
 //   warps 4-7    rows of tile A, one thread a row (its TMEM lane);  warps 8-11  rows of tile B.
-//                They also bring their rows of Q into shared memory, the next block's right
-//                after the last P of this one, so that its first S runs under this one's epilogue.
-// A row's state over its part of an item goes to the workspace when the item is cut; tiles A and B
-// count and merge apart.
+//                One thread of each also asks for its tile's Q by TMA, for the next block
+//                right after the last P of this one, so that its first S runs under this one's
+//                epilogue.
+// A row's state over its part of an item goes to the workspace when the item is cut, and
+// paged_tc_merge_kernel merges the parts.
 #include <cudaTypedefs.h>
 
 #include "fwd_bf16_common.cuh"
 #include "paged.h"
-#include "paged_merge.cuh"
+#include "paged_sched.cuh"
 
 namespace attn {
 
@@ -46,10 +47,10 @@ constexpr uint32_t kTmemCols = 512;
 struct Ctrl {
     uint64_t q_full[2], s_full[2], p_full[2], o_final[2];
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t final_mma, group[2];  // group: the 128 threads of a warpgroup meet (bounded waits)
+    uint64_t final_mma;
     Share share;
     uint32_t tmem_base;
-    int abort, last[2];
+    int abort;
 };
 
 template <int D>
@@ -68,22 +69,33 @@ struct Tiles {
 };
 __device__ __forceinline__ Tiles tiles_of(const paged::Args &a, const Walk &w) {
     Tiles r;
-    const int rows = w.seq.nq * a.G - w.k * a.R;  // >= 1
+    const int rows = w.seq.nq * a.G - w.k * a.R, half = a.R >> 1;  // rows >= 1; tile A takes `half`
     int ka = w.keys;
-    if (rows > BQ && a.causal) {
-        const int last = paged::div_g(a, w.k * a.R + BQ - 1);
+    if (rows > half && a.causal) {
+        const int last = paged::div_g(a, w.k * a.R + half - 1);
         ka = min(max(w.seq.n - w.seq.nq + last + 1, 0), w.seq.n);
     }
     r.t[0] = (ka + BK - 1) / BK;
-    r.t[1] = rows > BQ ? (w.keys + BK - 1) / BK : 0;
+    r.t[1] = rows > half ? (w.keys + BK - 1) / BK : 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) r.n[x] = max(0, min(w.j1, r.t[x]) - w.j0);
     return r;
 }
 
+// A cut item's states: (m, l) as [slot][tile][128 rows], u as [slot][tile][D / 4][128 rows][4], so
+// that neighbouring rows (lanes) are neighbours in memory.
+__device__ __forceinline__ float2 *state_ml(const paged::Args &a, int slot, int x, int r) {
+    return reinterpret_cast<float2 *>(a.ml) + (slot * 2 + x) * (long long)BQ + r;
+}
+template <int D>
+__device__ __forceinline__ float4 *state_u(const paged::Args &a, int slot, int x, int r) {
+    return reinterpret_cast<float4 *>(a.u) + (slot * 2 + x) * (long long)(BQ * D / 4) + r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
     using L = Layout<D>;
     constexpr int KS = L::kKStages, VS = L::kVStages;
     extern __shared__ uint8_t smem_raw[];
@@ -94,11 +106,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
-            ptx::mbar_init(&ctrl->q_full[x], BQ);
+            ptx::mbar_init(&ctrl->q_full[x], 1);
             ptx::mbar_init(&ctrl->s_full[x], 1);
             ptx::mbar_init(&ctrl->p_full[x], BQ);
             ptx::mbar_init(&ctrl->o_final[x], 1);
-            ptx::mbar_init(&ctrl->group[x], BQ);
         }
         for (int s = 0; s < KS; ++s) {
             ptx::mbar_init(&ctrl->k_full[s], 1);
@@ -282,34 +293,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool ok = ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
             return __all_sync(0xffffffffu, ok);
         };
-        uint32_t gph = 0;
-        auto group_sync = [&]() -> bool {
-            ptx::mbar_arrive(&ctrl->group[X]);
-            const bool met = wait_warp(&ctrl->group[X], gph);
-            gph ^= 1;
-            return met;
-        };
-        // this thread's row of the piece's queries into tile X's buffer (zeros past the block's rows)
+        const int half = a.R >> 1;
+        // tile X's queries of a piece on their way into its buffer: whole tokens (those past the
+        // sequence are another's, or zeros; rows past `half` hold whatever was there: a row's
+        // values reach that row alone, and none of those is stored)
+        int asked = 0;
         auto bring_q = [&](const Walk &p) {
-            const int row = p.k * a.R + X * BQ + r;
-            uint8_t *dst = smem + X * L::kTile + r * 128;
-            if (row < p.seq.nq * a.G) {
-                const int tok = paged::div_g(a, row);
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (p.seq.q0 + tok) * a.qs0 +
-                                                                   (p.hk * a.G + row - tok * a.G) * a.qs1);
-                uint4 v[D / 8];
+            if (r == 0) {
+                ptx::mbar_arrive_expect_tx(&ctrl->q_full[X], (uint32_t)half * (D * 2));
+                const int tok = p.seq.q0 + paged::div_g(a, p.k * a.R + X * half);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (i / 8) * kPanelBytes + (((i % 8) ^ (r & 7)) << 4)) = v[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (i / 8) * kPanelBytes + ((i % 8) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                for (int pn = 0; pn < D / 64; ++pn)
+                    ptx::tma_load_3d(smem + X * L::kTile + pn * kPanelBytes, &tm_q, &ctrl->q_full[X], pn * 64, p.hk * a.G, tok);
+                ++asked;
             }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&ctrl->q_full[X]);
         };
         int vs = 0;                     // V ring slot and phase, for the rows that are zeroed
         uint32_t vph = 0, sph = 0, oph = 0;
@@ -318,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (more && ok) {
             __syncwarp();
             const Tiles tl = tiles_of(a, w);
-            const int n = tl.n[X], i0 = w.k * a.R + X * BQ, i = i0 + r, nmax = w.keys == 0 ? 0 : w.j1 - w.j0;
-            const bool mine = i < w.seq.nq * a.G;
+            const int n = tl.n[X], i0 = w.k * a.R + X * half, i = i0 + r, nmax = w.keys == 0 ? 0 : w.j1 - w.j0;
+            const bool mine = r < half && i < w.seq.nq * a.G;
             const int tok = paged::div_g(a, i), seqn = w.seq.n;
             const int lim = a.causal && mine ? min(max(seqn - w.seq.nq + tok + 1, 0), seqn) : seqn;
             const int lim0 = a.causal ? min(max(seqn - w.seq.nq + paged::div_g(a, i0) + 1, 0), seqn) : seqn;
@@ -354,10 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++vs == VS) { vs = 0; vph ^= 1; }
             // where this row goes, before the walk moves on
             const bool whole = w.j0 == 0 && w.j1 >= tl.t[X];
-            const int c0 = w.first_share();
-            const int cn = tl.t[X] > 0 ? w.share_of(tl.t[X] - 1) - c0 + 1 : 1;
+            const int c0 = w.first_share(a);
             const bool first = w.j0 == 0;
-            const int rows = w.seq.nq * a.G - w.k * a.R, q0 = w.seq.q0, hk = w.hk;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
             if (mine) {
@@ -383,31 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_before();
                 continue;
             }
-            // the state of this part
-            const long long slot = paged::state_slot(blockIdx.x, c0);
-            const long long at = slot * a.R + X * BQ + r;
-            *reinterpret_cast<float2 *>(a.ml + at * 2) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
-#pragma unroll
+            // the state of this part, for paged_tc_merge_kernel
+            const int slot = paged::state_slot(blockIdx.x, c0);
+            *state_ml(a, slot, X, r) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+            float4 *u4 = state_u<D>(a, slot, X, r);
+#pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
                 uint32_t ov[32];
                 ptx::tmem_ld32(lane_addr + o_col + cc * 32, ov);
                 ptx::tmem_ld_wait();
                 ptx::reg_fence(ov);
-                uint4 *dst = reinterpret_cast<uint4 *>(a.u + at * D + cc * 32);
 #pragma unroll
-                for (int t = 0; t < 8; ++t) dst[t] = make_uint4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
+                for (int t = 0; t < 8; ++t)
+                    u4[(cc * 8 + t) * BQ] = make_float4(__uint_as_float(ov[4 * t]), __uint_as_float(ov[4 * t + 1]),
+                                                        __uint_as_float(ov[4 * t + 2]), __uint_as_float(ov[4 * t + 3]));
             }
             ptx::tc_fence_before();
-            ok = paged::finish_cut<D, 4, 4>(
-                a, a.marks + X * paged::all_slots(gridDim.x), gridDim.x, X * BQ, min(BQ, rows - X * BQ), blockIdx.x, c0,
-                cn, r, &ctrl->last[X], group_sync, [&](int rr, __nv_bfloat16 *&orow, float *&lse) {
-                    const int tk = paged::div_g(a, i0 + rr);
-                    const long long t = q0 + tk;
-                    const int h = hk * a.G + i0 + rr - tk * a.G;
-                    orow = a.o + t * a.os0 + h * a.os1;
-                    lse = a.lse ? a.lse + t * a.Hq + h : nullptr;
-                });
         }
+        // the queries asked for have arrived (their block's S waited for them, unless a wait gave up)
+        if (!ok && asked > 0) ptx::mbar_wait_quiet(&ctrl->q_full[X], (asked - 1) & 1, kWaitLimitNs);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -418,20 +407,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Merges the states of cut items ("How Does FlashAttention Preserve Global Softmax Across Tiles?",
+// section 3), in share order.  CTA (c, tile, columns / 32) takes the item that goes past the end of
+// share c, if one does; a thread takes a row.  A kernel of its own: the merge's registers in the
+// attention kernel's made its softmax spill (a 2048-token chunk 420 -> 800 us), and at its end one
+// warpgroup merging 128 rows took 8 to 11 us where the whole GPU takes 3.  It finds its item
+// before the attention kernel is done: every CTA of that one has passed its own wait when this
+// one starts, so the lengths are there.
+constexpr int kMergeCols = 32;
 template <int D>
-attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid, cudaStream_t st) {
+__global__ void __launch_bounds__(BQ) paged_tc_merge_kernel(const paged::Args a) {
+    __shared__ Share share;
+    const int c = blockIdx.x, X = blockIdx.y, col = blockIdx.z * kMergeCols, r = threadIdx.x;
+    if (threadIdx.x < 32) {
+        const Share s = paged::find_share(a, c, gridDim.x, 1);
+        if (threadIdx.x == 0) share = s;
+    }
+    __syncthreads();
+    ptx::grid_dep_wait();
+    ptx::launch_dependents();
+    Walk w;
+    // the boundary behind share c: where it cuts an item, and that item's first part is in c
+    if (share.cut == 0) return;
+    w.at(a, share);
+    if (w.first_share(a) != c) return;
+    const int half = a.R >> 1, row = w.k * a.R + X * half + r;
+    const Tiles tl = tiles_of(a, w);
+    const int n = w.parts(a, c, tl.t[X]);
+    if (n < 2 || r >= half || row >= w.seq.nq * a.G) return;
+    auto slot = [&](int p) { return paged::state_slot(c + p, c); };
+    float M = -INFINITY, sum = 0.f, v[kMergeCols];
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) M = fmaxf(M, __ldcg(state_ml(a, slot(p), X, r)).x);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int t = 0; t < kMergeCols; ++t) v[t] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < n; ++p) {
+        const float2 ml = __ldcg(state_ml(a, slot(p), X, r));
+        const float4 *src = state_u<D>(a, slot(p), X, r) + (col / 4) * BQ;
+        const float f = ptx::ex2(ml.x - ref);
+        sum = fmaf(f, ml.y, sum);
+#pragma unroll
+        for (int t = 0; t < kMergeCols / 4; ++t) {
+            const float4 y = __ldcg(src + t * BQ);
+            v[4 * t] = fmaf(f, y.x, v[4 * t]);
+            v[4 * t + 1] = fmaf(f, y.y, v[4 * t + 1]);
+            v[4 * t + 2] = fmaf(f, y.z, v[4 * t + 2]);
+            v[4 * t + 3] = fmaf(f, y.w, v[4 * t + 3]);
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int tok = paged::div_g(a, row), h = w.hk * a.G + row - tok * a.G;
+    const long long t0 = w.seq.q0 + tok;
+    uint4 *o4 = reinterpret_cast<uint4 *>(a.o + t0 * a.os0 + h * a.os1 + col);
+#pragma unroll
+    for (int t = 0; t < kMergeCols / 8; ++t) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pk[e] = sum > 0.f ? ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv) : 0u;
+        o4[t] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+    if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int D>
+attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
+                     cudaStream_t st) {
     auto kern = paged_tc_kernel<D>;
     int smem = Layout<D>::kBytes;
     if (smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mq, mk, mv, a);
+    if (e == cudaSuccess && grid > 1)  // one share cuts nothing
+        e = launch_pdl(paged_tc_merge_kernel<D>, dim3(grid, 2, D / kMergeCols), dim3(BQ), 0, st, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace
 
-attn_status_t launch_paged_tc(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid, cudaStream_t st) {
-    return d == 64 ? launch<64>(mk, mv, a, grid, st) : launch<128>(mk, mv, a, grid, st);
+attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
+                              int d, int grid, cudaStream_t st) {
+    return d == 64 ? launch<64>(mq, mk, mv, a, grid, st) : launch<128>(mq, mk, mv, a, grid, st);
 }
 
 }  // namespace attn
