@@ -3,8 +3,8 @@
 // The rows of a sequence that share key/value head hk are numbered token * G + g (G = Hq / Hkv
 // query heads a key head) and taken R at a time: block k holds rows [k R, (k + 1) R).  An item
 // (b, hk, k) walks the 2^kt-key tiles up to the last key that its last row sees.  All items' tiles
-// in order (sequence, head, block) form one line of `total` tiles, cut at equal distances into
-// shares, one a CTA, whatever the lengths: a batch of one long and many short sequences, or a
+// in order (sequence, head, block), `cost` more a block for its beginning and end, form one line,
+// cut at equal distances into shares, one a CTA, whatever the lengths: a batch of one long and many short sequences, or a
 // single one, loads every SM alike.  A boundary that falls less than min_cut tiles inside an item
 // goes to that end of it (a cut costs about as much as so many tiles).  An item inside one share
 // is finished there.  An item cut by a boundary leaves one state (m, l, u) per share in the
@@ -29,7 +29,7 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives u
 
 struct Args {
     int B, T, Hq, Hkv, G, causal, R, kt;  // R rows a block, 2^kt keys a tile
-    int page_log2, width, num_pages, min_share, min_cut;
+    int page_log2, width, num_pages, min_share, min_cut, cost;
     float scale_log2;
     const __nv_bfloat16 *q;
     __nv_bfloat16 *o;
@@ -80,13 +80,15 @@ __device__ __forceinline__ int block_keys(const Args &a, const Seq &s, int k) {
 __device__ __forceinline__ int block_tiles(const Args &a, const Seq &s, int k) {
     return max(1, (block_keys(a, s, k) + (1 << a.kt) - 1) >> a.kt);
 }
+// What the block takes of the line.
+__device__ __forceinline__ int block_len(const Args &a, const Seq &s, int k) { return a.cost + block_tiles(a, s, k); }
 
-// Tiles of all blocks of lane's sequence (one head); the whole warp helps with long ones.
-__device__ __forceinline__ int seq_tiles(const Args &a, const Seq &s, int nb) {
+// The line of all blocks of a lane's sequence (one head); the whole warp helps with long ones.
+__device__ __forceinline__ int seq_len_of(const Args &a, const Seq &s, int nb) {
     const int lane = threadIdx.x & 31;
     int w = 0;
     if (nb <= 4)
-        for (int k = 0; k < nb; ++k) w += block_tiles(a, s, k);
+        for (int k = 0; k < nb; ++k) w += block_len(a, s, k);
     for (unsigned big = __ballot_sync(0xffffffffu, nb > 4); big; big &= big - 1) {
         const int src = __ffs(big) - 1;
         Seq o;
@@ -95,7 +97,7 @@ __device__ __forceinline__ int seq_tiles(const Args &a, const Seq &s, int nb) {
         o.n = __shfl_sync(0xffffffffu, s.n, src);
         const int onb = __shfl_sync(0xffffffffu, nb, src);
         int t = 0;
-        for (int k = lane; k < onb; k += 32) t += block_tiles(a, o, k);
+        for (int k = lane; k < onb; k += 32) t += block_len(a, o, k);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
         if (lane == src) w = t;
@@ -104,7 +106,7 @@ __device__ __forceinline__ int seq_tiles(const Args &a, const Seq &s, int nb) {
 }
 
 struct Share {
-    int per, t0, t1;  // tiles between two boundaries, and this CTA's [t0, t1); the line is shorter than 2^31
+    int per, t0, t1;  // the line between two boundaries, and this CTA's [t0, t1); the line is shorter than 2^31
     int b, hk, k, j;  // where t0 lies (j = the item's tiles: at its end)
     int cut;          // the boundary looked for last lies inside an item
     Seq seq;
@@ -127,7 +129,7 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
         ahead = Seq{0, 0, 0};
         if (b + 32 < a.B) ahead = seq_info(a, b + 32, report);
         nb = num_blocks(a, s);
-        w = seq_tiles(a, s, nb);
+        w = seq_len_of(a, s, nb);
         total += __reduce_add_sync(0xffffffffu, w);
     }
     total *= a.Hkv;
@@ -150,7 +152,7 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
                 s = Seq{0, 0, 0};
                 if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
                 nb = num_blocks(a, s);
-                w = seq_tiles(a, s, nb);
+                w = seq_len_of(a, s, nb);
             }
             int incl = w * a.Hkv;
 #pragma unroll
@@ -177,7 +179,7 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
         r.k = 0;
 #pragma unroll 1
         for (int k0 = 0; nbs > 1; k0 += 32) {
-            const int k = k0 + lane, t = k < nbs ? block_tiles(a, r.seq, k) : 0;
+            const int k = k0 + lane, t = k < nbs ? block_len(a, r.seq, k) : 0;
             int in = t;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -193,18 +195,20 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
             }
             left -= __shfl_sync(0xffffffffu, in, 31);
         }
-        const int tiles = block_tiles(a, r.seq, r.k);
-        r.j = left < a.min_cut ? 0 : tiles - left < a.min_cut ? tiles : left;
-        r.cut = r.j == left && left > 0;
-        if (e == 0) r.t0 = at + r.j - left;
-        else r.t1 = at + r.j - left;
+        const int tiles = block_tiles(a, r.seq, r.k), j = left - a.cost;
+        r.j = j < a.min_cut ? 0 : tiles - j < a.min_cut ? tiles : j;
+        r.cut = r.j == j && j > 0 && j < tiles;
+        // to the item's start, to its end, or between two tiles
+        const int to = at - left + (r.j == 0 ? 0 : a.cost + r.j);
+        if (e == 0) r.t0 = to;
+        else r.t1 = to;
     }
     return r;
 }
 
 // A walk over the pieces of a share; every role of the CTA makes the same walk.
 struct Walk {
-    int per, t, t1;  // tiles a share; the line's tile at which the piece begins; where the share ends
+    int per, t, t1;  // the line between two boundaries; where the item begins; where the share ends
     Seq seq;
     int b, hk, k, nb;
     int j0, j1, tiles, keys;  // the piece: tiles [j0, j1) of the block's `tiles`, which hold `keys` keys
@@ -213,36 +217,34 @@ struct Walk {
         keys = block_keys(a, seq, k);
         tiles = max(1, (keys + (1 << a.kt) - 1) >> a.kt);
         j0 = j;
-        j1 = min(tiles, j + (t1 - t));
+        j1 = min(tiles, t1 - t - a.cost);
     }
-    // the item that the end of a share cuts, as one piece of all its tiles
-    __device__ __forceinline__ void at(const Args &a, const Share &sh) {
+    __device__ __forceinline__ void place(const Args &a, const Share &sh) {
         per = sh.per;
-        t = sh.t1 - sh.j;
-        t1 = 0x7fffffff;
         b = sh.b;
         hk = sh.hk;
         k = sh.k;
         seq = sh.seq;
         nb = num_blocks(a, seq);
+    }
+    // the item that the end of a share cuts, as one piece of all its tiles
+    __device__ __forceinline__ void at(const Args &a, const Share &sh) {
+        place(a, sh);
+        t = sh.t1 - sh.j - a.cost;
+        t1 = 0x7fffffff;
         piece(a, 0);
     }
     // false when the share is empty
     __device__ __forceinline__ bool begin(const Args &a, const Share &sh) {
-        per = sh.per;
-        t = sh.t0;
+        if (sh.t0 >= sh.t1) return false;
+        place(a, sh);
+        t = sh.t0 - (sh.j == 0 ? 0 : a.cost + sh.j);
         t1 = sh.t1;
-        if (t >= t1) return false;
-        b = sh.b;
-        hk = sh.hk;
-        k = sh.k;
-        seq = sh.seq;
-        nb = num_blocks(a, seq);
         piece(a, sh.j);
         return j0 < tiles || next(a);
     }
     __device__ __forceinline__ bool next(const Args &a) {
-        t += j1 - j0;
+        t += a.cost + tiles;
         if (t >= t1) return false;
         if (++k == nb) {
             k = 0;
@@ -262,11 +264,11 @@ struct Walk {
     // the share that holds the first part of the item, and the parts that its first n tiles fall
     // into: the boundaries c per that lie min_cut tiles or more inside the item
     __device__ __forceinline__ int first_share(const Args &a) const {
-        return (int)((unsigned)(t - j0 + a.min_cut + per - 1) / (unsigned)per) - 1;
+        return (int)((unsigned)(t + a.cost + a.min_cut + per - 1) / (unsigned)per) - 1;
     }
     __device__ __forceinline__ int parts(const Args &a, int c0, int n) const {
         const int last = min(tiles - a.min_cut, n - 1);  // no boundary behind this tile counts
-        return last < 0 ? 1 : max((int)((unsigned)(t - j0 + last) / (unsigned)per) - c0, 0) + 1;
+        return last < 0 ? 1 : max((int)((unsigned)(t + a.cost + last) / (unsigned)per) - c0, 0) + 1;
     }
 };
 
