@@ -18,6 +18,6 @@ attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, co
                                 cudaStream_t s);
 constexpr int kTcBoxKeys = 128;
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
-                              int d, int grid, cudaStream_t s);
+                              int d, int grid, bool cuts, cudaStream_t s);
 
 }  // namespace attn

@@ -16,6 +16,8 @@ using namespace paged;
 struct Plan {
     bool tc;
     int R, kt, grid, box;
+    int min_cut;
+    bool cuts;  // a block may be cut
     bool fits;  // the line of tiles is shorter than 2^31
     size_t off_ml, off_u, bytes;
 };
@@ -40,6 +42,12 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
+    pl.min_cut = 4;
+    pl.cuts = pl.grid > 1 && keys > (int64_t)((2 * pl.min_cut - 1) << pl.kt);
+    if (!pl.cuts) {  // every block is shorter than two such parts: no states
+        pl.off_ml = pl.off_u = pl.bytes = 0;
+        return pl;
+    }
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     pl.off_ml = up((pl.tc ? 0 : slots) * sizeof(unsigned long long));
     const size_t srows = pl.tc ? 256 : pl.R;  // rows a slot
@@ -114,7 +122,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     // keys 17 either way, 19 with cuts of 8).  128-row tiles: an uncut block needs no share of its
     // own (512 tokens over 512 keys take 62 us with shares of 4, 29 with 1).
     a.min_share = pl.tc ? 1 : 8;
-    a.min_cut = 4;
+    a.min_cut = pl.min_cut;
     // What a block's beginning and end cost, in tiles (a mixed batch of 244 blocks of 3 to 32 tiles:
     // 134 us counted as 0, 105 as 2, 97 as 4, 97 as 6; few rows: no difference).
     a.cost = 4;
@@ -141,7 +149,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
         CUtensorMap mq;
         const attn_status_t r = encode_q(&mq, p, 128 / a.G);
         if (r) return r;
-        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.grid, st);
+        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.grid, pl.cuts, st);
     }
     return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }

@@ -473,13 +473,13 @@ __global__ void __launch_bounds__(BQ) paged_tc_merge_kernel(const paged::Args a)
 
 template <int D>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
-                     cudaStream_t st) {
+                     bool cuts, cudaStream_t st) {
     auto kern = paged_tc_kernel<D>;
     int smem = Layout<D>::kBytes;
     if (smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mq, mk, mv, a);
-    if (e == cudaSuccess && grid > 1)  // one share cuts nothing
+    if (e == cudaSuccess && cuts)
         e = launch_pdl(paged_tc_merge_kernel<D>, dim3(grid, 2, D / kMergeCols), dim3(BQ), 0, st, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
@@ -487,8 +487,8 @@ attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
 }  // namespace
 
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
-                              int d, int grid, cudaStream_t st) {
-    return d == 64 ? launch<64>(mq, mk, mv, a, grid, st) : launch<128>(mq, mk, mv, a, grid, st);
+                              int d, int grid, bool cuts, cudaStream_t st) {
+    return d == 64 ? launch<64>(mq, mk, mv, a, grid, cuts, st) : launch<128>(mq, mk, mv, a, grid, cuts, st);
 }
 
 }  // namespace attn

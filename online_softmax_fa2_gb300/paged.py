@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -74,6 +75,34 @@ class PagedFwdParams(ctypes.Structure):
                 ("q", _vp), ("o", _vp), ("q_stride", _S2), ("o_stride", _S2), ("lse", _vp)]
 
 
+def _packer(cls):
+    """struct.Struct of a mirror's fields in order (nested ones in place), C alignment: filling it takes
+    a third of the time that filling the mirror takes, and a small call is as long as its host side."""
+    def fmt(c):
+        out = ""
+        for _, t in c._fields_:
+            if issubclass(t, ctypes.Structure):
+                out += fmt(t) + "0q"
+            elif issubclass(t, ctypes.Array):
+                out += "q" * t._length_
+            else:
+                out += {_i32: "i", _i64: "q", _vp: "P", _f32: "f"}[t]
+        return out
+    pack = struct.Struct("@" + fmt(cls) + "0q")
+    assert pack.size == ctypes.sizeof(cls)
+    return pack.pack
+
+
+_pack_norm_rope, _pack_norm_rope_bwd = _packer(NormRopeParams), _packer(NormRopeBwdParams)
+_pack_append, _pack_fwd = _packer(PagedAppendParams), _packer(PagedFwdParams)
+
+class _Block:
+    """Argument type of a parameter block: packed bytes, or a mirror."""
+    @classmethod
+    def from_param(cls, v):
+        return v if v is None or isinstance(v, bytes) else ctypes.byref(v)
+
+
 _lib = None
 
 
@@ -81,14 +110,14 @@ def _load():
     global _lib
     if _lib is None:
         lib = _ofa.load()
-        P, size = ctypes.POINTER, ctypes.c_size_t
+        size, params = ctypes.c_size_t, _Block
         for name, args, res in (
-                ("attn_qk_norm_rope", [P(NormRopeParams), _vp], _i32),
+                ("attn_qk_norm_rope", [params, _vp], _i32),
                 ("attn_qk_norm_rope_bwd_workspace_bytes", [_i64] * 5, size),
-                ("attn_qk_norm_rope_bwd", [P(NormRopeBwdParams), _vp, size, _vp], _i32),
-                ("attn_paged_append", [P(PagedAppendParams), _vp], _i32),
-                ("attn_paged_fwd_workspace_bytes", [P(PagedFwdParams)], size),
-                ("attn_paged_fwd", [P(PagedFwdParams), _vp, size, _vp], _i32)):
+                ("attn_qk_norm_rope_bwd", [params, _vp, size, _vp], _i32),
+                ("attn_paged_append", [params, _vp], _i32),
+                ("attn_paged_fwd_workspace_bytes", [params], size),
+                ("attn_paged_fwd", [params, _vp, size, _vp], _i32)):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, res
         _lib = lib
@@ -96,36 +125,38 @@ def _load():
 
 
 _DTYPES = {torch.float32: _ofa.F32, torch.bfloat16: _ofa.BF16}
+_BAD = "{} must be {} {} on cuda:{} with the last dimension contiguous, got {} {} with strides {} on {}"
 
 
 def _need(t, name, shape, dtype, dev):
-    """t as a tensor of that shape and dtype on dev, its last dimension contiguous."""
-    if t.dtype != dtype or t.device != dev or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    """The address of t, checked to be a tensor of that shape and dtype on device number dev with its
+    last dimension contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(_BAD.format(name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.stride(), t.device))
     return t.data_ptr()
 
 
 def _device(q, dim):
-    if not q.is_cuda:
+    dev = q.get_device()
+    if dev < 0:
         raise ValueError("every tensor must be on a CUDA device (there is no CPU path)")
     if q.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {q.dtype}: use torch.float32 or torch.bfloat16")
     if q.dim() != dim:
         raise ValueError(f"q must be {dim}-D, got {tuple(q.shape)}")
-    return q.device
+    return dev
 
 
 def _call(dev, stream, made, fn, *args):
-    """fn(*args, stream) with dev current; tensors made here are kept for a stream given."""
+    """fn(*args, stream) with device number dev current; tensors made here are kept for a stream given."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
         raw = stream.cuda_stream
         for t in made:
-            t.record_stream(stream)
-    if torch.cuda.current_device() == dev.index:
+            if t is not None:
+                t.record_stream(stream)
+    if torch.cuda.current_device() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -135,39 +166,41 @@ def _call(dev, stream, made, fn, *args):
 
 
 def _weight(w, name, d, dtype, dev):
-    return None if w is None else _need(w, name, (d,), dtype, dev)
+    return 0 if w is None else _need(w, name, (d,), dtype, dev)
 
 
 def _angles(cos_sin, dev):
-    """(pointer, rows, row stride, rot) of the angle table [P, rot], or Nones."""
+    """(pointer, rows, row stride, rot) of the angle table [P, rot], or zeros."""
     if cos_sin is None:
-        return None, 0, 0, 0
+        return 0, 0, 0, 0
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [positions, rot]")
-    rows, rot = cos_sin.shape
-    return _need(cos_sin, "cos_sin", (rows, rot), torch.float32, dev), rows, cos_sin.stride(0), rot
+    rows, rot = shape = cos_sin.shape
+    return _need(cos_sin, "cos_sin", shape, torch.float32, dev), rows, cos_sin.stride(0), rot
 
 
 def _norm_rope_params(q, k, qo, ko, wq, wk, cos_sin, positions, eps, interleaved):
+    """The values of attn_qk_norm_rope_params_t, in order."""
     dev, dt = _device(q, 4), q.dtype
-    B, N, Hq, d = q.shape
+    B, N, Hq, d = shape = q.shape
     Hkv = k.shape[2] if k.dim() == 4 else -1
-    kp = _need(k, "k", (B, N, Hkv, d), dt, dev)
-    qp = _need(q, "q", (B, N, Hq, d), dt, dev)
-    qop = None if qo is None else _need(qo, "q_out", (B, N, Hq, d), dt, dev)
-    kop = None if ko is None else _need(ko, "k_out", (B, N, Hkv, d), dt, dev)
+    kshape = (B, N, Hkv, d)
+    kp, qp = _need(k, "k", kshape, dt, dev), _need(q, "q", shape, dt, dev)
+    q0, q1, q2, _ = q.stride()
+    k0, k1, k2, _ = k.stride()
+    qop = kop = a0 = a1 = a2 = b0 = b1 = b2 = pos = p0 = p1 = 0
+    if qo is not None:
+        qop, kop = _need(qo, "q_out", shape, dt, dev), _need(ko, "k_out", kshape, dt, dev)
+        a0, a1, a2, _ = qo.stride()
+        b0, b1, b2, _ = ko.stride()
     cs, rows, row, rot = _angles(cos_sin, dev)
-    pos, ps = None, (0, 0)
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.device != dev:
-            raise ValueError(f"positions must be int32 on {dev}")
+        if positions.dtype != torch.int32 or positions.get_device() != dev:
+            raise ValueError(f"positions must be int32 on cuda:{dev}")
         positions = positions.expand(B, N)
-        pos, ps = positions.data_ptr(), positions.stride()
-    z = (0, 0, 0)
-    return NormRopeParams(_DTYPES[dt], 1 if interleaved else 0, B, N, Hq, Hkv, d, rot, qp, kp, qop, kop,
-                          q.stride()[:3], k.stride()[:3], z if qo is None else qo.stride()[:3],
-                          z if ko is None else ko.stride()[:3], _weight(wq, "wq", d, dt, dev),
-                          _weight(wk, "wk", d, dt, dev), cs, rows, row, pos, ps, eps)
+        pos, (p0, p1) = positions.data_ptr(), positions.stride()
+    return (_DTYPES[dt], 1 if interleaved else 0, B, N, Hq, Hkv, d, rot, qp, kp, qop, kop, q0, q1, q2, k0, k1, k2, a0, a1,
+            a2, b0, b1, b2, _weight(wq, "wq", d, dt, dev), _weight(wk, "wk", d, dt, dev), cs, rows, row, pos, p0, p1, eps)
 
 
 def attn_qk_norm_rope(q, k, wq=None, wk=None, cos_sin=None, positions=None, eps=1e-6, interleaved=False, q_out=None,
@@ -177,15 +210,14 @@ def attn_qk_norm_rope(q, k, wq=None, wk=None, cos_sin=None, positions=None, eps=
     at positions (int32 [B, N] or broadcast; None: 0 .. N - 1).  Pairs are (c, c + rot/2), or
     (2c, 2c + 1) when interleaved.  Returns (q_out, k_out), which may be given, q and k
     themselves included.  See include/attn.h, attn_qk_norm_rope."""
-    lib, made = _load(), []
+    lib, made = _load(), (q_out, k_out)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        made.append(q_out)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        made.append(k_out)
-    p = _norm_rope_params(q, k, q_out, k_out, wq, wk, cos_sin, positions, eps, interleaved)
-    _call(q.device, stream, made, lib.attn_qk_norm_rope, p)
+    p = _pack_norm_rope(*_norm_rope_params(q, k, q_out, k_out, wq, wk, cos_sin, positions, eps, interleaved))
+    _call(q.get_device(), stream, (q_out if made[0] is None else None, k_out if made[1] is None else None),
+          lib.attn_qk_norm_rope, p)
     return q_out, k_out
 
 
@@ -199,31 +231,31 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, 
     outputs.  Returns (dq, dk, dwq, dwk); dq and dk may be given (dq_out and dk_out themselves
     included), dwq and dwk are float32 [d], None where the weight is."""
     lib, made = _load(), []
-    dev = _device(q, 4)
+    f = _norm_rope_params(q, k, None, None, wq, wk, cos_sin, positions, eps, interleaved)
+    dev, dt, cuda = q.get_device(), q.dtype, q.device
+    B, N, Hq, Hkv, d = f[2:7]
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        dq = torch.empty(q.shape, dtype=dt, device=cuda)
         made.append(dq)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        dk = torch.empty(k.shape, dtype=dt, device=cuda)
         made.append(dk)
-    f = _norm_rope_params(q, k, None, None, wq, wk, cos_sin, positions, eps, interleaved)
-    B, N, Hq, Hkv, d = f.B, f.N, f.Hq, f.Hkv, f.d
     dwq = dwk = None
     if wq is not None:
-        dwq = torch.empty(d, dtype=torch.float32, device=dev)
+        dwq = torch.empty(d, dtype=torch.float32, device=cuda)
         made.append(dwq)
     if wk is not None:
-        dwk = torch.empty(d, dtype=torch.float32, device=dev)
+        dwk = torch.empty(d, dtype=torch.float32, device=cuda)
         made.append(dwk)
     if workspace is None and (dwq is not None or dwk is not None):
         workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
-                                device=dev)
+                                device=cuda)
         made.append(workspace)
-    sq, sk, dt = (B, N, Hq, d), (B, N, Hkv, d), q.dtype
-    p = NormRopeBwdParams(f, _need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev),
-                          _need(dq, "dq", sq, dt, dev), _need(dk, "dk", sk, dt, dev), dq_out.stride()[:3],
-                          dk_out.stride()[:3], dq.stride()[:3], dk.stride()[:3],
-                          None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr())
+    sq, sk = (B, N, Hq, d), (B, N, Hkv, d)
+    ptrs = (_need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev), _need(dq, "dq", sq, dt, dev),
+            _need(dk, "dk", sk, dt, dev))
+    p = _pack_norm_rope_bwd(*f, *ptrs, *dq_out.stride()[:3], *dk_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3],
+                            0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr())
     wsp, wsn = _workspace(workspace, dev)
     _call(dev, stream, made, lib.attn_qk_norm_rope_bwd, p, wsp, wsn)
     return dq, dk, dwq, dwk
@@ -232,24 +264,27 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, 
 def _workspace(t, dev):
     if t is None:
         return None, 0
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {dev}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q):
+    """The values of attn_paged_cache_t, in order."""
     if k_pages.dim() != 4 or k_pages.shape[3] != d:
         raise ValueError(f"k_pages must be [num_pages, page_size, Hkv, {d}], got {tuple(k_pages.shape)}")
     pages, page, Hkv, _ = shape = k_pages.shape
     kp, vp = _need(k_pages, "k_pages", shape, dt, dev), _need(v_pages, "v_pages", shape, dt, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, width]")
-    B, width = block_table.shape
-    bt = _need(block_table, "block_table", (B, width), torch.int32, dev)
+    B, width = table = block_table.shape
+    bt = _need(block_table, "block_table", table, torch.int32, dev)
     lens = _need(kv_lens, "kv_lens", (B,), torch.int32, dev)
-    cu = None if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)
-    return PagedCache(_DTYPES[dt], page, B, T, Hkv, d, kp, vp, k_pages.stride()[:3], v_pages.stride()[:3], pages, bt,
-                      width, block_table.stride(0), lens, cu)
+    cu = 0 if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)
+    k0, k1, k2, _ = k_pages.stride()
+    v0, v1, v2, _ = v_pages.stride()
+    return (_DTYPES[dt], page, B, T, Hkv, d, kp, vp, k0, k1, k2, v0, v1, v2, pages, bt, width, block_table.stride(0), lens,
+            cu)
 
 
 def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None, wq=None, wk=None, cos_sin=None,
@@ -258,40 +293,40 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
     slots of the paged cache, in place, and returns the normed and rotated queries.  kv_lens
     counts the new tokens; positions (int32 [T]; None: each token's place in its sequence) are
     the rotation's.  See include/attn.h, attn_paged_append."""
-    lib, made = _load(), []
+    lib, made = _load(), None
     dev, dt = _device(q, 3), q.dtype
-    T, Hq, d = q.shape
+    T, Hq, d = shape = q.shape
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        made.append(q_out)
+        made = q_out = torch.empty(shape, dtype=dt, device=q.device)
     c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
-    sk = (T, c.Hkv, d)
+    sk = (T, c[4], d)
     cs, rows, row, rot = _angles(cos_sin, dev)
-    p = PagedAppendParams(c, Hq, rot, _need(q, "q", q.shape, dt, dev), _need(k, "k", sk, dt, dev),
-                          _need(v, "v", sk, dt, dev), _need(q_out, "q_out", q.shape, dt, dev), q.stride()[:2],
-                          k.stride()[:2], v.stride()[:2], q_out.stride()[:2], _weight(wq, "wq", d, dt, dev),
-                          _weight(wk, "wk", d, dt, dev), cs, rows, row,
-                          None if positions is None else _need(positions, "positions", (T,), torch.int32, dev), eps,
-                          1 if interleaved else 0)
-    _call(dev, stream, made, lib.attn_paged_append, p)
+    p = _pack_append(*c, Hq, rot, _need(q, "q", shape, dt, dev), _need(k, "k", sk, dt, dev), _need(v, "v", sk, dt, dev),
+                     _need(q_out, "q_out", shape, dt, dev), *q.stride()[:2], *k.stride()[:2], *v.stride()[:2],
+                     *q_out.stride()[:2], _weight(wq, "wq", d, dt, dev), _weight(wk, "wk", d, dt, dev), cs, rows, row,
+                     0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev), eps,
+                     1 if interleaved else 0)
+    _call(dev, stream, (made,), lib.attn_paged_append, p)
     return q_out
 
 
 def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse):
+    """attn_paged_fwd_params_t, packed."""
     dev, dt = _device(q, 3), q.dtype
-    T, Hq, d = q.shape
+    T, Hq, d = shape = q.shape
     c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
-    lp = None
+    lp = op = o0 = o1 = 0
+    if out is not None:
+        op, (o0, o1, _) = _need(out, "out", shape, dt, dev), out.stride()
     if lse is not None:
         lp = _need(lse, "lse", (T, Hq), torch.float32, dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
     if max_q is None:
-        max_q = 0 if cu_q is not None else T // c.B if c.B else 0
-    o = q if out is None else out
-    return PagedFwdParams(c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q,
-                          _need(q, "q", q.shape, dt, dev), _need(o, "out", q.shape, dt, dev), q.stride()[:2],
-                          o.stride()[:2], lp)
+        max_q = 0 if cu_q is not None else T // c[2] if c[2] else 0
+    q0, q1, _ = q.stride()
+    return _pack_fwd(*c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q,
+                     _need(q, "q", shape, dt, dev), op, q0, q1, o0, o1, lp)
 
 
 def paged_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True) -> int:
@@ -320,6 +355,7 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             made.append(workspace)
-    wsp, wsn = _workspace(workspace, q.device)
-    _call(q.device, stream, made, lib.attn_paged_fwd, p, wsp, wsn)
+    dev = q.get_device()
+    wsp, wsn = _workspace(workspace, dev)
+    _call(dev, stream, made, lib.attn_paged_fwd, p, wsp, wsn)
     return out, lse

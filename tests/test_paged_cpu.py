@@ -34,6 +34,31 @@ def test_ctypes_mirrors_match_the_header(tmp_path, struct, cls):
         assert got[name] == getattr(cls, name).offset, (struct, name)
 
 
+@pytest.mark.parametrize("cls,pack", [
+    (paged.NormRopeParams, paged._pack_norm_rope), (paged.NormRopeBwdParams, paged._pack_norm_rope_bwd),
+    (paged.PagedAppendParams, paged._pack_append), (paged.PagedFwdParams, paged._pack_fwd)])
+def test_packed_blocks_are_the_mirrors(cls, pack):
+    """Every field of a block packed by position reads back from the mirror laid over it."""
+    def fields(c, path=()):
+        for name, t in c._fields_:
+            if issubclass(t, ctypes.Structure):
+                yield from fields(t, path + (name,))
+            else:
+                yield path + (name,), t
+    values, want, n = [], [], 1
+    for path, t in fields(cls):
+        k = t._length_ if issubclass(t, ctypes.Array) else 1
+        values += list(range(n, n + k))
+        want.append((path, list(range(n, n + k))))
+        n += k
+    p = cls.from_buffer_copy(pack(*values))
+    for path, w in want:
+        v = p
+        for name in path:
+            v = getattr(v, name)
+        assert (list(v) if isinstance(v, ctypes.Array) else [v]) == w, path
+
+
 def fill(p, **kw):
     for k, v in kw.items():
         if k.startswith("cache_"):
