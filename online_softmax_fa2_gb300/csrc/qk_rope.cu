@@ -25,6 +25,15 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
+// (d0, d1) = (a0 * b0, a1 * b1) in one packed instruction
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // 16 bytes past L1 (each is read once); not .nc, since an output may be the input itself.
 __device__ __forceinline__ uint4 ld16_rw(const void *p) {
     uint4 r;
@@ -105,11 +114,10 @@ struct Row2 {  // a lane's two chunks of a row
     }
 };
 
-// Where a lane's two chunks lie, and the angles that turn them.
+// Where a lane's two chunks lie.
 struct Lane {
     int e0, e1;     // first elements of the two chunks
     bool on, turn;  // has chunks (the group may be wider than the row); they are rotated
-    float co[8], si[8];
 };
 
 template <int L>
@@ -123,43 +131,49 @@ __device__ __forceinline__ Lane make_lane(int d, int rot) {
     return ln;
 }
 
-// The angles of one position: eight pairs a lane.  half split: pair c is (c, c + rot/2), so the
-// lane's pairs are 8p .. 8p + 7; adjacent: pair c is (2c, 2c + 1), so they are 4p .. 4p + 3
-// (first chunk) and 4 (p + rot/16) .. + 3 (second).
-__device__ __forceinline__ void load_angles(Lane &ln, const float *row, int rot, bool inter) {
+// The angles of one position: eight pairs a lane (cos 1 and sin 0 where nothing is rotated).  half
+// split: pair c is (c, c + rot/2), so the lane's pairs are 8p .. 8p + 7; adjacent: pair c is
+// (2c, 2c + 1), so they are 4p .. 4p + 3 (first chunk) and 4 (p + rot/16) .. + 3 (second).
+struct Angles {
+    float co[8], si[8];
+};
+__device__ __forceinline__ Angles load_angles(const Lane &ln, const float *row, int rot, bool inter) {
+    Angles an;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-        ln.co[t] = 1.f;
-        ln.si[t] = 0.f;
+        an.co[t] = 1.f;
+        an.si[t] = 0.f;
     }
-    if (!ln.turn) return;
+    if (!ln.turn) return an;
     const int a = inter ? ln.e0 / 2 : ln.e0, b = inter ? ln.e1 / 2 : ln.e0 + 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int at = s ? b : a;
         const float4 c = __ldg(reinterpret_cast<const float4 *>(row + at));
         const float4 n = __ldg(reinterpret_cast<const float4 *>(row + rot / 2 + at));
-        ln.co[4 * s] = c.x; ln.co[4 * s + 1] = c.y; ln.co[4 * s + 2] = c.z; ln.co[4 * s + 3] = c.w;
-        ln.si[4 * s] = n.x; ln.si[4 * s + 1] = n.y; ln.si[4 * s + 2] = n.z; ln.si[4 * s + 3] = n.w;
+        an.co[4 * s] = c.x; an.co[4 * s + 1] = c.y; an.co[4 * s + 2] = c.z; an.co[4 * s + 3] = c.w;
+        an.si[4 * s] = n.x; an.si[4 * s + 1] = n.y; an.si[4 * s + 2] = n.z; an.si[4 * s + 3] = n.w;
     }
+    return an;
 }
 
-// y <- R y (sign 1) or R^T y (sign -1) for the lane's 16 elements.
-__device__ __forceinline__ void turn(float (&y)[16], const Lane &ln, bool inter, float sign) {
-    if (!inter) {
+// Of the lane's 16 elements, pair t's are A(t) and B(t): in order (half split: t and 8 + t), or
+// neighbours (adjacent: 2t and 2t + 1).  apart() and together() bring the adjacent ones into the
+// half split's places and back, so that the arithmetic is the same two-element instructions.
+template <bool kInter>
+__device__ __forceinline__ void apart(const float (&f)[16], float (&y)[16]) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float a = y[t], b = y[8 + t], s = sign * ln.si[t];
-            y[t] = fmaf(a, ln.co[t], -b * s);
-            y[8 + t] = fmaf(a, s, b * ln.co[t]);
-        }
-    } else {
+    for (int t = 0; t < 8; ++t) {
+        y[t] = f[kInter ? 2 * t : t];
+        y[8 + t] = f[kInter ? 2 * t + 1 : 8 + t];
+    }
+}
+template <bool kInter>
+__device__ __forceinline__ void together(const float (&y)[16], float (&f)[16]) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const float a = y[2 * t], b = y[2 * t + 1], s = sign * ln.si[t];
-            y[2 * t] = fmaf(a, ln.co[t], -b * s);
-            y[2 * t + 1] = fmaf(a, s, b * ln.co[t]);
-        }
+    for (int t = 0; t < 8; ++t) {
+        f[kInter ? 2 * t : t] = y[t];
+        f[kInter ? 2 * t + 1 : 8 + t] = y[8 + t];
     }
 }
 
@@ -170,51 +184,86 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float sum16(const float (&f)[16]) {
+// sum of x y over the lane's 16 elements
+__device__ __forceinline__ float dot16(const float (&x)[16], const float (&y)[16]) {
     float s[4];
+    mul2(s[0], s[1], x[0], x[1], y[0], y[1]);
+    mul2(s[2], s[3], x[2], x[3], y[2], y[3]);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) s[t] = (f[t] + f[4 + t]) + (f[8 + t] + f[12 + t]);
-    return (s[0] + s[1]) + (s[2] + s[3]);
+    for (int t = 4; t < 16; t += 4) {
+        ptx::fma2(s[0], s[1], x[t], x[t + 1], y[t], y[t + 1], s[0], s[1]);
+        ptx::fma2(s[2], s[3], x[t + 2], x[t + 3], y[t + 2], y[t + 3], s[2], s[3]);
+    }
+    return (s[0] + s[2]) + (s[1] + s[3]);
 }
 
-// One kind of head of one token: rows h = first, first + step, ... below hi of a warp's group,
-// U of them in flight.  The loop runs alike for all groups (the shuffles need the whole warp).
-template <typename T, int L, int U>
-__device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, long long out_h, const T *w, int lo,
-                                          int hi, const Lane &ln, bool inter, int d, float eps) {
+// d = x y + z, d = x y, d = x c for 8 elements
+__device__ __forceinline__ void mul8(float *d, const float *x, const float *y) {
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) mul2(d[t], d[t + 1], x[t], x[t + 1], y[t], y[t + 1]);
+}
+__device__ __forceinline__ void fma8(float *d, const float *x, const float *y, const float *z) {
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) ptx::fma2(d[t], d[t + 1], x[t], x[t + 1], y[t], y[t + 1], z[t], z[t + 1]);
+}
+__device__ __forceinline__ void scale8(float *d, const float *x, float c) {
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) mul2(d[t], d[t + 1], x[t], x[t + 1], c, c);
+}
+
+// Heads [lo, lo + 32 / L * U) below hi of one tensor at one token, U a group and all in flight.  The
+// norm's weight goes into the angles once for all of them: with (a, b) = r (x_a w_a, x_b w_b),
+//   y_a = r (x_a (w_a cos) - x_b (w_b sin)),  y_b = r (x_a (w_a sin) + x_b (w_b cos)).
+// (The shuffles need the whole warp: rows past hi are zeros.)
+template <typename T, int L, int U, bool kInter>
+__device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, long long out_h, const T *w,
+                                          const float *angle_row, int lo, int hi, const Lane &ln, int rot, float inv_d,
+                                          float eps) {
     constexpr int GW = 32 / L;
-    const int grp = (threadIdx.x & 31) / L;
-    float wf[16];
-    if (w && ln.on) {
-        Row2<T> r;
-        r.load(w, ln.e0, ln.e1, true);
-        r.get(wf);
-    }
-    for (int h0 = lo; h0 < hi; h0 += GW * U) {
-        Row2<T> x[U];
+    const int h0 = lo + (threadIdx.x & 31) / L;
+    Row2<T> x[U], wr;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW + grp;
-            x[u].load(in + h * in_h, ln.e0, ln.e1, ln.on && h < hi);
+    for (int u = 0; u < U; ++u) x[u].load(in + (h0 + u * GW) * in_h, ln.e0, ln.e1, ln.on && h0 + u * GW < hi);
+    wr.load(w, ln.e0, ln.e1, w != nullptr && ln.on);
+    const Angles an = load_angles(ln, angle_row, rot, kInter);
+    float ac[8], as[8], bc[8], bs[8];  // w_a cos, w_a sin, w_b cos, -w_b sin
+    {
+        float wf[16], y[16];
+        wr.get(wf);
+        apart<kInter>(wf, y);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            ac[t] = an.co[t];
+            as[t] = an.si[t];
+            bc[t] = an.co[t];
+            bs[t] = -an.si[t];
         }
+        if (w) {
+            mul8(ac, ac, y);
+            mul8(as, as, y);
+            mul8(bc, bc, y + 8);
+            mul8(bs, bs, y + 8);
+        }
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW + grp;
-            float f[16];
-            x[u].get(f);
-            if (w) {
-                float q[16];
-#pragma unroll
-                for (int t = 0; t < 16; ++t) q[t] = f[t] * f[t];
-                const float r = rsqrtf(group_sum<L>(sum16(q)) / (float)d + eps);
-#pragma unroll
-                for (int t = 0; t < 16; ++t) f[t] *= r * wf[t];
-            }
-            turn(f, ln, inter, 1.f);
-            if (ln.on && h < hi) {
-                x[u].set(f);
-                x[u].store(out + h * out_h, ln.e0, ln.e1);
-            }
+    for (int u = 0; u < U; ++u) {
+        float f[16], y[16], z[16];
+        x[u].get(f);
+        float r = 1.f;
+        if (w) r = rsqrtf(fmaf(group_sum<L>(dot16(f, f)), inv_d, eps));
+        apart<kInter>(f, y);
+        if (w) {
+            scale8(y, y, r);
+            scale8(y + 8, y + 8, r);
+        }
+        mul8(z, y + 8, bs);
+        fma8(z, y, ac, z);
+        mul8(z + 8, y + 8, bc);
+        fma8(z + 8, y, as, z + 8);
+        together<kInter>(z, f);
+        if (ln.on && h0 + u * GW < hi) {
+            x[u].set(f);
+            x[u].store(out + (h0 + u * GW) * out_h, ln.e0, ln.e1);
         }
     }
 }
@@ -223,20 +272,13 @@ template <typename T, int L, int U>
 __device__ __forceinline__ void copy_rows(const T *in, long long in_h, T *out, long long out_h, int lo, int hi,
                                           const Lane &ln) {
     constexpr int GW = 32 / L;
-    const int grp = (threadIdx.x & 31) / L;
-    for (int h0 = lo; h0 < hi; h0 += GW * U) {
-        Row2<T> x[U];
+    const int h0 = lo + (threadIdx.x & 31) / L;
+    Row2<T> x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW + grp;
-            x[u].load(in + h * in_h, ln.e0, ln.e1, ln.on && h < hi);
-        }
+    for (int u = 0; u < U; ++u) x[u].load(in + (h0 + u * GW) * in_h, ln.e0, ln.e1, ln.on && h0 + u * GW < hi);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW + grp;
-            if (ln.on && h < hi) x[u].store(out + h * out_h, ln.e0, ln.e1);
-        }
-    }
+    for (int u = 0; u < U; ++u)
+        if (ln.on && h0 + u * GW < hi) x[u].store(out + (h0 + u * GW) * out_h, ln.e0, ln.e1);
 }
 
 // A position clamped into the angle table; one outside is reported.
@@ -265,10 +307,12 @@ __device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
     return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
+// A warp takes one task: a token, a tensor (q, k, v) and the part of its heads that its groups
+// hold at once, U heads each.  Tasks of a token: cq parts of q, then ck of k (and of v).
 struct RopeArgs {
-    int B, N, Hq, Hk, d, rot, inter, P, parts;
+    int N, Hq, Hk, d, rot, P, cq, ck;
     long long tasks;
-    float eps;
+    float inv_d, eps;
     const void *q, *k, *wq, *wk;
     void *qo, *ko;
     long long qs[3], ks[3], qos[3], kos[3];
@@ -279,54 +323,52 @@ struct RopeArgs {
     uint32_t *flags;
 };
 
-// Task (token, part): part i of `parts` of the token's query heads and of its key heads.
-template <typename T, int L>
+template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
     ptx::grid_dep_wait();
     ptx::launch_dependents();
-    const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (task >= a.tasks) return;
-    const long long tok = task / a.parts;
-    const int part = (int)(task % a.parts);
-    const int b = (int)(tok / a.N), n = (int)(tok % a.N);
-    Lane ln = make_lane<L>(a.d, a.rot);
+    const unsigned per = a.cq + a.ck, tok = task / per, part = task - tok * per;
+    const int b = (int)(tok / (unsigned)a.N), n = (int)(tok - (unsigned)b * a.N);
+    const Lane ln = make_lane<L>(a.d, a.rot);
     long long pos = n;
     if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
-    if (a.rot) load_angles(ln, a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row, a.rot, a.inter);
-    else load_angles(ln, nullptr, 0, false);
-    // heads [lo, hi) of this part, q and k alike
-    const int ql = (int)((long long)a.Hq * part / a.parts), qh = (int)((long long)a.Hq * (part + 1) / a.parts);
-    const int kl = (int)((long long)a.Hk * part / a.parts), kh = (int)((long long)a.Hk * (part + 1) / a.parts);
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;
-    norm_rows<T, L, U>(static_cast<const T *>(a.q) + b * a.qs[0] + n * a.qs[1], a.qs[2],
-                       static_cast<T *>(a.qo) + b * a.qos[0] + n * a.qos[1], a.qos[2], static_cast<const T *>(a.wq), ql,
-                       qh, ln, a.inter, a.d, a.eps);
-    norm_rows<T, L, U>(static_cast<const T *>(a.k) + b * a.ks[0] + n * a.ks[1], a.ks[2],
-                       static_cast<T *>(a.ko) + b * a.kos[0] + n * a.kos[1], a.kos[2], static_cast<const T *>(a.wk), kl,
-                       kh, ln, a.inter, a.d, a.eps);
+    const float *row = a.rot ? a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row : nullptr;
+    const int lo = (int)(part < (unsigned)a.cq ? part : part - a.cq) * (32 / L) * U;
+    if (part < (unsigned)a.cq)
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + b * a.qs[0] + n * a.qs[1], a.qs[2],
+                                   static_cast<T *>(a.qo) + b * a.qos[0] + n * a.qos[1], a.qos[2],
+                                   static_cast<const T *>(a.wq), row, lo, a.Hq, ln, a.rot, a.inv_d, a.eps);
+    else
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + b * a.ks[0] + n * a.ks[1], a.ks[2],
+                                   static_cast<T *>(a.ko) + b * a.kos[0] + n * a.kos[1], a.kos[2],
+                                   static_cast<const T *>(a.wk), row, lo, a.Hk, ln, a.rot, a.inv_d, a.eps);
 }
 
 struct AppendArgs {
-    int B, T, Hq, Hk, d, rot, inter, P, parts;
+    int B, T, Hq, Hk, d, rot, P, cq, ck;
     long long tasks;
-    float eps;
+    float inv_d, eps;
     const void *q, *k, *v, *wq, *wk;
     void *qo, *kp, *vp;
     long long qs[2], ks[2], vs[2], qos[2], kps[3], vps[3];
     const float *cs;
     long long cs_row;
     const int *pos, *bt, *lens, *cu;
-    long long bt_s, pages, page_size, width;
+    long long bt_s;
+    int pages, page_size, width;
     uint32_t *flags;
 };
 
-template <typename T, int L>
+template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a) {
     ptx::grid_dep_wait();
     ptx::launch_dependents();
-    const long long task = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (task >= a.tasks) return;
-    const int t = (int)(task / a.parts), part = (int)(task % a.parts);
+    const unsigned per = a.cq + 2 * a.ck;
+    const int t = (int)(task / per), part = (int)(task - (unsigned)t * per);
     const bool report = part == 0 && (threadIdx.x & 31) == 0;
     int b, i, nq;
     if (a.cu) {
@@ -345,35 +387,35 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         b = t / nq;
         i = t - b * nq;
     }
-    const long long room = a.width * a.page_size;
-    const int raw = __ldg(a.lens + b);
-    const long long len = raw < 0 ? 0 : raw > room ? room : raw;
+    const int room = a.width * a.page_size, raw = __ldg(a.lens + b), len = min(max(raw, 0), room);
     if (report && len != raw) atomicOr(a.flags, kFlagKvLenClamped);
-    const long long at = len - nq + i;  // the token's place in its sequence; < 0: it has none
-    Lane ln = make_lane<L>(a.d, a.rot);
-    if (a.rot) {
-        const long long pos = a.pos ? (long long)__ldg(a.pos + t) : max(at, 0ll);
-        load_angles(ln, a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row, a.rot, a.inter);
-    } else {
-        load_angles(ln, nullptr, 0, false);
+    const int at = len - nq + i;  // the token's place in its sequence; < 0: it has none
+    const Lane ln = make_lane<L>(a.d, a.rot);
+    const float *row = nullptr;
+    if (a.rot && part < a.cq + a.ck)
+        row = a.cs + table_row(a.pos ? __ldg(a.pos + t) : max(at, 0), a.P, a.flags, part == 0) * a.cs_row;
+    constexpr int kHeads = (32 / L) * U;
+    if (part < a.cq) {
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0], a.qs[1],
+                                   static_cast<T *>(a.qo) + t * a.qos[0], a.qos[1], static_cast<const T *>(a.wq), row,
+                                   part * kHeads, a.Hq, ln, a.rot, a.inv_d, a.eps);
+        return;
     }
-    const int ql = (int)((long long)a.Hq * part / a.parts), qh = (int)((long long)a.Hq * (part + 1) / a.parts);
-    const int kl = (int)((long long)a.Hk * part / a.parts), kh = (int)((long long)a.Hk * (part + 1) / a.parts);
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;
-    norm_rows<T, L, U>(static_cast<const T *>(a.q) + t * a.qs[0], a.qs[1], static_cast<T *>(a.qo) + t * a.qos[0],
-                       a.qos[1], static_cast<const T *>(a.wq), ql, qh, ln, a.inter, a.d, a.eps);
     if (at < 0) return;
     const int page = __ldg(a.bt + b * a.bt_s + at / a.page_size);
     if (page < 0 || page >= a.pages) {
-        if (report) atomicOr(a.flags, kFlagBadIndex);
+        if (part == a.cq && (threadIdx.x & 31) == 0) atomicOr(a.flags, kFlagBadIndex);
         return;
     }
     const long long slot = at % a.page_size;
-    norm_rows<T, L, U>(static_cast<const T *>(a.k) + t * a.ks[0], a.ks[1],
-                       static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1], a.kps[2],
-                       static_cast<const T *>(a.wk), kl, kh, ln, a.inter, a.d, a.eps);
-    copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0], a.vs[1],
-                       static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1], a.vps[2], kl, kh, ln);
+    if (part < a.cq + a.ck)
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0], a.ks[1],
+                                   static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1], a.kps[2],
+                                   static_cast<const T *>(a.wk), row, (part - a.cq) * kHeads, a.Hk, ln, a.rot, a.inv_d, a.eps);
+    else
+        copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0], a.vs[1],
+                           static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1], a.vps[2],
+                           (part - a.cq - a.ck) * kHeads, a.Hk, ln);
 }
 
 // ------------------------------------------------------------------------------- backward
@@ -384,8 +426,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 // weight gradients are the same from run to run.
 
 struct RopeBwdArgs {
-    int B, N, d, rot, inter, P, parts, nb[2], H[2];
-    float eps;
+    int N, d, rot, P, nb[2], H[2], parts[2];
+    long long tokens;
+    float inv_d, eps;
     const void *x[2], *dy[2], *w[2];
     void *dx[2];
     long long xs[2][3], dys[2][3], dxs[2][3];
@@ -397,7 +440,7 @@ struct RopeBwdArgs {
     uint32_t *flags;
 };
 
-template <typename T, int L>
+template <typename T, int L, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBwdArgs a) {
     constexpr int GW = 32 / L, U = sizeof(T) == 2 ? 2 : 1;
     __shared__ float red[kWarps][L * 16];
@@ -407,64 +450,71 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
     const int blk = (int)blockIdx.x - (s ? a.nb[0] : 0);
     const int warp = threadIdx.x >> 5, grp = (threadIdx.x & 31) / L;
     const T *w = static_cast<const T *>(a.w[s]);
-    Lane ln = make_lane<L>(a.d, a.rot);
-    float wf[16], dw[16];
-#pragma unroll
-    for (int t = 0; t < 16; ++t) wf[t] = dw[t] = 0.f;
-    if (w && ln.on) {
+    const Lane ln = make_lane<L>(a.d, a.rot);
+    float wf[16], dw[16];  // in the half split's places
+    {
         Row2<T> r;
-        r.load(w, ln.e0, ln.e1, true);
-        r.get(wf);
+        float f[16];
+        r.load(w, ln.e0, ln.e1, w != nullptr && ln.on);
+        r.get(f);
+        apart<kInter>(f, wf);
     }
-    const long long tasks = (long long)a.B * a.N * a.parts;
+#pragma unroll
+    for (int t = 0; t < 16; ++t) dw[t] = 0.f;
+    const unsigned parts = a.parts[s];
+    const long long tasks = a.tokens * parts;
     for (long long task = (long long)blk * kWarps + warp; task < tasks; task += (long long)a.nb[s] * kWarps) {
-        const long long tok = task / a.parts;
-        const int part = (int)(task % a.parts);
-        const int b = (int)(tok / a.N), n = (int)(tok % a.N);
-        long long pos = n;
-        if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
-        if (a.rot) load_angles(ln, a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row, a.rot, a.inter);
-        else load_angles(ln, nullptr, 0, false);
-        const int lo = (int)((long long)a.H[s] * part / a.parts), hi = (int)((long long)a.H[s] * (part + 1) / a.parts);
+        const unsigned tok = (unsigned)(task / parts), part = (unsigned)(task - (long long)tok * parts);
+        const int b = (int)(tok / (unsigned)a.N), n = (int)(tok - (unsigned)b * a.N);
+        const int h0 = (int)part * GW * U + grp, hi = a.H[s];
         const T *x = static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1];
         const T *dy = static_cast<const T *>(a.dy[s]) + b * a.dys[s][0] + n * a.dys[s][1];
         T *dx = static_cast<T *>(a.dx[s]) + b * a.dxs[s][0] + n * a.dxs[s][1];
-        for (int h0 = lo; h0 < hi; h0 += GW * U) {
-            Row2<T> rx[U], rg[U];
+        Row2<T> rx[U], rg[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * GW + grp;
-                const bool in = ln.on && h < hi;
-                if (w) rx[u].load(x + h * a.xs[s][2], ln.e0, ln.e1, in);
-                rg[u].load(dy + h * a.dys[s][2], ln.e0, ln.e1, in);
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * GW;
+            const bool in = ln.on && h < hi;
+            rx[u].load(x + h * a.xs[s][2], ln.e0, ln.e1, in && w != nullptr);
+            rg[u].load(dy + h * a.dys[s][2], ln.e0, ln.e1, in);
+        }
+        long long pos = n;
+        if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
+        const Angles an =
+            load_angles(ln, a.rot ? a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row : nullptr, a.rot, kInter);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * GW;
+            float f[16], y[16], g[16], q[8];
+            rg[u].get(f);
+            apart<kInter>(f, y);
+            // g = R^T dy: g_a = dy_a cos + dy_b sin, g_b = dy_b cos - dy_a sin
+            mul8(g, y + 8, an.si);
+            fma8(g, y, an.co, g);
+            mul8(q, y, an.si);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) q[t] = -q[t];
+            fma8(g + 8, y + 8, an.co, q);
+            if (w) {
+                rx[u].get(f);
+                const float r = rsqrtf(fmaf(group_sum<L>(dot16(f, f)), a.inv_d, a.eps));
+                apart<kInter>(f, y);
+                scale8(y, y, r);  // n
+                scale8(y + 8, y + 8, r);
+                fma8(dw, g, y, dw);
+                fma8(dw + 8, g + 8, y + 8, dw + 8);
+                mul8(g, g, wf);
+                mul8(g + 8, g + 8, wf + 8);
+                const float m = -group_sum<L>(dot16(g, y)) * a.inv_d;
+#pragma unroll
+                for (int t = 0; t < 16; t += 2) ptx::fma2(g[t], g[t + 1], m, m, y[t], y[t + 1], g[t], g[t + 1]);
+                scale8(g, g, r);
+                scale8(g + 8, g + 8, r);
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * GW + grp;
-                float g[16];
-                rg[u].get(g);
-                turn(g, ln, a.inter, -1.f);
-                if (w) {
-                    float f[16], q[16];
-                    rx[u].get(f);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) q[t] = f[t] * f[t];
-                    const float r = rsqrtf(group_sum<L>(sum16(q)) / (float)a.d + a.eps);
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        f[t] *= r;                  // n
-                        dw[t] = fmaf(g[t], f[t], dw[t]);
-                        g[t] *= wf[t];
-                        q[t] = g[t] * f[t];
-                    }
-                    const float m = group_sum<L>(sum16(q)) / (float)a.d;
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) g[t] = r * fmaf(-m, f[t], g[t]);
-                }
-                if (ln.on && h < hi) {
-                    rg[u].set(g);
-                    rg[u].store(dx + h * a.dxs[s][2], ln.e0, ln.e1);
-                }
+            if (ln.on && h < hi) {
+                together<kInter>(g, f);
+                rg[u].set(f);
+                rg[u].store(dx + h * a.dxs[s][2], ln.e0, ln.e1);
             }
         }
     }
@@ -476,10 +526,12 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
         for (int o = L; o < 32; o <<= 1) dw[t] += __shfl_xor_sync(0xffffffffu, dw[t], o);
     }
     if (grp == 0 && ln.on) {
+        float f[16];
+        together<kInter>(dw, f);
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            red[warp][ln.e0 + t] = dw[t];
-            red[warp][ln.e1 + t] = dw[8 + t];
+            red[warp][ln.e0 + t] = f[t];
+            red[warp][ln.e1 + t] = f[8 + t];
         }
     }
     __syncthreads();
@@ -527,15 +579,6 @@ void copy2(long long (&d)[2], const int64_t s[2]) {
     for (int i = 0; i < 2; ++i) d[i] = s[i];
 }
 
-// How many warps share a token: enough for about four warps a scheduler on the whole GPU when
-// there are few tokens, but no more than the heads (of the tensor with most) fill a group each.
-int token_parts(int64_t tokens, int64_t heads, int L) {
-    const int64_t want = 16LL * sm_count(), most = (heads + 32 / L - 1) / (32 / L);
-    int64_t p = tokens ? (want + tokens - 1) / tokens : 1;
-    p = p < 1 ? 1 : p > most ? most : p;
-    return (int)(p < 1 ? 1 : p);
-}
-
 int lanes_of(int64_t d) { return d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
 attn_status_t launched(cudaError_t e, const char *what) {
@@ -557,35 +600,65 @@ int rope_bwd_blocks(int64_t Hq, int64_t Hkv, int64_t tokens, int nb[2]) {
     return nb[0] + nb[1];
 }
 
+namespace {
+
+// Heads a group takes at once: 4 (2 in fp32) where that still leaves 16 warps an SM, else fewer, so
+// that a decode step's few rows spread over the GPU.
+int heads_at_once(int64_t tokens, int64_t heads, int L, bool half) {
+    const int most = half ? 4 : 2;
+    for (int u = most; u > 1; u >>= 1)
+        if (tokens * ((heads + 32 / L * u - 1) / (32 / L * u)) >= 16LL * sm_count()) return u;
+    return 1;
+}
+
+template <typename T, bool kInter>
+auto rope_kernel(int L, int U) -> void (*)(const RopeArgs) {
+    if (L == 4) return U == 4 ? qk_norm_rope_kernel<T, 4, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 4, 2, kInter> : qk_norm_rope_kernel<T, 4, 1, kInter>;
+    if (L == 8) return U == 4 ? qk_norm_rope_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 8, 2, kInter> : qk_norm_rope_kernel<T, 8, 1, kInter>;
+    return U == 4 ? qk_norm_rope_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 16, 2, kInter> : qk_norm_rope_kernel<T, 16, 1, kInter>;
+}
+template <typename T, bool kInter>
+auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
+    if (L == 4) return U == 4 ? paged_append_kernel<T, 4, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 4, 2, kInter> : paged_append_kernel<T, 4, 1, kInter>;
+    if (L == 8) return U == 4 ? paged_append_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
+    return U == 4 ? paged_append_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
+}
+template <typename T, bool kInter>
+auto bwd_kernel(int L) -> void (*)(const RopeBwdArgs) {
+    return L == 4 ? qk_norm_rope_bwd_kernel<T, 4, kInter> : L == 8 ? qk_norm_rope_bwd_kernel<T, 8, kInter> : qk_norm_rope_bwd_kernel<T, 16, kInter>;
+}
+
+}  // namespace
+
 attn_status_t launch_qk_norm_rope(const attn_qk_norm_rope_params_t &p, cudaStream_t st) {
     RopeArgs a;
-    a.B = (int)p.B; a.N = (int)p.N; a.Hq = (int)p.Hq; a.Hk = (int)p.Hkv; a.d = (int)p.d;
+    a.N = (int)p.N; a.Hq = (int)p.Hq; a.Hk = (int)p.Hkv; a.d = (int)p.d;
     a.rot = p.cos_sin ? (int)p.rot : 0;
-    a.inter = p.interleaved; a.P = (int)p.cos_sin_rows; a.eps = p.eps;
+    a.P = (int)p.cos_sin_rows; a.inv_d = 1.f / (float)p.d; a.eps = p.eps;
     a.q = p.q; a.k = p.k; a.wq = p.wq; a.wk = p.wk; a.qo = p.q_out; a.ko = p.k_out;
     copy3(a.qs, p.q_stride); copy3(a.ks, p.k_stride); copy3(a.qos, p.q_out_stride); copy3(a.kos, p.k_out_stride);
     a.cs = p.cos_sin; a.cs_row = p.cos_sin_stride; a.pos = p.positions; copy2(a.pos_s, p.positions_stride);
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(p.d);
-    const int64_t tokens = p.B * p.N;
-    a.parts = token_parts(tokens, p.Hq > p.Hkv ? p.Hq : p.Hkv, L);
-    a.tasks = tokens * a.parts;
-    const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    void (*kern)(const RopeArgs) =
-        L == 4   ? (h ? qk_norm_rope_kernel<__nv_bfloat16, 4> : qk_norm_rope_kernel<float, 4>)
-        : L == 8 ? (h ? qk_norm_rope_kernel<__nv_bfloat16, 8> : qk_norm_rope_kernel<float, 8>)
-                 : (h ? qk_norm_rope_kernel<__nv_bfloat16, 16> : qk_norm_rope_kernel<float, 16>);
+    const int U = heads_at_once(p.B * p.N, p.Hq + p.Hkv, L, h), n = 32 / L * U;
+    a.cq = (int)((p.Hq + n - 1) / n);
+    a.ck = (int)((p.Hkv + n - 1) / n);
+    a.tasks = p.B * p.N * (a.cq + a.ck);
+    if (a.tasks > 0xfffffff0LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
+    const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
+    auto kern = p.interleaved ? (h ? rope_kernel<__nv_bfloat16, true>(L, U) : rope_kernel<float, true>(L, U))
+                              : (h ? rope_kernel<__nv_bfloat16, false>(L, U) : rope_kernel<float, false>(L, U));
     return launched(launch_pdl(kern, grid, dim3(kThreads), 0, st, a), "qk_norm_rope");
 }
 
 attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, float *part, cudaStream_t st) {
     const attn_qk_norm_rope_params_t &p = bp.fwd;
     RopeBwdArgs a;
-    a.B = (int)p.B; a.N = (int)p.N; a.H[0] = (int)p.Hq; a.H[1] = (int)p.Hkv; a.d = (int)p.d;
+    a.N = (int)p.N; a.H[0] = (int)p.Hq; a.H[1] = (int)p.Hkv; a.d = (int)p.d;
     a.rot = p.cos_sin ? (int)p.rot : 0;
-    a.inter = p.interleaved; a.P = (int)p.cos_sin_rows; a.eps = p.eps;
+    a.P = (int)p.cos_sin_rows; a.inv_d = 1.f / (float)p.d; a.eps = p.eps;
     a.x[0] = p.q; a.x[1] = p.k; a.w[0] = p.wq; a.w[1] = p.wk;
     a.dy[0] = bp.dq_out; a.dy[1] = bp.dk_out; a.dx[0] = bp.dq; a.dx[1] = bp.dk;
     copy3(a.xs[0], p.q_stride); copy3(a.xs[1], p.k_stride);
@@ -596,14 +669,12 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(p.d);
-    const int64_t tokens = p.B * p.N;
-    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, tokens, a.nb);
-    a.parts = token_parts(tokens, p.Hq > p.Hkv ? p.Hq : p.Hkv, L);
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    void (*kern)(const RopeBwdArgs) =
-        L == 4   ? (h ? qk_norm_rope_bwd_kernel<__nv_bfloat16, 4> : qk_norm_rope_bwd_kernel<float, 4>)
-        : L == 8 ? (h ? qk_norm_rope_bwd_kernel<__nv_bfloat16, 8> : qk_norm_rope_bwd_kernel<float, 8>)
-                 : (h ? qk_norm_rope_bwd_kernel<__nv_bfloat16, 16> : qk_norm_rope_bwd_kernel<float, 16>);
+    a.tokens = p.B * p.N;
+    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, a.tokens, a.nb), n = 32 / L * (h ? 2 : 1);
+    for (int s = 0; s < 2; ++s) a.parts[s] = (a.H[s] + n - 1) / n;
+    auto kern = p.interleaved ? (h ? bwd_kernel<__nv_bfloat16, true>(L) : bwd_kernel<float, true>(L))
+                              : (h ? bwd_kernel<__nv_bfloat16, false>(L) : bwd_kernel<float, false>(L));
     attn_status_t r = launched(launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st, a), "qk_norm_rope_bwd");
     if (r || (!bp.dwq && !bp.dwk)) return r;
     return launched(launch_pdl(bwd_weight_kernel, dim3((unsigned)((p.d + 31) / 32), 2), dim3(256), 0, st,
@@ -616,24 +687,25 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     const attn_paged_cache_t &c = p.cache;
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hk = (int)c.Hkv; a.d = (int)c.d;
     a.rot = p.cos_sin ? (int)p.rot : 0;
-    a.inter = p.interleaved; a.P = (int)p.cos_sin_rows; a.eps = p.eps;
+    a.P = (int)p.cos_sin_rows; a.inv_d = 1.f / (float)c.d; a.eps = p.eps;
     a.q = p.q; a.k = p.k; a.v = p.v; a.wq = p.wq; a.wk = p.wk; a.qo = p.q_out; a.kp = c.k_pages; a.vp = c.v_pages;
     copy2(a.qs, p.q_stride); copy2(a.ks, p.k_stride); copy2(a.vs, p.v_stride); copy2(a.qos, p.q_out_stride);
     copy3(a.kps, c.k_stride); copy3(a.vps, c.v_stride);
     a.cs = p.cos_sin; a.cs_row = p.cos_sin_stride; a.pos = p.positions;
     a.bt = c.block_table; a.bt_s = c.table_stride; a.lens = c.kv_lens; a.cu = c.cu_q;
-    a.pages = c.num_pages; a.page_size = c.page_size; a.width = c.table_width;
+    a.pages = (int)c.num_pages; a.page_size = c.page_size; a.width = (int)c.table_width;
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(c.d);
-    a.parts = token_parts(c.T, p.Hq > c.Hkv ? p.Hq : c.Hkv, L);
-    a.tasks = c.T * a.parts;
-    const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
     const bool h = c.dtype == ATTN_DTYPE_BF16;
-    void (*kern)(const AppendArgs) =
-        L == 4   ? (h ? paged_append_kernel<__nv_bfloat16, 4> : paged_append_kernel<float, 4>)
-        : L == 8 ? (h ? paged_append_kernel<__nv_bfloat16, 8> : paged_append_kernel<float, 8>)
-                 : (h ? paged_append_kernel<__nv_bfloat16, 16> : paged_append_kernel<float, 16>);
+    const int U = heads_at_once(c.T, p.Hq + 2 * c.Hkv, L, h), n = 32 / L * U;
+    a.cq = (int)((p.Hq + n - 1) / n);
+    a.ck = (int)((c.Hkv + n - 1) / n);
+    a.tasks = c.T * (a.cq + 2 * a.ck);
+    if (a.tasks > 0xfffffff0LL) return fail(ATTN_ERR_UNSUPPORTED, "T * (Hq + 2 Hkv) is too large");
+    const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
+    auto kern = p.interleaved ? (h ? append_kernel<__nv_bfloat16, true>(L, U) : append_kernel<float, true>(L, U))
+                              : (h ? append_kernel<__nv_bfloat16, false>(L, U) : append_kernel<float, false>(L, U));
     return launched(launch_pdl(kern, grid, dim3(kThreads), 0, st, a), "paged_append");
 }
 
