@@ -18,6 +18,7 @@
 #include "attn_internal.h"
 #include "qk_rope.h"
 #include "sm100_ptx.cuh"
+#include "warp_mma.cuh"
 
 namespace attn {
 namespace {
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 
 struct RopeBwdArgs {
     int N, d, rot, P, nb[2], H[2], parts[2];
-    long long tokens;
+    unsigned tasks[2];
     float inv_d, eps;
     const void *x[2], *dy[2], *w[2];
     void *dx[2];
@@ -440,98 +441,258 @@ struct RopeBwdArgs {
     uint32_t *flags;
 };
 
-template <typename T, int L, bool kInter>
+// Four elements on their way into the thread's own shared-memory slot (zeros without `in`).
+__device__ __forceinline__ void fetch4(uint2 *dst, const __nv_bfloat16 *p, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(ptx::smem_u32(dst)), "l"(p), "r"(in ? 8u : 0u) : "memory");
+}
+__device__ __forceinline__ void fetch4(uint4 *dst, const float *p, bool in) {
+    wmma16::cp_async16(ptx::smem_u32(dst), p, in ? 16u : 0u);
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, uint2 &v) { v = *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ void load4(const float *p, uint4 &v) { v = *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void get4(const uint2 &v, float *f) {
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void get4(const uint4 &v, float *f) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *f) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]));
+}
+__device__ __forceinline__ void store4(float *p, const float *f) {
+    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void fetch8(float2 *dst, const float *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(p) : "memory");
+}
+template <typename T>
+struct Raw4 {
+    using type = uint2;
+};
+template <>
+struct Raw4<float> {
+    using type = uint4;
+};
+// Of a lane's eight elements, the pairs' first members and then the second ones, and back.
+template <bool kInter>
+__device__ __forceinline__ void apart8(const float (&f)[8], float (&y)[8]) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        y[t] = f[kInter ? 2 * t : t];
+        y[4 + t] = f[kInter ? 2 * t + 1 : 4 + t];
+    }
+}
+template <bool kInter>
+__device__ __forceinline__ void together8(const float (&y)[8], float (&f)[8]) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        f[kInter ? 2 * t : t] = y[t];
+        f[kInter ? 2 * t + 1 : 4 + t] = y[4 + t];
+    }
+}
+__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+    float s[4];
+    mul2(s[0], s[1], x[0], x[1], y[0], y[1]);
+    mul2(s[2], s[3], x[2], x[3], y[2], y[3]);
+    ptx::fma2(s[0], s[1], x[4], x[5], y[4], y[5], s[0], s[1]);
+    ptx::fma2(s[2], s[3], x[6], x[7], y[6], y[7], s[2], s[3]);
+    return (s[0] + s[2]) + (s[1] + s[3]);
+}
+
+// The rows and angles of a warp's next kDepth - 1 tasks are on their way while it works on one: each
+// lane copies what it will read itself into shared memory, so nothing waits but the lane.  (Through registers,
+// four heads a group at once, the loads of a warp stood idle while it computed: 48.9 us at B4
+// N2048 H16 d128 against .)  A lane holds two chunks of four elements.  With S1 = sum x^2,
+// S2 = sum w dt x (one run of shuffles for both),
+//   dw += (r dt) x,   dx = w (r dt) - (r^3 S2 / d) x.
+constexpr int kDepth = 3;
+
+template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBwdArgs a) {
-    constexpr int GW = 32 / L, U = sizeof(T) == 2 ? 2 : 1;
-    __shared__ float red[kWarps][L * 16];
+    constexpr int GW = 32 / L;
+    using V = typename Raw4<T>::type;
+    __shared__ V rows[kDepth][U][2][2][kThreads];  // [stage][head][x, dy][chunk][thread]
+    __shared__ float4 angles[kDepth][2][kThreads];  // cos, sin
+    __shared__ float red[kWarps][L * 8];
     ptx::grid_dep_wait();
     ptx::launch_dependents();
     const int s = (int)blockIdx.x >= a.nb[0];
-    const int blk = (int)blockIdx.x - (s ? a.nb[0] : 0);
-    const int warp = threadIdx.x >> 5, grp = (threadIdx.x & 31) / L;
+    const int blk = (int)blockIdx.x - (s ? a.nb[0] : 0), tid = threadIdx.x;
+    const int warp = tid >> 5, grp = (tid & 31) / L, p = tid & (L - 1), rp = a.rot / 8;
+    const bool on = p < a.d / 8, turn = p < rp;
+    const int e0 = turn ? 4 * p : 8 * p, e1 = turn ? 4 * (p + rp) : e0 + 4;
     const T *w = static_cast<const T *>(a.w[s]);
-    const Lane ln = make_lane<L>(a.d, a.rot);
-    float wf[16], dw[16];  // in the half split's places
+    float wf[8], dw[8];  // the pairs' first members, then the second ones
     {
-        Row2<T> r;
-        float f[16];
-        r.load(w, ln.e0, ln.e1, w != nullptr && ln.on);
-        r.get(f);
-        apart<kInter>(f, wf);
-    }
+        float f[8];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) dw[t] = 0.f;
-    const unsigned parts = a.parts[s];
-    const long long tasks = a.tokens * parts;
-    for (long long task = (long long)blk * kWarps + warp; task < tasks; task += (long long)a.nb[s] * kWarps) {
-        const unsigned tok = (unsigned)(task / parts), part = (unsigned)(task - (long long)tok * parts);
-        const int b = (int)(tok / (unsigned)a.N), n = (int)(tok - (unsigned)b * a.N);
-        const int h0 = (int)part * GW * U + grp, hi = a.H[s];
-        const T *x = static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1];
-        const T *dy = static_cast<const T *>(a.dy[s]) + b * a.dys[s][0] + n * a.dys[s][1];
-        T *dx = static_cast<T *>(a.dx[s]) + b * a.dxs[s][0] + n * a.dxs[s][1];
-        Row2<T> rx[U], rg[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW;
-            const bool in = ln.on && h < hi;
-            rx[u].load(x + h * a.xs[s][2], ln.e0, ln.e1, in && w != nullptr);
-            rg[u].load(dy + h * a.dys[s][2], ln.e0, ln.e1, in);
+        for (int t = 0; t < 8; ++t) f[t] = dw[t] = 0.f;
+        if (w && on) {
+            V v0, v1;
+            load4(w + e0, v0);
+            load4(w + e1, v1);
+            get4(v0, f);
+            get4(v1, f + 4);
         }
-        long long pos = n;
-        if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
-        const Angles an =
-            load_angles(ln, a.rot ? a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row : nullptr, a.rot, kInter);
+        apart8<kInter>(f, wf);
+    }
+    // a task is a token's heads GW U part .. + GW U - 1; a step of nb kWarps tasks as so many
+    // sequences, tokens and parts, so that the walk divides nothing
+    const unsigned parts = a.parts[s], step = (unsigned)a.nb[s] * kWarps, N = a.N, tasks = a.tasks[s];
+    const unsigned task0 = blk * kWarps + warp, tok0 = task0 / parts, stok = step / parts, sb = stok / N;
+    const int spart = (int)(step - stok * parts), sn = (int)(stok - sb * N), hi = a.H[s];
+    struct At {
+        int b, n, part;
+    };
+    auto advance = [&](At &at) {
+        at.part += spart;
+        at.n += sn;
+        at.b += (int)sb;
+        if (at.part >= (int)parts) {
+            at.part -= (int)parts;
+            ++at.n;
+        }
+        if (at.n >= (int)N) {
+            at.n -= (int)N;
+            ++at.b;
+        }
+    };
+    At now{(int)(tok0 / N), 0, (int)(task0 - tok0 * parts)};
+    now.n = (int)(tok0 - (unsigned)now.b * N);
+    const T *x0 = static_cast<const T *>(w ? a.x[s] : a.dy[s]), *dy0 = static_cast<const T *>(a.dy[s]);
+    // `at` and `task` name the task to ask for; past the last one nothing is asked for
+    auto fetch = [&](const At &at, unsigned task, int st) {
+        if (task < tasks) {
+            const T *x = x0 + at.b * a.xs[s][0] + at.n * a.xs[s][1], *dy = dy0 + at.b * a.dys[s][0] + at.n * a.dys[s][1];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = at.part * GW * U + u * GW + grp;
+                const bool in = on && h < hi;
+                const T *xr = x + (in ? h * a.xs[s][2] : 0), *gr = dy + (in ? h * a.dys[s][2] : 0);
+                if (w) {
+                    fetch4(&rows[st][u][0][0][tid], xr + (on ? e0 : 0), in);
+                    fetch4(&rows[st][u][0][1][tid], xr + (on ? e1 : 0), in);
+                }
+                fetch4(&rows[st][u][1][0][tid], gr + (on ? e0 : 0), in);
+                fetch4(&rows[st][u][1][1][tid], gr + (on ? e1 : 0), in);
+            }
+            if (turn) {
+                long long pos = at.n;
+                if (a.pos) pos = __ldg(a.pos + at.b * a.pos_s[0] + at.n * a.pos_s[1]);
+                const float *row = a.cs + table_row(pos, a.P, a.flags, at.part == 0) * a.cs_row;
+                if (kInter) {
+                    float2 *c = reinterpret_cast<float2 *>(&angles[st][0][tid]), *n = reinterpret_cast<float2 *>(&angles[st][1][tid]);
+                    fetch8(c, row + e0 / 2);
+                    fetch8(c + 1, row + e1 / 2);
+                    fetch8(n, row + a.rot / 2 + e0 / 2);
+                    fetch8(n + 1, row + a.rot / 2 + e1 / 2);
+                } else {
+                    wmma16::cp_async16(ptx::smem_u32(&angles[st][0][tid]), row + e0, 16u);
+                    wmma16::cp_async16(ptx::smem_u32(&angles[st][1][tid]), row + a.rot / 2 + e0, 16u);
+                }
+            }
+        }
+        wmma16::cp_async_commit();
+    };
+    At ask = now;
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) {
+        fetch(ask, task0 + i * step, i);
+        advance(ask);
+    }
+    int st = 0;
+#pragma unroll 1
+    for (unsigned task = task0; task < tasks; task += step) {
+        wmma16::cp_async_wait<kDepth - 2>();
+        V vx[U][2], vg[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                vx[u][c] = rows[st][u][0][c][tid];
+                vg[u][c] = rows[st][u][1][c][tid];
+            }
+        float co[4], si[4];
+        {
+            const float4 c = turn ? angles[st][0][tid] : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 n = turn ? angles[st][1][tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+            co[0] = c.x; co[1] = c.y; co[2] = c.z; co[3] = c.w;
+            si[0] = n.x; si[1] = n.y; si[2] = n.z; si[3] = n.w;
+        }
+        // into the stage read before this one (by this lane alone)
+        fetch(ask, task + (kDepth - 1) * step, st == 0 ? kDepth - 1 : st - 1);
+        advance(ask);
+        if (++st == kDepth) st = 0;
+        const int h0 = now.part * GW * U + grp;
+        T *dx = static_cast<T *>(a.dx[s]) + now.b * a.dxs[s][0] + now.n * a.dxs[s][1];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int h = h0 + u * GW;
-            float f[16], y[16], g[16], q[8];
-            rg[u].get(f);
-            apart<kInter>(f, y);
+            float f[8], y[8], g[8];
+            get4(vg[u][0], f);
+            get4(vg[u][1], f + 4);
+            apart8<kInter>(f, y);
             // g = R^T dy: g_a = dy_a cos + dy_b sin, g_b = dy_b cos - dy_a sin
-            mul8(g, y + 8, an.si);
-            fma8(g, y, an.co, g);
-            mul8(q, y, an.si);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) q[t] = -q[t];
-            fma8(g + 8, y + 8, an.co, q);
-            if (w) {
-                rx[u].get(f);
-                const float r = rsqrtf(fmaf(group_sum<L>(dot16(f, f)), a.inv_d, a.eps));
-                apart<kInter>(f, y);
-                scale8(y, y, r);  // n
-                scale8(y + 8, y + 8, r);
-                fma8(dw, g, y, dw);
-                fma8(dw + 8, g + 8, y + 8, dw + 8);
-                mul8(g, g, wf);
-                mul8(g + 8, g + 8, wf + 8);
-                const float m = -group_sum<L>(dot16(g, y)) * a.inv_d;
-#pragma unroll
-                for (int t = 0; t < 16; t += 2) ptx::fma2(g[t], g[t + 1], m, m, y[t], y[t + 1], g[t], g[t + 1]);
-                scale8(g, g, r);
-                scale8(g + 8, g + 8, r);
+            for (int t = 0; t < 4; t += 2) {
+                float q0, q1;
+                mul2(g[t], g[t + 1], y[4 + t], y[5 + t], si[t], si[t + 1]);
+                ptx::fma2(g[t], g[t + 1], y[t], y[t + 1], co[t], co[t + 1], g[t], g[t + 1]);
+                mul2(q0, q1, y[t], y[t + 1], -si[t], -si[t + 1]);
+                ptx::fma2(g[4 + t], g[5 + t], y[4 + t], y[5 + t], co[t], co[t + 1], q0, q1);
             }
-            if (ln.on && h < hi) {
-                together<kInter>(g, f);
-                rg[u].set(f);
-                rg[u].store(dx + h * a.dxs[s][2], ln.e0, ln.e1);
+            if (w) {
+                get4(vx[u][0], f);
+                get4(vx[u][1], f + 4);
+                apart8<kInter>(f, y);
+                float wx[8];
+#pragma unroll
+                for (int t = 0; t < 8; t += 2) mul2(wx[t], wx[t + 1], wf[t], wf[t + 1], y[t], y[t + 1]);
+                float s1 = dot8(y, y), s2 = dot8(g, wx);
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) {
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                    s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+                }
+                const float r = rsqrtf(fmaf(s1, a.inv_d, a.eps)), c = -(r * r) * (r * s2) * a.inv_d;
+#pragma unroll
+                for (int t = 0; t < 8; t += 2) {
+                    float q0, q1;
+                    mul2(g[t], g[t + 1], g[t], g[t + 1], r, r);
+                    ptx::fma2(dw[t], dw[t + 1], g[t], g[t + 1], y[t], y[t + 1], dw[t], dw[t + 1]);
+                    mul2(q0, q1, y[t], y[t + 1], c, c);
+                    ptx::fma2(g[t], g[t + 1], g[t], g[t + 1], wf[t], wf[t + 1], q0, q1);
+                }
+            }
+            if (on && h < hi) {
+                together8<kInter>(g, f);
+                store4(dx + h * a.dxs[s][2] + e0, f);
+                store4(dx + h * a.dxs[s][2] + e1, f + 4);
             }
         }
+        advance(now);
     }
+    wmma16::cp_async_wait<0>();
     if (!w) return;
     // the groups of a warp, then the warps of the block
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
+    for (int t = 0; t < 8; ++t) {
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) dw[t] += __shfl_xor_sync(0xffffffffu, dw[t], o);
     }
-    if (grp == 0 && ln.on) {
-        float f[16];
-        together<kInter>(dw, f);
+    if (grp == 0 && on) {
+        float f[8];
+        together8<kInter>(dw, f);
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            red[warp][ln.e0 + t] = f[t];
-            red[warp][ln.e1 + t] = f[8 + t];
+        for (int t = 0; t < 4; ++t) {
+            red[warp][e0 + t] = f[t];
+            red[warp][e1 + t] = f[4 + t];
         }
     }
     __syncthreads();
@@ -623,9 +784,13 @@ auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
     if (L == 8) return U == 4 ? paged_append_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
     return U == 4 ? paged_append_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
 }
+// Heads a group of the backward takes at once.
+template <typename T>
+constexpr int kBwdHeads = sizeof(T) == 2 ? 2 : 1;
 template <typename T, bool kInter>
 auto bwd_kernel(int L) -> void (*)(const RopeBwdArgs) {
-    return L == 4 ? qk_norm_rope_bwd_kernel<T, 4, kInter> : L == 8 ? qk_norm_rope_bwd_kernel<T, 8, kInter> : qk_norm_rope_bwd_kernel<T, 16, kInter>;
+    constexpr int U = kBwdHeads<T>;
+    return L == 8 ? qk_norm_rope_bwd_kernel<T, 8, U, kInter> : L == 16 ? qk_norm_rope_bwd_kernel<T, 16, U, kInter> : qk_norm_rope_bwd_kernel<T, 32, U, kInter>;
 }
 
 }  // namespace
@@ -668,11 +833,15 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     a.part = part;
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
-    const int L = lanes_of(p.d);
+    const int L = 2 * lanes_of(p.d);
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    a.tokens = p.B * p.N;
-    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, a.tokens, a.nb), n = 32 / L * (h ? 2 : 1);
-    for (int s = 0; s < 2; ++s) a.parts[s] = (a.H[s] + n - 1) / n;
+    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, p.B * p.N, a.nb), n = 32 / L * (h ? kBwdHeads<__nv_bfloat16> : kBwdHeads<float>);
+    for (int s = 0; s < 2; ++s) {
+        a.parts[s] = (a.H[s] + n - 1) / n;
+        const long long tasks = p.B * p.N * a.parts[s];
+        if (tasks > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
+        a.tasks[s] = (unsigned)tasks;
+    }
     auto kern = p.interleaved ? (h ? bwd_kernel<__nv_bfloat16, true>(L) : bwd_kernel<float, true>(L))
                               : (h ? bwd_kernel<__nv_bfloat16, false>(L) : bwd_kernel<float, false>(L));
     attn_status_t r = launched(launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st, a), "qk_norm_rope_bwd");
