@@ -9,8 +9,10 @@
 // The bound is memory: a row is read once and written once (backward: two reads, one write), so
 // everything between happens in registers.  A row belongs to a group of L lanes, each holding two
 // 8-element chunks: chunk p and chunk p + rot/16 for p < rot/16 (the two halves of the rotated
-// part, so that both members of every pair lie in one lane in either pairing), and two
-// neighbouring chunks of the part that is not rotated otherwise.  The row's sum of squares takes
+// part, so that both members of every pair lie in one lane in either pairing), and likewise one of
+// each half of the part that is not rotated otherwise (neighbouring lanes always hold neighbouring
+// chunks: with two neighbours a lane there, each load used half of its sectors, and the backward with
+// half the head rotated took 49 us for 40).  The row's sum of squares takes
 // log2 L shuffles.  A warp stays with one token, whose angles it holds in registers while it
 // walks the heads.  Sums, norms and angles are fp32; an output is rounded once.
 #include <cuda_bf16.h>
@@ -127,8 +129,8 @@ __device__ __forceinline__ Lane make_lane(int d, int rot) {
     const int p = (threadIdx.x & (L - 1)), rp = rot / 16;
     ln.on = p < d / 16;
     ln.turn = p < rp;
-    ln.e0 = ln.turn ? 8 * p : 8 * (2 * rp + 2 * (p - rp));
-    ln.e1 = ln.turn ? 8 * (p + rp) : ln.e0 + 8;
+    ln.e0 = ln.turn ? 8 * p : 8 * (p + rp);
+    ln.e1 = ln.turn ? 8 * (p + rp) : 8 * (p + d / 16);
     return ln;
 }
 
@@ -441,107 +443,96 @@ struct RopeBwdArgs {
     uint32_t *flags;
 };
 
-// Four elements on their way into the thread's own shared-memory slot (zeros without `in`).
-__device__ __forceinline__ void fetch4(uint2 *dst, const __nv_bfloat16 *p, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(ptx::smem_u32(dst)), "l"(p), "r"(in ? 8u : 0u) : "memory");
+// The rows and angles of a warp's next kDepth - 1 tasks are on their way into shared memory while it
+// works on one: each lane copies the chunks that it will read itself, and the warp the token's row of
+// the angle table.  With S1 = sum x^2 and S2 = sum w dt x (one run of shuffles for both),
+//   dw += (r dt) x,   dx = w (r dt) - (r^3 S2 / d) x.
+// What bounds it is the issue of instructions as much as memory: with eight elements a lane, each row's
+// addresses and shuffles spread over twice the warps, it took 45.6 us at B4 N2048 H16 d128 in bf16 (30.5 M
+// warp instructions) against .
+constexpr int kDepth = 4;
+
+template <int U>
+struct BwdStage {
+    uint4 rows[U][2][2][kThreads];  // [head][x, dy][chunk][thread]: a chunk is 16 bytes
+    float angles[kWarps][256];      // the token's table row
+};
+
+__device__ __forceinline__ void unpack(const uint4 &v, float *f, __nv_bfloat16) {
+    Chunk<__nv_bfloat16> c;
+    c.v = v;
+    c.get(f);
 }
-__device__ __forceinline__ void fetch4(uint4 *dst, const float *p, bool in) {
-    wmma16::cp_async16(ptx::smem_u32(dst), p, in ? 16u : 0u);
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, uint2 &v) { v = *reinterpret_cast<const uint2 *>(p); }
-__device__ __forceinline__ void load4(const float *p, uint4 &v) { v = *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void get4(const uint2 &v, float *f) {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void get4(const uint4 &v, float *f) {
+__device__ __forceinline__ void unpack(const uint4 &v, float *f, float) {
     f[0] = __uint_as_float(v.x);
     f[1] = __uint_as_float(v.y);
     f[2] = __uint_as_float(v.z);
     f[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *f) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(ptx::pack_bf16x2(f[0], f[1]), ptx::pack_bf16x2(f[2], f[3]));
+__device__ __forceinline__ uint4 repack(const float *f, __nv_bfloat16) {
+    Chunk<__nv_bfloat16> c;
+    c.set(f);
+    return c.v;
 }
-__device__ __forceinline__ void store4(float *p, const float *f) {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ uint4 repack(const float *f, float) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
-__device__ __forceinline__ void fetch8(float2 *dst, const float *p) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(p) : "memory");
-}
-template <typename T>
-struct Raw4 {
-    using type = uint2;
-};
-template <>
-struct Raw4<float> {
-    using type = uint4;
-};
-// Of a lane's eight elements, the pairs' first members and then the second ones, and back.
-template <bool kInter>
-__device__ __forceinline__ void apart8(const float (&f)[8], float (&y)[8]) {
+// Of a lane's 2 C elements, the pairs' first members and then the second ones, and back.
+template <bool kInter, int C>
+__device__ __forceinline__ void apart_c(const float (&f)[2 * C], float (&y)[2 * C]) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < C; ++t) {
         y[t] = f[kInter ? 2 * t : t];
-        y[4 + t] = f[kInter ? 2 * t + 1 : 4 + t];
+        y[C + t] = f[kInter ? 2 * t + 1 : C + t];
     }
 }
-template <bool kInter>
-__device__ __forceinline__ void together8(const float (&y)[8], float (&f)[8]) {
+template <bool kInter, int C>
+__device__ __forceinline__ void together_c(const float (&y)[2 * C], float (&f)[2 * C]) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < C; ++t) {
         f[kInter ? 2 * t : t] = y[t];
-        f[kInter ? 2 * t + 1 : 4 + t] = y[4 + t];
+        f[kInter ? 2 * t + 1 : C + t] = y[C + t];
     }
 }
-__device__ __forceinline__ float dot8(const float (&x)[8], const float (&y)[8]) {
+template <int E>
+__device__ __forceinline__ float dot_c(const float (&x)[E], const float (&y)[E]) {
     float s[4];
     mul2(s[0], s[1], x[0], x[1], y[0], y[1]);
     mul2(s[2], s[3], x[2], x[3], y[2], y[3]);
-    ptx::fma2(s[0], s[1], x[4], x[5], y[4], y[5], s[0], s[1]);
-    ptx::fma2(s[2], s[3], x[6], x[7], y[6], y[7], s[2], s[3]);
+#pragma unroll
+    for (int t = 4; t < E; t += 4) {
+        ptx::fma2(s[0], s[1], x[t], x[t + 1], y[t], y[t + 1], s[0], s[1]);
+        ptx::fma2(s[2], s[3], x[t + 2], x[t + 3], y[t + 2], y[t + 3], s[2], s[3]);
+    }
     return (s[0] + s[2]) + (s[1] + s[3]);
 }
 
-// The rows and angles of a warp's next kDepth - 1 tasks are on their way while it works on one: each
-// lane copies what it will read itself into shared memory, so nothing waits but the lane.  (Through registers,
-// four heads a group at once, the loads of a warp stood idle while it computed: 48.9 us at B4
-// N2048 H16 d128 against .)  A lane holds two chunks of four elements.  With S1 = sum x^2,
-// S2 = sum w dt x (one run of shuffles for both),
-//   dw += (r dt) x,   dx = w (r dt) - (r^3 S2 / d) x.
-constexpr int kDepth = 3;
-
+// L lanes a row, each with two 16-byte chunks (C elements): of the rotated part chunk p and the one rot/2
+// further, of the rest one of each half.
 template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBwdArgs a) {
-    constexpr int GW = 32 / L;
-    using V = typename Raw4<T>::type;
-    __shared__ V rows[kDepth][U][2][2][kThreads];  // [stage][head][x, dy][chunk][thread]
-    __shared__ float4 angles[kDepth][2][kThreads];  // cos, sin
-    __shared__ float red[kWarps][L * 8];
+    constexpr int GW = 32 / L, C = 16 / sizeof(T), E = 2 * C;
+    extern __shared__ __align__(16) uint8_t dsm[];
+    BwdStage<U> *stage = reinterpret_cast<BwdStage<U> *>(dsm);
+    __shared__ float red[kWarps][L * E];
     ptx::grid_dep_wait();
     ptx::launch_dependents();
     const int s = (int)blockIdx.x >= a.nb[0];
-    const int blk = (int)blockIdx.x - (s ? a.nb[0] : 0), tid = threadIdx.x;
-    const int warp = tid >> 5, grp = (tid & 31) / L, p = tid & (L - 1), rp = a.rot / 8;
-    const bool on = p < a.d / 8, turn = p < rp;
-    const int e0 = turn ? 4 * p : 8 * p, e1 = turn ? 4 * (p + rp) : e0 + 4;
+    const int blk = (int)blockIdx.x - (s ? a.nb[0] : 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = lane / L;
     const T *w = static_cast<const T *>(a.w[s]);
-    float wf[8], dw[8];  // the pairs' first members, then the second ones
+    const int p = lane & (L - 1), rp = a.rot / E;
+    const bool on = p < a.d / E, turn = p < rp;
+    const int e0 = turn ? C * p : C * (p + rp), e1 = turn ? C * (p + rp) : C * (p + a.d / E);
+    float wf[E], dw[E];  // the pairs' first members, then the second ones
     {
-        float f[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) f[t] = dw[t] = 0.f;
-        if (w && on) {
-            V v0, v1;
-            load4(w + e0, v0);
-            load4(w + e1, v1);
-            get4(v0, f);
-            get4(v1, f + 4);
-        }
-        apart8<kInter>(f, wf);
+        float f[E];
+        unpack(w && on ? *reinterpret_cast<const uint4 *>(w + e0) : make_uint4(0u, 0u, 0u, 0u), f, T{});
+        unpack(w && on ? *reinterpret_cast<const uint4 *>(w + e1) : make_uint4(0u, 0u, 0u, 0u), f + C, T{});
+        apart_c<kInter, C>(f, wf);
     }
+#pragma unroll
+    for (int t = 0; t < E; ++t) dw[t] = 0.f;
     // a task is a token's heads GW U part .. + GW U - 1; a step of nb kWarps tasks as so many
     // sequences, tokens and parts, so that the walk divides nothing
     const unsigned parts = a.parts[s], step = (unsigned)a.nb[s] * kWarps, N = a.N, tasks = a.tasks[s];
@@ -566,95 +557,93 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
     At now{(int)(tok0 / N), 0, (int)(task0 - tok0 * parts)};
     now.n = (int)(tok0 - (unsigned)now.b * N);
     const T *x0 = static_cast<const T *>(w ? a.x[s] : a.dy[s]), *dy0 = static_cast<const T *>(a.dy[s]);
-    // `at` and `task` name the task to ask for; past the last one nothing is asked for
-    auto fetch = [&](const At &at, unsigned task, int st) {
+    const int c0 = on ? e0 : 0, c1 = on ? e1 : 0;
+    // asks for the task that `at` and `task` name; past the last one for nothing
+    auto fetch = [&](const At &at, unsigned task, BwdStage<U> &st) {
         if (task < tasks) {
-            const T *x = x0 + at.b * a.xs[s][0] + at.n * a.xs[s][1], *dy = dy0 + at.b * a.dys[s][0] + at.n * a.dys[s][1];
+            const int h0 = at.part * GW * U + grp;
+            const T *x = x0 + at.b * a.xs[s][0] + at.n * a.xs[s][1] + (h0 < hi ? h0 * a.xs[s][2] : 0);
+            const T *dy = dy0 + at.b * a.dys[s][0] + at.n * a.dys[s][1] + (h0 < hi ? h0 * a.dys[s][2] : 0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = at.part * GW * U + u * GW + grp;
-                const bool in = on && h < hi;
-                const T *xr = x + (in ? h * a.xs[s][2] : 0), *gr = dy + (in ? h * a.dys[s][2] : 0);
+                const bool in = on && h0 + u * GW < hi;
                 if (w) {
-                    fetch4(&rows[st][u][0][0][tid], xr + (on ? e0 : 0), in);
-                    fetch4(&rows[st][u][0][1][tid], xr + (on ? e1 : 0), in);
+                    wmma16::cp_async16(ptx::smem_u32(&st.rows[u][0][0][threadIdx.x]), x + c0, in ? 16u : 0u);
+                    wmma16::cp_async16(ptx::smem_u32(&st.rows[u][0][1][threadIdx.x]), x + c1, in ? 16u : 0u);
                 }
-                fetch4(&rows[st][u][1][0][tid], gr + (on ? e0 : 0), in);
-                fetch4(&rows[st][u][1][1][tid], gr + (on ? e1 : 0), in);
+                wmma16::cp_async16(ptx::smem_u32(&st.rows[u][1][0][threadIdx.x]), dy + c0, in ? 16u : 0u);
+                wmma16::cp_async16(ptx::smem_u32(&st.rows[u][1][1][threadIdx.x]), dy + c1, in ? 16u : 0u);
+                if (u + 1 < U && h0 + (u + 1) * GW < hi) {
+                    x += GW * a.xs[s][2];
+                    dy += GW * a.dys[s][2];
+                }
             }
-            if (turn) {
+            if (a.rot) {
                 long long pos = at.n;
                 if (a.pos) pos = __ldg(a.pos + at.b * a.pos_s[0] + at.n * a.pos_s[1]);
                 const float *row = a.cs + table_row(pos, a.P, a.flags, at.part == 0) * a.cs_row;
-                if (kInter) {
-                    float2 *c = reinterpret_cast<float2 *>(&angles[st][0][tid]), *n = reinterpret_cast<float2 *>(&angles[st][1][tid]);
-                    fetch8(c, row + e0 / 2);
-                    fetch8(c + 1, row + e1 / 2);
-                    fetch8(n, row + a.rot / 2 + e0 / 2);
-                    fetch8(n + 1, row + a.rot / 2 + e1 / 2);
-                } else {
-                    wmma16::cp_async16(ptx::smem_u32(&angles[st][0][tid]), row + e0, 16u);
-                    wmma16::cp_async16(ptx::smem_u32(&angles[st][1][tid]), row + a.rot / 2 + e0, 16u);
-                }
+                for (int i = lane; i < a.rot / 4; i += 32)
+                    wmma16::cp_async16(ptx::smem_u32(&st.angles[warp][4 * i]), row + 4 * i, 16u);
             }
         }
         wmma16::cp_async_commit();
     };
     At ask = now;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i) {
-        fetch(ask, task0 + i * step, i);
+        fetch(ask, task0 + i * step, stage[i]);
         advance(ask);
     }
-    int st = 0;
+    int cur = 0;
 #pragma unroll 1
     for (unsigned task = task0; task < tasks; task += step) {
         wmma16::cp_async_wait<kDepth - 2>();
-        V vx[U][2], vg[U][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                vx[u][c] = rows[st][u][0][c][tid];
-                vg[u][c] = rows[st][u][1][c][tid];
-            }
-        float co[4], si[4];
-        {
-            const float4 c = turn ? angles[st][0][tid] : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float4 n = turn ? angles[st][1][tid] : make_float4(0.f, 0.f, 0.f, 0.f);
-            co[0] = c.x; co[1] = c.y; co[2] = c.z; co[3] = c.w;
-            si[0] = n.x; si[1] = n.y; si[2] = n.z; si[3] = n.w;
-        }
-        // into the stage read before this one (by this lane alone)
-        fetch(ask, task + (kDepth - 1) * step, st == 0 ? kDepth - 1 : st - 1);
+        __syncwarp();  // the other lanes' parts of the angles; and every lane is done with the stage asked for next
+        fetch(ask, task + (kDepth - 1) * step, stage[cur == 0 ? kDepth - 1 : cur - 1]);
         advance(ask);
-        if (++st == kDepth) st = 0;
+        const BwdStage<U> &st = stage[cur];
+        if (++cur == kDepth) cur = 0;
+        float co[C], si[C];
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+            co[t] = 1.f;
+            si[t] = 0.f;
+        }
+        if (turn) {  // pairs C p .. C p + C - 1; adjacent ones C/2 from each chunk
+            const float *row = st.angles[warp];
+            constexpr int V = kInter ? C / 2 : C;
+            const int at[2] = {kInter ? e0 / 2 : e0, e1 / 2};
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                co[i] = row[at[i / V] + i % V];
+                si[i] = row[a.rot / 2 + at[i / V] + i % V];
+            }
+        }
         const int h0 = now.part * GW * U + grp;
-        T *dx = static_cast<T *>(a.dx[s]) + now.b * a.dxs[s][0] + now.n * a.dxs[s][1];
+        T *dx = static_cast<T *>(a.dx[s]) + now.b * a.dxs[s][0] + now.n * a.dxs[s][1] + (h0 < hi ? h0 * a.dxs[s][2] : 0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * GW;
-            float f[8], y[8], g[8];
-            get4(vg[u][0], f);
-            get4(vg[u][1], f + 4);
-            apart8<kInter>(f, y);
+            float f[E], y[E], g[E];
+            unpack(st.rows[u][1][0][threadIdx.x], f, T{});
+            unpack(st.rows[u][1][1][threadIdx.x], f + C, T{});
+            apart_c<kInter, C>(f, y);
             // g = R^T dy: g_a = dy_a cos + dy_b sin, g_b = dy_b cos - dy_a sin
 #pragma unroll
-            for (int t = 0; t < 4; t += 2) {
+            for (int t = 0; t < C; t += 2) {
                 float q0, q1;
-                mul2(g[t], g[t + 1], y[4 + t], y[5 + t], si[t], si[t + 1]);
+                mul2(g[t], g[t + 1], y[C + t], y[C + 1 + t], si[t], si[t + 1]);
                 ptx::fma2(g[t], g[t + 1], y[t], y[t + 1], co[t], co[t + 1], g[t], g[t + 1]);
                 mul2(q0, q1, y[t], y[t + 1], -si[t], -si[t + 1]);
-                ptx::fma2(g[4 + t], g[5 + t], y[4 + t], y[5 + t], co[t], co[t + 1], q0, q1);
+                ptx::fma2(g[C + t], g[C + 1 + t], y[C + t], y[C + 1 + t], co[t], co[t + 1], q0, q1);
             }
             if (w) {
-                get4(vx[u][0], f);
-                get4(vx[u][1], f + 4);
-                apart8<kInter>(f, y);
-                float wx[8];
+                unpack(st.rows[u][0][0][threadIdx.x], f, T{});
+                unpack(st.rows[u][0][1][threadIdx.x], f + C, T{});
+                apart_c<kInter, C>(f, y);
+                float wx[E];
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) mul2(wx[t], wx[t + 1], wf[t], wf[t + 1], y[t], y[t + 1]);
-                float s1 = dot8(y, y), s2 = dot8(g, wx);
+                for (int t = 0; t < E; t += 2) mul2(wx[t], wx[t + 1], wf[t], wf[t + 1], y[t], y[t + 1]);
+                float s1 = dot_c(y, y), s2 = dot_c(g, wx);
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) {
                     s1 += __shfl_xor_sync(0xffffffffu, s1, o);
@@ -662,7 +651,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
                 }
                 const float r = rsqrtf(fmaf(s1, a.inv_d, a.eps)), c = -(r * r) * (r * s2) * a.inv_d;
 #pragma unroll
-                for (int t = 0; t < 8; t += 2) {
+                for (int t = 0; t < E; t += 2) {
                     float q0, q1;
                     mul2(g[t], g[t + 1], g[t], g[t + 1], r, r);
                     ptx::fma2(dw[t], dw[t + 1], g[t], g[t + 1], y[t], y[t + 1], dw[t], dw[t + 1]);
@@ -670,11 +659,12 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
                     ptx::fma2(g[t], g[t + 1], g[t], g[t + 1], wf[t], wf[t + 1], q0, q1);
                 }
             }
-            if (on && h < hi) {
-                together8<kInter>(g, f);
-                store4(dx + h * a.dxs[s][2] + e0, f);
-                store4(dx + h * a.dxs[s][2] + e1, f + 4);
+            if (on && h0 + u * GW < hi) {
+                together_c<kInter, C>(g, f);
+                *reinterpret_cast<uint4 *>(dx + e0) = repack(f, T{});
+                *reinterpret_cast<uint4 *>(dx + e1) = repack(f + C, T{});
             }
+            if (u + 1 < U && h0 + (u + 1) * GW < hi) dx += GW * a.dxs[s][2];
         }
         advance(now);
     }
@@ -682,17 +672,17 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
     if (!w) return;
     // the groups of a warp, then the warps of the block
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
+    for (int t = 0; t < E; ++t) {
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) dw[t] += __shfl_xor_sync(0xffffffffu, dw[t], o);
     }
     if (grp == 0 && on) {
-        float f[8];
-        together8<kInter>(dw, f);
+        float f[E];
+        together_c<kInter, C>(dw, f);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < C; ++t) {
             red[warp][e0 + t] = f[t];
-            red[warp][e1 + t] = f[4 + t];
+            red[warp][e1 + t] = f[C + t];
         }
     }
     __syncthreads();
@@ -749,11 +739,11 @@ attn_status_t launched(cudaError_t e, const char *what) {
 }  // namespace
 
 int rope_bwd_blocks(int64_t Hq, int64_t Hkv, int64_t tokens, int nb[2]) {
-    // both tensors' blocks together fill the GPU several times over (2 x 152 x 4), each tensor's
-    // share by its heads; never more blocks than warps of work
-    const int64_t most = 8LL * (sm_count() ? sm_count() : 152), H[2] = {Hq, Hkv};
+    // two blocks an SM (what shared memory holds), each tensor's share by its heads; never more blocks
+    // than warps of work
+    const int64_t most = 2LL * (sm_count() ? sm_count() : 152), H[2] = {Hq, Hkv};
     for (int s = 0; s < 2; ++s) {
-        int64_t n = (most * H[s] + (Hq + Hkv) - 1) / (Hq + Hkv);
+        int64_t n = (most * H[s] + (Hq + Hkv) / 2) / (Hq + Hkv);
         const int64_t cap = (tokens * H[s] + kWarps - 1) / kWarps;
         n = n > cap ? cap : n;
         nb[s] = (int)(n < 1 ? 1 : n);
@@ -784,13 +774,18 @@ auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
     if (L == 8) return U == 4 ? paged_append_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
     return U == 4 ? paged_append_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
 }
-// Heads a group of the backward takes at once.
-template <typename T>
-constexpr int kBwdHeads = sizeof(T) == 2 ? 2 : 1;
+// The backward's kernel, the heads a warp takes at once, and its shared memory.
+struct BwdPick {
+    void (*kern)(const RopeBwdArgs);
+    int heads, smem;
+};
 template <typename T, bool kInter>
-auto bwd_kernel(int L) -> void (*)(const RopeBwdArgs) {
-    constexpr int U = kBwdHeads<T>;
-    return L == 8 ? qk_norm_rope_bwd_kernel<T, 8, U, kInter> : L == 16 ? qk_norm_rope_bwd_kernel<T, 16, U, kInter> : qk_norm_rope_bwd_kernel<T, 32, U, kInter>;
+BwdPick bwd_pick(int64_t d) {
+    constexpr int U = 2, L0 = sizeof(T) == 2 ? 4 : 8;  // lanes a row of up to 64
+    return {d <= 64    ? qk_norm_rope_bwd_kernel<T, L0, U, kInter>
+            : d <= 128 ? qk_norm_rope_bwd_kernel<T, 2 * L0, U, kInter>
+                       : qk_norm_rope_bwd_kernel<T, 4 * L0, U, kInter>,
+            32 / (d <= 64 ? L0 : d <= 128 ? 2 * L0 : 4 * L0) * U, kDepth * (int)sizeof(BwdStage<U>)};
 }
 
 }  // namespace
@@ -833,18 +828,19 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     a.part = part;
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
-    const int L = 2 * lanes_of(p.d);
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, p.B * p.N, a.nb), n = 32 / L * (h ? kBwdHeads<__nv_bfloat16> : kBwdHeads<float>);
+    const BwdPick pick = p.interleaved ? (h ? bwd_pick<__nv_bfloat16, true>(p.d) : bwd_pick<float, true>(p.d))
+                                       : (h ? bwd_pick<__nv_bfloat16, false>(p.d) : bwd_pick<float, false>(p.d));
+    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, p.B * p.N, a.nb), n = pick.heads;
     for (int s = 0; s < 2; ++s) {
         a.parts[s] = (a.H[s] + n - 1) / n;
         const long long tasks = p.B * p.N * a.parts[s];
         if (tasks > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
         a.tasks[s] = (unsigned)tasks;
     }
-    auto kern = p.interleaved ? (h ? bwd_kernel<__nv_bfloat16, true>(L) : bwd_kernel<float, true>(L))
-                              : (h ? bwd_kernel<__nv_bfloat16, false>(L) : bwd_kernel<float, false>(L));
-    attn_status_t r = launched(launch_pdl(kern, dim3(blocks), dim3(kThreads), 0, st, a), "qk_norm_rope_bwd");
+    cudaError_t e = cudaFuncSetAttribute(pick.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pick.smem);
+    if (e == cudaSuccess) e = launch_pdl(pick.kern, dim3(blocks), dim3(kThreads), pick.smem, st, a);
+    const attn_status_t r = launched(e, "qk_norm_rope_bwd");
     if (r || (!bp.dwq && !bp.dwk)) return r;
     return launched(launch_pdl(bwd_weight_kernel, dim3((unsigned)((p.d + 31) / 32), 2), dim3(256), 0, st,
                                (const float *)part, a.nb[0], a.nb[1], (int)p.d, bp.dwq, bp.dwk),
