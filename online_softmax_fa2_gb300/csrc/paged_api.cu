@@ -143,8 +143,7 @@ extern "C" attn_status_t attn_qk_norm_rope(const attn_qk_norm_rope_params_t *p, 
 
 extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t d) {
     if (B < 1 || N < 1 || Hq < 1 || Hkv < 1 || d < 1 || Hq > 65535 || Hkv > 65535 || B > INT32_MAX / N) return 0;
-    int nb[2];
-    return (size_t)rope_bwd_blocks(Hq, Hkv, B * N, nb) * (size_t)d * sizeof(float);
+    return (size_t)rope_bwd_blocks() * (size_t)d * sizeof(float);
 }
 
 extern "C" attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t *bp, void *workspace,

@@ -37,10 +37,11 @@ __device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, f
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// 16 bytes past L1 (each is read once); not .nc, since an output may be the input itself.
+// 16 bytes; not .nc, since an output may be the input itself.  (Past L1, with L1::no_allocate, a load
+// that takes half a line costs the whole line: half the head rotated took 33 us for 27.)
 __device__ __forceinline__ uint4 ld16_rw(const void *p) {
     uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
     return r;
@@ -738,41 +739,27 @@ attn_status_t launched(cudaError_t e, const char *what) {
 
 }  // namespace
 
-int rope_bwd_blocks(int64_t Hq, int64_t Hkv, int64_t tokens, int nb[2]) {
-    // two blocks an SM (what shared memory holds), each tensor's share by its heads; never more blocks
-    // than warps of work
-    const int64_t most = 2LL * (sm_count() ? sm_count() : 152), H[2] = {Hq, Hkv};
-    for (int s = 0; s < 2; ++s) {
-        int64_t n = (most * H[s] + (Hq + Hkv) / 2) / (Hq + Hkv);
-        const int64_t cap = (tokens * H[s] + kWarps - 1) / kWarps;
-        n = n > cap ? cap : n;
-        nb[s] = (int)(n < 1 ? 1 : n);
-    }
-    return nb[0] + nb[1];
-}
+int rope_bwd_blocks() { return 2 * (sm_count() ? sm_count() : 152); }
 
 namespace {
 
-// Heads a group takes at once: 4 (2 in fp32) where that still leaves 16 warps an SM, else fewer, so
-// that a decode step's few rows spread over the GPU.
-int heads_at_once(int64_t tokens, int64_t heads, int L, bool half) {
-    const int most = half ? 4 : 2;
-    for (int u = most; u > 1; u >>= 1)
-        if (tokens * ((heads + 32 / L * u - 1) / (32 / L * u)) >= 16LL * sm_count()) return u;
-    return 1;
+// Heads a group takes at once: two (four leave more lanes idle and fewer warps: 24 and 8 heads 31 us
+// for 27), or one where two would leave less than 16 warps an SM, as in a decode step.
+int heads_at_once(int64_t tokens, int64_t heads, int L) {
+    return tokens * ((heads + 64 / L - 1) / (64 / L)) >= 16LL * sm_count() ? 2 : 1;
 }
 
 template <typename T, bool kInter>
 auto rope_kernel(int L, int U) -> void (*)(const RopeArgs) {
-    if (L == 4) return U == 4 ? qk_norm_rope_kernel<T, 4, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 4, 2, kInter> : qk_norm_rope_kernel<T, 4, 1, kInter>;
-    if (L == 8) return U == 4 ? qk_norm_rope_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 8, 2, kInter> : qk_norm_rope_kernel<T, 8, 1, kInter>;
-    return U == 4 ? qk_norm_rope_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? qk_norm_rope_kernel<T, 16, 2, kInter> : qk_norm_rope_kernel<T, 16, 1, kInter>;
+    if (L == 4) return U == 2 ? qk_norm_rope_kernel<T, 4, 2, kInter> : qk_norm_rope_kernel<T, 4, 1, kInter>;
+    if (L == 8) return U == 2 ? qk_norm_rope_kernel<T, 8, 2, kInter> : qk_norm_rope_kernel<T, 8, 1, kInter>;
+    return U == 2 ? qk_norm_rope_kernel<T, 16, 2, kInter> : qk_norm_rope_kernel<T, 16, 1, kInter>;
 }
 template <typename T, bool kInter>
 auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
-    if (L == 4) return U == 4 ? paged_append_kernel<T, 4, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 4, 2, kInter> : paged_append_kernel<T, 4, 1, kInter>;
-    if (L == 8) return U == 4 ? paged_append_kernel<T, 8, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
-    return U == 4 ? paged_append_kernel<T, 16, sizeof(T) == 2 ? 4 : 2, kInter> : U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
+    if (L == 4) return U == 2 ? paged_append_kernel<T, 4, 2, kInter> : paged_append_kernel<T, 4, 1, kInter>;
+    if (L == 8) return U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
+    return U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
 }
 // The backward's kernel, the heads a warp takes at once, and its shared memory.
 struct BwdPick {
@@ -802,7 +789,7 @@ attn_status_t launch_qk_norm_rope(const attn_qk_norm_rope_params_t &p, cudaStrea
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(p.d);
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    const int U = heads_at_once(p.B * p.N, p.Hq + p.Hkv, L, h), n = 32 / L * U;
+    const int U = heads_at_once(p.B * p.N, p.Hq + p.Hkv, L), n = 32 / L * U;
     a.cq = (int)((p.Hq + n - 1) / n);
     a.ck = (int)((p.Hkv + n - 1) / n);
     a.tasks = p.B * p.N * (a.cq + a.ck);
@@ -831,13 +818,24 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     const bool h = p.dtype == ATTN_DTYPE_BF16;
     const BwdPick pick = p.interleaved ? (h ? bwd_pick<__nv_bfloat16, true>(p.d) : bwd_pick<float, true>(p.d))
                                        : (h ? bwd_pick<__nv_bfloat16, false>(p.d) : bwd_pick<float, false>(p.d));
-    const int blocks = rope_bwd_blocks(p.Hq, p.Hkv, p.B * p.N, a.nb), n = pick.heads;
+    const int n = pick.heads;
     for (int s = 0; s < 2; ++s) {
         a.parts[s] = (a.H[s] + n - 1) / n;
         const long long tasks = p.B * p.N * a.parts[s];
         if (tasks > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
         a.tasks[s] = (unsigned)tasks;
     }
+    // two blocks an SM (what shared memory holds), each tensor's share by its tasks; never more blocks
+    // than warps of work
+    const int most = rope_bwd_blocks();
+    a.nb[0] = (int)((long long)most * a.parts[0] / (a.parts[0] + a.parts[1]));
+    a.nb[0] = a.nb[0] < 1 ? 1 : a.nb[0];
+    a.nb[1] = most - a.nb[0];
+    for (int s = 0; s < 2; ++s) {
+        const int cap = (int)((a.tasks[s] + kWarps - 1) / kWarps);
+        a.nb[s] = a.nb[s] < cap ? a.nb[s] : cap;
+    }
+    const int blocks = a.nb[0] + a.nb[1];
     cudaError_t e = cudaFuncSetAttribute(pick.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, pick.smem);
     if (e == cudaSuccess) e = launch_pdl(pick.kern, dim3(blocks), dim3(kThreads), pick.smem, st, a);
     const attn_status_t r = launched(e, "qk_norm_rope_bwd");
@@ -863,7 +861,7 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(c.d);
     const bool h = c.dtype == ATTN_DTYPE_BF16;
-    const int U = heads_at_once(c.T, p.Hq + 2 * c.Hkv, L, h), n = 32 / L * U;
+    const int U = heads_at_once(c.T, p.Hq + 2 * c.Hkv, L), n = 32 / L * U;
     a.cq = (int)((p.Hq + n - 1) / n);
     a.ck = (int)((c.Hkv + n - 1) / n);
     a.tasks = c.T * (a.cq + 2 * a.ck);

@@ -6,10 +6,10 @@
 namespace attn {
 
 attn_status_t launch_qk_norm_rope(const attn_qk_norm_rope_params_t &p, cudaStream_t s);
-// part: one row of d floats for every block of rope_bwd_blocks.
+// part: one row of d floats for each of rope_bwd_blocks() blocks.
 attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &p, float *part, cudaStream_t s);
-// Blocks of the backward for the queries' and for the keys' rows; returns their sum.
-int rope_bwd_blocks(int64_t Hq, int64_t Hkv, int64_t tokens, int nb[2]);
+// Blocks of the backward, at most.
+int rope_bwd_blocks();
 attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStream_t s);
 
 }  // namespace attn
