@@ -92,6 +92,52 @@ __device__ __forceinline__ float4 *state_u(const paged::Args &a, int slot, int x
     return reinterpret_cast<float4 *>(a.u) + (slot * 2 + x) * (long long)(BQ * D / 4) + r;
 }
 
+// o = u / l and lse of this thread's row (+0.0 and -inf for a row that saw no key; nothing where orow is
+// null).  A row of 32 columns at a time is 64 bytes in one thread; stored so, each of a warp's stores
+// would touch 32 lines for 512 bytes, and the stores of a block take 2 us.  So every four lanes
+// transpose their 4 x 4 pieces of 16 bytes first (two exchanges), and each store writes 64 bytes of
+// eight rows.  Whole warp.
+template <int D>
+__device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, __nv_bfloat16 *orow, float *lse) {
+    const int lane = threadIdx.x & 31, i = lane & 3;
+    const bool empty = !(l_run > 0.f), b0 = i & 1, b1 = i & 2;
+    const float inv = empty ? 0.f : 1.f / l_run;
+    uint4 *to[4];  // the quad's rows
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        to[j] = reinterpret_cast<uint4 *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(orow), (lane & ~3) | j));
+#pragma unroll 1
+    for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t ov[32], v[4][4];
+        ptx::tmem_ld32(taddr + cc * 32, ov);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence(ov);
+#pragma unroll
+        for (int t = 0; t < 16; ++t)
+            v[t / 4][t % 4] = empty ? 0u : ptx::pack_bf16x2(__uint_as_float(ov[2 * t]) * inv, __uint_as_float(ov[2 * t + 1]) * inv);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, b0 ? v[j][e] : v[j + 1][e], 1);
+                if (b0) v[j][e] = got;
+                else v[j + 1][e] = got;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? v[j][e] : v[j + 2][e], 2);
+                if (b1) v[j][e] = got;
+                else v[j + 2][e] = got;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (to[j]) to[j][cc * 4 + i] = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+    }
+    if (lse) *lse = empty ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -149,6 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             do {
                 if (w.keys == 0) continue;
+                if (lane < 2 * (D / 64)) {  // the block's queries into L2: they are asked for some tiles later
+                    const int tok = w.seq.q0 + paged::div_g(a, w.k * a.R + (lane & 1) * (a.R >> 1));
+                    ptx::tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.hk * a.G, tok);
+                }
                 const int *row = a.bt + w.b * a.bt_s;
                 int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
                 for (int j = w.j0; j < w.j1; ++j) {
@@ -374,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             oph ^= 1;
             ptx::tc_fence_after();
             if (whole) {
-                bf16fwd::write_row<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
+                write_rows<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
                 ptx::tc_fence_before();
                 continue;
             }
