@@ -28,6 +28,9 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t most = p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;  // tokens a sequence, or their mean
     const int64_t rows = most * G;
     Plan pl;
+    // Up to 32 rows a key head the warp-level kernel, more the 128-row tiles.  64 sequences of 2048 keys,
+    // 8 heads of 128: 16 rows take 99 us in blocks of 16, 100 of 32, 122 in tiles; 24 take 181, 103, 123; 32
+    // take 184, 107, 123; 48 take 264, 186, 125.
     pl.tc = rows > 32;
     // (the 128-row tiles take whole tokens, so that TMA can bring their queries)
     pl.R = pl.tc ? (int)(2 * (128 / G) * G) : rows <= 16 ? 16 : 32;
@@ -36,7 +39,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int sms = sm_count() ? sm_count() : 152;
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
-    const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 4);
+    const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 5);
     pl.fits = tiles < 2147483648.0 - 65536.0;
     const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d, pl.R));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);

@@ -119,6 +119,7 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
     const int lane = threadIdx.x & 31;
     Share r;
     r.b = r.hk = r.k = r.j = r.cut = 0;
+    r.seq = Seq{0, 0, 0};
     Seq s, ahead{0, 0, 0};
     int w = 0, nb = 0, total = 0;
     const bool report = c == 0 && last == 0;
@@ -171,7 +172,7 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
             r.seq.nq = __shfl_sync(0xffffffffu, s.nq, src);
             r.seq.n = __shfl_sync(0xffffffffu, s.n, src);
             left -= __shfl_sync(0xffffffffu, incl, src) - ws * a.Hkv;
-            r.hk = (int)((unsigned)left / (unsigned)ws);
+            r.hk = min((int)((unsigned)left / (unsigned)ws), a.Hkv - 1);
             left -= r.hk * ws;
             break;
         }

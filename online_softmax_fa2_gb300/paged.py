@@ -12,7 +12,8 @@ block_table int32 [B, width], kv_lens int32 [B] (the new tokens included) and cu
 The names' kernels and rules are those of include/attn.h.
 
 A call runs on torch's current stream of the tensors' device, which need not be the current
-device; with ``stream`` it runs there, and what it allocates is kept for that stream.
+device; ``stream`` is as calling under ``torch.cuda.stream(stream)``: it has to be a stream of that
+device, and what the call allocates is that stream's.
 """
 from __future__ import annotations
 
@@ -147,22 +148,23 @@ def _device(q, dim):
     return dev
 
 
-def _call(dev, stream, made, fn, *args):
-    """fn(*args, stream) with device number dev current; tensors made here are kept for a stream given."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        raw = stream.cuda_stream
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _call(dev, fn, *args):
+    """fn(*args, torch's current stream of device number dev) with that device current."""
     if torch.cuda.current_device() == dev:
-        st = fn(*args, raw)
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, raw)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise _ofa.AttnError(st, _ofa.last_error())
+
+
+def _on(stream, q, fn, *args):
+    """fn(*args) with stream, of q's device, as torch's current one: what it allocates belongs to it."""
+    if stream.device != q.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {q.device}")
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def _weight(w, name, d, dtype, dev):
@@ -210,14 +212,15 @@ def attn_qk_norm_rope(q, k, wq=None, wk=None, cos_sin=None, positions=None, eps=
     at positions (int32 [B, N] or broadcast; None: 0 .. N - 1).  Pairs are (c, c + rot/2), or
     (2c, 2c + 1) when interleaved.  Returns (q_out, k_out), which may be given, q and k
     themselves included.  See include/attn.h, attn_qk_norm_rope."""
-    lib, made = _load(), (q_out, k_out)
+    if stream is not None:
+        return _on(stream, q, attn_qk_norm_rope, q, k, wq, wk, cos_sin, positions, eps, interleaved, q_out, k_out)
+    lib = _load()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     p = _pack_norm_rope(*_norm_rope_params(q, k, q_out, k_out, wq, wk, cos_sin, positions, eps, interleaved))
-    _call(q.get_device(), stream, (q_out if made[0] is None else None, k_out if made[1] is None else None),
-          lib.attn_qk_norm_rope, p)
+    _call(q.get_device(), lib.attn_qk_norm_rope, p)
     return q_out, k_out
 
 
@@ -230,34 +233,32 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, 
     """Gradients of attn_qk_norm_rope: q, k are its inputs, dq_out, dk_out the gradients of its
     outputs.  Returns (dq, dk, dwq, dwk); dq and dk may be given (dq_out and dk_out themselves
     included), dwq and dwk are float32 [d], None where the weight is."""
-    lib, made = _load(), []
+    if stream is not None:
+        return _on(stream, q, attn_qk_norm_rope_bwd, q, k, dq_out, dk_out, wq, wk, cos_sin, positions, eps, interleaved, dq,
+                   dk, workspace)
+    lib = _load()
     f = _norm_rope_params(q, k, None, None, wq, wk, cos_sin, positions, eps, interleaved)
     dev, dt, cuda = q.get_device(), q.dtype, q.device
     B, N, Hq, Hkv, d = f[2:7]
     if dq is None:
         dq = torch.empty(q.shape, dtype=dt, device=cuda)
-        made.append(dq)
     if dk is None:
         dk = torch.empty(k.shape, dtype=dt, device=cuda)
-        made.append(dk)
     dwq = dwk = None
     if wq is not None:
         dwq = torch.empty(d, dtype=torch.float32, device=cuda)
-        made.append(dwq)
     if wk is not None:
         dwk = torch.empty(d, dtype=torch.float32, device=cuda)
-        made.append(dwk)
     if workspace is None and (dwq is not None or dwk is not None):
         workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
                                 device=cuda)
-        made.append(workspace)
     sq, sk = (B, N, Hq, d), (B, N, Hkv, d)
     ptrs = (_need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev), _need(dq, "dq", sq, dt, dev),
             _need(dk, "dk", sk, dt, dev))
     p = _pack_norm_rope_bwd(*f, *ptrs, *dq_out.stride()[:3], *dk_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3],
                             0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr())
     wsp, wsn = _workspace(workspace, dev)
-    _call(dev, stream, made, lib.attn_qk_norm_rope_bwd, p, wsp, wsn)
+    _call(dev, lib.attn_qk_norm_rope_bwd, p, wsp, wsn)
     return dq, dk, dwq, dwk
 
 
@@ -293,11 +294,14 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
     slots of the paged cache, in place, and returns the normed and rotated queries.  kv_lens
     counts the new tokens; positions (int32 [T]; None: each token's place in its sequence) are
     the rotation's.  See include/attn.h, attn_paged_append."""
-    lib, made = _load(), None
+    if stream is not None:
+        return _on(stream, q, attn_paged_append, q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin,
+                   positions, eps, interleaved, q_out)
+    lib = _load()
     dev, dt = _device(q, 3), q.dtype
     T, Hq, d = shape = q.shape
     if q_out is None:
-        made = q_out = torch.empty(shape, dtype=dt, device=q.device)
+        q_out = torch.empty(shape, dtype=dt, device=q.device)
     c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
     sk = (T, c[4], d)
     cs, rows, row, rot = _angles(cos_sin, dev)
@@ -306,7 +310,7 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
                      *q_out.stride()[:2], _weight(wq, "wq", d, dt, dev), _weight(wk, "wk", d, dt, dev), cs, rows, row,
                      0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev), eps,
                      1 if interleaved else 0)
-    _call(dev, stream, (made,), lib.attn_paged_append, p)
+    _call(dev, lib.attn_paged_append, p)
     return q_out
 
 
@@ -342,20 +346,20 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
     new tokens to the end of their sequences.  max_q: the largest number of new tokens of any
     sequence, where the caller knows it (it chooses the kernel; the results hold without it).
     Returns (o [T, Hq, d], lse [T, Hq]).  See include/attn.h, attn_paged_fwd."""
-    lib, made = _load(), []
+    if stream is not None:
+        return _on(stream, q, attn_paged_fwd, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, workspace,
+                   out, lse)
+    lib = _load()
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        made.append(out)
     if lse is None:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        made.append(lse)
     p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse)
+    dev = q.get_device()
     if workspace is None:
         n = lib.attn_paged_fwd_workspace_bytes(p)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-            made.append(workspace)
-    dev = q.get_device()
     wsp, wsn = _workspace(workspace, dev)
-    _call(dev, stream, made, lib.attn_paged_fwd, p, wsp, wsn)
+    _call(dev, lib.attn_paged_fwd, p, wsp, wsn)
     return out, lse

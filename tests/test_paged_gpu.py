@@ -301,3 +301,82 @@ def test_a_workspace_of_any_contents_shared_by_calls_of_many_shapes():
             a, b = run(s, max_q=mq, workspace=ws)
             assert torch.equal(a, o) and torch.equal(b, lse)
     assert ofa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hkv,d,page,mq", [
+    ([1 + b % 3 for b in range(200)], [(37 * b) % 400 for b in range(200)], 4, 2, 64, 16, 3),     # many chunks of 32 sequences
+    ([(b * 13) % 70 for b in range(130)], [(91 * b) % 500 for b in range(130)], 2, 1, 64, 32, 69),
+    ([9, 40], [300, 41], 33, 1, 128, 16, 40),          # head groups that leave rows of a tile unused
+    ([3, 100], [700, 120], 48, 1, 64, 64, 100),
+    ([1, 70], [5000, 4100], 4, 2, 128, 4096, 70),      # pages longer than a tile
+    ([1] * 3, [5000, 4096, 1], 4, 2, 128, 4096, 1),
+])
+def test_many_sequences_odd_groups_long_pages(new, lens, Hq, Hkv, d, page, mq):
+    s = paged_inputs(new, lens, Hq, Hkv, d, page, seed=21)
+    o, lse = run(s, max_q=mq)
+    check_paged(o, lse, s, new, lens, True, 1 / math.sqrt(d))
+    assert ofa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("mq", [1, 64])
+def test_no_pages_no_keys(mq):
+    q = torch.randn(6, 4, 64, device=DEV).bfloat16()
+    kp = torch.empty(0, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
+    for bt in (torch.zeros(6, 3, dtype=torch.int32, device=DEV), torch.zeros(6, 0, dtype=torch.int32, device=DEV)):
+        o, lse = ofa.attn_paged_fwd(q, kp, kp.clone(), bt, torch.zeros(6, dtype=torch.int32, device=DEV), max_q=mq)
+        assert bool((o.view(torch.int16) == 0).all()) and bool((lse == -math.inf).all())
+        assert ofa.device_error_flags() == 0
+
+
+def test_captured_chunk_and_training_gradients_replay_beside_another_graph():
+    """Two graphs over one workspace, replayed in turn with other lengths, and the gradients of the
+    head norms in a graph while the eager call's tensors live."""
+    s = paged_inputs([200, 40], [1500, 900], 8, 2, 128, 16, seed=2, poison=False)
+    one = paged_inputs([1] * 3, [4000, 100, 900], 8, 2, 128, 16, seed=3, poison=False)
+    n = max(ofa.paged_fwd_workspace_bytes(x["q"], x["kp"], x["vp"], x["bt"], x["lens"], x["cu"], max_q=m)
+            for x, m in ((s, 200), (one, 1)))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    q, k = torch.randn(2, 33, 4, 128, device=DEV).bfloat16(), torch.randn(2, 33, 2, 128, device=DEV).bfloat16()
+    w, cs = torch.rand(128, device=DEV).bfloat16(), angles(33, 128).to(DEV)
+    eager = ofa.attn_qk_norm_rope_bwd(q, k, q * 2, k * 3, w, w, cs)
+    calls = [lambda: run(s, max_q=200, workspace=ws), lambda: run(one, max_q=1, workspace=ws),
+             lambda: ofa.attn_qk_norm_rope_bwd(q, k, q * 2, k * 3, w, w, cs)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in calls:
+            c()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    for lens in ([1500, 900], [200, 41], [777, 900]):
+        s["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        one["lens"].copy_(torch.tensor([lens[0], 1, lens[1]], dtype=torch.int32))
+        for _ in range(2):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in o] for o in outs]
+        for c, o in zip(calls, got):
+            for a, b in zip(c(), o):
+                assert torch.equal(a, b)
+    for a, b in zip(eager, outs[2]):
+        assert torch.equal(a, b)
+    assert ofa.device_error_flags() == 0
+
+
+def test_a_stream_given_owns_what_the_call_allocates():
+    s = paged_inputs([1] * 4, [900, 30, 2000, 1], 8, 2, 64, 16, seed=2)
+    want = run(s)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    got = run(s, stream=st)
+    k = torch.randn(4, 2, 64, device=DEV).bfloat16()
+    st.wait_stream(torch.cuda.current_stream())
+    q2 = ofa.attn_paged_append(s["q"], k, k, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], stream=st)
+    st.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(q2, s["q"])
