@@ -52,7 +52,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
         return pl;
     }
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.off_ml = up((pl.tc ? 0 : slots) * sizeof(unsigned long long));
+    pl.off_ml = up(pl.tc ? pl.grid * kCutBytes : slots * sizeof(unsigned long long));
     const size_t srows = pl.tc ? 256 : pl.R;  // rows a slot
     pl.off_u = pl.off_ml + up(slots * srows * 2 * sizeof(float));
     pl.bytes = pl.off_u + slots * srows * (size_t)c.d * sizeof(float);
@@ -136,7 +136,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     a.qs0 = p.q_stride[0]; a.qs1 = p.q_stride[1]; a.os0 = p.o_stride[0]; a.os1 = p.o_stride[1];
     a.bt = c.block_table; a.bt_s = c.table_stride; a.lens = c.kv_lens; a.cu = c.cu_q;
     char *ws = static_cast<char *>(workspace);
-    a.marks = reinterpret_cast<unsigned long long *>(ws);
+    a.marks = pl.cuts ? reinterpret_cast<unsigned long long *>(ws) : nullptr;
     a.ml = reinterpret_cast<float *>(ws + pl.off_ml);
     a.u = reinterpret_cast<float *>(ws + pl.off_u);
     a.tag = next_call_tag();

@@ -25,6 +25,7 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr size_t kCutBytes = 32;  // a share's record of the item that it cuts (paged_tc_sm103.cu)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
 struct Args {
@@ -38,7 +39,7 @@ struct Args {
     const int *bt, *lens, *cu;
     uint32_t g_m, r_m;  // division by G and by R as a multiply-high and shifts (bf16fwd::fast_div_params)
     int g_s, r_s;
-    unsigned long long *marks;  // what is written, see paged_merge.cuh
+    unsigned long long *marks;  // what is written (paged_merge.cuh), or the cuts (paged_tc_sm103.cu)
     unsigned long long tag;
     float *ml, *u;  // states: (m, l) [slot][R][2], u [slot][R][D]
     uint32_t *flags;
@@ -108,21 +109,19 @@ __device__ __forceinline__ int seq_len_of(const Args &a, const Seq &s, int nb) {
 struct Share {
     int per, t0, t1;  // the line between two boundaries, and this CTA's [t0, t1); the line is shorter than 2^31
     int b, hk, k, j;  // where t0 lies (j = the item's tiles: at its end)
-    int cut;          // the boundary looked for last lies inside an item
     Seq seq;
 };
 
-// The share of CTA c of C; with last = 1, where its end lies (in b, hk, k, j and cut) and no t0.  One
-// warp; every lane gets the result.  It runs once, cold, before anything else can: short code
-// counts for more than fast code.
-__device__ __forceinline__ Share find_share(const Args &a, int c, int C, int last = 0) {
+// The share of CTA c of C.  One warp; every lane gets the result.  It runs once, cold, before
+// anything else can: short code counts for more than fast code.
+__device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
     const int lane = threadIdx.x & 31;
     Share r;
-    r.b = r.hk = r.k = r.j = r.cut = 0;
+    r.b = r.hk = r.k = r.j = 0;
     r.seq = Seq{0, 0, 0};
     Seq s, ahead{0, 0, 0};
     int w = 0, nb = 0, total = 0;
-    const bool report = c == 0 && last == 0;
+    const bool report = c == 0;
     if (lane < a.B) ahead = seq_info(a, lane, report);
 #pragma unroll 1
     for (int b = lane; b < a.B + lane; b += 32) {
@@ -138,9 +137,8 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
     r.t0 = r.t1 = 0;
     // the boundaries c + 1, then c: the item that each falls into, and which side of it it goes to
 #pragma unroll 1
-    for (int e = 1; e >= last; --e) {
+    for (int e = 1; e >= 0; --e) {
         const int at = (int)min((long long)r.per * (c + e), (long long)total);
-        r.cut = 0;
         if (at >= total) {
             if (e == 0) r.t0 = total;
             else r.t1 = total;
@@ -198,7 +196,6 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C, int las
         }
         const int tiles = block_tiles(a, r.seq, r.k), j = left - a.cost;
         r.j = j < a.min_cut ? 0 : tiles - j < a.min_cut ? tiles : j;
-        r.cut = r.j == j && j > 0 && j < tiles;
         // to the item's start, to its end, or between two tiles
         const int to = at - left + (r.j == 0 ? 0 : a.cost + r.j);
         if (e == 0) r.t0 = to;
@@ -220,25 +217,15 @@ struct Walk {
         j0 = j;
         j1 = min(tiles, t1 - t - a.cost);
     }
-    __device__ __forceinline__ void place(const Args &a, const Share &sh) {
+    // false when the share is empty
+    __device__ __forceinline__ bool begin(const Args &a, const Share &sh) {
+        if (sh.t0 >= sh.t1) return false;
         per = sh.per;
         b = sh.b;
         hk = sh.hk;
         k = sh.k;
         seq = sh.seq;
         nb = num_blocks(a, seq);
-    }
-    // the item that the end of a share cuts, as one piece of all its tiles
-    __device__ __forceinline__ void at(const Args &a, const Share &sh) {
-        place(a, sh);
-        t = sh.t1 - sh.j - a.cost;
-        t1 = 0x7fffffff;
-        piece(a, 0);
-    }
-    // false when the share is empty
-    __device__ __forceinline__ bool begin(const Args &a, const Share &sh) {
-        if (sh.t0 >= sh.t1) return false;
-        place(a, sh);
         t = sh.t0 - (sh.j == 0 ? 0 : a.cost + sh.j);
         t1 = sh.t1;
         piece(a, sh.j);

@@ -16,6 +16,7 @@
 //                One thread of each also asks for its tile's Q by TMA, for the next block
 //                right after the last P of this one, so that its first S runs under this one's
 //                epilogue.
+//   warp 2       finds the share; warp 3 writes down what the merge has to know.
 // A row's state over its part of an item goes to the workspace when the item is cut, and
 // paged_tc_merge_kernel merges the parts.
 #include <cudaTypedefs.h>
@@ -87,6 +88,14 @@ __device__ __forceinline__ Tiles tiles_of(const paged::Args &a, const Walk &w) {
 __device__ __forceinline__ float2 *state_ml(const paged::Args &a, int slot, int x, int r) {
     return reinterpret_cast<float2 *>(a.ml) + (slot * 2 + x) * (long long)BQ + r;
 }
+// The item whose first part is the end of a share, for the merge: parts of each tile (0: no such item),
+// its block's first row and the sequence's rows, its first token, its key head.
+struct Cut {
+    int n[2], row0, end;
+    int q0, hk, pad[2];
+};
+static_assert(sizeof(Cut) == 32 && sizeof(Cut) == paged::kCutBytes, "two 16-byte loads");
+
 template <int D>
 __device__ __forceinline__ float4 *state_u(const paged::Args &a, int slot, int x, int r) {
     return reinterpret_cast<float4 *>(a.u) + (slot * 2 + x) * (long long)(BQ * D / 4) + r;
@@ -248,6 +257,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::mbar_wait_quiet(&ctrl->v_full[vs], vp, kWaitLimitNs);
                 }
             }
+        } else if (warp == 3 && lane == 0 && a.marks) {
+            // -------------------------------------------------------- what the merge has to know
+            Cut cut{};
+            bool more = any;
+            while (more) {
+                cut = Cut{};
+                if (w.j0 == 0 && w.j1 < w.tiles) {
+                    const Tiles tl = tiles_of(a, w);
+                    for (int x = 0; x < 2; ++x) cut.n[x] = w.parts(a, blockIdx.x, tl.t[x]);
+                    cut.row0 = w.k * a.R;
+                    cut.end = w.seq.nq * a.G;
+                    cut.q0 = w.seq.q0;
+                    cut.hk = w.hk;
+                }
+                more = w.next(a);
+            }
+            reinterpret_cast<Cut *>(a.marks)[blockIdx.x] = cut;
         } else if (warp == 1 && lane == 0 && any) {
             // -------------------------------------------------------- tensor-core issuer
             constexpr uint32_t kIdS = ptx::idesc_bf16_f32(BQ, BK, false);
@@ -458,33 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merges the states of cut items ("How Does FlashAttention Preserve Global Softmax Across Tiles?",
-// section 3), in share order.  CTA (c, tile, columns / 32) takes the item that goes past the end of
-// share c, if one does; a thread takes a row.  A kernel of its own: the merge's registers in the
+// section 3), in share order.  CTA (c, tile, columns / 32) takes the item whose first part is the end of
+// share c, if there is one; a thread takes a row.  A kernel of its own: the merge's registers in the
 // attention kernel's made its softmax spill (a 2048-token chunk 420 -> 800 us), and at its end one
-// warpgroup merging 128 rows took 8 to 11 us where the whole GPU takes 3.  It finds its item
-// before the attention kernel is done: every CTA of that one has passed its own wait when this
-// one starts, so the lengths are there.
+// warpgroup merging 128 rows took 8 to 11 us.  No CTA of it finds room on an SM before the attention
+// kernel's are done, so what it has to know is written down for it (Cut) instead of searched for.
 constexpr int kMergeCols = 32;
 template <int D>
-__global__ void __launch_bounds__(BQ) paged_tc_merge_kernel(const paged::Args a) {
-    __shared__ Share share;
+__global__ void __launch_bounds__(BQ, 8) paged_tc_merge_kernel(const paged::Args a) {
     const int c = blockIdx.x, X = blockIdx.y, col = blockIdx.z * kMergeCols, r = threadIdx.x;
-    if (threadIdx.x < 32) {
-        const Share s = paged::find_share(a, c, gridDim.x, 1);
-        if (threadIdx.x == 0) share = s;
-    }
-    __syncthreads();
     ptx::grid_dep_wait();
     ptx::launch_dependents();
-    Walk w;
-    // the boundary behind share c: where it cuts an item, and that item's first part is in c
-    if (share.cut == 0) return;
-    w.at(a, share);
-    if (w.first_share(a) != c) return;
-    const int half = a.R >> 1, row = w.k * a.R + X * half + r;
-    const Tiles tl = tiles_of(a, w);
-    const int n = w.parts(a, c, tl.t[X]);
-    if (n < 2 || r >= half || row >= w.seq.nq * a.G) return;
+    const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + c);
+    const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // n[2], row0, end | q0, hk
+    const int n = X ? c0.y : c0.x, half = a.R >> 1, row = c0.z + X * half + r;
+    if (n < 2 || r >= half || row >= c0.w) return;
     auto slot = [&](int p) { return paged::state_slot(c + p, c); };
     float M = -INFINITY, sum = 0.f, v[kMergeCols];
 #pragma unroll 4
@@ -492,7 +506,7 @@ __global__ void __launch_bounds__(BQ) paged_tc_merge_kernel(const paged::Args a)
     const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int t = 0; t < kMergeCols; ++t) v[t] = 0.f;
-#pragma unroll 2
+#pragma unroll 1
     for (int p = 0; p < n; ++p) {
         const float2 ml = __ldcg(state_ml(a, slot(p), X, r));
         const float4 *src = state_u<D>(a, slot(p), X, r) + (col / 4) * BQ;
@@ -508,8 +522,8 @@ __global__ void __launch_bounds__(BQ) paged_tc_merge_kernel(const paged::Args a)
         }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int tok = paged::div_g(a, row), h = w.hk * a.G + row - tok * a.G;
-    const long long t0 = w.seq.q0 + tok;
+    const int tok = paged::div_g(a, row), h = c1.y * a.G + row - tok * a.G;
+    const long long t0 = c1.x + tok;
     uint4 *o4 = reinterpret_cast<uint4 *>(a.o + t0 * a.os0 + h * a.os1 + col);
 #pragma unroll
     for (int t = 0; t < kMergeCols / 8; ++t) {
