@@ -13,11 +13,11 @@
 // each half of the part that is not rotated otherwise (neighbouring lanes always hold neighbouring
 // chunks: with two neighbours a lane there, each load used half of its sectors, and the backward with
 // half the head rotated took 49 us for 40).  The row's sum of squares takes
-// log2 L shuffles.  A warp stays with one token, whose angles it holds in registers while it
-// walks the heads.  Sums, norms and angles are fp32; an output is rounded once.
+// log2 L shuffles.  Sums, norms and angles are fp32; an output is rounded once.
 #include <cuda_bf16.h>
 
 #include "attn_internal.h"
+#include "fwd_bf16_common.cuh"
 #include "qk_rope.h"
 #include "sm100_ptx.cuh"
 #include "warp_mma.cuh"
@@ -215,19 +215,17 @@ __device__ __forceinline__ void scale8(float *d, const float *x, float c) {
     for (int t = 0; t < 8; t += 2) mul2(d[t], d[t + 1], x[t], x[t + 1], c, c);
 }
 
-// Heads [lo, lo + 32 / L * U) below hi of one tensor at one token, U a group and all in flight.  The
-// norm's weight goes into the angles once for all of them: with (a, b) = r (x_a w_a, x_b w_b),
+// `count` (0 to U) consecutive heads of one tensor at one token, the group's own.  The norm's weight
+// goes into the angles once for all of them: with (a, b) = r (x_a w_a, x_b w_b),
 //   y_a = r (x_a (w_a cos) - x_b (w_b sin)),  y_b = r (x_a (w_a sin) + x_b (w_b cos)).
-// (The shuffles need the whole warp: rows past hi are zeros.)
+// (The shuffles need the whole warp: rows past count are zeros.)
 template <typename T, int L, int U, bool kInter>
 __device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, long long out_h, const T *w,
-                                          const float *angle_row, int lo, int hi, const Lane &ln, int rot, float inv_d,
+                                          const float *angle_row, int count, const Lane &ln, int rot, float inv_d,
                                           float eps) {
-    constexpr int GW = 32 / L;
-    const int h0 = lo + (threadIdx.x & 31) / L;
     Row2<T> x[U], wr;
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(in + (h0 + u * GW) * in_h, ln.e0, ln.e1, ln.on && h0 + u * GW < hi);
+    for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
     wr.load(w, ln.e0, ln.e1, w != nullptr && ln.on);
     const Angles an = load_angles(ln, angle_row, rot, kInter);
     float ac[8], as[8], bc[8], bs[8];  // w_a cos, w_a sin, w_b cos, -w_b sin
@@ -265,30 +263,39 @@ __device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, l
         mul8(z + 8, y + 8, bc);
         fma8(z + 8, y, as, z + 8);
         together<kInter>(z, f);
-        if (ln.on && h0 + u * GW < hi) {
+        if (ln.on && u < count) {
             x[u].set(f);
-            x[u].store(out + (h0 + u * GW) * out_h, ln.e0, ln.e1);
+            x[u].store(out + u * out_h, ln.e0, ln.e1);
         }
     }
 }
 
 template <typename T, int L, int U>
-__device__ __forceinline__ void copy_rows(const T *in, long long in_h, T *out, long long out_h, int lo, int hi,
-                                          const Lane &ln) {
-    constexpr int GW = 32 / L;
-    const int h0 = lo + (threadIdx.x & 31) / L;
+__device__ __forceinline__ void copy_rows(const T *in, long long in_h, T *out, long long out_h, int count, const Lane &ln) {
     Row2<T> x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(in + (h0 + u * GW) * in_h, ln.e0, ln.e1, ln.on && h0 + u * GW < hi);
+    for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (ln.on && h0 + u * GW < hi) x[u].store(out + (h0 + u * GW) * out_h, ln.e0, ln.e1);
+        if (ln.on && u < count) x[u].store(out + u * out_h, ln.e0, ln.e1);
+}
+
+// Division by a number that the host knows (fast_div_params of fwd_bf16_common.cuh).
+struct Div {
+    uint32_t m;
+    int s;
+    __device__ __forceinline__ unsigned operator()(unsigned x) const { return bf16fwd::div_fast(x, m, s); }
+};
+Div div_by(uint32_t d) {
+    Div r;
+    bf16fwd::fast_div_params(d, r.m, r.s);
+    return r;
 }
 
 // A position clamped into the angle table; one outside is reported.
 __device__ __forceinline__ int table_row(long long pos, int P, uint32_t *flags, bool report) {
     if (pos >= 0 && pos < P) return (int)pos;
-    if (report && (threadIdx.x & 31) == 0) atomicOr(flags, kFlagBadIndex);
+    if (report) atomicOr(flags, kFlagBadIndex);
     return pos < 0 ? 0 : P - 1;
 }
 
@@ -311,15 +318,18 @@ __device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
     return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
-// A warp takes one task: a token, a tensor (q, k, v) and the part of its heads that its groups
-// hold at once, U heads each.  Tasks of a token: cq parts of q, then ck of k (and of v).
+// A group takes a unit: U consecutive heads of one tensor at one token.  The units of all tokens form
+// one row, the groups of a warp neighbours in it (a warp that kept to one token left most of its
+// lanes idle when there are few heads: one query and one key head took 37 us for 6); first the
+// warps of q, then those of k.
 struct RopeArgs {
-    int N, Hq, Hk, d, rot, P, cq, ck;
-    long long tasks;
+    unsigned tokens, warps_q;
+    int N, H[2], d, rot, P, per[2];  // units a token
+    Div by_n, by_per[2];
     float inv_d, eps;
-    const void *q, *k, *wq, *wk;
-    void *qo, *ko;
-    long long qs[3], ks[3], qos[3], kos[3];
+    const void *x[2], *w[2];
+    void *o[2];
+    long long xs[2][3], os[2][3];
     const float *cs;
     long long cs_row;
     const int *pos;
@@ -329,27 +339,34 @@ struct RopeArgs {
 
 template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
+    constexpr int GW = 32 / L;
     ptx::grid_dep_wait();
     ptx::launch_dependents();
-    const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (task >= a.tasks) return;
-    const unsigned per = a.cq + a.ck, tok = task / per, part = task - tok * per;
-    const int b = (int)(tok / (unsigned)a.N), n = (int)(tok - (unsigned)b * a.N);
+    unsigned warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int s = warp >= a.warps_q;
+    if (s) warp -= a.warps_q;
+    const unsigned unit = warp * GW + (threadIdx.x & 31) / L;
+    unsigned tok = a.by_per[s](unit);
+    const int h0 = (int)(unit - tok * a.per[s]) * U;
+    const int count = tok < a.tokens ? min(U, a.H[s] - h0) : 0;
+    if (count == 0) tok = 0;  // the last warps' spare groups
+    const int b = (int)a.by_n(tok), n = (int)(tok - (unsigned)b * a.N);
     const Lane ln = make_lane<L>(a.d, a.rot);
-    long long pos = n;
-    if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
-    const float *row = a.rot ? a.cs + table_row(pos, a.P, a.flags, part == 0) * a.cs_row : nullptr;
-    const int lo = (int)(part < (unsigned)a.cq ? part : part - a.cq) * (32 / L) * U;
-    if (part < (unsigned)a.cq)
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + b * a.qs[0] + n * a.qs[1], a.qs[2],
-                                   static_cast<T *>(a.qo) + b * a.qos[0] + n * a.qos[1], a.qos[2],
-                                   static_cast<const T *>(a.wq), row, lo, a.Hq, ln, a.rot, a.inv_d, a.eps);
-    else
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + b * a.ks[0] + n * a.ks[1], a.ks[2],
-                                   static_cast<T *>(a.ko) + b * a.kos[0] + n * a.kos[1], a.kos[2],
-                                   static_cast<const T *>(a.wk), row, lo, a.Hk, ln, a.rot, a.inv_d, a.eps);
+    const float *row = nullptr;
+    if (a.rot) {
+        long long pos = n;
+        if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
+        row = a.cs + table_row(pos, a.P, a.flags, count > 0 && h0 == 0 && (threadIdx.x & (L - 1)) == 0) * a.cs_row;
+    }
+    norm_rows<T, L, U, kInter>(static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1] + h0 * a.xs[s][2],
+                               a.xs[s][2],
+                               static_cast<T *>(a.o[s]) + b * a.os[s][0] + n * a.os[s][1] + h0 * a.os[s][2], a.os[s][2],
+                               static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
 }
 
+// A warp takes one token, a tensor (q, k, v) and the part of its heads that its groups hold at once
+// (the token's sequence is looked up by the whole warp).  Tasks of a token: cq parts of q, then ck of k,
+// then ck of v.
 struct AppendArgs {
     int B, T, Hq, Hk, d, rot, P, cq, ck;
     long long tasks;
@@ -397,12 +414,15 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const Lane ln = make_lane<L>(a.d, a.rot);
     const float *row = nullptr;
     if (a.rot && part < a.cq + a.ck)
-        row = a.cs + table_row(a.pos ? __ldg(a.pos + t) : max(at, 0), a.P, a.flags, part == 0) * a.cs_row;
-    constexpr int kHeads = (32 / L) * U;
-    if (part < a.cq) {
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0], a.qs[1],
-                                   static_cast<T *>(a.qo) + t * a.qos[0], a.qos[1], static_cast<const T *>(a.wq), row,
-                                   part * kHeads, a.Hq, ln, a.rot, a.inv_d, a.eps);
+        row = a.cs + table_row(a.pos ? __ldg(a.pos + t) : max(at, 0), a.P, a.flags, report) * a.cs_row;
+    // the group's heads of the part's tensor
+    const int s = part < a.cq ? 0 : part < a.cq + a.ck ? 1 : 2, H = s == 0 ? a.Hq : a.Hk;
+    const int h0 = ((part - (s == 0 ? 0 : s == 1 ? a.cq : a.cq + a.ck)) * (32 / L) + (threadIdx.x & 31) / L) * U;
+    const int count = min(max(H - h0, 0), U), h = count > 0 ? h0 : 0;
+    if (s == 0) {
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0] + h * a.qs[1], a.qs[1],
+                                   static_cast<T *>(a.qo) + t * a.qos[0] + h * a.qos[1], a.qos[1],
+                                   static_cast<const T *>(a.wq), row, count, ln, a.rot, a.inv_d, a.eps);
         return;
     }
     if (at < 0) return;
@@ -412,14 +432,13 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         return;
     }
     const long long slot = at % a.page_size;
-    if (part < a.cq + a.ck)
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0], a.ks[1],
-                                   static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1], a.kps[2],
-                                   static_cast<const T *>(a.wk), row, (part - a.cq) * kHeads, a.Hk, ln, a.rot, a.inv_d, a.eps);
+    if (s == 1)
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1],
+                                   static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1] + h * a.kps[2], a.kps[2],
+                                   static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
     else
-        copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0], a.vs[1],
-                           static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1], a.vps[2],
-                           (part - a.cq - a.ck) * kHeads, a.Hk, ln);
+        copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0] + h * a.vs[1], a.vs[1],
+                           static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1] + h * a.vps[2], a.vps[2], count, ln);
 }
 
 // ------------------------------------------------------------------------------- backward
@@ -430,8 +449,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 // weight gradients are the same from run to run.
 
 struct RopeBwdArgs {
-    int N, d, rot, P, nb[2], H[2], parts[2];
-    unsigned tasks[2];
+    unsigned tokens, units[2];  // U heads of a token each, as in the forward
+    int N, d, rot, P, nb[2], H[2], per[2];
+    Div by_n, by_per[2];
     float inv_d, eps;
     const void *x[2], *dy[2], *w[2];
     void *dx[2];
@@ -444,19 +464,19 @@ struct RopeBwdArgs {
     uint32_t *flags;
 };
 
-// The rows and angles of a warp's next kDepth - 1 tasks are on their way into shared memory while it
-// works on one: each lane copies the chunks that it will read itself, and the warp the token's row of
-// the angle table.  With S1 = sum x^2 and S2 = sum w dt x (one run of shuffles for both),
+// The rows and angles of a group's next kDepth - 1 units are on their way into shared memory while it
+// works on one: each lane copies the chunks that it will read itself, and waits for nothing but them.
+// With S1 = sum x^2 and S2 = sum w dt x (one run of shuffles for both),
 //   dw += (r dt) x,   dx = w (r dt) - (r^3 S2 / d) x.
-// What bounds it is the issue of instructions as much as memory: with eight elements a lane, each row's
-// addresses and shuffles spread over twice the warps, it took 45.6 us at B4 N2048 H16 d128 in bf16 (30.5 M
-// warp instructions) against .
+// What bounds it is the issue of instructions as much as memory: with loads into registers it took
+// 49 us at B4 N2048 H16 d128 in bf16, with eight elements a lane (each row's addresses and shuffles
+// spread over twice the warps) 46, so 36, 5.7 TB/s.
 constexpr int kDepth = 4;
 
-template <int U>
+template <int U, int C>
 struct BwdStage {
-    uint4 rows[U][2][2][kThreads];  // [head][x, dy][chunk][thread]: a chunk is 16 bytes
-    float angles[kWarps][256];      // the token's table row
+    uint4 rows[U][2][2][kThreads];       // [head][x, dy][chunk][thread]: a chunk is 16 bytes, C elements
+    float4 angles[2][C / 4][kThreads];   // cos, sin of the lane's C pairs
 };
 
 __device__ __forceinline__ void unpack(const uint4 &v, float *f, __nv_bfloat16) {
@@ -477,6 +497,13 @@ __device__ __forceinline__ uint4 repack(const float *f, __nv_bfloat16) {
 }
 __device__ __forceinline__ uint4 repack(const float *f, float) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+// Angles on their way, through L1 (the groups of a token want the same ones).
+__device__ __forceinline__ void fetch_16(void *dst, const float *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(p) : "memory");
+}
+__device__ __forceinline__ void fetch_8(void *dst, const float *p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(p) : "memory");
 }
 // Of a lane's 2 C elements, the pairs' first members and then the second ones, and back.
 template <bool kInter, int C>
@@ -514,7 +541,7 @@ template <typename T, int L, int U, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBwdArgs a) {
     constexpr int GW = 32 / L, C = 16 / sizeof(T), E = 2 * C;
     extern __shared__ __align__(16) uint8_t dsm[];
-    BwdStage<U> *stage = reinterpret_cast<BwdStage<U> *>(dsm);
+    BwdStage<U, C> *stage = reinterpret_cast<BwdStage<U, C> *>(dsm);
     __shared__ float red[kWarps][L * E];
     ptx::grid_dep_wait();
     ptx::launch_dependents();
@@ -534,94 +561,87 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
     }
 #pragma unroll
     for (int t = 0; t < E; ++t) dw[t] = 0.f;
-    // a task is a token's heads GW U part .. + GW U - 1; a step of nb kWarps tasks as so many
-    // sequences, tokens and parts, so that the walk divides nothing
-    const unsigned parts = a.parts[s], step = (unsigned)a.nb[s] * kWarps, N = a.N, tasks = a.tasks[s];
-    const unsigned task0 = blk * kWarps + warp, tok0 = task0 / parts, stok = step / parts, sb = stok / N;
-    const int spart = (int)(step - stok * parts), sn = (int)(stok - sb * N), hi = a.H[s];
-    struct At {
-        int b, n, part;
-    };
-    auto advance = [&](At &at) {
-        at.part += spart;
-        at.n += sn;
-        at.b += (int)sb;
-        if (at.part >= (int)parts) {
-            at.part -= (int)parts;
-            ++at.n;
-        }
-        if (at.n >= (int)N) {
-            at.n -= (int)N;
-            ++at.b;
-        }
-    };
-    At now{(int)(tok0 / N), 0, (int)(task0 - tok0 * parts)};
-    now.n = (int)(tok0 - (unsigned)now.b * N);
+    const unsigned step = (unsigned)a.nb[s] * kWarps * GW, units = a.units[s];
     const T *x0 = static_cast<const T *>(w ? a.x[s] : a.dy[s]), *dy0 = static_cast<const T *>(a.dy[s]);
     const int c0 = on ? e0 : 0, c1 = on ? e1 : 0;
-    // asks for the task that `at` and `task` name; past the last one for nothing
-    auto fetch = [&](const At &at, unsigned task, BwdStage<U> &st) {
-        if (task < tasks) {
-            const int h0 = at.part * GW * U + grp;
-            const T *x = x0 + at.b * a.xs[s][0] + at.n * a.xs[s][1] + (h0 < hi ? h0 * a.xs[s][2] : 0);
-            const T *dy = dy0 + at.b * a.dys[s][0] + at.n * a.dys[s][1] + (h0 < hi ? h0 * a.dys[s][2] : 0);
+    struct At {
+        int b, n, h, count;
+    };
+    auto place = [&](unsigned unit) -> At {
+        const unsigned tok = a.by_per[s](unit);
+        At at;
+        at.h = (int)(unit - tok * a.per[s]) * U;
+        at.b = (int)a.by_n(tok);
+        at.n = (int)(tok - (unsigned)at.b * a.N);
+        at.count = min(U, a.H[s] - at.h);
+        return at;
+    };
+    // asks for a unit; past the last one for zeros, while other groups of the warp go on
+    auto fetch = [&](unsigned unit, BwdStage<U, C> &st) {
+        if (unit - grp < units) {
+            const At at = unit < units ? place(unit) : At{0, 0, 0, 0};
+            const T *x = x0 + at.b * a.xs[s][0] + at.n * a.xs[s][1] + at.h * a.xs[s][2];
+            const T *dy = dy0 + at.b * a.dys[s][0] + at.n * a.dys[s][1] + at.h * a.dys[s][2];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool in = on && h0 + u * GW < hi;
+                const bool in = on && u < at.count;
                 if (w) {
                     wmma16::cp_async16(ptx::smem_u32(&st.rows[u][0][0][threadIdx.x]), x + c0, in ? 16u : 0u);
                     wmma16::cp_async16(ptx::smem_u32(&st.rows[u][0][1][threadIdx.x]), x + c1, in ? 16u : 0u);
                 }
                 wmma16::cp_async16(ptx::smem_u32(&st.rows[u][1][0][threadIdx.x]), dy + c0, in ? 16u : 0u);
                 wmma16::cp_async16(ptx::smem_u32(&st.rows[u][1][1][threadIdx.x]), dy + c1, in ? 16u : 0u);
-                if (u + 1 < U && h0 + (u + 1) * GW < hi) {
-                    x += GW * a.xs[s][2];
-                    dy += GW * a.dys[s][2];
+                if (u + 1 < at.count) {
+                    x += a.xs[s][2];
+                    dy += a.dys[s][2];
                 }
             }
-            if (a.rot) {
+            if (turn && at.count > 0) {  // pairs C p .. C p + C - 1; adjacent ones C/2 from each chunk
                 long long pos = at.n;
                 if (a.pos) pos = __ldg(a.pos + at.b * a.pos_s[0] + at.n * a.pos_s[1]);
-                const float *row = a.cs + table_row(pos, a.P, a.flags, at.part == 0) * a.cs_row;
-                for (int i = lane; i < a.rot / 4; i += 32)
-                    wmma16::cp_async16(ptx::smem_u32(&st.angles[warp][4 * i]), row + 4 * i, 16u);
+                const float *row = a.cs + table_row(pos, a.P, a.flags, p == 0 && at.h == 0) * a.cs_row;
+#pragma unroll
+                for (int i = 0; i < C / 4; ++i) {
+                    float4 *c = &st.angles[0][i][threadIdx.x], *n = &st.angles[1][i][threadIdx.x];
+                    if (kInter && C == 4) {
+                        fetch_8(c, row + e0 / 2);
+                        fetch_8(reinterpret_cast<float2 *>(c) + 1, row + e1 / 2);
+                        fetch_8(n, row + a.rot / 2 + e0 / 2);
+                        fetch_8(reinterpret_cast<float2 *>(n) + 1, row + a.rot / 2 + e1 / 2);
+                    } else {
+                        const int at4 = kInter ? (i ? e1 : e0) / 2 : e0 + 4 * i;
+                        fetch_16(c, row + at4);
+                        fetch_16(n, row + a.rot / 2 + at4);
+                    }
+                }
             }
         }
         wmma16::cp_async_commit();
     };
-    At ask = now;
+    unsigned unit = (unsigned)(blk * kWarps + warp) * GW + grp;
 #pragma unroll 1
-    for (int i = 0; i < kDepth - 1; ++i) {
-        fetch(ask, task0 + i * step, stage[i]);
-        advance(ask);
-    }
+    for (int i = 0; i < kDepth - 1; ++i) fetch(unit + i * step, stage[i]);
     int cur = 0;
+    // the groups of a warp go on together (their shuffles meet) until the first of them is past the end
 #pragma unroll 1
-    for (unsigned task = task0; task < tasks; task += step) {
+    for (; unit - grp < units; unit += step) {
         wmma16::cp_async_wait<kDepth - 2>();
-        __syncwarp();  // the other lanes' parts of the angles; and every lane is done with the stage asked for next
-        fetch(ask, task + (kDepth - 1) * step, stage[cur == 0 ? kDepth - 1 : cur - 1]);
-        advance(ask);
-        const BwdStage<U> &st = stage[cur];
+        fetch(unit + (kDepth - 1) * step, stage[cur == 0 ? kDepth - 1 : cur - 1]);
+        const BwdStage<U, C> &st = stage[cur];
         if (++cur == kDepth) cur = 0;
         float co[C], si[C];
 #pragma unroll
-        for (int t = 0; t < C; ++t) {
-            co[t] = 1.f;
-            si[t] = 0.f;
-        }
-        if (turn) {  // pairs C p .. C p + C - 1; adjacent ones C/2 from each chunk
-            const float *row = st.angles[warp];
-            constexpr int V = kInter ? C / 2 : C;
-            const int at[2] = {kInter ? e0 / 2 : e0, e1 / 2};
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                co[i] = row[at[i / V] + i % V];
-                si[i] = row[a.rot / 2 + at[i / V] + i % V];
+        for (int t = 0; t < C / 4; ++t) {
+            float4 c = make_float4(1.f, 1.f, 1.f, 1.f), n = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (turn && unit < units) {
+                c = st.angles[0][t][threadIdx.x];
+                n = st.angles[1][t][threadIdx.x];
             }
+            co[4 * t] = c.x; co[4 * t + 1] = c.y; co[4 * t + 2] = c.z; co[4 * t + 3] = c.w;
+            si[4 * t] = n.x; si[4 * t + 1] = n.y; si[4 * t + 2] = n.z; si[4 * t + 3] = n.w;
         }
-        const int h0 = now.part * GW * U + grp;
-        T *dx = static_cast<T *>(a.dx[s]) + now.b * a.dxs[s][0] + now.n * a.dxs[s][1] + (h0 < hi ? h0 * a.dxs[s][2] : 0);
+        const At now = unit < units ? place(unit) : At{0, 0, 0, 0};
+        T *dx = static_cast<T *>(a.dx[s]) + now.b * a.dxs[s][0] + now.n * a.dxs[s][1] + now.h * a.dxs[s][2];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float f[E], y[E], g[E];
@@ -660,14 +680,13 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
                     ptx::fma2(g[t], g[t + 1], g[t], g[t + 1], wf[t], wf[t + 1], q0, q1);
                 }
             }
-            if (on && h0 + u * GW < hi) {
+            if (on && u < now.count) {
                 together_c<kInter, C>(g, f);
                 *reinterpret_cast<uint4 *>(dx + e0) = repack(f, T{});
                 *reinterpret_cast<uint4 *>(dx + e1) = repack(f + C, T{});
             }
-            if (u + 1 < U && h0 + (u + 1) * GW < hi) dx += GW * a.dxs[s][2];
+            if (u + 1 < now.count) dx += a.dxs[s][2];
         }
-        advance(now);
     }
     wmma16::cp_async_wait<0>();
     if (!w) return;
@@ -745,9 +764,7 @@ namespace {
 
 // Heads a group takes at once: two (four leave more lanes idle and fewer warps: 24 and 8 heads 31 us
 // for 27), or one where two would leave less than 16 warps an SM, as in a decode step.
-int heads_at_once(int64_t tokens, int64_t heads, int L) {
-    return tokens * ((heads + 64 / L - 1) / (64 / L)) >= 16LL * sm_count() ? 2 : 1;
-}
+int heads_at_once(int64_t rows, int L) { return rows * L / 64 >= 16LL * sm_count() ? 2 : 1; }
 
 template <typename T, bool kInter>
 auto rope_kernel(int L, int U) -> void (*)(const RopeArgs) {
@@ -761,10 +778,10 @@ auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
     if (L == 8) return U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
     return U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
 }
-// The backward's kernel, the heads a warp takes at once, and its shared memory.
+// The backward's kernel, the heads a group takes at once, the groups of a warp, and its shared memory.
 struct BwdPick {
     void (*kern)(const RopeBwdArgs);
-    int heads, smem;
+    int U, groups, smem;
 };
 template <typename T, bool kInter>
 BwdPick bwd_pick(int64_t d) {
@@ -772,29 +789,35 @@ BwdPick bwd_pick(int64_t d) {
     return {d <= 64    ? qk_norm_rope_bwd_kernel<T, L0, U, kInter>
             : d <= 128 ? qk_norm_rope_bwd_kernel<T, 2 * L0, U, kInter>
                        : qk_norm_rope_bwd_kernel<T, 4 * L0, U, kInter>,
-            32 / (d <= 64 ? L0 : d <= 128 ? 2 * L0 : 4 * L0) * U, kDepth * (int)sizeof(BwdStage<U>)};
+            U, 32 / (d <= 64 ? L0 : d <= 128 ? 2 * L0 : 4 * L0), kDepth * (int)sizeof(BwdStage<U, 16 / sizeof(T)>)};
 }
 
 }  // namespace
 
 attn_status_t launch_qk_norm_rope(const attn_qk_norm_rope_params_t &p, cudaStream_t st) {
     RopeArgs a;
-    a.N = (int)p.N; a.Hq = (int)p.Hq; a.Hk = (int)p.Hkv; a.d = (int)p.d;
+    a.N = (int)p.N; a.H[0] = (int)p.Hq; a.H[1] = (int)p.Hkv; a.d = (int)p.d;
     a.rot = p.cos_sin ? (int)p.rot : 0;
     a.P = (int)p.cos_sin_rows; a.inv_d = 1.f / (float)p.d; a.eps = p.eps;
-    a.q = p.q; a.k = p.k; a.wq = p.wq; a.wk = p.wk; a.qo = p.q_out; a.ko = p.k_out;
-    copy3(a.qs, p.q_stride); copy3(a.ks, p.k_stride); copy3(a.qos, p.q_out_stride); copy3(a.kos, p.k_out_stride);
+    a.x[0] = p.q; a.x[1] = p.k; a.w[0] = p.wq; a.w[1] = p.wk; a.o[0] = p.q_out; a.o[1] = p.k_out;
+    copy3(a.xs[0], p.q_stride); copy3(a.xs[1], p.k_stride); copy3(a.os[0], p.q_out_stride); copy3(a.os[1], p.k_out_stride);
     a.cs = p.cos_sin; a.cs_row = p.cos_sin_stride; a.pos = p.positions; copy2(a.pos_s, p.positions_stride);
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
-    const int L = lanes_of(p.d);
+    const int L = lanes_of(p.d), GW = 32 / L;
     const bool h = p.dtype == ATTN_DTYPE_BF16;
-    const int U = heads_at_once(p.B * p.N, p.Hq + p.Hkv, L), n = 32 / L * U;
-    a.cq = (int)((p.Hq + n - 1) / n);
-    a.ck = (int)((p.Hkv + n - 1) / n);
-    a.tasks = p.B * p.N * (a.cq + a.ck);
-    if (a.tasks > 0xfffffff0LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
-    const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
+    a.tokens = (unsigned)(p.B * p.N);
+    a.by_n = div_by((uint32_t)p.N);
+    const int U = heads_at_once((long long)a.tokens * (p.Hq + p.Hkv), L);
+    long long warps[2];
+    for (int s = 0; s < 2; ++s) {
+        a.per[s] = (a.H[s] + U - 1) / U;
+        a.by_per[s] = div_by((uint32_t)a.per[s]);
+        warps[s] = ((long long)a.tokens * a.per[s] + GW - 1) / GW;
+        if ((warps[s] + kWarps) * GW > 0xffffffffLL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
+    }
+    a.warps_q = (unsigned)warps[0];
+    const dim3 grid((unsigned)((warps[0] + warps[1] + kWarps - 1) / kWarps));
     auto kern = p.interleaved ? (h ? rope_kernel<__nv_bfloat16, true>(L, U) : rope_kernel<float, true>(L, U))
                               : (h ? rope_kernel<__nv_bfloat16, false>(L, U) : rope_kernel<float, false>(L, U));
     return launched(launch_pdl(kern, grid, dim3(kThreads), 0, st, a), "qk_norm_rope");
@@ -818,21 +841,23 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     const bool h = p.dtype == ATTN_DTYPE_BF16;
     const BwdPick pick = p.interleaved ? (h ? bwd_pick<__nv_bfloat16, true>(p.d) : bwd_pick<float, true>(p.d))
                                        : (h ? bwd_pick<__nv_bfloat16, false>(p.d) : bwd_pick<float, false>(p.d));
-    const int n = pick.heads;
+    a.tokens = (unsigned)(p.B * p.N);
+    a.by_n = div_by((uint32_t)p.N);
     for (int s = 0; s < 2; ++s) {
-        a.parts[s] = (a.H[s] + n - 1) / n;
-        const long long tasks = p.B * p.N * a.parts[s];
-        if (tasks > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
-        a.tasks[s] = (unsigned)tasks;
+        a.per[s] = (a.H[s] + pick.U - 1) / pick.U;
+        a.by_per[s] = div_by((uint32_t)a.per[s]);
+        const long long units = (long long)a.tokens * a.per[s];
+        if (units > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
+        a.units[s] = (unsigned)units;
     }
-    // two blocks an SM (what shared memory holds), each tensor's share by its tasks; never more blocks
+    // two blocks an SM (what shared memory holds), each tensor's share by its units; never more blocks
     // than warps of work
     const int most = rope_bwd_blocks();
-    a.nb[0] = (int)((long long)most * a.parts[0] / (a.parts[0] + a.parts[1]));
+    a.nb[0] = (int)((long long)most * a.per[0] / (a.per[0] + a.per[1]));
     a.nb[0] = a.nb[0] < 1 ? 1 : a.nb[0];
     a.nb[1] = most - a.nb[0];
     for (int s = 0; s < 2; ++s) {
-        const int cap = (int)((a.tasks[s] + kWarps - 1) / kWarps);
+        const int cap = (int)((a.units[s] + kWarps * pick.groups - 1) / (kWarps * pick.groups));
         a.nb[s] = a.nb[s] < cap ? a.nb[s] : cap;
     }
     const int blocks = a.nb[0] + a.nb[1];
@@ -861,7 +886,7 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     const int L = lanes_of(c.d);
     const bool h = c.dtype == ATTN_DTYPE_BF16;
-    const int U = heads_at_once(c.T, p.Hq + 2 * c.Hkv, L), n = 32 / L * U;
+    const int U = heads_at_once(c.T * (p.Hq + 2 * c.Hkv), L), n = 32 / L * U;
     a.cq = (int)((p.Hq + n - 1) / n);
     a.ck = (int)((c.Hkv + n - 1) / n);
     a.tasks = c.T * (a.cq + 2 * a.ck);
