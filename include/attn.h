@@ -438,8 +438,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq, i
 /*
  * attn_qk_norm_rope_bwd -- with n_c = x_c r (r = 1 / sqrt(mean x^2 + eps)), dt = R^T dy:
  *     dw_c = sum over rows dt_c n_c,   dx_c = r (w_c dt_c - n_c mean_j w_j dt_j n_j).
- * The row sums are added in a fixed order (the same bits from run to run).  The workspace is
- * caller-owned device memory, 16-byte aligned, of any contents on entry; it may be NULL when both
+ * The weight gradients are summed in fp32 in a fixed order (the same bits from run to run).  The
+ * workspace is caller-owned device memory, 16-byte aligned, of any contents on entry; it may be NULL when both
  * weights are.  Queues one kernel, and one more for the weight gradients.
  */
 attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t *params, void *workspace,
@@ -543,15 +543,18 @@ size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
 /*
  * attn_paged_fwd -- attention of the new tokens, one or many per sequence in one call, over the
  * paged cache.  ("How Does FlashAttention Preserve Global Softmax Across Tiles?", sections 3, 6
- * and 8.)  The keys of a sequence are read once for all query heads that share them.  The work is
- * cut into equal shares of key tiles over the GPU; a row whose keys fall into several shares is
- * merged from their states (m, l, u), in a fixed order: the same bits from run to run.
+ * and 8.)  A key or value row is read once for all query heads that share it.  The work is cut into
+ * equal shares of key tiles over the GPU; a row whose keys fall into several shares is merged from
+ * their states (m, l, u), in a fixed order: the same bits from run to run (another max_q may take
+ * another kernel, and give other last bits).  The weights are rounded to bf16 before the value
+ * product, as in attn_fwd; sums and states are fp32.
  * Values at positions >= kv_lens[b] are never used, whatever lies there.  A visible value that is
  * infinite or NaN reaches every query row of its tile, as 0 * inf does in a product.
  * workspace: caller-owned device memory, 16-byte aligned, of any contents on entry; calls that
- * overlap on the GPU need one each.
+ * overlap on the GPU need one each.  It may be NULL where attn_paged_fwd_workspace_bytes is 0.
  * Supported: bfloat16, d in {64, 128}, page_size a power of two >= 16, 1 <= Hq / Hkv <= 64,
- * scale > 0; tensors 16-byte aligned, strides non-zero multiples of 8 elements.
+ * T * Hq / Hkv <= 2^30, scale > 0; tensors 16-byte aligned, strides non-zero multiples of 8 elements.
+ * Queues one kernel, or two (up to 32 rows max_q * Hq / Hkv a key head, or more).
  */
 attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *workspace, size_t workspace_bytes,
                              attn_stream_t stream);
