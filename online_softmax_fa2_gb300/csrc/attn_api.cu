@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "attn_internal.h"
+#include "attn_more.h"
 
 namespace attn {
 

@@ -10,13 +10,10 @@
 namespace attn {
 
 // Error bits of the device error word (see attn_device_error_flags).
-enum : uint32_t { kFlagWaitTimeout = 1u, kFlagKvLenClamped = 2u, kFlagBadIndex = 4u };
+enum : uint32_t { kFlagWaitTimeout = 1u, kFlagKvLenClamped = 2u };
 
 // Records a message for attn_last_error() and returns `st`.
 attn_status_t fail(attn_status_t st, const char *fmt, ...);
-
-// Clears the calling thread's last error message (at the start of every entry point).
-void clear_error();
 
 // Device address of the device error word of the current device (nullptr on failure).
 uint32_t *device_flags();
@@ -57,10 +54,6 @@ attn_status_t encode(CUtensorMap *m, const void *ptr, int64_t B, int64_t N, int6
 // already filled by the prep kernel.
 attn_status_t launch_bwd_tc(const attn_bwd_params_t &p, float *dq_acc, const float *crow, const float *lrow,
                             cudaStream_t s);
-
-// A tag for the counters of a call that merges in its own kernel: 48 bits, never 0, another one
-// every call (decode.cu).
-unsigned long long next_call_tag();
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

@@ -38,10 +38,13 @@
 #include "warp_mma.cuh"
 
 namespace attn {
+namespace {
 
-// Tags of calls that count on workspace words: 48 bits, distinct for every call of the process, never 0; the
+using namespace wmma16;
+
+// Tags of fused decode calls: 48 bits, distinct for every call of the process, never 0; the
 // sequence starts from the clock so that it does not repeat an earlier process's.
-unsigned long long next_call_tag() {
+unsigned long long next_decode_tag() {
     static std::atomic<unsigned long long> next{
         (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 2654435761ull};
     for (;;) {
@@ -49,10 +52,6 @@ unsigned long long next_call_tag() {
         if (t) return t;
     }
 }
-
-namespace {
-
-using namespace wmma16;
 
 constexpr int kThreads = 128;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -572,7 +571,7 @@ attn_status_t launch_decode_split(const attn_fwd_params_t &p, int num_splits, fl
     a.bias = p.bias; a.bs0 = p.bias_stride[0]; a.bs1 = p.bias_stride[1]; a.bs2 = p.bias_stride[2];
     a.kv_lens = p.kv_lens; a.part = partials;
     a.counters = counters;
-    a.tag = counters ? next_call_tag() : 0ull;
+    a.tag = counters ? next_decode_tag() : 0ull;
     a.o = static_cast<__nv_bfloat16 *>(p.o);
     a.os0 = p.o_stride[0]; a.os1 = p.o_stride[1]; a.os2 = p.o_stride[2];
     a.lse = p.lse;

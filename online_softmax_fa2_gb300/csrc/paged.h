@@ -1,7 +1,7 @@
 // paged.h -- host side of the attention over a paged cache (arguments validated by paged_api.cu).
 #pragma once
 
-#include "attn_internal.h"
+#include "attn_more.h"
 
 namespace attn {
 namespace paged {

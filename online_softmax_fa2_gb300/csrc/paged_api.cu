@@ -2,7 +2,6 @@
 // and the attention over it: argument checks on the host, then the launchers.
 #include <cmath>
 
-#include "attn_internal.h"
 #include "paged.h"
 #include "qk_rope.h"
 

@@ -2,6 +2,9 @@
 // choice of a kernel, the cut of its workspace, the tensor maps.
 #include <cudaTypedefs.h>
 
+#include <atomic>
+#include <chrono>
+
 #include "paged.h"
 #include "paged_merge.cuh"
 
@@ -98,6 +101,15 @@ attn_status_t encode_q(CUtensorMap *m, const attn_paged_fwd_params_t &p, int tok
     return ATTN_OK;
 }
 
+// A tag for the marks of one call: never 0, another one every call of the process; the sequence starts
+// from the clock, so that it does not repeat an earlier process's.
+unsigned long long next_tag() {
+    static std::atomic<unsigned long long> next{
+        (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 2654435761ull};
+    for (;;)
+        if (const unsigned long long t = next.fetch_add(1)) return t;
+}
+
 int log2_of(int x) {
     int l = 0;
     while ((1 << l) < x) ++l;
@@ -139,7 +151,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     a.marks = pl.cuts ? reinterpret_cast<unsigned long long *>(ws) : nullptr;
     a.ml = reinterpret_cast<float *>(ws + pl.off_ml);
     a.u = reinterpret_cast<float *>(ws + pl.off_u);
-    a.tag = next_call_tag();
+    a.tag = next_tag();
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
     CUtensorMap mk{}, mv{};  // not used when there are no pages

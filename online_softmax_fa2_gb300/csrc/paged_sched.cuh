@@ -16,7 +16,7 @@
 
 #include <cuda_bf16.h>
 
-#include "attn_internal.h"
+#include "attn_more.h"
 #include "fwd_bf16_common.cuh"
 #include "sm100_ptx.cuh"
 

@@ -39,6 +39,21 @@ using bf16fwd::kSmemMax;
 using paged::kLn2;
 using paged::kWaitLimitNs;
 
+// 3-D tiled bulk-tensor load global -> shared, completion counted on `bar` (bytes).
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+// Brings a 3-D box into L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *m, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0),
+                 "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 constexpr int kThreads = 384;
 // Registers: launched at 168 a thread (384 x 168 = 64512), split 128 x 56 + 256 x 224 = 64512.
 constexpr uint32_t kRegsIssue = 56, kRegsSoftmax = 224;
@@ -206,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.keys == 0) continue;
                 if (lane < 2 * (D / 64)) {  // the block's queries into L2: they are asked for some tiles later
                     const int tok = w.seq.q0 + paged::div_g(a, w.k * a.R + (lane & 1) * (a.R >> 1));
-                    ptx::tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.hk * a.G, tok);
+                    tma_prefetch_3d(&tm_q, (lane >> 1) * 64, w.hk * a.G, tok);
                 }
                 const int *row = a.bt + w.b * a.bt_s;
                 int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
@@ -380,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tok = p.seq.q0 + paged::div_g(a, p.k * a.R + X * half);
 #pragma unroll
                 for (int pn = 0; pn < D / 64; ++pn)
-                    ptx::tma_load_3d(smem + X * L::kTile + pn * kPanelBytes, &tm_q, &ctrl->q_full[X], pn * 64, p.hk * a.G, tok);
+                    tma_load_3d(smem + X * L::kTile + pn * kPanelBytes, &tm_q, &ctrl->q_full[X], pn * 64, p.hk * a.G, tok);
                 ++asked;
             }
         };

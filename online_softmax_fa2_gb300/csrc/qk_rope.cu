@@ -16,7 +16,6 @@
 // log2 L shuffles.  Sums, norms and angles are fp32; an output is rounded once.
 #include <cuda_bf16.h>
 
-#include "attn_internal.h"
 #include "fwd_bf16_common.cuh"
 #include "qk_rope.h"
 #include "sm100_ptx.cuh"

@@ -1,7 +1,7 @@
 // qk_rope.h -- launchers of qk_rope.cu (arguments validated by the caller, paged_api.cu).
 #pragma once
 
-#include "attn_internal.h"
+#include "attn_more.h"
 
 namespace attn {
 
