@@ -74,7 +74,8 @@ attn_status_t check_norm_rope_sizes(const attn_qk_norm_rope_params_t *p) {
     return ATTN_OK;
 }
 
-attn_status_t check_cache(const attn_paged_cache_t &c) {
+// The sizes of a cache and its batch.
+attn_status_t check_cache_sizes(const attn_paged_cache_t &c) {
     attn_status_t st = check_dtype(c.dtype);
     if (st) return st;
     if (c.B < 0 || c.T < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%lld T=%lld)", (long long)c.B, (long long)c.T);
@@ -90,6 +91,12 @@ attn_status_t check_cache(const attn_paged_cache_t &c) {
         return fail(ATTN_ERR_UNSUPPORTED, "table_width * page_size must be below 2^31");
     if (!c.cu_q && c.T % c.B)
         return fail(ATTN_ERR_INVALID_ARG, "without cu_q, T = %lld must be a multiple of B = %lld", (long long)c.T, (long long)c.B);
+    return ATTN_OK;
+}
+
+attn_status_t check_cache(const attn_paged_cache_t &c) {
+    attn_status_t st = check_cache_sizes(c);
+    if (st || c.T == 0) return st;
     if (!c.kv_lens || (!c.block_table && c.table_width > 0))
         return fail(ATTN_ERR_INVALID_ARG, "kv_lens or block_table is NULL");
     const int64_t sizes[3] = {c.num_pages, c.page_size, c.Hkv};
@@ -201,7 +208,10 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_append_params_t *p, 
 
 extern "C" size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *p) {
     clear_error();
-    if (!p || check_paged_fwd(p) || p->cache.T < 1 || p->cache.B < 1) return 0;
+    if (!p || check_paged_fwd(p) || check_cache_sizes(p->cache) || p->cache.T < 1) {
+        clear_error();
+        return 0;
+    }
     return paged_fwd_workspace(*p);
 }
 

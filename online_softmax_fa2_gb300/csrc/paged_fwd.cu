@@ -21,14 +21,15 @@ struct Plan {
     int R, kt, grid, box;
     int min_cut;
     bool cuts;  // a block may be cut
-    bool fits;  // the line of tiles is shorter than 2^31
+    bool fits;  // the line of tiles is shorter than kLongestLine
     size_t off_ml, off_u, bytes;
 };
 
 Plan make_plan(const attn_paged_fwd_params_t &p) {
     const attn_paged_cache_t &c = p.cache;
     const int64_t G = p.Hq / c.Hkv;
-    const int64_t most = p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;  // tokens a sequence, or their mean
+    // tokens a sequence, or their mean
+    const int64_t most = p.max_q > c.T ? c.T : p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;
     const int64_t rows = most * G;
     Plan pl;
     // Up to 32 rows a key head the warp-level kernel, more the 128-row tiles.  64 sequences of 2048 keys,
@@ -43,7 +44,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 5);
-    pl.fits = tiles < 2147483648.0 - 65536.0;
+    pl.fits = tiles < (double)kLongestLine;
     const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d, pl.R));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
@@ -118,7 +119,10 @@ int log2_of(int x) {
 
 }  // namespace
 
-size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p) { return make_plan(p).bytes; }
+size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p) {
+    const Plan pl = make_plan(p);
+    return pl.fits ? pl.bytes : 0;
+}
 
 attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t st) {
     const attn_paged_cache_t &c = p.cache;

@@ -82,10 +82,16 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
     }
     ptx::grid_dep_wait();
     ptx::launch_dependents();
+    int *sums_of_32 = reinterpret_cast<int *>(smem);  // where the copies will go
+    if (a.B > 32) {
+        line_sums(a, sums_of_32);
+        __syncthreads();
+    }
     if (warp == 4) {
-        const Share sh = find_share(a, blockIdx.x, gridDim.x);
+        const Share sh = find_share(a, blockIdx.x, gridDim.x, sums_of_32);
         if (lane == 0) ctrl->share = sh;
     }
+    if (a.B > 32) ptx::fence_proxy_async_smem();  // the sums, before a copy takes their place
     __syncthreads();
     Walk w;
     if (!w.begin(a, ctrl->share)) return;

@@ -25,6 +25,7 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr long long kLongestLine = 0x7fff0000;  // tiles of a line, so that a distance along it is an int
 constexpr size_t kCutBytes = 32;  // a share's record of the item that it cuts (paged_tc_sm103.cu)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
@@ -107,34 +108,70 @@ __device__ __forceinline__ int seq_len_of(const Args &a, const Seq &s, int nb) {
 }
 
 struct Share {
-    int per, t0, t1;  // the line between two boundaries, and this CTA's [t0, t1); the line is shorter than 2^31
+    int per, t0, t1;  // the line between two boundaries, and this CTA's [t0, t1); an int: kLongestLine
     int b, hk, k, j;  // where t0 lies (j = the item's tiles: at its end)
     Seq seq;
 };
 
-// The share of CTA c of C.  One warp; every lane gets the result.  It runs once, cold, before
-// anything else can: short code counts for more than fast code.
-__device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
+// The sum over the warp of v >= 0.
+__device__ __forceinline__ long long wide_sum(int v) {
+    const unsigned u = (unsigned)v;
+    return ((long long)__reduce_add_sync(0xffffffffu, u >> 16) << 16) + __reduce_add_sync(0xffffffffu, u & 0xffffu);
+}
+
+// The line of one head of every 32 sequences, into sums[0 .. (B - 1) / 32] of shared memory (at most
+// 8 KB); all warps of the CTA, which meet afterwards.  (One warp walking over 1024 sequences, once
+// for the total and once for each boundary, took 52 us at the start of a call.)
+__device__ __forceinline__ void line_sums(const Args &a, int *sums) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int g = threadIdx.x >> 5; g * 32 < a.B; g += blockDim.x >> 5) {
+        Seq s{0, 0, 0};
+        if (g * 32 + lane < a.B) s = seq_info(a, g * 32 + lane, blockIdx.x == 0);
+        const long long w = wide_sum(seq_len_of(a, s, num_blocks(a, s)));
+        if (lane == 0) sums[g] = (int)min(w, 0x7fffffffll);
+    }
+}
+
+// The warp's running sum of v.
+__device__ __forceinline__ int warp_scan(int v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// The share of CTA c of C; sums: line_sums, for more than 32 sequences.  One warp; every lane gets the
+// result.  It runs once, cold, before anything else can: short code counts for more than fast code.
+__device__ __forceinline__ Share find_share(const Args &a, int c, int C, const int *sums) {
+    const int lane = threadIdx.x & 31, groups = (a.B + 31) / 32;
     Share r;
     r.b = r.hk = r.k = r.j = 0;
     r.seq = Seq{0, 0, 0};
-    Seq s, ahead{0, 0, 0};
-    int w = 0, nb = 0, total = 0;
-    const bool report = c == 0;
-    if (lane < a.B) ahead = seq_info(a, lane, report);
-#pragma unroll 1
-    for (int b = lane; b < a.B + lane; b += 32) {
-        s = ahead;
-        ahead = Seq{0, 0, 0};
-        if (b + 32 < a.B) ahead = seq_info(a, b + 32, report);
+    Seq s{0, 0, 0};
+    int w = 0, nb = 0;
+    long long line = 0;
+    if (groups == 1) {
+        if (lane < a.B) s = seq_info(a, lane, c == 0);
         nb = num_blocks(a, s);
         w = seq_len_of(a, s, nb);
-        total += __reduce_add_sync(0xffffffffu, w);
+        line = wide_sum(w);
+    } else {
+#pragma unroll 1
+        for (int g = lane; g < groups + lane; g += 32) line += wide_sum(g < groups ? sums[g] : 0);
     }
-    total *= a.Hkv;
-    r.per = max((int)((unsigned)(total + C - 1) / (unsigned)C), a.min_share);
+    line *= a.Hkv;
+    r.per = 1;
     r.t0 = r.t1 = 0;
+    if (line > kLongestLine) {  // entries of cu_q that go back and forth: more rows than the batch has tokens
+        if (c == 0 && lane == 0) atomicOr(a.flags, kFlagBadIndex);
+        return r;
+    }
+    const int total = (int)line;
+    r.per = max((int)((unsigned)(total + C - 1) / (unsigned)C), a.min_share);
     // the boundaries c + 1, then c: the item that each falls into, and which side of it it goes to
 #pragma unroll 1
     for (int e = 1; e >= 0; --e) {
@@ -144,26 +181,28 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
             else r.t1 = total;
             continue;
         }
-        int left = at;
+        int left = at, b0 = 0;
+        if (groups > 1) {
 #pragma unroll 1
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            if (a.B > 32) {  // (up to 32 sequences: s and w are theirs still)
-                s = Seq{0, 0, 0};
-                if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
-                nb = num_blocks(a, s);
-                w = seq_len_of(a, s, nb);
-            }
-            int incl = w * a.Hkv;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += o;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, incl > left);
-            if (!past) {
+            for (int g0 = 0; g0 < groups; g0 += 32) {
+                const int v = g0 + lane < groups ? sums[g0 + lane] * a.Hkv : 0, incl = warp_scan(v);
+                const unsigned past = __ballot_sync(0xffffffffu, incl > left);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    b0 = 32 * (g0 + l);
+                    left -= __shfl_sync(0xffffffffu, incl - v, l);
+                    break;
+                }
                 left -= __shfl_sync(0xffffffffu, incl, 31);
-                continue;
             }
+            s = Seq{0, 0, 0};
+            if (b0 + lane < a.B) s = seq_info(a, b0 + lane, false);
+            nb = num_blocks(a, s);
+            w = seq_len_of(a, s, nb);
+        }
+        {
+            const int incl = warp_scan(w * a.Hkv);
+            const unsigned past = __ballot_sync(0xffffffffu, incl > left);
             const int src = __ffs(past) - 1, ws = __shfl_sync(0xffffffffu, w, src);
             r.b = b0 + src;
             r.seq.q0 = __shfl_sync(0xffffffffu, s.q0, src);
@@ -172,19 +211,12 @@ __device__ __forceinline__ Share find_share(const Args &a, int c, int C) {
             left -= __shfl_sync(0xffffffffu, incl, src) - ws * a.Hkv;
             r.hk = min((int)((unsigned)left / (unsigned)ws), a.Hkv - 1);
             left -= r.hk * ws;
-            break;
         }
         const int nbs = num_blocks(a, r.seq);
         r.k = 0;
 #pragma unroll 1
         for (int k0 = 0; nbs > 1; k0 += 32) {
-            const int k = k0 + lane, t = k < nbs ? block_len(a, r.seq, k) : 0;
-            int in = t;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, in, d);
-                if (lane >= d) in += x;
-            }
+            const int k = k0 + lane, t = k < nbs ? block_len(a, r.seq, k) : 0, in = warp_scan(t);
             const unsigned hit = __ballot_sync(0xffffffffu, in > left);
             if (hit || k0 + 32 >= nbs) {
                 const int l = hit ? __ffs(hit) - 1 : 0;

@@ -176,6 +176,17 @@ def test_paged_null_and_empty(lib):
     assert lib.attn_paged_fwd(fwd(cache_T=0, cache_B=0), None, 0, None) == S.OK
 
 
+def test_workspace_of_invalid_or_overlong_arguments_is_none(lib):
+    need = lambda **kw: lib.attn_paged_fwd_workspace_bytes(fwd(**kw))  # noqa: E731
+    assert need(cache_table_width=1024) > 0
+    for kw in (dict(cache_table_width=-5), dict(cache_table_width=1 << 62), dict(cache_B=0), dict(cache_T=0),
+               dict(cache_T=1 << 29, cache_B=1, cache_table_width=1 << 20), dict(max_q=-1), dict(cache_d=96)):
+        assert need(**kw) == 0, kw
+        assert ofa.last_error() == ""
+    # more tokens a sequence than there are tokens: as many as there are
+    assert need(max_q=2, cache_table_width=1024) == need(max_q=(1 << 63) - 1, cache_table_width=1024) > 0
+
+
 def test_python_refusals_without_a_gpu():
     x = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

@@ -380,3 +380,32 @@ def test_a_stream_given_owns_what_the_call_allocates():
     q2 = ofa.attn_paged_append(s["q"], k, k, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], stream=st)
     st.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(q2, s["q"])
+
+
+@pytest.mark.parametrize("new,lens,Hq,Hkv,mq", [
+    ([1] * 1500, [(37 * b) % 61 for b in range(1500)], 2, 2, 1),
+    ([(b * 7) % 4 for b in range(1100)], [(29 * b) % 90 for b in range(1099)] + [9000], 4, 1, 3),
+    ([(b * 7) % 3 for b in range(1089)] + [300], [(29 * b) % 50 for b in range(1089)] + [2000], 2, 2, 300),
+])
+def test_thousands_of_sequences(new, lens, Hq, Hkv, mq):
+    # more than 32 x 32: the line's parts are found in two steps
+    s = paged_inputs(new, lens, Hq, Hkv, 64, 16, seed=31)
+    o, lse = run(s, max_q=mq)
+    check_paged(o, lse, s, new, lens, True, 1 / math.sqrt(64))
+    assert ofa.device_error_flags() == 0
+
+
+def test_a_cu_that_goes_back_and_forth_past_every_length_is_reported():
+    # every other sequence claims all tokens over 65536 keys: 2 heads x 512 sequences x 2048 blocks of
+    # 1028 tiles, more than 2^31, though T tokens alone are far below it.  Nothing is computed.
+    T, B, page = 1 << 15, 1024, 1024
+    q = torch.randn(T, 2, 64, device=DEV).bfloat16()
+    kp = torch.randn(64, page, 2, 64, device=DEV).bfloat16()
+    bt = torch.arange(64, dtype=torch.int32, device=DEV).repeat(B, 1)
+    lens = torch.full((B,), 64 * page, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, T] * (B // 2) + [0], dtype=torch.int32, device=DEV)
+    out, lse = torch.full_like(q, 3.0), torch.full((T, 2), 5.0, device=DEV)
+    ofa.device_error_flags()
+    ofa.attn_paged_fwd(q, kp, kp, bt, lens, cu, max_q=1, causal=False, out=out, lse=lse)
+    assert ofa.device_error_flags() == 4
+    assert bool((out == 3.0).all()) and bool((lse == 5.0).all())
