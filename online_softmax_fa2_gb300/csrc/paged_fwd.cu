@@ -17,7 +17,7 @@ namespace {
 using namespace paged;
 
 struct Plan {
-    bool tc;
+    int tc, tile_rows;  // row tiles a block (0: the kernel for few rows), rows of one at most
     int R, kt, grid, box;
     int min_cut;
     bool cuts;  // a block may be cut
@@ -35,9 +35,10 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     // Up to 32 rows a key head the warp-level kernel, more the 128-row tiles.  64 sequences of 2048 keys,
     // 8 heads of 128: 16 rows take 99 us in blocks of 16, 100 of 32, 122 in tiles; 24 take 181, 103, 123; 32
     // take 184, 107, 123; 48 take 264, 186, 125.
-    pl.tc = rows > 32;
+    pl.tc = rows > (128 / G) * G ? 2 : rows > 32 ? 1 : 0;
+    pl.tile_rows = rows > (64 / G) * G ? 128 : 64;
     // (the 128-row tiles take whole tokens, so that TMA can bring their queries)
-    pl.R = pl.tc ? (int)(2 * (128 / G) * G) : rows <= 16 ? 16 : 32;
+    pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : rows <= 16 ? 16 : 32;
     pl.kt = pl.tc ? 7 : 6;
     pl.box = pl.tc ? kTcBoxKeys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;
@@ -45,7 +46,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 5);
     pl.fits = tiles < (double)kLongestLine;
-    const int64_t full = (int64_t)sms * (pl.tc ? 1 : rows_blocks(c.d, pl.R));
+    const int64_t full = (int64_t)sms * (pl.tc ? 3 - pl.tc : rows_blocks(c.d, pl.R));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
@@ -57,7 +58,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     }
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
     pl.off_ml = up(pl.tc ? pl.grid * kCutBytes : slots * sizeof(unsigned long long));
-    const size_t srows = pl.tc ? 256 : pl.R;  // rows a slot
+    const size_t srows = pl.tc ? 128 * pl.tc : pl.R;  // rows a slot
     pl.off_u = pl.off_ml + up(slots * srows * 2 * sizeof(float));
     pl.bytes = pl.off_u + slots * srows * (size_t)c.d * sizeof(float);
     return pl;
@@ -166,9 +167,9 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     }
     if (pl.tc) {
         CUtensorMap mq;
-        const attn_status_t r = encode_q(&mq, p, 128 / a.G);
+        const attn_status_t r = encode_q(&mq, p, pl.tile_rows / a.G);
         if (r) return r;
-        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.grid, pl.cuts, st);
+        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.tc, pl.tile_rows, pl.grid, pl.cuts, st);
     }
     return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }
