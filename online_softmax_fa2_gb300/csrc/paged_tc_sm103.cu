@@ -578,42 +578,73 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
 
 // Merges the states of cut items ("How Does FlashAttention Preserve Global Softmax Across Tiles?",
 // section 3), in share order.  CTA (c, tile, columns / 32) takes the item whose first part is the end of
-// share c, if there is one; a thread takes a row.  A kernel of its own: the merge's registers in the
+// share c, if there is one; GR threads share a row, each every GR-th part: four where items are cut into
+// many parts (launch_paged_tc), else one.  A kernel of its own: the merge's registers in the
 // attention kernel's made its softmax spill (a 2048-token chunk 420 -> 800 us), and at its end one
 // warpgroup merging 128 rows took 8 to 11 us.  No CTA of it finds room on an SM before the attention
 // kernel's are done, so what it has to know is written down for it (Cut) instead of searched for.
 constexpr int kMergeCols = 32;
-template <int D, int NT>
-__global__ void __launch_bounds__(BQ, 8) paged_tc_merge_kernel(const paged::Args a) {
-    const int c = blockIdx.x, X = blockIdx.y, col = blockIdx.z * kMergeCols, r = threadIdx.x;
+template <int D, int NT, int GR>
+__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a) {
+    static_assert(GR == 1 || GR == 4, "the sums below");
+    __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][kMergeCols + 1];
+    const int c = blockIdx.x, X = blockIdx.y, col = blockIdx.z * kMergeCols, r = threadIdx.x % BQ, g = threadIdx.x / BQ;
     ptx::grid_dep_wait();
     ptx::launch_dependents();
     const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + c);
     const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // n[2], row0, end | q0, hk
     const int n = X ? c0.y : c0.x, half = a.R / NT, row = c0.z + X * half + r;
-    if (n < 2 || r >= half || row >= c0.w) return;
+    if (n < 2) return;  // the whole CTA
+    const bool mine = r < half && row < c0.w;
+    const int parts = mine ? n : 0;
     auto slot = [&](int p) { return paged::state_slot(c + p, c); };
     float M = -INFINITY, sum = 0.f, v[kMergeCols];
 #pragma unroll 4
-    for (int p = 0; p < n; ++p) M = fmaxf(M, __ldcg(state_ml<NT>(a, slot(p), X, r)).x);
+    for (int p = g; p < parts; p += GR) M = fmaxf(M, __ldcg(state_ml<NT>(a, slot(p), X, r)).x);
+    if (GR > 1) {
+        top[g][r] = M;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < GR; ++k) M = fmaxf(M, top[k][r]);
+    }
     const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int t = 0; t < kMergeCols; ++t) v[t] = 0.f;
 #pragma unroll 1
-    for (int p = 0; p < n; ++p) {
+    for (int p = g; p < parts; p += GR) {
         const float2 ml = __ldcg(state_ml<NT>(a, slot(p), X, r));
         const float4 *src = state_u<D, NT>(a, slot(p), X, r) + (col / 4) * BQ;
+        float4 y[kMergeCols / 4];
+#pragma unroll
+        for (int t = 0; t < kMergeCols / 4; ++t) y[t] = __ldcg(src + t * BQ);
         const float f = ptx::ex2(ml.x - ref);
         sum = fmaf(f, ml.y, sum);
 #pragma unroll
         for (int t = 0; t < kMergeCols / 4; ++t) {
-            const float4 y = __ldcg(src + t * BQ);
-            v[4 * t] = fmaf(f, y.x, v[4 * t]);
-            v[4 * t + 1] = fmaf(f, y.y, v[4 * t + 1]);
-            v[4 * t + 2] = fmaf(f, y.z, v[4 * t + 2]);
-            v[4 * t + 3] = fmaf(f, y.w, v[4 * t + 3]);
+            v[4 * t] = fmaf(f, y[t].x, v[4 * t]);
+            v[4 * t + 1] = fmaf(f, y[t].y, v[4 * t + 1]);
+            v[4 * t + 2] = fmaf(f, y[t].z, v[4 * t + 2]);
+            v[4 * t + 3] = fmaf(f, y[t].w, v[4 * t + 3]);
         }
     }
+    // groups 2 and 3 to 0 and 1, then 1 to 0 (through the buffer that it read itself)
+#pragma unroll
+    for (int from = GR / 2; from > 0; --from) {
+        if (g >= from && g < 2 * from) {
+            float *to = part[from == 2 ? g - 2 : 1][r];
+#pragma unroll
+            for (int t = 0; t < kMergeCols; ++t) to[t] = v[t];
+            to[kMergeCols] = sum;
+        }
+        __syncthreads();
+        if (g < from) {
+            const float *other = part[from == 2 ? g : 1][r];
+#pragma unroll
+            for (int t = 0; t < kMergeCols; ++t) v[t] += other[t];
+            sum += other[kMergeCols];
+        }
+    }
+    if (g > 0 || !mine) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int tok = paged::div_g(a, row), h = c1.y * a.G + row - tok * a.G;
     const long long t0 = c1.x + tok;
@@ -630,30 +661,35 @@ __global__ void __launch_bounds__(BQ, 8) paged_tc_merge_kernel(const paged::Args
 
 template <int D, int NT, int QR>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
-                     bool cuts, cudaStream_t st) {
+                     bool cuts, bool many, cudaStream_t st) {
     auto kern = paged_tc_kernel<D, NT, QR>;
     int smem = Layout<D, NT, QR>::kBytes;
     if (NT == 2 && smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT)), smem, st, mq, mk, mv, a);
     if (e == cudaSuccess && cuts)
-        e = launch_pdl(paged_tc_merge_kernel<D, NT>, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
+        e = many ? launch_pdl(paged_tc_merge_kernel<D, NT, 4>, dim3(grid, NT, D / kMergeCols), dim3(4 * BQ), 0, st, a)
+                 : launch_pdl(paged_tc_merge_kernel<D, NT, 1>, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
 template <int D>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int tiles,
-                     int tile_rows, int grid, bool cuts, cudaStream_t st) {
-    return tiles == 2        ? launch<D, 2, 128>(mq, mk, mv, a, grid, cuts, st)
-           : tile_rows == 64 ? launch<D, 1, 64>(mq, mk, mv, a, grid, cuts, st)
-                             : launch<D, 1, 128>(mq, mk, mv, a, grid, cuts, st);
+                     int tile_rows, int grid, bool cuts, bool many, cudaStream_t st) {
+    return tiles == 2        ? launch<D, 2, 128>(mq, mk, mv, a, grid, cuts, many, st)
+           : tile_rows == 64 ? launch<D, 1, 64>(mq, mk, mv, a, grid, cuts, many, st)
+                             : launch<D, 1, 128>(mq, mk, mv, a, grid, cuts, many, st);
 }
 
 }  // namespace
 
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
                               int d, int tiles, int tile_rows, int grid, bool cuts, cudaStream_t st) {
-    return d == 64 ? launch<64>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, st)
-                   : launch<128>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, st);
+    // Items cut into more than four parts or so (16 tokens of 4 query heads over a key head, d 128, 131072
+    // keys in all): 8 items 47 us with one thread a row, 27 with four; 32 items 25.8 and 23.2; 64 items
+    // 24.9 and 25.7; the 77 us of a ragged batch of chunks become 82.
+    const bool many = (double)a.Hkv * ((double)a.T * a.G / a.R + a.B) * 4. < (double)grid;
+    return d == 64 ? launch<64>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
+                   : launch<128>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
 }
 
 }  // namespace attn
