@@ -554,7 +554,7 @@ size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
  * overlap on the GPU need one each.  It may be NULL where attn_paged_fwd_workspace_bytes is 0.
  * Supported: bfloat16, d in {64, 128}, page_size a power of two >= 16, 1 <= Hq / Hkv <= 64,
  * T * Hq / Hkv <= 2^30, scale > 0; tensors 16-byte aligned, strides non-zero multiples of 8 elements.
- * Queues one kernel, or two (up to 32 rows max_q * Hq / Hkv a key head, or more).
+ * Queues one kernel or two.
  */
 attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *workspace, size_t workspace_bytes,
                              attn_stream_t stream);

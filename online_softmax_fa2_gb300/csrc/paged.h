@@ -13,7 +13,7 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
 
 // The kernels (paged_rows.cu, paged_tc_sm103.cu); maps of the key and value pages with a box of min(page, box_keys) keys.
 constexpr int kRowsBoxKeys = 64;
-constexpr int rows_blocks(int64_t d, int R) { return d == 64 && R == 16 ? 3 : 2; }  // CTAs an SM of the few-rows kernel
+constexpr int rows_blocks(int64_t d) { return d == 64 ? 3 : 2; }  // CTAs an SM of the few-rows kernel
 attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
                                 cudaStream_t s);
 constexpr int kTcBoxKeys = 128;

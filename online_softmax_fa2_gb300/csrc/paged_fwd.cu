@@ -32,13 +32,15 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t most = p.max_q > c.T ? c.T : p.max_q > 0 ? p.max_q : (c.T + c.B - 1) / c.B;
     const int64_t rows = most * G;
     Plan pl;
-    // Up to 32 rows a key head the warp-level kernel, more the 128-row tiles.  64 sequences of 2048 keys,
-    // 8 heads of 128: 16 rows take 99 us in blocks of 16, 100 of 32, 122 in tiles; 24 take 181, 103, 123; 32
-    // take 184, 107, 123; 48 take 264, 186, 125.
-    pl.tc = rows > (128 / G) * G ? 2 : rows > 32 ? 1 : 0;
+    // Up to 16 rows a key head the warp-level kernel, then the tiles: 64 sequences of 2048 keys, 8 heads of
+    // 128: 16 rows take 97 us in blocks of 16 and 104 in tiles, 24 take 178 and 105; d = 64: 16 rows 60
+    // and 68, 24 rows 105 and 68.  One tile a block up to its 128 rows (96 rows of 64 dimensions 69 us,
+    // 87 with two tiles; 160 rows 111 and 100), of 64 rows where that is enough (512 sequences of 128
+    // keys, 64 rows: 75 us, 84 in a tile of 128; 96 rows: 129 and 88).
+    pl.tc = rows > (128 / G) * G ? 2 : rows > 16 ? 1 : 0;
     pl.tile_rows = rows > (64 / G) * G ? 128 : 64;
-    // (the 128-row tiles take whole tokens, so that TMA can bring their queries)
-    pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : rows <= 16 ? 16 : 32;
+    // (the tiles take whole tokens, so that TMA can bring their queries)
+    pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : 16;
     pl.kt = pl.tc ? 7 : 6;
     pl.box = pl.tc ? kTcBoxKeys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;
@@ -46,7 +48,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     const int64_t keys = c.table_width * c.page_size;
     const double tiles = (double)c.Hkv * ((double)c.T * G / pl.R + c.B) * (double)((keys >> pl.kt) + 5);
     pl.fits = tiles < (double)kLongestLine;
-    const int64_t full = (int64_t)sms * (pl.tc ? 3 - pl.tc : rows_blocks(c.d, pl.R));
+    const int64_t full = (int64_t)sms * (pl.tc ? 3 - pl.tc : rows_blocks(c.d));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
@@ -137,11 +139,11 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     a.page_log2 = log2_of(c.page_size);
     a.width = c.num_pages > 0 ? (int)c.table_width : 0;  // without pages there are no keys
     a.num_pages = (int)c.num_pages;
-    // Least tiles a share, and inside an item at either side of a cut.  Few rows: a cut costs 4 to 8
-    // tiles (8 decodes over 2048 keys take 29 us with shares of 4 tiles, 27 with 8; one over 1024
-    // keys 17 either way, 19 with cuts of 8).  128-row tiles: an uncut block needs no share of its
-    // own (512 tokens over 512 keys take 62 us with shares of 4, 29 with 1).
-    a.min_share = pl.tc ? 1 : 8;
+    // Least tiles a share.  Few rows: a cut costs 4 to 8 tiles (8 decodes over 2048 keys take 29 us with
+    // shares of 4 tiles, 27 with 8).  128-row tiles: one sequence of 8192 keys, 8 tokens of 64/8 heads
+    // takes 25.6 us with shares of 1, 20.0 of 4, 24.1 of 8; 64 tokens of 32/8 heads over 2048 keys
+    // 20.7, 19.9 and 24.8.
+    a.min_share = pl.tc ? 4 : 8;
     a.min_cut = pl.min_cut;
     // What a block's beginning and end cost, in tiles (a mixed batch of 244 blocks of 3 to 32 tiles:
     // 134 us counted as 0, 105 as 2, 97 as 4, 97 as 6; few rows: no difference).

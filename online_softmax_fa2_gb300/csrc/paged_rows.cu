@@ -1,10 +1,10 @@
 // paged_rows.cu -- attention over a paged cache for few rows per key/value head (a decode step,
-// a few drafted tokens): R = 16 MT rows a block, MT in {1, 2}.
+// a few drafted tokens): R = 16 rows a block.
 //
 // The bound is the cache, read once for all rows that share a key head.  Warp 4 copies 64-key
 // tiles of K and V, page by page, into a ring of shared-memory stages with TMA (128-byte
 // swizzle); warps 0-3 compute on them with warp-level tensor-core products (mma.sync m16n8k16):
-// 16 or 32 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
+// 16 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
 // copy (64 keys x 16 rows x 128 dimensions take 128 products of the SM's warps against 1.4 us of copy at the
 // SM's share of HBM).
 //   S = Q K^T   warp w takes keys 16 w .. 16 w + 15 of the tile, all rows;
@@ -27,20 +27,18 @@ namespace {
 
 constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int KT = 64;  // keys a tile
+constexpr int R = 16;   // rows a block
 
-template <int D, int MT>
+template <int D>
 struct Rows {
-    static constexpr int R = 16 * MT;
     static constexpr int kPanels = D / 64;
     static constexpr int kPanelBytes = KT * 128;
     static constexpr int kTile = kPanels * kPanelBytes;  // K or V
-    static constexpr int kBlocks = rows_blocks(D, R);
+    static constexpr int kBlocks = rows_blocks(D);
     static constexpr int kStages = (kBlocks == 3 ? 64 : 96) * 1024 / (2 * kTile);
     static constexpr int kQRow = 2 * D + 16, kPRow = 2 * KT + 16;  // padded: ldmatrix without bank conflicts
     static constexpr int kQOff = kStages * 2 * kTile;
-    // this block's queries and, where there is room, the next one's
-    static constexpr int kQBufs = MT == 2 ? 1 : 2;
-    static constexpr int kPOff = kQOff + kQBufs * R * kQRow;
+    static constexpr int kPOff = kQOff + 2 * R * kQRow;  // this block's queries and the next one's
     static constexpr int kRedOff = kPOff + R * kPRow;    // [4][R] maxima, [4][R] sums
     static constexpr int kCtrlOff = kRedOff + 2 * 4 * R * 4;
 };
@@ -51,20 +49,20 @@ struct Ctrl {
     int abort, last;
 };
 
-template <int D, int MT>
+template <int D>
 constexpr int smem_bytes() {
-    constexpr int n = Rows<D, MT>::kCtrlOff + (int)sizeof(Ctrl) + 1024;
-    static_assert((n + 1024) * Rows<D, MT>::kBlocks <= 228 * 1024, "shared memory of the CTAs an SM holds");
+    constexpr int n = Rows<D>::kCtrlOff + (int)sizeof(Ctrl) + 1024;
+    static_assert((n + 1024) * Rows<D>::kBlocks <= 228 * 1024, "shared memory of the CTAs an SM holds");
     return n;
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
+template <int D>
+__global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
-    using L = Rows<D, MT>;
-    constexpr int R = L::R, NS = L::kStages, DW = D / 4;  // DW: a warp's dimensions of O
+    using L = Rows<D>;
+    constexpr int NS = L::kStages, DW = D / 4;  // DW: a warp's dimensions of O
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + L::kCtrlOff);
@@ -174,31 +172,25 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
         const Walk p = w;
         const int rows = min(R, p.seq.nq * a.G - p.k * R), row0 = p.k * R;
         const uint8_t *sQ = smem + L::kQOff + qb * R * L::kQRow;
-        int lim[MT][2];  // keys < lim are visible to this lane's rows 16 mt + 8 e + g
-        float m[MT][2], l[MT][2], o[MT][DW / 8][4];
+        int lim[2];  // keys < lim are visible to this lane's rows 8 e + g
+        float m[2], l[2], o[DW / 8][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 16 * mt + 8 * e + g;
-                lim[mt][e] = (a.causal && r < rows) ? min(max(p.seq.n - p.seq.nq + div_g(a, row0 + r) + 1, 0), p.seq.n) : p.seq.n;
-                m[mt][e] = -INFINITY;
-                l[mt][e] = 0.f;
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * e + g;
+            lim[e] = (a.causal && r < rows) ? min(max(p.seq.n - p.seq.nq + div_g(a, row0 + r) + 1, 0), p.seq.n) : p.seq.n;
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+        }
         const int lim0 = a.causal ? min(max(p.seq.n - p.seq.nq + div_g(a, row0) + 1, 0), p.seq.n) : p.seq.n;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int nt = 0; nt < DW / 8; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < DW / 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
         cp_async_wait<0>();
         consumer_sync();  // the queries are there; the last piece is done with the other buffer and with sums
         more = w.next(a);
-        if (L::kQBufs == 2) {
-            qb ^= 1;
-            if (more) bring_q(w, qb);
-        }
+        qb ^= 1;
+        if (more) bring_q(w, qb);
 
         for (int j = p.j0; p.keys > 0 && j < p.j1; ++j) {
             const int kv0 = j * KT;
@@ -209,45 +201,38 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
             uint8_t *sK = smem + st * 2 * L::kTile, *sV = sK + L::kTile;
 
             // S of this warp's 16 keys
-            float s[MT][2][4], s2[MT][2][4];  // even and odd k steps: two chains of products
+            float s[2][4], s2[2][4];  // even and odd k steps: two chains of products
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][0][e] = s[mt][1][e] = s2[mt][0][e] = s2[mt][1][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[0][e] = s[1][e] = s2[0][e] = s2[1][e] = 0.f;
             const int krow = 16 * warp + (mi >> 1) * 8 + mr;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 uint32_t kf[4];
                 const int ch = (kk & 3) * 2 + (mi & 1);
                 ldsm_x4(smem_addr(sK + (kk >> 2) * L::kPanelBytes + krow * 128 + ((ch ^ (krow & 7)) << 4)), kf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t qf[4];
-                    ldsm_x4(smem_addr(sQ + (16 * mt + (mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf);
-                    mma_16816((kk & 1 ? s2 : s)[mt][0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
-                    mma_16816((kk & 1 ? s2 : s)[mt][1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
-                }
+                uint32_t qf[4];
+                ldsm_x4(smem_addr(sQ + ((mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf);
+                mma_16816((kk & 1 ? s2 : s)[0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
+                mma_16816((kk & 1 ? s2 : s)[1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
             }
             // scale, mask, row maxima of this warp's keys
             const bool edge = kv0 + KT > lim0;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int e = 0; e < 2; ++e) {
+                float x[4] = {s[0][2 * e] + s2[0][2 * e], s[0][2 * e + 1] + s2[0][2 * e + 1],
+                              s[1][2 * e] + s2[1][2 * e], s[1][2 * e + 1] + s2[1][2 * e + 1]};
+                const int key = kv0 + 16 * warp + 2 * t;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x[4] = {s[mt][0][2 * e] + s2[mt][0][2 * e], s[mt][0][2 * e + 1] + s2[mt][0][2 * e + 1],
-                                  s[mt][1][2 * e] + s2[mt][1][2 * e], s[mt][1][2 * e + 1] + s2[mt][1][2 * e + 1]};
-                    const int key = kv0 + 16 * warp + 2 * t;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[i] *= a.scale_log2;
-                        if (edge && key + (i >> 1) * 8 + (i & 1) >= lim[mt][e]) x[i] = -INFINITY;
-                        s[mt][i >> 1][2 * e + (i & 1)] = x[i];
-                    }
-                    float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    if (t == 0) red[warp * R + 16 * mt + 8 * e + g] = mx;
+                for (int i = 0; i < 4; ++i) {
+                    x[i] *= a.scale_log2;
+                    if (edge && key + (i >> 1) * 8 + (i & 1) >= lim[e]) x[i] = -INFINITY;
+                    s[i >> 1][2 * e + (i & 1)] = x[i];
                 }
+                float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                if (t == 0) red[warp * R + 8 * e + g] = mx;
+            }
             // value rows past the sequence may hold anything: zero, so that 0 * v is 0
             const bool ragged = kv0 + KT > p.seq.n;
             if (ragged)
@@ -257,53 +242,44 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
                         *reinterpret_cast<uint4 *>(sV + panel * L::kPanelBytes + key * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
             consumer_sync();
-            float al[MT][2];
+            float al[2];
             bool moved = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * e + g;
+                const float mn = fmaxf(fmaxf(m[e], fmaxf(red[r], red[R + r])), fmaxf(red[2 * R + r], red[3 * R + r]));
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                al[e] = ptx::ex2(m[e] - ref);
+                moved |= mn != m[e];
+                m[e] = mn;
+                float p[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 16 * mt + 8 * e + g;
-                    const float mn = fmaxf(fmaxf(m[mt][e], fmaxf(red[r], red[R + r])), fmaxf(red[2 * R + r], red[3 * R + r]));
-                    const float ref = mn == -INFINITY ? 0.f : mn;
-                    al[mt][e] = ptx::ex2(m[mt][e] - ref);
-                    moved |= mn != m[mt][e];
-                    m[mt][e] = mn;
-                    float p[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = ptx::ex2(s[mt][i >> 1][2 * e + (i & 1)] - ref);
-                    l[mt][e] = fmaf(al[mt][e], l[mt][e], (p[0] + p[1]) + (p[2] + p[3]));
-                    uint8_t *pr = sP + r * L::kPRow + (16 * warp + 2 * t) * 2;
-                    *reinterpret_cast<uint32_t *>(pr) = pack_bf16(p[0], p[1]);
-                    *reinterpret_cast<uint32_t *>(pr + 16) = pack_bf16(p[2], p[3]);
-                }
+                for (int i = 0; i < 4; ++i) p[i] = ptx::ex2(s[i >> 1][2 * e + (i & 1)] - ref);
+                l[e] = fmaf(al[e], l[e], (p[0] + p[1]) + (p[2] + p[3]));
+                uint8_t *pr = sP + r * L::kPRow + (16 * warp + 2 * t) * 2;
+                *reinterpret_cast<uint32_t *>(pr) = pack_bf16(p[0], p[1]);
+                *reinterpret_cast<uint32_t *>(pr + 16) = pack_bf16(p[2], p[3]);
+            }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int nt = 0; nt < DW / 8; ++nt)
 #pragma unroll
-                    for (int nt = 0; nt < DW / 8; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[mt][nt][e] *= al[mt][e >> 1];
+                    for (int e = 0; e < 4; ++e) o[nt][e] *= al[e >> 1];
             }
             consumer_sync();
             // O of this warp's dimensions
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk) {
-                uint32_t pf[MT][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    ldsm_x4(smem_addr(sP + (16 * mt + (mi & 1) * 8 + mr) * L::kPRow + (2 * kk + (mi >> 1)) * 16), pf[mt]);
+                uint32_t pf[4];
+                ldsm_x4(smem_addr(sP + ((mi & 1) * 8 + mr) * L::kPRow + (2 * kk + (mi >> 1)) * 16), pf);
                 const int vrow = 16 * kk + (mi & 1) * 8 + mr;
 #pragma unroll
                 for (int nt = 0; nt < DW / 16; ++nt) {
                     uint32_t vf[4];
                     const int c = (warp * DW + nt * 16) / 8 + (mi >> 1);
                     ldsm_x4_trans(smem_addr(sV + (c >> 3) * L::kPanelBytes + vrow * 128 + (((c & 7) ^ (vrow & 7)) << 4)), vf);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma_16816(o[mt][2 * nt], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], vf[0], vf[1]);
-                        mma_16816(o[mt][2 * nt + 1], pf[mt][0], pf[mt][1], pf[mt][2], pf[mt][3], vf[2], vf[3]);
-                    }
+                    mma_16816(o[2 * nt], pf[0], pf[1], pf[2], pf[3], vf[0], vf[1]);
+                    mma_16816(o[2 * nt + 1], pf[0], pf[1], pf[2], pf[3], vf[2], vf[3]);
                 }
             }
             if (ragged) ptx::fence_proxy_async_smem();  // the zeros above, before the stage's next copy
@@ -312,53 +288,42 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
             if (++st == NS) { st = 0; ph ^= 1; }
         }
 
-        if (L::kQBufs == 1 && more) bring_q(w, 0);  // every warp is past its last S
-
         // ------------------------------------------------------------ the piece's rows
         // row sums: over the quad, then over the four warps
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v = l[mt][e];
-                v += __shfl_xor_sync(0xffffffffu, v, 1);
-                v += __shfl_xor_sync(0xffffffffu, v, 2);
-                l[mt][e] = v;
-            }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (t == 0) sums[warp * R + 16 * mt + 8 * e + g] = l[mt][e];
+        for (int e = 0; e < 2; ++e) {
+            float v = l[e];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (t == 0) sums[warp * R + 8 * e + g] = v;
+        }
         consumer_sync();
         const bool whole = p.whole();
         const int c0 = whole ? 0 : p.first_share(a);
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * e + g;
+            if (r >= rows) continue;
+            const float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
+            if (whole) {
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
+                __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 16 * mt + 8 * e + g;
-                if (r >= rows) continue;
-                const float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
-                if (whole) {
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
-                    __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
+                for (int nt = 0; nt < DW / 8; ++nt)
+                    *reinterpret_cast<uint32_t *>(orow + 8 * nt) = sum > 0.f ? pack_bf16(o[nt][2 * e] * inv, o[nt][2 * e + 1] * inv) : 0u;
+                if (a.lse && warp == 0 && t == 0)
+                    a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (m[e] + log2f(sum)) * kLn2 : -INFINITY;
+            } else {
+                float *ur = a.u + (slot * R + r) * D + warp * DW + 2 * t;
 #pragma unroll
-                    for (int nt = 0; nt < DW / 8; ++nt)
-                        *reinterpret_cast<uint32_t *>(orow + 8 * nt) = sum > 0.f ? pack_bf16(o[mt][nt][2 * e] * inv, o[mt][nt][2 * e + 1] * inv) : 0u;
-                    if (a.lse && warp == 0 && t == 0)
-                        a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (m[mt][e] + log2f(sum)) * kLn2 : -INFINITY;
-                } else {
-                    float *ur = a.u + (slot * R + r) * D + warp * DW + 2 * t;
-#pragma unroll
-                    for (int nt = 0; nt < DW / 8; ++nt)
-                        *reinterpret_cast<float2 *>(ur + 8 * nt) = make_float2(o[mt][nt][2 * e], o[mt][nt][2 * e + 1]);
-                    if (warp == 0 && t == 0)
-                        *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum > 0.f ? m[mt][e] : -INFINITY, sum);
-                }
+                for (int nt = 0; nt < DW / 8; ++nt)
+                    *reinterpret_cast<float2 *>(ur + 8 * nt) = make_float2(o[nt][2 * e], o[nt][2 * e + 1]);
+                if (warp == 0 && t == 0)
+                    *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum > 0.f ? m[e] : -INFINITY, sum);
             }
+        }
         if (!whole)
             finish_cut(
                 a, a.marks, gridDim.x, blockIdx.x, c0, p.parts(a, c0, p.tiles), threadIdx.x, &ctrl->last,
@@ -376,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, Rows<D, MT>::kBlocks)
     }
 }
 
-template <int D, int MT>
+template <int D>
 attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int grid, cudaStream_t st) {
-    auto kern = paged_rows_kernel<D, MT>;
-    const int smem = smem_bytes<D, MT>();
+    auto kern = paged_rows_kernel<D>;
+    const int smem = smem_bytes<D>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_rows launch: %s", cudaGetErrorString(e));
@@ -388,8 +353,7 @@ attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a
 }  // namespace
 
 attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int d, int grid, cudaStream_t st) {
-    if (d == 64) return a.R == 16 ? launch<64, 1>(mk, mv, a, grid, st) : launch<64, 2>(mk, mv, a, grid, st);
-    return a.R == 16 ? launch<128, 1>(mk, mv, a, grid, st) : launch<128, 2>(mk, mv, a, grid, st);
+    return d == 64 ? launch<64>(mk, mv, a, grid, st) : launch<128>(mk, mv, a, grid, st);
 }
 
 }  // namespace attn
