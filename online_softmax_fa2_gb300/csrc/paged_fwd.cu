@@ -52,7 +52,10 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
-    pl.min_cut = 4;
+    // Tiles that a boundary has to leave at either side of a cut.  128-row tiles: a mixed batch of chunks takes
+    // 77.2 us with 4, 74.9 with 3, 74.6 with 2; 512 tokens over 512 keys 14.4, 14.4, 16.8, over 2048 keys
+    // 33.7, 30.3, 29.2.  Few rows: one decode over 1024 keys takes 17 us with 4, 19 with 8.
+    pl.min_cut = pl.tc ? 3 : 4;
     pl.cuts = pl.grid > 1 && keys > (int64_t)((2 * pl.min_cut - 1) << pl.kt);
     if (!pl.cuts) {  // every block is shorter than two such parts: no states
         pl.off_ml = pl.off_u = pl.bytes = 0;
@@ -145,8 +148,9 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     // 20.7, 19.9 and 24.8.
     a.min_share = pl.tc ? 4 : 8;
     a.min_cut = pl.min_cut;
-    // What a block's beginning and end cost, in tiles (a mixed batch of 244 blocks of 3 to 32 tiles:
-    // 134 us counted as 0, 105 as 2, 97 as 4, 97 as 6; few rows: no difference).
+    // What a block's beginning and end cost, in tiles (128-row tiles: a batch of 244 blocks of 3 to 32
+    // tiles, 134 us counted as 0, 105 as 2, 97 as 4, 97 as 6 at first; now 75, 77 as 5, and one sequence
+    // of 2048 keys, 8 tokens, 17 us as 4, 20 as 3 or 5; few rows: no difference).
     a.cost = 4;
     a.scale_log2 = p.scale * kLog2e;
     a.q = static_cast<const __nv_bfloat16 *>(p.q);
