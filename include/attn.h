@@ -431,8 +431,8 @@ typedef struct {
     float *dwk;
 } attn_qk_norm_rope_bwd_params_t;
 
-/* Bytes of workspace attn_qk_norm_rope_bwd needs (partial weight gradients; 0 for a negative or
- * zero size). */
+/* Bytes of workspace attn_qk_norm_rope_bwd needs on the current device (partial weight gradients; 0
+ * for a negative or zero size). */
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int64_t B, int64_t N, int64_t Hq, int64_t Hkv, int64_t d);
 
 /*
@@ -462,6 +462,7 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t *params
  *                     kv_lens[b] - nq + i).  NULL: every sequence has T / B of them.  Tokens
  *                     before cu_q[0] and from cu_q[B] on belong to no sequence: their outputs are
  *                     left as they were.  Entries outside [0, T] or decreasing set bit 2.
+ * B <= 65535, T < 2^31, table_width * page_size < 2^31.
  */
 typedef struct {
     int32_t dtype;       /* attn_dtype_t */
@@ -511,7 +512,8 @@ typedef struct {
 /*
  * attn_paged_append -- norms and rotates q and k, writes the keys and the values (as they are) to
  * their slots of the cache, and q to q_out, in one pass.  A token whose place kv_lens[b] - nq + i
- * is negative (a place of the batch without a sequence) writes no key or value.
+ * is negative (a place of the batch without a sequence) writes no key or value.  No two tokens of a
+ * call may have the same slot (sequences may share pages that no token of the call is written to).
  * Supported: as attn_qk_norm_rope; any page_size >= 1; B >= 1 when T > 0.  Queues one kernel.
  */
 attn_status_t attn_paged_append(const attn_paged_append_params_t *params, attn_stream_t stream);

@@ -12,6 +12,12 @@
 //   per row; P = exp2(S - m) goes to shared memory in bf16;
 //   O += P V    warp w takes dimensions [w D/4, (w + 1) D/4), all keys and rows.
 // So no state is merged across warps, and a row's accumulator takes D/16 registers a thread.
+//
+// Two CTAs an SM with 96 KB of ring each, three with 64 KB at d = 64.  Measured (d 128, 32/8 heads): 64 ragged
+// sequences to 8192 keys (1.32 GB) 205 us, 6.4 TB/s; one of 131072 keys (537 MB) 93 us, of which the
+// ends of the call (lengths and pages before the first copy, the merge after the last) are about 12;
+// d 64, 16 heads, 32 ragged sequences to 4096 keys x 4 tokens (275 MB) 58 us.  Short sequences pay
+// about 1 us a block beside 0.9 us a tile: 1024 of 64 to 128 keys take 96 us for 80 us of whole pages.
 #include <cudaTypedefs.h>
 
 #include "paged.h"

@@ -321,8 +321,8 @@ __device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
 // one row, the groups of a warp neighbours in it (a warp that kept to one token left most of its
 // lanes idle when there are few heads: 32768 tokens of one query and one key head took 37 us, so 15);
 // first the warps of q, then those of k.  Measured: 24 us for 33.5 M elements in bf16 (B4 N2048 H16
-// d128), 5.7 TB/s; a quarter of the issue slots of the row pass before the two-element instructions
-// and the folded weight, which took 30.
+// d128), 5.7 TB/s, with half of the issue slots used; 30 us before the two-element instructions and the
+// folded weight.
 struct RopeArgs {
     unsigned tokens, warps_q;
     int N, H[2], d, rot, P, per[2];  // units a token

@@ -97,6 +97,7 @@ def _packer(cls):
 _pack_norm_rope, _pack_norm_rope_bwd = _packer(NormRopeParams), _packer(NormRopeBwdParams)
 _pack_append, _pack_fwd = _packer(PagedAppendParams), _packer(PagedFwdParams)
 
+
 class _Block:
     """Argument type of a parameter block: packed bytes, or a mirror."""
     @classmethod
@@ -146,6 +147,14 @@ def _device(q, dim):
     if q.dim() != dim:
         raise ValueError(f"q must be {dim}-D, got {tuple(q.shape)}")
     return dev
+
+
+def _bytes(dev, fn, *args):
+    """Workspace bytes fn(*args) for device number dev (they depend on its multiprocessors)."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _call(dev, fn, *args):
@@ -225,6 +234,7 @@ def attn_qk_norm_rope(q, k, wq=None, wk=None, cos_sin=None, positions=None, eps=
 
 
 def qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d) -> int:
+    """Bytes of workspace attn_qk_norm_rope_bwd needs on the current device (with any weight)."""
     return int(_load().attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d))
 
 
@@ -250,8 +260,8 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, 
     if wk is not None:
         dwk = torch.empty(d, dtype=torch.float32, device=cuda)
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(lib.attn_qk_norm_rope_bwd_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
-                                device=cuda)
+        workspace = torch.empty(_bytes(dev, lib.attn_qk_norm_rope_bwd_workspace_bytes, B, N, Hq, Hkv, d),
+                                dtype=torch.uint8, device=cuda)
     sq, sk = (B, N, Hq, d), (B, N, Hkv, d)
     ptrs = (_need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev), _need(dq, "dq", sq, dt, dev),
             _need(dk, "dk", sk, dt, dev))
@@ -336,7 +346,7 @@ def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, ca
 def paged_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True) -> int:
     """Bytes of workspace attn_paged_fwd needs for these arguments (the lengths' values play no part)."""
     p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, None, None, None)
-    return int(_load().attn_paged_fwd_workspace_bytes(p))
+    return int(_bytes(q.get_device(), _load().attn_paged_fwd_workspace_bytes, p))
 
 
 def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True, scale=None,
@@ -357,7 +367,7 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
     p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse)
     dev = q.get_device()
     if workspace is None:
-        n = lib.attn_paged_fwd_workspace_bytes(p)
+        n = _bytes(dev, lib.attn_paged_fwd_workspace_bytes, p)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     wsp, wsn = _workspace(workspace, dev)
