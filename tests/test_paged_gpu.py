@@ -409,3 +409,67 @@ def test_a_cu_that_goes_back_and_forth_past_every_length_is_reported():
     ofa.attn_paged_fwd(q, kp, kp, bt, lens, cu, max_q=1, causal=False, out=out, lse=lse)
     assert ofa.device_error_flags() == 4
     assert bool((out == 3.0).all()) and bool((lse == 5.0).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page", [(1, 1, 128, 16), (10, 2, 64, 64), (16, 2, 128, 32), (33, 1, 64, 16), (64, 1, 128, 128)])
+def test_every_hint_takes_a_kernel_that_is_right(Hq, Hkv, d, page):
+    # blocks of 16 rows, one tile of 64 or 128 rows, two tiles, whatever the tokens; items cut or whole
+    new, lens = [3, 70, 1, 0, 9, 2], [900, 2500, 6000, 3, 9, 0]
+    s = paged_inputs(new, lens, Hq, Hkv, d, page, seed=41)
+    G = Hq // Hkv
+    for rows in (1, 17, 40, 64, 65, 100, 128, 129, 1000):
+        if rows * 2 <= G:
+            continue
+        for causal in (True, False):
+            o, lse = run(s, causal, max_q=-(-rows // G))
+            check_paged(o, lse, s, new, lens, causal, 1 / math.sqrt(d), f"{rows} rows, causal {causal}")
+    assert ofa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("mq", [1, 8, 16, 40])
+def test_a_hidden_key_or_value_of_any_content_reaches_no_row(mq):
+    # NaN and infinities past the lengths, inside the last page and in pages of other sequences' tails, and
+    # the type's lowest value in keys that are seen: rows stay finite, hidden ones do not count
+    new, lens = [1, 8, 40], [33, 65, 140]
+    s = paged_inputs(new, lens, 8, 1, 128, 64, seed=43)
+    want = run(s, max_q=mq)
+    bad = torch.isnan(s["kp"])
+    for fill in (math.inf, -math.inf, torch.finfo(torch.bfloat16).min):
+        s["kp"][bad] = fill
+        s["vp"][bad] = fill
+        got = run(s, max_q=mq)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_paged(*want, s, new, lens, True, 1 / math.sqrt(128))
+
+
+def test_a_chunk_kernel_captured_with_one_tile_replays_over_a_shared_workspace():
+    a = paged_inputs([8, 3, 5], [3000, 200, 900], 16, 2, 128, 16, seed=51, poison=False)
+    b = paged_inputs([16], [20000], 8, 1, 64, 32, seed=52, poison=False)
+    n = max(ofa.paged_fwd_workspace_bytes(x["q"], x["kp"], x["vp"], x["bt"], x["lens"], x["cu"], max_q=m)
+            for x, m in ((a, 8), (b, 16)))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    calls = [lambda: run(a, max_q=8, workspace=ws), lambda: run(b, max_q=16, workspace=ws)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in calls:
+            c()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    for la, lb in (([3000, 200, 900], 20000), ([9, 200, 1], 17), ([2999, 0, 640], 12345)):
+        a["lens"].copy_(torch.tensor(la, dtype=torch.int32))
+        b["lens"].fill_(lb)
+        for _ in range(2):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in o] for o in outs]
+        for c, o in zip(calls, got):
+            for x, y in zip(c(), o):
+                assert torch.equal(x, y)
+    assert ofa.device_error_flags() == 0
