@@ -131,11 +131,12 @@ _BAD = "{} must be {} {} on cuda:{} with the last dimension contiguous, got {} {
 
 
 def _need(t, name, shape, dtype, dev):
-    """The address of t, checked to be a tensor of that shape and dtype on device number dev with its
-    last dimension contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or t.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(_BAD.format(name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.stride(), t.device))
-    return t.data_ptr()
+    """The address and the strides of t, checked to be a tensor of that shape and dtype on device number
+    dev with its last dimension contiguous."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(_BAD.format(name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), st, t.device))
+    return t.data_ptr(), st
 
 
 def _device(q, dim):
@@ -151,7 +152,7 @@ def _device(q, dim):
 
 def _bytes(dev, fn, *args):
     """Workspace bytes fn(*args) for device number dev (they depend on its multiprocessors)."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
@@ -159,7 +160,7 @@ def _bytes(dev, fn, *args):
 
 def _call(dev, fn, *args):
     """fn(*args, torch's current stream of device number dev) with that device current."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -177,7 +178,7 @@ def _on(stream, q, fn, *args):
 
 
 def _weight(w, name, d, dtype, dev):
-    return 0 if w is None else _need(w, name, (d,), dtype, dev)
+    return 0 if w is None else _need(w, name, (d,), dtype, dev)[0]
 
 
 def _angles(cos_sin, dev):
@@ -187,7 +188,8 @@ def _angles(cos_sin, dev):
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [positions, rot]")
     rows, rot = shape = cos_sin.shape
-    return _need(cos_sin, "cos_sin", shape, torch.float32, dev), rows, cos_sin.stride(0), rot
+    p, st = _need(cos_sin, "cos_sin", shape, torch.float32, dev)
+    return p, rows, st[0], rot
 
 
 def _norm_rope_params(q, k, qo, ko, wq, wk, cos_sin, positions, eps, interleaved):
@@ -196,14 +198,12 @@ def _norm_rope_params(q, k, qo, ko, wq, wk, cos_sin, positions, eps, interleaved
     B, N, Hq, d = shape = q.shape
     Hkv = k.shape[2] if k.dim() == 4 else -1
     kshape = (B, N, Hkv, d)
-    kp, qp = _need(k, "k", kshape, dt, dev), _need(q, "q", shape, dt, dev)
-    q0, q1, q2, _ = q.stride()
-    k0, k1, k2, _ = k.stride()
+    kp, (k0, k1, k2, _) = _need(k, "k", kshape, dt, dev)
+    qp, (q0, q1, q2, _) = _need(q, "q", shape, dt, dev)
     qop = kop = a0 = a1 = a2 = b0 = b1 = b2 = pos = p0 = p1 = 0
     if qo is not None:
-        qop, kop = _need(qo, "q_out", shape, dt, dev), _need(ko, "k_out", kshape, dt, dev)
-        a0, a1, a2, _ = qo.stride()
-        b0, b1, b2, _ = ko.stride()
+        qop, (a0, a1, a2, _) = _need(qo, "q_out", shape, dt, dev)
+        kop, (b0, b1, b2, _) = _need(ko, "k_out", kshape, dt, dev)
     cs, rows, row, rot = _angles(cos_sin, dev)
     if positions is not None:
         if positions.dtype != torch.int32 or positions.get_device() != dev:
@@ -263,9 +263,11 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, cos_sin=None, 
         workspace = torch.empty(_bytes(dev, lib.attn_qk_norm_rope_bwd_workspace_bytes, B, N, Hq, Hkv, d),
                                 dtype=torch.uint8, device=cuda)
     sq, sk = (B, N, Hq, d), (B, N, Hkv, d)
-    ptrs = (_need(dq_out, "dq_out", sq, dt, dev), _need(dk_out, "dk_out", sk, dt, dev), _need(dq, "dq", sq, dt, dev),
-            _need(dk, "dk", sk, dt, dev))
-    p = _pack_norm_rope_bwd(*f, *ptrs, *dq_out.stride()[:3], *dk_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3],
+    dqop, (a0, a1, a2, _) = _need(dq_out, "dq_out", sq, dt, dev)
+    dkop, (b0, b1, b2, _) = _need(dk_out, "dk_out", sk, dt, dev)
+    dqp, (c0, c1, c2, _) = _need(dq, "dq", sq, dt, dev)
+    dkp, (d0, d1, d2, _) = _need(dk, "dk", sk, dt, dev)
+    p = _pack_norm_rope_bwd(*f, dqop, dkop, dqp, dkp, a0, a1, a2, b0, b1, b2, c0, c1, c2, d0, d1, d2,
                             0 if dwq is None else dwq.data_ptr(), 0 if dwk is None else dwk.data_ptr())
     wsp, wsn = _workspace(workspace, dev)
     _call(dev, lib.attn_qk_norm_rope_bwd, p, wsp, wsn)
@@ -285,17 +287,15 @@ def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q):
     if k_pages.dim() != 4 or k_pages.shape[3] != d:
         raise ValueError(f"k_pages must be [num_pages, page_size, Hkv, {d}], got {tuple(k_pages.shape)}")
     pages, page, Hkv, _ = shape = k_pages.shape
-    kp, vp = _need(k_pages, "k_pages", shape, dt, dev), _need(v_pages, "v_pages", shape, dt, dev)
+    kp, (k0, k1, k2, _) = _need(k_pages, "k_pages", shape, dt, dev)
+    vp, (v0, v1, v2, _) = _need(v_pages, "v_pages", shape, dt, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, width]")
     B, width = table = block_table.shape
-    bt = _need(block_table, "block_table", table, torch.int32, dev)
-    lens = _need(kv_lens, "kv_lens", (B,), torch.int32, dev)
-    cu = 0 if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)
-    k0, k1, k2, _ = k_pages.stride()
-    v0, v1, v2, _ = v_pages.stride()
-    return (_DTYPES[dt], page, B, T, Hkv, d, kp, vp, k0, k1, k2, v0, v1, v2, pages, bt, width, block_table.stride(0), lens,
-            cu)
+    bt, (row, _) = _need(block_table, "block_table", table, torch.int32, dev)
+    lens, _ = _need(kv_lens, "kv_lens", (B,), torch.int32, dev)
+    cu = 0 if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)[0]
+    return _DTYPES[dt], page, B, T, Hkv, d, kp, vp, k0, k1, k2, v0, v1, v2, pages, bt, width, row, lens, cu
 
 
 def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None, wq=None, wk=None, cos_sin=None,
@@ -315,10 +315,13 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
     c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
     sk = (T, c[4], d)
     cs, rows, row, rot = _angles(cos_sin, dev)
-    p = _pack_append(*c, Hq, rot, _need(q, "q", shape, dt, dev), _need(k, "k", sk, dt, dev), _need(v, "v", sk, dt, dev),
-                     _need(q_out, "q_out", shape, dt, dev), *q.stride()[:2], *k.stride()[:2], *v.stride()[:2],
-                     *q_out.stride()[:2], _weight(wq, "wq", d, dt, dev), _weight(wk, "wk", d, dt, dev), cs, rows, row,
-                     0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev), eps,
+    qp, (q0, q1, _) = _need(q, "q", shape, dt, dev)
+    kp, (k0, k1, _) = _need(k, "k", sk, dt, dev)
+    vp, (v0, v1, _) = _need(v, "v", sk, dt, dev)
+    op, (o0, o1, _) = _need(q_out, "q_out", shape, dt, dev)
+    p = _pack_append(*c, Hq, rot, qp, kp, vp, op, q0, q1, k0, k1, v0, v1, o0, o1, _weight(wq, "wq", d, dt, dev),
+                     _weight(wk, "wk", d, dt, dev), cs, rows, row,
+                     0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev)[0], eps,
                      1 if interleaved else 0)
     _call(dev, lib.attn_paged_append, p)
     return q_out
@@ -331,16 +334,16 @@ def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, ca
     c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
     lp = op = o0 = o1 = 0
     if out is not None:
-        op, (o0, o1, _) = _need(out, "out", shape, dt, dev), out.stride()
+        op, (o0, o1, _) = _need(out, "out", shape, dt, dev)
     if lse is not None:
-        lp = _need(lse, "lse", (T, Hq), torch.float32, dev)
+        lp, _ = _need(lse, "lse", (T, Hq), torch.float32, dev)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
     if max_q is None:
         max_q = 0 if cu_q is not None else T // c[2] if c[2] else 0
-    q0, q1, _ = q.stride()
+    qp, (q0, q1, _) = _need(q, "q", shape, dt, dev)
     return _pack_fwd(*c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q,
-                     _need(q, "q", shape, dt, dev), op, q0, q1, o0, o1, lp)
+                     qp, op, q0, q1, o0, o1, lp)
 
 
 def paged_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True) -> int:
