@@ -473,3 +473,26 @@ def test_a_chunk_kernel_captured_with_one_tile_replays_over_a_shared_workspace()
             for x, y in zip(c(), o):
                 assert torch.equal(x, y)
     assert ofa.device_error_flags() == 0
+
+
+def test_tile_kernels_of_both_kinds_beside_each_other_and_a_prefill():
+    # one-tile blocks (two CTAs an SM, half the tensor memory each), two-tile blocks and attn_fwd on
+    # three streams at once
+    a = paged_inputs([8, 5, 8], [3000, 700, 2000], 16, 2, 64, 16, seed=61, poison=False)
+    b = paged_inputs([200, 60], [1500, 2900], 8, 2, 128, 32, seed=62, poison=False)
+    q = torch.randn(2, 1024, 8, 128, device=DEV).bfloat16()
+    jobs = [lambda: run(a, max_q=8), lambda: run(b, max_q=200), lambda: ofa.attn_fwd(q, q, q, causal=True)]
+    want = [j() for j in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for st, j, g in zip(streams, jobs, got):
+            with torch.cuda.stream(st):
+                g.append(j())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for x in g:
+            assert torch.equal(x[0], w[0]) and torch.equal(x[1], w[1])
+    assert ofa.device_error_flags() == 0
