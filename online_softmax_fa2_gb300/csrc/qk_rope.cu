@@ -466,15 +466,16 @@ struct RopeBwdArgs {
     uint32_t *flags;
 };
 
-// The rows and angles of a group's next kDepth - 1 units are on their way into shared memory while it
-// works on one: each lane copies the chunks that it will read itself, and waits for nothing but them.
+// The rows and angles of a group's next unit are on their way into shared memory while it works on one: each lane copies the chunks that it will read itself, and waits for nothing but them.
 // (Angles copied once for the groups of a warp that share a token: no faster.)
 // With S1 = sum x^2 and S2 = sum w dt x (one run of shuffles for both),
 //   dw += (r dt) x,   dx = w (r dt) - (r^3 S2 / d) x.
 // What bounds it is the issue of instructions as much as memory: with loads into registers it took
 // 49 us at B4 N2048 H16 d128 in bf16, with eight elements a lane (each row's addresses and shuffles
-// spread over twice the warps) 46, so 38, 5.4 TB/s.
-constexpr int kDepth = 4;
+// spread over twice the warps) 46, so 36, 34.8 with the sums below (5.8 TB/s).  Two units in shared memory and four blocks an SM:
+// four units and two blocks, as many bytes on their way, took 37.5 with half as many warps to issue from,
+// three and three 36.0.
+constexpr int kDepth = 2, kBwdBlocks = 4;
 
 template <int U, int C>
 struct BwdStage {
@@ -717,31 +718,37 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
     }
 }
 
-// dw[s][c] = the sum of the partials of tensor s: a block takes 32 columns of one tensor, its 8
-// warps every eighth partial.
-__global__ void __launch_bounds__(256) bwd_weight_kernel(const float *part, int nb0, int nb1, int d, float *dwq,
+// dw[s][c] = the sum of the partials of tensor s: a block takes 32 columns of one tensor, its 32
+// warps every 32nd partial, eight loads in flight (its time is their latency).
+constexpr int kWeightWarps = 32, kWeightLoads = 8;
+__global__ void __launch_bounds__(32 * kWeightWarps) bwd_weight_kernel(const float *part, int nb0, int nb1, int d, float *dwq,
                                                          float *dwk) {
-    __shared__ float red[8][33];
+    __shared__ float red[kWeightWarps][33];
     ptx::grid_dep_wait();
     ptx::launch_dependents();
     const int s = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     float *dst = s ? dwk : dwq;
     if (!dst) return;
     const int lo = s ? nb0 : 0, hi = s ? nb0 + nb1 : nb0;
-    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
     if (c < d) {
-        int i = lo + w;
-        for (; i + 24 < hi; i += 32)
+        for (int i = lo + w; i < hi; i += kWeightWarps * kWeightLoads) {
+            float t[kWeightLoads];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) t[k] += part[(long long)(i + 8 * k) * d + c];
-        for (; i < hi; i += 8) t[0] += part[(long long)i * d + c];
+            for (int k = 0; k < kWeightLoads; ++k) {
+                const int at = i + kWeightWarps * k;
+                t[k] = at < hi ? part[(long long)at * d + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kWeightLoads; ++k) sum += t[k];
+        }
     }
-    red[w][threadIdx.x & 31] = (t[0] + t[1]) + (t[2] + t[3]);
+    red[w][threadIdx.x & 31] = sum;
     __syncthreads();
     if (w == 0 && c < d) {
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v += red[k][threadIdx.x];
+        for (int k = 0; k < kWeightWarps; ++k) v += red[k][threadIdx.x];
         dst[c] = v;
     }
 }
@@ -761,7 +768,7 @@ attn_status_t launched(cudaError_t e, const char *what) {
 
 }  // namespace
 
-int rope_bwd_blocks() { return 2 * (sm_count() ? sm_count() : 152); }
+int rope_bwd_blocks() { return kBwdBlocks * (sm_count() ? sm_count() : 152); }
 
 namespace {
 
@@ -853,7 +860,7 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
         if (units > 0x70000000LL) return fail(ATTN_ERR_UNSUPPORTED, "B * N * (Hq + Hkv) is too large");
         a.units[s] = (unsigned)units;
     }
-    // two blocks an SM (what shared memory holds), each tensor's share by its units; never more blocks
+    // what an SM's shared memory holds of blocks, each tensor's share by its units; never more blocks
     // than warps of work
     const int most = rope_bwd_blocks();
     a.nb[0] = (int)((long long)most * a.per[0] / (a.per[0] + a.per[1]));
@@ -868,7 +875,7 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
     if (e == cudaSuccess) e = launch_pdl(pick.kern, dim3(blocks), dim3(kThreads), pick.smem, st, a);
     const attn_status_t r = launched(e, "qk_norm_rope_bwd");
     if (r || (!bp.dwq && !bp.dwk)) return r;
-    return launched(launch_pdl(bwd_weight_kernel, dim3((unsigned)((p.d + 31) / 32), 2), dim3(256), 0, st,
+    return launched(launch_pdl(bwd_weight_kernel, dim3((unsigned)((p.d + 31) / 32), 2), dim3(32 * kWeightWarps), 0, st,
                                (const float *)part, a.nb[0], a.nb[1], (int)p.d, bp.dwq, bp.dwk),
                     "qk_norm_rope_bwd weights");
 }
