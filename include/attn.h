@@ -461,7 +461,9 @@ attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t *params
  *                     packed tokens are sequence b's newest (token i of its nq lies at position
  *                     kv_lens[b] - nq + i).  NULL: every sequence has T / B of them.  Tokens
  *                     before cu_q[0] and from cu_q[B] on belong to no sequence: their outputs are
- *                     left as they were.  Entries outside [0, T] or decreasing set bit 2.
+ *                     left as they were.  Entries outside [0, T] or decreasing set bit 2 and are
+ *                     clamped (to [0, T], and to the entry before); a token that two sequences claim
+ *                     then, or none, has no outputs that can be relied on.
  * B <= 65535, T < 2^31, table_width * page_size < 2^31.
  */
 typedef struct {

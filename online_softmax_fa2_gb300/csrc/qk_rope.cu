@@ -380,6 +380,7 @@ struct AppendArgs {
     long long cs_row;
     const int *pos, *bt, *lens, *cu;
     long long bt_s;
+    unsigned cu_groups, cu_step;  // groups of 32 sequences, and the warps that look at their entries of cu
     int pages, page_size, width;
     uint32_t *flags;
 };
@@ -395,16 +396,20 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const bool report = part == 0 && (threadIdx.x & 31) == 0;
     int b, i, nq;
     if (a.cu) {
+        // Entries that are out of range or decrease are reported whatever tokens they belong to: the
+        // first warps of the grid look at 32 of them each.
+        for (unsigned e = task; e < a.cu_groups; e += a.cu_step) {
+            const int at = min((int)e * 32 + (threadIdx.x & 31), a.B - 1);
+            const int r0 = __ldg(a.cu + at), r1 = __ldg(a.cu + at + 1);
+            if (r0 < 0 || r1 < r0 || r1 > a.T) atomicOr(a.flags, kFlagBadIndex);
+        }
         b = find_sequence(a.cu, a.B, t);
         if (b >= a.B) return;  // behind the last sequence: left as it was
-        const int c0 = __ldg(a.cu + b);
-        nq = __ldg(a.cu + b + 1) - c0;
+        // the sequence's tokens as the attention takes them (seq_info of paged_sched.cuh)
+        const int c0 = min(max(__ldg(a.cu + b), 0), a.T);
+        nq = min(max(__ldg(a.cu + b + 1), c0), a.T) - c0;
         i = t - c0;
-        if (i < 0) return;  // before the first sequence: left as it was
-        if (i >= nq) {      // cu_q decreases somewhere
-            if (report) atomicOr(a.flags, kFlagBadIndex);
-            return;
-        }
+        if (i < 0 || i >= nq) return;  // before the first sequence, or cu_q decreases: left as it was
     } else {
         nq = a.T / a.B;
         b = t / nq;
@@ -901,6 +906,8 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     a.ck = (int)((c.Hkv + n - 1) / n);
     a.tasks = c.T * (a.cq + 2 * a.ck);
     if (a.tasks > 0xfffffff0LL) return fail(ATTN_ERR_UNSUPPORTED, "T * (Hq + 2 Hkv) is too large");
+    a.cu_groups = (unsigned)((a.B + 31) / 32);
+    a.cu_step = a.tasks < a.cu_groups ? (unsigned)a.tasks : a.cu_groups;
     const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
     auto kern = p.interleaved ? (h ? append_kernel<__nv_bfloat16, true>(L, U) : append_kernel<float, true>(L, U))
                               : (h ? append_kernel<__nv_bfloat16, false>(L, U) : append_kernel<float, false>(L, U));

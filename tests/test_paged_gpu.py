@@ -496,3 +496,29 @@ def test_tile_kernels_of_both_kinds_beside_each_other_and_a_prefill():
         for x in g:
             assert torch.equal(x[0], w[0]) and torch.equal(x[1], w[1])
     assert ofa.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("cu,ok", [([0, 4, 2, 6], False), ([0, 9, 9, 9], False), ([-5, 2, 3, 6], False), ([6, 4, 2, 0], False),
+                                   ([0, 2, 4, 7], False), ([2, 3, 4, 5], True)])
+def test_a_malformed_cu_is_reported_and_clamped(cu, ok):
+    lens, T = [20, 30, 17], 6
+    s = paged_inputs([2, 2, 2], lens, 2, 1, 64, 16)
+    c = [min(max(x, 0), T) for x in cu]
+    claims = [(b, t) for b in range(3) for t in range(c[b], max(c[b + 1], c[b]))]
+    for mq in (0, 2, 64):
+        out, lse = torch.full_like(s["q"], 3.0), torch.full((T, 2), 5.0, device=DEV)
+        ofa.device_error_flags()
+        ofa.attn_paged_fwd(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], torch.tensor(cu, dtype=torch.int32, device=DEV),
+                           max_q=mq, out=out, lse=lse)
+        assert ofa.device_error_flags() == (0 if ok else 4)
+        for t in range(T):
+            of = [b for b, u in claims if u == t]
+            if not of:
+                assert bool((out[t] == 3.0).all()) and bool((lse[t] == 5.0).all())
+            if len(of) == 1:  # the row of a batch of that sequence's clamped tokens alone
+                b = of[0]
+                sub = dict(s, q=s["q"][c[b]:c[b + 1]], bt=s["bt"][b:b + 1], lens=s["lens"][b:b + 1],
+                           cu=torch.tensor([0, c[b + 1] - c[b]], dtype=torch.int32, device=DEV))
+                o1, l1 = run(sub, max_q=mq)
+                check_paged(o1, l1, sub, [c[b + 1] - c[b]], [lens[b]], True, 1 / 8)
+                assert torch.equal(out[t], o1[t - c[b]]) and torch.equal(lse[t], l1[t - c[b]])

@@ -222,3 +222,59 @@ def test_append_survives_a_malformed_cu(cu):
     ofa.attn_paged_append(s["q"], k, v, s["kp"], s["vp"], s["bt"], s["lens"], torch.tensor(cu, dtype=torch.int32, device=DEV))
     torch.cuda.synchronize()
     ofa.device_error_flags()
+
+
+@pytest.mark.parametrize("cu,places", [  # places: (sequence, token, place) of the tokens that one sequence has
+    ([0, 9, 9, 9], [(0, t, 14 + t) for t in range(6)]),
+    ([-5, 2, 3, 6], [(0, 0, 18), (0, 1, 19), (1, 2, 29), (2, 3, 14), (2, 4, 15), (2, 5, 16)]),
+    ([0, 4, 2, 6], [(0, 0, 16), (0, 1, 17), (2, 4, 15), (2, 5, 16)]),
+    ([6, 4, 2, 0], []),
+    ([3, 1, 6, 6], [(1, t, 24 + t) for t in range(1, 6)]),
+    ([0, 2, 4, 7], [(0, 0, 18), (0, 1, 19), (1, 2, 28), (1, 3, 29), (2, 4, 15), (2, 5, 16)]),
+    ([2, 3, 4, 5], [(0, 2, 19), (1, 3, 29), (2, 4, 16)]),
+])
+def test_append_places_tokens_of_a_malformed_cu_as_the_attention_does_and_reports_it(cu, places):
+    T, lens = 6, [20, 30, 17]
+    s = paged_inputs([2, 2, 2], lens, 2, 1, 64, 16, poison=False)
+    k, v = draw(2, T, 1, 64), draw(3, T, 1, 64)
+    kp, vp, bt = s["kp"].clone(), s["vp"].clone(), s["bt"].cpu()
+    for b, t, at in places:
+        kp[bt[b, at // 16], at % 16], vp[bt[b, at // 16], at % 16] = k[t], v[t]
+    out = torch.full_like(s["q"], 7.0)
+    ofa.device_error_flags()
+    ofa.attn_paged_append(s["q"], k, v, s["kp"], s["vp"], s["bt"], s["lens"],
+                          torch.tensor(cu, dtype=torch.int32, device=DEV), q_out=out)
+    assert ofa.device_error_flags() == (0 if cu == [2, 3, 4, 5] else 4)
+    # what the attention's sequences (c0 = cu[b], c1 = max(cu[b + 1], c0), in [0, T]) do not hold stays
+    c = [min(max(x, 0), T) for x in cu]
+    owned, claimed = set(), set()
+    for b in range(3):
+        nq = max(c[b + 1], c[b]) - c[b]
+        claimed |= set(range(c[b], c[b] + nq))
+        owned |= {(int(bt[b, p // 16]), p % 16) for p in range(max(lens[b] - nq, 0), lens[b])}
+    sure = {(int(bt[b, at // 16]), at % 16) for b, _, at in places}
+    for page in range(kp.shape[0]):
+        for slot in range(16):
+            if (page, slot) in sure or (page, slot) not in owned:
+                assert torch.equal(s["kp"][page, slot], kp[page, slot]) and torch.equal(s["vp"][page, slot], vp[page, slot])
+    for _, t, _ in places:
+        assert torch.equal(out[t], s["q"][t])
+    for t in range(T):
+        if t not in claimed:
+            assert bool((out[t] == 7.0).all())
+
+
+@pytest.mark.parametrize("B,at", [(3, 1), (40, 39), (5000, 4097)])
+def test_append_reports_a_bad_cu_entry_wherever_it_stands(B, at):
+    # one token in the first sequence, the others empty; one entry behind it out of range, negative or falling back
+    s = paged_inputs([1], [5], 2, 1, 64, 16, poison=False)
+    k = draw(2, 1, 1, 64)
+    bt, lens = s["bt"].repeat(B, 1), s["lens"].repeat(B)
+    cu = torch.ones(B + 1, dtype=torch.int32)
+    cu[0] = 0
+    for bad in (None, 2, -1, 0, 2 ** 31 - 1, -2 ** 31):
+        c = cu.clone()
+        if bad is not None:
+            c[at + 1] = bad
+        ofa.attn_paged_append(s["q"], k, k, s["kp"], s["vp"], bt, lens, c.to(DEV))
+        assert ofa.device_error_flags() == (0 if bad is None else 4), bad
