@@ -552,6 +552,8 @@ size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
  * their states (m, l, u), in a fixed order: the same bits from run to run (another max_q may take
  * another kernel, and give other last bits).  The weights are rounded to bf16 before the value
  * product, as in attn_fwd; sums and states are fp32.
+ * A row that sees no key, or only keys of logit -inf, has o = +0.0 and lse = -inf.  A NaN in a query or in
+ * a visible key, and a logit of +inf, make o and lse of the rows that see them NaN, and of no others.
  * Values at positions >= kv_lens[b] are never used, whatever lies there.  A visible value that is
  * infinite or NaN reaches every query row of its tile, as 0 * inf does in a product.
  * workspace: caller-owned device memory, 16-byte aligned, of any contents on entry; calls that

@@ -142,11 +142,12 @@ __device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int 
                 __nv_bfloat16 *orow;
                 float *lse;
                 out(r, orow, lse);
-                const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
+                const bool empty = sum[u] == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
+                const float inv = empty ? 0.f : 1.f / sum[u];
                 uint32_t *o32 = reinterpret_cast<uint32_t *>(orow + C * lane);
 #pragma unroll
-                for (int e = 0; e < C; e += 2) o32[e / 2] = sum[u] > 0.f ? ptx::pack_bf16x2(v[u][e] * inv, v[u][e + 1] * inv) : 0u;
-                if (lse && lane == 0) *lse = sum[u] > 0.f ? (M[u] + log2f(sum[u])) * kLn2 : -INFINITY;
+                for (int e = 0; e < C; e += 2) o32[e / 2] = empty ? 0u : ptx::pack_bf16x2(v[u][e] * inv, v[u][e + 1] * inv);
+                if (lse && lane == 0) *lse = empty ? -INFINITY : (M[u] + log2f(sum[u])) * kLn2;
             }
         }
     }

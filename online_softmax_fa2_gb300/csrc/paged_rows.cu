@@ -313,21 +313,22 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (r >= rows) continue;
             const float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             if (whole) {
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
+                const float inv = empty ? 0.f : 1.f / sum;
                 const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                 __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
 #pragma unroll
                 for (int nt = 0; nt < DW / 8; ++nt)
-                    *reinterpret_cast<uint32_t *>(orow + 8 * nt) = sum > 0.f ? pack_bf16(o[nt][2 * e] * inv, o[nt][2 * e + 1] * inv) : 0u;
+                    *reinterpret_cast<uint32_t *>(orow + 8 * nt) = empty ? 0u : pack_bf16(o[nt][2 * e] * inv, o[nt][2 * e + 1] * inv);
                 if (a.lse && warp == 0 && t == 0)
-                    a.lse[(long long)tok * a.Hq + h] = sum > 0.f ? (m[e] + log2f(sum)) * kLn2 : -INFINITY;
+                    a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m[e] + log2f(sum)) * kLn2;
             } else {
                 float *ur = a.u + (slot * R + r) * D + warp * DW + 2 * t;
 #pragma unroll
                 for (int nt = 0; nt < DW / 8; ++nt)
                     *reinterpret_cast<float2 *>(ur + 8 * nt) = make_float2(o[nt][2 * e], o[nt][2 * e + 1]);
                 if (warp == 0 && t == 0)
-                    *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum > 0.f ? m[e] : -INFINITY, sum);
+                    *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(sum == 0.f ? -INFINITY : m[e], sum);
             }
         }
         if (!whole)

@@ -190,7 +190,7 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float alpha) {
 template <int D>
 __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, __nv_bfloat16 *orow, float *lse) {
     const int lane = threadIdx.x & 31, i = lane & 3;
-    const bool empty = !(l_run > 0.f), b0 = i & 1, b1 = i & 2;
+    const bool empty = l_run == 0.f, b0 = i & 1, b1 = i & 2;  // a NaN is no empty row
     const float inv = empty ? 0.f : 1.f / l_run;
     uint4 *to[4];  // the quad's rows
 #pragma unroll
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             }
             // the state of this part, for paged_tc_merge_kernel
             const int slot = paged::state_slot(blockIdx.x, c0);
-            *state_ml<NT>(a, slot, X, r) = make_float2(l_run > 0.f ? m_run : -INFINITY, l_run);
+            *state_ml<NT>(a, slot, X, r) = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
             float4 *u4 = state_u<D, NT>(a, slot, X, r);
 #pragma unroll 1
             for (int cc = 0; cc < D / 32; ++cc) {
@@ -651,7 +651,8 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
         }
     }
     if (g > 0 || !mine) return;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
+    const float inv = empty ? 0.f : 1.f / sum;
     const int tok = paged::div_g(a, row), h = c1.y * a.G + row - tok * a.G;
     const long long t0 = c1.x + tok;
     uint4 *o4 = reinterpret_cast<uint4 *>(a.o + t0 * a.os0 + h * a.os1 + col);
@@ -659,10 +660,10 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     for (int t = 0; t < kMergeCols / 8; ++t) {
         uint32_t pk[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pk[e] = sum > 0.f ? ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv) : 0u;
+        for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv);
         o4[t] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     }
-    if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = sum > 0.f ? (M + log2f(sum)) * kLn2 : -INFINITY;
+    if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
 template <int D, int NT, int QR>

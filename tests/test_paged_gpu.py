@@ -522,3 +522,54 @@ def test_a_malformed_cu_is_reported_and_clamped(cu, ok):
                 o1, l1 = run(sub, max_q=mq)
                 check_paged(o1, l1, sub, [c[b + 1] - c[b]], [lens[b]], True, 1 / 8)
                 assert torch.equal(out[t], o1[t - c[b]]) and torch.equal(lse[t], l1[t - c[b]])
+
+
+@pytest.mark.parametrize("mq", [1, 12, 30, 150])  # the warp-level kernel, one tile of 64 or 128 rows, two tiles
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_nan_reaches_the_rows_that_see_it_and_no_others(mq, d, page, causal):
+    # sequences whose blocks are cut into parts (9000 keys) and one whose block is whole (100)
+    new, lens, Hq, Hkv = [2, 150, 1, 3], [700, 900, 9000, 100], 8, 2
+    G, starts = Hq // Hkv, [0, 2, 152, 153]
+    s = paged_inputs(new, lens, Hq, Hkv, d, page, seed=71)
+    for j in range(-(-100 // page)):
+        s["kp"][s["bt"][3, j].long(), :, 0, 0] = 1.0  # (sequence 3, key head 0: -inf logits for a query that starts with -inf)
+    clean = run(s, causal, max_q=mq)
+    check_paged(*clean, s, new, lens, causal, 1 / math.sqrt(d))
+    nan = torch.zeros(sum(new), Hq, dtype=torch.bool)
+    q, kp = s["q"].clone(), s["kp"].clone()
+    for t, h, at, v in ((1, 3, 5, math.nan), (60, 7, 0, math.nan), (100, 2, d - 1, math.inf), (152, 6, 17, math.nan),
+                        (154, 4, 3, math.nan)):
+        q[t, h, at] = v
+        nan[t, h] = True
+    for b, j, hk, v in ((0, 333, 0, math.nan), (1, 820, 1, math.nan), (2, 8999, 0, math.inf), (3, 98, 1, -math.inf),
+                        (3, 99, 1, math.nan)):
+        kp[s["bt"][b, j // page].long(), j % page, hk, 9] = v
+        for i in range(new[b]):
+            if not causal or j <= i + lens[b] - new[b]:
+                rows = slice(hk * G, (hk + 1) * G)
+                if v == v:  # an infinite key: logits of +inf where the query's element has its sign
+                    nan[starts[b] + i, rows] |= (q[starts[b] + i, rows, 9].cpu() * v) > 0
+                else:
+                    nan[starts[b] + i, rows] = True
+    q[153, 1, 0] = -math.inf
+    for kind in ("queries", "keys", "both"):
+        x = dict(s, q=s["q"] if kind == "keys" else q, kp=s["kp"] if kind == "queries" else kp)
+        o, lse = run(x, causal, max_q=mq)
+        assert ofa.device_error_flags() == 0
+        if kind == "both":
+            hit = torch.isnan(lse).cpu()
+            assert torch.equal(hit, nan) and torch.equal(torch.isnan(o).all(-1).cpu(), nan)
+            assert torch.equal(torch.isnan(o).any(-1).cpu(), nan)
+            assert bool((o[153, 1].view(torch.int16) == 0).all()) and float(lse[153, 1]) == -math.inf
+        else:
+            hit = torch.isnan(lse).cpu()
+            assert bool(hit.any()) and not bool((hit & ~nan).any()) and torch.equal(hit, torch.isnan(o).any(-1).cpu())
+        same = ~nan.clone()
+        same[153, 1] = False
+        if kind != "queries":
+            # an infinite key whose logit is -inf leaves a row with one key less
+            for b, j, hk in ((2, 8999, 0), (3, 98, 1)):
+                for i in range(new[b]):
+                    same[starts[b] + i, hk * G:(hk + 1) * G] = False
+        assert torch.equal(o.cpu()[same], clean[0].cpu()[same]) and torch.equal(lse.cpu()[same], clean[1].cpu()[same])
