@@ -124,6 +124,9 @@ attn_status_t check_paged_fwd(const attn_paged_fwd_params_t *p) {
     if (p->Hq / c.Hkv > 64) return fail(ATTN_ERR_UNSUPPORTED, "Hq / Hkv must be <= 64 (got %lld)", (long long)(p->Hq / c.Hkv));
     if (c.T > (1 << 30) / (p->Hq / c.Hkv)) return fail(ATTN_ERR_UNSUPPORTED, "T * Hq / Hkv must be at most 2^30");
     if (p->max_q < 0) return fail(ATTN_ERR_INVALID_ARG, "max_q is negative");
+    // the last tile's end, past the keys by up to 127, stays an int
+    if (c.table_width > 0 && c.table_width > (INT32_MAX - 255) / c.page_size)
+        return fail(ATTN_ERR_UNSUPPORTED, "table_width * page_size must be at most 2^31 - 256");
     return ATTN_OK;
 }
 

@@ -187,6 +187,17 @@ def test_workspace_of_invalid_or_overlong_arguments_is_none(lib):
     assert need(max_q=2, cache_table_width=1024) == need(max_q=(1 << 63) - 1, cache_table_width=1024) > 0
 
 
+@pytest.mark.parametrize("page,width,fits", [(16, (1 << 27) - 16, True), (16, (1 << 27) - 15, False), (16, (1 << 27) - 1, False),
+                                             (256, (1 << 23) - 1, True), (128, (1 << 24) - 1, False), (1 << 30, 1, True)])
+def test_a_table_whose_last_tile_ends_past_an_int_is_refused(lib, page, width, fits):
+    # the tile that holds key 2^31 - 17 ends at 2^31
+    kw = dict(cache_page_size=page, cache_table_width=width, cache_table_stride=width)
+    assert (lib.attn_paged_fwd_workspace_bytes(fwd(**kw)) > 0) == fits
+    if not fits:
+        assert lib.attn_paged_fwd(fwd(**kw), 0x10000, 1 << 40, None) == S.UNSUPPORTED
+        assert "table_width" in ofa.last_error()
+
+
 def test_python_refusals_without_a_gpu():
     x = torch.zeros(1, 2, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

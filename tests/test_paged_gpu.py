@@ -573,3 +573,31 @@ def test_a_nan_reaches_the_rows_that_see_it_and_no_others(mq, d, page, causal):
                 for i in range(new[b]):
                     same[starts[b] + i, hk * G:(hk + 1) * G] = False
         assert torch.equal(o.cpu()[same], clean[0].cpu()[same]) and torch.equal(lse.cpu()[same], clean[1].cpu()[same])
+
+
+@pytest.mark.parametrize("nq", [1, 20])  # the warp-level kernel and the tiles
+def test_the_longest_table(nq):
+    # 2^31 - 261 keys in a table of 2^31 - 256: 8 pages of 256 keys, each a million times
+    d, page, width, pages = 64, 256, (1 << 23) - 1, 8
+    n = width * page - 5
+    g = torch.Generator().manual_seed(81)
+    q = torch.randn(nq, 1, d, generator=g).bfloat16()
+    kp, vp = (torch.randn(pages, page, 1, d, generator=g).bfloat16() for _ in range(2))
+    vp += 2.0  # (outputs near 2, so that a relative bound says something)
+    bt = torch.arange(width, dtype=torch.int32) % pages
+    count = bt.bincount(minlength=pages).double()[:, None].expand(pages, page).clone()
+    count[bt[-1], -5:] -= 1
+    o, lse = ofa.attn_paged_fwd(q.to(DEV), kp.to(DEV), vp.to(DEV), bt[None].to(DEV),
+                                torch.tensor([n], dtype=torch.int32, device=DEV), causal=False)
+    assert ofa.device_error_flags() == 0
+    X = q[:, 0].double() @ kp.reshape(-1, d).double().T / 8 + count.reshape(-1).log()
+    L = torch.logsumexp(X, -1)
+    V = vp.reshape(-1, d).double()
+    P = torch.exp(X - L[:, None])
+    # A CTA's share is at most 2^31 / 152 keys, in tiles of 64 or 128: its row sums are chains of as many
+    # fp32 additions of half a step of 2^-24 as it has tiles (and 20 in a tile), its accumulator's of one
+    # a 16 keys, which a tensor core may cut off instead of rounding (a whole step, 2^-23).
+    tiles, steps = 2 ** 31 / 152 / 64 + 20, 2 ** 31 / 152 / 16
+    assert float((lse[:, 0].cpu().double() - L).abs().max()) <= tiles * 2.0 ** -24 + 2.0 ** -18 * (1 + float(L.max()))
+    err = (o[:, 0].cpu().double() - P @ V).abs()
+    assert bool((err <= (2 * 2.0 ** -8 + tiles * 2.0 ** -24 + steps * 2.0 ** -23) * (P @ V.abs())).all())
