@@ -284,7 +284,7 @@ struct Walk {
     // the share that holds the first part of the item, and the parts that its first n tiles fall
     // into: the boundaries c per that lie min_cut tiles or more inside the item
     __device__ __forceinline__ int first_share(const Args &a) const {
-        return (int)((unsigned)(t + a.cost + a.min_cut + per - 1) / (unsigned)per) - 1;
+        return (int)(((unsigned)t + (unsigned)(a.cost + a.min_cut + per - 1)) / (unsigned)per) - 1;  // (past 2^31 on the longest lines)
     }
     __device__ __forceinline__ int parts(const Args &a, int c0, int n) const {
         const int last = min(tiles - a.min_cut, n - 1);  // no boundary behind this tile counts
