@@ -257,10 +257,13 @@ __device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, l
             scale8(y, y, r);
             scale8(y + 8, y + 8, r);
         }
+        // (times sine 0 an infinite element would make a NaN of the one that it is held beside)
         mul8(z, y + 8, bs);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) z[t] = ln.turn ? z[t] : -0.f;
         fma8(z, y, ac, z);
         mul8(z + 8, y + 8, bc);
-        fma8(z + 8, y, as, z + 8);
+        if (ln.turn) fma8(z + 8, y, as, z + 8);
         together<kInter>(z, f);
         if (ln.on && u < count) {
             x[u].set(f);
@@ -658,13 +661,18 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeBw
             unpack(st.rows[u][1][1][threadIdx.x], f + C, T{});
             apart_c<kInter, C>(f, y);
             // g = R^T dy: g_a = dy_a cos + dy_b sin, g_b = dy_b cos - dy_a sin
+            if (turn) {
 #pragma unroll
-            for (int t = 0; t < C; t += 2) {
-                float q0, q1;
-                mul2(g[t], g[t + 1], y[C + t], y[C + 1 + t], si[t], si[t + 1]);
-                ptx::fma2(g[t], g[t + 1], y[t], y[t + 1], co[t], co[t + 1], g[t], g[t + 1]);
-                mul2(q0, q1, y[t], y[t + 1], -si[t], -si[t + 1]);
-                ptx::fma2(g[C + t], g[C + 1 + t], y[C + t], y[C + 1 + t], co[t], co[t + 1], q0, q1);
+                for (int t = 0; t < C; t += 2) {
+                    float q0, q1;
+                    mul2(g[t], g[t + 1], y[C + t], y[C + 1 + t], si[t], si[t + 1]);
+                    ptx::fma2(g[t], g[t + 1], y[t], y[t + 1], co[t], co[t + 1], g[t], g[t + 1]);
+                    mul2(q0, q1, y[t], y[t + 1], -si[t], -si[t + 1]);
+                    ptx::fma2(g[C + t], g[C + 1 + t], y[C + t], y[C + 1 + t], co[t], co[t + 1], q0, q1);
+                }
+            } else {  // (no products with sine 0: an infinite element would reach the one that it is held beside)
+#pragma unroll
+                for (int t = 0; t < E; ++t) g[t] = y[t];
             }
             if (w) {
                 unpack(st.rows[u][0][0][threadIdx.x], f, T{});

@@ -278,3 +278,53 @@ def test_append_reports_a_bad_cu_entry_wherever_it_stands(B, at):
             c[at + 1] = bad
         ofa.attn_paged_append(s["q"], k, k, s["kp"], s["vp"], bt, lens, c.to(DEV))
         assert ofa.device_error_flags() == (0 if bad is None else 4), bad
+
+
+def bits(t):
+    return t.view(torch.int16 if t.dtype is torch.bfloat16 else torch.int32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rot,inter", [(64, 32, False), (128, 64, True), (192, 64, False), (112, 16, True), (256, 0, False)])
+def test_what_is_not_rotated_reaches_no_other_element(d, rot, inter, dtype):
+    # infinities, NaN and negative zeros in the dimensions behind the rotated ones
+    B, N, H = 2, 19, 3
+    x = draw(1, B, N, H, d, dtype=dtype)
+    cs = angles(N, rot).to(DEV) if rot else None
+    want, _ = ofa.attn_qk_norm_rope(x, x, None, None, cs, interleaved=inter)
+    assert torch.equal(bits(want[..., rot:]), bits(x[..., rot:]))
+    g = torch.Generator().manual_seed(7)
+    bad = torch.rand(B, N, H, d, generator=g) < 0.1
+    bad[..., :rot] = False
+    bad = bad.to(DEV)
+    for v in (math.inf, -math.inf, math.nan, -0.0):
+        y = x.masked_fill(bad, v)
+        for got in ofa.attn_qk_norm_rope(y, y, None, None, cs, interleaved=inter):
+            assert torch.equal(bits(got[~bad]), bits(want[~bad])), v
+            assert bool(torch.isnan(got[bad]).all()) if v != v else torch.equal(bits(got[bad]), bits(y[bad])), v
+        back = ofa.attn_qk_norm_rope_bwd(x, x, y, y, None, None, cs, interleaved=inter)[1]
+        clean = ofa.attn_qk_norm_rope_bwd(x, x, x, x, None, None, cs, interleaved=inter)[1]
+        assert torch.equal(bits(back[~bad]), bits(clean[~bad])), v
+        assert bool(torch.isnan(back[bad]).all()) if v != v else torch.equal(bits(back[bad]), bits(y[bad])), v
+    # with a norm the root of an infinite mean is 0: 0 for every finite element, NaN for the infinite one alone
+    w = (1 + 0.3 * draw(3, d, dtype=torch.float32)).to(dtype)
+    y = x.clone()
+    y[0, 4, 1, d - 3] = math.inf
+    got, _ = ofa.attn_qk_norm_rope(y, y, w, w, cs, eps=EPS, interleaved=inter)
+    hit = torch.zeros_like(bad)
+    hit[0, 4, 1, d - 3] = True
+    assert torch.equal(torch.isnan(got), hit)
+    row = got[0, 4, 1]
+    assert bool((row[~hit[0, 4, 1]] == 0).all())
+
+
+def test_append_without_norms_or_angles_copies_every_element():
+    s = paged_inputs([3, 5], [20, 9], 4, 2, 64, 16, poison=False)
+    k, v = draw(2, 8, 2, 64), draw(3, 8, 2, 64)
+    for t, at, x in ((k, 5, math.inf), (k, 40, -0.0), (v, 7, math.inf), (s["q"], 9, -math.inf), (s["q"], 41, -0.0)):
+        t[:, :, at] = x
+    q2 = ofa.attn_paged_append(s["q"], k, v, s["kp"], s["vp"], s["bt"], s["lens"], s["cu"])
+    assert torch.equal(bits(q2), bits(s["q"]))
+    for b, t, at in [(0, i, 17 + i) for i in range(3)] + [(1, 3 + i, 4 + i) for i in range(5)]:
+        page = s["bt"][b, at // 16].long()
+        assert torch.equal(bits(s["kp"][page, at % 16]), bits(k[t])) and torch.equal(bits(s["vp"][page, at % 16]), bits(v[t]))
