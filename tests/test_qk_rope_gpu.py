@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import online_softmax_fa2_gb300 as ofa
-from paged_helpers import U, angles, check, norm_rope, norm_rope_bwd, paged_inputs
+from paged_helpers import U, angles, check, norm_rope, norm_rope_bwd, paged_inputs, pair_index
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -328,3 +328,50 @@ def test_append_without_norms_or_angles_copies_every_element():
     for b, t, at in [(0, i, 17 + i) for i in range(3)] + [(1, 3 + i, 4 + i) for i in range(5)]:
         page = s["bt"][b, at // 16].long()
         assert torch.equal(bits(s["kp"][page, at % 16]), bits(k[t])) and torch.equal(bits(s["vp"][page, at % 16]), bits(v[t]))
+
+
+def weight_chain(rows, H, other, d, dtype):
+    """Additions that a term of a weight gradient goes through at most: a group of lanes takes two heads of a
+    token at a time; its sum over all of them, the groups of a warp (3), the 4 warps of a block, every
+    32nd block's partial, and 32 of those."""
+    blocks = 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    per, per_other = -(-H // 2), -(-other // 2)
+    groups = 32 // ((4 if dtype is torch.bfloat16 else 8) * (1 if d <= 64 else 2 if d <= 128 else 4))
+    mine = max(blocks * per // (per + per_other), 1)  # (the queries' share is rounded down, the keys' up)
+    mine = min(mine, -(-rows * per // (4 * groups)))
+    return 2 * -(-rows * per // (mine * 4 * groups)) + 3 + 4 + -(-blocks // 32) + 32
+
+
+@pytest.mark.parametrize("dtype,B,N,Hq,Hkv,d,rot,inter", [
+    (torch.bfloat16, 2, 4099, 5, 3, 64, 64, True),
+    (torch.bfloat16, 1, 5003, 7, 2, 128, 64, False),
+    (torch.bfloat16, 3, 1501, 3, 1, 256, 256, True),
+    (torch.float32, 2, 2999, 5, 3, 64, 32, False),
+    (torch.float32, 1, 4001, 3, 5, 128, 128, True),
+    (torch.float32, 2, 1009, 4, 3, 192, 64, True),
+    (torch.float32, 1, 2503, 1, 2, 256, 256, False),
+])
+def test_weight_gradients_leave_no_row_out(dtype, B, N, Hq, Hkv, d, rot, inter):
+    # several units a group of lanes, the last round ragged; a bound that one row more or less breaks
+    q, k = draw(1, B, N, Hq, d, dtype=dtype), draw(2, B, N, Hkv, d, dtype=dtype)
+    dq2, dk2 = draw(5, B, N, Hq, d, dtype=dtype), draw(6, B, N, Hkv, d, dtype=dtype)
+    wq, wk = ((1 + 0.3 * draw(i, d, dtype=torch.float32)).to(dtype) for i in (3, 4))
+    cs = angles(N, rot).to(DEV)
+    dq, dk, dwq, dwk = ofa.attn_qk_norm_rope_bwd(q, k, dq2, dk2, wq, wk, cs, eps=EPS, interleaved=inter)
+    tab = table_for(cs, torch.arange(N).expand(B, N))
+    a, b = pair_index(d, rot, inter)
+    for x, dy, w, dx, dw, H, other in ((q, dq2, wq, dq, dwq, Hq, Hkv), (k, dk2, wk, dk, dwk, Hkv, Hq)):
+        rx, rw, lim, _ = norm_rope_bwd(x.cpu(), dy.cpu(), w.cpu(), tab, inter, EPS)
+        check(dx, rx, lim, "dx")
+        f, t = x.cpu().double(), dy.cpu().double().abs()
+        n = f / (f.square().mean(-1, keepdim=True) + EPS).sqrt()
+        turned, co, si = t.clone(), tab[..., :rot // 2].double().abs(), tab[..., rot // 2:].double().abs()
+        turned[..., a], turned[..., b] = t[..., a] * co + t[..., b] * si, t[..., b] * co + t[..., a] * si
+        # terms good to 32 U of what they are made of (the turn's three roundings, the norm's, two products)
+        bound = (32 + weight_chain(B * N, H, other, d, dtype)) * U * (turned * n.abs()).sum((0, 1, 2))
+        check(dw, rw, bound, "dw")
+        for at in (0, B * N - 1, B * N // 2):  # the sum without one token's last head is out of it
+            y = dy.cpu().clone()
+            y.view(B * N, H, d)[at, H - 1] = 0
+            less = norm_rope_bwd(x.cpu(), y, w.cpu(), tab, inter, EPS)[1]
+            assert bool(((less - rw).abs() > 2 * bound).any())
