@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import online_softmax_fa2_gb300 as ofa
+from online_softmax_fa2_gb300 import paged
 from paged_helpers import angles, check_paged, paged_inputs
 
 pytestmark = pytest.mark.gpu
@@ -601,3 +602,17 @@ def test_the_longest_table(nq):
     assert float((lse[:, 0].cpu().double() - L).abs().max()) <= tiles * 2.0 ** -24 + 2.0 ** -18 * (1 + float(L.max()))
     err = (o[:, 0].cpu().double() - P @ V).abs()
     assert bool((err <= (2 * 2.0 ** -8 + tiles * 2.0 ** -24 + steps * 2.0 ** -23) * (P @ V.abs())).all())
+
+
+@pytest.mark.parametrize("mq", [1, 12, 30, 150])
+def test_without_lse_the_outputs_are_the_same(mq):
+    # the C entry takes a null lse: whole items, cut ones and rows that see no key
+    new, lens = [2, 150, 1, 3], [700, 900, 9000, 2]
+    s = paged_inputs(new, lens, 8, 2, 128, 16, seed=91)
+    want, _ = run(s, max_q=mq)
+    o = torch.full_like(want, 7.0)
+    p = paged._paged_fwd_params(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], mq, True, None, o, None)
+    n = ofa.paged_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["cu"], max_q=mq)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert paged._load().attn_paged_fwd(p, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(o, want) and ofa.device_error_flags() == 0
