@@ -52,9 +52,12 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
-    // Tiles that a boundary has to leave at either side of a cut.  128-row tiles: a mixed batch of chunks takes
-    // 77.2 us with 4, 74.9 with 3, 74.6 with 2; 512 tokens over 512 keys 14.4, 14.4, 16.8, over 2048 keys
-    // 33.7, 30.3, 29.2.  Few rows: one decode over 1024 keys takes 17 us with 4, 19 with 8.
+    // Tiles that a boundary has to leave at either side of a cut.  Less cuts more finely and merges more, and
+    // the tiles are between the two: with 4, 3 and 2 a mixed batch of chunks takes 76.9, 74.3 and 74.0 us, 512
+    // tokens over 2048 keys 33.7, 30.3 and 29.3, 64 sequences of 2048 keys with 8 tokens 89.8, 88.3 and 86.9,
+    // but 512 tokens over 512 keys 14.5, 14.5 and 16.9, 256 sequences of 512 keys with 64 tokens 146.3, 146.3
+    // and 152.  Few rows, with 6, 4 and 3: one decode over 1024 keys 14.0, 13.0 and 12.9 us, over 8192 keys
+    // 18.3, 17.0 and 16.9, 8 over 2048 keys 21.1, 19.7 and 19.8.
     pl.min_cut = pl.tc ? 3 : 4;
     pl.cuts = pl.grid > 1 && keys > (int64_t)((2 * pl.min_cut - 1) << pl.kt);
     if (!pl.cuts) {  // every block is shorter than two such parts: no states
@@ -148,9 +151,13 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     // 20.7, 19.9 and 24.8.
     a.min_share = pl.tc ? 4 : 8;
     a.min_cut = pl.min_cut;
-    // What a block's beginning and end cost, in tiles (128-row tiles: a batch of 244 blocks of 3 to 32
-    // tiles, 134 us counted as 0, 105 as 2, 97 as 4, 97 as 6 at first; now 75, 77 as 5, and one sequence
-    // of 2048 keys, 8 tokens, 17 us as 4, 20 as 3 or 5; few rows: no difference).
+    // What a block's beginning and end cost, in tiles.  Batches of many blocks take any value near it (a
+    // mixed one of 244 blocks of 3 to 32 tiles 73.5 us as 3, 74.4 as 4, 76.9 as 5; before later steps 134 as 0,
+    // 97 as 4 or 6; 64 sequences of 2048 keys with 8 tokens of 64/8 heads 86.4, 88.3, 87.6).  Short items
+    // decide: as the least share of the tiles, and half of that of few rows, it puts the cuts of an item of
+    // 4 n tiles at whole shares (one sequence, 8 tokens of 64/8 heads over 2048 keys 19.7, 17.0, 19.2 us as
+    // 3, 4, 5, over 8192 keys 22.3, 19.9, 22.4; few rows, one token over 1024 keys 14.8, 13.0, 14.9, 8 of
+    // them over 2048 keys 20.8, 19.7, 20.9).
     a.cost = 4;
     a.scale_log2 = p.scale * kLog2e;
     a.q = static_cast<const __nv_bfloat16 *>(p.q);

@@ -5,11 +5,13 @@
 // tiles of K and V, page by page, into a ring of shared-memory stages with TMA (128-byte
 // swizzle); warps 0-3 compute on them with warp-level tensor-core products (mma.sync m16n8k16):
 // 16 rows are far below the 128 of a tcgen05 tile, and the tensor work is small next to the
-// copy (64 keys x 16 rows x 128 dimensions take 128 products of the SM's warps against 1.4 us of copy at the
+// copy (64 keys x 16 rows x 128 dimensions take 128 products of the SM's warps against 0.75 us of copy, 32 KB at an
 // SM's share of HBM).
 //   S = Q K^T   warp w takes keys 16 w .. 16 w + 15 of the tile, all rows;
 //   the row maxima of the four warps meet in shared memory, so that the CTA keeps one reference
-//   per row; P = exp2(S - m) goes to shared memory in bf16;
+//   per row; P = exp2(S - m) goes to shared memory in bf16, as the product takes it: half a step of 2^-8
+//   of a weight, which averages out over the keys (the outputs lie 1.3 to 1.4 times as far from 64 bits
+//   as with fp32 weights), where fp32 weights would want V in 32 bits too and twice the products;
 //   O += P V    warp w takes dimensions [w D/4, (w + 1) D/4), all keys and rows.
 // So no state is merged across warps, and a row's accumulator takes D/16 registers a thread.
 //

@@ -516,6 +516,8 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
                     ptx::fence_proxy_async_smem();
                 }
                 if (++vs == VS) { vs = 0; vph ^= 1; }
+                // the weights go to the product in bf16, half a step of 2^-8 each (l_run has them in fp32):
+                // V in 32 bits would take twice the room and run at half the rate
                 bf16fwd::store_p(lane_addr + s_col, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&ctrl->p_full[X]);

@@ -357,7 +357,8 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
     """Attention of the packed new tokens q [T, Hq, d] over the paged cache, one or many per
     sequence in one call; query head h reads key/value head h // (Hq // Hkv).  causal aligns the
     new tokens to the end of their sequences.  max_q: the largest number of new tokens of any
-    sequence, where the caller knows it (it chooses the kernel; the results hold without it).
+    sequence, where the caller knows it (it chooses the kernel; the results hold without it, but a
+    long chunk among single tokens then takes about twice the time).
     Returns (o [T, Hq, d], lse [T, Hq]).  See include/attn.h, attn_paged_fwd."""
     if stream is not None:
         return _on(stream, q, attn_paged_fwd, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, workspace,
