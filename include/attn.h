@@ -566,8 +566,8 @@ size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
  * workspace: caller-owned device memory, 16-byte aligned, of any contents on entry; calls that
  * overlap on the GPU need one each.  It may be NULL where attn_paged_fwd_workspace_bytes is 0.
  * Supported: bfloat16, d in {64, 128}, page_size a power of two >= 16, 1 <= Hq / Hkv <= 64,
- * T * Hq / Hkv <= 2^30, table_width * page_size <= 2^31 - 256, scale > 0; tensors 16-byte aligned, strides non-zero multiples of 8 elements.
- * Queues one kernel or two.
+ * T * Hq / Hkv <= 2^30, table_width * page_size <= 2^31 - 256, scale > 0; tensors 16-byte aligned,
+ * strides non-zero multiples of 8 elements.  Queues one kernel or two.
  */
 attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *workspace, size_t workspace_bytes,
                              attn_stream_t stream);
