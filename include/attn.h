@@ -572,6 +572,118 @@ size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *params);
 attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *workspace, size_t workspace_bytes,
                              attn_stream_t stream);
 
+/*
+ * A paged cache in 8 bits.
+ *
+ * A row (the d elements of one key head, key or value, of one token) is held as d codes of e4m3 (one
+ * byte each: sign, 4 bits of exponent, 3 of mantissa, largest 448, no infinity) and one scale byte e: its
+ * elements are code * 2^(e - 127).  A power of two costs a floating format nothing (an element is
+ * off by half a step, 2^-4 of itself, wherever the row's largest lies) and is exact in every product.
+ *
+ *   k_pages, v_pages  of attn_paged_cache_t: e4m3 codes, strides in elements, which are bytes
+ *   k, v              scale bytes [num_pages, Hkv, page_size], strides in bytes (page, head), the
+ *                     slots of a page contiguous; all 256 values are valid, 255 makes the row NaN
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+} attn_paged_scales_t;
+
+/* Arguments of attn_paged_append_q8: those of attn_paged_append (cache.dtype is the type of q, k, v,
+ * q_out and the weights), and the scales. */
+typedef struct {
+    attn_paged_append_params_t append;
+    attn_paged_scales_t scales;
+} attn_paged_append_q8_params_t;
+
+/*
+ * attn_paged_append_q8 -- attn_paged_append into a cache in 8 bits: the keys are quantised as they come
+ * from the norm and the rotation, in fp32, the values as they are.  e - 127 is the smallest exponent >=
+ * -127 that brings the row's largest finite magnitude within 448 * 2^(e - 127) (0 for a row of zeros), and
+ * the elements are rounded to the nearest code, ties to even.  A NaN or an infinity is held as NaN.
+ * Supported: as attn_paged_append; the pages' strides are multiples of 16 bytes, as their bases.  Queues one kernel.
+ */
+attn_status_t attn_paged_append_q8(const attn_paged_append_q8_params_t *params, attn_stream_t stream);
+
+/*
+ * Arguments of attn_paged_read_q8: cache as for the append, with cu_q and T naming the rows: rows
+ * cu_q[b] .. cu_q[b + 1] - 1 of the T are sequence b's last (row i of its n is the key at position
+ * kv_lens[b] - n + i); cache.dtype is the type of k and v.
+ *   k, v   [T, Hkv, d], written (strides token, head); either may be NULL
+ */
+typedef struct {
+    attn_paged_cache_t cache;
+    attn_paged_scales_t scales;
+    void *k;
+    void *v;
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+} attn_paged_read_q8_params_t;
+
+/*
+ * attn_paged_read_q8 -- rows of a cache in 8 bits as the numbers that they stand for, rounded once (in
+ * bfloat16 exact but for values under 2^-126 or over its range).  Rows of no sequence, and those whose
+ * position would be negative, are left as they were; a row on a page out of range too (bit 2).
+ * Supported: as attn_paged_append_q8.  Queues one kernel.
+ */
+attn_status_t attn_paged_read_q8(const attn_paged_read_q8_params_t *params, attn_stream_t stream);
+
+/* Arguments of attn_paged_fwd_q8: those of attn_paged_fwd (cache.dtype is the type of q and o), and the scales. */
+typedef struct {
+    attn_paged_fwd_params_t fwd;
+    attn_paged_scales_t scales;
+} attn_paged_fwd_q8_params_t;
+
+/* Bytes of workspace attn_paged_fwd_q8 needs, as attn_paged_fwd_workspace_bytes. */
+size_t attn_paged_fwd_q8_workspace_bytes(const attn_paged_fwd_q8_params_t *params);
+
+/*
+ * attn_paged_fwd_q8 -- attn_paged_fwd over a cache in 8 bits.  The products take the codes in fp16, where
+ * they are exact; a query row goes in as its elements times a power of two that brings the largest finite one
+ * near 2^14 (exact down to 2^-31 of it), the weights are rounded to fp16.  A sequence's
+ * values are taken relative to the largest scale met: those of a scale 2^15 and more below it lose
+ * bits under 2^-33 of the largest value that scale can hold.
+ * Everything else as attn_paged_fwd; a row that holds a NaN makes the rows that see it NaN.
+ * Supported: as attn_paged_fwd; the bases and strides of pages and scales are multiples of 16 bytes.
+ */
+attn_status_t attn_paged_fwd_q8(const attn_paged_fwd_q8_params_t *params, void *workspace, size_t workspace_bytes,
+                                attn_stream_t stream);
+
+/*
+ * Arguments of attn_paged_prefix_fwd: attention of a batch whose sequences share prefixes.  Besides its
+ * sequence's own keys (fwd, as for attn_paged_fwd: kv_lens, the block table and the causal rule do not count the
+ * prefix), a token sees every key of its prefix:
+ *   prefix_table   int32 [P, prefix_width], row stride prefix_stride: pages of the same cache, as a block table
+ *   prefix_lens    int32 [P], clamped to [0, prefix_width * page_size] (bit 1 of the device error word)
+ *   cu_prefix      int32 [P + 1], not decreasing: tokens cu_prefix[p] .. cu_prefix[p + 1] - 1 of the T see
+ *                  prefix p; tokens before cu_prefix[0] and from cu_prefix[P] on have none.  NULL: every
+ *                  prefix has T / P of them.  Bad entries as for cu_q.
+ *   scales         of a cache in 8 bits (codes and rules of attn_paged_fwd_q8), or k and v NULL: cache.dtype
+ */
+typedef struct {
+    attn_paged_fwd_params_t fwd;
+    attn_paged_scales_t scales;
+    int64_t P, prefix_width, prefix_stride;
+    const int32_t *prefix_table;
+    const int32_t *prefix_lens;
+    const int32_t *cu_prefix;
+} attn_paged_prefix_params_t;
+
+/* Bytes of workspace attn_paged_prefix_fwd needs (the states of T * Hq rows, and what the attention itself needs). */
+size_t attn_paged_prefix_fwd_workspace_bytes(const attn_paged_prefix_params_t *params);
+
+/*
+ * attn_paged_prefix_fwd -- the prefix's keys and values are read once for all tokens that see it (rows of the
+ * same product), whose states (m, l, u) over it go to the workspace in fp32; the attention over the own keys
+ * starts from them.  ("How Does FlashAttention Preserve Global Softmax Across Tiles?", section 3.)  The result
+ * is that of attn_paged_fwd over the prefix's keys followed by the own ones, lse included.
+ * Supported: as attn_paged_fwd, or attn_paged_fwd_q8; 1 <= P <= 65535.  Queues two to four kernels.
+ */
+attn_status_t attn_paged_prefix_fwd(const attn_paged_prefix_params_t *params, void *workspace, size_t workspace_bytes,
+                                    attn_stream_t stream);
+
 /* Message describing the last non-OK status returned on the calling thread ("" if none). */
 const char *attn_last_error(void);
 

@@ -14,6 +14,8 @@ Around the attention (module ``paged``, same rules; include/attn.h):
     q2, k2 = attn_qk_norm_rope(q, k, wq, wk, cos_sin)         # head norms and position rotation
     q2 = attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, ...)
     o, lse = attn_paged_fwd(q2, k_pages, v_pages, block_table, kv_lens, cu_q)
+    attn_paged_append_q8, attn_paged_fwd_q8, attn_paged_read_q8: the cache in 8 bits
+    attn_paged_prefix_fwd: sequences that share prefixes
 
 Shapes: q [B, Nq, H, dk], k [B, Nk, H, dk], v [B, Nk, H, dv] (any strides with the last
 dimension contiguous), bias [B, H, Nq, Nk] fp32 (any strides with the last dimension
@@ -33,7 +35,9 @@ __all__ = ["attn_fwd", "attn_fwd_partial", "attn_merge_states_rows", "attn_bwd",
            "attn_decode_splitkv_fused", "attn_decode_splitkv_noalloc",
            "attn_merge_states", "decode_workspace_bytes", "bwd_workspace_bytes",
            "attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_append", "attn_paged_fwd",
-           "paged_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes",
+           "attn_paged_append_q8", "attn_paged_read_q8", "attn_paged_fwd_q8", "attn_paged_prefix_fwd",
+           "paged_fwd_workspace_bytes", "paged_fwd_q8_workspace_bytes", "paged_prefix_fwd_workspace_bytes",
+           "qk_norm_rope_bwd_workspace_bytes",
            "device_error_flags", "last_error", "library_path", "load", "AttnError", "Status"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -441,5 +445,7 @@ def device_error_flags(clear=True) -> int:
     return int(v.value)
 
 
-from .paged import (attn_paged_append, attn_paged_fwd, attn_qk_norm_rope, attn_qk_norm_rope_bwd,  # noqa: E402
-                    paged_fwd_workspace_bytes, qk_norm_rope_bwd_workspace_bytes)
+from .paged import (attn_paged_append, attn_paged_append_q8, attn_paged_fwd, attn_paged_fwd_q8,  # noqa: E402
+                    attn_paged_prefix_fwd, attn_paged_read_q8, attn_qk_norm_rope, attn_qk_norm_rope_bwd,
+                    paged_fwd_q8_workspace_bytes, paged_fwd_workspace_bytes, paged_prefix_fwd_workspace_bytes,
+                    qk_norm_rope_bwd_workspace_bytes)

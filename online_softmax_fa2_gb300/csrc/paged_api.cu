@@ -94,11 +94,37 @@ attn_status_t check_cache_sizes(const attn_paged_cache_t &c) {
     return ATTN_OK;
 }
 
-attn_status_t check_cache(const attn_paged_cache_t &c) {
+// Pages of codes or scale bytes: the base, and the n strides of dimensions longer than one, are present, positive, and
+// multiples of `step` bytes.
+attn_status_t check_bytes(const char *name, const void *p, const int64_t *s, const int64_t *sizes, int n, int64_t step) {
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "%s is NULL", name);
+    for (int i = 0; i < n; ++i) {
+        if (sizes[i] <= 1) continue;
+        if (s[i] < 1) return fail(ATTN_ERR_INVALID_ARG, "%s_stride[%d] = %lld is not positive", name, i, (long long)s[i]);
+        if (s[i] % step) return fail(ATTN_ERR_MISALIGNED, "%s strides must be multiples of %lld bytes", name, (long long)step);
+    }
+    if (reinterpret_cast<uintptr_t>(p) % (uintptr_t)step) return fail(ATTN_ERR_MISALIGNED, "%s must be %lld-byte aligned", name, (long long)step);
+    return ATTN_OK;
+}
+
+// A cache in 8 bits: codes in steps of 16 bytes, scale bytes in steps of `step`.
+attn_status_t check_q8(const attn_paged_cache_t &c, const attn_paged_scales_t &sc, int64_t step) {
+    const int64_t sizes[3] = {c.num_pages, c.page_size, c.Hkv}, rows[2] = {c.num_pages, c.Hkv};
+    attn_status_t st = ATTN_OK;
+    if (c.num_pages > 0 &&
+        ((st = check_bytes("k_pages", c.k_pages, c.k_stride, sizes, 3, 16)) || (st = check_bytes("v_pages", c.v_pages, c.v_stride, sizes, 3, 16)) ||
+         (st = check_bytes("k_scales", sc.k, sc.k_stride, rows, 2, step)) || (st = check_bytes("v_scales", sc.v, sc.v_stride, rows, 2, step))))
+        return st;
+    return ATTN_OK;
+}
+
+// scales: of a cache in 8 bits (of any alignment), or null.
+attn_status_t check_cache(const attn_paged_cache_t &c, const attn_paged_scales_t *scales) {
     attn_status_t st = check_cache_sizes(c);
     if (st || c.T == 0) return st;
     if (!c.kv_lens || (!c.block_table && c.table_width > 0))
         return fail(ATTN_ERR_INVALID_ARG, "kv_lens or block_table is NULL");
+    if (scales) return check_q8(c, *scales, 1);
     const int64_t sizes[3] = {c.num_pages, c.page_size, c.Hkv};
     if (c.num_pages > 0) {
         if ((st = check_tensor("k", c.k_pages, c.k_stride, 3, c.dtype))) return st;
@@ -127,6 +153,40 @@ attn_status_t check_paged_fwd(const attn_paged_fwd_params_t *p) {
     // the last tile's end, past the keys by up to 127, stays an int
     if (c.table_width > 0 && c.table_width > (INT32_MAX - 255) / c.page_size)
         return fail(ATTN_ERR_UNSUPPORTED, "table_width * page_size must be at most 2^31 - 256");
+    return ATTN_OK;
+}
+
+// The pointers of an attention that has tokens.
+attn_status_t check_paged_tensors(const attn_paged_fwd_params_t *p, const attn_paged_scales_t *scales) {
+    const attn_paged_cache_t &c = p->cache;
+    const int64_t nq[2] = {c.T, p->Hq};
+    attn_status_t st;
+    if ((st = check_tensor("q", p->q, p->q_stride, 2, c.dtype)) || (st = check_tensor("o", p->o, p->o_stride, 2, c.dtype)) ||
+        (st = check_written("q", p->q_stride, nq, 2)) || (st = check_written("o", p->o_stride, nq, 2)))
+        return st;
+    return scales ? check_q8(c, *scales, 16) : ATTN_OK;
+}
+
+attn_status_t check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need && (!workspace || !aligned16(workspace) || bytes < need))
+        return fail(ATTN_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)", need, bytes);
+    return ATTN_OK;
+}
+
+const attn_paged_scales_t *scales_of(const attn_paged_prefix_params_t &p) { return p.scales.k || p.scales.v ? &p.scales : nullptr; }
+
+// The sizes of both attentions of a call.
+attn_status_t check_prefix_sizes(const attn_paged_prefix_params_t *p) {
+    attn_status_t st;
+    if ((st = check_paged_fwd(&p->fwd)) || (st = check_cache_sizes(p->fwd.cache))) return st;
+    if (p->fwd.cache.T == 0) return ATTN_OK;
+    if (p->P < 1 || p->P > 65535) return fail(ATTN_ERR_INVALID_ARG, "P must be in [1, 65535] (got %lld)", (long long)p->P);
+    if (p->prefix_width < 0 || p->prefix_width > INT32_MAX || p->prefix_stride < 0)
+        return fail(ATTN_ERR_INVALID_ARG, "prefix_width or prefix_stride is out of range");
+    if (p->prefix_width > 0 && p->prefix_width > (INT32_MAX - 255) / p->fwd.cache.page_size)
+        return fail(ATTN_ERR_UNSUPPORTED, "prefix_width * page_size must be at most 2^31 - 256");
+    if (!p->cu_prefix && p->fwd.cache.T % p->P)
+        return fail(ATTN_ERR_INVALID_ARG, "without cu_prefix, T = %lld must be a multiple of P = %lld", (long long)p->fwd.cache.T, (long long)p->P);
     return ATTN_OK;
 }
 
@@ -190,11 +250,11 @@ extern "C" attn_status_t attn_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_param
     return launch_qk_norm_rope_bwd(*bp, static_cast<float *>(workspace), s);
 }
 
-extern "C" attn_status_t attn_paged_append(const attn_paged_append_params_t *p, attn_stream_t stream) {
-    clear_error();
-    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+namespace {
+
+attn_status_t append(const attn_paged_append_params_t *p, const attn_paged_scales_t *scales, attn_stream_t stream) {
     const attn_paged_cache_t &c = p->cache;
-    attn_status_t st = check_cache(c);
+    attn_status_t st = check_cache(c, scales);
     if (st) return st;
     if (p->Hq < 1 || p->Hq > 65535) return fail(ATTN_ERR_INVALID_ARG, "Hq = %lld", (long long)p->Hq);
     if ((st = check_rope(c.d, p->rot, p->interleaved, p->eps, p->wq, p->wk, p->cos_sin, p->cos_sin_rows, p->cos_sin_stride)))
@@ -206,32 +266,102 @@ extern "C" attn_status_t attn_paged_append(const attn_paged_append_params_t *p, 
         (st = check_tensor("q_out", p->q_out, p->q_out_stride, 2, c.dtype)) ||
         (st = check_written("q_out", p->q_out_stride, nq, 2)))
         return st;
-    return launch_paged_append(*p, reinterpret_cast<cudaStream_t>(stream));
+    return launch_paged_append(*p, scales, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *p) {
-    clear_error();
+size_t fwd_workspace(const attn_paged_fwd_params_t *p, const attn_paged_scales_t *scales) {
     if (!p || check_paged_fwd(p) || check_cache_sizes(p->cache) || p->cache.T < 1) {
         clear_error();
         return 0;
     }
-    return paged_fwd_workspace(*p);
+    return paged_fwd_workspace(*p, scales);
+}
+
+attn_status_t fwd(const attn_paged_fwd_params_t *p, const attn_paged_scales_t *scales, void *workspace, size_t workspace_bytes,
+                  attn_stream_t stream) {
+    attn_status_t st = check_paged_fwd(p);
+    if (st || (st = check_cache(p->cache, scales))) return st;
+    if (p->cache.T == 0) return ATTN_OK;
+    if ((st = check_paged_tensors(p, scales)) || (st = check_workspace(workspace, workspace_bytes, paged_fwd_workspace(*p, scales))))
+        return st;
+    return launch_paged_fwd(*p, scales, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" attn_status_t attn_paged_append(const attn_paged_append_params_t *p, attn_stream_t stream) {
+    clear_error();
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+    return append(p, nullptr, stream);
+}
+
+extern "C" attn_status_t attn_paged_append_q8(const attn_paged_append_q8_params_t *p, attn_stream_t stream) {
+    clear_error();
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+    return append(&p->append, &p->scales, stream);
+}
+
+extern "C" attn_status_t attn_paged_read_q8(const attn_paged_read_q8_params_t *p, attn_stream_t stream) {
+    clear_error();
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+    const attn_paged_cache_t &c = p->cache;
+    attn_status_t st = check_cache(c, &p->scales);
+    if (st) return st;
+    if (c.d < 1) return fail(ATTN_ERR_INVALID_ARG, "d must be >= 1 (got %lld)", (long long)c.d);
+    if (c.d > 256 || c.d % 16) return fail(ATTN_ERR_UNSUPPORTED, "d must be a multiple of 16 up to 256 (got %lld)", (long long)c.d);
+    if (c.T == 0 || (!p->k && !p->v)) return ATTN_OK;
+    const int64_t n[2] = {c.T, c.Hkv};
+    if (p->k && ((st = check_tensor("k", p->k, p->k_stride, 2, c.dtype)) || (st = check_written("k", p->k_stride, n, 2)))) return st;
+    if (p->v && ((st = check_tensor("v", p->v, p->v_stride, 2, c.dtype)) || (st = check_written("v", p->v_stride, n, 2)))) return st;
+    return launch_paged_read_q8(*p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t attn_paged_fwd_workspace_bytes(const attn_paged_fwd_params_t *p) {
+    clear_error();
+    return fwd_workspace(p, nullptr);
 }
 
 extern "C" attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *p, void *workspace, size_t workspace_bytes,
                                         attn_stream_t stream) {
     clear_error();
     if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
-    const attn_paged_cache_t &c = p->cache;
-    attn_status_t st = check_paged_fwd(p);
-    if (st || (st = check_cache(c))) return st;
-    if (c.T == 0) return ATTN_OK;
-    const int64_t nq[2] = {c.T, p->Hq};
-    if ((st = check_tensor("q", p->q, p->q_stride, 2, c.dtype)) || (st = check_tensor("o", p->o, p->o_stride, 2, c.dtype)) ||
-        (st = check_written("q", p->q_stride, nq, 2)) || (st = check_written("o", p->o_stride, nq, 2)))
-        return st;
-    const size_t need = paged_fwd_workspace(*p);
-    if (need && (!workspace || !aligned16(workspace) || workspace_bytes < need))
-        return fail(ATTN_ERR_WORKSPACE, "workspace must be 16-byte aligned and hold %zu bytes (got %zu)", need, workspace_bytes);
-    return launch_paged_fwd(*p, workspace, reinterpret_cast<cudaStream_t>(stream));
+    return fwd(p, nullptr, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t attn_paged_fwd_q8_workspace_bytes(const attn_paged_fwd_q8_params_t *p) {
+    clear_error();
+    return p ? fwd_workspace(&p->fwd, &p->scales) : 0;
+}
+
+extern "C" attn_status_t attn_paged_fwd_q8(const attn_paged_fwd_q8_params_t *p, void *workspace, size_t workspace_bytes,
+                                           attn_stream_t stream) {
+    clear_error();
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+    return fwd(&p->fwd, &p->scales, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t attn_paged_prefix_fwd_workspace_bytes(const attn_paged_prefix_params_t *p) {
+    clear_error();
+    if (!p || check_prefix_sizes(p) || p->fwd.cache.T < 1) {
+        clear_error();
+        return 0;
+    }
+    return paged_prefix_workspace(*p);
+}
+
+extern "C" attn_status_t attn_paged_prefix_fwd(const attn_paged_prefix_params_t *p, void *workspace, size_t workspace_bytes,
+                                               attn_stream_t stream) {
+    clear_error();
+    if (!p) return fail(ATTN_ERR_INVALID_ARG, "params is NULL");
+    const attn_paged_scales_t *scales = scales_of(*p);
+    attn_status_t st = check_prefix_sizes(p);
+    if (st || (st = check_cache(p->fwd.cache, scales))) return st;
+    if (p->fwd.cache.T == 0) return ATTN_OK;
+    if (!p->prefix_lens || (!p->prefix_table && p->prefix_width > 0))
+        return fail(ATTN_ERR_INVALID_ARG, "prefix_lens or prefix_table is NULL");
+    if ((st = check_paged_tensors(&p->fwd, scales))) return st;
+    const size_t need = paged_prefix_workspace(*p);
+    if (!need) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
+    if ((st = check_workspace(workspace, workspace_bytes, need))) return st;
+    return launch_paged_prefix(*p, workspace, reinterpret_cast<cudaStream_t>(stream));
 }

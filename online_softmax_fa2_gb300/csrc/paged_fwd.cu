@@ -25,7 +25,7 @@ struct Plan {
     size_t off_ml, off_u, bytes;
 };
 
-Plan make_plan(const attn_paged_fwd_params_t &p) {
+Plan make_plan(const attn_paged_fwd_params_t &p, bool q8) {
     const attn_paged_cache_t &c = p.cache;
     const int64_t G = p.Hq / c.Hkv;
     // tokens a sequence, or their mean
@@ -37,12 +37,12 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
     // and 68, 24 rows 105 and 68.  One tile a block up to its 128 rows (96 rows of 64 dimensions 69 us,
     // 87 with two tiles; 160 rows 111 and 100), of 64 rows where that is enough (512 sequences of 128
     // keys, 64 rows: 75 us, 84 in a tile of 128; 96 rows: 129 and 88).
-    pl.tc = rows > (128 / G) * G ? 2 : rows > 16 ? 1 : 0;
+    pl.tc = q8 ? 0 : rows > (128 / G) * G ? 2 : rows > 16 ? 1 : 0;
     pl.tile_rows = rows > (64 / G) * G ? 128 : 64;
     // (the tiles take whole tokens, so that TMA can bring their queries)
     pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : 16;
-    pl.kt = pl.tc ? 7 : 6;
-    pl.box = pl.tc ? kTcBoxKeys : kRowsBoxKeys;
+    pl.kt = pl.tc || q8 ? 7 : 6;
+    pl.box = pl.tc ? kTcBoxKeys : q8 ? kRowsQ8Keys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;
     // no more shares than tiles there can be
     const int64_t keys = c.table_width * c.page_size;
@@ -73,21 +73,24 @@ Plan make_plan(const attn_paged_fwd_params_t &p) {
 }
 
 // 4-D map over pages [num_pages, page_size, Hkv, d] with element strides s (page, slot, head); a
-// box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle.  L2 fetches whole
+// box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle; of codes all d, swizzled over as
+// many bytes.  L2 fetches whole
 // rows of a head and no more: with 64 dimensions (128 bytes) a 256-byte fetch would bring the next
 // head's row too (351 MB read for 278 MB of cache, measured).
 attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cache_t &c, const int64_t s[3], int box,
-                           const char *name) {
+                           bool q8, const char *name) {
     auto enc = get_encoder();
     if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    auto bytes = [](int64_t st, int64_t size) -> cuuint64_t { return size <= 1 ? 16u : (cuuint64_t)(st * 2); };
+    auto bytes = [q8](int64_t st, int64_t size) -> cuuint64_t { return size <= 1 ? 16u : (cuuint64_t)(q8 ? st : st * 2); };
     cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv, (cuuint64_t)c.num_pages};
     cuuint64_t strides[3] = {bytes(s[1], c.page_size), bytes(s[2], c.Hkv), bytes(s[0], c.num_pages)};
-    cuuint32_t b[4] = {64, (cuuint32_t)(c.page_size < box ? c.page_size : box), 1, 1};
+    cuuint32_t b[4] = {q8 ? (cuuint32_t)c.d : 64u, (cuuint32_t)(c.page_size < box ? c.page_size : box), 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, b, es,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUresult r = enc(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
+                           strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           q8 && c.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                           q8 ? (c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B)
+                           : c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(ATTN_ERR_INVALID_ARG, "TMA descriptor for %s rejected (CUresult %d)", name, (int)r);
     return ATTN_OK;
@@ -126,18 +129,14 @@ int log2_of(int x) {
     return l;
 }
 
-}  // namespace
+const State kNoState{kNone, 0, nullptr, nullptr, nullptr};
 
-size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p) {
-    const Plan pl = make_plan(p);
-    return pl.fits ? pl.bytes : 0;
-}
-
-attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace, cudaStream_t st) {
+attn_status_t launch(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales, const State &state, void *workspace,
+                     cudaStream_t st) {
     const attn_paged_cache_t &c = p.cache;
-    const Plan pl = make_plan(p);
+    const Plan pl = make_plan(p, scales != nullptr);
     if (!pl.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
-    Args a;
+    Args a{};
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hkv = (int)c.Hkv; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
     a.R = pl.R; a.kt = pl.kt;
     bf16fwd::fast_div_params((uint32_t)a.G, a.g_m, a.g_s);
@@ -172,11 +171,21 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
     a.tag = next_tag();
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
+    a.state = state;
+    const bool q8 = scales != nullptr;
+    if (q8) {
+        a.ks = static_cast<const uint8_t *>(scales->k);
+        a.vs = static_cast<const uint8_t *>(scales->v);
+        for (int i = 0; i < 2; ++i) {
+            a.kss[i] = scales->k_stride[i];
+            a.vss[i] = scales->v_stride[i];
+        }
+    }
     CUtensorMap mk{}, mv{};  // not used when there are no pages
     if (c.num_pages > 0) {
         attn_status_t r;
-        if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, "k_pages"))) return r;
-        if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, "v_pages"))) return r;
+        if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, q8, "k_pages"))) return r;
+        if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, q8, "v_pages"))) return r;
     }
     if (pl.tc) {
         CUtensorMap mq;
@@ -184,7 +193,65 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, void *workspace
         if (r) return r;
         return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.tc, pl.tile_rows, pl.grid, pl.cuts, st);
     }
-    return launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
+    return q8 ? launch_paged_rows_q8(mk, mv, a, (int)c.d, pl.grid, st) : launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
+}
+
+// The attention of all packed tokens over their prefixes: the prefixes are the sequences, their tokens all see
+// every key.  How many tokens a prefix has is not known here: their mean chooses the kernel.
+attn_paged_fwd_params_t over_prefixes(const attn_paged_prefix_params_t &p) {
+    attn_paged_fwd_params_t f = p.fwd;
+    f.cache.B = p.P;
+    f.cache.block_table = p.prefix_table;
+    f.cache.table_width = p.prefix_width;
+    f.cache.table_stride = p.prefix_stride;
+    f.cache.kv_lens = p.prefix_lens;
+    f.cache.cu_q = p.cu_prefix;
+    f.causal = 0;
+    f.max_q = 0;
+    f.lse = nullptr;
+    return f;
+}
+
+size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales) {
+    const Plan pl = make_plan(p, scales != nullptr);
+    return pl.fits ? pl.bytes : 0;
+}
+
+attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales, void *workspace, cudaStream_t st) {
+    return launch(p, scales, kNoState, workspace, st);
+}
+
+// The states, then what the two attentions need, one after the other, in the same place.
+size_t paged_prefix_workspace(const attn_paged_prefix_params_t &p) {
+    const bool q8 = p.scales.k != nullptr;
+    const Plan over = make_plan(over_prefixes(p), q8), own = make_plan(p.fwd, q8);
+    if (!over.fits || !own.fits) return 0;
+    const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq;
+    return round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float)) +
+           (over.bytes > own.bytes ? over.bytes : own.bytes);
+}
+
+attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *workspace, cudaStream_t st) {
+    const attn_paged_scales_t *scales = p.scales.k ? &p.scales : nullptr;
+    const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq;
+    char *ws = static_cast<char *>(workspace);
+    State s;
+    s.mode = kWritten;
+    s.P = (int)p.P;
+    s.cu = p.cu_prefix;
+    s.ml = reinterpret_cast<float2 *>(ws);
+    s.u = reinterpret_cast<float *>(ws + round_up(rows * 2 * sizeof(float)));
+    void *rest = ws + round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float));
+    const Plan own = make_plan(p.fwd, scales != nullptr);
+    if (!own.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
+    const attn_status_t r = launch(over_prefixes(p), scales, s, rest, st);
+    if (r) return r;
+    s.mode = kMerged;
+    return launch(p.fwd, scales, s, rest, st);
 }
 
 }  // namespace attn

@@ -18,7 +18,7 @@
 
 #include <type_traits>
 
-#include "paged_sched.cuh"
+#include "paged_state.cuh"
 
 namespace attn {
 namespace paged {
@@ -63,11 +63,11 @@ __device__ __forceinline__ bool all_marked(const Args &a, unsigned long long *ma
 }
 
 // The merge for few rows: the states at slots slot(0) .. slot(n - 1), n <= kGroup, u as [slot][R][D],
-// to the slot `to`, or, with to < 0, to the rows that out(r, orow, lse) names.  Four warps, tid 0 ..
+// to the slot `to`, or, with to < 0, row by row to end(r, v, m, l), v the lane's columns of u.  Four warps, tid 0 ..
 // 127, a row a warp at a time (U of them in flight); of a row's states, lane p holds the weights
 // of p and p + 32.
-template <int D, int U, int P, class Slot, class Out>
-__device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int to, int tid, Slot slot, Out out) {
+template <int D, int U, int P, class Slot, class End>
+__device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int to, int tid, Slot slot, End end) {
     constexpr int C = D / 32;  // columns a lane: C lane .. C lane + C - 1
     using Vec = typename std::conditional<C == 4, float4, float2>::type;
     const int warp = tid >> 5, lane = tid & 31;
@@ -139,18 +139,29 @@ __device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int 
                 *reinterpret_cast<Vec *>(a.u + at * D + C * lane) = y;
                 if (lane == 0) *reinterpret_cast<float2 *>(a.ml + at * 2) = make_float2(M[u], sum[u]);
             } else {
-                __nv_bfloat16 *orow;
-                float *lse;
-                out(r, orow, lse);
-                const bool empty = sum[u] == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
-                const float inv = empty ? 0.f : 1.f / sum[u];
-                uint32_t *o32 = reinterpret_cast<uint32_t *>(orow + C * lane);
-#pragma unroll
-                for (int e = 0; e < C; e += 2) o32[e / 2] = empty ? 0u : ptx::pack_bf16x2(v[u][e] * inv, v[u][e + 1] * inv);
-                if (lse && lane == 0) *lse = empty ? -INFINITY : (M[u] + log2f(sum[u])) * kLn2;
+                end(r, v[u], M[u], sum[u]);
             }
         }
     }
+}
+
+// The end of row (tok, h) whose columns D / 32 lane .. a warp's lanes hold: outputs, or states (kState).
+template <int D, bool kState>
+__device__ __forceinline__ void end_row(const Args &a, int tok, int h, float (&v)[D / 32], float m, float sum) {
+    constexpr int C = D / 32;
+    const int lane = threadIdx.x & 31;
+    if (kState && a.state.mode == kWritten) {
+        write_state<C>(a, tok, h, D, C * lane, v, sum);
+        if (lane == 0) write_state_ml(a, tok, h, m, sum);
+        return;
+    }
+    if (kState && a.state.mode == kMerged) join<C>(a, tok, h, D, C * lane, v, m, sum);
+    const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
+    const float inv = empty ? 0.f : 1.f / sum;
+    uint32_t *o32 = reinterpret_cast<uint32_t *>(a.o + tok * a.os0 + h * a.os1 + C * lane);
+#pragma unroll
+    for (int e = 0; e < C; e += 2) o32[e / 2] = empty ? 0u : ptx::pack_bf16x2(v[e] * inv, v[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // This share's state is written (by these 128 threads): mark it, and merge what is complete, by

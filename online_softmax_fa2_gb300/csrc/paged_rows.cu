@@ -66,7 +66,8 @@ constexpr int smem_bytes() {
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-template <int D>
+// kState: with states of the packed tokens' rows (paged_state.cuh).
+template <int D, bool kState>
 __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
     using L = Rows<D>;
@@ -313,11 +314,25 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * e + g;
             if (r >= rows) continue;
-            const float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
+            float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             if (whole) {
+                const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
+                if (kState) {
+                    Weights jw{1.f, 0.f};
+                    if (a.state.mode == kMerged) jw = join_ml(a, tok, h, m[e], sum);
+                    else if (warp == 0 && t == 0) write_state_ml(a, tok, h, m[e], sum);
+#pragma unroll
+                    for (int nt = 0; nt < DW / 8; ++nt) {
+                        float v[2] = {o[nt][2 * e], o[nt][2 * e + 1]};
+                        if (a.state.mode == kWritten) write_state<2>(a, tok, h, D, warp * DW + 2 * t + 8 * nt, v, sum);
+                        else join_u<2>(a, tok, h, D, warp * DW + 2 * t + 8 * nt, jw, v);
+                        o[nt][2 * e] = v[0];
+                        o[nt][2 * e + 1] = v[1];
+                    }
+                    if (a.state.mode == kWritten) continue;
+                }
                 const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
                 const float inv = empty ? 0.f : 1.f / sum;
-                const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                 __nv_bfloat16 *orow = a.o + tok * a.os0 + h * a.os1 + warp * DW + 2 * t;
 #pragma unroll
                 for (int nt = 0; nt < DW / 8; ++nt)
@@ -341,10 +356,9 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     return true;
                 },
                 [&](int n, int to, auto slot) {
-                    merge_parts<D, 2, 8>(a, rows, n, to, threadIdx.x, slot, [&](int r, __nv_bfloat16 *&orow, float *&lse) {
-                        const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
-                        orow = a.o + tok * a.os0 + h * a.os1;
-                        lse = a.lse ? a.lse + (long long)tok * a.Hq + h : nullptr;
+                    merge_parts<D, 2, 8>(a, rows, n, to, threadIdx.x, slot, [&](int r, float (&v)[D / 32], float mx, float sum) {
+                        const int tg = div_g(a, row0 + r);
+                        end_row<D, kState>(a, p.seq.q0 + tg, p.hk * a.G + row0 + r - tg * a.G, v, mx, sum);
                     });
                 });
     }
@@ -352,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
 
 template <int D>
 attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int grid, cudaStream_t st) {
-    auto kern = paged_rows_kernel<D>;
+    auto kern = a.state.mode == kNone ? paged_rows_kernel<D, false> : paged_rows_kernel<D, true>;
     const int smem = smem_bytes<D>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);

@@ -29,6 +29,17 @@ constexpr long long kLongestLine = 0x7fff0000;  // tiles of a line, so that a di
 constexpr size_t kCutBytes = 32;  // a share's record of the item that it cuts (paged_tc_sm103.cu)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
+// The states of all packed tokens' rows over keys that another call holds (a shared prefix): ml [T][Hq], u
+// [T][Hq][D].  Written in place of the outputs by the call over those keys, merged into the outputs by the other.
+struct State {
+    int mode;      // kNone, kWritten, kMerged
+    int P;         // (merged) tokens cu[0] .. cu[P] - 1 have one; cu null: all
+    const int *cu;
+    float2 *ml;
+    float *u;
+};
+constexpr int kNone = 0, kWritten = 1, kMerged = 2;
+
 struct Args {
     int B, T, Hq, Hkv, G, causal, R, kt;  // R rows a block, 2^kt keys a tile
     int page_log2, width, num_pages, min_share, min_cut, cost;
@@ -44,6 +55,10 @@ struct Args {
     unsigned long long tag;
     float *ml, *u;  // states: (m, l) [slot][R][2], u [slot][R][D]
     uint32_t *flags;
+    // a cache in 8 bits: its scale bytes and their strides (page, head)
+    const uint8_t *ks, *vs;
+    long long kss[2], vss[2];
+    State state;
 };
 
 __device__ __forceinline__ int div_g(const Args &a, int x) { return (int)bf16fwd::div_fast((uint32_t)x, a.g_m, a.g_s); }

@@ -37,7 +37,7 @@
 
 #include "fwd_bf16_common.cuh"
 #include "paged.h"
-#include "paged_sched.cuh"
+#include "paged_state.cuh"
 
 namespace attn {
 
@@ -228,7 +228,72 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
     if (lse) *lse = empty ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
 }
 
-template <int D, int NT, int QR>
+// The same of a row that leaves its state, or starts from one (paged_state.cuh); tok < 0: no row.
+template <int D>
+__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, int tok, int h) {
+    paged::Weights w{1.f, 0.f};
+    const bool on = tok >= 0, keep = a.state.mode == paged::kWritten;
+    if (on && keep) paged::write_state_ml(a, tok, h, m, sum);
+    if (on && !keep) w = paged::join_ml(a, tok, h, m, sum);
+    const bool empty = sum == 0.f;  // a NaN is no empty row
+    const float inv = empty ? 0.f : 1.f / sum;
+#pragma unroll 1
+    for (int cc = 0; cc < D / 16; ++cc) {
+        uint32_t ov[16];
+        tmem_ld16(taddr + cc * 16, ov);
+        ptx::tmem_ld_wait();
+        float v[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            asm volatile("" : "+r"(ov[t]));
+            v[t] = __uint_as_float(ov[t]);
+        }
+        if (on && keep) paged::write_state<16>(a, tok, h, D, cc * 16, v, sum);
+        if (on && !keep) {
+            paged::join_u<16>(a, tok, h, D, cc * 16, w, v);
+            uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 16);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv);
+                to[t] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+        }
+        __syncwarp();  // the next columns are loaded by the whole warp
+    }
+    if (on && !keep && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// And of one that sees no key here.
+template <int D>
+__device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int h) {
+    float m = -INFINITY, sum = 0.f;
+    paged::Weights w{0.f, 0.f};
+    const bool keep = a.state.mode == paged::kWritten;
+    if (keep) paged::write_state_ml(a, tok, h, m, sum);
+    else w = paged::join_ml(a, tok, h, m, sum);
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 8) {
+        float v[8] = {};
+        if (keep) {
+            paged::write_state<8>(a, tok, h, D, c, v, sum);
+            continue;
+        }
+        w.own = 0.f;
+        paged::join_u<8>(a, tok, h, D, c, w, v);
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+        *reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    }
+    if (!keep && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// kState: with states of the packed tokens' rows.
+template <int D, int NT, int QR, bool kState>
 __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
@@ -532,11 +597,17 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             const bool first = w.j0 == 0;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
+            int to_tok = -1, to_head = 0;
             if (mine) {
                 const long long t = w.seq.q0 + tok;
                 const int h = w.hk * a.G + i - tok * a.G;
-                orow = a.o + t * a.os0 + h * a.os1;
-                lrow = a.lse ? a.lse + t * a.Hq + h : nullptr;
+                if (kState) {
+                    to_tok = (int)t;
+                    to_head = h;
+                } else {
+                    orow = a.o + t * a.os0 + h * a.os1;
+                    lrow = a.lse ? a.lse + t * a.Hq + h : nullptr;
+                }
             }
             // the next block's queries, under the last product of this one (this tile's last S, the
             // buffer's last reader, is done)
@@ -544,14 +615,18 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             if (more && has_tile(w)) bring_q(w);
             if (n == 0) {
                 // no key tile here: the item's first share writes rows that see no key at all
-                if (tx == 0 && first && mine) bf16fwd::write_empty_row<D>(orow, lrow);
+                if (tx == 0 && first && mine) {
+                    if (kState) end_empty_row<D>(a, to_tok, to_head);
+                    else bf16fwd::write_empty_row<D>(orow, lrow);
+                }
                 continue;
             }
             if (!wait_warp(&ctrl->o_final[X], oph)) { ok = false; break; }
             oph ^= 1;
             ptx::tc_fence_after();
             if (whole) {
-                write_rows<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
+                if (kState) end_row<D>(a, lane_addr + o_col, l_run, m_run, to_tok, to_head);
+                else write_rows<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
                 ptx::tc_fence_before();
                 continue;
             }
@@ -592,7 +667,7 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
 // warpgroup merging 128 rows took 8 to 11 us.  No CTA of it finds room on an SM before the attention
 // kernel's are done, so what it has to know is written down for it (Cut) instead of searched for.
 constexpr int kMergeCols = 32;
-template <int D, int NT, int GR>
+template <int D, int NT, int GR, bool kState>
 __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a) {
     static_assert(GR == 1 || GR == 4, "the sums below");
     __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][kMergeCols + 1];
@@ -653,6 +728,15 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
         }
     }
     if (g > 0 || !mine) return;
+    if (kState) {
+        const int tk = paged::div_g(a, row), hd = c1.y * a.G + row - tk * a.G, at = c1.x + tk;
+        if (a.state.mode == paged::kWritten) {
+            paged::write_state<kMergeCols>(a, at, hd, D, col, v, sum);
+            if (col == 0) paged::write_state_ml(a, at, hd, M, sum);
+            return;
+        }
+        paged::join<kMergeCols>(a, at, hd, D, col, v, M, sum);
+    }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
     const int tok = paged::div_g(a, row), h = c1.y * a.G + row - tok * a.G;
@@ -671,14 +755,17 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
 template <int D, int NT, int QR>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
                      bool cuts, bool many, cudaStream_t st) {
-    auto kern = paged_tc_kernel<D, NT, QR>;
+    const bool state = a.state.mode != paged::kNone;
+    auto kern = state ? paged_tc_kernel<D, NT, QR, true> : paged_tc_kernel<D, NT, QR, false>;
+    auto merge1 = state ? paged_tc_merge_kernel<D, NT, 1, true> : paged_tc_merge_kernel<D, NT, 1, false>;
+    auto merge4 = state ? paged_tc_merge_kernel<D, NT, 4, true> : paged_tc_merge_kernel<D, NT, 4, false>;
     int smem = Layout<D, NT, QR>::kBytes;
     if (NT == 2 && smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT)), smem, st, mq, mk, mv, a);
     if (e == cudaSuccess && cuts)
-        e = many ? launch_pdl(paged_tc_merge_kernel<D, NT, 4>, dim3(grid, NT, D / kMergeCols), dim3(4 * BQ), 0, st, a)
-                 : launch_pdl(paged_tc_merge_kernel<D, NT, 1>, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
+        e = many ? launch_pdl(merge4, dim3(grid, NT, D / kMergeCols), dim3(4 * BQ), 0, st, a)
+                 : launch_pdl(merge1, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
 template <int D>

@@ -17,6 +17,8 @@
 #include <cuda_bf16.h>
 
 #include "fwd_bf16_common.cuh"
+#include "paged_tokens.cuh"
+#include "q8.cuh"
 #include "qk_rope.h"
 #include "sm100_ptx.cuh"
 #include "warp_mma.cuh"
@@ -214,12 +216,58 @@ __device__ __forceinline__ void scale8(float *d, const float *x, float c) {
     for (int t = 0; t < 8; t += 2) mul2(d[t], d[t + 1], x[t], x[t + 1], c, c);
 }
 
+// Where a row goes: as T, or as codes and a scale byte.  Called by the whole warp, f the lane's 16 elements
+// (zeros without a row), on where it has some to store.
+template <typename T>
+struct ToRows {
+    T *out;
+    long long out_h;
+    __device__ __forceinline__ void operator()(int u, float (&f)[16], const Lane &ln, bool on) const {
+        if (!on) return;
+        Row2<T> y;
+        y.set(f);
+        y.store(out + u * out_h, ln.e0, ln.e1);
+    }
+};
+template <int L>
+struct ToCodes {
+    uint8_t *out, *scale;
+    long long out_h, scale_h;
+    __device__ __forceinline__ static float largest(const float (&f)[16]) {  // of the group; a NaN is passed over
+        float m = 0.f;
+#pragma unroll
+        for (int t = 0; t < 16; ++t) m = fmaxf(m, fabsf(f[t]));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
+    __device__ __forceinline__ void operator()(int u, float (&f)[16], const Lane &ln, bool on) const {
+        float m = largest(f);
+        if (__any_sync(0xffffffffu, isinf(m))) {  // e4m3 has no infinity: it becomes a NaN
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+                if (isinf(f[t])) f[t] = NAN;
+            m = largest(f);
+        }
+        const uint32_t e = q8::scale_byte(m);
+        const float s = q8::inverse(e);
+        scale8(f, f, s);
+        scale8(f + 8, f + 8, s);
+        if (!on) return;
+        uint8_t *row = out + u * out_h;
+        *reinterpret_cast<uint2 *>(row + ln.e0) = make_uint2(q8::encode4(f[0], f[1], f[2], f[3]), q8::encode4(f[4], f[5], f[6], f[7]));
+        *reinterpret_cast<uint2 *>(row + ln.e1) =
+            make_uint2(q8::encode4(f[8], f[9], f[10], f[11]), q8::encode4(f[12], f[13], f[14], f[15]));
+        if ((threadIdx.x & (L - 1)) == 0) scale[u * scale_h] = (uint8_t)e;
+    }
+};
+
 // `count` (0 to U) consecutive heads of one tensor at one token, the group's own.  The norm's weight
 // goes into the angles once for all of them: with (a, b) = r (x_a w_a, x_b w_b),
 //   y_a = r (x_a (w_a cos) - x_b (w_b sin)),  y_b = r (x_a (w_a sin) + x_b (w_b cos)).
 // (The shuffles need the whole warp: rows past count are zeros.)
-template <typename T, int L, int U, bool kInter>
-__device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, long long out_h, const T *w,
+template <typename T, int L, int U, bool kInter, class Store>
+__device__ __forceinline__ void norm_rows(const T *in, long long in_h, const Store &store, const T *w,
                                           const float *angle_row, int count, const Lane &ln, int rot, float inv_d,
                                           float eps) {
     Row2<T> x[U], wr;
@@ -265,10 +313,7 @@ __device__ __forceinline__ void norm_rows(const T *in, long long in_h, T *out, l
         mul8(z + 8, y + 8, bc);
         if (ln.turn) fma8(z + 8, y, as, z + 8);
         together<kInter>(z, f);
-        if (ln.on && u < count) {
-            x[u].set(f);
-            x[u].store(out + u * out_h, ln.e0, ln.e1);
-        }
+        store(u, f, ln, ln.on && u < count);
     }
 }
 
@@ -280,6 +325,18 @@ __device__ __forceinline__ void copy_rows(const T *in, long long in_h, T *out, l
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (ln.on && u < count) x[u].store(out + u * out_h, ln.e0, ln.e1);
+}
+template <typename T, int L, int U>
+__device__ __forceinline__ void quantise_rows(const T *in, long long in_h, const ToCodes<L> &store, int count, const Lane &ln) {
+    Row2<T> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float f[16];
+        x[u].get(f);
+        store(u, f, ln, ln.on && u < count);
+    }
 }
 
 // Division by a number that the host knows (fast_div_params of fwd_bf16_common.cuh).
@@ -299,25 +356,6 @@ __device__ __forceinline__ int table_row(long long pos, int P, uint32_t *flags, 
     if (pos >= 0 && pos < P) return (int)pos;
     if (report) atomicOr(flags, kFlagBadIndex);
     return pos < 0 ? 0 : P - 1;
-}
-
-// The sequence of packed token t: the number of entries of cu[1 .. B] that are <= t (cu does not
-// decrease), two rounds of 32 probes a warp for up to 1024 sequences.  B when t lies behind the
-// last sequence.
-__device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = B;  // the answer is lo + (entries <= t among cu[lo + 1 .. lo + n])
-    while (n > 32) {
-        const int step = (n + 31) / 32, at = min((lane + 1) * step, n);
-        const int hits = __popc(__ballot_sync(0xffffffffu, __ldg(cu + lo + at) <= t));
-        // probes are ordered: the first `hits` of them hold
-        const int skip = min(hits * step, n);
-        lo += skip;
-        n = min(step, n - skip);
-        if (hits == 32) return lo;
-    }
-    const bool le = lane < n && __ldg(cu + lo + 1 + lane) <= t;
-    return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
 // A group takes a unit: U consecutive heads of one tensor at one token.  The units of all tokens form
@@ -362,10 +400,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         if (a.pos) pos = __ldg(a.pos + b * a.pos_s[0] + n * a.pos_s[1]);
         row = a.cs + table_row(pos, a.P, a.flags, count > 0 && h0 == 0 && (threadIdx.x & (L - 1)) == 0) * a.cs_row;
     }
+    const ToRows<T> store{static_cast<T *>(a.o[s]) + b * a.os[s][0] + n * a.os[s][1] + h0 * a.os[s][2], a.os[s][2]};
     norm_rows<T, L, U, kInter>(static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1] + h0 * a.xs[s][2],
-                               a.xs[s][2],
-                               static_cast<T *>(a.o[s]) + b * a.os[s][0] + n * a.os[s][1] + h0 * a.os[s][2], a.os[s][2],
-                               static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
+                               a.xs[s][2], store, static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
 }
 
 // A warp takes one token, a tensor (q, k, v) and the part of its heads that its groups hold at once
@@ -383,12 +420,14 @@ struct AppendArgs {
     long long cs_row;
     const int *pos, *bt, *lens, *cu;
     long long bt_s;
+    uint8_t *scales[2];  // of a cache in 8 bits: k, v
+    long long scale_s[2][2];
     unsigned cu_groups, cu_step;  // groups of 32 sequences, and the warps that look at their entries of cu
     int pages, page_size, width;
     uint32_t *flags;
 };
 
-template <typename T, int L, int U, bool kInter>
+template <typename T, int L, int U, bool kInter, bool kQ8>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a) {
     ptx::grid_dep_wait();
     ptx::launch_dependents();
@@ -398,26 +437,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const int t = (int)(task / per), part = (int)(task - (unsigned)t * per);
     const bool report = part == 0 && (threadIdx.x & 31) == 0;
     int b, i, nq;
-    if (a.cu) {
-        // Entries that are out of range or decrease are reported whatever tokens they belong to: the
-        // first warps of the grid look at 32 of them each.
-        for (unsigned e = task; e < a.cu_groups; e += a.cu_step) {
-            const int at = min((int)e * 32 + (threadIdx.x & 31), a.B - 1);
-            const int r0 = __ldg(a.cu + at), r1 = __ldg(a.cu + at + 1);
-            if (r0 < 0 || r1 < r0 || r1 > a.T) atomicOr(a.flags, kFlagBadIndex);
-        }
-        b = find_sequence(a.cu, a.B, t);
-        if (b >= a.B) return;  // behind the last sequence: left as it was
-        // the sequence's tokens as the attention takes them (seq_info of paged_sched.cuh)
-        const int c0 = min(max(__ldg(a.cu + b), 0), a.T);
-        nq = min(max(__ldg(a.cu + b + 1), c0), a.T) - c0;
-        i = t - c0;
-        if (i < 0 || i >= nq) return;  // before the first sequence, or cu_q decreases: left as it was
-    } else {
-        nq = a.T / a.B;
-        b = t / nq;
-        i = t - b * nq;
-    }
+    if (a.cu) report_bad_entries(a.cu, a.B, a.T, task, a.cu_groups, a.cu_step, a.flags);
+    if (!find_token(a.cu, a.B, a.T, t, b, i, nq)) return;  // left as it was
     const int room = a.width * a.page_size, raw = __ldg(a.lens + b), len = min(max(raw, 0), room);
     if (report && len != raw) atomicOr(a.flags, kFlagKvLenClamped);
     const int at = len - nq + i;  // the token's place in its sequence; < 0: it has none
@@ -430,8 +451,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const int h0 = ((part - (s == 0 ? 0 : s == 1 ? a.cq : a.cq + a.ck)) * (32 / L) + (threadIdx.x & 31) / L) * U;
     const int count = min(max(H - h0, 0), U), h = count > 0 ? h0 : 0;
     if (s == 0) {
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0] + h * a.qs[1], a.qs[1],
-                                   static_cast<T *>(a.qo) + t * a.qos[0] + h * a.qos[1], a.qos[1],
+        const ToRows<T> store{static_cast<T *>(a.qo) + t * a.qos[0] + h * a.qos[1], a.qos[1]};
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0] + h * a.qs[1], a.qs[1], store,
                                    static_cast<const T *>(a.wq), row, count, ln, a.rot, a.inv_d, a.eps);
         return;
     }
@@ -442,11 +463,23 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         return;
     }
     const long long slot = at % a.page_size;
-    if (s == 1)
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1],
-                                   static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1] + h * a.kps[2], a.kps[2],
+    if constexpr (kQ8) {
+        const int x = s - 1;
+        const long long *ps = x ? a.vps : a.kps;
+        const ToCodes<L> store{static_cast<uint8_t *>(x ? a.vp : a.kp) + page * ps[0] + slot * ps[1] + h * ps[2],
+                               a.scales[x] + page * a.scale_s[x][0] + h * a.scale_s[x][1] + slot, ps[2], a.scale_s[x][1]};
+        if (s == 1)
+            norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1], store,
+                                       static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
+        else
+            quantise_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0] + h * a.vs[1], a.vs[1], store, count, ln);
+        return;
+    }
+    if (s == 1) {
+        const ToRows<T> store{static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1] + h * a.kps[2], a.kps[2]};
+        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1], store,
                                    static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
-    else
+    } else
         copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0] + h * a.vs[1], a.vs[1],
                            static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1] + h * a.vps[2], a.vps[2], count, ln);
 }
@@ -795,11 +828,16 @@ auto rope_kernel(int L, int U) -> void (*)(const RopeArgs) {
     if (L == 8) return U == 2 ? qk_norm_rope_kernel<T, 8, 2, kInter> : qk_norm_rope_kernel<T, 8, 1, kInter>;
     return U == 2 ? qk_norm_rope_kernel<T, 16, 2, kInter> : qk_norm_rope_kernel<T, 16, 1, kInter>;
 }
-template <typename T, bool kInter>
+template <typename T, bool kInter, bool kQ8>
 auto append_kernel(int L, int U) -> void (*)(const AppendArgs) {
-    if (L == 4) return U == 2 ? paged_append_kernel<T, 4, 2, kInter> : paged_append_kernel<T, 4, 1, kInter>;
-    if (L == 8) return U == 2 ? paged_append_kernel<T, 8, 2, kInter> : paged_append_kernel<T, 8, 1, kInter>;
-    return U == 2 ? paged_append_kernel<T, 16, 2, kInter> : paged_append_kernel<T, 16, 1, kInter>;
+    if (L == 4) return U == 2 ? paged_append_kernel<T, 4, 2, kInter, kQ8> : paged_append_kernel<T, 4, 1, kInter, kQ8>;
+    if (L == 8) return U == 2 ? paged_append_kernel<T, 8, 2, kInter, kQ8> : paged_append_kernel<T, 8, 1, kInter, kQ8>;
+    return U == 2 ? paged_append_kernel<T, 16, 2, kInter, kQ8> : paged_append_kernel<T, 16, 1, kInter, kQ8>;
+}
+template <bool kQ8>
+auto append_kernel(bool half, bool inter, int L, int U) -> void (*)(const AppendArgs) {
+    return inter ? (half ? append_kernel<__nv_bfloat16, true, kQ8>(L, U) : append_kernel<float, true, kQ8>(L, U))
+                 : (half ? append_kernel<__nv_bfloat16, false, kQ8>(L, U) : append_kernel<float, false, kQ8>(L, U));
 }
 // The backward's kernel, the heads a group takes at once, the groups of a warp, and its shared memory.
 struct BwdPick {
@@ -893,8 +931,8 @@ attn_status_t launch_qk_norm_rope_bwd(const attn_qk_norm_rope_bwd_params_t &bp, 
                     "qk_norm_rope_bwd weights");
 }
 
-attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStream_t st) {
-    AppendArgs a;
+attn_status_t launch_paged_append(const attn_paged_append_params_t &p, const attn_paged_scales_t *scales, cudaStream_t st) {
+    AppendArgs a{};
     const attn_paged_cache_t &c = p.cache;
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hk = (int)c.Hkv; a.d = (int)c.d;
     a.rot = p.cos_sin ? (int)p.rot : 0;
@@ -904,6 +942,11 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     copy3(a.kps, c.k_stride); copy3(a.vps, c.v_stride);
     a.cs = p.cos_sin; a.cs_row = p.cos_sin_stride; a.pos = p.positions;
     a.bt = c.block_table; a.bt_s = c.table_stride; a.lens = c.kv_lens; a.cu = c.cu_q;
+    if (scales) {
+        a.scales[0] = static_cast<uint8_t *>(scales->k);
+        a.scales[1] = static_cast<uint8_t *>(scales->v);
+        copy2(a.scale_s[0], scales->k_stride); copy2(a.scale_s[1], scales->v_stride);
+    }
     a.pages = (int)c.num_pages; a.page_size = c.page_size; a.width = (int)c.table_width;
     a.flags = device_flags();
     if (!a.flags) return fail(ATTN_ERR_CUDA, "could not resolve the device error word");
@@ -917,8 +960,7 @@ attn_status_t launch_paged_append(const attn_paged_append_params_t &p, cudaStrea
     a.cu_groups = (unsigned)((a.B + 31) / 32);
     a.cu_step = a.tasks < a.cu_groups ? (unsigned)a.tasks : a.cu_groups;
     const dim3 grid((unsigned)((a.tasks + kWarps - 1) / kWarps));
-    auto kern = p.interleaved ? (h ? append_kernel<__nv_bfloat16, true>(L, U) : append_kernel<float, true>(L, U))
-                              : (h ? append_kernel<__nv_bfloat16, false>(L, U) : append_kernel<float, false>(L, U));
+    auto kern = scales ? append_kernel<true>(h, p.interleaved, L, U) : append_kernel<false>(h, p.interleaved, L, U);
     return launched(launch_pdl(kern, grid, dim3(kThreads), 0, st, a), "paged_append");
 }
 

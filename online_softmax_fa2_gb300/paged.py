@@ -4,11 +4,19 @@
     dq, dk, dwq, dwk = attn_qk_norm_rope_bwd(q, k, dq2, dk2, wq, wk, cos_sin)
     q2 = attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq=..., wk=..., cos_sin=...)
     o, lse = attn_paged_fwd(q2, k_pages, v_pages, block_table, kv_lens, cu_q, max_q=...)
+    # the cache in 8 bits: codes (float8_e4m3fn) and a scale byte a row (float8_e8m0fnu)
+    q2 = attn_paged_append_q8(q, k, v, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, wq=..., ...)
+    o, lse = attn_paged_fwd_q8(q2, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, max_q=...)
+    k, v = attn_paged_read_q8(k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, rows, cu_k)
+    # sequences behind shared prefixes, each read once
+    o, lse = attn_paged_prefix_fwd(q2, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q, cu_prefix)
 
 Shapes: q [B, N, Hq, d] and k [B, N, Hkv, d] for the first two; packed tokens q [T, Hq, d], k and
 v [T, Hkv, d] for the others, with k_pages and v_pages [num_pages, page_size, Hkv, d],
 block_table int32 [B, width], kv_lens int32 [B] (the new tokens included) and cu_q int32 [B + 1]
 (None: T / B new tokens in every sequence).  Any strides with the last dimension contiguous.
+A cache in 8 bits has pages of torch.float8_e4m3fn and scales [num_pages, Hkv, page_size] of
+torch.float8_e8m0fnu (torch.uint8 does for either); an element is code * 2^(scale byte - 127).
 The names' kernels and rules are those of include/attn.h.
 
 A call runs on torch's current stream of the tensors' device, which need not be the current
@@ -26,7 +34,9 @@ import torch
 import online_softmax_fa2_gb300 as _ofa
 
 __all__ = ["attn_qk_norm_rope", "attn_qk_norm_rope_bwd", "attn_paged_append", "attn_paged_fwd",
-           "paged_fwd_workspace_bytes", "qk_norm_rope_bwd_workspace_bytes"]
+           "attn_paged_append_q8", "attn_paged_read_q8", "attn_paged_fwd_q8", "attn_paged_prefix_fwd",
+           "paged_fwd_workspace_bytes", "paged_fwd_q8_workspace_bytes", "paged_prefix_fwd_workspace_bytes",
+           "qk_norm_rope_bwd_workspace_bytes"]
 
 _i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 _S2, _S3 = _i64 * 2, _i64 * 3
@@ -76,6 +86,32 @@ class PagedFwdParams(ctypes.Structure):
                 ("q", _vp), ("o", _vp), ("q_stride", _S2), ("o_stride", _S2), ("lse", _vp)]
 
 
+class PagedScales(ctypes.Structure):
+    """Mirror of attn_paged_scales_t (include/attn.h)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_stride", _S2), ("v_stride", _S2)]
+
+
+class PagedAppendQ8Params(ctypes.Structure):
+    """Mirror of attn_paged_append_q8_params_t (include/attn.h)."""
+    _fields_ = [("append", PagedAppendParams), ("scales", PagedScales)]
+
+
+class PagedReadQ8Params(ctypes.Structure):
+    """Mirror of attn_paged_read_q8_params_t (include/attn.h)."""
+    _fields_ = [("cache", PagedCache), ("scales", PagedScales), ("k", _vp), ("v", _vp), ("k_stride", _S2), ("v_stride", _S2)]
+
+
+class PagedFwdQ8Params(ctypes.Structure):
+    """Mirror of attn_paged_fwd_q8_params_t (include/attn.h)."""
+    _fields_ = [("fwd", PagedFwdParams), ("scales", PagedScales)]
+
+
+class PagedPrefixParams(ctypes.Structure):
+    """Mirror of attn_paged_prefix_params_t (include/attn.h)."""
+    _fields_ = [("fwd", PagedFwdParams), ("scales", PagedScales), ("P", _i64), ("prefix_width", _i64), ("prefix_stride", _i64),
+                ("prefix_table", _vp), ("prefix_lens", _vp), ("cu_prefix", _vp)]
+
+
 def _packer(cls):
     """struct.Struct of a mirror's fields in order (nested ones in place), C alignment: filling it takes
     a third of the time that filling the mirror takes, and a small call is as long as its host side."""
@@ -96,6 +132,8 @@ def _packer(cls):
 
 _pack_norm_rope, _pack_norm_rope_bwd = _packer(NormRopeParams), _packer(NormRopeBwdParams)
 _pack_append, _pack_fwd = _packer(PagedAppendParams), _packer(PagedFwdParams)
+_pack_append_q8, _pack_read_q8 = _packer(PagedAppendQ8Params), _packer(PagedReadQ8Params)
+_pack_fwd_q8, _pack_prefix = _packer(PagedFwdQ8Params), _packer(PagedPrefixParams)
 
 
 class _Block:
@@ -119,7 +157,13 @@ def _load():
                 ("attn_qk_norm_rope_bwd", [params, _vp, size, _vp], _i32),
                 ("attn_paged_append", [params, _vp], _i32),
                 ("attn_paged_fwd_workspace_bytes", [params], size),
-                ("attn_paged_fwd", [params, _vp, size, _vp], _i32)):
+                ("attn_paged_fwd", [params, _vp, size, _vp], _i32),
+                ("attn_paged_append_q8", [params, _vp], _i32),
+                ("attn_paged_read_q8", [params, _vp], _i32),
+                ("attn_paged_fwd_q8_workspace_bytes", [params], size),
+                ("attn_paged_fwd_q8", [params, _vp, size, _vp], _i32),
+                ("attn_paged_prefix_fwd_workspace_bytes", [params], size),
+                ("attn_paged_prefix_fwd", [params, _vp, size, _vp], _i32)):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, res
         _lib = lib
@@ -127,6 +171,7 @@ def _load():
 
 
 _DTYPES = {torch.float32: _ofa.F32, torch.bfloat16: _ofa.BF16}
+_CODES, _SCALES = (torch.float8_e4m3fn, torch.uint8), (torch.float8_e8m0fnu, torch.uint8)
 _BAD = "{} must be {} {} on cuda:{} with the last dimension contiguous, got {} {} with strides {} on {}"
 
 
@@ -282,13 +327,18 @@ def _workspace(t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q):
-    """The values of attn_paged_cache_t, in order."""
+def _one_of(t, dtypes):
+    """t's dtype where it is one of dtypes, else the first of them (which a check then asks for)."""
+    return t.dtype if t.dtype in dtypes else dtypes[0]
+
+
+def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q, q8=False):
+    """The values of attn_paged_cache_t, in order.  q8: pages of codes."""
     if k_pages.dim() != 4 or k_pages.shape[3] != d:
         raise ValueError(f"k_pages must be [num_pages, page_size, Hkv, {d}], got {tuple(k_pages.shape)}")
     pages, page, Hkv, _ = shape = k_pages.shape
-    kp, (k0, k1, k2, _) = _need(k_pages, "k_pages", shape, dt, dev)
-    vp, (v0, v1, v2, _) = _need(v_pages, "v_pages", shape, dt, dev)
+    kp, (k0, k1, k2, _) = _need(k_pages, "k_pages", shape, _one_of(k_pages, _CODES) if q8 else dt, dev)
+    vp, (v0, v1, v2, _) = _need(v_pages, "v_pages", shape, _one_of(v_pages, _CODES) if q8 else dt, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, width]")
     B, width = table = block_table.shape
@@ -296,6 +346,32 @@ def _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q):
     lens, _ = _need(kv_lens, "kv_lens", (B,), torch.int32, dev)
     cu = 0 if cu_q is None else _need(cu_q, "cu_q", (B + 1,), torch.int32, dev)[0]
     return _DTYPES[dt], page, B, T, Hkv, d, kp, vp, k0, k1, k2, v0, v1, v2, pages, bt, width, row, lens, cu
+
+
+def _scales(k_scales, v_scales, k_pages, dev):
+    """The values of attn_paged_scales_t, in order."""
+    pages, page, Hkv, _ = k_pages.shape
+    kp, (k0, k1, _) = _need(k_scales, "k_scales", (pages, Hkv, page), _one_of(k_scales, _SCALES), dev)
+    vp, (v0, v1, _) = _need(v_scales, "v_scales", (pages, Hkv, page), _one_of(v_scales, _SCALES), dev)
+    return kp, vp, k0, k1, v0, v1
+
+
+def _append_params(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin, positions, eps, interleaved,
+                   q_out, q8):
+    """The values of attn_paged_append_params_t, in order."""
+    dev, dt = _device(q, 3), q.dtype
+    T, Hq, d = shape = q.shape
+    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q, q8)
+    sk = (T, c[4], d)
+    cs, rows, row, rot = _angles(cos_sin, dev)
+    qp, (q0, q1, _) = _need(q, "q", shape, dt, dev)
+    kp, (k0, k1, _) = _need(k, "k", sk, dt, dev)
+    vp, (v0, v1, _) = _need(v, "v", sk, dt, dev)
+    op, (o0, o1, _) = _need(q_out, "q_out", shape, dt, dev)
+    return (*c, Hq, rot, qp, kp, vp, op, q0, q1, k0, k1, v0, v1, o0, o1, _weight(wq, "wq", d, dt, dev),
+            _weight(wk, "wk", d, dt, dev), cs, rows, row,
+            0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev)[0], eps,
+            1 if interleaved else 0)
 
 
 def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None, wq=None, wk=None, cos_sin=None,
@@ -308,30 +384,63 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
         return _on(stream, q, attn_paged_append, q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin,
                    positions, eps, interleaved, q_out)
     lib = _load()
-    dev, dt = _device(q, 3), q.dtype
-    T, Hq, d = shape = q.shape
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dt, device=q.device)
-    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
-    sk = (T, c[4], d)
-    cs, rows, row, rot = _angles(cos_sin, dev)
-    qp, (q0, q1, _) = _need(q, "q", shape, dt, dev)
-    kp, (k0, k1, _) = _need(k, "k", sk, dt, dev)
-    vp, (v0, v1, _) = _need(v, "v", sk, dt, dev)
-    op, (o0, o1, _) = _need(q_out, "q_out", shape, dt, dev)
-    p = _pack_append(*c, Hq, rot, qp, kp, vp, op, q0, q1, k0, k1, v0, v1, o0, o1, _weight(wq, "wq", d, dt, dev),
-                     _weight(wk, "wk", d, dt, dev), cs, rows, row,
-                     0 if positions is None else _need(positions, "positions", (T,), torch.int32, dev)[0], eps,
-                     1 if interleaved else 0)
-    _call(dev, lib.attn_paged_append, p)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p = _pack_append(*_append_params(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin, positions, eps,
+                                     interleaved, q_out, False))
+    _call(q.get_device(), lib.attn_paged_append, p)
     return q_out
 
 
-def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse):
-    """attn_paged_fwd_params_t, packed."""
+def attn_paged_append_q8(q, k, v, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q=None, wq=None, wk=None,
+                         cos_sin=None, positions=None, eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """attn_paged_append into a cache in 8 bits: codes and scales are written in place, one power of two a
+    row.  See include/attn.h, attn_paged_append_q8."""
+    if stream is not None:
+        return _on(stream, q, attn_paged_append_q8, q, k, v, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, wq,
+                   wk, cos_sin, positions, eps, interleaved, q_out)
+    lib = _load()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p = _append_params(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin, positions, eps, interleaved, q_out,
+                       True)
+    dev = q.get_device()
+    _call(dev, lib.attn_paged_append_q8, _pack_append_q8(*p, *_scales(k_scales, v_scales, k_pages, dev)))
+    return q_out
+
+
+def attn_paged_read_q8(k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, rows, cu_k=None, dtype=torch.bfloat16,
+                       k_out=None, v_out=None, stream=None):
+    """Keys and values of a cache in 8 bits as packed rows [rows, Hkv, d] of dtype (bfloat16 or float32): rows
+    cu_k[b] .. cu_k[b + 1] - 1 (int32 [B + 1]; None: rows / B each) are the last ones of sequence b.  Rows of
+    no sequence are left as they were.  Returns (k_out, v_out), which may be given.  See include/attn.h,
+    attn_paged_read_q8."""
+    if stream is not None:
+        return _on(stream, k_pages, attn_paged_read_q8, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, rows, cu_k,
+                   dtype, k_out, v_out)
+    lib = _load()
+    dev = k_pages.get_device()
+    if dev < 0:
+        raise ValueError("every tensor must be on a CUDA device (there is no CPU path)")
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}: use torch.float32 or torch.bfloat16")
+    c = _cache(rows, k_pages.shape[-1], dtype, dev, k_pages, v_pages, block_table, kv_lens, cu_k, True)
+    shape = (rows, c[4], c[5])
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    kp, (k0, k1, _) = _need(k_out, "k_out", shape, dtype, dev)
+    vp, (v0, v1, _) = _need(v_out, "v_out", shape, dtype, dev)
+    _call(dev, lib.attn_paged_read_q8, _pack_read_q8(*c, *_scales(k_scales, v_scales, k_pages, dev), kp, vp, k0, k1, v0, v1))
+    return k_out, v_out
+
+
+def _paged_fwd_values(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse, q8=False):
+    """The values of attn_paged_fwd_params_t, in order."""
     dev, dt = _device(q, 3), q.dtype
     T, Hq, d = shape = q.shape
-    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q)
+    c = _cache(T, d, dt, dev, k_pages, v_pages, block_table, kv_lens, cu_q, q8)
     lp = op = o0 = o1 = 0
     if out is not None:
         op, (o0, o1, _) = _need(out, "out", shape, dt, dev)
@@ -342,8 +451,31 @@ def _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, ca
     if max_q is None:
         max_q = 0 if cu_q is not None else T // c[2] if c[2] else 0
     qp, (q0, q1, _) = _need(q, "q", shape, dt, dev)
-    return _pack_fwd(*c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q,
-                     qp, op, q0, q1, o0, o1, lp)
+    return (*c, 1 if causal else 0, 1.0 / math.sqrt(d) if scale is None else scale, Hq, max_q, qp, op, q0, q1, o0, o1, lp)
+
+
+def _paged_fwd_params(*args):
+    """attn_paged_fwd_params_t, packed."""
+    return _pack_fwd(*_paged_fwd_values(*args))
+
+
+def _outputs(q, out, lse):
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    return out, lse
+
+
+def _run(q, p, need, fn, workspace):
+    """fn with the packed p and a workspace of need(p) bytes where none is given."""
+    dev = q.get_device()
+    if workspace is None:
+        n = _bytes(dev, need, p)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    wsp, wsn = _workspace(workspace, dev)
+    _call(dev, fn, p, wsp, wsn)
 
 
 def paged_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=None, causal=True) -> int:
@@ -364,16 +496,74 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
         return _on(stream, q, attn_paged_fwd, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, workspace,
                    out, lse)
     lib = _load()
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    out, lse = _outputs(q, out, lse)
     p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse)
+    _run(q, p, lib.attn_paged_fwd_workspace_bytes, lib.attn_paged_fwd, workspace)
+    return out, lse
+
+
+def paged_fwd_q8_workspace_bytes(q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q=None, max_q=None,
+                                 causal=True) -> int:
+    """Bytes of workspace attn_paged_fwd_q8 needs for these arguments (the lengths' values play no part)."""
+    p = _paged_fwd_values(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, None, None, None, True)
     dev = q.get_device()
-    if workspace is None:
-        n = _bytes(dev, lib.attn_paged_fwd_workspace_bytes, p)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    wsp, wsn = _workspace(workspace, dev)
-    _call(dev, lib.attn_paged_fwd, p, wsp, wsn)
+    return int(_bytes(dev, _load().attn_paged_fwd_q8_workspace_bytes, _pack_fwd_q8(*p, *_scales(k_scales, v_scales, k_pages, dev))))
+
+
+def attn_paged_fwd_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q=None, max_q=None, causal=True,
+                      scale=None, workspace=None, out=None, lse=None, stream=None):
+    """attn_paged_fwd over a cache in 8 bits.  See include/attn.h, attn_paged_fwd_q8."""
+    if stream is not None:
+        return _on(stream, q, attn_paged_fwd_q8, q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, max_q, causal,
+                   scale, workspace, out, lse)
+    lib = _load()
+    out, lse = _outputs(q, out, lse)
+    p = _paged_fwd_values(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse, True)
+    p = _pack_fwd_q8(*p, *_scales(k_scales, v_scales, k_pages, q.get_device()))
+    _run(q, p, lib.attn_paged_fwd_q8_workspace_bytes, lib.attn_paged_fwd_q8, workspace)
+    return out, lse
+
+
+def _prefix_params(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q, cu_prefix, max_q, causal, scale,
+                   out, lse, k_scales, v_scales):
+    """attn_paged_prefix_params_t, packed."""
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales come together")
+    q8 = k_scales is not None
+    f = _paged_fwd_values(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse, q8)
+    dev = q.get_device()
+    if prefix_table.dim() != 2:
+        raise ValueError("prefix_table must be int32 [P, width]")
+    P, width = table = prefix_table.shape
+    pt, (row, _) = _need(prefix_table, "prefix_table", table, torch.int32, dev)
+    pl, _ = _need(prefix_lens, "prefix_lens", (P,), torch.int32, dev)
+    pc = 0 if cu_prefix is None else _need(cu_prefix, "cu_prefix", (P + 1,), torch.int32, dev)[0]
+    sc = _scales(k_scales, v_scales, k_pages, dev) if q8 else (0,) * 6
+    return _pack_prefix(*f, *sc, P, width, row, pt, pl, pc)
+
+
+def paged_prefix_fwd_workspace_bytes(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q=None,
+                                     cu_prefix=None, max_q=None, causal=True, k_scales=None, v_scales=None) -> int:
+    """Bytes of workspace attn_paged_prefix_fwd needs for these arguments (the lengths' values play no part)."""
+    p = _prefix_params(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q, cu_prefix, max_q, causal, None,
+                       None, None, k_scales, v_scales)
+    return int(_bytes(q.get_device(), _load().attn_paged_prefix_fwd_workspace_bytes, p))
+
+
+def attn_paged_prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q=None, cu_prefix=None,
+                          max_q=None, causal=True, scale=None, k_scales=None, v_scales=None, workspace=None, out=None, lse=None,
+                          stream=None):
+    """attn_paged_fwd for sequences that share prefixes: packed tokens cu_prefix[p] .. cu_prefix[p + 1] - 1
+    (int32 [P + 1]; None: T / P each) see all prefix_lens[p] (int32 [P]) keys of the pages prefix_table[p]
+    (int32 [P, width]) besides their sequence's own, which kv_lens, block_table and causal are about.  A prefix is
+    read once for all of its tokens.  With k_scales and v_scales the cache is one in 8 bits.  See include/attn.h,
+    attn_paged_prefix_fwd."""
+    if stream is not None:
+        return _on(stream, q, attn_paged_prefix_fwd, q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q,
+                   cu_prefix, max_q, causal, scale, k_scales, v_scales, workspace, out, lse)
+    lib = _load()
+    out, lse = _outputs(q, out, lse)
+    p = _prefix_params(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q, cu_prefix, max_q, causal, scale,
+                       out, lse, k_scales, v_scales)
+    _run(q, p, lib.attn_paged_prefix_fwd_workspace_bytes, lib.attn_paged_prefix_fwd, workspace)
     return out, lse
