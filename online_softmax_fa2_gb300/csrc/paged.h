@@ -23,7 +23,7 @@ attn_status_t launch_paged_rows(const CUtensorMap &mk, const CUtensorMap &mv, co
 constexpr int kRowsQ8Keys = 128;  // a tile of the few-rows kernel over a cache in 8 bits
 attn_status_t launch_paged_rows_q8(const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int d, int grid,
                                    cudaStream_t s);
-constexpr int kTcBoxKeys = 128;
+constexpr int kTcBoxKeys = 128, kTcQ8BoxKeys = 64;
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
                               int d, int tiles, int tile_rows, int grid, bool cuts, cudaStream_t s);
 // (tiles a block: 2 of up to 128 rows, or 1 of up to tile_rows, 64 or 128, with two CTAs an SM)

@@ -72,19 +72,6 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     return r * D + ((c ^ (D == 128 ? r & 7 : (r >> 1) & 3)) << 4);
 }
 
-// Untiled bulk copy global -> shared, completion counted on `bar` (bytes; all multiples of 16).
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(ptx::smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // d += a * b for one m16n8k16 tile of fp16
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -176,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     } else {
                         // (of a page out of range, whose codes are zeros, another page's scales)
                         const uint8_t *src = sc + (page < a.num_pages ? page : 0) * sc_page + p.hk * sc_head + slot;
-                        bulk_load(smem + L::kScaleOff + st * 2 * KT + (part & 1) * KT + (box << pb_log2), src, 1u << pb_log2,
+                        ptx::bulk_load(smem + L::kScaleOff + st * 2 * KT + (part & 1) * KT + (box << pb_log2), src, 1u << pb_log2,
                                   &ctrl->full[st]);
                     }
                 }
@@ -229,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             const float up = __uint_as_float((uint32_t)(127 + 141 - ex) << 23);
             uint32_t h[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
+            for (int k = 0; k < 4; ++k) h[k] = q8::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xffff0000u) * up);
             // dimensions 4s, 4s + 1 of a group of 16 to places 2s, 2s + 1; 4s + 2, 4s + 3 to 2s + 8, 2s + 9
             uint8_t *to = sQ + r * L::kQRow + (c >> 1) * 32 + (c & 1) * 8;
             *reinterpret_cast<uint2 *>(to) = make_uint2(h[0], h[2]);
@@ -363,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     l[e] += p0 + p1;
                     // (a hidden key's scale may be anything)
                     *reinterpret_cast<uint32_t *>(sP + (8 * e + g) * L::kPRow + at * 2) =
-                        pack_f16(p0 == 0.f ? 0.f : p0 * sc[0], p1 == 0.f ? 0.f : p1 * sc[1]);
+                        q8::pack_f16(p0 == 0.f ? 0.f : p0 * sc[0], p1 == 0.f ? 0.f : p1 * sc[1]);
                 }
             }
             if (__any_sync(0xffffffffu, moved)) {

@@ -35,8 +35,11 @@
 // 537 MB, 5.1 TB/s).  16 ragged sequences to 4096 keys, chunks to 512 tokens, 28/4 heads of 128: 75 us.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "fwd_bf16_common.cuh"
 #include "paged.h"
+#include "q8.cuh"
 #include "paged_state.cuh"
 
 namespace attn {
@@ -86,37 +89,61 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 // NT row tiles a CTA.  Registers: launched at 168 a thread (384 x 168 = 64512), split 128 x 56 +
 // 256 x 224 = 64512; with one tile at 128 (256 x 128 = 32768, two CTAs an SM), split 128 x 48 + 128 x 208.
-constexpr int threads(int NT) { return 128 + 128 * NT; }
-constexpr int launch_regs(int NT) { return NT == 2 ? 168 : 128; }
-constexpr uint32_t issue_regs(int NT) { return NT == 2 ? 56 : 48; }
-constexpr uint32_t softmax_regs(int NT) { return NT == 2 ? 224 : 208; }
-static_assert(128 * (issue_regs(2) + 2 * softmax_regs(2)) <= threads(2) * launch_regs(2), "register split");
-static_assert(128 * (issue_regs(1) + softmax_regs(1)) <= threads(1) * launch_regs(1), "register split");
+// Over codes two tiles have a warpgroup more: 512 x 128 = 65536, split 256 x 48 + 256 x 208.
+constexpr bool own_converters(int NT, bool q8) { return q8 && NT == 2; }
+constexpr int threads(int NT, bool q8) { return 128 + 128 * NT + (own_converters(NT, q8) ? 128 : 0); }
+constexpr int launch_regs(int NT, bool q8) { return NT == 2 && !q8 ? 168 : 128; }
+constexpr uint32_t issue_regs(int NT, bool q8) { return NT == 2 && !q8 ? 56 : 48; }
+constexpr uint32_t softmax_regs(int NT, bool q8) { return NT == 2 && !q8 ? 224 : 208; }
+constexpr bool split_fits(int NT, bool q8) {
+    return (int)((threads(NT, q8) - 128 * NT) * issue_regs(NT, q8) + 128 * NT * softmax_regs(NT, q8)) <= threads(NT, q8) * launch_regs(NT, q8);
+}
+static_assert(split_fits(1, false) && split_fits(2, false) && split_fits(1, true) && split_fits(2, true), "register split");
 
+template <int NT>
 struct Ctrl {
-    uint64_t q_full[2], s_full[2], p_full[2], o_final[2];
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t q_full[NT], s_full[NT], p_full[NT], o_final[NT];
+    uint64_t k_full[2 * NT], k_empty[2 * NT], v_full[2 * NT], v_empty[2 * NT];  // as many as a layout's stages, or more
     uint64_t final_mma;
     Share share;
-    Walk parked[8];  // a softmax warp's walk while it goes through the key tiles of a piece
+    Walk parked[4 * NT];  // a softmax warp's walk while it goes through the key tiles of a piece
     uint32_t tmem_base;
     int abort;
 };
+
+// What a cache of codes needs besides.  Codes come in units of 64 keys of K or V, in a ring of kRawStages: K's two
+// units of a tile, then V's.  A tile's 256 scale bytes, K's and V's, come with its first unit, into one of two slots (a
+// unit is asked for when the one kRawStages <= 4 before it is done: then the tile before the last is too); what the
+// softmax has to know of a tile lies in a ring of eight (the conversion runs at most four tiles ahead of it).
+constexpr int kUnitKeys = 64, kScaleSlots = 2, kNotes = 8;
+template <int NT>
+struct CtrlQ8 : Ctrl<NT> {
+    uint64_t q_ready[NT], raw_full[4], raw_empty[4];
+    uint16_t notes[kNotes];  // of a tile: the unit of its keys, then that of u (exponents as scale bytes)
+};
+template <int NT, bool kQ8>
+using CtrlOf = typename std::conditional<kQ8, CtrlQ8<NT>, Ctrl<NT>>::type;
 
 // D dimensions, NT row tiles of QR rows.  A tile of 64 rows is multiplied as one of 128 whose upper half
 // is whatever lies behind it in shared memory (a row's values reach that row alone).  The room that it
 // leaves is L1's: 1024 sequences of 128 keys, 64 rows a head of 128, 157 us in tiles of 128, 147 in tiles
 // of 64, 160 with a second K tile in its place; long sequences alike (87 to 89 us for 64 of 2048 keys).
-template <int D, int NT, int QR>
+template <int D, int NT, int QR, bool kQ8>
 struct Layout {
-    static constexpr uint32_t kTmemCols = 256 * NT, kIssueRegs = issue_regs(NT), kSoftmaxRegs = softmax_regs(NT);
+    static constexpr uint32_t kTmemCols = 256 * NT, kIssueRegs = issue_regs(NT, kQ8), kSoftmaxRegs = softmax_regs(NT, kQ8);
     static constexpr int kQPanel = QR * 128, kQTile = (D / 64) * kQPanel;
     static constexpr int kTile = (D / 64) * kPanelBytes;  // 128 keys of K or V
-    static constexpr int kKStages = NT == 2 ? (D == 128 ? 3 : 4) : D == 64 ? 2 : 1;
-    static constexpr int kVStages = NT == 2 ? (D == 128 ? 2 : 4) : D == 64 ? 2 : 1;
+    static constexpr int kKStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 3 : 4) : D == 64 ? 2 : 1;
+    static constexpr int kVStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 2 : 4) : D == 64 ? 2 : 1;
     static constexpr int kKOff = NT * kQTile, kVOff = kKOff + kKStages * kTile;
-    static constexpr int kDataBytes = kVOff + kVStages * kTile;
-    static constexpr int kBytes = kDataBytes + (int)sizeof(Ctrl);
+    // codes: units of [64 keys][D], scale bytes [slot][K, V][128]
+    static constexpr int kRawStages = NT == 1 && D == 128 && QR == 128 ? 2 : 4, kRawUnit = kUnitKeys * D;
+    static constexpr int kRawOff = kVOff + kVStages * kTile, kScaleOff = kRawOff + (kQ8 ? kRawStages * kRawUnit : 0);
+    static constexpr int kDataBytes = kScaleOff + (kQ8 ? kScaleSlots * 2 * BK : 0);
+    static constexpr int kBytes = kDataBytes + (int)sizeof(CtrlOf<NT, kQ8>);
+    // the warps that make operands of codes: a warpgroup of their own, or the two that are idle otherwise
+    static constexpr int kConvWarps = own_converters(NT, kQ8) ? 4 : 2, kConvFirst = own_converters(NT, kQ8) ? 4 + 4 * NT : 2;
+    static_assert(kKStages <= 2 * NT && kVStages <= 2 * NT && kRawStages <= 4 && kScaleSlots == 2, "barriers and slots");
     static_assert(NT == 2 ? kBytes <= kSmemMax : 2 * (kBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -187,11 +214,11 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float alpha) {
 // would touch 32 lines for 512 bytes, and the stores of a block take 2 us.  So every four lanes
 // transpose their 4 x 4 pieces of 16 bytes first (two exchanges), and each store writes 64 bytes of
 // eight rows.  Whole warp.
-template <int D>
-__device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, __nv_bfloat16 *orow, float *lse) {
+template <int D, bool kQ8>
+__device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, uint32_t unit, __nv_bfloat16 *orow, float *lse) {
     const int lane = threadIdx.x & 31, i = lane & 3;
     const bool empty = l_run == 0.f, b0 = i & 1, b1 = i & 2;  // a NaN is no empty row
-    const float inv = empty ? 0.f : 1.f / l_run;
+    const float inv = empty ? 0.f : kQ8 ? q8::pow2(unit) / l_run : 1.f / l_run;
     uint4 *to[4];  // the quad's rows
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -229,8 +256,8 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
 }
 
 // The same of a row that leaves its state, or starts from one (paged_state.cuh); tok < 0: no row.
-template <int D>
-__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, int tok, int h) {
+template <int D, bool kQ8>
+__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, uint32_t unit, int tok, int h) {
     paged::Weights w{1.f, 0.f};
     const bool on = tok >= 0, keep = a.state.mode == paged::kWritten;
     if (on && keep) paged::write_state_ml(a, tok, h, m, sum);
@@ -246,7 +273,7 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             asm volatile("" : "+r"(ov[t]));
-            v[t] = __uint_as_float(ov[t]);
+            v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
         }
         if (on && keep) paged::write_state<16>(a, tok, h, D, cc * 16, v, sum);
         if (on && !keep) {
@@ -292,15 +319,262 @@ __device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int
     if (!keep && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
+// Writes down what the merge has to know of the item that goes on past the share's end.  One thread.
+template <int NT>
+__device__ __forceinline__ void write_cut(const paged::Args &a, const Share &share) {
+    if (!a.marks) return;
+    Walk w;
+    Cut cut{};
+    bool more = w.begin(a, share);
+    while (more) {
+        cut = Cut{};
+        if (w.j0 == 0 && w.j1 < w.tiles) {
+            const Tiles tl = tiles_of<NT>(a, w);
+            for (int x = 0; x < NT; ++x) cut.n[x] = w.parts(a, blockIdx.x, tl.t[x]);
+            cut.row0 = w.k * a.R;
+            cut.end = w.seq.nq * a.G;
+            cut.q0 = w.seq.q0;
+            cut.hk = w.hk;
+        }
+        more = w.next(a);
+    }
+    reinterpret_cast<Cut *>(a.marks)[blockIdx.x] = cut;
+}
+
+// ---------------------------------------------------------------- a cache of codes
+//
+// The products take fp16, where codes are exact (paged_rows_q8.cu): warps make an operand of each 64 keys of codes that
+// TMA brings, code times 2^(e - E) with E the largest scale byte of a tile's keys, or for V one that holds for
+// as many tiles as no byte passes it by more than 6 (448 * 2^6 < 65504); both go to the softmax, which takes E into the
+// tile's factor of the logits, and rescales u when V's changes.  (Codes are exact down to 15 below E.)
+
+// The producer: the codes of a tile in four units, the scale bytes with the first.  Whole warp.
+template <int D, int NT, int QR>
+__device__ __forceinline__ void produce_codes(const paged::Args &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                              const CUtensorMap &tm_v, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
+    using L = Layout<D, NT, QR, true>;
+    constexpr int RS = L::kRawStages;
+    const int lane = threadIdx.x & 31;
+    volatile int *abort = &ctrl->abort;
+    if (!w.begin(a, ctrl->share)) return;
+    const int pb_log2 = min(a.page_log2, 6), boxes = kUnitKeys >> pb_log2;  // at most 4, of codes
+    const int sb_log2 = min(a.page_log2, 7), sboxes = BK >> sb_log2;        // at most 8 of K's scale bytes, and of V's
+    const int sbox = (lane - 4) >> 1, which = lane & 1;
+    const uint8_t *sc = which ? a.vs : a.ks;
+    const long long sc_page = which ? a.vss[0] : a.kss[0], sc_head = which ? a.vss[1] : a.kss[1];
+    int rs = 0, rp = 0, issued = 0, sslot = 0;
+    bool ok = true;
+    do {
+        if (w.keys == 0) continue;
+        if (lane < NT * (D / 64)) {  // the block's queries into L2: they are asked for some tiles later
+            const int tok = w.seq.q0 + paged::div_g(a, w.k * a.R + (lane % NT) * (a.R / NT));
+            tma_prefetch_3d(&tm_q, (lane / NT) * 64, w.hk * a.G, tok);
+        }
+        const int *row = a.bt + w.b * a.bt_s;
+        int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+            const int kv0 = j * BK, first = kv0 >> a.page_log2;
+            const int last = (min(kv0 + BK, w.seq.n) - 1) >> a.page_log2;
+            if (held < 0 || last >= held + 32) {
+                held = first;
+                const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
+                pages = at <= end ? __ldg(row + at) : 0;
+                if (pages < 0 || pages >= a.num_pages) {
+                    atomicOr(a.flags, kFlagBadIndex);
+                    pages = a.num_pages;  // outside the tensor: TMA fills zeros
+                }
+            }
+            auto page_of = [&](int key) { return __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31)); };
+            const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {  // K, K, V, V
+                if (issued >= RS) ok = ptx::mbar_wait(&ctrl->raw_empty[rs], rp ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                // boxes that hold a key of the sequence
+                const int left = held_keys - (u & 1) * kUnitKeys;
+                const int nbox = left > 0 ? min(boxes, ((left - 1) >> pb_log2) + 1) : 0;
+                const int nsbox = u == 0 ? min(sboxes, ((held_keys - 1) >> sb_log2) + 1) : 0;
+                if (lane == 0)
+                    ptx::mbar_arrive_expect_tx(&ctrl->raw_full[rs], ((uint32_t)(nbox * D) << pb_log2) + ((uint32_t)(2 * nsbox) << sb_log2));
+                __syncwarp();
+                const bool scales = lane >= 4;
+                const int key = scales ? kv0 + (sbox << sb_log2) : kv0 + (u & 1) * kUnitKeys + (lane << pb_log2);
+                const int page = page_of(key), slot = key & ((1 << a.page_log2) - 1);
+                if (lane < nbox)
+                    ptx::tma_load_4d(smem + L::kRawOff + rs * L::kRawUnit + ((lane << pb_log2) * D), u < 2 ? &tm_k : &tm_v,
+                                     &ctrl->raw_full[rs], 0, slot, w.hk, page);
+                else if (scales && sbox < nsbox)  // (of a page out of range, whose codes are zeros, another page's)
+                    ptx::bulk_load(smem + L::kScaleOff + sslot * 2 * BK + which * BK + (sbox << sb_log2),
+                                   sc + (page < a.num_pages ? page : 0) * sc_page + w.hk * sc_head + slot, 1u << sb_log2,
+                                   &ctrl->raw_full[rs]);
+                ++issued;
+                if (++rs == RS) { rs = 0; rp ^= 1; }
+            }
+            sslot = (sslot + 1) % kScaleSlots;
+        }
+    } while (ok && w.next(a));
+    if (!ok || *abort)  // copies in flight land before the CTA leaves
+        for (int i = min(issued, RS); i > 0; --i) {
+            if (--rs < 0) { rs = RS - 1; rp ^= 1; }
+            ptx::mbar_wait_quiet(&ctrl->raw_full[rs], rp, kWaitLimitNs);
+        }
+}
+
+// 64 keys of codes to fp16, times 2^(e - top), into the panels of an operand; keys from `held` on become zeros.
+template <int D, int CT>
+__device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *scales, uint8_t *to, int row0, int held, int top,
+                                             int ct) {
+    constexpr int C = D / 16, N = kUnitKeys * C / CT;  // 16-byte chunks of codes a key, and a thread
+    constexpr int M = N < 4 ? N : 4;                       // of them at once
+    static_assert(N * CT == kUnitKeys * C && N % M == 0, "whole turns");
+#pragma unroll
+    for (int it0 = 0; it0 < N; it0 += M) {
+        uint4 x[M];
+        uint32_t e[M];
+#pragma unroll
+        for (int t = 0; t < M; ++t) {
+            const int i = ct + (it0 + t) * CT;
+            x[t] = *reinterpret_cast<const uint4 *>(raw + i * 16);
+            e[t] = scales[i / C];
+        }
+#pragma unroll
+        for (int t = 0; t < M; ++t) {
+            const int i = ct + (it0 + t) * CT, key = i / C, c = i % C, row = row0 + key;
+            // 2^(e - top), 0 from 25 below on; NaN for 255
+            const float f = e[t] == 255u ? NAN : __uint_as_float((uint32_t)max((int)e[t] - top + 127, 0) << 23);
+            const __half2 f2 = __float2half2_rn(f);
+            uint32_t h[8];
+            const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                q8::decode4(w[k], h[2 * k], h[2 * k + 1]);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[2 * k + z]), f2);
+                    h[2 * k + z] = key < held ? *reinterpret_cast<const uint32_t *>(&v) : 0u;
+                }
+            }
+            // the second panel's threads store their halves the other way round: all banks at once
+            uint8_t *panel = to + (c >> 2) * kPanelBytes + row * 128;
+            const int c2 = 2 * (c & 3), odd = (c >> 2) & 1;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4 *>(panel + (((c2 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+            *reinterpret_cast<uint4 *>(panel + (((c2 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+        }
+    }
+}
+
+// The converters.  Whole warps.
+template <int D, int NT, int QR>
+__device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
+    using L = Layout<D, NT, QR, true>;
+    constexpr int RS = L::kRawStages, KS = L::kKStages, VS = L::kVStages, CT = 32 * L::kConvWarps;
+    const int lane = threadIdx.x & 31, ct = (int)threadIdx.x - 32 * L::kConvFirst;
+    volatile int *abort = &ctrl->abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const bool ok = ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+        return __all_sync(0xffffffffu, ok);
+    };
+    if (!w.begin(a, ctrl->share)) return;
+    int rs = 0, st[2] = {0, 0}, sslot = 0;
+    uint32_t rp = 0, sp[2] = {1, 1}, tile = 0;  // a fresh barrier's phase before the first counts as complete
+    do {
+        if (w.keys == 0) continue;
+        int unit = -1;  // of u, for this piece
+        for (int j = w.j0; j < w.j1; ++j, ++tile) {
+            const int kv0 = j * BK, held = w.seq.n - kv0;
+            const uint8_t *scales = smem + L::kScaleOff + sslot * 2 * BK;
+            int top = 0;
+#pragma unroll 1
+            for (int kind = 0; kind < 2; ++kind) {
+                uint64_t *full = kind ? ctrl->v_full : ctrl->k_full, *empty = kind ? ctrl->v_empty : ctrl->k_empty;
+                uint8_t *to = smem + (kind ? L::kVOff : L::kKOff) + st[kind] * L::kTile;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait(&ctrl->raw_full[rs], rp)) return;
+                    if (kind == 0 && h == 0) {
+                        // the largest scale bytes of the tile's keys (255, a NaN, is none)
+                        uint32_t big[2] = {0, 0};
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t e4 = *reinterpret_cast<const uint32_t *>(scales + x * BK + 4 * lane);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i, e4 >>= 8)
+                                if (4 * lane + i < held && (e4 & 255u) != 255u) big[x] = max(big[x], e4 & 255u);
+                            big[x] = __reduce_max_sync(0xffffffffu, big[x]);
+                        }
+                        top = (int)big[0];
+                        if ((int)big[1] > unit + (unit < 0 ? 0 : 6)) unit = (int)big[1];
+                        if (ct == 0)
+                            *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
+                    }
+                    if (h == 0 && !wait(&empty[st[kind]], sp[kind])) return;
+                    convert_unit<D, CT>(smem + L::kRawOff + rs * L::kRawUnit, scales + kind * BK + h * kUnitKeys, to, h * kUnitKeys,
+                                        held - h * kUnitKeys, kind ? unit : top, ct);
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&ctrl->raw_empty[rs]);
+                    if (++rs == RS) { rs = 0; rp ^= 1; }
+                }
+                ptx::fence_proxy_async_smem();  // the operand, before a product reads it
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&full[st[kind]]);
+                if (++st[kind] == (kind ? VS : KS)) { st[kind] = 0; sp[kind] ^= 1; }
+            }
+            sslot = (sslot + 1) % kScaleSlots;
+        }
+    } while (w.next(a));
+}
+
+// Row r of a tile of queries from bf16 to fp16 in place, times a power of two that brings its largest finite element
+// into [2^14, 2^15).  Returns the inverse.
+template <int D>
+__device__ __forceinline__ float queries_to_f16(uint8_t *tile, int panel_bytes, int r) {
+    uint32_t top = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        const int ex = max((int)(top >> 7), 27);  // its exponent field, or one whose 2^(141 - ex) is finite
+        const float up = __uint_as_float((uint32_t)(127 + 141 - ex) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * panel_bytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            const uint4 v = *at;
+            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (pass == 0) {
+                    const uint32_t lo = x[k] & 0x7fffu, hi = (x[k] >> 16) & 0x7fffu;
+                    top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+                } else {
+                    x[k] = q8::pack_f16(__uint_as_float(x[k] << 16) * up, __uint_as_float(x[k] & 0xffff0000u) * up);
+                }
+            }
+            if (pass == 1) *at = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+    }
+    return __uint_as_float((uint32_t)(max((int)(top >> 7), 27) - 14) << 23);
+}
+
+__device__ __forceinline__ void store_p_f16(uint32_t taddr, const float (&x)[BK]) {
+#pragma unroll
+    for (int cc = 0; cc < BK / 64; ++cc) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int t = 0; t < 32; ++t) pk[t] = q8::pack_f16(x[cc * 64 + 2 * t], x[cc * 64 + 2 * t + 1]);
+        ptx::tmem_st32(taddr + cc * 32, pk);
+    }
+    ptx::tmem_st_wait();
+}
+
 // kState: with states of the packed tokens' rows.
-template <int D, int NT, int QR, bool kState>
-__global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
+template <int D, int NT, int QR, bool kState, bool kQ8>
+__global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
-    using L = Layout<D, NT, QR>;
+    using L = Layout<D, NT, QR, kQ8>;
+    using Control = CtrlOf<NT, kQ8>;
     constexpr int KS = L::kKStages, VS = L::kVStages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem + L::kDataBytes);
+    Control *ctrl = reinterpret_cast<Control *>(smem + L::kDataBytes);
     volatile int *abort = &ctrl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -312,12 +586,19 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             ptx::mbar_init(&ctrl->o_final[x], 1);
         }
         for (int s = 0; s < KS; ++s) {
-            ptx::mbar_init(&ctrl->k_full[s], 1);
+            ptx::mbar_init(&ctrl->k_full[s], kQ8 ? L::kConvWarps : 1);
             ptx::mbar_init(&ctrl->k_empty[s], 1);
         }
         for (int s = 0; s < VS; ++s) {
-            ptx::mbar_init(&ctrl->v_full[s], 1);
+            ptx::mbar_init(&ctrl->v_full[s], kQ8 ? L::kConvWarps : 1);
             ptx::mbar_init(&ctrl->v_empty[s], 1);
+        }
+        if constexpr (kQ8) {
+            for (int x = 0; x < NT; ++x) ptx::mbar_init(&ctrl->q_ready[x], BQ);
+            for (int s = 0; s < L::kRawStages; ++s) {
+                ptx::mbar_init(&ctrl->raw_full[s], 1);
+                ptx::mbar_init(&ctrl->raw_empty[s], L::kConvWarps);
+            }
         }
         ptx::mbar_init(&ctrl->final_mma, 1);
         ctrl->abort = 0;
@@ -345,10 +626,17 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
     const uint32_t tmem = ctrl->tmem_base;
     // (a walk of its own in each role: one made here, before the roles part, would be spilled in all of them)
 
-    if (warp < 4) {
+    if (warp < 4 || (own_converters(NT, kQ8) && warp >= L::kConvFirst)) {
         ptx::regs_dec<L::kIssueRegs>();
         Walk w;
-        if (warp == 0 && w.begin(a, ctrl->share)) {
+        if (kQ8 && warp == 0) {
+            if constexpr (kQ8) produce_codes<D, NT, QR>(a, tm_q, tm_k, tm_v, smem, ctrl, w);
+        } else if (kQ8 && warp >= L::kConvFirst && warp < L::kConvFirst + L::kConvWarps) {
+            if constexpr (kQ8) {
+                convert_codes<D, NT, QR>(a, smem, ctrl, w);
+                if (!own_converters(NT, kQ8) && warp == 3 && lane == 0) write_cut<NT>(a, ctrl->share);
+            }
+        } else if (warp == 0 && w.begin(a, ctrl->share)) {
             // -------------------------------------------------------- TMA producer
             const int pb_log2 = min(a.page_log2, 7), boxes = BK >> pb_log2;
             int ks = 0, vs = 0, kp = 0, vp = 0, nk = 0, nv = 0;
@@ -408,27 +696,12 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
                     ptx::mbar_wait_quiet(&ctrl->v_full[vs], vp, kWaitLimitNs);
                 }
             }
-        } else if (warp == 3 && lane == 0 && a.marks) {
-            // -------------------------------------------------------- what the merge has to know
-            Cut cut{};
-            bool more = w.begin(a, ctrl->share);
-            while (more) {
-                cut = Cut{};
-                if (w.j0 == 0 && w.j1 < w.tiles) {
-                    const Tiles tl = tiles_of<NT>(a, w);
-                    for (int x = 0; x < NT; ++x) cut.n[x] = w.parts(a, blockIdx.x, tl.t[x]);
-                    cut.row0 = w.k * a.R;
-                    cut.end = w.seq.nq * a.G;
-                    cut.q0 = w.seq.q0;
-                    cut.hk = w.hk;
-                }
-                more = w.next(a);
-            }
-            reinterpret_cast<Cut *>(a.marks)[blockIdx.x] = cut;
+        } else if (warp == 3 && lane == 0) {
+            write_cut<NT>(a, ctrl->share);
         } else if (warp == 1 && lane == 0 && w.begin(a, ctrl->share)) {
             // -------------------------------------------------------- tensor-core issuer
-            constexpr uint32_t kIdS = ptx::idesc_bf16_f32(BQ, BK, false);
-            constexpr uint32_t kIdO = ptx::idesc_bf16_f32(BQ, D, true);
+            constexpr uint32_t kIdS = kQ8 ? ptx::idesc_f16_f32(BQ, BK, false) : ptx::idesc_bf16_f32(BQ, BK, false);
+            constexpr uint32_t kIdO = kQ8 ? ptx::idesc_f16_f32(BQ, D, true) : ptx::idesc_bf16_f32(BQ, D, true);
             const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem), 16);
             constexpr uint32_t kStep = L::kTile >> 4, kKLo = L::kKOff >> 4;
             constexpr uint32_t kVLo = (L::kVOff >> 4) + (((uint32_t)kPanelBytes >> 4) << 16) - (1u << 16);
@@ -471,7 +744,8 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
 #pragma unroll
                 for (int x = 0; x < NT; ++x)
                     if (ok && tl.n[x] > 0) {
-                        ok = wait(&ctrl->q_full[x], par(2 + x));
+                        if constexpr (kQ8) ok = wait(&ctrl->q_ready[x], par(2 + x));
+                        else ok = wait(&ctrl->q_full[x], par(2 + x));
                         if (!ok) break;
                         flip(2 + x);
                         ptx::tc_fence_after();
@@ -545,7 +819,7 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             return (X ? t.n[1] : t.n[0]) > 0;
         };
         int vs = 0;                     // V ring slot and phase, for the rows that are zeroed
-        uint32_t vph = 0, sph = 0, oph = 0;
+        uint32_t vph = 0, sph = 0, oph = 0, qph = 0, tiles = 0;
         bool ok = true, more = w.begin(a, ctrl->share);
         if (more && has_tile(w)) bring_q(w);
         while (more && ok) {
@@ -560,22 +834,41 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             if (lane == 0) ctrl->parked[warp - 4] = w;
             __syncwarp();
             float m_run = -INFINITY, l_run = 0.f;
+            float c_row = c;
+            uint32_t unit = 127;  // u is in units of 2^(unit - 127)
+            if constexpr (kQ8) {
+                if (n > 0) {
+                    if (!wait_warp(&ctrl->q_full[X], qph)) { ok = false; break; }
+                    qph ^= 1;
+                    if (QR == BQ || r < QR) c_row *= queries_to_f16<D>(smem + X * L::kQTile, L::kQPanel, r);
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive(&ctrl->q_ready[X]);
+                }
+            }
             for (int jj = 0; jj < n; ++jj) {
                 const int kv0 = (j0 + jj) * BK;
                 if (!wait_warp(&ctrl->s_full[X], sph)) { ok = false; break; }
                 sph ^= 1;
                 ptx::tc_fence_after();
-                float x[BK];
+                float x[BK], ct = c_row, grow = 1.f;
+                bool grown = false;
+                if constexpr (kQ8) {
+                    const uint32_t note = *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[(tiles + jj) % kNotes]);
+                    ct = fmaxf(c_row * q8::pow2(note & 255u), 1.17549435e-38f);  // (not 0: -inf times it stays -inf)
+                    grown = jj > 0 && (note >> 8) != unit;
+                    if (grown) grow = q8::pow2(unit + 127 > (note >> 8) ? unit + 127 - (note >> 8) : 0);
+                    unit = note >> 8;
+                }
                 bf16fwd::load_s_row(lane_addr + s_col, x);
-                const float mt = bf16fwd::tile_logits<false>(x, c, kv0, kv0 + BK > lim0, lim);
+                const float mt = bf16fwd::tile_logits<false>(x, ct, kv0, kv0 + BK > lim0, lim);
                 bool rescale;
                 const float alpha = bf16fwd::update_max(mt, m_run, rescale);
-                const float lsum = bf16fwd::tile_exp<false>(x, c, m_run);
+                const float lsum = bf16fwd::tile_exp<false>(x, ct, m_run);
                 l_run = fmaf(alpha, l_run, lsum);
-                if (__any_sync(0xffffffffu, rescale)) scale_o<D>(lane_addr + o_col, alpha);
+                if (__any_sync(0xffffffffu, rescale || grown)) scale_o<D>(lane_addr + o_col, kQ8 ? alpha * grow : alpha);
                 // value rows past the sequence may hold anything: the first of the two tiles that
                 // uses this V zeroes them before its product reads them
-                if (kv0 + BK > seqn && (X == 0 || jj >= na)) {
+                if (!kQ8 && kv0 + BK > seqn && (X == 0 || jj >= na)) {
                     if (!wait_warp(&ctrl->v_full[vs], vph)) { ok = false; break; }
                     if (kv0 + r >= seqn) bf16fwd::zero_v_row<D>(smem + L::kVOff + vs * L::kTile, r);
                     ptx::fence_proxy_async_smem();
@@ -583,12 +876,14 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
                 if (++vs == VS) { vs = 0; vph ^= 1; }
                 // the weights go to the product in bf16, half a step of 2^-8 each (l_run has them in fp32):
                 // V in 32 bits would take twice the room and run at half the rate
-                bf16fwd::store_p(lane_addr + s_col, x);
+                if constexpr (kQ8) store_p_f16(lane_addr + s_col, x);
+                else bf16fwd::store_p(lane_addr + s_col, x);
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&ctrl->p_full[X]);
             }
             if (!ok) break;
             w = ctrl->parked[warp - 4];
+            tiles += nmax;
             for (int jj = n; jj < nmax; ++jj)  // tiles that only the other rows see
                 if (++vs == VS) { vs = 0; vph ^= 1; }
             // where this row goes, before the walk moves on
@@ -625,8 +920,8 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
             oph ^= 1;
             ptx::tc_fence_after();
             if (whole) {
-                if (kState) end_row<D>(a, lane_addr + o_col, l_run, m_run, to_tok, to_head);
-                else write_rows<D>(lane_addr + o_col, l_run, m_run, orow, lrow);
+                if (kState) end_row<D, kQ8>(a, lane_addr + o_col, l_run, m_run, unit, to_tok, to_head);
+                else write_rows<D, kQ8>(lane_addr + o_col, l_run, m_run, unit, orow, lrow);
                 ptx::tc_fence_before();
                 continue;
             }
@@ -640,6 +935,11 @@ __global__ void __launch_bounds__(threads(NT), NT == 2 ? 1 : 2)
                 ptx::tmem_ld32(lane_addr + o_col + cc * 32, ov);
                 ptx::tmem_ld_wait();
                 ptx::reg_fence(ov);
+                if constexpr (kQ8) {
+                    const float vu = q8::pow2(unit);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) ov[t] = __float_as_uint(__uint_as_float(ov[t]) * vu);
+                }
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
                     u4[(cc * 8 + t) * BQ] = make_float4(__uint_as_float(ov[4 * t]), __uint_as_float(ov[4 * t + 1]),
@@ -752,28 +1052,28 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
-template <int D, int NT, int QR>
+template <int D, int NT, int QR, bool kQ8>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
                      bool cuts, bool many, cudaStream_t st) {
     const bool state = a.state.mode != paged::kNone;
-    auto kern = state ? paged_tc_kernel<D, NT, QR, true> : paged_tc_kernel<D, NT, QR, false>;
+    auto kern = state ? paged_tc_kernel<D, NT, QR, true, kQ8> : paged_tc_kernel<D, NT, QR, false, kQ8>;
     auto merge1 = state ? paged_tc_merge_kernel<D, NT, 1, true> : paged_tc_merge_kernel<D, NT, 1, false>;
     auto merge4 = state ? paged_tc_merge_kernel<D, NT, 4, true> : paged_tc_merge_kernel<D, NT, 4, false>;
-    int smem = Layout<D, NT, QR>::kBytes;
+    int smem = Layout<D, NT, QR, kQ8>::kBytes;
     if (NT == 2 && smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT)), smem, st, mq, mk, mv, a);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT, kQ8)), smem, st, mq, mk, mv, a);
     if (e == cudaSuccess && cuts)
         e = many ? launch_pdl(merge4, dim3(grid, NT, D / kMergeCols), dim3(4 * BQ), 0, st, a)
                  : launch_pdl(merge1, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
-template <int D>
+template <int D, bool kQ8>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int tiles,
                      int tile_rows, int grid, bool cuts, bool many, cudaStream_t st) {
-    return tiles == 2        ? launch<D, 2, 128>(mq, mk, mv, a, grid, cuts, many, st)
-           : tile_rows == 64 ? launch<D, 1, 64>(mq, mk, mv, a, grid, cuts, many, st)
-                             : launch<D, 1, 128>(mq, mk, mv, a, grid, cuts, many, st);
+    return tiles == 2        ? launch<D, 2, 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
+           : tile_rows == 64 ? launch<D, 1, 64, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
+                             : launch<D, 1, 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st);
 }
 
 }  // namespace
@@ -784,8 +1084,11 @@ attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, cons
     // keys in all): 8 items 47 us with one thread a row, 27 with four; 32 items 25.8 and 23.2; 64 items
     // 24.9 and 25.7; the 77 us of a ragged batch of chunks become 82.
     const bool many = (double)a.Hkv * ((double)a.T * a.G / a.R + a.B) * 4. < (double)grid;
-    return d == 64 ? launch<64>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
-                   : launch<128>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
+    if (a.ks)
+        return d == 64 ? launch<64, true>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
+                       : launch<128, true>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
+    return d == 64 ? launch<64, false>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
+                   : launch<128, false>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
 }
 
 }  // namespace attn

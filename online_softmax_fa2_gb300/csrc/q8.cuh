@@ -1,6 +1,7 @@
 // q8.cuh -- rows of a paged cache in 8 bits: e4m3 codes and one scale byte e, elements code * 2^(e - 127).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace attn {
@@ -34,6 +35,12 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t &lo, uint32_t &hi) 
         "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 }  // namespace q8
