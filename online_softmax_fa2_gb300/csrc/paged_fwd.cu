@@ -37,7 +37,9 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8) {
     // and 68, 24 rows 105 and 68.  One tile a block up to its 128 rows (96 rows of 64 dimensions 69 us,
     // 87 with two tiles; 160 rows 111 and 100), of 64 rows where that is enough (512 sequences of 128
     // keys, 64 rows: 75 us, 84 in a tile of 128; 96 rows: 129 and 88).
-    pl.tc = rows > (128 / G) * G ? 2 : rows > 16 ? 1 : 0;
+    // (Over codes of 128 dimensions one tile is of 64 rows, two CTAs an SM have no room for more.)
+    const int64_t one = q8 && c.d == 128 ? 64 : 128;
+    pl.tc = rows > (one / G) * G ? 2 : rows > 16 ? 1 : 0;
     pl.tile_rows = rows > (64 / G) * G ? 128 : 64;
     // (the tiles take whole tokens, so that TMA can bring their queries)
     pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : 16;
@@ -74,11 +76,11 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8) {
 
 // 4-D map over pages [num_pages, page_size, Hkv, d] with element strides s (page, slot, head); a
 // box is 64 dimensions of `box` keys of one head of one page, 128-byte swizzle; of codes all d, swizzled over as
-// many bytes, or plain (for the tiles).  L2 fetches whole
+// many bytes.  L2 fetches whole
 // rows of a head and no more: with 64 dimensions (128 bytes) a 256-byte fetch would bring the next
 // head's row too (351 MB read for 278 MB of cache, measured).
 attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cache_t &c, const int64_t s[3], int box,
-                           bool q8, bool plain, const char *name) {
+                           bool q8, const char *name) {
     auto enc = get_encoder();
     if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     auto bytes = [q8](int64_t st, int64_t size) -> cuuint64_t { return size <= 1 ? 16u : (cuuint64_t)(q8 ? st : st * 2); };
@@ -88,9 +90,7 @@ attn_status_t encode_pages(CUtensorMap *m, const void *ptr, const attn_paged_cac
     cuuint32_t es[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims,
                            strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           plain             ? CU_TENSOR_MAP_SWIZZLE_NONE
-                           : q8 && c.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                             : CU_TENSOR_MAP_SWIZZLE_128B,
+                           q8 && c.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            q8 ? (c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_128B)
                            : c.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -186,8 +186,8 @@ attn_status_t launch(const attn_paged_fwd_params_t &p, const attn_paged_scales_t
     CUtensorMap mk{}, mv{};  // not used when there are no pages
     if (c.num_pages > 0) {
         attn_status_t r;
-        if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, q8, q8 && pl.tc, "k_pages"))) return r;
-        if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, q8, q8 && pl.tc, "v_pages"))) return r;
+        if ((r = encode_pages(&mk, c.k_pages, c, c.k_stride, pl.box, q8, "k_pages"))) return r;
+        if ((r = encode_pages(&mv, c.v_pages, c, c.v_stride, pl.box, q8, "v_pages"))) return r;
     }
     if (pl.tc) {
         CUtensorMap mq;

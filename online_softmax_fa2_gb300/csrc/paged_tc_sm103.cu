@@ -111,11 +111,11 @@ struct Ctrl {
     int abort;
 };
 
-// What a cache of codes needs besides.  Codes come in units of 64 keys of K or V, in a ring of kRawStages: K's two
-// units of a tile, then V's.  A tile's 256 scale bytes, K's and V's, come with its first unit, into one of two slots (a
-// unit is asked for when the one kRawStages <= 4 before it is done: then the tile before the last is too); what the
-// softmax has to know of a tile lies in a ring of eight (the conversion runs at most four tiles ahead of it).
-constexpr int kUnitKeys = 64, kScaleSlots = 2, kNotes = 8;
+// What a cache of codes needs besides.  Codes come in units of 64 keys of K or V: a tile's four units, K's two and V's
+// two, have a place each.  A unit comes with the scale bytes that its warp has not seen: of the tile's 128 keys, K's or V's
+// (the first unit both), or, where the warp has converted the tile's other half before, of its own keys.  What the softmax
+// has to know of a tile lies in a ring of eight (the conversion runs at most four tiles ahead of it).
+constexpr int kUnitKeys = 64, kNotes = 8;
 template <int NT>
 struct CtrlQ8 : Ctrl<NT> {
     uint64_t q_ready[NT], raw_full[4], raw_empty[4];
@@ -136,14 +136,17 @@ struct Layout {
     static constexpr int kKStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 3 : 4) : D == 64 ? 2 : 1;
     static constexpr int kVStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 2 : 4) : D == 64 ? 2 : 1;
     static constexpr int kKOff = NT * kQTile, kVOff = kKOff + kKStages * kTile;
-    // codes: units of [64 keys][D], scale bytes [slot][K, V][128]
-    static constexpr int kRawStages = NT == 1 && D == 128 && QR == 128 ? 2 : 4, kRawUnit = kUnitKeys * D;
-    static constexpr int kRawOff = kVOff + kVStages * kTile, kScaleOff = kRawOff + (kQ8 ? kRawStages * kRawUnit : 0);
-    static constexpr int kDataBytes = kScaleOff + (kQ8 ? kScaleSlots * 2 * BK : 0);
+    // codes: four units of [64 keys][D], then their scale bytes
+    static constexpr int kRawUnit = kUnitKeys * D, kRawOff = kVOff + kVStages * kTile, kScaleOff = kRawOff + (kQ8 ? 4 * kRawUnit : 0);
+    static constexpr int kHalf = own_converters(NT, kQ8) ? BK : kUnitKeys;  // scale bytes of a second half
+    __host__ __device__ static constexpr int scale_off(int u) {
+        return kScaleOff + (u > 0 ? 2 * BK : 0) + (u > 1 ? kHalf : 0) + (u > 2 ? BK : 0);
+    }
+    static constexpr int kDataBytes = kScaleOff + (kQ8 ? 3 * BK + 2 * kHalf : 0);
     static constexpr int kBytes = kDataBytes + (int)sizeof(CtrlOf<NT, kQ8>);
     // the warps that make operands of codes: a warpgroup of their own, or the two that are idle otherwise
     static constexpr int kConvWarps = own_converters(NT, kQ8) ? 4 : 2, kConvFirst = own_converters(NT, kQ8) ? 4 + 4 * NT : 2;
-    static_assert(kKStages <= 2 * NT && kVStages <= 2 * NT && kRawStages <= 4 && kScaleSlots == 2, "barriers and slots");
+    static_assert(kKStages <= 2 * NT && kVStages <= 2 * NT, "barriers");
     static_assert(NT == 2 ? kBytes <= kSmemMax : 2 * (kBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -353,16 +356,12 @@ template <int D, int NT, int QR>
 __device__ __forceinline__ void produce_codes(const paged::Args &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                                               const CUtensorMap &tm_v, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
     using L = Layout<D, NT, QR, true>;
-    constexpr int RS = L::kRawStages;
     const int lane = threadIdx.x & 31;
     volatile int *abort = &ctrl->abort;
     if (!w.begin(a, ctrl->share)) return;
-    const int pb_log2 = min(a.page_log2, 6), boxes = kUnitKeys >> pb_log2;  // at most 4, of codes
-    const int sb_log2 = min(a.page_log2, 7), sboxes = BK >> sb_log2;        // at most 8 of K's scale bytes, and of V's
-    const int sbox = (lane - 4) >> 1, which = lane & 1;
-    const uint8_t *sc = which ? a.vs : a.ks;
-    const long long sc_page = which ? a.vss[0] : a.kss[0], sc_head = which ? a.vss[1] : a.kss[1];
-    int rs = 0, rp = 0, issued = 0, sslot = 0;
+    const int pb_log2 = min(a.page_log2, 6), boxes = kUnitKeys >> pb_log2;  // at most 4 a unit
+    const int sbox = (lane - 4) & 7, second = lane >= 12;  // scale bytes, lanes 4 .. 11: of the unit's own; 12 .. 19: V's, with the first unit
+    int tile = 0, issued = 0;
     bool ok = true;
     do {
         if (w.keys == 0) continue;
@@ -388,61 +387,58 @@ __device__ __forceinline__ void produce_codes(const paged::Args &a, const CUtens
             const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
 #pragma unroll
             for (int u = 0; u < 4; ++u) {  // K, K, V, V
-                if (issued >= RS) ok = ptx::mbar_wait(&ctrl->raw_empty[rs], rp ^ 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+                if (tile > 0) ok = ptx::mbar_wait(&ctrl->raw_empty[u], (tile - 1) & 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                // boxes that hold a key of the sequence
-                const int left = held_keys - (u & 1) * kUnitKeys;
-                const int nbox = left > 0 ? min(boxes, ((left - 1) >> pb_log2) + 1) : 0;
-                const int nsbox = u == 0 ? min(sboxes, ((held_keys - 1) >> sb_log2) + 1) : 0;
-                if (lane == 0)
-                    ptx::mbar_arrive_expect_tx(&ctrl->raw_full[rs], ((uint32_t)(nbox * D) << pb_log2) + ((uint32_t)(2 * nsbox) << sb_log2));
+                // boxes that hold a key of the sequence, of the unit and from key k0 of the tile on
+                auto boxes_from = [&](int k0) { return held_keys > k0 ? ((held_keys - k0 - 1) >> pb_log2) + 1 : 0; };
+                const int k0 = L::kHalf == kUnitKeys && (u & 1) ? kUnitKeys : 0, kinds = u == 0 ? 2 : 1;
+                const int nbox = min(boxes, boxes_from((u & 1) * kUnitKeys)), nsbox = min((BK - k0) >> pb_log2, boxes_from(k0));
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->raw_full[u], (uint32_t)(nbox * D + kinds * nsbox) << pb_log2);
                 __syncwarp();
-                const bool scales = lane >= 4;
-                const int key = scales ? kv0 + (sbox << sb_log2) : kv0 + (u & 1) * kUnitKeys + (lane << pb_log2);
+                const bool scales = lane >= 4 && lane < 4 + 8 * kinds;
+                const int key = kv0 + (scales ? k0 + (sbox << pb_log2) : (u & 1) * kUnitKeys + (lane << pb_log2));
                 const int page = page_of(key), slot = key & ((1 << a.page_log2) - 1);
                 if (lane < nbox)
-                    ptx::tma_load_4d(smem + L::kRawOff + rs * L::kRawUnit + ((lane << pb_log2) * D), u < 2 ? &tm_k : &tm_v,
-                                     &ctrl->raw_full[rs], 0, slot, w.hk, page);
-                else if (scales && sbox < nsbox)  // (of a page out of range, whose codes are zeros, another page's)
-                    ptx::bulk_load(smem + L::kScaleOff + sslot * 2 * BK + which * BK + (sbox << sb_log2),
-                                   sc + (page < a.num_pages ? page : 0) * sc_page + w.hk * sc_head + slot, 1u << sb_log2,
-                                   &ctrl->raw_full[rs]);
+                    ptx::tma_load_4d(smem + L::kRawOff + u * L::kRawUnit + ((lane << pb_log2) * D), u < 2 ? &tm_k : &tm_v,
+                                     &ctrl->raw_full[u], 0, slot, w.hk, page);
+                else if (scales && sbox < nsbox) {  // (of a page out of range, whose codes are zeros, another page's)
+                    const bool v = u >= 2 || second;
+                    const long long *st = v ? a.vss : a.kss;
+                    ptx::bulk_load(smem + L::scale_off(u) + second * BK + (sbox << pb_log2),
+                                   (v ? a.vs : a.ks) + (page < a.num_pages ? page : 0) * st[0] + w.hk * st[1] + slot, 1u << pb_log2,
+                                   &ctrl->raw_full[u]);
+                }
                 ++issued;
-                if (++rs == RS) { rs = 0; rp ^= 1; }
             }
-            sslot = (sslot + 1) % kScaleSlots;
+            ++tile;
         }
     } while (ok && w.next(a));
     if (!ok || *abort)  // copies in flight land before the CTA leaves
-        for (int i = min(issued, RS); i > 0; --i) {
-            if (--rs < 0) { rs = RS - 1; rp ^= 1; }
-            ptx::mbar_wait_quiet(&ctrl->raw_full[rs], rp, kWaitLimitNs);
-        }
+        for (int i = max(issued - 4, 0); i < issued; ++i) ptx::mbar_wait_quiet(&ctrl->raw_full[i & 3], (i >> 2) & 1, kWaitLimitNs);
 }
 
-// 64 keys of codes to fp16, times 2^(e - top), into the panels of an operand; keys from `held` on become zeros.
-template <int D, int CT>
-__device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *scales, uint8_t *to, int row0, int held, int top,
-                                             int ct) {
-    constexpr int C = D / 16, N = kUnitKeys * C / CT;  // 16-byte chunks of codes a key, and a thread
-    constexpr int M = N < 4 ? N : 4;                       // of them at once
-    static_assert(N * CT == kUnitKeys * C && N % M == 0, "whole turns");
+// 64 keys of codes to fp16, times 2^(e - top), into the panels of an operand; keys from `held` on become zeros.  Whole
+// warp.  Eight neighbouring lanes take eight keys' chunks of one column: TMA's swizzle of the codes and that of the operand
+// both spread those over all banks.
+template <int D>
+__device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *scales, uint8_t *to, int held, int top) {
+    constexpr int C = D / 64;  // chunks of a key and lane, a panel apart
+    const int lane = threadIdx.x & 31, r8 = lane & 7, col = lane >> 3;
+    const uint8_t *from = raw + r8 * D;
+    uint8_t *out = to + r8 * 128;
+    const int lo = ((2 * col) ^ r8) << 4;
+#pragma unroll 2
+    for (int g = 0; g < 8; ++g) {
+        uint4 x[C];
 #pragma unroll
-    for (int it0 = 0; it0 < N; it0 += M) {
-        uint4 x[M];
-        uint32_t e[M];
+        for (int t = 0; t < C; ++t)
+            x[t] = *reinterpret_cast<const uint4 *>(from + g * 8 * D + (((col + 4 * t) ^ (D == 128 ? r8 : (r8 >> 1) & 3)) << 4));
+        const int e = scales[8 * g + r8];
+        // 2^(e - top), 0 from 25 below on; NaN for 255
+        const __half2 f2 = __float2half2_rn(e == 255 ? NAN : __uint_as_float((uint32_t)max(e - top + 127, 0) << 23));
+        const bool none = 8 * g + r8 >= held;
 #pragma unroll
-        for (int t = 0; t < M; ++t) {
-            const int i = ct + (it0 + t) * CT;
-            x[t] = *reinterpret_cast<const uint4 *>(raw + i * 16);
-            e[t] = scales[i / C];
-        }
-#pragma unroll
-        for (int t = 0; t < M; ++t) {
-            const int i = ct + (it0 + t) * CT, key = i / C, c = i % C, row = row0 + key;
-            // 2^(e - top), 0 from 25 below on; NaN for 255
-            const float f = e[t] == 255u ? NAN : __uint_as_float((uint32_t)max((int)e[t] - top + 127, 0) << 23);
-            const __half2 f2 = __float2half2_rn(f);
+        for (int t = 0; t < C; ++t) {
             uint32_t h[8];
             const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
 #pragma unroll
@@ -451,76 +447,80 @@ __device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[2 * k + z]), f2);
-                    h[2 * k + z] = key < held ? *reinterpret_cast<const uint32_t *>(&v) : 0u;
+                    h[2 * k + z] = *reinterpret_cast<const uint32_t *>(&v);
                 }
             }
-            // the second panel's threads store their halves the other way round: all banks at once
-            uint8_t *panel = to + (c >> 2) * kPanelBytes + row * 128;
-            const int c2 = 2 * (c & 3), odd = (c >> 2) & 1;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4 *>(panel + (((c2 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-            *reinterpret_cast<uint4 *>(panel + (((c2 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+            if (none) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) h[k] = 0u;
+            }
+            uint8_t *at = out + g * 8 * 128 + t * kPanelBytes;
+            *reinterpret_cast<uint4 *>(at + lo) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(at + (lo ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
     }
 }
 
-// The converters.  Whole warps.
+// The largest of a tile's 128 scale bytes whose keys are held (255, a NaN, is none; 0 without any).  Whole warp.
+__device__ __forceinline__ int largest_scale(const uint8_t *scales, int held) {
+    const int lane = threadIdx.x & 31;
+    uint32_t e4 = *reinterpret_cast<const uint32_t *>(scales + 4 * lane), big = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, e4 >>= 8)
+        if (4 * lane + i < held && (e4 & 255u) != 255u) big = max(big, e4 & 255u);
+    return (int)__reduce_max_sync(0xffffffffu, big);
+}
+// The unit of u from one tile on whose largest scale byte is `big`.
+__device__ __forceinline__ int next_unit(int unit, int big) { return unit < 0 || big > unit + 6 ? big : unit; }
+
+// A converting warp: with four of them a unit of each tile, with two K's or V's units.  (Four warps that took every unit
+// together waited for one another and for a fence after each: 2450 clocks a tile beside the 2200 of the conversion.)
 template <int D, int NT, int QR>
 __device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
     using L = Layout<D, NT, QR, true>;
-    constexpr int RS = L::kRawStages, KS = L::kKStages, VS = L::kVStages, CT = 32 * L::kConvWarps;
-    const int lane = threadIdx.x & 31, ct = (int)threadIdx.x - 32 * L::kConvFirst;
+    constexpr int H = 4 / L::kConvWarps;  // units of a tile
+    const int lane = threadIdx.x & 31, cw = (int)(threadIdx.x >> 5) - L::kConvFirst;
+    const int kind = cw * H >> 1, h0 = H == 1 ? cw & 1 : 0;  // 0 K, 1 V; the first of its units
     volatile int *abort = &ctrl->abort;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         const bool ok = ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
         return __all_sync(0xffffffffu, ok);
     };
+    uint64_t *full = kind ? ctrl->v_full : ctrl->k_full, *empty = kind ? ctrl->v_empty : ctrl->k_empty;
+    uint8_t *ring = smem + (kind ? L::kVOff : L::kKOff);
+    const int stages = kind ? L::kVStages : L::kKStages;
     if (!w.begin(a, ctrl->share)) return;
-    int rs = 0, st[2] = {0, 0}, sslot = 0;
-    uint32_t rp = 0, sp[2] = {1, 1}, tile = 0;  // a fresh barrier's phase before the first counts as complete
+    int st = 0;
+    uint32_t sp = 1, tile = 0;  // a fresh barrier's phase before the first counts as complete
     do {
         if (w.keys == 0) continue;
         int unit = -1;  // of u, for this piece
         for (int j = w.j0; j < w.j1; ++j, ++tile) {
-            const int kv0 = j * BK, held = w.seq.n - kv0;
-            const uint8_t *scales = smem + L::kScaleOff + sslot * 2 * BK;
+            const int held = w.seq.n - j * BK;
             int top = 0;
-#pragma unroll 1
-            for (int kind = 0; kind < 2; ++kind) {
-                uint64_t *full = kind ? ctrl->v_full : ctrl->k_full, *empty = kind ? ctrl->v_empty : ctrl->k_empty;
-                uint8_t *to = smem + (kind ? L::kVOff : L::kKOff) + st[kind] * L::kTile;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait(&ctrl->raw_full[rs], rp)) return;
-                    if (kind == 0 && h == 0) {
-                        // the largest scale bytes of the tile's keys (255, a NaN, is none)
-                        uint32_t big[2] = {0, 0};
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t e4 = *reinterpret_cast<const uint32_t *>(scales + x * BK + 4 * lane);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i, e4 >>= 8)
-                                if (4 * lane + i < held && (e4 & 255u) != 255u) big[x] = max(big[x], e4 & 255u);
-                            big[x] = __reduce_max_sync(0xffffffffu, big[x]);
-                        }
-                        top = (int)big[0];
-                        if ((int)big[1] > unit + (unit < 0 ? 0 : 6)) unit = (int)big[1];
-                        if (ct == 0)
-                            *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
+            for (int k = 0; k < H; ++k) {
+                const int h = h0 + k, u = 2 * kind + h;
+                const uint8_t *scales = smem + L::scale_off(u);
+                if (!wait(&ctrl->raw_full[u], tile & 1u)) return;
+                if (k == 0) {
+                    top = largest_scale(scales, held);
+                    if (kind == 1) top = unit = next_unit(unit, top);
+                    if (cw == 0) {  // (V's bytes, for the note only)
+                        unit = next_unit(unit, largest_scale(scales + BK, held));
+                        if (lane == 0) *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
                     }
-                    if (h == 0 && !wait(&empty[st[kind]], sp[kind])) return;
-                    convert_unit<D, CT>(smem + L::kRawOff + rs * L::kRawUnit, scales + kind * BK + h * kUnitKeys, to, h * kUnitKeys,
-                                        held - h * kUnitKeys, kind ? unit : top, ct);
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&ctrl->raw_empty[rs]);
-                    if (++rs == RS) { rs = 0; rp ^= 1; }
+                    if (!wait(&empty[st], sp)) return;
                 }
+                convert_unit<D>(smem + L::kRawOff + u * L::kRawUnit, scales + (H == 2 ? 0 : h * kUnitKeys),
+                                ring + st * L::kTile + h * kUnitKeys * 128, held - h * kUnitKeys, top);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&ctrl->raw_empty[u]);
                 ptx::fence_proxy_async_smem();  // the operand, before a product reads it
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&full[st[kind]]);
-                if (++st[kind] == (kind ? VS : KS)) { st[kind] = 0; sp[kind] ^= 1; }
+                if (lane == 0) ptx::mbar_arrive(&full[st]);
             }
-            sslot = (sslot + 1) % kScaleSlots;
+            if (++st == stages) { st = 0; sp ^= 1; }
         }
     } while (w.next(a));
 }
@@ -586,18 +586,18 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             ptx::mbar_init(&ctrl->o_final[x], 1);
         }
         for (int s = 0; s < KS; ++s) {
-            ptx::mbar_init(&ctrl->k_full[s], kQ8 ? L::kConvWarps : 1);
+            ptx::mbar_init(&ctrl->k_full[s], kQ8 ? 2 : 1);  // (an arrival for each half of the tile)
             ptx::mbar_init(&ctrl->k_empty[s], 1);
         }
         for (int s = 0; s < VS; ++s) {
-            ptx::mbar_init(&ctrl->v_full[s], kQ8 ? L::kConvWarps : 1);
+            ptx::mbar_init(&ctrl->v_full[s], kQ8 ? 2 : 1);
             ptx::mbar_init(&ctrl->v_empty[s], 1);
         }
         if constexpr (kQ8) {
             for (int x = 0; x < NT; ++x) ptx::mbar_init(&ctrl->q_ready[x], BQ);
-            for (int s = 0; s < L::kRawStages; ++s) {
+            for (int s = 0; s < 4; ++s) {
                 ptx::mbar_init(&ctrl->raw_full[s], 1);
-                ptx::mbar_init(&ctrl->raw_empty[s], L::kConvWarps);
+                ptx::mbar_init(&ctrl->raw_empty[s], 1);
             }
         }
         ptx::mbar_init(&ctrl->final_mma, 1);
@@ -1073,7 +1073,7 @@ attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
                      int tile_rows, int grid, bool cuts, bool many, cudaStream_t st) {
     return tiles == 2        ? launch<D, 2, 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
            : tile_rows == 64 ? launch<D, 1, 64, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
-                             : launch<D, 1, 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st);
+                             : launch<D, 1, kQ8 && D == 128 ? 64 : 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st);
 }
 
 }  // namespace
