@@ -100,10 +100,10 @@ constexpr bool split_fits(int NT, bool q8) {
 }
 static_assert(split_fits(1, false) && split_fits(2, false) && split_fits(1, true) && split_fits(2, true), "register split");
 
-template <int NT>
+template <int NT, int ST>
 struct Ctrl {
     uint64_t q_full[NT], s_full[NT], p_full[NT], o_final[NT];
-    uint64_t k_full[2 * NT], k_empty[2 * NT], v_full[2 * NT], v_empty[2 * NT];  // as many as a layout's stages, or more
+    uint64_t k_full[ST], k_empty[ST], v_full[ST], v_empty[ST];  // as many as a layout's stages, or more
     uint64_t final_mma;
     Share share;
     Walk parked[4 * NT];  // a softmax warp's walk while it goes through the key tiles of a piece
@@ -111,18 +111,16 @@ struct Ctrl {
     int abort;
 };
 
-// What a cache of codes needs besides.  Codes come in units of 64 keys of K or V: a tile's four units, K's two and V's
-// two, have a place each.  A unit comes with the scale bytes that its warp has not seen: of the tile's 128 keys, K's or V's
-// (the first unit both), or, where the warp has converted the tile's other half before, of its own keys.  What the softmax
-// has to know of a tile lies in a ring of eight (the conversion runs at most four tiles ahead of it).
+// What a cache of codes needs besides.  A tile's codes come in four units of 64 keys, K's two and V's two, each with a place
+// of its own; its scale bytes lie in a ring of two.  What the softmax has to know of a tile lies in a ring of eight (the
+// conversion runs at most four tiles ahead of it).
 constexpr int kUnitKeys = 64, kNotes = 8;
-template <int NT>
-struct CtrlQ8 : Ctrl<NT> {
+template <int NT, int ST>
+struct CtrlQ8 : Ctrl<NT, ST> {
     uint64_t q_ready[NT], raw_full[4], raw_empty[4];
+    uint64_t sc_full[2][2], sc_empty[2][2];  // K's and V's scale bytes, two slots each
     uint16_t notes[kNotes];  // of a tile: the unit of its keys, then that of u (exponents as scale bytes)
 };
-template <int NT, bool kQ8>
-using CtrlOf = typename std::conditional<kQ8, CtrlQ8<NT>, Ctrl<NT>>::type;
 
 // D dimensions, NT row tiles of QR rows.  A tile of 64 rows is multiplied as one of 128 whose upper half
 // is whatever lies behind it in shared memory (a row's values reach that row alone).  The room that it
@@ -136,17 +134,14 @@ struct Layout {
     static constexpr int kKStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 3 : 4) : D == 64 ? 2 : 1;
     static constexpr int kVStages = kQ8 && NT == 2 ? 2 : NT == 2 ? (D == 128 ? 2 : 4) : D == 64 ? 2 : 1;
     static constexpr int kKOff = NT * kQTile, kVOff = kKOff + kKStages * kTile;
-    // codes: four units of [64 keys][D], then their scale bytes
-    static constexpr int kRawUnit = kUnitKeys * D, kRawOff = kVOff + kVStages * kTile, kScaleOff = kRawOff + (kQ8 ? 4 * kRawUnit : 0);
-    static constexpr int kHalf = own_converters(NT, kQ8) ? BK : kUnitKeys;  // scale bytes of a second half
-    __host__ __device__ static constexpr int scale_off(int u) {
-        return kScaleOff + (u > 0 ? 2 * BK : 0) + (u > 1 ? kHalf : 0) + (u > 2 ? BK : 0);
-    }
-    static constexpr int kDataBytes = kScaleOff + (kQ8 ? 3 * BK + 2 * kHalf : 0);
-    static constexpr int kBytes = kDataBytes + (int)sizeof(CtrlOf<NT, kQ8>);
+    // codes: four units of [64 keys][D]; scale bytes [K, V][slot][128]
+    static constexpr int kRawUnit = kUnitKeys * D, kRawOff = kVOff + kVStages * kTile;
+    static constexpr int kScaleOff = kRawOff + (kQ8 ? 4 * kRawUnit : 0), kDataBytes = kScaleOff + (kQ8 ? 4 * BK : 0);
+    static constexpr int kMostStages = kKStages > kVStages ? kKStages : kVStages;
+    using Control = typename std::conditional<kQ8, CtrlQ8<NT, kMostStages>, Ctrl<NT, kMostStages>>::type;
+    static constexpr int kBytes = kDataBytes + (int)sizeof(Control);
     // the warps that make operands of codes: a warpgroup of their own, or the two that are idle otherwise
     static constexpr int kConvWarps = own_converters(NT, kQ8) ? 4 : 2, kConvFirst = own_converters(NT, kQ8) ? 4 + 4 * NT : 2;
-    static_assert(kKStages <= 2 * NT && kVStages <= 2 * NT, "barriers");
     static_assert(NT == 2 ? kBytes <= kSmemMax : 2 * (kBytes + 1024) <= 228 * 1024, "shared memory budget");
 };
 
@@ -351,31 +346,54 @@ __device__ __forceinline__ void write_cut(const paged::Args &a, const Share &sha
 // as many tiles as no byte passes it by more than 6 (448 * 2^6 < 65504); both go to the softmax, which takes E into the
 // tile's factor of the logits, and rescales u when V's changes.  (Codes are exact down to 15 below E.)
 
-// The producer: the codes of a tile in four units, the scale bytes with the first.  Whole warp.
-template <int D, int NT, int QR>
-__device__ __forceinline__ void produce_codes(const paged::Args &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
-                                              const CUtensorMap &tm_v, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
-    using L = Layout<D, NT, QR, true>;
+// A producer of K's (0), V's (1) or both kinds' (2) codes, in the order in which the converting warps come to them, and
+// scale bytes, four a lane, loaded a tile ahead.  (Copies by lanes of a warp go out one after the other, each as long as a
+// step here: with scale bytes in bulk copies of a page, 20 a tile, one producer of units in halves took 867 us for a
+// chunk of 2048 tokens over 18432 keys, two 555.)  Its code is there once for both: the CTA's roles together fill the
+// instruction cache, and what makes a loop longer costs all of them (two copies of this one 644 us for 554; waits in line
+// 560 for 511; the converters' loop unrolled 638 for 544).  Whole warp.
+template <class L, int D, int NT>
+__device__ __forceinline__ void produce_codes(int kinds, const paged::Args &a, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                              const CUtensorMap &tm_v, uint8_t *smem, typename L::Control *ctrl, Walk &w) {
+    const int steps = kinds == 2 ? 4 : 2;  // units a tile
     const int lane = threadIdx.x & 31;
     volatile int *abort = &ctrl->abort;
     if (!w.begin(a, ctrl->share)) return;
-    const int pb_log2 = min(a.page_log2, 6), boxes = kUnitKeys >> pb_log2;  // at most 4 a unit
-    const int sbox = (lane - 4) & 7, second = lane >= 12;  // scale bytes, lanes 4 .. 11: of the unit's own; 12 .. 19: V's, with the first unit
-    int tile = 0, issued = 0;
+    const int pb_log2 = min(a.page_log2, 6);  // keys of a box
+    auto unit_of = [&](int i) { return kinds == 2 ? 2 * (i & 1) + (i >> 1) : 2 * kinds + i; };
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const bool ok = ptx::mbar_wait_short(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+        return __all_sync(0xffffffffu, ok);
+    };
+    int tile = 0, step = 0;
     bool ok = true;
     do {
         if (w.keys == 0) continue;
-        if (lane < NT * (D / 64)) {  // the block's queries into L2: they are asked for some tiles later
+        if (kinds != 1 && lane < NT * (D / 64)) {  // the block's queries into L2: they are asked for some tiles later
             const int tok = w.seq.q0 + paged::div_g(a, w.k * a.R + (lane % NT) * (a.R / NT));
             tma_prefetch_3d(&tm_q, (lane / NT) * 64, w.hk * a.G, tok);
         }
         const int *row = a.bt + w.b * a.bt_s;
         int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
-        for (int j = w.j0; ok && j < w.j1; ++j) {
-            const int kv0 = j * BK, first = kv0 >> a.page_log2;
-            const int last = (min(kv0 + BK, w.seq.n) - 1) >> a.page_log2;
-            if (held < 0 || last >= held + 32) {
-                held = first;
+        uint32_t ahead[2];
+        bool loaded = false;
+        auto last_page = [&](int kv0) { return (min(kv0 + BK, w.seq.n) - 1) >> a.page_log2; };
+        auto page_of = [&](int key) { return __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31)); };
+        auto load_scales = [&](int kv0) {
+            const int key = kv0 + 4 * lane, slot = key & ((1 << a.page_log2) - 1);
+            int page = page_of(key);
+            page = page < a.num_pages ? page : 0;  // (of a page out of range, whose codes are zeros, another page's)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (kinds == 2 || kinds == x) {
+                    const uint8_t *at = x ? a.vs + page * a.vss[0] + w.hk * a.vss[1] : a.ks + page * a.kss[0] + w.hk * a.kss[1];
+                    ahead[x] = key < w.seq.n ? __ldg(reinterpret_cast<const uint32_t *>(at + slot)) : 0u;
+                }
+        };
+        for (int j = w.j0; j < w.j1; ++j, ++tile) {
+            const int kv0 = j * BK;
+            if (held < 0 || last_page(kv0) >= held + 32) {
+                held = kv0 >> a.page_log2;
                 const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
                 pages = at <= end ? __ldg(row + at) : 0;
                 if (pages < 0 || pages >= a.num_pages) {
@@ -383,60 +401,68 @@ __device__ __forceinline__ void produce_codes(const paged::Args &a, const CUtens
                     pages = a.num_pages;  // outside the tensor: TMA fills zeros
                 }
             }
-            auto page_of = [&](int key) { return __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31)); };
-            const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
+            if (!loaded) load_scales(kv0);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {  // K, K, V, V
-                if (tile > 0) ok = ptx::mbar_wait(&ctrl->raw_empty[u], (tile - 1) & 1, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                // boxes that hold a key of the sequence, of the unit and from key k0 of the tile on
-                auto boxes_from = [&](int k0) { return held_keys > k0 ? ((held_keys - k0 - 1) >> pb_log2) + 1 : 0; };
-                const int k0 = L::kHalf == kUnitKeys && (u & 1) ? kUnitKeys : 0, kinds = u == 0 ? 2 : 1;
-                const int nbox = min(boxes, boxes_from((u & 1) * kUnitKeys)), nsbox = min((BK - k0) >> pb_log2, boxes_from(k0));
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->raw_full[u], (uint32_t)(nbox * D + kinds * nsbox) << pb_log2);
-                __syncwarp();
-                const bool scales = lane >= 4 && lane < 4 + 8 * kinds;
-                const int key = kv0 + (scales ? k0 + (sbox << pb_log2) : (u & 1) * kUnitKeys + (lane << pb_log2));
-                const int page = page_of(key), slot = key & ((1 << a.page_log2) - 1);
-                if (lane < nbox)
-                    ptx::tma_load_4d(smem + L::kRawOff + u * L::kRawUnit + ((lane << pb_log2) * D), u < 2 ? &tm_k : &tm_v,
-                                     &ctrl->raw_full[u], 0, slot, w.hk, page);
-                else if (scales && sbox < nsbox) {  // (of a page out of range, whose codes are zeros, another page's)
-                    const bool v = u >= 2 || second;
-                    const long long *st = v ? a.vss : a.kss;
-                    ptx::bulk_load(smem + L::scale_off(u) + second * BK + (sbox << pb_log2),
-                                   (v ? a.vs : a.ks) + (page < a.num_pages ? page : 0) * st[0] + w.hk * st[1] + slot, 1u << pb_log2,
-                                   &ctrl->raw_full[u]);
+            for (int x = 0; x < 2; ++x)
+                if (kinds == 2 || kinds == x) {
+                    if (ok && tile > 1) ok = wait(&ctrl->sc_empty[x][tile & 1], ((tile >> 1) - 1) & 1);
+                    if (!ok) break;
+                    *reinterpret_cast<uint32_t *>(smem + L::kScaleOff + (2 * x + (tile & 1)) * BK + 4 * lane) = ahead[x];
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&ctrl->sc_full[x][tile & 1]);
                 }
-                ++issued;
+            if (!ok) break;
+            loaded = j + 1 < w.j1 && last_page(kv0 + BK) < held + 32;
+            if (loaded) load_scales(kv0 + BK);
+            const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
+#pragma unroll 1
+            for (step = 0; step < steps; ++step) {
+                const int u = unit_of(step);
+                if (tile > 0) ok = wait(&ctrl->raw_empty[u], (tile - 1) & 1);
+                if (!ok) break;
+                // boxes that hold a key of the sequence
+                const int c0 = (u & 1) * kUnitKeys;
+                const int nbox = held_keys > c0 ? min(kUnitKeys >> pb_log2, ((held_keys - c0 - 1) >> pb_log2) + 1) : 0;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->raw_full[u], (uint32_t)(nbox * D) << pb_log2);
+                __syncwarp();
+                const int key = kv0 + c0 + (lane << pb_log2), page = page_of(key);
+                if (lane < nbox)
+                    ptx::tma_load_4d(smem + L::kRawOff + u * L::kRawUnit + ((lane << pb_log2) * D), u >= 2 ? &tm_v : &tm_k,
+                                     &ctrl->raw_full[u], 0, key & ((1 << a.page_log2) - 1), w.hk, page);
             }
-            ++tile;
+            if (!ok) break;
+            step = 0;
         }
     } while (ok && w.next(a));
     if (!ok || *abort)  // copies in flight land before the CTA leaves
-        for (int i = max(issued - 4, 0); i < issued; ++i) ptx::mbar_wait_quiet(&ctrl->raw_full[i & 3], (i >> 2) & 1, kWaitLimitNs);
+        for (int i = 0; i < steps; ++i) {
+            const int fills = tile + (i < step ? 1 : 0);
+            if (fills > 0) ptx::mbar_wait_quiet(&ctrl->raw_full[unit_of(i)], (fills - 1) & 1, kWaitLimitNs);
+        }
 }
 
-// 64 keys of codes to fp16, times 2^(e - top), into the panels of an operand; keys from `held` on become zeros.  Whole
-// warp.  Eight neighbouring lanes take eight keys' chunks of one column: TMA's swizzle of the codes and that of the operand
-// both spread those over all banks.
+// 2^(e - top) for the scale byte e, 0 from 25 below on; NaN for 255.
+__device__ __forceinline__ __half2 factor_of(int e, int top) {
+    return __float2half2_rn(e == 255 ? NAN : __uint_as_float((uint32_t)max(e - top + 127, 0) << 23));
+}
+
+// A unit of codes to fp16, key 32 i + k times lane k's factor[i], into the panels of an operand; keys from `held` on become
+// zeros.  Whole warp.  Eight neighbouring lanes take eight keys' chunks of one column: TMA's swizzle of the codes and that of
+// the operand both spread those over all banks.
 template <int D>
-__device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *scales, uint8_t *to, int held, int top) {
+__device__ __forceinline__ void convert_unit(const uint8_t *raw, uint8_t *to, int held, __half2 factor0, __half2 factor1) {
     constexpr int C = D / 64;  // chunks of a key and lane, a panel apart
     const int lane = threadIdx.x & 31, r8 = lane & 7, col = lane >> 3;
     const uint8_t *from = raw + r8 * D;
     uint8_t *out = to + r8 * 128;
     const int lo = ((2 * col) ^ r8) << 4;
-#pragma unroll 2
-    for (int g = 0; g < 8; ++g) {
+#pragma unroll 1
+    for (int g = 0; g < kUnitKeys / 8; ++g) {
         uint4 x[C];
 #pragma unroll
         for (int t = 0; t < C; ++t)
             x[t] = *reinterpret_cast<const uint4 *>(from + g * 8 * D + (((col + 4 * t) ^ (D == 128 ? r8 : (r8 >> 1) & 3)) << 4));
-        const int e = scales[8 * g + r8];
-        // 2^(e - top), 0 from 25 below on; NaN for 255
-        const __half2 f2 = __float2half2_rn(e == 255 ? NAN : __uint_as_float((uint32_t)max(e - top + 127, 0) << 23));
-        const bool none = 8 * g + r8 >= held;
+        const __half2 f2 = __shfl_sync(0xffffffffu, g < 4 ? factor0 : factor1, 8 * (g & 3) + r8);
 #pragma unroll
         for (int t = 0; t < C; ++t) {
             uint32_t h[8];
@@ -450,14 +476,17 @@ __device__ __forceinline__ void convert_unit(const uint8_t *raw, const uint8_t *
                     h[2 * k + z] = *reinterpret_cast<const uint32_t *>(&v);
                 }
             }
-            if (none) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) h[k] = 0u;
-            }
             uint8_t *at = out + g * 8 * 128 + t * kPanelBytes;
             *reinterpret_cast<uint4 *>(at + lo) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4 *>(at + (lo ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
+    }
+    if (held < kUnitKeys) {  // the tile's end: whatever lies there
+        __syncwarp();
+#pragma unroll 1
+        for (int i = max(held, 0) * 8 + lane; i < kUnitKeys * 8; i += 32)
+#pragma unroll
+            for (int t = 0; t < C; ++t) *reinterpret_cast<uint4 *>(to + t * kPanelBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -475,15 +504,14 @@ __device__ __forceinline__ int next_unit(int unit, int big) { return unit < 0 ||
 
 // A converting warp: with four of them a unit of each tile, with two K's or V's units.  (Four warps that took every unit
 // together waited for one another and for a fence after each: 2450 clocks a tile beside the 2200 of the conversion.)
-template <int D, int NT, int QR>
-__device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *smem, CtrlQ8<NT> *ctrl, Walk &w) {
-    using L = Layout<D, NT, QR, true>;
+template <class L, int D>
+__device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *smem, typename L::Control *ctrl, Walk &w) {
     constexpr int H = 4 / L::kConvWarps;  // units of a tile
     const int lane = threadIdx.x & 31, cw = (int)(threadIdx.x >> 5) - L::kConvFirst;
     const int kind = cw * H >> 1, h0 = H == 1 ? cw & 1 : 0;  // 0 K, 1 V; the first of its units
     volatile int *abort = &ctrl->abort;
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = ptx::mbar_wait(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
+        const bool ok = ptx::mbar_wait_short(bar, parity, abort, a.flags, kFlagWaitTimeout, kWaitLimitNs);
         return __all_sync(0xffffffffu, ok);
     };
     uint64_t *full = kind ? ctrl->v_full : ctrl->k_full, *empty = kind ? ctrl->v_empty : ctrl->k_empty;
@@ -497,23 +525,30 @@ __device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *sme
         int unit = -1;  // of u, for this piece
         for (int j = w.j0; j < w.j1; ++j, ++tile) {
             const int held = w.seq.n - j * BK;
-            int top = 0;
+            const uint8_t *scales = smem + L::kScaleOff + (2 * kind + (tile & 1)) * BK;
+            if (!wait(&ctrl->sc_full[kind][tile & 1], (tile >> 1) & 1u)) return;
+            int top = largest_scale(scales, held);
+            if (kind == 1) top = unit = next_unit(unit, top);
+            if (cw == 0) {  // V's bytes, for the note only
+                if (!wait(&ctrl->sc_full[1][tile & 1], (tile >> 1) & 1u)) return;
+                unit = next_unit(unit, largest_scale(scales + 2 * BK, held));
+                if (lane == 0) {
+                    *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
+                    ptx::mbar_arrive(&ctrl->sc_empty[1][tile & 1]);
+                }
+            }
+            __half2 factor[2 * H];
+#pragma unroll
+            for (int i = 0; i < 2 * H; ++i) factor[i] = factor_of(scales[h0 * kUnitKeys + 32 * i + lane], top);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctrl->sc_empty[kind][tile & 1]);
+            if (!wait(&empty[st], sp)) return;
 #pragma unroll
             for (int k = 0; k < H; ++k) {
                 const int h = h0 + k, u = 2 * kind + h;
-                const uint8_t *scales = smem + L::scale_off(u);
                 if (!wait(&ctrl->raw_full[u], tile & 1u)) return;
-                if (k == 0) {
-                    top = largest_scale(scales, held);
-                    if (kind == 1) top = unit = next_unit(unit, top);
-                    if (cw == 0) {  // (V's bytes, for the note only)
-                        unit = next_unit(unit, largest_scale(scales + BK, held));
-                        if (lane == 0) *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
-                    }
-                    if (!wait(&empty[st], sp)) return;
-                }
-                convert_unit<D>(smem + L::kRawOff + u * L::kRawUnit, scales + (H == 2 ? 0 : h * kUnitKeys),
-                                ring + st * L::kTile + h * kUnitKeys * 128, held - h * kUnitKeys, top);
+                convert_unit<D>(smem + L::kRawOff + u * L::kRawUnit, ring + st * L::kTile + h * kUnitKeys * 128, held - h * kUnitKeys,
+                                factor[2 * k], factor[2 * k + 1]);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&ctrl->raw_empty[u]);
                 ptx::fence_proxy_async_smem();  // the operand, before a product reads it
@@ -534,7 +569,7 @@ __device__ __forceinline__ float queries_to_f16(uint8_t *tile, int panel_bytes, 
     for (int pass = 0; pass < 2; ++pass) {
         const int ex = max((int)(top >> 7), 27);  // its exponent field, or one whose 2^(141 - ex) is finite
         const float up = __uint_as_float((uint32_t)(127 + 141 - ex) << 23);
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < D / 8; ++c) {
             uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * panel_bytes + r * 128 + (((c & 7) ^ (r & 7)) << 4));
             const uint4 v = *at;
@@ -571,7 +606,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
     using L = Layout<D, NT, QR, kQ8>;
-    using Control = CtrlOf<NT, kQ8>;
+    using Control = typename L::Control;
     constexpr int KS = L::kKStages, VS = L::kVStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     Control *ctrl = reinterpret_cast<Control *>(smem + L::kDataBytes);
@@ -599,6 +634,11 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                 ptx::mbar_init(&ctrl->raw_full[s], 1);
                 ptx::mbar_init(&ctrl->raw_empty[s], 1);
             }
+            for (int x = 0; x < 2; ++x)
+                for (int s = 0; s < 2; ++s) {
+                    ptx::mbar_init(&ctrl->sc_full[x][s], 1);
+                    ptx::mbar_init(&ctrl->sc_empty[x][s], L::kConvWarps / 2 + x);  // V's are read for the notes too
+                }
         }
         ptx::mbar_init(&ctrl->final_mma, 1);
         ctrl->abort = 0;
@@ -629,11 +669,11 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
     if (warp < 4 || (own_converters(NT, kQ8) && warp >= L::kConvFirst)) {
         ptx::regs_dec<L::kIssueRegs>();
         Walk w;
-        if (kQ8 && warp == 0) {
-            if constexpr (kQ8) produce_codes<D, NT, QR>(a, tm_q, tm_k, tm_v, smem, ctrl, w);
+        if (kQ8 && (warp == 0 || (own_converters(NT, kQ8) && warp == 2))) {
+            if constexpr (kQ8) produce_codes<L, D, NT>(own_converters(NT, kQ8) ? warp >> 1 : 2, a, tm_q, tm_k, tm_v, smem, ctrl, w);
         } else if (kQ8 && warp >= L::kConvFirst && warp < L::kConvFirst + L::kConvWarps) {
             if constexpr (kQ8) {
-                convert_codes<D, NT, QR>(a, smem, ctrl, w);
+                convert_codes<L, D>(a, smem, ctrl, w);
                 if (!own_converters(NT, kQ8) && warp == 3 && lane == 0) write_cut<NT>(a, ctrl->share);
             }
         } else if (warp == 0 && w.begin(a, ctrl->share)) {

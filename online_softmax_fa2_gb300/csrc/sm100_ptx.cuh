@@ -74,6 +74,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// The same with all but the first look out of line, where the length of the code counts.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *err_word,
+                                                   uint32_t flag, uint64_t limit_ns) {
+    return mbar_wait(bar, parity, abort, err_word, flag, limit_ns);
+}
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, volatile int *abort, uint32_t *err_word,
+                                                uint32_t flag, uint64_t limit_ns) {
+    return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, abort, err_word, flag, limit_ns);
+}
+
 // Bounded wait with no abort flag and no error report (used while a CTA winds down after
 // an abort, to let in-flight copies and tensor-core work finish).  Returns true on success.
 __device__ __forceinline__ bool mbar_wait_quiet(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
