@@ -227,14 +227,14 @@ attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, const attn_page
     return launch(p, scales, kNoState, workspace, st);
 }
 
-// The states, then what the two attentions need, one after the other, in the same place.
+// The states, then what the two attentions need (the second begins before the first has ended).
 size_t paged_prefix_workspace(const attn_paged_prefix_params_t &p) {
     const bool q8 = p.scales.k != nullptr;
     const Plan over = make_plan(over_prefixes(p), q8), own = make_plan(p.fwd, q8);
     if (!over.fits || !own.fits) return 0;
     const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq;
     return round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float)) +
-           (over.bytes > own.bytes ? over.bytes : own.bytes);
+           round_up(over.bytes) + own.bytes;
 }
 
 attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *workspace, cudaStream_t st) {
@@ -247,13 +247,13 @@ attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *wor
     s.cu = p.cu_prefix;
     s.ml = reinterpret_cast<float2 *>(ws);
     s.u = reinterpret_cast<float *>(ws + round_up(rows * 2 * sizeof(float)));
-    void *rest = ws + round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float));
-    const Plan own = make_plan(p.fwd, scales != nullptr);
-    if (!own.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
+    char *rest = ws + round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float));
+    const Plan over = make_plan(over_prefixes(p), scales != nullptr), own = make_plan(p.fwd, scales != nullptr);
+    if (!own.fits || !over.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
     const attn_status_t r = launch(over_prefixes(p), scales, s, rest, st);
     if (r) return r;
     s.mode = kMerged;
-    return launch(p.fwd, scales, s, rest, st);
+    return launch(p.fwd, scales, s, rest + round_up(over.bytes), st);
 }
 
 }  // namespace attn

@@ -145,17 +145,21 @@ __device__ __forceinline__ void merge_parts(const Args &a, int rows, int n, int 
     }
 }
 
-// The end of row (tok, h) whose columns D / 32 lane .. a warp's lanes hold: outputs, or states (kState).
+// The end of row `row` of a sequence whose first token is q0, of key head hk; a warp's lanes hold columns D / 32 lane .. of
+// it: outputs, or states (kState).
 template <int D, bool kState>
-__device__ __forceinline__ void end_row(const Args &a, int tok, int h, float (&v)[D / 32], float m, float sum) {
+__device__ __forceinline__ void end_row(const Args &a, int q0, int hk, int row, float (&v)[D / 32], float m, float sum) {
     constexpr int C = D / 32;
-    const int lane = threadIdx.x & 31;
-    if (kState && a.state.mode == kWritten) {
-        write_state<C>(a, tok, h, D, C * lane, v, sum);
-        if (lane == 0) write_state_ml(a, tok, h, m, sum);
-        return;
+    const int lane = threadIdx.x & 31, tg = div_g(a, row), tok = q0 + tg, h = hk * a.G + row - tg * a.G;
+    if (kState && a.state.mode != kNone) {
+        const StateAt at = state_at(a, D, hk, (long long)q0 * a.G + row);
+        if (a.state.mode == kWritten) {
+            write_state<C>(a, at, C * lane, v, sum);
+            if (lane == 0) write_state_ml(a, at, m, sum);
+            return;
+        }
+        join<C>(a, at, tok, C * lane, v, m, sum);
     }
-    if (kState && a.state.mode == kMerged) join<C>(a, tok, h, D, C * lane, v, m, sum);
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
     uint32_t *o32 = reinterpret_cast<uint32_t *>(a.o + tok * a.os0 + h * a.os1 + C * lane);

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         ctrl->abort = 0;
         ptx::fence_mbar_init();
     }
-    ptx::grid_dep_wait();
+    begin_after_earlier_grids(a, kState);
     ptx::launch_dependents();
     int *sums_of_32 = reinterpret_cast<int *>(smem);  // where the copies will go
     if (a.B > 32) {
@@ -101,7 +101,10 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     if (a.B > 32) ptx::fence_proxy_async_smem();  // the sums, before a copy takes their place
     __syncthreads();
     Walk w;
-    if (!w.begin(a, ctrl->share)) return;
+    if (!w.begin(a, ctrl->share)) {
+        if (kState) wait_for_states(a);
+        return;
+    }
 
     if (warp == 4) {
         // ------------------------------------------------------------ TMA producer
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (t == 0) sums[warp * R + 8 * e + g] = v;
         }
         consumer_sync();
+        if (kState) wait_for_states(a);
         const bool whole = p.whole();
         const int c0 = whole ? 0 : p.first_share(a);
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
@@ -318,14 +322,15 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (whole) {
                 const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                 if (kState) {
-                    Weights jw{1.f, 0.f};
-                    if (a.state.mode == kMerged) jw = join_ml(a, tok, h, m[e], sum);
-                    else if (warp == 0 && t == 0) write_state_ml(a, tok, h, m[e], sum);
+                    const StateAt at = state_at(a, D, p.hk, (long long)p.seq.q0 * a.G + row0 + r);
+                    Weights jw{1.f, 0.f, false};
+                    if (a.state.mode == kMerged) jw = join_ml(a, at, tok, m[e], sum);
+                    else if (warp == 0 && t == 0) write_state_ml(a, at, m[e], sum);
 #pragma unroll
                     for (int nt = 0; nt < DW / 8; ++nt) {
                         float v[2] = {o[nt][2 * e], o[nt][2 * e + 1]};
-                        if (a.state.mode == kWritten) write_state<2>(a, tok, h, D, warp * DW + 2 * t + 8 * nt, v, sum);
-                        else join_u<2>(a, tok, h, D, warp * DW + 2 * t + 8 * nt, jw, v);
+                        if (a.state.mode == kWritten) write_state<2>(a, at, warp * DW + 2 * t + 8 * nt, v, sum);
+                        else join_u<2>(a, at, warp * DW + 2 * t + 8 * nt, jw, v);
                         o[nt][2 * e] = v[0];
                         o[nt][2 * e + 1] = v[1];
                     }
@@ -357,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 },
                 [&](int n, int to, auto slot) {
                     merge_parts<D, 2, 8>(a, rows, n, to, threadIdx.x, slot, [&](int r, float (&v)[D / 32], float mx, float sum) {
-                        const int tg = div_g(a, row0 + r);
-                        end_row<D, kState>(a, p.seq.q0 + tg, p.hk * a.G + row0 + r - tg * a.G, v, mx, sum);
+                        end_row<D, kState>(a, p.seq.q0, p.hk, row0 + r, v, mx, sum);
                     });
                 });
     }

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         ctrl->abort = 0;
         ptx::fence_mbar_init();
     }
-    ptx::grid_dep_wait();
+    begin_after_earlier_grids(a, true);
     ptx::launch_dependents();
     int *sums_of_32 = reinterpret_cast<int *>(smem);  // where the copies will go
     if (a.B > 32) {
@@ -116,7 +116,10 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     if (a.B > 32) ptx::fence_proxy_async_smem();  // the sums, before a copy takes their place
     __syncthreads();
     Walk w;
-    if (!w.begin(a, ctrl->share)) return;
+    if (!w.begin(a, ctrl->share)) {
+        wait_for_states(a);
+        return;
+    }
 
     if (warp == 4) {
         // ------------------------------------------------------------ TMA producer
@@ -396,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (t == 0) sums[warp * R + 8 * e + g] = v;
         }
         consumer_sync();
+        wait_for_states(a);
         const bool whole = p.whole();
         const int c0 = whole ? 0 : p.first_share(a);
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
@@ -406,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (r >= rows) continue;
             float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
-            Weights jw{1.f, 0.f};
-            if (whole && a.state.mode == kMerged) jw = join_ml(a, tok, h, m[e], sum);
+            const StateAt at = state_at(a, D, p.hk, (long long)p.seq.q0 * a.G + row0 + r);
+            Weights jw{1.f, 0.f, false};
+            if (whole && a.state.mode == kMerged) jw = join_ml(a, at, tok, m[e], sum);
             const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
             const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
@@ -417,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 if (!whole) {
                     *reinterpret_cast<float4 *>(a.u + (slot * R + r) * D + col) = make_float4(v[0], v[1], v[2], v[3]);
                 } else if (a.state.mode == kWritten) {
-                    write_state<4>(a, tok, h, D, col, v, sum);
+                    write_state<4>(a, at, col, v, sum);
                 } else {
-                    if (a.state.mode == kMerged) join_u<4>(a, tok, h, D, col, jw, v);
+                    if (a.state.mode == kMerged) join_u<4>(a, at, col, jw, v);
                     *reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + col) =
                         empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
                 }
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (warp == 0 && t == 0) {
                 if (!whole)
                     *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(empty ? -INFINITY : m[e], sum);
-                else if (a.state.mode == kWritten) write_state_ml(a, tok, h, m[e], sum);
+                else if (a.state.mode == kWritten) write_state_ml(a, at, m[e], sum);
                 else if (a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m[e] + log2f(sum)) * kLn2;
             }
         }
@@ -440,8 +445,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 },
                 [&](int n, int to, auto slot) {
                     merge_parts<D, 2, 8>(a, rows, n, to, threadIdx.x, slot, [&](int r, float (&v)[D / 32], float mx, float sum) {
-                        const int tg = div_g(a, row0 + r);
-                        end_row<D, true>(a, p.seq.q0 + tg, p.hk * a.G + row0 + r - tg * a.G, v, mx, sum);
+                        end_row<D, true>(a, p.seq.q0, p.hk, row0 + r, v, mx, sum);
                     });
                 });
     }

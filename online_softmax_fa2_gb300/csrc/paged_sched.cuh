@@ -29,8 +29,10 @@ constexpr long long kLongestLine = 0x7fff0000;  // tiles of a line, so that a di
 constexpr size_t kCutBytes = 32;  // a share's record of the item that it cuts (paged_tc_sm103.cu)
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives up after 1 s
 
-// The states of all packed tokens' rows over keys that another call holds (a shared prefix): ml [T][Hq], u
-// [T][Hq][D].  Written in place of the outputs by the call over those keys, merged into the outputs by the other.
+// The states of all packed tokens' rows over keys that another call holds (a shared prefix); with the G query heads of a
+// key head in a row, token t's are rows t G .. t G + G - 1 of N = T G: ml [Hkv][N], u [Hkv][D / 4][N][4], so that
+// neighbouring rows (lanes) are neighbours in memory.  (As [row][D] the tiles' states took 42 us more for 14000 rows of
+// four key heads.)  Written in place of the outputs by the call over those keys, merged into the outputs by the other.
 struct State {
     int mode;      // kNone, kWritten, kMerged
     int P;         // (merged) tokens cu[0] .. cu[P] - 1 have one; cu null: all

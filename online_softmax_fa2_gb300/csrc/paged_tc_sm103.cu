@@ -255,11 +255,14 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
 
 // The same of a row that leaves its state, or starts from one (paged_state.cuh); tok < 0: no row.
 template <int D, bool kQ8>
-__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, uint32_t unit, int tok, int h) {
-    paged::Weights w{1.f, 0.f};
+__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, uint32_t unit, int tok, int g, int hk) {
+    paged::Weights w{1.f, 0.f, false};
     const bool on = tok >= 0, keep = a.state.mode == paged::kWritten;
-    if (on && keep) paged::write_state_ml(a, tok, h, m, sum);
-    if (on && !keep) w = paged::join_ml(a, tok, h, m, sum);
+    const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
+    const int h = hk * a.G + g;
+    paged::wait_for_states(a);
+    if (on && keep) paged::write_state_ml(a, at, m, sum);
+    if (on && !keep) w = paged::join_ml(a, at, tok, m, sum);
     const bool empty = sum == 0.f;  // a NaN is no empty row
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
@@ -273,9 +276,9 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
             asm volatile("" : "+r"(ov[t]));
             v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
         }
-        if (on && keep) paged::write_state<16>(a, tok, h, D, cc * 16, v, sum);
+        if (on && keep) paged::write_state<16>(a, at, cc * 16, v, sum);
         if (on && !keep) {
-            paged::join_u<16>(a, tok, h, D, cc * 16, w, v);
+            paged::join_u<16>(a, at, cc * 16, w, v);
             uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 16);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -292,23 +295,26 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
 
 // And of one that sees no key here.
 template <int D>
-__device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int h) {
+__device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int g, int hk) {
     float m = -INFINITY, sum = 0.f;
-    paged::Weights w{0.f, 0.f};
+    paged::Weights w{0.f, 0.f, false};
     const bool keep = a.state.mode == paged::kWritten;
-    if (keep) paged::write_state_ml(a, tok, h, m, sum);
-    else w = paged::join_ml(a, tok, h, m, sum);
+    const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
+    const int h = hk * a.G + g;
+    paged::wait_for_states(a);
+    if (keep) paged::write_state_ml(a, at, m, sum);
+    else w = paged::join_ml(a, at, tok, m, sum);
     const bool empty = sum == 0.f;
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
     for (int c = 0; c < D; c += 8) {
         float v[8] = {};
         if (keep) {
-            paged::write_state<8>(a, tok, h, D, c, v, sum);
+            paged::write_state<8>(a, at, c, v, sum);
             continue;
         }
         w.own = 0.f;
-        paged::join_u<8>(a, tok, h, D, c, w, v);
+        paged::join_u<8>(a, at, c, w, v);
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
         ptx::tmem_alloc(&ctrl->tmem_base, L::kTmemCols);
         ptx::tmem_relinquish();
     }
-    ptx::grid_dep_wait();
+    paged::begin_after_earlier_grids(a, kState);
     ptx::launch_dependents();
     int *sums_of_32 = reinterpret_cast<int *>(smem);  // where the copies will go
     if (a.B > 32) {
@@ -932,13 +938,14 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             const bool first = w.j0 == 0;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
-            int to_tok = -1, to_head = 0;
+            int to_tok = -1, to_g = 0;
+            const int hk = w.hk;
             if (mine) {
                 const long long t = w.seq.q0 + tok;
                 const int h = w.hk * a.G + i - tok * a.G;
                 if (kState) {
                     to_tok = (int)t;
-                    to_head = h;
+                    to_g = i - tok * a.G;
                 } else {
                     orow = a.o + t * a.os0 + h * a.os1;
                     lrow = a.lse ? a.lse + t * a.Hq + h : nullptr;
@@ -951,7 +958,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             if (n == 0) {
                 // no key tile here: the item's first share writes rows that see no key at all
                 if (tx == 0 && first && mine) {
-                    if (kState) end_empty_row<D>(a, to_tok, to_head);
+                    if (kState) end_empty_row<D>(a, to_tok, to_g, hk);
                     else bf16fwd::write_empty_row<D>(orow, lrow);
                 }
                 continue;
@@ -960,7 +967,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             oph ^= 1;
             ptx::tc_fence_after();
             if (whole) {
-                if (kState) end_row<D, kQ8>(a, lane_addr + o_col, l_run, m_run, unit, to_tok, to_head);
+                if (kState) end_row<D, kQ8>(a, lane_addr + o_col, l_run, m_run, unit, to_tok, to_g, hk);
                 else write_rows<D, kQ8>(lane_addr + o_col, l_run, m_run, unit, orow, lrow);
                 ptx::tc_fence_before();
                 continue;
@@ -990,6 +997,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
         // the queries asked for have arrived (their block's S waited for them, unless a wait gave up)
         if (!ok && asked > 0) ptx::mbar_wait_quiet(&ctrl->q_full[X], (asked - 1) & 1, kWaitLimitNs);
     }
+    if (kState) paged::wait_for_states(a);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1069,13 +1077,13 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     }
     if (g > 0 || !mine) return;
     if (kState) {
-        const int tk = paged::div_g(a, row), hd = c1.y * a.G + row - tk * a.G, at = c1.x + tk;
+        const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
         if (a.state.mode == paged::kWritten) {
-            paged::write_state<kMergeCols>(a, at, hd, D, col, v, sum);
-            if (col == 0) paged::write_state_ml(a, at, hd, M, sum);
+            paged::write_state<kMergeCols>(a, at, col, v, sum);
+            if (col == 0) paged::write_state_ml(a, at, M, sum);
             return;
         }
-        paged::join<kMergeCols>(a, at, hd, D, col, v, M, sum);
+        paged::join<kMergeCols>(a, at, c1.x + paged::div_g(a, row), col, v, M, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
