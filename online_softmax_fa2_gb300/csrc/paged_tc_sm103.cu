@@ -1008,28 +1008,28 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
 }
 
 // Merges the states of cut items ("How Does FlashAttention Preserve Global Softmax Across Tiles?",
-// section 3), in share order.  CTA (c, tile, columns / 32) takes the item whose first part is the end of
-// share c, if there is one; GR threads share a row, each every GR-th part: four where items are cut into
-// many parts (launch_paged_tc), else one.  A kernel of its own: the merge's registers in the
-// attention kernel's made its softmax spill (a 2048-token chunk 420 -> 800 us), and at its end one
-// warpgroup merging 128 rows took 8 to 11 us.  No CTA of it finds room on an SM before the attention
-// kernel's are done, so what it has to know is written down for it (Cut) instead of searched for.
-constexpr int kMergeCols = 32;
+// section 3), in share order.  A kernel of its own: the merge's registers in the attention kernel's made its softmax spill
+// (a 2048-token chunk 420 -> 800 us), and at its end one warpgroup merging 128 rows took 8 to 11 us.  No CTA of it finds
+// room on an SM before the attention kernel's are done, so what it has to know is written down for it (Cut) instead of
+// searched for.
+//
+// CTA (c, tile, columns) takes the item whose first part is the end of share c, if there is one; with GR = 4, where
+// items are cut into many parts (launch_paged_tc), four threads share a row, each every fourth part, and a CTA looks at
+// kMergeShares shares, so that the few CTAs with work and the others are one wave: 64 rows x 4 heads over 8192 keys in 19
+// parts an item 8.5 us from a CTA a share and 32 columns, .. so.
+constexpr int merge_cols(int GR) { return GR == 1 ? 32 : 16; }
+constexpr int merge_shares(int GR) { return GR == 1 ? 1 : 8; }
+
 template <int D, int NT, int GR, bool kState>
-__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a) {
-    static_assert(GR == 1 || GR == 4, "the sums below");
-    __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][kMergeCols + 1];
-    const int c = blockIdx.x, X = blockIdx.y, col = blockIdx.z * kMergeCols, r = threadIdx.x % BQ, g = threadIdx.x / BQ;
-    ptx::grid_dep_wait();
-    ptx::launch_dependents();
-    const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + c);
-    const int4 c0 = __ldcg(rec), c1 = __ldcg(rec + 1);  // n[2], row0, end | q0, hk
+__device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, int col, int4 c0, int4 c1,
+                                           float (&top)[GR][BQ], float (&part)[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR) + 1]) {
+    constexpr int C = merge_cols(GR);
+    const int r = threadIdx.x % BQ, g = threadIdx.x / BQ;
     const int n = X ? c0.y : c0.x, half = a.R / NT, row = c0.z + X * half + r;
-    if (n < 2) return;  // the whole CTA
     const bool mine = r < half && row < c0.w;
     const int parts = mine ? n : 0;
     auto slot = [&](int p) { return paged::state_slot(c + p, c); };
-    float M = -INFINITY, sum = 0.f, v[kMergeCols];
+    float M = -INFINITY, sum = 0.f, v[C];
 #pragma unroll 4
     for (int p = g; p < parts; p += GR) M = fmaxf(M, __ldcg(state_ml<NT>(a, slot(p), X, r)).x);
     if (GR > 1) {
@@ -1040,18 +1040,18 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     }
     const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-    for (int t = 0; t < kMergeCols; ++t) v[t] = 0.f;
+    for (int t = 0; t < C; ++t) v[t] = 0.f;
 #pragma unroll 1
     for (int p = g; p < parts; p += GR) {
         const float2 ml = __ldcg(state_ml<NT>(a, slot(p), X, r));
         const float4 *src = state_u<D, NT>(a, slot(p), X, r) + (col / 4) * BQ;
-        float4 y[kMergeCols / 4];
+        float4 y[C / 4];
 #pragma unroll
-        for (int t = 0; t < kMergeCols / 4; ++t) y[t] = __ldcg(src + t * BQ);
+        for (int t = 0; t < C / 4; ++t) y[t] = __ldcg(src + t * BQ);
         const float f = ptx::ex2(ml.x - ref);
         sum = fmaf(f, ml.y, sum);
 #pragma unroll
-        for (int t = 0; t < kMergeCols / 4; ++t) {
+        for (int t = 0; t < C / 4; ++t) {
             v[4 * t] = fmaf(f, y[t].x, v[4 * t]);
             v[4 * t + 1] = fmaf(f, y[t].y, v[4 * t + 1]);
             v[4 * t + 2] = fmaf(f, y[t].z, v[4 * t + 2]);
@@ -1064,26 +1064,26 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
         if (g >= from && g < 2 * from) {
             float *to = part[from == 2 ? g - 2 : 1][r];
 #pragma unroll
-            for (int t = 0; t < kMergeCols; ++t) to[t] = v[t];
-            to[kMergeCols] = sum;
+            for (int t = 0; t < C; ++t) to[t] = v[t];
+            to[C] = sum;
         }
         __syncthreads();
         if (g < from) {
             const float *other = part[from == 2 ? g : 1][r];
 #pragma unroll
-            for (int t = 0; t < kMergeCols; ++t) v[t] += other[t];
-            sum += other[kMergeCols];
+            for (int t = 0; t < C; ++t) v[t] += other[t];
+            sum += other[C];
         }
     }
     if (g > 0 || !mine) return;
     if (kState) {
         const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
         if (a.state.mode == paged::kWritten) {
-            paged::write_state<kMergeCols>(a, at, col, v, sum);
+            paged::write_state<C>(a, at, col, v, sum);
             if (col == 0) paged::write_state_ml(a, at, M, sum);
             return;
         }
-        paged::join<kMergeCols>(a, at, c1.x + paged::div_g(a, row), col, v, M, sum);
+        paged::join<C>(a, at, c1.x + paged::div_g(a, row), col, v, M, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
@@ -1091,13 +1091,35 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     const long long t0 = c1.x + tok;
     uint4 *o4 = reinterpret_cast<uint4 *>(a.o + t0 * a.os0 + h * a.os1 + col);
 #pragma unroll
-    for (int t = 0; t < kMergeCols / 8; ++t) {
+    for (int t = 0; t < C / 8; ++t) {
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv);
         o4[t] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     }
     if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
+}
+
+template <int D, int NT, int GR, bool kState>
+__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a, int shares) {
+    static_assert(GR == 1 || GR == 4, "the sums below");
+    constexpr int S = merge_shares(GR);
+    __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR) + 1];
+    const int X = blockIdx.y, col = blockIdx.z * merge_cols(GR);
+    // (a call that merges states begins under this one: what it reads of them it waits for)
+    if (kState) ptx::launch_dependents();
+    ptx::grid_dep_wait();
+    if (!kState) ptx::launch_dependents();
+    const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + blockIdx.x * S);
+    bool again = false;
+#pragma unroll 1
+    for (int i = 0; i < S && (int)blockIdx.x * S + i < shares; ++i) {
+        const int4 c0 = __ldcg(rec + 2 * i), c1 = __ldcg(rec + 2 * i + 1);  // n[2], row0, end | q0, hk
+        if ((X ? c0.y : c0.x) < 2) continue;  // the whole CTA
+        if (GR > 1 && again) __syncthreads();  // the last one's buffers
+        again = true;
+        merge_item<D, NT, GR, kState>(a, blockIdx.x * S + i, X, col, c0, c1, top, part);
+    }
 }
 
 template <int D, int NT, int QR, bool kQ8>
@@ -1111,9 +1133,11 @@ attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
     if (NT == 2 && smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT, kQ8)), smem, st, mq, mk, mv, a);
-    if (e == cudaSuccess && cuts)
-        e = many ? launch_pdl(merge4, dim3(grid, NT, D / kMergeCols), dim3(4 * BQ), 0, st, a)
-                 : launch_pdl(merge1, dim3(grid, NT, D / kMergeCols), dim3(BQ), 0, st, a);
+    if (e == cudaSuccess && cuts) {
+        const int x = many ? (grid + merge_shares(4) - 1) / merge_shares(4) : grid;
+        e = many ? launch_pdl(merge4, dim3(x, NT, D / merge_cols(4)), dim3(4 * BQ), 0, st, a, grid)
+                 : launch_pdl(merge1, dim3(x, NT, D / merge_cols(1)), dim3(BQ), 0, st, a, grid);
+    }
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
 template <int D, bool kQ8>
