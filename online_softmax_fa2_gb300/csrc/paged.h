@@ -25,7 +25,8 @@ attn_status_t launch_paged_rows_q8(const CUtensorMap &mk, const CUtensorMap &mv,
                                    cudaStream_t s);
 constexpr int kTcBoxKeys = 128, kTcQ8BoxKeys = 64;
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
-                              int d, int tiles, int tile_rows, int grid, bool cuts, cudaStream_t s);
+                              int d, int tiles, int tile_rows, int grid, cudaStream_t st);
+attn_status_t launch_paged_tc_merge(const paged::Args &a, int d, int tiles, int grid, cudaStream_t st);  // of its cut items
 // (tiles a block: 2 of up to 128 rows, or 1 of up to tile_rows, 64 or 128, with two CTAs an SM)
 
 }  // namespace attn

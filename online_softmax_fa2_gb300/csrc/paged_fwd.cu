@@ -4,6 +4,7 @@
 
 #include <atomic>
 #include <chrono>
+#include <utility>
 
 #include "paged.h"
 #include "paged_merge.cuh"
@@ -25,7 +26,11 @@ struct Plan {
     size_t off_ml, off_u, bytes;
 };
 
-Plan make_plan(const attn_paged_fwd_params_t &p, bool q8) {
+// Tiles a CTA of a prefix's attention takes beside the own keys'.
+constexpr int kBesideTiles = 10, kBesideRows = 80;
+
+// beside: another attention runs at the same time, on `taken` SMs.
+Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, int taken = 0) {
     const attn_paged_cache_t &c = p.cache;
     const int64_t G = p.Hq / c.Hkv;
     // tokens a sequence, or their mean
@@ -52,6 +57,16 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8) {
     pl.fits = tiles < (double)kLongestLine;
     const int64_t full = (int64_t)sms * (pl.tc ? 3 - pl.tc : rows_blocks(c.d));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
+    if (beside && pl.tc) {
+        // (enough tiles a CTA that the states of its part are little beside them)
+        const int64_t most_tiles = c.Hkv * ((c.T * G + pl.R - 1) / pl.R + c.B - 1) * ((keys >> pl.kt) + 5), some = (most_tiles + kBesideTiles - 1) / kBesideTiles;
+        if (some < pl.grid) pl.grid = (int)(some < 1 ? 1 : some);
+    }
+    // the SMs that are left, unless they would be few or have much to do
+    if (beside && !pl.tc && taken <= sms / 2 + 10 && tiles < (double)kBesideRows * (double)full) {
+        const int64_t left = full / sms * (sms - taken);
+        if (left < pl.grid) pl.grid = (int)left;
+    }
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
     // Tiles that a boundary has to leave at either side of a cut.  Less cuts more finely and merges more, and
@@ -131,12 +146,10 @@ int log2_of(int x) {
     return l;
 }
 
-const State kNoState{kNone, 0, nullptr, nullptr, nullptr};
-
-attn_status_t launch(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales, const State &state, void *workspace,
-                     cudaStream_t st) {
+// Queues the attention; its cut items are left to merge(), with the args that come back, where `merged` is given.
+attn_status_t launch(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales, const Plan &pl, const State &state,
+                     void *workspace, cudaStream_t st, Args *merged = nullptr) {
     const attn_paged_cache_t &c = p.cache;
-    const Plan pl = make_plan(p, scales != nullptr);
     if (!pl.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
     Args a{};
     a.B = (int)c.B; a.T = (int)c.T; a.Hq = (int)p.Hq; a.Hkv = (int)c.Hkv; a.G = (int)(p.Hq / c.Hkv); a.causal = p.causal;
@@ -193,7 +206,10 @@ attn_status_t launch(const attn_paged_fwd_params_t &p, const attn_paged_scales_t
         CUtensorMap mq;
         const attn_status_t r = encode_q(&mq, p, pl.tile_rows / a.G);
         if (r) return r;
-        return launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.tc, pl.tile_rows, pl.grid, pl.cuts, st);
+        const attn_status_t t = launch_paged_tc(mq, mk, mv, a, (int)c.d, pl.tc, pl.tile_rows, pl.grid, st);
+        if (merged) *merged = a;
+        if (t || !pl.cuts || merged) return t;
+        return launch_paged_tc_merge(a, (int)c.d, pl.tc, pl.grid, st);
     }
     return q8 ? launch_paged_rows_q8(mk, mv, a, (int)c.d, pl.grid, st) : launch_paged_rows(mk, mv, a, (int)c.d, pl.grid, st);
 }
@@ -216,6 +232,34 @@ attn_paged_fwd_params_t over_prefixes(const attn_paged_prefix_params_t &p) {
 
 size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Both attentions of a call, and their places in the workspace.
+//
+// Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, starts on the
+// SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
+// their own, 32/8 heads of 128: one after the other 65 us.
+struct PrefixPlan {
+    Plan over, own;
+    bool beside;
+    size_t off_u, off_ml2, off_u2, off_over, off_own, bytes;
+};
+PrefixPlan make_prefix_plan(const attn_paged_prefix_params_t &p) {
+    const bool q8 = p.scales.k != nullptr;
+    PrefixPlan r;
+    r.own = make_plan(p.fwd, q8);
+    r.over = make_plan(over_prefixes(p), q8, !r.own.tc);
+    r.beside = r.over.tc && !r.own.tc && r.over.cuts;
+    if (r.beside) r.own = make_plan(p.fwd, q8, true, r.over.grid);
+    const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq, ml = round_up(rows * 2 * sizeof(float)),
+                 u = round_up(rows * p.fwd.cache.d * sizeof(float));
+    r.off_u = ml;
+    r.off_ml2 = r.off_u + u;
+    r.off_u2 = r.off_ml2 + (r.beside ? ml : 0);
+    r.off_over = r.off_u2 + (r.beside ? u : 0);
+    r.off_own = r.off_over + round_up(r.over.bytes);
+    r.bytes = r.off_own + r.own.bytes;
+    return r;
+}
+
 }  // namespace
 
 size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales) {
@@ -224,36 +268,46 @@ size_t paged_fwd_workspace(const attn_paged_fwd_params_t &p, const attn_paged_sc
 }
 
 attn_status_t launch_paged_fwd(const attn_paged_fwd_params_t &p, const attn_paged_scales_t *scales, void *workspace, cudaStream_t st) {
-    return launch(p, scales, kNoState, workspace, st);
+    return launch(p, scales, make_plan(p, scales != nullptr), State{}, workspace, st);
 }
 
-// The states, then what the two attentions need (the second begins before the first has ended).
 size_t paged_prefix_workspace(const attn_paged_prefix_params_t &p) {
-    const bool q8 = p.scales.k != nullptr;
-    const Plan over = make_plan(over_prefixes(p), q8), own = make_plan(p.fwd, q8);
-    if (!over.fits || !own.fits) return 0;
-    const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq;
-    return round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float)) +
-           round_up(over.bytes) + own.bytes;
+    const PrefixPlan pl = make_prefix_plan(p);
+    return pl.over.fits && pl.own.fits ? pl.bytes : 0;
 }
 
 attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *workspace, cudaStream_t st) {
     const attn_paged_scales_t *scales = p.scales.k ? &p.scales : nullptr;
-    const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq;
+    const PrefixPlan pl = make_prefix_plan(p);
+    if (!pl.own.fits || !pl.over.fits)
+        return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
     char *ws = static_cast<char *>(workspace);
-    State s;
+    State s{};
     s.mode = kWritten;
     s.P = (int)p.P;
     s.cu = p.cu_prefix;
     s.ml = reinterpret_cast<float2 *>(ws);
-    s.u = reinterpret_cast<float *>(ws + round_up(rows * 2 * sizeof(float)));
-    char *rest = ws + round_up(rows * 2 * sizeof(float)) + round_up(rows * p.fwd.cache.d * sizeof(float));
-    const Plan over = make_plan(over_prefixes(p), scales != nullptr), own = make_plan(p.fwd, scales != nullptr);
-    if (!own.fits || !over.fits) return fail(ATTN_ERR_UNSUPPORTED, "Hkv (T Hq / Hkv + B) table_width page_size is too large");
-    const attn_status_t r = launch(over_prefixes(p), scales, s, rest, st);
+    s.u = reinterpret_cast<float *>(ws + pl.off_u);
+    if (pl.beside) {
+        s.ml2 = reinterpret_cast<float2 *>(ws + pl.off_ml2);
+        s.u2 = reinterpret_cast<float *>(ws + pl.off_u2);
+    }
+    s.marks = pl.beside;
+    Args merge;
+    attn_status_t r = launch(over_prefixes(p), scales, pl.over, s, ws + pl.off_over, st, pl.beside ? &merge : nullptr);
     if (r) return r;
+    s.mode = pl.beside ? kLeft : kMerged;
+    r = launch(p.fwd, scales, pl.own, s, ws + pl.off_own, st);
+    if (r || !pl.beside) return r;
+    merge.o = static_cast<__nv_bfloat16 *>(p.fwd.o);
+    merge.lse = p.fwd.lse;
     s.mode = kMerged;
-    return launch(p.fwd, scales, s, rest + round_up(over.bytes), st);
+    s.B = (int)p.fwd.cache.B;
+    s.only = p.fwd.cache.cu_q;
+    std::swap(s.ml, s.ml2);
+    std::swap(s.u, s.u2);
+    merge.state = s;
+    return launch_paged_tc_merge(merge, (int)p.fwd.cache.d, pl.over.tc, pl.over.grid, st);
 }
 
 }  // namespace attn

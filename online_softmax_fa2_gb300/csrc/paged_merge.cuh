@@ -151,14 +151,14 @@ template <int D, bool kState>
 __device__ __forceinline__ void end_row(const Args &a, int q0, int hk, int row, float (&v)[D / 32], float m, float sum) {
     constexpr int C = D / 32;
     const int lane = threadIdx.x & 31, tg = div_g(a, row), tok = q0 + tg, h = hk * a.G + row - tg * a.G;
-    if (kState && a.state.mode != kNone) {
+    if (kState) {
         const StateAt at = state_at(a, D, hk, (long long)q0 * a.G + row);
-        if (a.state.mode == kWritten) {
-            write_state<C>(a, at, C * lane, v, sum);
-            if (lane == 0) write_state_ml(a, at, m, sum);
+        const Ending e = ending(a, at, tok, m, sum);
+        end_u<C>(e, at, C * lane, v, sum);
+        if (e.written) {
+            if (lane == 0) write_ml(e, at, m, sum);
             return;
         }
-        join<C>(a, at, tok, C * lane, v, m, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     __syncthreads();
     Walk w;
     if (!w.begin(a, ctrl->share)) {
-        if (kState) wait_for_states(a);
+        if (kState) end_after_earlier_grids(a);
         return;
     }
 
@@ -323,18 +323,18 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
                 if (kState) {
                     const StateAt at = state_at(a, D, p.hk, (long long)p.seq.q0 * a.G + row0 + r);
-                    Weights jw{1.f, 0.f, false};
-                    if (a.state.mode == kMerged) jw = join_ml(a, at, tok, m[e], sum);
-                    else if (warp == 0 && t == 0) write_state_ml(a, at, m[e], sum);
+                    const Ending end = ending(a, at, tok, m[e], sum);
 #pragma unroll
                     for (int nt = 0; nt < DW / 8; ++nt) {
                         float v[2] = {o[nt][2 * e], o[nt][2 * e + 1]};
-                        if (a.state.mode == kWritten) write_state<2>(a, at, warp * DW + 2 * t + 8 * nt, v, sum);
-                        else join_u<2>(a, at, warp * DW + 2 * t + 8 * nt, jw, v);
+                        end_u<2>(end, at, warp * DW + 2 * t + 8 * nt, v, sum);
                         o[nt][2 * e] = v[0];
                         o[nt][2 * e + 1] = v[1];
                     }
-                    if (a.state.mode == kWritten) continue;
+                    if (end.written) {
+                        if (warp == 0 && t == 0) write_ml(end, at, m[e], sum);
+                        continue;
+                    }
                 }
                 const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
                 const float inv = empty ? 0.f : 1.f / sum;
@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     });
                 });
     }
+    if (kState) end_after_earlier_grids(a);
 }
 
 template <int D>

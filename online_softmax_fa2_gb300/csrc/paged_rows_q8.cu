@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     __syncthreads();
     Walk w;
     if (!w.begin(a, ctrl->share)) {
-        wait_for_states(a);
+        end_after_earlier_grids(a);
         return;
     }
 
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
             const StateAt at = state_at(a, D, p.hk, (long long)p.seq.q0 * a.G + row0 + r);
-            Weights jw{1.f, 0.f, false};
-            if (whole && a.state.mode == kMerged) jw = join_ml(a, at, tok, m[e], sum);
+            Ending end{1.f, 0.f, false, false, nullptr, nullptr};
+            if (whole) end = ending(a, at, tok, m[e], sum);
             const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
             const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll
@@ -421,18 +421,17 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 float v[4] = {o[2 * gi][2 * e] * vu, o[2 * gi + 1][2 * e] * vu, o[2 * gi][2 * e + 1] * vu, o[2 * gi + 1][2 * e + 1] * vu};
                 if (!whole) {
                     *reinterpret_cast<float4 *>(a.u + (slot * R + r) * D + col) = make_float4(v[0], v[1], v[2], v[3]);
-                } else if (a.state.mode == kWritten) {
-                    write_state<4>(a, at, col, v, sum);
-                } else {
-                    if (a.state.mode == kMerged) join_u<4>(a, at, col, jw, v);
+                    continue;
+                }
+                end_u<4>(end, at, col, v, sum);
+                if (!end.written)
                     *reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + col) =
                         empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
-                }
             }
             if (warp == 0 && t == 0) {
                 if (!whole)
                     *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(empty ? -INFINITY : m[e], sum);
-                else if (a.state.mode == kWritten) write_state_ml(a, at, m[e], sum);
+                else if (end.written) write_ml(end, at, m[e], sum);
                 else if (a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m[e] + log2f(sum)) * kLn2;
             }
         }
@@ -449,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     });
                 });
     }
+    end_after_earlier_grids(a);
 }
 
 template <int D>

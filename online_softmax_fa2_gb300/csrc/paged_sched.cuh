@@ -33,14 +33,22 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives u
 // key head in a row, token t's are rows t G .. t G + G - 1 of N = T G: ml [Hkv][N], u [Hkv][D / 4][N][4], so that
 // neighbouring rows (lanes) are neighbours in memory.  (As [row][D] the tiles' states took 42 us more for 14000 rows of
 // four key heads.)  Written in place of the outputs by the call over those keys, merged into the outputs by the other.
+//
+// Where the own keys' attention runs beside the prefixes' (paged_fwd.cu), neither waits for the other: its states go to ml2
+// and u2 (kLeft; rows of tokens without a prefix are finished), and the prefixes' merge, which comes last, merges both
+// (kMerged, the own states as ml and u): of the items that it merges, and of the rows that the prefixes' attention has
+// finished, whose states are its ml2 and u2 (other rows hold kCutRow as l there).
 struct State {
-    int mode;      // kNone, kWritten, kMerged
-    int P;         // (merged) tokens cu[0] .. cu[P] - 1 have one; cu null: all
-    const int *cu;
-    float2 *ml;
-    float *u;
+    int mode;      // kNone, kWritten, kMerged, kLeft
+    int P;         // (merged, left) tokens cu[0] .. cu[P] - 1 have one; cu null: all
+    int B;         // (merged) rows of tokens outside only[0] .. only[B] - 1 are left as they were; only null: none
+    const int *cu, *only;
+    float2 *ml, *ml2;
+    float *u, *u2;
+    bool marks;    // (written) cut rows are marked
 };
-constexpr int kNone = 0, kWritten = 1, kMerged = 2;
+constexpr int kNone = 0, kWritten = 1, kMerged = 2, kLeft = 3;
+constexpr float kCutRow = -1.f;
 
 struct Args {
     int B, T, Hq, Hkv, G, causal, R, kt;  // R rows a block, 2^kt keys a tile

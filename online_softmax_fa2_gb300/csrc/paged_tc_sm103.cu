@@ -256,13 +256,12 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
 // The same of a row that leaves its state, or starts from one (paged_state.cuh); tok < 0: no row.
 template <int D, bool kQ8>
 __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, uint32_t unit, int tok, int g, int hk) {
-    paged::Weights w{1.f, 0.f, false};
-    const bool on = tok >= 0, keep = a.state.mode == paged::kWritten;
+    const bool on = tok >= 0;
     const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
     const int h = hk * a.G + g;
     paged::wait_for_states(a);
-    if (on && keep) paged::write_state_ml(a, at, m, sum);
-    if (on && !keep) w = paged::join_ml(a, at, tok, m, sum);
+    paged::Ending e{1.f, 0.f, false, false, nullptr, nullptr};
+    if (on) e = paged::ending(a, at, tok, m, sum);
     const bool empty = sum == 0.f;  // a NaN is no empty row
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
@@ -276,9 +275,8 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
             asm volatile("" : "+r"(ov[t]));
             v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
         }
-        if (on && keep) paged::write_state<16>(a, at, cc * 16, v, sum);
-        if (on && !keep) {
-            paged::join_u<16>(a, at, cc * 16, w, v);
+        if (on) paged::end_u<16>(e, at, cc * 16, v, sum);
+        if (on && !e.written) {
             uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 16);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -290,37 +288,32 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
         }
         __syncwarp();  // the next columns are loaded by the whole warp
     }
-    if (on && !keep && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+    if (on && e.written) paged::write_ml(e, at, m, sum);
+    else if (on && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // And of one that sees no key here.
 template <int D>
 __device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int g, int hk) {
     float m = -INFINITY, sum = 0.f;
-    paged::Weights w{0.f, 0.f, false};
-    const bool keep = a.state.mode == paged::kWritten;
     const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
     const int h = hk * a.G + g;
     paged::wait_for_states(a);
-    if (keep) paged::write_state_ml(a, at, m, sum);
-    else w = paged::join_ml(a, at, tok, m, sum);
+    const paged::Ending e = paged::ending(a, at, tok, m, sum);
     const bool empty = sum == 0.f;
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
     for (int c = 0; c < D; c += 8) {
         float v[8] = {};
-        if (keep) {
-            paged::write_state<8>(a, at, c, v, sum);
-            continue;
-        }
-        w.own = 0.f;
-        paged::join_u<8>(a, at, c, w, v);
+        paged::end_u<8>(e, at, c, v, sum);
+        if (e.written) continue;
         uint32_t pk[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+        for (int i = 0; i < 4; ++i) pk[i] = empty ? 0u : ptx::pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
         *reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
     }
-    if (!keep && a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+    if (e.written) paged::write_ml(e, at, m, sum);
+    else if (a.lse) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // Writes down what the merge has to know of the item that goes on past the share's end.  One thread.
@@ -973,6 +966,8 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                 continue;
             }
             // the state of this part, for paged_tc_merge_kernel
+            if (kState && a.state.marks && first && mine)
+                a.state.ml[paged::state_at(a, D, hk, (long long)to_tok * a.G + to_g).ml] = make_float2(0.f, paged::kCutRow);
             const int slot = paged::state_slot(blockIdx.x, c0);
             *state_ml<NT>(a, slot, X, r) = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
             float4 *u4 = state_u<D, NT>(a, slot, X, r);
@@ -997,7 +992,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
         // the queries asked for have arrived (their block's S waited for them, unless a wait gave up)
         if (!ok && asked > 0) ptx::mbar_wait_quiet(&ctrl->q_full[X], (asked - 1) & 1, kWaitLimitNs);
     }
-    if (kState) paged::wait_for_states(a);
+    if (kState) paged::end_after_earlier_grids(a);
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -1077,13 +1072,15 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     }
     if (g > 0 || !mine) return;
     if (kState) {
+        const int tk = c1.x + paged::div_g(a, row);
         const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
-        if (a.state.mode == paged::kWritten) {
-            paged::write_state<C>(a, at, col, v, sum);
-            if (col == 0) paged::write_state_ml(a, at, M, sum);
+        if (!paged::is_wanted(a, tk)) return;
+        const paged::Ending e = paged::ending(a, at, tk, M, sum);
+        paged::end_u<C>(e, at, col, v, sum);
+        if (e.written) {
+            if (col == 0) paged::write_ml(e, at, M, sum);
             return;
         }
-        paged::join<C>(a, at, c1.x + paged::div_g(a, row), col, v, M, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
@@ -1100,9 +1097,36 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
+// Rows that the prefixes' attention has finished, 128 of a key head, and the own keys' states of them.
+template <int D, int GR>
+__device__ __forceinline__ void merge_whole(const paged::Args &a, int block, int col) {
+    constexpr int C = merge_cols(GR) / GR;  // columns a thread
+    const int n = a.T * a.G, blocks = (n + BQ - 1) / BQ, hk = block / blocks, row = block % blocks * BQ + threadIdx.x % BQ;
+    if (hk >= a.Hkv || row >= n) return;
+    const int tok = paged::div_g(a, row), h = hk * a.G + row - tok * a.G, c0 = col + (threadIdx.x / BQ) * C;
+    if (!paged::has_state(a, tok) || !paged::is_wanted(a, tok)) return;
+    const paged::StateAt at = paged::state_at(a, D, hk, row);
+    const float2 ml = __ldcg(a.state.ml2 + at.ml);
+    if (ml.y == paged::kCutRow) return;
+    float m = ml.x, sum = ml.y, v[C];
+    const float4 *u = reinterpret_cast<const float4 *>(a.state.u2) + at.u;
+#pragma unroll
+    for (int c = 0; c < C; c += 4) *reinterpret_cast<float4 *>(v + c) = __ldcg(u + (c0 + c) / 4 * at.n);
+    const paged::Ending e = paged::ending(a, at, tok, m, sum);
+    paged::end_u<C>(e, at, c0, v, sum);
+    const bool empty = sum == 0.f;
+    const float inv = empty ? 0.f : 1.f / sum;
+    uint2 *o = reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + c0);
+#pragma unroll
+    for (int c = 0; c < C; c += 4)
+        o[c / 4] = empty ? make_uint2(0u, 0u) : make_uint2(ptx::pack_bf16x2(v[c] * inv, v[c + 1] * inv), ptx::pack_bf16x2(v[c + 2] * inv, v[c + 3] * inv));
+    if (a.lse && c0 == 0) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+
+// Blocks from `items` on take rows that were finished.
 template <int D, int NT, int GR, bool kState>
-__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a, int shares) {
-    static_assert(GR == 1 || GR == 4, "the sums below");
+__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a, int shares, int items) {
+    static_assert(GR == 1 || GR == 4, "the sums of merge_item");
     constexpr int S = merge_shares(GR);
     __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR) + 1];
     const int X = blockIdx.y, col = blockIdx.z * merge_cols(GR);
@@ -1110,6 +1134,10 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
     if (kState) ptx::launch_dependents();
     ptx::grid_dep_wait();
     if (!kState) ptx::launch_dependents();
+    if (kState && (int)blockIdx.x >= items) {
+        merge_whole<D, GR>(a, ((int)blockIdx.x - items) * NT + X, col);
+        return;
+    }
     const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + blockIdx.x * S);
     bool again = false;
 #pragma unroll 1
@@ -1123,44 +1151,53 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
 }
 
 template <int D, int NT, int QR, bool kQ8>
-attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid,
-                     bool cuts, bool many, cudaStream_t st) {
-    const bool state = a.state.mode != paged::kNone;
-    auto kern = state ? paged_tc_kernel<D, NT, QR, true, kQ8> : paged_tc_kernel<D, NT, QR, false, kQ8>;
-    auto merge1 = state ? paged_tc_merge_kernel<D, NT, 1, true> : paged_tc_merge_kernel<D, NT, 1, false>;
-    auto merge4 = state ? paged_tc_merge_kernel<D, NT, 4, true> : paged_tc_merge_kernel<D, NT, 4, false>;
+attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int grid, cudaStream_t st) {
+    auto kern = a.state.mode != paged::kNone ? paged_tc_kernel<D, NT, QR, true, kQ8> : paged_tc_kernel<D, NT, QR, false, kQ8>;
     int smem = Layout<D, NT, QR, kQ8>::kBytes;
     if (NT == 2 && smem < 116 * 1024) smem = 116 * 1024;  // one CTA an SM: it owns all 512 TMEM columns
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(threads(NT, kQ8)), smem, st, mq, mk, mv, a);
-    if (e == cudaSuccess && cuts) {
-        const int x = many ? (grid + merge_shares(4) - 1) / merge_shares(4) : grid;
-        e = many ? launch_pdl(merge4, dim3(x, NT, D / merge_cols(4)), dim3(4 * BQ), 0, st, a, grid)
-                 : launch_pdl(merge1, dim3(x, NT, D / merge_cols(1)), dim3(BQ), 0, st, a, grid);
-    }
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc launch: %s", cudaGetErrorString(e));
 }
 template <int D, bool kQ8>
 attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a, int tiles,
-                     int tile_rows, int grid, bool cuts, bool many, cudaStream_t st) {
-    return tiles == 2        ? launch<D, 2, 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
-           : tile_rows == 64 ? launch<D, 1, 64, kQ8>(mq, mk, mv, a, grid, cuts, many, st)
-                             : launch<D, 1, kQ8 && D == 128 ? 64 : 128, kQ8>(mq, mk, mv, a, grid, cuts, many, st);
+                     int tile_rows, int grid, cudaStream_t st) {
+    return tiles == 2        ? launch<D, 2, 128, kQ8>(mq, mk, mv, a, grid, st)
+           : tile_rows == 64 ? launch<D, 1, 64, kQ8>(mq, mk, mv, a, grid, st)
+                             : launch<D, 1, kQ8 && D == 128 ? 64 : 128, kQ8>(mq, mk, mv, a, grid, st);
+}
+
+template <int D, int NT, int GR>
+cudaError_t launch_merge(const paged::Args &a, int grid, cudaStream_t st) {
+    auto kern = a.state.mode != paged::kNone ? paged_tc_merge_kernel<D, NT, GR, true> : paged_tc_merge_kernel<D, NT, GR, false>;
+    const int items = (grid + merge_shares(GR) - 1) / merge_shares(GR);
+    const int whole = a.state.ml2 ? (a.Hkv * ((a.T * a.G + BQ - 1) / BQ) + NT - 1) / NT : 0;
+    return launch_pdl(kern, dim3(items + whole, NT, D / merge_cols(GR)), dim3(GR * BQ), 0, st, a, grid, items);
+}
+template <int D, int NT>
+cudaError_t launch_merge(const paged::Args &a, int grid, bool many, cudaStream_t st) {
+    return many ? launch_merge<D, NT, 4>(a, grid, st) : launch_merge<D, NT, 1>(a, grid, st);
 }
 
 }  // namespace
 
 attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const paged::Args &a,
-                              int d, int tiles, int tile_rows, int grid, bool cuts, cudaStream_t st) {
+                              int d, int tiles, int tile_rows, int grid, cudaStream_t st) {
+    if (a.ks)
+        return d == 64 ? launch<64, true>(mq, mk, mv, a, tiles, tile_rows, grid, st)
+                       : launch<128, true>(mq, mk, mv, a, tiles, tile_rows, grid, st);
+    return d == 64 ? launch<64, false>(mq, mk, mv, a, tiles, tile_rows, grid, st)
+                   : launch<128, false>(mq, mk, mv, a, tiles, tile_rows, grid, st);
+}
+
+attn_status_t launch_paged_tc_merge(const paged::Args &a, int d, int tiles, int grid, cudaStream_t st) {
     // Items cut into more than four parts or so (16 tokens of 4 query heads over a key head, d 128, 131072
     // keys in all): 8 items 47 us with one thread a row, 27 with four; 32 items 25.8 and 23.2; 64 items
     // 24.9 and 25.7; the 77 us of a ragged batch of chunks become 82.
-    const bool many = (double)a.Hkv * ((double)a.T * a.G / a.R + a.B) * 4. < (double)grid;
-    if (a.ks)
-        return d == 64 ? launch<64, true>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
-                       : launch<128, true>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
-    return d == 64 ? launch<64, false>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st)
-                   : launch<128, false>(mq, mk, mv, a, tiles, tile_rows, grid, cuts, many, st);
+    const bool many = (double)a.Hkv * ((a.T * a.G + a.R - 1) / a.R + a.B - 1) * 4. < (double)grid;
+    const cudaError_t e = d == 64 ? (tiles == 2 ? launch_merge<64, 2>(a, grid, many, st) : launch_merge<64, 1>(a, grid, many, st))
+                                  : (tiles == 2 ? launch_merge<128, 2>(a, grid, many, st) : launch_merge<128, 1>(a, grid, many, st));
+    return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc merge launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace attn
