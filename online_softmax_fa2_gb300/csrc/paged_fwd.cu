@@ -26,8 +26,10 @@ struct Plan {
     size_t off_ml, off_u, bytes;
 };
 
-// Tiles a CTA of a prefix's attention takes beside the own keys'.
-constexpr int kBesideTiles = 10, kBesideRows = 80;
+// Tiles that a CTA of a prefix's attention takes beside the own keys' (a tile of codes takes longer): with 6, 8 and 10 the
+// 64 sequences of PrefixPlan's take 63, 56 and 56 us; 32 sequences of 4 tokens over codes behind two prefixes of 4096 keys,
+// 16/4 heads, 29, 38 and 39.  And the most tiles a CTA of the own keys' for which it keeps to the other SMs.
+constexpr int kBesideTiles = 8, kBesideTilesQ8 = 6, kBesideRows = 80;
 
 // beside: another attention runs at the same time, on `taken` SMs.
 Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, int taken = 0) {
@@ -59,11 +61,11 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, i
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
     if (beside && pl.tc) {
         // (enough tiles a CTA that the states of its part are little beside them)
-        const int64_t most_tiles = c.Hkv * ((c.T * G + pl.R - 1) / pl.R + c.B - 1) * ((keys >> pl.kt) + 5), some = (most_tiles + kBesideTiles - 1) / kBesideTiles;
+        const int64_t most_tiles = c.Hkv * ((c.T * G + pl.R - 1) / pl.R + c.B - 1) * ((keys >> pl.kt) + 5), each = q8 ? kBesideTilesQ8 : kBesideTiles, some = (most_tiles + each - 1) / each;
         if (some < pl.grid) pl.grid = (int)(some < 1 ? 1 : some);
     }
     // the SMs that are left, unless they would be few or have much to do
-    if (beside && !pl.tc && taken <= sms / 2 + 10 && tiles < (double)kBesideRows * (double)full) {
+    if (beside && !pl.tc && taken <= sms / 2 && tiles < (double)kBesideRows * (double)full) {
         const int64_t left = full / sms * (sms - taken);
         if (left < pl.grid) pl.grid = (int)left;
     }
@@ -234,9 +236,10 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Both attentions of a call, and their places in the workspace.
 //
-// Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, starts on the
+// Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, runs on the
 // SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
-// their own, 32/8 heads of 128: one after the other 65 us.
+// their own, 32/8 heads of 128: 56 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
+// every SM busy by themselves: one after the other, the second beginning as SMs come free.
 struct PrefixPlan {
     Plan over, own;
     bool beside;
