@@ -1,17 +1,20 @@
 """Builds the library: nvcc compiles each CUDA source for sm_103a, in parallel, and links
-``libattn_gb300.so`` in the package directory (in-tree; git-ignored)."""
+``libattn_gb300.so`` in the package directory (in-tree; git-ignored).  Beside it g++ compiles the quick
+binding of the paged cache's calls against this machine's torch, ``_binding.so``."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_gb300.so")
+BINDING = os.path.join(HERE, "_binding.so")
 SOURCES = ["attn_api.cu", "fwd_f32.cu", "fwd_bf16_sm103.cu", "fwd_bf16_pair_sm103.cu", "decode.cu",
            "bwd.cu", "bwd_tc_sm103.cu", "qk_rope.cu", "paged_fwd.cu", "paged_rows.cu",
            "paged_rows_q8.cu", "paged_read_q8.cu", "paged_tc_sm103.cu", "paged_api.cu"]
@@ -52,8 +55,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 f.write(r.stderr)
         return o
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_binding():
+        s = os.path.join(CSRC, "binding.cpp")
+        if force or _stale(BINDING, [s, headers[-1]]):
+            import torch
+            t = os.path.dirname(torch.__file__)
+            tmp = BINDING + f".tmp{os.getpid()}"
+            r = subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(t, "include"),
+                                "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"), s, "-o", tmp,
+                                "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl"],
+                               capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, BINDING)
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)

@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
 import struct
 
 import torch
@@ -168,6 +169,36 @@ def _load():
             f.argtypes, f.restype = args, res
         _lib = lib
     return _lib
+
+
+_quick = None
+
+
+def _binding():
+    """The module _binding (csrc/binding.cpp), which takes ordinary calls of the paged cache in one step."""
+    global _quick
+    if _quick is None:
+        import importlib.util
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        _load()
+        spec = importlib.util.spec_from_file_location("online_softmax_fa2_gb300._binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.open(_ofa.library_path())
+        _quick = m
+    return _quick
+
+
+def _quick_call(dev, name, *args):
+    """The call by the quick binding, or None where it does not take it."""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        return None
+    r = getattr(_quick or _binding(), name)(dev, torch._C._cuda_getCurrentRawStream(dev), *args)
+    if r.__class__ is int:
+        raise _ofa.AttnError(r, _ofa.last_error())
+    return r
 
 
 _DTYPES = {torch.float32: _ofa.F32, torch.bfloat16: _ofa.BF16}
@@ -383,6 +414,10 @@ def attn_paged_append(q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q=None
     if stream is not None:
         return _on(stream, q, attn_paged_append, q, k, v, k_pages, v_pages, block_table, kv_lens, cu_q, wq, wk, cos_sin,
                    positions, eps, interleaved, q_out)
+    r = _quick_call(q.get_device(), "append", q, k, v, k_pages, v_pages, None, None, block_table, kv_lens, cu_q, wq, wk, cos_sin,
+                    positions, eps, interleaved, q_out)
+    if r is not None:
+        return r
     lib = _load()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -399,6 +434,10 @@ def attn_paged_append_q8(q, k, v, k_pages, v_pages, k_scales, v_scales, block_ta
     if stream is not None:
         return _on(stream, q, attn_paged_append_q8, q, k, v, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, wq,
                    wk, cos_sin, positions, eps, interleaved, q_out)
+    r = None if k_scales is None else _quick_call(q.get_device(), "append", q, k, v, k_pages, v_pages, k_scales, v_scales, block_table,
+                                                  kv_lens, cu_q, wq, wk, cos_sin, positions, eps, interleaved, q_out)
+    if r is not None:
+        return r
     lib = _load()
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -418,6 +457,11 @@ def attn_paged_read_q8(k_pages, v_pages, k_scales, v_scales, block_table, kv_len
     if stream is not None:
         return _on(stream, k_pages, attn_paged_read_q8, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, rows, cu_k,
                    dtype, k_out, v_out)
+    if dtype in _DTYPES:
+        r = _quick_call(k_pages.get_device(), "read_q8", k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, rows, cu_k,
+                        dtype is torch.bfloat16, k_out, v_out)
+        if r is not None:
+            return r
     lib = _load()
     dev = k_pages.get_device()
     if dev < 0:
@@ -495,6 +539,10 @@ def attn_paged_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_q=None, max_q=N
     if stream is not None:
         return _on(stream, q, attn_paged_fwd, q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, workspace,
                    out, lse)
+    r = _quick_call(q.get_device(), "fwd", q, k_pages, v_pages, None, None, block_table, kv_lens, cu_q, max_q, causal, scale,
+                    workspace, out, lse)
+    if r is not None:
+        return r
     lib = _load()
     out, lse = _outputs(q, out, lse)
     p = _paged_fwd_params(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse)
@@ -516,6 +564,10 @@ def attn_paged_fwd_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, kv_l
     if stream is not None:
         return _on(stream, q, attn_paged_fwd_q8, q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, max_q, causal,
                    scale, workspace, out, lse)
+    r = None if k_scales is None else _quick_call(q.get_device(), "fwd", q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens,
+                                                  cu_q, max_q, causal, scale, workspace, out, lse)
+    if r is not None:
+        return r
     lib = _load()
     out, lse = _outputs(q, out, lse)
     p = _paged_fwd_values(q, k_pages, v_pages, block_table, kv_lens, cu_q, max_q, causal, scale, out, lse, True)
@@ -561,6 +613,11 @@ def attn_paged_prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, prefix_tabl
     if stream is not None:
         return _on(stream, q, attn_paged_prefix_fwd, q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q,
                    cu_prefix, max_q, causal, scale, k_scales, v_scales, workspace, out, lse)
+    if (k_scales is None) == (v_scales is None):
+        r = _quick_call(q.get_device(), "prefix_fwd", q, k_pages, v_pages, k_scales, v_scales, block_table, kv_lens, cu_q, max_q,
+                        causal, scale, workspace, out, lse, prefix_table, prefix_lens, cu_prefix)
+        if r is not None:
+            return r
     lib = _load()
     out, lse = _outputs(q, out, lse)
     p = _prefix_params(q, k_pages, v_pages, block_table, kv_lens, prefix_table, prefix_lens, cu_q, cu_prefix, max_q, causal, scale,
