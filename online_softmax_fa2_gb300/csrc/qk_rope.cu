@@ -266,13 +266,15 @@ struct ToCodes {
 // goes into the angles once for all of them: with (a, b) = r (x_a w_a, x_b w_b),
 //   y_a = r (x_a (w_a cos) - x_b (w_b sin)),  y_b = r (x_a (w_a sin) + x_b (w_b cos)).
 // (The shuffles need the whole warp: rows past count are zeros.)
-template <typename T, int L, int U, bool kInter, class Store>
-__device__ __forceinline__ void norm_rows(const T *in, long long in_h, const Store &store, const T *w,
-                                          const float *angle_row, int count, const Lane &ln, int rot, float inv_d,
-                                          float eps) {
-    Row2<T> x[U], wr;
+template <typename T, int U>
+__device__ __forceinline__ void load_rows(Row2<T> (&x)[U], const T *in, long long in_h, int count, const Lane &ln) {
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
+}
+template <typename T, int L, int U, bool kInter, class Store>
+__device__ __forceinline__ void norm_rows(Row2<T> (&x)[U], const Store &store, const T *w, const float *angle_row, int count,
+                                          const Lane &ln, int rot, float inv_d, float eps) {
+    Row2<T> wr;
     wr.load(w, ln.e0, ln.e1, w != nullptr && ln.on);
     const Angles an = load_angles(ln, angle_row, rot, kInter);
     float ac[8], as[8], bc[8], bs[8];  // w_a cos, w_a sin, w_b cos, -w_b sin
@@ -313,28 +315,6 @@ __device__ __forceinline__ void norm_rows(const T *in, long long in_h, const Sto
         mul8(z + 8, y + 8, bc);
         if (ln.turn) fma8(z + 8, y, as, z + 8);
         together<kInter>(z, f);
-        store(u, f, ln, ln.on && u < count);
-    }
-}
-
-template <typename T, int L, int U>
-__device__ __forceinline__ void copy_rows(const T *in, long long in_h, T *out, long long out_h, int count, const Lane &ln) {
-    Row2<T> x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (ln.on && u < count) x[u].store(out + u * out_h, ln.e0, ln.e1);
-}
-template <typename T, int L, int U>
-__device__ __forceinline__ void quantise_rows(const T *in, long long in_h, const ToCodes<L> &store, int count, const Lane &ln) {
-    Row2<T> x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u].load(in + u * in_h, ln.e0, ln.e1, ln.on && u < count);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float f[16];
-        x[u].get(f);
         store(u, f, ln, ln.on && u < count);
     }
 }
@@ -401,8 +381,9 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         row = a.cs + table_row(pos, a.P, a.flags, count > 0 && h0 == 0 && (threadIdx.x & (L - 1)) == 0) * a.cs_row;
     }
     const ToRows<T> store{static_cast<T *>(a.o[s]) + b * a.os[s][0] + n * a.os[s][1] + h0 * a.os[s][2], a.os[s][2]};
-    norm_rows<T, L, U, kInter>(static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1] + h0 * a.xs[s][2],
-                               a.xs[s][2], store, static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
+    Row2<T> x[U];
+    load_rows(x, static_cast<const T *>(a.x[s]) + b * a.xs[s][0] + n * a.xs[s][1] + h0 * a.xs[s][2], a.xs[s][2], count, ln);
+    norm_rows<T, L, U, kInter>(x, store, static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
 }
 
 // A warp takes one token, a tensor (q, k, v) and the part of its heads that its groups hold at once
@@ -436,24 +417,26 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const unsigned per = a.cq + 2 * a.ck;
     const int t = (int)(task / per), part = (int)(task - (unsigned)t * per);
     const bool report = part == 0 && (threadIdx.x & 31) == 0;
+    // the group's heads of the part's tensor; their rows are asked for before the token's place is looked up
+    const int s = part < a.cq ? 0 : part < a.cq + a.ck ? 1 : 2, H = s == 0 ? a.Hq : a.Hk;
+    const int h0 = ((part - (s == 0 ? 0 : s == 1 ? a.cq : a.cq + a.ck)) * (32 / L) + (threadIdx.x & 31) / L) * U;
+    const int count = min(max(H - h0, 0), U), h = count > 0 ? h0 : 0;
+    const Lane ln = make_lane<L>(a.d, a.rot);
+    const long long *in_s = s == 0 ? a.qs : s == 1 ? a.ks : a.vs;
+    Row2<T> x[U];
+    load_rows(x, static_cast<const T *>(s == 0 ? a.q : s == 1 ? a.k : a.v) + t * in_s[0] + h * in_s[1], in_s[1], count, ln);
     int b, i, nq;
     if (a.cu) report_bad_entries(a.cu, a.B, a.T, task, a.cu_groups, a.cu_step, a.flags);
     if (!find_token(a.cu, a.B, a.T, t, b, i, nq)) return;  // left as it was
     const int room = a.width * a.page_size, raw = __ldg(a.lens + b), len = min(max(raw, 0), room);
     if (report && len != raw) atomicOr(a.flags, kFlagKvLenClamped);
     const int at = len - nq + i;  // the token's place in its sequence; < 0: it has none
-    const Lane ln = make_lane<L>(a.d, a.rot);
     const float *row = nullptr;
     if (a.rot && part < a.cq + a.ck)
         row = a.cs + table_row(a.pos ? __ldg(a.pos + t) : max(at, 0), a.P, a.flags, report) * a.cs_row;
-    // the group's heads of the part's tensor
-    const int s = part < a.cq ? 0 : part < a.cq + a.ck ? 1 : 2, H = s == 0 ? a.Hq : a.Hk;
-    const int h0 = ((part - (s == 0 ? 0 : s == 1 ? a.cq : a.cq + a.ck)) * (32 / L) + (threadIdx.x & 31) / L) * U;
-    const int count = min(max(H - h0, 0), U), h = count > 0 ? h0 : 0;
     if (s == 0) {
         const ToRows<T> store{static_cast<T *>(a.qo) + t * a.qos[0] + h * a.qos[1], a.qos[1]};
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.q) + t * a.qs[0] + h * a.qs[1], a.qs[1], store,
-                                   static_cast<const T *>(a.wq), row, count, ln, a.rot, a.inv_d, a.eps);
+        norm_rows<T, L, U, kInter>(x, store, static_cast<const T *>(a.wq), row, count, ln, a.rot, a.inv_d, a.eps);
         return;
     }
     if (at < 0) return;
@@ -463,25 +446,31 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         return;
     }
     const long long slot = at % a.page_size;
+    const long long *ps = s == 1 ? a.kps : a.vps;
+    void *pages = s == 1 ? a.kp : a.vp;
     if constexpr (kQ8) {
-        const int x = s - 1;
-        const long long *ps = x ? a.vps : a.kps;
-        const ToCodes<L> store{static_cast<uint8_t *>(x ? a.vp : a.kp) + page * ps[0] + slot * ps[1] + h * ps[2],
-                               a.scales[x] + page * a.scale_s[x][0] + h * a.scale_s[x][1] + slot, ps[2], a.scale_s[x][1]};
-        if (s == 1)
-            norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1], store,
-                                       static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
-        else
-            quantise_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0] + h * a.vs[1], a.vs[1], store, count, ln);
-        return;
+        const ToCodes<L> store{static_cast<uint8_t *>(pages) + page * ps[0] + slot * ps[1] + h * ps[2],
+                               a.scales[s - 1] + page * a.scale_s[s - 1][0] + h * a.scale_s[s - 1][1] + slot, ps[2], a.scale_s[s - 1][1]};
+        if (s == 1) {
+            norm_rows<T, L, U, kInter>(x, store, static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[16];
+            x[u].get(f);
+            store(u, f, ln, ln.on && u < count);
+        }
+    } else {
+        T *to = static_cast<T *>(pages) + page * ps[0] + slot * ps[1] + h * ps[2];
+        if (s == 1) {
+            norm_rows<T, L, U, kInter>(x, ToRows<T>{to, ps[2]}, static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (ln.on && u < count) x[u].store(to + u * ps[2], ln.e0, ln.e1);
     }
-    if (s == 1) {
-        const ToRows<T> store{static_cast<T *>(a.kp) + page * a.kps[0] + slot * a.kps[1] + h * a.kps[2], a.kps[2]};
-        norm_rows<T, L, U, kInter>(static_cast<const T *>(a.k) + t * a.ks[0] + h * a.ks[1], a.ks[1], store,
-                                   static_cast<const T *>(a.wk), row, count, ln, a.rot, a.inv_d, a.eps);
-    } else
-        copy_rows<T, L, U>(static_cast<const T *>(a.v) + t * a.vs[0] + h * a.vs[1], a.vs[1],
-                           static_cast<T *>(a.vp) + page * a.vps[0] + slot * a.vps[1] + h * a.vps[2], a.vps[2], count, ln);
 }
 
 // ------------------------------------------------------------------------------- backward
