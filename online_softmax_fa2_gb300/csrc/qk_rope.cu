@@ -386,9 +386,15 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     norm_rows<T, L, U, kInter>(x, store, static_cast<const T *>(a.w[s]), row, count, ln, a.rot, a.inv_d, a.eps);
 }
 
+// Blocks an SM, at least.  What a warp waits for (its rows, its token's place, the angles) is hidden by other warps: into
+// codes eight blocks of 64 registers a thread take 46 us for the tokens below, six of 74 49; twice the heads a warp, at 111
+// registers, 50 to 57, half 59.
+template <typename T>
+constexpr int append_blocks(bool q8) { return q8 && sizeof(T) == 2 ? 8 : 1; }
+
 // A warp takes one token, a tensor (q, k, v) and the part of its heads that its groups hold at once
 // (the token's sequence is looked up by the whole warp).  Measured: 44 us for 10148 tokens of 32 query and
-// 8 key heads of 128 in bf16, 5.8 TB/s.  Tasks of a token: cq parts of q, then ck of k,
+// 8 key heads of 128 in bf16, 5.8 TB/s; into codes 46 us, 5.0 TB/s.  Tasks of a token: cq parts of q, then ck of k,
 // then ck of v.
 struct AppendArgs {
     int B, T, Hq, Hk, d, rot, P, cq, ck;
@@ -409,7 +415,7 @@ struct AppendArgs {
 };
 
 template <typename T, int L, int U, bool kInter, bool kQ8>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, append_blocks<T>(kQ8)) paged_append_kernel(const AppendArgs a) {
     ptx::grid_dep_wait();
     ptx::launch_dependents();
     const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5);
