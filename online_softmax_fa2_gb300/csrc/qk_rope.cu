@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
 // codes eight blocks of 64 registers a thread take 46 us for the tokens below, six of 74 49; twice the heads a warp, at 111
 // registers, 50 to 57, half 59.
 template <typename T>
-constexpr int append_blocks(bool q8) { return q8 && sizeof(T) == 2 ? 8 : 1; }
+constexpr int append_blocks(bool q8) { return q8 && sizeof(T) == 2 ? 8 : 0; }  // (0: as the compiler likes)
 
 // A warp takes one token, a tensor (q, k, v) and the part of its heads that its groups hold at once
 // (the token's sequence is looked up by the whole warp).  Measured: 44 us for 10148 tokens of 32 query and
