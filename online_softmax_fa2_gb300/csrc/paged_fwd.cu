@@ -49,7 +49,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, i
     pl.tc = rows > (one / G) * G ? 2 : rows > 16 ? 1 : 0;
     pl.tile_rows = rows > (64 / G) * G ? 128 : 64;
     // (the tiles take whole tokens, so that TMA can bring their queries)
-    pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : 16;
+    pl.R = pl.tc ? (int)(pl.tc * (pl.tile_rows / G) * G) : q8 && rows <= 8 ? 8 : 16;
     pl.kt = pl.tc || q8 ? 7 : 6;
     pl.box = pl.tc ? (q8 ? kTcQ8BoxKeys : kTcBoxKeys) : q8 ? kRowsQ8Keys : kRowsBoxKeys;
     const int sms = sm_count() ? sm_count() : 152;

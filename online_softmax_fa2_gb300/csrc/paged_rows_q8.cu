@@ -1,4 +1,4 @@
-// paged_rows_q8.cu -- attention over a paged cache in 8 bits for few rows per key/value head: R = 16 rows a
+// paged_rows_q8.cu -- attention over a paged cache in 8 bits for few rows per key/value head: R = 8 or 16 rows a
 // block.
 //
 // As paged_rows.cu, with tiles of 128 keys: the same bytes a tile, and the same shares of the line.
@@ -12,6 +12,8 @@
 //   a value's scale goes into its weights, as 2^(f_j - F) with F the largest f_j met: u is held in units of
 //   2^(F - 127), and rescaled when F grows as it is when the maximum does.  The weights, at most 1, are
 //   rounded to fp16 (half a step 2^-11 of a weight of 2^-14 or more, 2^-25 below).
+// With 16 rows the rows are the products' 16 and the keys or dimensions their 8; with 8 rows or fewer (a decode step of up to 8
+// query heads a key head) it is the other way round, S and O transposed: half the products, and half the logits a thread.
 // Fragments come by ldmatrix from the codes as they lie, two codes an element, in an order of the
 // contraction that the other operand is brought into:
 //   K   a register holds four neighbouring dimensions of a key, in the places of 2t, 2t + 1, 2t + 8 and
@@ -34,9 +36,8 @@ namespace {
 
 constexpr int kConsumers = 128, kThreads = kConsumers + 32;
 constexpr int KT = kRowsQ8Keys;  // keys a tile
-constexpr int R = 16;            // rows a block
 
-template <int D>
+template <int D, int R>
 struct Rows {
     static constexpr int kTile = KT * D;                // codes of K or V; rows of 128 or 64 bytes, swizzled over as many
     static constexpr int kBlocks = rows_blocks(D);
@@ -57,10 +58,10 @@ struct Ctrl {
     int abort, last;
 };
 
-template <int D>
+template <int D, int R>
 constexpr int smem_bytes() {
-    constexpr int n = Rows<D>::kCtrlOff + (int)sizeof(Ctrl) + 1024;
-    static_assert((n + 1024) * Rows<D>::kBlocks <= 228 * 1024, "shared memory of the CTAs an SM holds");
+    constexpr int n = Rows<D, R>::kCtrlOff + (int)sizeof(Ctrl) + 1024;
+    static_assert((n + 1024) * Rows<D, R>::kBlocks <= 228 * 1024, "shared memory of the CTAs an SM holds");
     return n;
 }
 
@@ -81,10 +82,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
+// Four 8x8 matrices, each transposed as it is stored; lane i gives the address of row i % 8 (a column of the registers) of
+// matrix i / 8.
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
     paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
-    using L = Rows<D>;
+    using L = Rows<D, R>;
+    constexpr bool kTurned = R == 8;  // S and O transposed
     constexpr int NS = L::kStages, DW = D / 4;  // DW: a warp's dimensions of O
     constexpr int NG = DW / 16;                 // in groups of 16
     extern __shared__ uint8_t smem_raw[];
@@ -190,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     float *sums = red + 4 * R;
     int st = 0, ph = 0;
     // a block's queries, D / 8 neighbouring threads a row, 16 bytes each (rows past the block's end are zero)
-    constexpr int QC = R * (D / 8) / kConsumers;
+    constexpr int QN = R * (D / 8), QC = (QN + kConsumers - 1) / kConsumers;  // (whole warps without a row, with 8 of 64)
     uint4 qv[QC];
     auto bring_q = [&](const Walk &p) {
         const int left = p.seq.nq * a.G - p.k * R;
@@ -198,14 +207,17 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         for (int u = 0; u < QC; ++u) {
             const int i = threadIdx.x + u * kConsumers, r = i / (D / 8), c = i % (D / 8), row = p.k * R + r, tok = div_g(a, row);
             qv[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < left)
+            if (i < QN && r < left)
                 qv[u] = __ldg(reinterpret_cast<const uint4 *>(a.q + (p.seq.q0 + tok) * a.qs0 + (p.hk * a.G + row - tok * a.G) * a.qs1 + c * 8));
         }
     };
+    // this lane's two rows
+    auto row_of = [&](int e) { return kTurned ? 2 * t + e : 8 * e + g; };
     auto store_q = [&]() {
 #pragma unroll
         for (int u = 0; u < QC; ++u) {
             const int i = threadIdx.x + u * kConsumers, r = i / (D / 8), c = i % (D / 8);
+            if (i >= QN) break;
             const uint32_t w[4] = {qv[u].x, qv[u].y, qv[u].z, qv[u].w};
             uint32_t top = 0;  // the largest finite magnitude, as bits of a bf16
 #pragma unroll
@@ -232,11 +244,11 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     while (more) {
         const Walk p = w;
         const int rows = min(R, p.seq.nq * a.G - p.k * R), row0 = p.k * R;
-        int lim[2];  // keys < lim are visible to this lane's rows 8 e + g
-        float m[2], l[2], o[DW / 8][4];
+        int lim[2];  // keys < lim are visible to this lane's rows
+        float m[2], l[2], o[kTurned ? NG : DW / 8][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 8 * e + g;
+            const int r = row_of(e);
             lim[e] = (a.causal && r < rows) ? min(max(p.seq.n - p.seq.nq + div_g(a, row0 + r) + 1, 0), p.seq.n) : p.seq.n;
             m[e] = -INFINITY;
             l[e] = 0.f;
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         const int lim0 = a.causal ? min(max(p.seq.n - p.seq.nq + div_g(a, row0) + 1, 0), p.seq.n) : p.seq.n;
         uint32_t F = 0;  // u is in units of 2^(F - 127)
 #pragma unroll
-        for (int nt = 0; nt < DW / 8; ++nt)
+        for (int nt = 0; nt < (kTurned ? NG : DW / 8); ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
         consumer_sync();  // the last piece is done with the queries and with sums
@@ -252,10 +264,12 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         consumer_sync();
         more = w.next(a);
         if (more) bring_q(w);
-        uint32_t qf[D / 16][4];
+        uint32_t qf[kTurned ? D / 32 : D / 16][4];  // of 16 dimensions, or 32
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) ldsm_x4(smem_addr(sQ + ((mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf[kk]);
-        const float un[2] = {unit[g], unit[8 + g]};
+        for (int kk = 0; kk < (kTurned ? D / 32 : D / 16); ++kk)
+            ldsm_x4(smem_addr(kTurned ? sQ + mr * L::kQRow + (4 * kk + mi) * 16
+                                      : sQ + ((mi & 1) * 8 + mr) * L::kQRow + (2 * kk + (mi >> 1)) * 16), qf[kk]);
+        const float un[2] = {unit[row_of(0)], unit[row_of(1)]};
 
         for (int j = p.j0; p.keys > 0 && j < p.j1; ++j) {
             const int kv0 = j * KT;
@@ -266,46 +280,73 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             uint8_t *sK = smem + st * 2 * L::kTile, *sV = sK + L::kTile;
             const uint8_t *sKs = smem + L::kScaleOff + st * 2 * KT, *sVs = sKs + KT;
 
-            // S of this warp's 32 keys, four products of eight
-            float s[4][4];
+            // S of this warp's 32 keys: s[n] of rows 8 e + g and keys 8 n + 2 t + i in 2 e + i, or (turned) of keys
+            // 16 n + 8 i + g and rows 2 t + e in 2 i + e
+            constexpr int NS_ = kTurned ? 2 : 4;
+            float s[NS_][4];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int nt = 0; nt < NS_; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t kf[4];
+                uint32_t kf[4], lo[4], hi[4];
                 ldsm_x4(smem_addr(sK + chunk_at<D>(32 * warp + 8 * mi + mr, kk)), kf);
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    uint32_t b0, b1;
-                    q8::decode4(kf[nt], b0, b1);
-                    mma_f16(s[nt], qf[kk], b0, b1);
+                for (int nt = 0; nt < 4; ++nt) q8::decode4(kf[nt], lo[nt], hi[nt]);
+                if constexpr (kTurned) {
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint32_t k4[4] = {lo[2 * nt], lo[2 * nt + 1], hi[2 * nt], hi[2 * nt + 1]};
+                        mma_f16(s[nt], k4, qf[kk / 2][2 * (kk & 1)], qf[kk / 2][2 * (kk & 1) + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) mma_f16(s[nt], qf[kk], lo[nt], hi[nt]);
                 }
             }
+            // the places of s: key of the tile and element of row e's i-th
+            auto key_of = [&](int nt, int i) { return 32 * warp + (kTurned ? 16 * nt + 8 * i + g : 8 * nt + 2 * t + i); };
+            auto at_of = [](int e, int i) { return kTurned ? 2 * i + e : 2 * e + i; };
+            auto bytes_of = [&](const uint8_t *from, int nt, uint32_t (&b)[2]) {
+                if constexpr (kTurned) {
+                    b[0] = from[key_of(nt, 0)];
+                    b[1] = from[key_of(nt, 1)];
+                } else {
+                    const uint32_t two = *reinterpret_cast<const uint16_t *>(from + key_of(nt, 0));
+                    b[0] = two & 255u;
+                    b[1] = two >> 8;
+                }
+            };
             // scale, mask, row maxima of this warp's keys
             const bool edge = kv0 + KT > lim0;
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int at = 32 * warp + 8 * nt + 2 * t;
-                const uint32_t es = *reinterpret_cast<const uint16_t *>(sKs + at);
-                const float sc[2] = {q8::pow2(es & 255u), q8::pow2(es >> 8)};
+            for (int nt = 0; nt < NS_; ++nt) {
+                uint32_t b[2];
+                bytes_of(sKs, nt, b);
+                const float sc[2] = {q8::pow2(b[0]), q8::pow2(b[1])};
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = s[nt][2 * e + i] * un[e] * sc[i];
-                        if (edge && kv0 + at + i >= lim[e]) x = -INFINITY;
-                        s[nt][2 * e + i] = x;
+                        float x = s[nt][at_of(e, i)] * un[e] * sc[i];
+                        if (edge && kv0 + key_of(nt, i) >= lim[e]) x = -INFINITY;
+                        s[nt][at_of(e, i)] = x;
                         mx[e] = fmaxf(mx[e], x);
                     }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                if (t == 0) red[warp * R + 8 * e + g] = mx[e];
+                if constexpr (kTurned) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+                    if (g == 0) red[warp * R + row_of(e)] = mx[e];
+                } else {
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                    if (t == 0) red[warp * R + row_of(e)] = mx[e];
+                }
             }
             // the largest value scale of the tile's keys (255, a NaN, is none)
             uint32_t big = 0;
@@ -328,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             F = big;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * e + g;
+                const int r = row_of(e);
                 const float mn = fmaxf(fmaxf(m[e], fmaxf(red[r], red[R + r])), fmaxf(red[2 * R + r], red[3 * R + r]));
                 const float ref = mn == -INFINITY ? 0.f : mn;
                 al[e] = ptx::ex2(m[e] - ref);
@@ -336,39 +377,55 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                 m[e] = mn;
                 l[e] *= al[e];
             }
+            uint32_t pk[NS_][2];  // weights: two keys of row e, or (turned) two rows of the i-th key
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int at = 32 * warp + 8 * nt + 2 * t;
-                const uint32_t es = *reinterpret_cast<const uint16_t *>(sVs + at);
-                float sc[2];  // 2^(f - F); NaN for 255
+            for (int nt = 0; nt < NS_; ++nt) {
+                uint32_t b[2];
+                bytes_of(sVs, nt, b);
+                float sc[2], w[4];  // 2^(f - F); NaN for 255
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t f = i ? es >> 8 : es & 255u;
-                    sc[i] = f == 255u ? NAN : __uint_as_float((f + 127 > F ? f + 127 - F : 0u) << 23);
-                }
+                for (int i = 0; i < 2; ++i) sc[i] = b[i] == 255u ? NAN : __uint_as_float((b[i] + 127 > F ? b[i] + 127 - F : 0u) << 23);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float ref = m[e] == -INFINITY ? 0.f : m[e];
-                    const float p0 = ptx::ex2(s[nt][2 * e] - ref), p1 = ptx::ex2(s[nt][2 * e + 1] - ref);
-                    l[e] += p0 + p1;
-                    // (a hidden key's scale may be anything)
-                    *reinterpret_cast<uint32_t *>(sP + (8 * e + g) * L::kPRow + at * 2) =
-                        q8::pack_f16(p0 == 0.f ? 0.f : p0 * sc[0], p1 == 0.f ? 0.f : p1 * sc[1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float p0 = ptx::ex2(s[nt][at_of(e, i)] - ref);
+                        l[e] += p0;
+                        w[at_of(e, i)] = p0 == 0.f ? 0.f : p0 * sc[i];  // (a hidden key's scale may be anything)
+                    }
                 }
+                pk[nt][0] = q8::pack_f16(w[0], w[1]);
+                pk[nt][1] = q8::pack_f16(w[2], w[3]);
+            }
+            if constexpr (kTurned) {
+                stsm_x4_trans(smem_addr(sP + mr * L::kPRow + (32 * warp + 8 * mi) * 2), pk[0][0], pk[0][1], pk[1][0], pk[1][1]);
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint32_t *>(sP + row_of(e) * L::kPRow + (32 * warp + 8 * nt + 2 * t) * 2) = pk[nt % NS_][e];
             }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int nt = 0; nt < DW / 8; ++nt)
+                for (int nt = 0; nt < (kTurned ? NG : DW / 8); ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nt][e] *= al[e >> 1] * grow;
+                    for (int e = 0; e < 4; ++e) o[nt][e] *= al[kTurned ? e & 1 : e >> 1] * grow;
             }
             consumer_sync();
-            // O of this warp's dimensions: products 2 gi and 2 gi + 1 take the even and the odd dimensions of a group
+            // O of this warp's dimensions: o[2 gi] and o[2 gi + 1] of the even and the odd dimensions of a group, or (turned)
+            // o[gi] of dimensions 2 g in 0, 1 and 2 g + 1 in 2, 3
 #pragma unroll
             for (int kk = 0; kk < KT / 32; ++kk) {
                 uint32_t pf[2][4];
+                if constexpr (kTurned) {
+                    ldsm_x4(smem_addr(sP + mr * L::kPRow + (4 * kk + mi) * 16), pf[0]);
+                } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) ldsm_x4(smem_addr(sP + ((mi & 1) * 8 + mr) * L::kPRow + (4 * kk + 2 * h + (mi >> 1)) * 16), pf[h]);
+                    for (int h = 0; h < 2; ++h)
+                        ldsm_x4(smem_addr(sP + ((mi & 1) * 8 + mr) * L::kPRow + (4 * kk + 2 * h + (mi >> 1)) * 16), pf[h]);
+                }
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
                     uint32_t vf[4];  // 32 keys of 16 dimensions
@@ -378,8 +435,13 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
                     for (int k = 0; k < 4; ++k) q8::decode4(__byte_perm(vf[k], 0, 0x3120), ev[k], od[k]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        mma_f16(o[2 * gi], pf[h], ev[2 * h], ev[2 * h + 1]);
-                        mma_f16(o[2 * gi + 1], pf[h], od[2 * h], od[2 * h + 1]);
+                        if constexpr (kTurned) {
+                            const uint32_t v4[4] = {ev[2 * h], od[2 * h], ev[2 * h + 1], od[2 * h + 1]};
+                            mma_f16(o[gi], v4, pf[0][2 * h], pf[0][2 * h + 1]);
+                        } else {
+                            mma_f16(o[2 * gi], pf[h], ev[2 * h], ev[2 * h + 1]);
+                            mma_f16(o[2 * gi + 1], pf[h], od[2 * h], od[2 * h + 1]);
+                        }
                     }
                 }
             }
@@ -390,13 +452,19 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         }
 
         // ------------------------------------------------------------ the piece's rows
-        // row sums: over the quad, then over the four warps
+        // row sums: over the lanes of a row, then over the four warps
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             float v = l[e];
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            if (t == 0) sums[warp * R + 8 * e + g] = v;
+            if constexpr (kTurned) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+                if (g == 0) sums[warp * R + row_of(e)] = v;
+            } else {
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                if (t == 0) sums[warp * R + row_of(e)] = v;
+            }
         }
         consumer_sync();
         wait_for_states(a);
@@ -406,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
         const float vu = q8::pow2(F);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int r = 8 * e + g;
+            const int r = row_of(e);
             if (r >= rows) continue;
             float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
@@ -415,20 +483,29 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
             if (whole) end = ending(a, at, tok, m[e], sum);
             const bool empty = sum == 0.f;  // a NaN is no empty row: it goes on into o and lse
             const float inv = empty ? 0.f : 1.f / sum;
+            constexpr int C = kTurned ? 2 : 4;  // neighbouring columns a lane has of a group
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-                const int col = warp * DW + 16 * gi + 4 * t;
-                float v[4] = {o[2 * gi][2 * e] * vu, o[2 * gi + 1][2 * e] * vu, o[2 * gi][2 * e + 1] * vu, o[2 * gi + 1][2 * e + 1] * vu};
-                if (!whole) {
-                    *reinterpret_cast<float4 *>(a.u + (slot * R + r) * D + col) = make_float4(v[0], v[1], v[2], v[3]);
-                    continue;
+                const int col = warp * DW + 16 * gi + C * (kTurned ? g : t);
+                float v[C];
+                if constexpr (kTurned) {
+                    v[0] = o[gi][e] * vu;
+                    v[1] = o[gi][2 + e] * vu;
+                } else {
+                    v[0] = o[2 * gi][2 * e] * vu;
+                    v[1] = o[2 * gi + 1][2 * e] * vu;
+                    v[2] = o[2 * gi][2 * e + 1] * vu;
+                    v[3] = o[2 * gi + 1][2 * e + 1] * vu;
                 }
-                end_u<4>(end, at, col, v, sum);
-                if (!end.written)
-                    *reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + col) =
-                        empty ? make_uint2(0u, 0u) : make_uint2(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv));
+                if (whole) end_u<C>(end, at, col, v, sum);
+                if (whole && end.written) continue;
+#pragma unroll
+                for (int c = 0; c < C; c += 2) {
+                    if (!whole) *reinterpret_cast<float2 *>(a.u + (slot * R + r) * D + col + c) = make_float2(v[c], v[c + 1]);
+                    else *reinterpret_cast<uint32_t *>(a.o + tok * a.os0 + h * a.os1 + col + c) = empty ? 0u : pack_bf16(v[c] * inv, v[c + 1] * inv);
+                }
             }
-            if (warp == 0 && t == 0) {
+            if (warp == 0 && (kTurned ? g : t) == 0) {
                 if (!whole)
                     *reinterpret_cast<float2 *>(a.ml + (slot * R + r) * 2) = make_float2(empty ? -INFINITY : m[e], sum);
                 else if (end.written) write_ml(end, at, m[e], sum);
@@ -451,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
     end_after_earlier_grids(a);
 }
 
-template <int D>
+template <int D, int R>
 attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int grid, cudaStream_t st) {
-    auto kern = paged_rows_q8_kernel<D>;
-    const int smem = smem_bytes<D>();
+    auto kern = paged_rows_q8_kernel<D, R>;
+    const int smem = smem_bytes<D, R>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, mk, mv, a);
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_rows_q8 launch: %s", cudaGetErrorString(e));
@@ -463,7 +540,8 @@ attn_status_t launch(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a
 }  // namespace
 
 attn_status_t launch_paged_rows_q8(const CUtensorMap &mk, const CUtensorMap &mv, const Args &a, int d, int grid, cudaStream_t st) {
-    return d == 64 ? launch<64>(mk, mv, a, grid, st) : launch<128>(mk, mv, a, grid, st);
+    if (a.R == 8) return d == 64 ? launch<64, 8>(mk, mv, a, grid, st) : launch<128, 8>(mk, mv, a, grid, st);
+    return d == 64 ? launch<64, 16>(mk, mv, a, grid, st) : launch<128, 16>(mk, mv, a, grid, st);
 }
 
 }  // namespace attn
