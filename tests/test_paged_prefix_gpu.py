@@ -240,3 +240,112 @@ def test_python_refusals():
     with pytest.raises(ofa.AttnError) as e:
         ofa.attn_paged_prefix_fwd(*a, k_scales=s["ks"], v_scales=s["vs"], workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
     assert e.value.status == ofa.Status.WORKSPACE
+
+
+BESIDE = [  # decode steps: the own keys' attention beside the prefixes'; new, lens, prefix lengths, cuts, Hq, Hkv, d, page
+    ([1] * 40, [30 + 5 * i for i in range(40)], [3000, 10, 0, 700], [3, 13, 20, 30, 38], 8, 2, 128, 16),   # finished and cut prefixes, tokens with none
+    ([1] * 70, [1 + 40 * i % 900 for i in range(70)], [5000], [0, 70], 32, 8, 128, 64),
+    ([2] * 12, [2] * 12, [129] * 3, [0, 8, 16, 24], 16, 2, 64, 32),
+    ([3, 0, 4, 1] * 8, [900, 0, 4, 0] * 8, [2500, 2500], [0, 33, 64], 4, 2, 64, 128),
+    ([1] * 300, [17] * 300, [6000], [0, 300], 4, 1, 128, 16),                                             # more rows than two tiles
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("case", BESIDE)
+def test_decode_steps_behind_prefixes(case, q8):
+    new, lens, plens, cuts, Hq, Hkv, d, page = case
+    s, groups = inputs(new, lens, plens, cuts, Hq, Hkv, d, page, q8, seed=5)
+    want = None
+    n = ofa.paged_prefix_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["pt"], s["plens"], s["cu"], s["pcu"], max(new),
+                                             k_scales=s.get("ks"), v_scales=s.get("vs"))
+    ofa.device_error_flags()
+    for fill in (0, 255, 191):  # (191: -1.5 in every word, 255: NaN)
+        o, lse = run(s, max_q=max(new), workspace=torch.full((n,), fill, dtype=torch.uint8, device=DEV))
+        assert ofa.device_error_flags() == 0
+        if want is None:
+            check_attention(o, lse, s, new, lens, True, 1 / math.sqrt(d), groups, plens, what=f"fill {fill}")
+            want = o, lse
+        assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse.view(torch.int32), want[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_decode_steps_captured_one_after_the_other(q8):
+    """Steps of two batches in one graph over one workspace, replayed with other lengths in the same tensors."""
+    new = [1] * 24
+    steps = [inputs(new, [40 + i for i in range(24)], [1500], [0, 24], 8, 2, 128, 16, q8, seed=k) for k in (6, 7)]
+    ws = torch.zeros(max(ofa.paged_prefix_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["pt"], s["plens"], s["cu"], s["pcu"], 1,
+                                                              k_scales=s.get("ks"), v_scales=s.get("vs")) for s, _ in steps), dtype=torch.uint8, device=DEV)
+    outs = [(torch.zeros_like(s["q"]), torch.zeros(24, 8, device=DEV)) for s, _ in steps]
+
+    def go():
+        for (s, _), (o, lse) in zip(steps, outs):
+            run(s, max_q=1, workspace=ws, out=o, lse=lse)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        go()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+        go()
+    for lens, plen in (([40 + i for i in range(24)], 1500), ([1 + 2 * i for i in range(24)], 700), ([0] * 24, 3)):
+        for s, _ in steps:
+            s["lens"].copy_(torch.tensor(lens))
+            s["plens"].fill_(plen)
+        ws.random_(0, 256)
+        graph.replay()
+        torch.cuda.synchronize()
+        for (s, groups), (o, lse) in zip(steps, outs):
+            check_attention(o, lse, s, new, lens, True, 1 / math.sqrt(128), groups, [plen], what=str(plen))
+    assert ofa.device_error_flags() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    data = [inputs([1] * 30, [100 + i for i in range(30)], [2000], [0, 30], 16, 4, 128, 16, q8, seed=8)[0] for q8 in (False, True)]
+    data.append(inputs([60, 1, 30], [200, 300, 30], [900], [0, 91], 8, 2, 64, 32, False, seed=9)[0])
+    want = [run(s) for s in data]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in data], [[] for _ in data]
+    for _ in range(6):
+        for i, s in enumerate(data):
+            got[i].append(run(s, stream=streams[i]))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        for o, lse in outs:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+def test_steps_back_to_back_read_what_the_append_before_wrote():
+    """Appends and prefix attention queued without a pause: each attention starts early beside the work before it, and still
+    sees its tokens, lengths and keys."""
+    Hq, Hkv, d, page, P, B, steps = 8, 2, 128, 16, 900, 40, 6
+    g = torch.Generator().manual_seed(5)
+    rnd = lambda *x: torch.randn(*x, generator=g).bfloat16().to(DEV)  # noqa: E731
+    pages = 57 + B + 1
+    perm = torch.randperm(pages, generator=g).int().to(DEV)
+    pt, bt = perm[:57][None], perm[57:57 + B].view(B, 1)
+    plens = torch.tensor([P], dtype=torch.int32, device=DEV)
+    base = [rnd(pages, page, Hkv, d) for _ in "kv"]
+    qkv = [(rnd(B, Hq, d), rnd(B, Hkv, d), rnd(B, Hkv, d)) for _ in range(steps)]
+
+    def go(sync):
+        cache = [t.clone() for t in base]
+        lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+        got = []
+        torch.cuda.synchronize()
+        for q, k, v in qkv:
+            lens += 1
+            qr = ofa.attn_paged_append(q, k, v, *cache, bt, lens)
+            got.append(ofa.attn_paged_prefix_fwd(qr, *cache, bt, lens, pt, plens))
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return got
+
+    want = go(True)
+    for _ in range(5):
+        for (o, lse), (wo, wl) in zip(go(False), want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
