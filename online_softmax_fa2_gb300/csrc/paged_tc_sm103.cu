@@ -21,6 +21,8 @@
 //                right after the last P of this one, so that its first S runs under this one's
 //                epilogue.
 //   warp 2       finds the share; warp 3 writes down what the merge has to know.
+//   Over a cache in 8 bits warps 12-15 (with one tile warps 2 and 3) make fp16 operands of the codes, warp 0 brings K's and
+//   warp 2 V's (with one tile warp 0 both): see "a cache of codes" below.
 // A row's state over its part of an item goes to the workspace when the item is cut, and
 // paged_tc_merge_kernel merges the parts.
 //
@@ -344,6 +346,11 @@ __device__ __forceinline__ void write_cut(const paged::Args &a, const Share &sha
 // TMA brings, code times 2^(e - E) with E the largest scale byte of a tile's keys, or for V one that holds for
 // as many tiles as no byte passes it by more than 6 (448 * 2^6 < 65504); both go to the softmax, which takes E into the
 // tile's factor of the logits, and rescales u when V's changes.  (Codes are exact down to 15 below E.)
+//
+// What bounds it: shared memory.  Of a 256 x 128 tile the products read 192 KB of it (1536 clocks of 128 bytes), the codes'
+// way takes 128 KB more (in by TMA, out to registers, back as fp16), of the 3030 clocks that the tile takes over bf16:
+// 3700 here, 2048 tokens over 18432 keys of 32/8 heads 462 us against 394, 1.26 PFLOP/s; 16 ragged sequences to 4096 keys,
+// chunks to 512 tokens, 28/4 heads 100 us against 75.  The issuer waits for operands 220 clocks of a tile, for weights 670.
 
 // A producer of K's (0), V's (1) or both kinds' (2) codes, in the order in which the converting warps come to them, and
 // scale bytes, four a lane, loaded a tile ahead.  (Copies by lanes of a warp go out one after the other, each as long as a
@@ -1009,9 +1016,9 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
 // searched for.
 //
 // CTA (c, tile, columns) takes the item whose first part is the end of share c, if there is one; with GR = 4, where
-// items are cut into many parts (launch_paged_tc), four threads share a row, each every fourth part, and a CTA looks at
-// kMergeShares shares, so that the few CTAs with work and the others are one wave: 64 rows x 4 heads over 8192 keys in 19
-// parts an item 8.5 us from a CTA a share and 32 columns, .. so.
+// items are cut into many parts (launch_paged_tc_merge), four threads share a row, each every fourth part, and a CTA looks
+// at merge_shares shares, so that the few CTAs with work and the others are one wave: 64 tokens of 32/8 heads over 8192
+// keys, in 19 parts an item, 8.5 us with a CTA a share and 32 columns, 6 so.
 constexpr int merge_cols(int GR) { return GR == 1 ? 32 : 16; }
 constexpr int merge_shares(int GR) { return GR == 1 ? 1 : 8; }
 
