@@ -26,10 +26,11 @@ struct Plan {
     size_t off_ml, off_u, bytes;
 };
 
-// Tiles that a CTA of a prefix's attention takes beside the own keys' (a tile of codes takes longer): with 6, 8 and 10 the
-// 64 sequences of PrefixPlan's take 63, 56 and 56 us; 32 sequences of 4 tokens over codes behind two prefixes of 4096 keys,
-// 16/4 heads, 29, 38 and 39.  And the most tiles a CTA of the own keys' for which it keeps to the other SMs.
-constexpr int kBesideTiles = 8, kBesideTilesQ8 = 6, kBesideRows = 80;
+// Tiles that a CTA of a prefix's attention takes beside the own keys' (a tile of codes takes longer): with 8, 10, 12 and 14
+// the 64 sequences of PrefixPlan's take 55, 54, 53 and 57 us; 32 sequences of 4 tokens over codes behind two prefixes of 4096
+// keys, 16/4 heads, with 5, 6, 8 and 10 29, 29, 37 and 42.  And the most tiles a CTA of the own keys' for which it keeps to
+// the other SMs.
+constexpr int kBesideTiles = 10, kBesideTilesQ8 = 6, kBesideRows = 80;
 
 // beside: another attention runs at the same time, on `taken` SMs.
 Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, int taken = 0) {
@@ -238,7 +239,7 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 //
 // Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, runs on the
 // SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
-// their own, 32/8 heads of 128: 56 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
+// their own, 32/8 heads of 128: 54 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
 // every SM busy by themselves: one after the other, the second beginning as SMs come free.
 struct PrefixPlan {
     Plan over, own;

@@ -1145,12 +1145,20 @@ __global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel
         merge_whole<D, GR>(a, ((int)blockIdx.x - items) * NT + X, col);
         return;
     }
+    // a record a lane: one look at all
     const int4 *rec = reinterpret_cast<const int4 *>(reinterpret_cast<const Cut *>(a.marks) + blockIdx.x * S);
+    const int lane = threadIdx.x & 31;
+    int4 r0 = make_int4(0, 0, 0, 0), r1 = r0;  // n[2], row0, end | q0, hk
+    if (lane < S && (int)blockIdx.x * S + lane < shares) {
+        r0 = __ldcg(rec + 2 * lane);
+        r1 = __ldcg(rec + 2 * lane + 1);
+    }
     bool again = false;
 #pragma unroll 1
-    for (int i = 0; i < S && (int)blockIdx.x * S + i < shares; ++i) {
-        const int4 c0 = __ldcg(rec + 2 * i), c1 = __ldcg(rec + 2 * i + 1);  // n[2], row0, end | q0, hk
-        if ((X ? c0.y : c0.x) < 2) continue;  // the whole CTA
+    for (unsigned cut = __ballot_sync(0xffffffffu, (X ? r0.y : r0.x) >= 2); cut; cut &= cut - 1) {
+        const int i = __ffs(cut) - 1;
+        auto of = [&](int v) { return __shfl_sync(0xffffffffu, v, i); };
+        const int4 c0 = make_int4(of(r0.x), of(r0.y), of(r0.z), of(r0.w)), c1 = make_int4(of(r1.x), of(r1.y), 0, 0);
         if (GR > 1 && again) __syncthreads();  // the last one's buffers
         again = true;
         merge_item<D, NT, GR, kState>(a, blockIdx.x * S + i, X, col, c0, c1, top, part);
