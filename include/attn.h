@@ -602,7 +602,8 @@ typedef struct {
  * attn_paged_append_q8 -- attn_paged_append into a cache in 8 bits: the keys are quantised as they come
  * from the norm and the rotation, in fp32, the values as they are.  e - 127 is the smallest exponent >=
  * -127 that brings the row's largest finite magnitude within 448 * 2^(e - 127) (0 for a row of zeros), and
- * the elements are rounded to the nearest code, ties to even.  A NaN or an infinity is held as NaN.
+ * the elements are rounded to the nearest code, ties to even.  A NaN or an infinity is held as NaN.  Two tokens with one
+ * place leave it with codes and a scale of either.
  * Supported: as attn_paged_append; the pages' strides are multiples of 16 bytes, as their bases.  Queues one kernel.
  */
 attn_status_t attn_paged_append_q8(const attn_paged_append_q8_params_t *params, attn_stream_t stream);
@@ -684,7 +685,9 @@ size_t attn_paged_prefix_fwd_workspace_bytes(const attn_paged_prefix_params_t *p
  * same product); the rows' states (m, l, u) over it and over the own keys meet in the workspace, in fp32, and are
  * merged.  ("How Does FlashAttention Preserve Global Softmax Across Tiles?", section 3.)  The result
  * is that of attn_paged_fwd over the prefix's keys followed by the own ones, lse included, with its rules for empty rows,
- * NaN and tokens of no sequence; no token has to belong to a prefix.
+ * NaN and tokens of no sequence; no token has to belong to a prefix.  (A row that the causal rule lets see no own key, as it lies
+ * before them all, sees its whole prefix.)  How the GPU is shared out between the prefixes and the own keys goes by the
+ * tables' widths: tables no wider than their longest entry (a view will do) are fastest.
  * Supported: as attn_paged_fwd, or attn_paged_fwd_q8; 1 <= P <= 65535.  Queues two to four kernels.
  */
 attn_status_t attn_paged_prefix_fwd(const attn_paged_prefix_params_t *params, void *workspace, size_t workspace_bytes,

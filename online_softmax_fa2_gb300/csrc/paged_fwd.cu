@@ -26,14 +26,8 @@ struct Plan {
     size_t off_ml, off_u, bytes;
 };
 
-// Tiles that a CTA of a prefix's attention takes beside the own keys' (a tile of codes takes longer): with 8, 10, 12 and 14
-// the 64 sequences of PrefixPlan's take 55, 54, 53 and 57 us; 32 sequences of 4 tokens over codes behind two prefixes of 4096
-// keys, 16/4 heads, with 5, 6, 8 and 10 29, 29, 37 and 42.  And the most tiles a CTA of the own keys' for which it keeps to
-// the other SMs.
-constexpr int kBesideTiles = 10, kBesideTilesQ8 = 6, kBesideRows = 80;
-
-// beside: another attention runs at the same time, on `taken` SMs.
-Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, int taken = 0) {
+// ctas: at most as many, 0: as many as the GPU holds.
+Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, int ctas = 0) {
     const attn_paged_cache_t &c = p.cache;
     const int64_t G = p.Hq / c.Hkv;
     // tokens a sequence, or their mean
@@ -60,16 +54,7 @@ Plan make_plan(const attn_paged_fwd_params_t &p, bool q8, bool beside = false, i
     pl.fits = tiles < (double)kLongestLine;
     const int64_t full = (int64_t)sms * (pl.tc ? 3 - pl.tc : rows_blocks(c.d));
     pl.grid = (int)(tiles < (double)full ? (int64_t)tiles + 1 : full);
-    if (beside && pl.tc) {
-        // (enough tiles a CTA that the states of its part are little beside them)
-        const int64_t most_tiles = c.Hkv * ((c.T * G + pl.R - 1) / pl.R + c.B - 1) * ((keys >> pl.kt) + 5), each = q8 ? kBesideTilesQ8 : kBesideTiles, some = (most_tiles + each - 1) / each;
-        if (some < pl.grid) pl.grid = (int)(some < 1 ? 1 : some);
-    }
-    // the SMs that are left, unless they would be few or have much to do
-    if (beside && !pl.tc && taken <= sms / 2 && tiles < (double)kBesideRows * (double)full) {
-        const int64_t left = full / sms * (sms - taken);
-        if (left < pl.grid) pl.grid = (int)left;
-    }
+    if (ctas > 0 && ctas < pl.grid) pl.grid = ctas;
     if (pl.grid > kGroup * kGroup) pl.grid = kGroup * kGroup;  // as many parts as two levels merge
     const size_t slots = pl.tc ? 2 * (size_t)pl.grid : (size_t)all_slots(pl.grid);
     // Tiles that a boundary has to leave at either side of a cut.  Less cuts more finely and merges more, and
@@ -239,20 +224,62 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 //
 // Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, runs on the
 // SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
-// their own, 32/8 heads of 128: 54 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
+// their own, 32/8 heads of 128: 52 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
 // every SM busy by themselves: one after the other, the second beginning as SMs come free.
 struct PrefixPlan {
     Plan over, own;
     bool beside;
     size_t off_u, off_ml2, off_u2, off_over, off_own, bytes;
 };
+
+// Blocks of an attention, and the line that they make, as far as the host knows them: of the mean's rows, over all the
+// keys that its table has room for.
+double blocks_of(const attn_paged_fwd_params_t &p, const Plan &pl) {
+    const attn_paged_cache_t &c = p.cache;
+    const int64_t mean = (c.T + c.B - 1) / c.B * (p.Hq / c.Hkv);
+    return (double)c.B * (double)((mean + pl.R - 1) / pl.R) * (double)c.Hkv;
+}
+double line_of(const attn_paged_fwd_params_t &p, const Plan &pl) {
+    return blocks_of(p, pl) * (double)(((p.cache.table_width * p.cache.page_size) >> pl.kt) + 4);
+}
+
+// SMs for the prefixes' attention, so that both end together.  On x of them it takes 4 + t W / x us beside its ends, the own
+// keys' on the others s U / CTAs, W and U their lines; t and s are what sweeps of x came to.  (20 kinds of batches,
+// 32 to 256 sequences with up to 64 to 4096 keys of their own behind 1 to 4 prefixes of 512 to 32768, 4 or 8 key heads, both
+// types of cache: x so chosen is within 4% of the best x but for four, within 9%.  With ten tiles a CTA, or six of codes,
+// whatever the own keys, the same took up to 30% more: 256 sequences with up to 512 keys behind 4096 105 us, so 81.)
+// Where x comes near a multiple of the blocks it is made one, which cuts all of them alike, or none.
+int prefix_sms(const PrefixPlan &r, const attn_paged_fwd_params_t &over, const attn_paged_fwd_params_t &own, bool q8) {
+    const int sms = sm_count() ? sm_count() : 152, most = sms - 8;
+    const double t = q8 ? 1.75 : 1.4, s = q8 ? 0.7 : 0.5, W = line_of(over, r.over), U = line_of(own, r.own);
+    int best = most;
+    double least = 1e30;
+    for (int x = 1; x <= most; ++x) {
+        if (W > 40. * x || (x > 1 && W < 4. * x)) continue;  // tiles a CTA
+        const double a = 4. + t * W / x, b = s * U / ((sms - x) * rows_blocks(own.cache.d)), longer = a > b ? a : b;
+        if (longer < least) {
+            least = longer;
+            best = x;
+        }
+    }
+    const double blocks = blocks_of(over, r.over), times = (double)(int64_t)(best / blocks + 0.5), even = times * blocks;
+    if (even >= 1. && even <= most && even - best <= best / 6. && best - even <= best / 6.) best = (int)even;
+    return best;
+}
+
 PrefixPlan make_prefix_plan(const attn_paged_prefix_params_t &p) {
     const bool q8 = p.scales.k != nullptr;
+    const attn_paged_fwd_params_t over = over_prefixes(p);
     PrefixPlan r;
     r.own = make_plan(p.fwd, q8);
-    r.over = make_plan(over_prefixes(p), q8, !r.own.tc);
-    r.beside = r.over.tc && !r.own.tc && r.over.cuts;
-    if (r.beside) r.own = make_plan(p.fwd, q8, true, r.over.grid);
+    r.over = make_plan(over, q8);
+    r.beside = r.over.tc && !r.own.tc;
+    if (r.beside) {
+        const int sms = sm_count() ? sm_count() : 152;
+        const int x = prefix_sms(r, over, p.fwd, q8);
+        r.over = make_plan(over, q8, x * (3 - r.over.tc));
+        r.own = make_plan(p.fwd, q8, (sms - x) * rows_blocks(p.fwd.cache.d));
+    }
     const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq, ml = round_up(rows * 2 * sizeof(float)),
                  u = round_up(rows * p.fwd.cache.d * sizeof(float));
     r.off_u = ml;

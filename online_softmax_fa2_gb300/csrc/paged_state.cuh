@@ -79,6 +79,34 @@ __device__ __forceinline__ void end_u(const Ending &e, const StateAt &at, int co
     for (int c = 0; c < C; ++c) v[c] = fmaf(e.before, y[c], e.own == 0.f ? 0.f : e.own * v[c]);
 }
 
+// The earlier state of C columns of a row, asked for before it is needed: (m, l) first, then u.
+template <int C>
+struct Earlier {
+    bool on;
+    float2 s;
+    float4 y[C / 4];
+    __device__ __forceinline__ void ask_ml(const Args &a, const StateAt &at, int tok, bool row) {
+        on = row && a.state.mode == kMerged && has_state(a, tok);
+        s = on ? __ldcg(a.state.ml + at.ml) : make_float2(-INFINITY, 0.f);
+    }
+    __device__ __forceinline__ void ask_u(const Args &a, const StateAt &at, int col) {
+        const float4 *u = reinterpret_cast<const float4 *>(a.state.u) + at.u + col / 4 * at.n;
+#pragma unroll
+        for (int c = 0; c < C / 4; ++c) y[c] = on ? __ldcg(u + c * at.n) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // As ending() and end_u().
+    __device__ __forceinline__ void merge(float (&v)[C], float &m, float &sum) const {
+        if (!on) return;
+        const float M = fmaxf(m, s.x), ref = M == -INFINITY ? 0.f : M;
+        const float own = sum == 0.f ? 0.f : ptx::ex2(m - ref), before = ptx::ex2(s.x - ref);
+        sum = fmaf(before, s.y, own == 0.f ? 0.f : own * sum);
+        m = M;
+        const float *x = reinterpret_cast<const float *>(y);
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = fmaf(before, x[c], own == 0.f ? 0.f : own * v[c]);
+    }
+};
+
 // Whether a merged row's outputs are the call's to write.
 __device__ __forceinline__ bool is_wanted(const Args &a, int tok) {
     if (!a.state.only) return true;

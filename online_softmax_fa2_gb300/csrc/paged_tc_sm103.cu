@@ -267,21 +267,19 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
     const bool empty = sum == 0.f;  // a NaN is no empty row
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
-    for (int cc = 0; cc < D / 16; ++cc) {
-        uint32_t ov[16];
-        tmem_ld16(taddr + cc * 16, ov);
+    for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t ov[32];
+        ptx::tmem_ld32(taddr + cc * 32, ov);
         ptx::tmem_ld_wait();
-        float v[16];
+        ptx::reg_fence(ov);
+        float v[32];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            asm volatile("" : "+r"(ov[t]));
-            v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
-        }
-        if (on) paged::end_u<16>(e, at, cc * 16, v, sum);
+        for (int t = 0; t < 32; ++t) v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
+        if (on) paged::end_u<32>(e, at, cc * 32, v, sum);
         if (on && !e.written) {
-            uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 16);
+            uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 32);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < 4; ++t) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) pk[e] = empty ? 0u : ptx::pack_bf16x2(v[8 * t + 2 * e] * inv, v[8 * t + 2 * e + 1] * inv);
@@ -1019,19 +1017,27 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
 // items are cut into many parts (launch_paged_tc_merge), four threads share a row, each every fourth part, and a CTA looks
 // at merge_shares shares, so that the few CTAs with work and the others are one wave: 64 tokens of 32/8 heads over 8192
 // keys, in 19 parts an item, 8.5 us with a CTA a share and 32 columns, 6 so.
-constexpr int merge_cols(int GR) { return GR == 1 ? 32 : 16; }
+// With states a thread takes 16 columns, so that what it asks for ahead stays in registers (of 32, the rows that were finished
+// alone took 8 us more).
+constexpr int merge_cols(int GR, bool state) { return GR == 1 && !state ? 32 : 16; }
 constexpr int merge_shares(int GR) { return GR == 1 ? 1 : 8; }
 
 template <int D, int NT, int GR, bool kState>
 __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, int col, int4 c0, int4 c1,
-                                           float (&top)[GR][BQ], float (&part)[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR) + 1]) {
-    constexpr int C = merge_cols(GR);
+                                           float (&top)[GR][BQ], float (&part)[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR, kState) + 1]) {
+    constexpr int C = merge_cols(GR, kState);
     const int r = threadIdx.x % BQ, g = threadIdx.x / BQ;
     const int n = X ? c0.y : c0.x, half = a.R / NT, row = c0.z + X * half + r;
     const bool mine = r < half && row < c0.w;
     const int parts = mine ? n : 0;
     auto slot = [&](int p) { return paged::state_slot(c + p, c); };
     float M = -INFINITY, sum = 0.f, v[C];
+    const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
+    paged::Earlier<kState ? C : 4> earlier;  // under the parts, as far as registers go
+    if (kState) {
+        earlier.ask_ml(a, at, c1.x + paged::div_g(a, row), mine && g == 0);
+        if (GR == 1) earlier.ask_u(a, at, col);
+    }
 #pragma unroll 4
     for (int p = g; p < parts; p += GR) M = fmaxf(M, __ldcg(state_ml<NT>(a, slot(p), X, r)).x);
     if (GR > 1) {
@@ -1043,7 +1049,7 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int t = 0; t < C; ++t) v[t] = 0.f;
-#pragma unroll 1
+#pragma unroll(kState && GR == 1 ? 2 : 1)
     for (int p = g; p < parts; p += GR) {
         const float2 ml = __ldcg(state_ml<NT>(a, slot(p), X, r));
         const float4 *src = state_u<D, NT>(a, slot(p), X, r) + (col / 4) * BQ;
@@ -1060,6 +1066,7 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
             v[4 * t + 3] = fmaf(f, y[t].w, v[4 * t + 3]);
         }
     }
+    if (kState && GR > 1) earlier.ask_u(a, at, col);
     // groups 2 and 3 to 0 and 1, then 1 to 0 (through the buffer that it read itself)
 #pragma unroll
     for (int from = GR / 2; from > 0; --from) {
@@ -1078,16 +1085,16 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
         }
     }
     if (g > 0 || !mine) return;
-    if (kState) {
+    if constexpr (kState) {
         const int tk = c1.x + paged::div_g(a, row);
-        const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
         if (!paged::is_wanted(a, tk)) return;
-        const paged::Ending e = paged::ending(a, at, tk, M, sum);
-        paged::end_u<C>(e, at, col, v, sum);
-        if (e.written) {
+        if (a.state.mode == paged::kWritten) {
+            const paged::Ending e = paged::ending(a, at, tk, M, sum);
+            paged::end_u<C>(e, at, col, v, sum);
             if (col == 0) paged::write_ml(e, at, M, sum);
             return;
         }
+        earlier.merge(v, M, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
     const float inv = empty ? 0.f : 1.f / sum;
@@ -1104,45 +1111,49 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     if (a.lse && col == 0) a.lse[t0 * a.Hq + h] = empty ? -INFINITY : (M + log2f(sum)) * kLn2;
 }
 
-// Rows that the prefixes' attention has finished, 128 of a key head, and the own keys' states of them.
+// Rows that the prefixes' attention has finished, 128 of a key head, and the own keys' states of them: eight columns a
+// thread, GR groups of them a CTA.
 template <int D, int GR>
-__device__ __forceinline__ void merge_whole(const paged::Args &a, int block, int col) {
-    constexpr int C = merge_cols(GR) / GR;  // columns a thread
-    const int n = a.T * a.G, blocks = (n + BQ - 1) / BQ, hk = block / blocks, row = block % blocks * BQ + threadIdx.x % BQ;
+__device__ __forceinline__ void merge_whole(const paged::Args &a, int block) {
+    constexpr int C = 8, Z = D / C / GR;
+    const int n = a.T * a.G, blocks = (n + BQ - 1) / BQ, rows = block / Z, hk = rows / blocks, row = rows % blocks * BQ + threadIdx.x % BQ;
     if (hk >= a.Hkv || row >= n) return;
-    const int tok = paged::div_g(a, row), h = hk * a.G + row - tok * a.G, c0 = col + (threadIdx.x / BQ) * C;
-    if (!paged::has_state(a, tok) || !paged::is_wanted(a, tok)) return;
+    const int tok = paged::div_g(a, row), h = hk * a.G + row - tok * a.G, col = (block % Z * GR + threadIdx.x / BQ) * C;
+    if (!paged::is_wanted(a, tok)) return;
     const paged::StateAt at = paged::state_at(a, D, hk, row);
+    paged::Earlier<C> own;
+    own.ask_ml(a, at, tok, true);
+    if (!own.on) return;
+    own.ask_u(a, at, col);
+    const float4 *u = reinterpret_cast<const float4 *>(a.state.u2) + at.u + col / 4 * at.n;
     const float2 ml = __ldcg(a.state.ml2 + at.ml);
-    if (ml.y == paged::kCutRow) return;
-    float m = ml.x, sum = ml.y, v[C];
-    const float4 *u = reinterpret_cast<const float4 *>(a.state.u2) + at.u;
+    float m = ml.x, sum = ml.y, v[C];  // (of a cut row whatever lies there)
 #pragma unroll
-    for (int c = 0; c < C; c += 4) *reinterpret_cast<float4 *>(v + c) = __ldcg(u + (c0 + c) / 4 * at.n);
-    const paged::Ending e = paged::ending(a, at, tok, m, sum);
-    paged::end_u<C>(e, at, c0, v, sum);
+    for (int c = 0; c < C; c += 4) *reinterpret_cast<float4 *>(v + c) = __ldcg(u + c / 4 * at.n);
+    if (ml.y == paged::kCutRow) return;
+    own.merge(v, m, sum);
     const bool empty = sum == 0.f;
     const float inv = empty ? 0.f : 1.f / sum;
-    uint2 *o = reinterpret_cast<uint2 *>(a.o + tok * a.os0 + h * a.os1 + c0);
+    uint32_t pk[4];
 #pragma unroll
-    for (int c = 0; c < C; c += 4)
-        o[c / 4] = empty ? make_uint2(0u, 0u) : make_uint2(ptx::pack_bf16x2(v[c] * inv, v[c + 1] * inv), ptx::pack_bf16x2(v[c + 2] * inv, v[c + 3] * inv));
-    if (a.lse && c0 == 0) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+    for (int i = 0; i < 4; ++i) pk[i] = empty ? 0u : ptx::pack_bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+    *reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    if (a.lse && col == 0) a.lse[(long long)tok * a.Hq + h] = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // Blocks from `items` on take rows that were finished.
 template <int D, int NT, int GR, bool kState>
-__global__ void __launch_bounds__(BQ *GR, GR == 1 ? 8 : 2) paged_tc_merge_kernel(const paged::Args a, int shares, int items) {
+__global__ void __launch_bounds__(BQ *GR, GR > 1 ? 2 : kState ? 4 : 8) paged_tc_merge_kernel(const paged::Args a, int shares, int items) {
     static_assert(GR == 1 || GR == 4, "the sums of merge_item");
     constexpr int S = merge_shares(GR);
-    __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR) + 1];
-    const int X = blockIdx.y, col = blockIdx.z * merge_cols(GR);
+    __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR, kState) + 1];
+    const int X = blockIdx.y, col = blockIdx.z * merge_cols(GR, kState);
     // (a call that merges states begins under this one: what it reads of them it waits for)
     if (kState) ptx::launch_dependents();
     ptx::grid_dep_wait();
     if (!kState) ptx::launch_dependents();
     if (kState && (int)blockIdx.x >= items) {
-        merge_whole<D, GR>(a, ((int)blockIdx.x - items) * NT + X, col);
+        merge_whole<D, GR>(a, (((int)blockIdx.x - items) * NT + X) * (int)gridDim.z + (int)blockIdx.z);
         return;
     }
     // a record a lane: one look at all
@@ -1182,12 +1193,16 @@ attn_status_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtenso
                              : launch<D, 1, kQ8 && D == 128 ? 64 : 128, kQ8>(mq, mk, mv, a, grid, st);
 }
 
+template <int D, int NT, int GR, bool kState>
+cudaError_t launch_merge(const paged::Args &a, int grid, cudaStream_t st) {
+    constexpr int Z = D / merge_cols(GR, kState);
+    const int items = a.marks ? (grid + merge_shares(GR) - 1) / merge_shares(GR) : 0;
+    const int whole = a.state.ml2 ? (a.Hkv * ((a.T * a.G + BQ - 1) / BQ) * (D / 8 / GR) + NT * Z - 1) / (NT * Z) : 0;
+    return launch_pdl(paged_tc_merge_kernel<D, NT, GR, kState>, dim3(items + whole, NT, Z), dim3(GR * BQ), 0, st, a, grid, items);
+}
 template <int D, int NT, int GR>
 cudaError_t launch_merge(const paged::Args &a, int grid, cudaStream_t st) {
-    auto kern = a.state.mode != paged::kNone ? paged_tc_merge_kernel<D, NT, GR, true> : paged_tc_merge_kernel<D, NT, GR, false>;
-    const int items = (grid + merge_shares(GR) - 1) / merge_shares(GR);
-    const int whole = a.state.ml2 ? (a.Hkv * ((a.T * a.G + BQ - 1) / BQ) + NT - 1) / NT : 0;
-    return launch_pdl(kern, dim3(items + whole, NT, D / merge_cols(GR)), dim3(GR * BQ), 0, st, a, grid, items);
+    return a.state.mode != paged::kNone ? launch_merge<D, NT, GR, true>(a, grid, st) : launch_merge<D, NT, GR, false>(a, grid, st);
 }
 template <int D, int NT>
 cudaError_t launch_merge(const paged::Args &a, int grid, bool many, cudaStream_t st) {
@@ -1208,8 +1223,9 @@ attn_status_t launch_paged_tc(const CUtensorMap &mq, const CUtensorMap &mk, cons
 attn_status_t launch_paged_tc_merge(const paged::Args &a, int d, int tiles, int grid, cudaStream_t st) {
     // Items cut into more than four parts or so (16 tokens of 4 query heads over a key head, d 128, 131072
     // keys in all): 8 items 47 us with one thread a row, 27 with four; 32 items 25.8 and 23.2; 64 items
-    // 24.9 and 25.7; the 77 us of a ragged batch of chunks become 82.
-    const bool many = (double)a.Hkv * ((a.T * a.G + a.R - 1) / a.R + a.B - 1) * 4. < (double)grid;
+    // 24.9 and 25.7; the 77 us of a ragged batch of chunks become 82.  With the own keys' states, which one thread a row
+    // asks for ahead, from 16 parts on: 64 sequences behind 8192 keys, eight items in five parts each 52 and 56 us.
+    const bool many = (double)a.Hkv * ((a.T * a.G + a.R - 1) / a.R + a.B - 1) * (a.state.ml2 ? 16. : 4.) < (double)grid;
     const cudaError_t e = d == 64 ? (tiles == 2 ? launch_merge<64, 2>(a, grid, many, st) : launch_merge<64, 1>(a, grid, many, st))
                                   : (tiles == 2 ? launch_merge<128, 2>(a, grid, many, st) : launch_merge<128, 1>(a, grid, many, st));
     return e == cudaSuccess ? ATTN_OK : fail(ATTN_ERR_CUDA, "paged_tc merge launch: %s", cudaGetErrorString(e));
