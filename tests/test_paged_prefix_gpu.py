@@ -269,6 +269,28 @@ def test_decode_steps_behind_prefixes(case, q8):
         assert torch.equal(o.view(torch.int16), want[0].view(torch.int16)) and torch.equal(lse.view(torch.int32), want[1].view(torch.int32))
 
 
+SHORT = [  # prefixes too short to be cut; more sequences than a warp looks at at once, and than 32 times as many
+    ([1] * 24, [10 + 30 * i for i in range(24)], [600], [0, 24], 8, 2, 128, 16),
+    ([1] * 40, [0, 3] * 20, [128, 0, 513], [2, 20, 21, 40], 16, 4, 64, 64),
+    ([1, 0, 2] * 400, [7 * i % 50 for i in range(1200)], [13 * i % 600 for i in range(50)], [24 * i for i in range(51)], 4, 1, 64, 16),
+    ([1] * 1100, [i % 40 for i in range(1100)], [3000, 5, 640], [0, 500, 520, 1090], 2, 1, 64, 16),
+]
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("case", SHORT)
+def test_short_prefixes_and_many_sequences(case, q8):
+    new, lens, plens, cuts, Hq, Hkv, d, page = case
+    s, groups = inputs(new, lens, plens, cuts, Hq, Hkv, d, page, q8, seed=6)
+    ofa.device_error_flags()
+    for fill in (255, 191):
+        n = ofa.paged_prefix_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["pt"], s["plens"], s["cu"], s["pcu"],
+                                                 max(new), k_scales=s.get("ks"), v_scales=s.get("vs"))
+        o, lse = run(s, max_q=max(new), workspace=torch.full((n,), fill, dtype=torch.uint8, device=DEV))
+        assert ofa.device_error_flags() == 0
+    check_attention(o, lse, s, new, lens, True, 1 / math.sqrt(d), groups, plens)
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_decode_steps_captured_one_after_the_other(q8):
     """Steps of two batches in one graph over one workspace, replayed with other lengths in the same tensors."""
