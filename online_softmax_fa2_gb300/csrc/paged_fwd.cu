@@ -244,10 +244,10 @@ double line_of(const attn_paged_fwd_params_t &p, const Plan &pl) {
 }
 
 // SMs for the prefixes' attention, so that both end together.  On x of them it takes 4 + t W / x us beside its ends, the own
-// keys' on the others s U / CTAs, W and U their lines; t and s are what sweeps of x came to.  (20 kinds of batches,
+// keys' on the others s U / CTAs, W and U their lines; t and s are what sweeps of x came to.  (22 kinds of batches,
 // 32 to 256 sequences with up to 64 to 4096 keys of their own behind 1 to 4 prefixes of 512 to 32768, 4 or 8 key heads, both
-// types of cache: x so chosen is within 4% of the best x but for four, within 9%.  With ten tiles a CTA, or six of codes,
-// whatever the own keys, the same took up to 30% more: 256 sequences with up to 512 keys behind 4096 105 us, so 81.)
+// types of cache: x so chosen takes at most 5% longer than the best x.  With ten tiles a CTA, or six of codes, whatever the
+// own keys, the same took up to 60% more: 256 sequences with up to 512 keys behind 4096 105 us, so 81.)
 // Where x comes near a multiple of the blocks it is made one, which cuts all of them alike, or none.
 int prefix_sms(const PrefixPlan &r, const attn_paged_fwd_params_t &over, const attn_paged_fwd_params_t &own, bool q8) {
     const int sms = sm_count() ? sm_count() : 152, most = sms - 8;
