@@ -578,7 +578,7 @@ attn_status_t attn_paged_fwd(const attn_paged_fwd_params_t *params, void *worksp
  * A row (the d elements of one key head, key or value, of one token) is held as d codes of e4m3 (one
  * byte each: sign, 4 bits of exponent, 3 of mantissa, largest 448, no infinity) and one scale byte e: its
  * elements are code * 2^(e - 127).  A power of two costs a floating format nothing (an element is
- * off by half a step, 2^-4 of itself, wherever the row's largest lies, down to 2^-14 of that) and is exact in every product.
+ * off by half a step, 2^-4 of itself, wherever the row's largest lies, down to 2^-13 of that) and is exact in every product.
  *
  *   k_pages, v_pages  of attn_paged_cache_t: e4m3 codes, strides in elements, which are bytes
  *   k, v              scale bytes [num_pages, Hkv, page_size], strides in bytes (page, head), the
@@ -688,7 +688,7 @@ size_t attn_paged_prefix_fwd_workspace_bytes(const attn_paged_prefix_params_t *p
  * NaN and tokens of no sequence; no token has to belong to a prefix.  (A row that the causal rule lets see no own key, as it lies
  * before them all, sees its whole prefix.)  How the GPU is shared out between the prefixes and the own keys goes by the
  * tables' widths: tables no wider than their longest entry (a view will do) are fastest.
- * Supported: as attn_paged_fwd, or attn_paged_fwd_q8; 1 <= P <= 65535.  Queues two to four kernels.
+ * Supported: as attn_paged_fwd, or attn_paged_fwd_q8; 1 <= P <= 65535.  Queues two or three kernels.
  */
 attn_status_t attn_paged_prefix_fwd(const attn_paged_prefix_params_t *params, void *workspace, size_t workspace_bytes,
                                     attn_stream_t stream);

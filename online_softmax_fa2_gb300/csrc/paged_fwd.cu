@@ -225,7 +225,9 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 // Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, runs on the
 // SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
 // their own, 32/8 heads of 128: 52 us; one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
-// every SM busy by themselves: one after the other, the second beginning as SMs come free.
+// every SM busy by themselves: one after the other, the second beginning as SMs come free.  No merge lies between, which every
+// CTA of the second would begin after: it joins the parts of cut rows itself (8 chunks to 512 tokens behind 4096 keys, 28/4
+// heads, 143 us, 148 with one; 16 tokens each of 64 sequences behind 2048 91 and 96; 2 chunks of 2048 behind 8192 450 and 447).
 struct PrefixPlan {
     Plan over, own;
     bool beside;
@@ -323,11 +325,20 @@ attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *wor
         s.ml2 = reinterpret_cast<float2 *>(ws + pl.off_ml2);
         s.u2 = reinterpret_cast<float *>(ws + pl.off_u2);
     }
-    s.marks = pl.beside;
+    // (rows that a call of few rows cuts are merged as it ends)
+    const bool joined = pl.over.tc && !pl.beside;  // cut rows, by the own keys' attention
+    s.marks = pl.beside || joined;
     Args merge;
-    attn_status_t r = launch(over_prefixes(p), scales, pl.over, s, ws + pl.off_over, st, pl.beside ? &merge : nullptr);
+    attn_status_t r = launch(over_prefixes(p), scales, pl.over, s, ws + pl.off_over, st, s.marks ? &merge : nullptr);
     if (r) return r;
     s.mode = pl.beside ? kLeft : kMerged;
+    s.marks = false;
+    if (joined) {
+        s.part_ml = merge.ml;
+        s.part_u = merge.u;
+        s.shares = pl.over.grid;
+        s.tiles = pl.over.tc;
+    }
     r = launch(p.fwd, scales, pl.own, s, ws + pl.off_own, st);
     if (r || !pl.beside) return r;
     merge.o = static_cast<__nv_bfloat16 *>(p.fwd.o);

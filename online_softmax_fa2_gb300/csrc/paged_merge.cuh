@@ -154,7 +154,7 @@ __device__ __forceinline__ void end_row(const Args &a, int q0, int hk, int row, 
     if (kState) {
         const StateAt at = state_at(a, D, hk, (long long)q0 * a.G + row);
         const Ending e = ending(a, at, tok, m, sum);
-        end_u<C>(e, at, C * lane, v, sum);
+        end_u<C>(a, e, at, C * lane, v, sum);
         if (e.written) {
             if (lane == 0) write_ml(e, at, m, sum);
             return;

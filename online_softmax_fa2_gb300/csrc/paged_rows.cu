@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D>::kBlocks)
 #pragma unroll
                     for (int nt = 0; nt < DW / 8; ++nt) {
                         float v[2] = {o[nt][2 * e], o[nt][2 * e + 1]};
-                        end_u<2>(end, at, warp * DW + 2 * t + 8 * nt, v, sum);
+                        end_u<2>(a, end, at, warp * DW + 2 * t + 8 * nt, v, sum);
                         o[nt][2 * e] = v[0];
                         o[nt][2 * e + 1] = v[1];
                     }

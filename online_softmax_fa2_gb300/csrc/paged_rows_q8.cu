@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                     v[2] = o[2 * gi][2 * e + 1] * vu;
                     v[3] = o[2 * gi + 1][2 * e + 1] * vu;
                 }
-                if (whole) end_u<C>(end, at, col, v, sum);
+                if (whole) end_u<C>(a, end, at, col, v, sum);
                 if (whole && end.written) continue;
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {

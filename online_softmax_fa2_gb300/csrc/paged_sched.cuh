@@ -38,6 +38,9 @@ constexpr uint64_t kWaitLimitNs = 1000000000ull;  // every mbarrier wait gives u
 // and u2 (kLeft; rows of tokens without a prefix are finished), and the prefixes' merge, which comes last, merges both
 // (kMerged, the own states as ml and u): of the items that it merges, and of the rows that the prefixes' attention has
 // finished, whose states are its ml2 and u2 (other rows hold kCutRow as l there).
+//
+// Where tiles take both, one after the other, no merge lies between: of a row that the prefixes' attention has cut, ml holds
+// kCutRow as l and, as m, which parts it is in (cut_row of paged_state.cuh); the own keys' attention joins them.
 struct State {
     int mode;      // kNone, kWritten, kMerged, kLeft
     int P;         // (merged, left) tokens cu[0] .. cu[P] - 1 have one; cu null: all
@@ -46,6 +49,8 @@ struct State {
     float2 *ml, *ml2;
     float *u, *u2;
     bool marks;    // (written) cut rows are marked
+    const float *part_ml, *part_u;  // (merged) the parts of cut rows, of `shares` shares and `tiles` row tiles an item
+    int shares, tiles;
 };
 constexpr int kNone = 0, kWritten = 1, kMerged = 2, kLeft = 3;
 constexpr float kCutRow = -1.f;

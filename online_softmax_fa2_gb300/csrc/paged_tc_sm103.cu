@@ -262,8 +262,8 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
     const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
     const int h = hk * a.G + g;
     paged::wait_for_states(a);
-    paged::Ending e{1.f, 0.f, false, false, nullptr, nullptr};
-    if (on) e = paged::ending(a, at, tok, m, sum);
+    paged::Ending e{1.f, 0.f, false, false, nullptr, nullptr, false};
+    if (on) e = paged::ending<true>(a, at, tok, m, sum);
     const bool empty = sum == 0.f;  // a NaN is no empty row
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
@@ -275,7 +275,7 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
         float v[32];
 #pragma unroll
         for (int t = 0; t < 32; ++t) v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
-        if (on) paged::end_u<32>(e, at, cc * 32, v, sum);
+        if (on) paged::end_u<32, D>(a, e, at, cc * 32, v, sum);
         if (on && !e.written) {
             uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 32);
 #pragma unroll
@@ -299,13 +299,13 @@ __device__ __forceinline__ void end_empty_row(const paged::Args &a, int tok, int
     const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
     const int h = hk * a.G + g;
     paged::wait_for_states(a);
-    const paged::Ending e = paged::ending(a, at, tok, m, sum);
+    const paged::Ending e = paged::ending<true>(a, at, tok, m, sum);
     const bool empty = sum == 0.f;
     const float inv = empty ? 0.f : 1.f / sum;
 #pragma unroll 1
     for (int c = 0; c < D; c += 8) {
         float v[8] = {};
-        paged::end_u<8>(e, at, c, v, sum);
+        paged::end_u<8, D>(a, e, at, c, v, sum);
         if (e.written) continue;
         uint32_t pk[4];
 #pragma unroll
@@ -932,7 +932,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                 if (++vs == VS) { vs = 0; vph ^= 1; }
             // where this row goes, before the walk moves on
             const bool whole = w.j0 == 0 && w.j1 >= tx;
-            const int c0 = w.first_share(a);
+            const int c0 = w.first_share(a), parts = kState ? w.parts(a, c0, tx) : 0;
             const bool first = w.j0 == 0;
             __nv_bfloat16 *orow = nullptr;
             float *lrow = nullptr;
@@ -972,7 +972,8 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             }
             // the state of this part, for paged_tc_merge_kernel
             if (kState && a.state.marks && first && mine)
-                a.state.ml[paged::state_at(a, D, hk, (long long)to_tok * a.G + to_g).ml] = make_float2(0.f, paged::kCutRow);
+                a.state.ml[paged::state_at(a, D, hk, (long long)to_tok * a.G + to_g).ml] =
+                    make_float2(paged::cut_row(c0, X, r, parts), paged::kCutRow);
             const int slot = paged::state_slot(blockIdx.x, c0);
             *state_ml<NT>(a, slot, X, r) = make_float2(l_run == 0.f ? -INFINITY : m_run, l_run);
             float4 *u4 = state_u<D, NT>(a, slot, X, r);
@@ -1033,7 +1034,7 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     auto slot = [&](int p) { return paged::state_slot(c + p, c); };
     float M = -INFINITY, sum = 0.f, v[C];
     const paged::StateAt at = paged::state_at(a, D, c1.y, (long long)c1.x * a.G + row);
-    paged::Earlier<kState ? C : 4> earlier;  // under the parts, as far as registers go
+    paged::Earlier<kState ? C : 4, D> earlier;  // under the parts, as far as registers go
     if (kState) {
         earlier.ask_ml(a, at, c1.x + paged::div_g(a, row), mine && g == 0);
         if (GR == 1) earlier.ask_u(a, at, col);
@@ -1086,14 +1087,8 @@ __device__ __forceinline__ void merge_item(const paged::Args &a, int c, int X, i
     }
     if (g > 0 || !mine) return;
     if constexpr (kState) {
-        const int tk = c1.x + paged::div_g(a, row);
-        if (!paged::is_wanted(a, tk)) return;
-        if (a.state.mode == paged::kWritten) {
-            const paged::Ending e = paged::ending(a, at, tk, M, sum);
-            paged::end_u<C>(e, at, col, v, sum);
-            if (col == 0) paged::write_ml(e, at, M, sum);
-            return;
-        }
+        if (!paged::is_wanted(a, c1.x + paged::div_g(a, row))) return;
+        earlier.join_parts(a, col);
         earlier.merge(v, M, sum);
     }
     const bool empty = sum == 0.f;  // (a part whose sum is NaN makes it NaN, whatever its weight)
@@ -1148,10 +1143,8 @@ __global__ void __launch_bounds__(BQ *GR, GR > 1 ? 2 : kState ? 4 : 8) paged_tc_
     constexpr int S = merge_shares(GR);
     __shared__ float top[GR][BQ], part[GR == 1 ? 1 : 2][GR == 1 ? 1 : BQ][merge_cols(GR, kState) + 1];
     const int X = blockIdx.y, col = blockIdx.z * merge_cols(GR, kState);
-    // (a call that merges states begins under this one: what it reads of them it waits for)
-    if (kState) ptx::launch_dependents();
     ptx::grid_dep_wait();
-    if (!kState) ptx::launch_dependents();
+    ptx::launch_dependents();
     if (kState && (int)blockIdx.x >= items) {
         merge_whole<D, GR>(a, (((int)blockIdx.x - items) * NT + X) * (int)gridDim.z + (int)blockIdx.z);
         return;

@@ -166,6 +166,25 @@ def test_malformed_cuts_fault_nothing(cu):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+def test_malformed_cuts_after_others_in_one_workspace(q8):
+    """Rows that no prefix's attention has reached find what an earlier call left there, entries of cut rows among it."""
+    new, lens, plens, cuts = [300, 200, 150], [300, 400, 900], [5000, 3000], [0, 420, 650]
+    s, groups = inputs(new, lens, plens, cuts, 8, 2, 64, 16, q8, seed=8)
+    n = ofa.paged_prefix_fwd_workspace_bytes(s["q"], s["kp"], s["vp"], s["bt"], s["lens"], s["pt"], s["plens"], s["cu"], s["pcu"], 300,
+                                             k_scales=s.get("ks"), v_scales=s.get("vs"))
+    ws = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    ofa.device_error_flags()
+    for bad in ([0, 700, 650], [0, 0, 650], [400, 100, 650], [-9, 90, 20]):
+        s["pcu"] = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+        o, lse = run(s, max_q=300, workspace=ws)
+        assert ofa.device_error_flags() == 0
+        check_attention(o, lse, s, new, lens, True, 1 / 8, groups, plens, what=str(bad))
+        s["pcu"] = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        run(s, max_q=300, workspace=ws)
+        assert (ofa.device_error_flags() != 0) == (bad != [0, 0, 650])
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_a_serving_run(q8):
     """A prompt appended once, eight answers that go on from it in pages of their own, step by step: what each step
     gives is the attention over the prompt and the answer, and equals attn_paged_fwd's over one table of both within
