@@ -250,6 +250,7 @@ double line_of(const attn_paged_fwd_params_t &p, const Plan &pl) {
 // 32 to 256 sequences with up to 64 to 4096 keys of their own behind 1 to 4 prefixes of 512 to 32768, 4 or 8 key heads, both
 // types of cache: x so chosen takes at most 5% longer than the best x.  With ten tiles a CTA, or six of codes, whatever the
 // own keys, the same took up to 60% more: 256 sequences with up to 512 keys behind 4096 105 us, so 81.)
+// (The bounds on x are for tables wider than their entries, whose lines say too much.)
 // Where x comes near a multiple of the blocks it is made one, which cuts all of them alike, or none.
 int prefix_sms(const PrefixPlan &r, const attn_paged_fwd_params_t &over, const attn_paged_fwd_params_t &own, bool q8) {
     const int sms = sm_count() ? sm_count() : 152, most = sms - 8;
@@ -257,7 +258,7 @@ int prefix_sms(const PrefixPlan &r, const attn_paged_fwd_params_t &over, const a
     int best = most;
     double least = 1e30;
     for (int x = 1; x <= most; ++x) {
-        if (W > 40. * x || (x > 1 && W < 4. * x)) continue;  // tiles a CTA
+        if ((W > 40. * x && 4 * x < sms) || (x > 1 && W < 4. * x)) continue;  // 4 to 40 tiles a CTA, or a quarter of the SMs
         const double a = 4. + t * W / x, b = s * U / ((sms - x) * rows_blocks(own.cache.d)), longer = a > b ? a : b;
         if (longer < least) {
             least = longer;
