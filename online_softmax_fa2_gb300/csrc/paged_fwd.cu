@@ -277,8 +277,13 @@ PrefixPlan make_prefix_plan(const attn_paged_prefix_params_t &p) {
     r.own = make_plan(p.fwd, q8);
     r.over = make_plan(over, q8);
     r.beside = r.over.tc && !r.own.tc;
-    if (r.beside) {
-        const int sms = sm_count() ? sm_count() : 152;
+    const int sms = sm_count() ? sm_count() : 152;
+    // A long prefix of codes takes every SM first, and the own keys' attention begins as they come free: beside it, the copies
+    // of the next tile, the only ones in flight, wait for memory.  256 sequences with up to 1024 keys behind 32768, 32/8
+    // heads of 128, 204 us so, 298 side by side, 128 with up to 2048 behind 16384 127 and 140; 64 with up to 1024 behind
+    // 32768, where the bound is, 87 and 86, behind 8192 64 and 52.
+    const bool first = q8 && line_of(over, r.over) * (double)p.fwd.cache.d > 13. * 128. * sms;
+    if (r.beside && !first) {
         const int x = prefix_sms(r, over, p.fwd, q8);
         r.over = make_plan(over, q8, x * (3 - r.over.tc));
         r.own = make_plan(p.fwd, q8, (sms - x) * rows_blocks(p.fwd.cache.d));

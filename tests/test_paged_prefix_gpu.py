@@ -292,6 +292,7 @@ SHORT = [  # prefixes too short to be cut; more sequences than a warp looks at a
     ([1] * 24, [10 + 30 * i for i in range(24)], [600], [0, 24], 8, 2, 128, 16),
     ([1] * 40, [0, 3] * 20, [128, 0, 513], [2, 20, 21, 40], 16, 4, 64, 64),
     ([1, 0, 2] * 400, [7 * i % 50 for i in range(1200)], [13 * i % 600 for i in range(50)], [24 * i for i in range(51)], 4, 1, 64, 16),
+    ([1] * 20, [5 + 40 * i for i in range(20)], [4000], [0, 20], 64, 64, 128, 64),   # and long prefixes of many heads
     ([1] * 1100, [i % 40 for i in range(1100)], [3000, 5, 640], [0, 500, 520, 1090], 2, 1, 64, 16),
 ]
 
