@@ -69,7 +69,8 @@ inline uint32_t dropout_p8(float p) {
 // Launches kern as a programmatic dependent of the previous kernel in the stream: its CTAs
 // may be scheduled once every CTA of that kernel has executed griddepcontrol.launch_dependents
 // (or exited), so its launch and set-up overlap that kernel's tail.  A kernel launched this
-// way executes griddepcontrol.wait before it reads or writes global memory.
+// way executes griddepcontrol.wait before it reads or writes global memory; the second attention behind
+// shared prefixes alone begins by a tag that the grid before it releases after its own wait (paged_state.cuh).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                               Args &&...args) {

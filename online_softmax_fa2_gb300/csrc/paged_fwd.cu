@@ -231,7 +231,7 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 struct PrefixPlan {
     Plan over, own;
     bool beside;
-    size_t off_u, off_ml2, off_u2, off_over, off_own, bytes;
+    size_t off_begun, off_u, off_ml2, off_u2, off_over, off_own, bytes;
 };
 
 // Blocks of an attention, and the line that they make, as far as the host knows them: of the mean's rows, over all the
@@ -290,7 +290,8 @@ PrefixPlan make_prefix_plan(const attn_paged_prefix_params_t &p) {
     }
     const size_t rows = (size_t)p.fwd.cache.T * p.fwd.Hq, ml = round_up(rows * 2 * sizeof(float)),
                  u = round_up(rows * p.fwd.cache.d * sizeof(float));
-    r.off_u = ml;
+    r.off_begun = ml;
+    r.off_u = r.off_begun + round_up(sizeof(unsigned long long));
     r.off_ml2 = r.off_u + u;
     r.off_u2 = r.off_ml2 + (r.beside ? ml : 0);
     r.off_over = r.off_u2 + (r.beside ? u : 0);
@@ -327,6 +328,8 @@ attn_status_t launch_paged_prefix(const attn_paged_prefix_params_t &p, void *wor
     s.cu = p.cu_prefix;
     s.ml = reinterpret_cast<float2 *>(ws);
     s.u = reinterpret_cast<float *>(ws + pl.off_u);
+    s.begun = reinterpret_cast<unsigned long long *>(ws + pl.off_begun);
+    s.tag = next_tag();
     if (pl.beside) {
         s.ml2 = reinterpret_cast<float2 *>(ws + pl.off_ml2);
         s.u2 = reinterpret_cast<float *>(ws + pl.off_u2);

@@ -49,6 +49,7 @@ struct State {
     float2 *ml, *ml2;
     float *u, *u2;
     bool marks;    // (written) cut rows are marked
+    unsigned long long *begun, tag;  // the call's tag, once what the call reads is there (begin_after_earlier_grids)
     const float *part_ml, *part_u;  // (merged) the parts of cut rows, of `shares` shares and `tiles` row tiles an item
     int shares, tiles;
 };

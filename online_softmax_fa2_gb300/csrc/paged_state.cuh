@@ -197,18 +197,30 @@ __device__ __forceinline__ bool is_wanted(const Args &a, int tok) {
     return tok >= __ldg(a.state.only) && tok < __ldg(a.state.only + a.state.B);
 }
 
-// A kernel that merges states reads what the grids before it write at its very end, and begins while those still run: it
-// waits for them where it needs them, in every CTA.  One that leaves its states needs nothing of them; its first CTA waits
-// at its end, since a grid behind this one takes this one's end for theirs.  Their workspaces are different ones.  What
-// else such a kernel reads was there before those grids began: they let it start after their own wait.
+// A kernel that merges states reads what the grid before it, the call's first, writes at its very end, and begins while that
+// still runs: it waits for it where it needs it, in every CTA.  One that leaves its states needs nothing of it; its first CTA
+// waits at its end, since a grid behind this one takes this one's end for that one's.  Their workspaces are different ones.
+//
+// What else such a kernel reads (lengths, tables, queries, pages) was written by grids before the call's first, whose end only
+// that one has waited for: a grid's wait covers the grid right before it.  So the first grid releases the call's tag
+// after its wait, and a thread here that acquires the tag has those writes in its past as the first grid has; one that finds
+// another value waits for the first grid's end.  Nobody spins.  The tag is taken away at this grid's end: a captured call finds
+// none at its next replay.  (64 sequences behind 8192 keys take as long as without.)
 __device__ __forceinline__ void begin_after_earlier_grids(const Args &a, bool state) {
-    if (!state || a.state.mode < kMerged) ptx::grid_dep_wait();
+    if (!state || a.state.mode < kMerged) {
+        ptx::grid_dep_wait();
+        if (state && a.state.mode == kWritten && blockIdx.x == 0 && threadIdx.x == 0) ptx::store_release(a.state.begun, a.state.tag);
+        return;
+    }
+    if (ptx::load_acquire(a.state.begun) != a.state.tag) ptx::grid_dep_wait();
+    ptx::fence_proxy_async_global();  // pages and queries come by TMA
 }
 __device__ __forceinline__ void wait_for_states(const Args &a) {
     if (a.state.mode == kMerged) ptx::grid_dep_wait();
 }
 __device__ __forceinline__ void end_after_earlier_grids(const Args &a) {
     if (a.state.mode == kMerged || (a.state.mode == kLeft && blockIdx.x == 0)) ptx::grid_dep_wait();
+    if (a.state.mode >= kMerged && blockIdx.x == 0 && threadIdx.x == 0) *a.state.begun = 0;
 }
 
 }  // namespace paged
