@@ -184,7 +184,7 @@ struct Earlier {
         if (!on) return;
         const float M = fmaxf(m, s.x), ref = M == -INFINITY ? 0.f : M;
         const float own = sum == 0.f ? 0.f : ptx::ex2(m - ref), before = ptx::ex2(s.x - ref);
-        sum = fmaf(before, s.y, own == 0.f ? 0.f : own * sum);
+        sum = fmaf(before, s.y, sum == 0.f ? 0.f : own * sum);  // (a weight of 0 keeps a NaN)
         m = M;
 #pragma unroll
         for (int c = 0; c < C; ++c) v[c] = fmaf(before, y[c], own == 0.f ? 0.f : own * v[c]);
