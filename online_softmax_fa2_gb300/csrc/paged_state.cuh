@@ -87,6 +87,7 @@ struct Ending {
     bool cut;  // it is in parts
     CutRow parts;
     float m;   // its maximum
+    bool none; // the row has seen no key here (a weight of 0 is not none: it keeps a NaN)
 };
 __device__ __forceinline__ bool has_state(const Args &a, int tok) {
     if (!a.state.cu) return true;
@@ -113,9 +114,10 @@ __device__ __forceinline__ Ending ending(const Args &a, const StateAt &at, int t
         e.m = s.x;
     }
     const float M = fmaxf(m, s.x), ref = M == -INFINITY ? 0.f : M;
-    e.own = sum == 0.f ? 0.f : ptx::ex2(m - ref);
+    e.none = sum == 0.f;
+    e.own = e.none ? 0.f : ptx::ex2(m - ref);
     e.before = ptx::ex2(s.x - ref);
-    sum = fmaf(e.before, s.y, sum == 0.f ? 0.f : e.own * sum);
+    sum = fmaf(e.before, s.y, e.none ? 0.f : e.own * sum);
     m = M;
     return e;
 }
@@ -149,7 +151,7 @@ __device__ __forceinline__ void end_u(const Args &a, const Ending &e, const Stat
         *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(u + col / 4 * at.n) + col / 2 % 2);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = fmaf(e.before, y[c], e.own == 0.f ? 0.f : e.own * v[c]);
+    for (int c = 0; c < C; ++c) v[c] = fmaf(e.before, y[c], e.none ? 0.f : e.own * v[c]);
 }
 
 // The earlier state of C columns of a row, asked for before it is needed: (m, l) first, then u.  D > 0: it may be in parts.
@@ -183,11 +185,12 @@ struct Earlier {
     __device__ __forceinline__ void merge(float (&v)[C], float &m, float &sum) const {
         if (!on) return;
         const float M = fmaxf(m, s.x), ref = M == -INFINITY ? 0.f : M;
-        const float own = sum == 0.f ? 0.f : ptx::ex2(m - ref), before = ptx::ex2(s.x - ref);
-        sum = fmaf(before, s.y, sum == 0.f ? 0.f : own * sum);  // (a weight of 0 keeps a NaN)
+        const bool none = sum == 0.f;  // (a weight of 0 is not none: it keeps a NaN)
+        const float own = none ? 0.f : ptx::ex2(m - ref), before = ptx::ex2(s.x - ref);
+        sum = fmaf(before, s.y, none ? 0.f : own * sum);
         m = M;
 #pragma unroll
-        for (int c = 0; c < C; ++c) v[c] = fmaf(before, y[c], own == 0.f ? 0.f : own * v[c]);
+        for (int c = 0; c < C; ++c) v[c] = fmaf(before, y[c], none ? 0.f : own * v[c]);
     }
 };
 

@@ -1,4 +1,4 @@
-"""NaN behind shared prefixes: what one of the two attentions makes NaN stays NaN whatever the other one's
+"""NaN and infinities behind shared prefixes: what one of the two attentions makes NaN stays NaN whatever the other one's
 weight, on every path that joins two states (rows finished and cut, side by side and one after the other)."""
 import math
 
@@ -75,12 +75,12 @@ def test_a_nan_query(path, q8):
     check_nan(run(s, max_q=max(new)), want, hit)
 
 
-@pytest.mark.parametrize("nan_in", ["k"])
+@pytest.mark.parametrize("nan_in", ["k", "v"])
 @pytest.mark.parametrize("heavy", ["own", "prefix"])
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("path", PATHS)
 def test_a_nan_in_the_lighter_part(path, q8, heavy, nan_in):
-    """One NaN key among those of the part whose weight beside the other's is 0 in fp32 (logits 512 apart)."""
+    """One NaN key, or value, among those of the part whose weight beside the other's is 0 in fp32 (logits 512 apart)."""
     s, groups, seq = make(path, q8)
     mq = max(path[0])
     s["q"] = torch.ones_like(s["q"])  # a logit is the sum of a key's elements, times the scale
@@ -99,4 +99,8 @@ def test_a_nan_in_the_lighter_part(path, q8, heavy, nan_in):
     set_key(s, nan_in, table, [at], 0, math.nan)
     hit = where[:, None] & (torch.arange(16, device=DEV) < 8)
     got = run(s, max_q=mq, scale=scale)
-    check_nan(got, want, hit)
+    if nan_in == "k":
+        check_nan(got, want, hit)
+    else:  # lse knows nothing of values
+        assert torch.equal(got[0].isnan().all(-1), hit) and torch.equal(got[0].isnan().any(-1), hit) and torch.equal(got[1], want[1])
+        assert torch.equal(got[0][~hit], want[0][~hit])
