@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                     for (int i = 0; i < 2; ++i) {
                         const float p0 = ptx::ex2(s[nt][at_of(e, i)] - ref);
                         l[e] += p0;
-                        w[at_of(e, i)] = p0 == 0.f ? 0.f : p0 * sc[i];  // (a hidden key's scale may be anything)
+                        w[at_of(e, i)] = s[nt][at_of(e, i)] == -INFINITY ? 0.f : p0 * sc[i];  // (a hidden key's scale may be anything)
                     }
                 }
                 pk[nt][0] = q8::pack_f16(w[0], w[1]);
