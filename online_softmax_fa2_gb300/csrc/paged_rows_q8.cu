@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = s[nt][at_of(e, i)] * un[e] * sc[i];
+                        float x = s[nt][at_of(e, i)] * q8::finite(un[e] * sc[i]);
                         if (edge && kv0 + key_of(nt, i) >= lim[e]) x = -INFINITY;
                         s[nt][at_of(e, i)] = x;
                         mx[e] = fmaxf(mx[e], x);

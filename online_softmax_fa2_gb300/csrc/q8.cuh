@@ -12,6 +12,13 @@ __device__ __forceinline__ float pow2(uint32_t e) {
     return __uint_as_float((e << 23) | (((e + 1) & 0xffu) <= 1u ? 0x400000u : 0u));
 }
 
+// A factor of logits, at most the largest float (0 times it is 0); a NaN stays one.  A query row's power of two and a key's
+// meet before the sum of their products does: either alone may take it out of fp32, with logits of ordinary size.
+__device__ __forceinline__ float finite(float x) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(3.402823466e38f));
+    return x;
+}
+
 // The scale byte of a row whose largest finite magnitude is m: the least e >= 0 with m <= 448 * 2^(e - 127).
 // With m = 1.f * 2^(x - 127) and 448 = 1.75 * 2^8 that is x - 8, one more where 1.f > 1.75.
 __device__ __forceinline__ uint32_t scale_byte(float m) {

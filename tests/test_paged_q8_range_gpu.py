@@ -64,3 +64,16 @@ def test_a_nan_value_of_no_weight(shape):
         set_bytes(s, "v", b, [5], torch.full((1, Hkv), 255))
     o, lse = run(s, scale=1.0, max_q=max(new))
     assert bool(o.isnan().all()) and bool(lse.isfinite().all()) and bool(want[0].isfinite().all())
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_queries_near_the_largest_over_the_smallest_keys(shape):
+    """Elements of 2^126 against rows of scale byte 0 and up: logits of ordinary size, whose parts do not fit fp32."""
+    new, lens, Hq, Hkv, d = shape
+    s = q8_inputs(new, lens, Hq, Hkv, d, 16, seed=38)
+    g = torch.Generator().manual_seed(5)
+    s["q"] = (torch.randn(s["q"].shape, generator=g).clamp(-2, 2).double() * 2.0 ** 126).bfloat16().to(DEV)
+    for b, n in enumerate(lens):
+        set_codes(s, "k", b, torch.arange(n), torch.randn(n, d, generator=g))
+        set_bytes(s, "k", b, torch.arange(n), torch.randint(0, 4, (n, Hkv), generator=g))
+    go(s, new, lens, 0.125)
