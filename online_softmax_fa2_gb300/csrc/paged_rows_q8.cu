@@ -9,9 +9,12 @@
 //   a query row is multiplied by a power of two that brings its largest finite element into [2^14, 2^15), and
 //   the row's logits by its inverse;
 //   a key's scale multiplies its logits, in fp32;
-//   a value's scale goes into its weights, as 2^(f_j - F) with F the largest f_j met: u is held in units of
-//   2^(F - 127), and rescaled when F grows as it is when the maximum does.  The weights, at most 1, are
-//   rounded to fp16 (half a step 2^-11 of a weight of 2^-14 or more, 2^-25 below).
+//   a value's scale goes into its weights, which are w_ij = 2^(x_ij log2 e - m_i + f_j - 127 - y_i + 14), with y_i a running
+//   maximum of its own of what a row's keys count with, weight times scale.  u is held relative to y and l to the maximum
+//   m of the logits; a key that the row does not see, or that weighs nothing in it, moves neither, whatever its value's scale.
+//   The weights, at most 2^14, are rounded to fp16: half a step 2^-11 of one of 2^-14 or more, 2^-25 below, so a key loses
+//   2^-39 at most of what the row's largest counts with.  (With a unit for all rows of a block, the largest
+//   scale met, a value 2^26 above the others took the outputs of rows that gave it no weight to 0.)
 // With 16 rows the rows are the products' 16 and the keys or dimensions their 8; with 8 rows or fewer (a decode step of up to 8
 // query heads a key head) it is the other way round, S and O transposed: half the products, and half the logits a thread.
 // Fragments come by ldmatrix from the codes as they lie, two codes an element, in an order of the
@@ -53,8 +56,8 @@ struct Rows {
     static constexpr int kScaleOff = kStages * 2 * kTile;
     static constexpr int kQOff = kScaleOff + kStages * 2 * KT;
     static constexpr int kPOff = kQOff + R * kQRow;
-    static constexpr int kRedOff = kPOff + R * kPRow;        // [4][R] maxima, [4][R] sums
-    static constexpr int kUnitOff = kRedOff + 2 * 4 * R * 4; // [R] a row's inverse power of two, times the scale
+    static constexpr int kRedOff = kPOff + R * kPRow;        // [4][R] maxima, [4][R] with scales, beside the first, [4][R] sums
+    static constexpr int kUnitOff = kRedOff + 3 * 4 * R * 4; // [R] a row's inverse power of two, times the scale
     static constexpr int kCtrlOff = kUnitOff + R * 4;
 };
 
@@ -72,6 +75,8 @@ constexpr int smem_bytes() {
 }
 
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+constexpr float kRoom = 14.f;  // log2 of the largest weight as fp16 has it
 
 // Where 16-byte chunk c of row r of a tile lies (TMA's swizzle of 128 or 64 bytes).
 template <int D>
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
     // ---------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3, mi = lane >> 3, mr = lane & 7;
     uint8_t *sP = smem + L::kPOff, *sQ = smem + L::kQOff;
-    float *sums = red + 4 * R;
+    float *red_y = red + 4 * R, *sums = red + 8 * R;
     int st = 0, ph = 0;
     // a block's queries, D / 8 neighbouring threads a row, 16 bytes each (rows past the block's end are zero)
     constexpr int QN = R * (D / 8), QC = (QN + kConsumers - 1) / kConsumers;  // (whole warps without a row, with 8 of 64)
@@ -251,16 +256,15 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
         const Walk p = w;
         const int rows = min(R, p.seq.nq * a.G - p.k * R), row0 = p.k * R;
         int lim[2];  // keys < lim are visible to this lane's rows
-        float m[2], l[2], o[kTurned ? NG : DW / 8][4];
+        float m[2], y[2], l[2], o[kTurned ? NG : DW / 8][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = row_of(e);
             lim[e] = (a.causal && r < rows) ? min(max(p.seq.n - p.seq.nq + div_g(a, row0 + r) + 1, 0), p.seq.n) : p.seq.n;
-            m[e] = -INFINITY;
+            m[e] = y[e] = -INFINITY;
             l[e] = 0.f;
         }
         const int lim0 = a.causal ? min(max(p.seq.n - p.seq.nq + div_g(a, row0) + 1, 0), p.seq.n) : p.seq.n;
-        uint32_t F = 0;  // u is in units of 2^(F - 127)
 #pragma unroll
         for (int nt = 0; nt < (kTurned ? NG : DW / 8); ++nt)
 #pragma unroll
@@ -324,14 +328,18 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                     b[1] = two >> 8;
                 }
             };
-            // scale, mask, row maxima of this warp's keys
+            // scale, mask, row maxima of this warp's keys, of the logits and with the values' scales (255 is a NaN, which
+            // becomes the weight, and which a maximum passes over)
             const bool edge = kv0 + KT > lim0;
-            float mx[2] = {-INFINITY, -INFINITY};
+            float mx[2] = {-INFINITY, -INFINITY}, my[2] = {-INFINITY, -INFINITY}, up[NS_][2];
 #pragma unroll
             for (int nt = 0; nt < NS_; ++nt) {
-                uint32_t b[2];
+                uint32_t b[2], f[2];
                 bytes_of(sKs, nt, b);
+                bytes_of(sVs, nt, f);
                 const float sc[2] = {q8::pow2(b[0]), q8::pow2(b[1])};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) up[nt][i] = f[i] == 255u ? NAN : (float)((int)f[i] - 127);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -342,26 +350,24 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                         mx[e] = fmaxf(mx[e], x);
                     }
             }
+            // (differences of logits first: beside a large one an exponent would be lost)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if constexpr (kTurned) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-                    if (g == 0) red[warp * R + row_of(e)] = mx[e];
-                } else {
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                    if (t == 0) red[warp * R + row_of(e)] = mx[e];
+                for (int nt = 0; nt < NS_; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) my[e] = fmaxf(my[e], (s[nt][at_of(e, i)] - mx[e]) + up[nt][i]);
+#pragma unroll
+                for (int d = kTurned ? 4 : 1; d < (kTurned ? 32 : 4); d <<= 1) {
+                    const float ox = __shfl_xor_sync(0xffffffffu, mx[e], d), oy = __shfl_xor_sync(0xffffffffu, my[e], d);
+                    const float big = fmaxf(mx[e], ox);
+                    my[e] = fmaxf(my[e] + (mx[e] - big), oy + (ox - big));
+                    mx[e] = big;
                 }
-            }
-            // the largest value scale of the tile's keys (255, a NaN, is none)
-            uint32_t big = 0;
-            {
-                uint32_t v4 = *reinterpret_cast<const uint32_t *>(sVs + 4 * lane);
-#pragma unroll
-                for (int i = 0; i < 4; ++i, v4 >>= 8)
-                    if (kv0 + 4 * lane + i < p.seq.n && (v4 & 255u) != 255u) big = max(big, v4 & 255u);
-                big = max(F, __reduce_max_sync(0xffffffffu, big));
+                if ((kTurned ? g : t) == 0) {
+                    red[warp * R + row_of(e)] = mx[e];
+                    red_y[warp * R + row_of(e)] = my[e];
+                }
             }
             // value rows past the sequence may hold anything: zero, so that 0 * v is 0
             const bool ragged = kv0 + KT > p.seq.n;
@@ -369,38 +375,37 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                 for (int i = threadIdx.x; i < KT * (D / 16); i += kConsumers)
                     if (kv0 + i / (D / 16) >= p.seq.n) *reinterpret_cast<uint4 *>(sV + i * 16) = make_uint4(0u, 0u, 0u, 0u);
             consumer_sync();
-            float al[2];
-            bool moved = big != F;
-            const float grow = moved ? q8::pow2(F + 127 > big ? F + 127 - big : 0) : 1.f;  // 2^(F - big)
-            F = big;
+            float al[2], ref[2], ref_y[2];  // al: of u
+            bool moved = false;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = row_of(e);
                 const float mn = fmaxf(fmaxf(m[e], fmaxf(red[r], red[R + r])), fmaxf(red[2 * R + r], red[3 * R + r]));
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                al[e] = ptx::ex2(m[e] - ref);
-                moved |= mn != m[e];
+                ref[e] = mn == -INFINITY ? 0.f : mn;
+                const float old = y[e] + (m[e] - ref[e]);
+                float yn = old;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) yn = fmaxf(yn, red_y[w * R + r] + (red[w * R + r] - ref[e]));
+                const float base = yn == -INFINITY ? 0.f : yn;
+                al[e] = ptx::ex2(old - base);
+                ref_y[e] = base - kRoom;
+                l[e] *= ptx::ex2(m[e] - ref[e]);
+                moved |= al[e] != 1.f;
                 m[e] = mn;
-                l[e] *= al[e];
+                y[e] = yn;
             }
             uint32_t pk[NS_][2];  // weights: two keys of row e, or (turned) two rows of the i-th key
 #pragma unroll
             for (int nt = 0; nt < NS_; ++nt) {
-                uint32_t b[2];
-                bytes_of(sVs, nt, b);
-                float sc[2], w[4];  // 2^(f - F); NaN for 255
+                float w[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sc[i] = b[i] == 255u ? NAN : __uint_as_float((b[i] + 127 > F ? b[i] + 127 - F : 0u) << 23);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = m[e] == -INFINITY ? 0.f : m[e];
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float p0 = ptx::ex2(s[nt][at_of(e, i)] - ref);
-                        l[e] += p0;
-                        w[at_of(e, i)] = s[nt][at_of(e, i)] == -INFINITY ? 0.f : p0 * sc[i];  // (a hidden key's scale may be anything)
+                        const float x = s[nt][at_of(e, i)] - ref[e];
+                        l[e] += ptx::ex2(x);
+                        w[at_of(e, i)] = x == -INFINITY ? 0.f : ptx::ex2(x + (up[nt][i] - ref_y[e]));  // (a hidden key's scale may be anything)
                     }
-                }
                 pk[nt][0] = q8::pack_f16(w[0], w[1]);
                 pk[nt][1] = q8::pack_f16(w[2], w[3]);
             }
@@ -417,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
 #pragma unroll
                 for (int nt = 0; nt < (kTurned ? NG : DW / 8); ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nt][e] *= al[kTurned ? e & 1 : e >> 1] * grow;
+                    for (int e = 0; e < 4; ++e) o[nt][e] *= al[kTurned ? e & 1 : e >> 1];
             }
             consumer_sync();
             // O of this warp's dimensions: o[2 gi] and o[2 gi + 1] of the even and the odd dimensions of a group, or (turned)
@@ -477,11 +482,12 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
         const bool whole = p.whole();
         const int c0 = whole ? 0 : p.first_share(a);
         const long long slot = whole ? 0 : state_slot(blockIdx.x, c0);
-        const float vu = q8::pow2(F);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = row_of(e);
             if (r >= rows) continue;
+            // u relative to m, in two steps: the factor itself may be past fp32's range
+            const float vu = y[e] == -INFINITY ? 0.f : ptx::ex2(0.5f * (y[e] - kRoom));
             float sum = (sums[r] + sums[R + r]) + (sums[2 * R + r] + sums[3 * R + r]);
             const int tg = div_g(a, row0 + r), tok = p.seq.q0 + tg, h = p.hk * a.G + row0 + r - tg * a.G;
             const StateAt at = state_at(a, D, p.hk, (long long)p.seq.q0 * a.G + row0 + r);
@@ -495,13 +501,13 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                 const int col = warp * DW + 16 * gi + C * (kTurned ? g : t);
                 float v[C];
                 if constexpr (kTurned) {
-                    v[0] = o[gi][e] * vu;
-                    v[1] = o[gi][2 + e] * vu;
+                    v[0] = o[gi][e] * vu * vu;
+                    v[1] = o[gi][2 + e] * vu * vu;
                 } else {
-                    v[0] = o[2 * gi][2 * e] * vu;
-                    v[1] = o[2 * gi + 1][2 * e] * vu;
-                    v[2] = o[2 * gi][2 * e + 1] * vu;
-                    v[3] = o[2 * gi + 1][2 * e + 1] * vu;
+                    v[0] = o[2 * gi][2 * e] * vu * vu;
+                    v[1] = o[2 * gi + 1][2 * e] * vu * vu;
+                    v[2] = o[2 * gi][2 * e + 1] * vu * vu;
+                    v[3] = o[2 * gi + 1][2 * e + 1] * vu * vu;
                 }
                 if (whole) end_u<C>(a, end, at, col, v, sum);
                 if (whole && end.written) continue;
