@@ -643,11 +643,11 @@ size_t attn_paged_fwd_q8_workspace_bytes(const attn_paged_fwd_q8_params_t *param
 /*
  * attn_paged_fwd_q8 -- attn_paged_fwd over a cache in 8 bits.  The products take the codes in fp16, where
  * they are exact; a query row goes in as its elements times a power of two that brings the largest finite one
- * near 2^14 (exact down to 2^-31 of it), the weights are rounded to fp16 before the value product: with up to 16 rows a
- * key head as weight times scale, relative to the row's largest such product, of which a key loses bits under 2^-39.
- * With more rows a sequence's values are taken relative to the largest scale met, and the keys to the largest of
- * their 128 (hidden ones among them): rows whose scale is 2^15 or more below that lose bits under 2^-33 of the largest value that
- * scale can hold.
+ * near 2^14 (exact down to 2^-31 of it), the weights are rounded to fp16 before the value product.  Of a weight under 2^-21
+ * of the row's largest bits under 2^-32 of that are lost, or, where a weight goes in times its value's scale (with up
+ * to 16 rows a key head, and where the scales of 128 neighbouring keys lie 2^16 or more apart), bits under 2^-32 of
+ * the largest such product that the row has.  What a row does not see, or gives no weight, takes nothing from it, whatever its scale.
+ * (With more than 16 rows, rows of scale byte 0, under 2^-118, count as zeros beside ones of byte 25 and up among those 128 keys.)
  * Everything else as attn_paged_fwd; a row that holds a NaN makes the rows that see it NaN.
  * Supported: as attn_paged_fwd; the bases and strides of pages and scales are multiples of 16 bytes.  A cache whose
  * heads lie apart ([num_pages, Hkv, page_size, d] in memory, passed by its strides) is read faster: 132 us for

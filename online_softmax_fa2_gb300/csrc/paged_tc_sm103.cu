@@ -115,13 +115,13 @@ struct Ctrl {
 
 // What a cache of codes needs besides.  A tile's codes come in four units of 64 keys, K's two and V's two, each with a place
 // of its own; its scale bytes lie in a ring of two.  What the softmax has to know of a tile lies in a ring of eight (the
-// conversion runs at most four tiles ahead of it).
+// conversion runs at most four tiles ahead of it, the producers two tiles ahead of that).
 constexpr int kUnitKeys = 64, kNotes = 8;
 template <int NT, int ST>
 struct CtrlQ8 : Ctrl<NT, ST> {
     uint64_t q_ready[NT], raw_full[4], raw_empty[4];
     uint64_t sc_full[2][2], sc_empty[2][2];  // K's and V's scale bytes, two slots each
-    uint16_t notes[kNotes];  // of a tile: the unit of its keys, then that of u (exponents as scale bytes)
+    volatile uint32_t notes[kNotes];  // of a tile: what its keys and, << 16, its values are relative to (next_unit)
 };
 
 // D dimensions, NT row tiles of QR rows.  A tile of 64 rows is multiplied as one of 128 whose upper half
@@ -215,10 +215,10 @@ __device__ __forceinline__ void scale_o(uint32_t taddr, float alpha) {
 // transpose their 4 x 4 pieces of 16 bytes first (two exchanges), and each store writes 64 bytes of
 // eight rows.  Whole warp.
 template <int D, bool kQ8>
-__device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, uint32_t unit, __nv_bfloat16 *orow, float *lse) {
+__device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_run, int unit, __nv_bfloat16 *orow, float *lse) {
     const int lane = threadIdx.x & 31, i = lane & 3;
     const bool empty = l_run == 0.f, b0 = i & 1, b1 = i & 2;  // a NaN is no empty row
-    const float inv = empty ? 0.f : kQ8 ? q8::pow2(unit) / l_run : 1.f / l_run;
+    const float inv = empty ? 0.f : 1.f / l_run, back = kQ8 ? q8::pow2_low(unit) : 1.f;
     uint4 *to[4];  // the quad's rows
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -232,7 +232,9 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
         ptx::reg_fence(ov);
 #pragma unroll
         for (int t = 0; t < 16; ++t)
-            v[t / 4][t % 4] = empty ? 0u : ptx::pack_bf16x2(__uint_as_float(ov[2 * t]) * inv, __uint_as_float(ov[2 * t + 1]) * inv);
+            v[t / 4][t % 4] = empty ? 0u
+                              : kQ8 ? ptx::pack_bf16x2(__uint_as_float(ov[2 * t]) * inv * back, __uint_as_float(ov[2 * t + 1]) * inv * back)
+                                    : ptx::pack_bf16x2(__uint_as_float(ov[2 * t]) * inv, __uint_as_float(ov[2 * t + 1]) * inv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
 #pragma unroll
@@ -257,7 +259,7 @@ __device__ __forceinline__ void write_rows(uint32_t taddr, float l_run, float m_
 
 // The same of a row that leaves its state, or starts from one (paged_state.cuh); tok < 0: no row.
 template <int D, bool kQ8>
-__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, uint32_t unit, int tok, int g, int hk) {
+__device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, float sum, float m, int unit, int tok, int g, int hk) {
     const bool on = tok >= 0;
     const paged::StateAt at = paged::state_at(a, D, hk, (long long)tok * a.G + g);
     const int h = hk * a.G + g;
@@ -274,7 +276,7 @@ __device__ __forceinline__ void end_row(const paged::Args &a, uint32_t taddr, fl
         ptx::reg_fence(ov);
         float v[32];
 #pragma unroll
-        for (int t = 0; t < 32; ++t) v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2(unit) : 1.f);
+        for (int t = 0; t < 32; ++t) v[t] = __uint_as_float(ov[t]) * (kQ8 ? q8::pow2_low(unit) : 1.f);
         if (on) paged::end_u<32, D>(a, e, at, cc * 32, v, sum);
         if (on && !e.written) {
             uint4 *to = reinterpret_cast<uint4 *>(a.o + tok * a.os0 + h * a.os1 + cc * 32);
@@ -341,14 +343,49 @@ __device__ __forceinline__ void write_cut(const paged::Args &a, const Share &sha
 // ---------------------------------------------------------------- a cache of codes
 //
 // The products take fp16, where codes are exact (paged_rows_q8.cu): warps make an operand of each 64 keys of codes that
-// TMA brings, code times 2^(e - E) with E the largest scale byte of a tile's keys, or for V one that holds for
-// as many tiles as no byte passes it by more than 6 (448 * 2^6 < 65504); both go to the softmax, which takes E into the
-// tile's factor of the logits, and rescales u when V's changes.  (Codes are exact down to 15 below E.)
+// TMA brings, code times 2^(e - E) with an E that holds for as many tiles as all scale bytes e lie where that is
+// exact, from 15 below it to 6 above it (448 * 2^6 < 65504); K's and V's go to the softmax, which takes K's into the
+// tile's factor of the logits.  (Keys that no row of the block sees become zeros; so
+// does beside others, from 25 below E on, a row of scale byte 0, of zeros nearly always.)
+// A tile whose scale bytes lie further apart is a wide one: its codes go in as they are.  The softmax then multiplies S by the
+// keys' own scales, or the weights by the values' own relative to what the row's largest weight times
+// scale has been (odd_tile), so that a row loses nothing to keys that it does not see, or that weigh nothing in it,
+// whatever their scales.  A row's u is in a unit of its own, which is V's E as long as that stays.
+// The reference of a row's weights lies 2^7 below its maximum: as it may lag by 2^8, the weights reach 2^15, and lose
+// bits from 2^-21 of the largest on, 2^-32 of it at most.
 //
 // What bounds it: shared memory.  Of a 256 x 128 tile the products read 192 KB of it (1536 clocks of 128 bytes), the codes'
 // way takes 128 KB more (in by TMA, out to registers, back as fp16), of the 3030 clocks that the tile takes over bf16:
 // 3700 here, 2048 tokens over 18432 keys of 32/8 heads 462 us against 394, 1.26 PFLOP/s; 16 ragged sequences to 4096 keys,
 // chunks to 512 tokens, 28/4 heads 100 us against 75.  The issuer waits for operands 220 clocks of a tile, for weights 670.
+
+// A tile's 128 scale bytes, four a lane (of keys past the held ones 0), against what its operand is relative to, `unit` (below 0:
+// nothing yet), which stays as long as they all lie where codes are exact: from kExact below to kAbove above.  Otherwise the
+// largest of them is the unit, or, where they lie further apart than kExact, the tile is a wide one, which keeps the unit and
+// adds kWide.  (0, a row of zeros, and 255, a NaN, are none of them.)  Whole warp.
+constexpr int kExact = 15, kAbove = 6, kWide = 256;
+__device__ __forceinline__ int next_unit(int unit, uint32_t e4, int held) {
+    const int left = held - 4 * (int)(threadIdx.x & 31), now = unit & 255;
+    // nearly always: no key past the held ones, no byte of the two, all in range (two bytes a step)
+    const uint32_t lo = e4 & 0xff00ffu, hi = (e4 >> 8) & 0xff00ffu;
+    const uint32_t least = (uint32_t)max(now - kExact, 1) * 0x10001u, most = (uint32_t)min(now + kAbove, 254) * 0x10001u;
+    const bool in = __vminu2(__vminu2(lo, hi), least) == least && __vmaxu2(__vmaxu2(lo, hi), most) == most;
+    if (__all_sync(0xffffffffu, in && left >= 4 && unit >= 0)) return now;
+    e4 &= left >= 4 ? 0xffffffffu : left > 0 ? 0xffffffffu >> (32 - 8 * left) : 0u;
+    uint32_t big = 0, small = 255;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i, e4 >>= 8) {
+        const uint32_t e = e4 & 255u;
+        if (e - 1u < 254u) {
+            big = max(big, e);
+            small = min(small, e);
+        }
+    }
+    const int b = (int)__reduce_max_sync(0xffffffffu, big), t = (int)__reduce_min_sync(0xffffffffu, small);
+    if (unit >= 0 && b <= now + kAbove && t >= now - kExact) return now;  // (none: 0 and 255)
+    if (b == 0) return unit < 0 ? 0 : now;
+    return b - t <= kExact ? b : kWide | (unit < 0 ? 0 : now);
+}
 
 // A producer of K's (0), V's (1) or both kinds' (2) codes, in the order in which the converting warps come to them, and
 // scale bytes, four a lane, loaded a tile ahead.  (Copies by lanes of a warp go out one after the other, each as long as a
@@ -380,6 +417,7 @@ __device__ __forceinline__ void produce_codes(int kinds, const paged::Args &a, c
         const int *row = a.bt + w.b * a.bt_s;
         int held = -1, pages = 0;  // this lane holds the page of table entry held + lane
         uint32_t ahead[2];
+        int unit_k = -1, unit_v = -1;
         bool loaded = false;
         auto last_page = [&](int kv0) { return (min(kv0 + BK, w.seq.n) - 1) >> a.page_log2; };
         auto page_of = [&](int key) { return __shfl_sync(0xffffffffu, pages, min(max((key >> a.page_log2) - held, 0), 31)); };
@@ -394,48 +432,64 @@ __device__ __forceinline__ void produce_codes(int kinds, const paged::Args &a, c
                     ahead[x] = key < w.seq.n ? __ldg(reinterpret_cast<const uint32_t *>(at + slot)) : 0u;
                 }
         };
-        for (int j = w.j0; j < w.j1; ++j, ++tile) {
-            const int kv0 = j * BK;
-            if (held < 0 || last_page(kv0) >= held + 32) {
-                held = kv0 >> a.page_log2;
-                const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
-                pages = at <= end ? __ldg(row + at) : 0;
-                if (pages < 0 || pages >= a.num_pages) {
-                    atomicOr(a.flags, kFlagBadIndex);
-                    pages = a.num_pages;  // outside the tensor: TMA fills zeros
-                }
-            }
-            if (!loaded) load_scales(kv0);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (kinds == 2 || kinds == x) {
-                    if (ok && tile > 1) ok = wait(&ctrl->sc_empty[x][tile & 1], ((tile >> 1) - 1) & 1);
+        // a step of the loop is tile j's copies, then what tile j + 1 needs: its unit is found under those copies (before its own
+        // it took a 2048-token chunk over 18432 keys from 462 to 474 us)
+        for (int j = w.j0 - 1; ok;) {
+            if (j >= w.j0) {
+                const int kv0 = j * BK;
+#pragma unroll 1
+                for (int x = kinds == 1; x <= (kinds > 0); ++x) {
+                    if (tile > 1) ok = wait(&ctrl->sc_empty[x][tile & 1], ((tile >> 1) - 1) & 1);
                     if (!ok) break;
-                    *reinterpret_cast<uint32_t *>(smem + L::kScaleOff + (2 * x + (tile & 1)) * BK + 4 * lane) = ahead[x];
+                    *reinterpret_cast<uint32_t *>(smem + L::kScaleOff + (2 * x + (tile & 1)) * BK + 4 * lane) = x ? ahead[1] : ahead[0];
+                    if (lane == 0) reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes])[x] = (uint16_t)(x ? unit_v : unit_k);
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&ctrl->sc_full[x][tile & 1]);
                 }
-            if (!ok) break;
-            loaded = j + 1 < w.j1 && last_page(kv0 + BK) < held + 32;
-            if (loaded) load_scales(kv0 + BK);
-            const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
-#pragma unroll 1
-            for (step = 0; step < steps; ++step) {
-                const int u = unit_of(step);
-                if (tile > 0) ok = wait(&ctrl->raw_empty[u], (tile - 1) & 1);
                 if (!ok) break;
-                // boxes that hold a key of the sequence
-                const int c0 = (u & 1) * kUnitKeys;
-                const int nbox = held_keys > c0 ? min(kUnitKeys >> pb_log2, ((held_keys - c0 - 1) >> pb_log2) + 1) : 0;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->raw_full[u], (uint32_t)(nbox * D) << pb_log2);
-                __syncwarp();
-                const int key = kv0 + c0 + (lane << pb_log2), page = page_of(key);
-                if (lane < nbox)
-                    ptx::tma_load_4d(smem + L::kRawOff + u * L::kRawUnit + ((lane << pb_log2) * D), u >= 2 ? &tm_v : &tm_k,
-                                     &ctrl->raw_full[u], 0, key & ((1 << a.page_log2) - 1), w.hk, page);
+                loaded = j + 1 < w.j1 && last_page(kv0 + BK) < held + 32;
+                if (loaded) load_scales(kv0 + BK);
+                const int held_keys = w.seq.n - kv0;  // of the tile: 1 or more
+#pragma unroll 1
+                for (step = 0; step < steps; ++step) {
+                    const int u = unit_of(step);
+                    if (tile > 0) ok = wait(&ctrl->raw_empty[u], (tile - 1) & 1);
+                    if (!ok) break;
+                    // boxes that hold a key of the sequence
+                    const int c0 = (u & 1) * kUnitKeys;
+                    const int nbox = held_keys > c0 ? min(kUnitKeys >> pb_log2, ((held_keys - c0 - 1) >> pb_log2) + 1) : 0;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&ctrl->raw_full[u], (uint32_t)(nbox * D) << pb_log2);
+                    __syncwarp();
+                    const int key = kv0 + c0 + (lane << pb_log2), page = page_of(key);
+                    if (lane < nbox)
+                        ptx::tma_load_4d(smem + L::kRawOff + u * L::kRawUnit + ((lane << pb_log2) * D), u >= 2 ? &tm_v : &tm_k,
+                                         &ctrl->raw_full[u], 0, key & ((1 << a.page_log2) - 1), w.hk, page);
+                }
+                if (!ok) break;
+                step = 0;
+                ++tile;
             }
-            if (!ok) break;
-            step = 0;
+            if (++j == w.j1) break;
+            const int kv0 = j * BK;
+            if (!loaded) {
+                if (held < 0 || last_page(kv0) >= held + 32) {
+                    held = kv0 >> a.page_log2;
+                    const int at = held + lane, end = (w.seq.n - 1) >> a.page_log2;
+                    pages = at <= end ? __ldg(row + at) : 0;
+                    if (pages < 0 || pages >= a.num_pages) {
+                        atomicOr(a.flags, kFlagBadIndex);
+                        pages = a.num_pages;  // outside the tensor: TMA fills zeros
+                    }
+                }
+                load_scales(kv0);
+            }
+            loaded = false;
+#pragma unroll 1
+            for (int x = kinds == 1; x <= (kinds > 0); ++x) {  // (keys that no row of the block sees have no say)
+                const int unit = next_unit(x ? unit_v : unit_k, x ? ahead[1] : ahead[0], w.keys - kv0);
+                if (x) unit_v = unit;
+                else unit_k = unit;
+            }
         }
     } while (ok && w.next(a));
     if (!ok || *abort)  // copies in flight land before the CTA leaves
@@ -494,17 +548,6 @@ __device__ __forceinline__ void convert_unit(const uint8_t *raw, uint8_t *to, in
     }
 }
 
-// The largest of a tile's 128 scale bytes whose keys are held (255, a NaN, is none; 0 without any).  Whole warp.
-__device__ __forceinline__ int largest_scale(const uint8_t *scales, int held) {
-    const int lane = threadIdx.x & 31;
-    uint32_t e4 = *reinterpret_cast<const uint32_t *>(scales + 4 * lane), big = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i, e4 >>= 8)
-        if (4 * lane + i < held && (e4 & 255u) != 255u) big = max(big, e4 & 255u);
-    return (int)__reduce_max_sync(0xffffffffu, big);
-}
-// The unit of u from one tile on whose largest scale byte is `big`.
-__device__ __forceinline__ int next_unit(int unit, int big) { return unit < 0 || big > unit + 6 ? big : unit; }
 
 // A converting warp: with four of them a unit of each tile, with two K's or V's units.  (Four warps that took every unit
 // together waited for one another and for a fence after each: 2450 clocks a tile beside the 2200 of the conversion.)
@@ -526,24 +569,21 @@ __device__ __forceinline__ void convert_codes(const paged::Args &a, uint8_t *sme
     uint32_t sp = 1, tile = 0;  // a fresh barrier's phase before the first counts as complete
     do {
         if (w.keys == 0) continue;
-        int unit = -1;  // of u, for this piece
         for (int j = w.j0; j < w.j1; ++j, ++tile) {
-            const int held = w.seq.n - j * BK;
+            const int held = w.keys - j * BK;  // (keys that no row of the block sees become zeros)
             const uint8_t *scales = smem + L::kScaleOff + (2 * kind + (tile & 1)) * BK;
             if (!wait(&ctrl->sc_full[kind][tile & 1], (tile >> 1) & 1u)) return;
-            int top = largest_scale(scales, held);
-            if (kind == 1) top = unit = next_unit(unit, top);
-            if (cw == 0) {  // V's bytes, for the note only
+            const int unit = reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes])[kind];
+            if (cw == 0) {  // V's note is there before the tile's S is
                 if (!wait(&ctrl->sc_full[1][tile & 1], (tile >> 1) & 1u)) return;
-                unit = next_unit(unit, largest_scale(scales + 2 * BK, held));
-                if (lane == 0) {
-                    *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[tile % kNotes]) = (uint16_t)(top | (unit << 8));
-                    ptx::mbar_arrive(&ctrl->sc_empty[1][tile & 1]);
-                }
+                if (lane == 0) ptx::mbar_arrive(&ctrl->sc_empty[1][tile & 1]);
             }
             __half2 factor[2 * H];
 #pragma unroll
-            for (int i = 0; i < 2 * H; ++i) factor[i] = factor_of(scales[h0 * kUnitKeys + 32 * i + lane], top);
+            for (int i = 0; i < 2 * H; ++i) {
+                const int e = scales[h0 * kUnitKeys + 32 * i + lane];
+                factor[i] = factor_of(e, unit >= kWide && e != 255 ? e : unit & 255);
+            }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&ctrl->sc_empty[kind][tile & 1]);
             if (!wait(&empty[st], sp)) return;
@@ -593,6 +633,132 @@ __device__ __forceinline__ float queries_to_f16(uint8_t *tile, int panel_bytes, 
     return __uint_as_float((uint32_t)(max((int)(top >> 7), 27) - 14) << 23);
 }
 
+// The reference of a row's weights over codes: as bf16fwd::update_max, kRoom below the maximum.
+constexpr float kRoom = 7.f;
+// (moved: where it is set for the first time too, with an alpha of 1)
+__device__ __forceinline__ float update_reference(float mt, float &m_run, bool &moved) {
+    moved = mt > m_run + (kRoom + bf16fwd::kRescaleThreshold);
+    if (!moved) return 1.f;
+    const float alpha = m_run == -INFINITY ? 1.f : ptx::ex2(m_run - (mt - kRoom));
+    m_run = mt - kRoom;
+    return alpha;
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 16 keys of a tile at this lane's row, and their scale bytes out of `word`, of which lane l has those of keys 4 l ..
+template <class Body>
+__device__ __forceinline__ void for_keys(uint32_t taddr, uint32_t word, Body body) {
+#pragma unroll 1
+    for (int cc = 0; cc < BK / 16; ++cc) {
+        uint32_t r[16], e[4];
+        tmem_ld16(taddr + cc * 16, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = __shfl_sync(0xffffffffu, word, 4 * cc + i);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) asm volatile("" : "+r"(r[t]));
+        body(cc, r, [&](int t) { return (int)((e[t / 4] >> (8 * (t % 4))) & 255u); });
+    }
+}
+
+// Four scale bytes from position `key` of a sequence of n keys on, whose pages `row` lists.
+__device__ __forceinline__ uint32_t load_scales(const paged::Args &a, const int *row, const uint8_t *from, long long stride, int key, int n) {
+    if (key >= n) return 0u;
+    int page = __ldg(row + (key >> a.page_log2));
+    page = page < 0 || page >= a.num_pages ? 0 : page;
+    return __ldg(reinterpret_cast<const uint32_t *>(from + page * stride + (key & ((1 << a.page_log2) - 1))));
+}
+
+// A row on its way through a piece: the reference and the sum of its weights, and u's unit, 2^(unit - 127); `own` where that has
+// been the tiles' own so far, from which u may be scaled up by 2^24.
+struct Row {
+    float m, l;
+    int unit, own;
+};
+// Logits from which a product that is rounded in the maximum and not in the exponent would part the two.
+constexpr float kLarge = 1048576.f;
+// The softmax of a tile that is a wide one in K or V, or relative to something else than a row's u, or with logits of kLarge: 16
+// keys at a time, three times through S.  Its logits are the products times each key's own factor.  Its weights go in times 2^(e - unit), e a key's
+// scale byte (of a tile that is not wide what V's operand is relative to), in a unit that brings the largest of these near 2^14, or
+// keeps what u has; u is scaled to that unit.  Rare, and out of line, where it takes no room in the instruction
+// cache: within the loop it took chunks from 463 to 634 us.  Whether the row can go on without.  Whole warp.
+template <int D>
+__device__ __noinline__ bool odd_tile(const paged::Args &a, const Walk &w, uint32_t s_addr, uint32_t o_addr, int kv0, int lim, int k_unit,
+                                      int v_unit, float c_row, bool first, Row &row) {
+    Row s = row;
+    constexpr int kNone = -100000;
+    constexpr uint32_t kLeast = 0x800000u, kMost = 0x7f000000u;  // bits of a weight less kLeast: below kMost, not 0 nor a NaN
+    const int key = kv0 + 4 * (int)(threadIdx.x & 31);
+    const int *pages = a.bt + w.b * a.bt_s;
+    const bool even = v_unit < kWide;
+    const uint32_t kw = k_unit < kWide ? (uint32_t)k_unit * 0x01010101u : load_scales(a, pages, a.ks + w.hk * a.kss[1], a.kss[0], key, w.seq.n);
+    const uint32_t vw = even ? (uint32_t)v_unit * 0x01010101u : load_scales(a, pages, a.vs + w.hk * a.vss[1], a.vss[0], key, w.seq.n);
+    float mt = -INFINITY;
+    for_keys(s_addr, kw, [&](int cc, uint32_t (&r)[16], auto byte) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            float x = __uint_as_float(r[t]) * q8::finite(c_row * q8::pow2((uint32_t)byte(t)));
+            if (kv0 + 16 * cc + t >= lim) x = -INFINITY;
+            mt = fmaxf(mt, x);
+            r[t] = __float_as_uint(x);
+        }
+        tmem_st16(s_addr + cc * 16, r);
+    });
+    ptx::tmem_st_wait();
+    bool rescale;
+    const float alpha = update_reference(mt, s.m, rescale), ref = s.m == -INFINITY ? 0.f : s.m;
+    float sum = 0.f;
+    int need = kNone;  // the largest exponent, as in the bits of a weight, and scale byte
+    for_keys(s_addr, vw, [&](int cc, uint32_t (&r)[16], auto byte) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const float p = ptx::ex2(__uint_as_float(r[t]) - ref);
+            sum += p;
+            r[t] = __float_as_uint(p);
+            if (r[t] - kLeast < kMost && byte(t) != 255) need = max(need, (int)(r[t] >> 23) + byte(t));
+        }
+        tmem_st16(s_addr + cc * 16, r);
+    });
+    ptx::tmem_st_wait();
+    const bool old = !first && s.l != 0.f && alpha > 0.f, some = need != kNone;
+    s.l = fmaf(alpha, s.l, sum);
+    const int now = s.unit, al = (int)(__float_as_uint(alpha) >> 23);
+    need -= 127 + 14;
+    int to = some ? need : kNone;
+    if (old) to = max(to, now + al - 127 - (some && s.own ? 24 : 0));
+    bool own = old && !some && s.own;
+    if (even && (to == kNone || (to <= v_unit && to >= v_unit - 20))) {  // the tiles' own again
+        to = v_unit;
+        own = true;
+    }
+    to = to == kNone ? 127 : min(max(to, -15), 254);
+    if (!first) {
+        const int e = al + now - to;
+        const float f = !old || e <= 0 ? 0.f : __uint_as_float((__float_as_uint(alpha) & 0x7fffffu) | ((uint32_t)min(e, 254) << 23));
+        if (__any_sync(0xffffffffu, f != 1.f)) scale_o<D>(o_addr, f);
+    }
+    s.unit = to;
+    s.own = own;
+    for_keys(s_addr, vw, [&](int cc, uint32_t (&r)[16], auto byte) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const int e = (int)(r[t] >> 23) + byte(t) - to;
+            if (r[t] - kLeast < kMost && byte(t) != 255) r[t] = e <= 0 ? 0u : (r[t] & 0x7fffffu) | ((uint32_t)min(e, 254) << 23);
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) pk[t] = q8::pack_f16(__uint_as_float(r[2 * t]), __uint_as_float(r[2 * t + 1]));
+        tmem_st8(s_addr + cc * 8, pk);  // (columns that have been read)
+    });
+    ptx::tmem_st_wait();
+    row = s;
+    return even && to == v_unit && !(fabsf(s.m) > kLarge && s.m != -INFINITY);
+}
+
 __device__ __forceinline__ void store_p_f16(uint32_t taddr, const float (&x)[BK]) {
 #pragma unroll
     for (int cc = 0; cc < BK / 64; ++cc) {
@@ -608,7 +774,7 @@ __device__ __forceinline__ void store_p_f16(uint32_t taddr, const float (&x)[BK]
 template <int D, int NT, int QR, bool kState, bool kQ8>
 __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                    const __grid_constant__ CUtensorMap tm_v, const paged::Args a) {
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ paged::Args a) {
     using L = Layout<D, NT, QR, kQ8>;
     using Control = typename L::Control;
     constexpr int KS = L::kKStages, VS = L::kVStages;
@@ -879,7 +1045,8 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
             __syncwarp();
             float m_run = -INFINITY, l_run = 0.f;
             float c_row = c;
-            uint32_t unit = 127;  // u is in units of 2^(unit - 127)
+            int unit = 0, own = 1;  // u is in units of 2^(unit - 127) (odd_tile)
+            int even = 0;           // that of V's operand which all rows' u is in, -1: none
             if constexpr (kQ8) {
                 if (n > 0) {
                     if (!wait_warp(&ctrl->q_full[X], qph)) { ok = false; break; }
@@ -889,46 +1056,84 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                     ptx::mbar_arrive(&ctrl->q_ready[X]);
                 }
             }
-            for (int jj = 0; jj < n; ++jj) {
-                const int kv0 = (j0 + jj) * BK;
-                if (!wait_warp(&ctrl->s_full[X], sph)) { ok = false; break; }
-                sph ^= 1;
-                ptx::tc_fence_after();
-                float x[BK], ct = c_row, grow = 1.f;
-                bool grown = false;
-                if constexpr (kQ8) {
-                    const uint32_t note = *reinterpret_cast<volatile uint16_t *>(&ctrl->notes[(tiles + jj) % kNotes]);
-                    ct = fmaxf(c_row * q8::pow2(note & 255u), 1.17549435e-38f);  // (not 0: -inf times it stays -inf)
-                    grown = jj > 0 && (note >> 8) != unit;
-                    if (grown) grow = q8::pow2(unit + 127 > (note >> 8) ? unit + 127 - (note >> 8) : 0);
-                    unit = note >> 8;
+            int jj = 0;
+            bool odd = false;
+            for (;;) {
+                for (; jj < n; ++jj) {
+                    const int kv0 = (j0 + jj) * BK;
+                    if (!wait_warp(&ctrl->s_full[X], sph)) { ok = false; break; }
+                    sph ^= 1;
+                    ptx::tc_fence_after();
+                    float x[BK], ct = c_row, alpha;
+                    bool moved;
+                    if constexpr (kQ8) {
+                        const uint32_t note = ctrl->notes[(tiles + jj) % kNotes];
+                        if (jj == 0) even = unit = (int)(note >> 16);
+                        odd = (note & kWide) || (int)(note >> 16) != even || (note >> 16) >= kWide;
+                        if (odd) break;
+                        ct = q8::finite(fmaxf(c_row * q8::pow2(note & 255u), 1.17549435e-38f));  // (not 0: -inf times it stays -inf)
+                    }
+                    bf16fwd::load_s_row(lane_addr + s_col, x);
+                    const float mt = bf16fwd::tile_logits<false>(x, ct, kv0, kv0 + BK > lim0, lim);
+                    if constexpr (kQ8) {
+                        const float before = m_run;
+                        alpha = update_reference(mt, m_run, moved);
+                        if (__any_sync(0xffffffffu, moved)) {
+                            // (rows that are none of the block's hold anything, and have no say)
+                            odd = __any_sync(0xffffffffu, mine && moved && fabsf(m_run) > kLarge);
+                            if (odd) {
+                                m_run = before;
+                                break;
+                            }
+                            if (jj > 0) scale_o<D>(lane_addr + o_col, alpha);
+                        }
+                    } else {
+                        alpha = bf16fwd::update_max(mt, m_run, moved);
+                    }
+                    const float lsum = bf16fwd::tile_exp<false>(x, ct, m_run);
+                    l_run = fmaf(alpha, l_run, lsum);
+                    if (!kQ8 && __any_sync(0xffffffffu, moved)) scale_o<D>(lane_addr + o_col, alpha);
+                    // value rows past the sequence may hold anything: the first of the two tiles that
+                    // uses this V zeroes them before its product reads them
+                    if (!kQ8 && kv0 + BK > seqn && (X == 0 || jj >= na)) {
+                        if (!wait_warp(&ctrl->v_full[vs], vph)) { ok = false; break; }
+                        if (kv0 + r >= seqn) bf16fwd::zero_v_row<D>(smem + L::kVOff + vs * L::kTile, r);
+                        ptx::fence_proxy_async_smem();
+                    }
+                    if (++vs == VS) { vs = 0; vph ^= 1; }
+                    // the weights go to the product in bf16, half a step of 2^-8 each (l_run has them in fp32):
+                    // V in 32 bits would take twice the room and run at half the rate
+                    if constexpr (kQ8) store_p_f16(lane_addr + s_col, x);
+                    else bf16fwd::store_p(lane_addr + s_col, x);
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&ctrl->p_full[X]);
                 }
-                bf16fwd::load_s_row(lane_addr + s_col, x);
-                const float mt = bf16fwd::tile_logits<false>(x, ct, kv0, kv0 + BK > lim0, lim);
-                bool rescale;
-                const float alpha = bf16fwd::update_max(mt, m_run, rescale);
-                const float lsum = bf16fwd::tile_exp<false>(x, ct, m_run);
-                l_run = fmaf(alpha, l_run, lsum);
-                if (__any_sync(0xffffffffu, rescale || grown)) scale_o<D>(lane_addr + o_col, kQ8 ? alpha * grow : alpha);
-                // value rows past the sequence may hold anything: the first of the two tiles that
-                // uses this V zeroes them before its product reads them
-                if (!kQ8 && kv0 + BK > seqn && (X == 0 || jj >= na)) {
-                    if (!wait_warp(&ctrl->v_full[vs], vph)) { ok = false; break; }
-                    if (kv0 + r >= seqn) bf16fwd::zero_v_row<D>(smem + L::kVOff + vs * L::kTile, r);
-                    ptx::fence_proxy_async_smem();
+                if (!kQ8 || !odd) break;
+                if constexpr (kQ8) {  // tile jj, behind the loop
+                    const uint32_t note = ctrl->notes[(tiles + jj) % kNotes];
+                    Row row{m_run, l_run, unit, own};
+                    const bool fits = odd_tile<D>(a, ctrl->parked[warp - 4], lane_addr + s_col, lane_addr + o_col, (j0 + jj) * BK, lim,
+                                                  (int)(note & 0xffffu), (int)(note >> 16), c_row, jj == 0, row);
+                    even = __all_sync(0xffffffffu, fits || !mine) ? (int)(note >> 16) : -1;
+                    m_run = row.m;
+                    l_run = row.l;
+                    unit = row.unit;
+                    own = row.own;
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&ctrl->p_full[X]);
+                    odd = false;
+                    ++jj;
                 }
-                if (++vs == VS) { vs = 0; vph ^= 1; }
-                // the weights go to the product in bf16, half a step of 2^-8 each (l_run has them in fp32):
-                // V in 32 bits would take twice the room and run at half the rate
-                if constexpr (kQ8) store_p_f16(lane_addr + s_col, x);
-                else bf16fwd::store_p(lane_addr + s_col, x);
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(&ctrl->p_full[X]);
             }
             if (!ok) break;
+            if constexpr (kQ8) {  // relative to the maximum, as others' states are
+                m_run += kRoom;
+                l_run *= 0.0078125f;
+                unit -= (int)kRoom;
+            }
             w = ctrl->parked[warp - 4];
             tiles += nmax;
-            for (int jj = n; jj < nmax; ++jj)  // tiles that only the other rows see
+            for (jj = n; jj < nmax; ++jj)  // tiles that only the other rows see
                 if (++vs == VS) { vs = 0; vph ^= 1; }
             // where this row goes, before the walk moves on
             const bool whole = w.j0 == 0 && w.j1 >= tx;
@@ -984,7 +1189,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                 ptx::tmem_ld_wait();
                 ptx::reg_fence(ov);
                 if constexpr (kQ8) {
-                    const float vu = q8::pow2(unit);
+                    const float vu = q8::pow2_low(unit);
 #pragma unroll
                     for (int t = 0; t < 32; ++t) ov[t] = __float_as_uint(__uint_as_float(ov[t]) * vu);
                 }

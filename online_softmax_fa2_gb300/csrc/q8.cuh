@@ -12,6 +12,9 @@ __device__ __forceinline__ float pow2(uint32_t e) {
     return __uint_as_float((e << 23) | (((e + 1) & 0xffu) <= 1u ? 0x400000u : 0u));
 }
 
+// The same for e from -22 to 254, where it may be one of the least subnormals.
+__device__ __forceinline__ float pow2_low(int e) { return __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x400000u >> -e); }
+
 // A factor of logits, at most the largest float (0 times it is 0); a NaN stays one.  A query row's power of two and a key's
 // meet before the sum of their products does: either alone may take it out of fp32, with logits of ordinary size.
 __device__ __forceinline__ float finite(float x) {

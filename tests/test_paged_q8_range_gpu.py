@@ -8,6 +8,7 @@ import torch
 import online_softmax_fa2_gb300 as ofa
 from paged_q8_helpers import q8_inputs
 from paged_range_helpers import check_visible
+from test_paged_prefix_gpu import inputs, run as run_prefix
 from test_paged_q8_gpu import run
 
 pytestmark = pytest.mark.gpu
@@ -17,6 +18,9 @@ SHAPES = [  # new, lens, Hq, Hkv, d
     ([4, 1], [70, 40], 4, 2, 128),          # up to 8 rows a key head
     ([8, 3], [150, 200], 4, 2, 64),         # up to 16
     ([1, 2], [900, 300], 4, 2, 128),        # few rows, cut
+    ([30, 12], [140, 300], 4, 2, 128),      # one tile
+    ([30, 12], [140, 2300], 4, 2, 64),      # one tile, cut
+    ([150, 70], [200, 300], 4, 2, 128),     # two tiles
 ]
 
 
@@ -179,3 +183,18 @@ def test_queries_near_the_largest_over_the_smallest_keys(shape):
         set_codes(s, "k", b, torch.arange(n), torch.randn(n, d, generator=g))
         set_bytes(s, "k", b, torch.arange(n), torch.randint(0, 4, (n, Hkv), generator=g))
     go(s, new, lens, 0.125)
+
+
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[3], SHAPES[5]])
+def test_large_hidden_keys_behind_a_prefix(shape):
+    """Side by side and one after the other; a prefix's own values 2^35 above or below the own keys'."""
+    new, lens, Hq, Hkv, d = shape
+    for up in (35, -35):
+        s, groups = inputs(new, lens, [500], [0, sum(new)], Hq, Hkv, d, 16, True, seed=39)
+        pg = s["pt"][0].long()
+        b = s["vs"].view(torch.uint8)[pg].int()
+        s["vs"].view(torch.uint8)[pg] = torch.where(b == 255, b, b + up).to(torch.uint8)
+        for i, n in enumerate(lens):
+            set_bytes(s, "v", i, [n - 1], bytes_at(s, "v", i, [n - 1]).cpu().int() + 60)
+        o, lse = run_prefix(s, scale=0.1, max_q=max(new))
+        check_visible(o, lse, s, new, lens, True, 0.1, groups, [500], what=f"up {up}")
