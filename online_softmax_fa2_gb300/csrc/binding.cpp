@@ -117,9 +117,21 @@ void fill_scales(attn_paged_scales_t &s, const attn_paged_cache_t &c, int dev, P
     strides(s.v_stride, vs);
 }
 
+// f() without the interpreter's lock, as a call by ctypes has it: a launch may wait for room in the stream's queue, behind work that
+// waits for a Python thread, and an allocation for the driver.
+template <class F>
+auto unlocked(F f) {
+    struct Unlock {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Unlock() { PyEval_RestoreThread(state); }
+    } unlock;
+    return f();
+}
+
 // A tensor to write: the given one, or a new one.
 at::Tensor output(PyObject *o, int dev, at::ScalarType dt, at::IntArrayRef shape, const at::Tensor &like) {
-    return given(o) ? tensor(o, dev, dt, shape) : at::empty(shape, like.options().dtype(dt));
+    if (given(o)) return tensor(o, dev, dt, shape);
+    return unlocked([&] { return at::empty(shape, like.options().dtype(dt)); });
 }
 
 PyObject *result(attn_status_t st, const at::Tensor &a) { return st ? PyLong_FromLong(st) : THPVariable_Wrap(a); }
@@ -188,7 +200,7 @@ PyObject *append(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const at::Tensor o = output(a[16], dev, dt, q.sizes(), q);
         x.q_out = o.data_ptr();
         strides(x.q_out_stride, o);
-        return result(q8 ? lib.attn_paged_append_q8_(&p, stream) : lib.attn_paged_append_(&x, stream), o);
+        return result(unlocked([&] { return q8 ? lib.attn_paged_append_q8_(&p, stream) : lib.attn_paged_append_(&x, stream); }), o);
     });
 }
 
@@ -209,7 +221,7 @@ PyObject *read_q8(PyObject *, PyObject *const *args, Py_ssize_t n) {
         p.v = v.data_ptr();
         strides(p.k_stride, k);
         strides(p.v_stride, v);
-        return result(lib.attn_paged_read_q8_(&p, stream), k, v);
+        return result(unlocked([&] { return lib.attn_paged_read_q8_(&p, stream); }), k, v);
     });
 }
 
@@ -253,7 +265,7 @@ struct Attention {
             return {workspace.data_ptr(), (size_t)workspace.nbytes()};
         }
         if (!bytes) return {nullptr, 0};
-        workspace = at::empty({(int64_t)bytes}, o.options().dtype(at::kByte));
+        workspace = unlocked([&] { return at::empty({(int64_t)bytes}, o.options().dtype(at::kByte)); });
         return {workspace.data_ptr(), bytes};
     }
 };
@@ -265,10 +277,10 @@ PyObject *fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (t.q8) {
             attn_paged_fwd_q8_params_t p{t.p.fwd, t.p.scales};
             const auto ws = t.room(dev, a[11], given(a[11]) ? 0 : lib.attn_paged_fwd_q8_workspace_bytes_(&p));
-            return result(lib.attn_paged_fwd_q8_(&p, ws.first, ws.second, stream), t.o, t.lse);
+            return result(unlocked([&] { return lib.attn_paged_fwd_q8_(&p, ws.first, ws.second, stream); }), t.o, t.lse);
         }
         const auto ws = t.room(dev, a[11], given(a[11]) ? 0 : lib.attn_paged_fwd_workspace_bytes_(&t.p.fwd));
-        return result(lib.attn_paged_fwd_(&t.p.fwd, ws.first, ws.second, stream), t.o, t.lse);
+        return result(unlocked([&] { return lib.attn_paged_fwd_(&t.p.fwd, ws.first, ws.second, stream); }), t.o, t.lse);
     });
 }
 
@@ -286,7 +298,7 @@ PyObject *prefix_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         t.p.prefix_lens = static_cast<const int32_t *>(tensor(a[15], dev, at::kInt, {t.p.P}).data_ptr());
         t.p.cu_prefix = static_cast<const int32_t *>(vector(a[16], dev, at::kInt, t.p.P + 1));
         const auto ws = t.room(dev, a[11], given(a[11]) ? 0 : lib.attn_paged_prefix_fwd_workspace_bytes_(&t.p));
-        return result(lib.attn_paged_prefix_fwd_(&t.p, ws.first, ws.second, stream), t.o, t.lse);
+        return result(unlocked([&] { return lib.attn_paged_prefix_fwd_(&t.p, ws.first, ws.second, stream); }), t.o, t.lse);
     });
 }
 
