@@ -27,8 +27,8 @@ from __future__ import annotations
 
 import ctypes
 import math
-import os
 import struct
+import warnings
 
 import torch
 
@@ -175,19 +175,23 @@ _quick = None
 
 
 def _binding():
-    """The module _binding (csrc/binding.cpp), which takes ordinary calls of the paged cache in one step."""
+    """The module _binding (csrc/binding.cpp), which takes ordinary calls of the paged cache in one step; False where it
+    cannot be loaded, which is said once: the calls then take this file's way."""
     global _quick
     if _quick is None:
         import importlib.util
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        from . import build
         _load()
-        spec = importlib.util.spec_from_file_location("online_softmax_fa2_gb300._binding", path)
-        m = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(m)
-        m.open(_ofa.library_path())
-        _quick = m
+        try:
+            spec = importlib.util.spec_from_file_location("online_softmax_fa2_gb300._binding", build.BINDING)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.open(_ofa.library_path())
+            _quick = m
+        except (ImportError, OSError) as e:
+            warnings.warn(f"calls of the paged cache take some 15 us longer without their quick binding: {e} (build it with "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`)", RuntimeWarning)
+            _quick = False
     return _quick
 
 
@@ -195,7 +199,10 @@ def _quick_call(dev, name, *args):
     """The call by the quick binding, or None where it does not take it."""
     if dev < 0 or dev != torch._C._cuda_getDevice():
         return None
-    r = getattr(_quick or _binding(), name)(dev, torch._C._cuda_getCurrentRawStream(dev), *args)
+    m = _quick or _binding()
+    if not m:
+        return None
+    r = getattr(m, name)(dev, torch._C._cuda_getCurrentRawStream(dev), *args)
     if r.__class__ is int:
         raise _ofa.AttnError(r, _ofa.last_error())
     return r
