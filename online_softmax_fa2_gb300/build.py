@@ -1,10 +1,11 @@
 """Builds the library: nvcc compiles each CUDA source for sm_103a, in parallel, and links
 ``libattn_gb300.so`` in the package directory (in-tree; git-ignored).  Beside it g++ compiles the quick
-binding of the paged cache's calls against this machine's torch, ``_binding.so``; the library stands without it, and so
+binding of the paged cache's calls against this machine's torch and Python, ``_binding.so`` (which those are, ``_build/_binding.stamp`` says); the library stands without it, and so
 do the calls (paged.py), so that a machine where it cannot be built gets a warning."""
 from __future__ import annotations
 
 import os
+import platform
 import shutil
 import subprocess
 import sys
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_gb300.so")
 BINDING = os.path.join(HERE, "_binding.so")
+STAMP = os.path.join(BUILD, "_binding.stamp")
 SOURCES = ["attn_api.cu", "fwd_f32.cu", "fwd_bf16_sm103.cu", "fwd_bf16_pair_sm103.cu", "decode.cu",
            "bwd.cu", "bwd_tc_sm103.cu", "qk_rope.cu", "paged_fwd.cu", "paged_rows.cu",
            "paged_rows_q8.cu", "paged_read_q8.cu", "paged_tc_sm103.cu", "paged_api.cu"]
@@ -39,6 +41,22 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_stamp() -> str:
+    """What a quick binding is compiled against: one built for anything else is built anew, and not loaded."""
+    import torch
+    return " ".join(["torch", torch.__version__, "abi", str(int(torch._C._GLIBCXX_USE_CXX11_ABI)), str(sysconfig.get_config_var("SOABI")),
+                     platform.machine()])
+
+
+def binding_is_current() -> bool:
+    """Whether there is a quick binding that was built for this torch and Python."""
+    try:
+        with open(STAMP) as f:
+            return os.path.exists(BINDING) and f.read() == binding_stamp()
+    except (ImportError, OSError):
+        return False
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
@@ -59,9 +77,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_binding():
         s = os.path.join(CSRC, "binding.cpp")
-        if force or _stale(BINDING, [s, headers[-1]]):
-            if os.path.exists(BINDING):
-                os.remove(BINDING)  # an old one's parameter blocks may not be the library's
+        if force or _stale(BINDING, [s, headers[-1]]) or not binding_is_current():
+            for old in (STAMP, BINDING):
+                if os.path.exists(old):
+                    os.remove(old)  # an old one's parameter blocks may not be the library's
             import torch
             t = os.path.dirname(torch.__file__)
             tmp = BINDING + f".tmp{os.getpid()}"
@@ -74,6 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if r.returncode != 0:
                 raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
             os.replace(tmp, BINDING)
+            with open(STAMP, "w") as f:
+                f.write(binding_stamp())
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(compile_binding)

@@ -183,6 +183,8 @@ def _binding():
         from . import build
         _load()
         try:
+            if not build.binding_is_current():
+                raise ImportError(f"{build.BINDING} is missing, or was built for another torch or Python")
             spec = importlib.util.spec_from_file_location("online_softmax_fa2_gb300._binding", build.BINDING)
             m = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(m)

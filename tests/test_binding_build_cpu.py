@@ -18,6 +18,7 @@ def built():
 def test_the_library_is_linked_without_a_compiler_for_the_binding(monkeypatch, tmp_path):
     monkeypatch.setattr(ofa_build, "LIB", str(tmp_path / "lib.so"))
     monkeypatch.setattr(ofa_build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(ofa_build, "STAMP", str(tmp_path / "_binding.stamp"), raising=False)
     (tmp_path / "_binding.so").write_bytes(b"of older sources")
     os.utime(tmp_path / "_binding.so", (0, 0))
     run = ofa_build.subprocess.run
@@ -44,6 +45,38 @@ def test_without_a_binding_there_is_a_warning_and_no_more(monkeypatch, tmp_path,
     with warnings.catch_warnings():
         warnings.simplefilter("error")
         assert paged._binding() is False  # said once
+
+
+@pytest.fixture
+def elsewhere(monkeypatch, tmp_path):
+    """The binding and its stamp in a folder of their own, as a build has left them."""
+    for name in ("BINDING", "STAMP"):
+        old = getattr(ofa_build, name)
+        new = tmp_path / os.path.basename(old)
+        new.write_bytes(open(old, "rb").read())
+        monkeypatch.setattr(ofa_build, name, str(new))
+
+
+def test_a_binding_of_another_torch_is_built_anew(elsewhere):
+    assert ofa_build.binding_is_current()
+    before = os.stat(ofa_build.BINDING).st_mtime_ns
+    ofa_build.build()
+    assert os.stat(ofa_build.BINDING).st_mtime_ns == before  # nothing to do
+    with open(ofa_build.STAMP, "w") as f:
+        f.write(ofa_build.binding_stamp().replace("torch ", "torch 0."))
+    assert not ofa_build.binding_is_current()
+    ofa_build.build()
+    assert ofa_build.binding_is_current() and os.stat(ofa_build.BINDING).st_mtime_ns > before
+    os.remove(ofa_build.STAMP)  # of no known origin
+    assert not ofa_build.binding_is_current()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(elsewhere, monkeypatch):
+    monkeypatch.setattr(paged, "_quick", None)
+    stamp = ofa_build.binding_stamp()
+    monkeypatch.setattr(ofa_build, "binding_stamp", lambda: stamp + " and another")
+    with pytest.warns(RuntimeWarning, match="another torch"):
+        assert paged._binding() is False
 
 
 @pytest.mark.gpu
