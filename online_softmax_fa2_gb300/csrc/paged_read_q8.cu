@@ -98,7 +98,14 @@ __global__ void __launch_bounds__(kThreads) paged_read_q8_kernel(const ReadArgs 
         bool on = lane < a.run && t < a.T;
         if (a.cu) {
             b = find_sequence(a.cu, a.B, first);
-            while (on && b < a.B && __ldg(a.cu + b + 1) <= t) ++b;
+            if (on && b < a.B && __ldg(a.cu + b + 1) <= t) {  // a later sequence's, behind empty ones perhaps: find it by halves
+                int end = a.B;
+                for (++b; b < end;) {
+                    const int mid = (b + end) / 2;
+                    if (__ldg(a.cu + mid + 1) <= t) b = mid + 1;
+                    else end = mid;
+                }
+            }
             on = on && b < a.B;
             if (on) {  // the sequence's rows as find_token takes them
                 const int c0 = min(max(__ldg(a.cu + b), 0), a.T);
