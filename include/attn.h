@@ -646,12 +646,13 @@ size_t attn_paged_fwd_q8_workspace_bytes(const attn_paged_fwd_q8_params_t *param
  * near 2^14 (exact down to 2^-31 of it), the weights are rounded to fp16 before the value product.  Of a weight under 2^-21
  * of the row's largest bits under 2^-32 of that are lost, or, where a weight goes in times its value's scale (with up
  * to 16 rows a key head, and where the scales of 128 neighbouring keys lie 2^16 or more apart), bits under 2^-32 of
- * the largest such product that the row has.  What a row does not see, or gives no weight, takes nothing from it, whatever its scale.
- * (With more than 16 rows, rows of scale byte 0, under 2^-118, count as zeros beside ones of byte 25 and up among those 128 keys.)
+ * the largest such product that the row has.  What a row does not see, or gives no weight, takes nothing from it,
+ * whatever its scale.  (With more than 16 rows, 128 keys whose scales lie so far apart take five times as long as others,
+ * and rows of scale byte 0, under 2^-118, count as zeros beside ones of byte 25 and up among them.)
  * Everything else as attn_paged_fwd; a row that holds a NaN makes the rows that see it NaN.
  * Supported: as attn_paged_fwd; the bases and strides of pages and scales are multiples of 16 bytes.  A cache whose
- * heads lie apart ([num_pages, Hkv, page_size, d] in memory, passed by its strides) is read faster: 132 us for
- * 220 at 16 heads of 64, 114 for 120 at 8 of 128 (64 ragged sequences to 8192 keys).
+ * heads lie apart ([num_pages, Hkv, page_size, d] in memory, passed by its strides) is read faster: 135 us for
+ * 217 at 16 heads of 64, 112 for 120 at 8 of 128 (64 ragged sequences to 8192 keys).
  */
 attn_status_t attn_paged_fwd_q8(const attn_paged_fwd_q8_params_t *params, void *workspace, size_t workspace_bytes,
                                 attn_stream_t stream);

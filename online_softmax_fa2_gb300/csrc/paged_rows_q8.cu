@@ -24,11 +24,11 @@
 //   V   transposed, a register holds two neighbouring dimensions of two keys: a byte permutation makes the keys
 //       of the even dimension and those of the odd one neighbours, for two products of eight dimensions.
 //
-// The bound is the cache's bytes; measured, 32/8 heads of 128 unless said: 64 ragged sequences to 8192 keys (647 MB) 114 us,
-// 5.7 TB/s (655 MB read, 39% of the issue slots used), with the consumers doing nothing but handing the stages back 113; of that the
+// The bound is the cache's bytes; measured, 32/8 heads of 128 unless said: 64 ragged sequences to 8192 keys (647 MB) 112 to 114 us,
+// 5.7 TB/s (655 MB read, 43% of the issue slots used), with the consumers doing nothing but handing the stages back 113; of that the
 // ends of the call are about 12.  With 16 rows a block for the same 4 it took 123, three CTAs of two stages an SM the same,
-// tiles of 64 keys 136.  16 heads of 64: 132 us with 8 rows a block, 164 with 16.  A cache whose heads lie apart
-// (places first) gives TMA rows of d bytes instead of whole boxes: 120 and 220 us.
+// tiles of 64 keys 136.  16 heads of 64: 135 us with 8 rows a block (130 with one unit for all rows), with 16 some 30 more.  A cache
+// whose heads lie apart (places first) gives TMA rows of d bytes instead of whole boxes: 120 and 217 us.
 #include <cudaTypedefs.h>
 
 #include "paged.h"

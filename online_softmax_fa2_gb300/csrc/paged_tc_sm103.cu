@@ -354,10 +354,13 @@ __device__ __forceinline__ void write_cut(const paged::Args &a, const Share &sha
 // The reference of a row's weights lies 2^7 below its maximum: as it may lag by 2^8, the weights reach 2^15, and lose
 // bits from 2^-21 of the largest on, 2^-32 of it at most.
 //
-// What bounds it: shared memory.  Of a 256 x 128 tile the products read 192 KB of it (1536 clocks of 128 bytes), the codes'
-// way takes 128 KB more (in by TMA, out to registers, back as fp16), of the 3030 clocks that the tile takes over bf16:
-// 3700 here, 2048 tokens over 18432 keys of 32/8 heads 462 us against 394, 1.26 PFLOP/s; 16 ragged sequences to 4096 keys,
-// chunks to 512 tokens, 28/4 heads 100 us against 75.  The issuer waits for operands 220 clocks of a tile, for weights 670.
+// What bounds it, as far as it is known: a 256 x 128 tile takes 3700 clocks, 3030 over bf16.  Shared memory is busy four fifths of
+// them: the products read 192 KB of it (1536 clocks of 128 bytes), the codes come in by TMA (32 KB), and all loads and
+// stores of the threads, the codes' way out to registers and back as fp16 above all, take 1150.  The issuer waits for operands
+// 220 clocks of a tile, for weights 670, so the softmax's warps come next, which share their issue slots with the converting
+// ones.  (The kernels spill 290 to 400 bytes a thread, 30 loads of them a tile over all warps.)  2048 tokens over 18432 keys of
+// 32/8 heads 462 us against 394, 1.26 PFLOP/s; 16 ragged sequences to 4096 keys, chunks to 512 tokens, 28/4 heads 99 us against
+// 75.  With every tile a wide one 2440 and 405 us.
 
 // A tile's 128 scale bytes, four a lane (of keys past the held ones 0), against what its operand is relative to, `unit` (below 0:
 // nothing yet), which stays as long as they all lie where codes are exact: from kExact below to kAbove above.  Otherwise the
