@@ -689,7 +689,9 @@ size_t attn_paged_prefix_fwd_workspace_bytes(const attn_paged_prefix_params_t *p
  * is that of attn_paged_fwd over the prefix's keys followed by the own ones, lse included, with its rules for empty rows,
  * NaN and tokens of no sequence; no token has to belong to a prefix.  (A row that the causal rule lets see no own key, as it lies
  * before them all, sees its whole prefix.)  How the GPU is shared out between the prefixes and the own keys goes by the
- * tables' widths: tables no wider than their longest entry (a view will do) are fastest.
+ * tables' widths: tables no wider than their longest entry (a view will do) are fastest.  (One token of 64 sequences to
+ * 1024 keys behind 8192, 32/8 heads of 128, 56 us: with a block table of 131072 keys 88, with such a prefix table 122, with
+ * both 57; over 8 bits 54, 92, 67, 67.)
  * Supported: as attn_paged_fwd, or attn_paged_fwd_q8; 1 <= P <= 65535.  Queues two or three kernels.
  */
 attn_status_t attn_paged_prefix_fwd(const attn_paged_prefix_params_t *params, void *workspace, size_t workspace_bytes,
