@@ -651,8 +651,8 @@ size_t attn_paged_fwd_q8_workspace_bytes(const attn_paged_fwd_q8_params_t *param
  * and rows of scale byte 0, under 2^-118, count as zeros beside ones of byte 25 and up among them.)
  * Everything else as attn_paged_fwd; a row that holds a NaN makes the rows that see it NaN.
  * Supported: as attn_paged_fwd; the bases and strides of pages and scales are multiples of 16 bytes.  A cache whose
- * heads lie apart ([num_pages, Hkv, page_size, d] in memory, passed by its strides) is read faster: 135 us for
- * 217 at 16 heads of 64, 112 for 120 at 8 of 128 (64 ragged sequences to 8192 keys).
+ * heads lie apart ([num_pages, Hkv, page_size, d] in memory, passed by its strides) is read faster: 136 us for
+ * 217 to 239 at 16 heads of 64, 113 for 120 to 130 at 8 of 128 (64 ragged sequences to 8192 keys).
  */
 attn_status_t attn_paged_fwd_q8(const attn_paged_fwd_q8_params_t *params, void *workspace, size_t workspace_bytes,
                                 attn_stream_t stream);

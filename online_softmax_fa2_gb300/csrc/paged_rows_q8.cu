@@ -27,8 +27,9 @@
 // The bound is the cache's bytes; measured, 32/8 heads of 128 unless said: 64 ragged sequences to 8192 keys (647 MB) 112 to 114 us,
 // 5.7 TB/s (655 MB read, 43% of the issue slots used), with the consumers doing nothing but handing the stages back 113; of that the
 // ends of the call are about 12.  With 16 rows a block for the same 4 it took 123, three CTAs of two stages an SM the same,
-// tiles of 64 keys 136.  16 heads of 64: 135 us with 8 rows a block (130 with one unit for all rows), with 16 some 30 more.  A cache
-// whose heads lie apart (places first) gives TMA rows of d bytes instead of whole boxes: 120 and 217 us.
+// tiles of 64 keys 136.  16 heads of 64: 136 us with 8 rows a block (130 with one unit for all rows and no bounds
+// of a factor), with 16 some 30 more.  A cache
+// whose heads lie apart (places first) gives TMA rows of d bytes instead of whole boxes: 120 to 130 and 217 to 239 us.
 #include <cudaTypedefs.h>
 
 #include "paged.h"
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, Rows<D, R>::kBlocks)
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float x = s[nt][at_of(e, i)] * q8::finite(un[e] * sc[i]);
+                        float x = s[nt][at_of(e, i)] * q8::factor(un[e] * sc[i]);
                         if (edge && kv0 + key_of(nt, i) >= lim[e]) x = -INFINITY;
                         s[nt][at_of(e, i)] = x;
                         mx[e] = fmaxf(mx[e], x);

@@ -685,10 +685,10 @@ struct Row {
 // Logits from which a product that is rounded in the maximum and not in the exponent would part the two.
 constexpr float kLarge = 1048576.f;
 // The softmax of a tile that is a wide one in K or V, or relative to something else than a row's u, or with logits of kLarge: 16
-// keys at a time, three times through S.  Its logits are the products times each key's own factor.  Its weights go in times 2^(e - unit), e a key's
-// scale byte (of a tile that is not wide what V's operand is relative to), in a unit that brings the largest of these near 2^14, or
-// keeps what u has; u is scaled to that unit.  Rare, and out of line, where it takes no room in the instruction
-// cache: within the loop it took chunks from 463 to 634 us.  Whether the row can go on without.  Whole warp.
+// keys at a time, three times through S.  Its logits are the products times each key's own factor.  Its weights go in times
+// 2^(e - unit), e a key's scale byte (of a tile that is not wide what V's operand is relative to), in a unit that brings the
+// largest of these near 2^14, or keeps what u has; u is scaled to that unit.  Rare, and out of line, where it takes no room
+// in the instruction cache: within the loop it took chunks from 463 to 634 us.  Returns whether the row can go on without.  Whole warp.
 template <int D>
 __device__ __noinline__ bool odd_tile(const paged::Args &a, const Walk &w, uint32_t s_addr, uint32_t o_addr, int kv0, int lim, int k_unit,
                                       int v_unit, float c_row, bool first, Row &row) {
@@ -704,7 +704,7 @@ __device__ __noinline__ bool odd_tile(const paged::Args &a, const Walk &w, uint3
     for_keys(s_addr, kw, [&](int cc, uint32_t (&r)[16], auto byte) {
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
-            float x = __uint_as_float(r[t]) * q8::finite(c_row * q8::pow2((uint32_t)byte(t)));
+            float x = __uint_as_float(r[t]) * q8::factor(c_row * q8::pow2((uint32_t)byte(t)));
             if (kv0 + 16 * cc + t >= lim) x = -INFINITY;
             mt = fmaxf(mt, x);
             r[t] = __float_as_uint(x);
@@ -1074,7 +1074,7 @@ __global__ void __launch_bounds__(threads(NT, kQ8), NT == 2 ? 1 : 2)
                         if (jj == 0) even = unit = (int)(note >> 16);
                         odd = (note & kWide) || (int)(note >> 16) != even || (note >> 16) >= kWide;
                         if (odd) break;
-                        ct = q8::finite(fmaxf(c_row * q8::pow2(note & 255u), 1.17549435e-38f));  // (not 0: -inf times it stays -inf)
+                        ct = q8::factor(c_row * q8::pow2(note & 255u));
                     }
                     bf16fwd::load_s_row(lane_addr + s_col, x);
                     const float mt = bf16fwd::tile_logits<false>(x, ct, kv0, kv0 + BK > lim0, lim);

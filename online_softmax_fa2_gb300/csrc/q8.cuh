@@ -15,10 +15,10 @@ __device__ __forceinline__ float pow2(uint32_t e) {
 // The same for e from -22 to 254, where it may be one of the least subnormals.
 __device__ __forceinline__ float pow2_low(int e) { return __uint_as_float(e > 0 ? (uint32_t)e << 23 : 0x400000u >> -e); }
 
-// A factor of logits, at most the largest float (0 times it is 0); a NaN stays one.  A query row's power of two and a key's
-// meet before the sum of their products does: either alone may take it out of fp32, with logits of ordinary size.
-__device__ __forceinline__ float finite(float x) {
-    asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(3.402823466e38f));
+// A factor of logits, within the normal floats (0 times it is 0, -inf times it -inf); a NaN stays one.  A query row's power of two
+// and a key's meet before the sum of their products does: either alone may take it out of fp32, with logits of ordinary size.
+__device__ __forceinline__ float factor(float x) {
+    asm("min.NaN.f32 %0, %0, %1;\n\tmax.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(3.402823466e38f), "f"(1.17549435e-38f));
     return x;
 }
 

@@ -185,6 +185,27 @@ def test_queries_near_the_largest_over_the_smallest_keys(shape):
     go(s, new, lens, 0.125)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_logits_of_minus_infinity(shape, wide):
+    """Over keys so small, with queries so small but for an infinite element, that the factor of the products is under fp32: a
+    row of such logits alone is empty, and a key without one is all that another row sees."""
+    new, lens, Hq, Hkv, d = shape
+    s = q8_inputs(new, lens, Hq, Hkv, d, 16, seed=40)
+    s["q"] = torch.zeros_like(s["q"])
+    s["q"][..., 0] = -math.inf
+    s["q"][:, 1::2, 0] = -1e-30
+    for b, n in enumerate(lens):
+        x = torch.ones(n, d)
+        set_codes(s, "k", b, torch.arange(n), x)
+        set_bytes(s, "k", b, torch.arange(n), torch.full((n, Hkv), 60) + (20 * (torch.arange(n) % 2)[:, None] if wide else 0))
+    ofa.device_error_flags()
+    o, lse = run(s, scale=0.1, max_q=max(new))
+    assert ofa.device_error_flags() == 0
+    assert bool((lse[:, 0::2] == -math.inf).all()) and bool((o[:, 0::2].contiguous().view(torch.int16) == 0).all())
+    check_visible(o[:, 1::2], lse[:, 1::2], dict(s, q=s["q"][:, 1::2].contiguous()), new, lens, True, 0.1)
+
+
 @pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[3], SHAPES[5]])
 def test_large_hidden_keys_behind_a_prefix(shape):
     """Side by side and one after the other; a prefix's own values 2^35 above or below the own keys'."""
