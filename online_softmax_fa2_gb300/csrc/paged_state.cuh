@@ -208,7 +208,7 @@ __device__ __forceinline__ bool is_wanted(const Args &a, int tok) {
 // that one has waited for: a grid's wait covers the grid right before it.  So the first grid releases the call's tag
 // after its wait, and a thread here that acquires the tag has those writes in its past as the first grid has; one that finds
 // another value waits for the first grid's end.  Nobody spins.  The tag is taken away at this grid's end: a captured call finds
-// none at its next replay.  (64 sequences behind 8192 keys take as long as without.)
+// none at its next replay.  (64 sequences behind 8192 keys, over boxes, 55 to 57 us, 52 to 55 without.)
 __device__ __forceinline__ void begin_after_earlier_grids(const Args &a, bool state) {
     if (!state || a.state.mode < kMerged) {
         ptx::grid_dep_wait();
