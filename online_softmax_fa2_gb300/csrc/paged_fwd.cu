@@ -224,8 +224,9 @@ size_t round_up(size_t x) { return (x + 255) & ~(size_t)255; }
 //
 // Few rows a sequence behind prefixes on the tiles (a decode step): the own keys' attention, bound by memory, runs on the
 // SMs that the prefixes' leaves it, and the prefixes' merge comes last.  64 sequences behind 8192 keys with up to 1024 of
-// their own, 32/8 heads of 128: 55 us (52 before the second waited for its word that it may begin); one after the other 65, of which the own keys' is 35.  Many rows (prompt chunks) keep
-// every SM busy by themselves: one after the other, the second beginning as SMs come free.  No merge lies between, which every
+// their own, 32/8 heads of 128: 55 us (52 before the second looked for the word that it may begin); one after the other 65, of
+// which the own keys' is 35.  Many rows (prompt chunks) keep every SM busy by themselves: one after the other, the second beginning
+// as SMs come free.  No merge lies between, which every
 // CTA of the second would begin after: it joins the parts of cut rows itself (8 chunks to 512 tokens behind 4096 keys, 28/4
 // heads, 143 us, 148 with one; 16 tokens each of 64 sequences behind 2048 91 and 96; 2 chunks of 2048 behind 8192 450 and 447).
 struct PrefixPlan {
